@@ -29,6 +29,13 @@ PARAM_BYTES = struct.calcsize(_PARAM_FMT)   # 36, sizeof(dg_canvas_params)
 _lib = None
 
 
+class _PagedKV(ctypes.Structure):   # dg_paged_kv
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 class DGError(RuntimeError):
     def __init__(self, fn: str, code: int):
         super().__init__(f"{fn} failed: {status_string(code)} ({code})")
@@ -52,6 +59,7 @@ def load(path: str | None = None):
     P, i32, i64, u32, u64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                                   ctypes.c_uint64, ctypes.c_size_t)
     st = ctypes.c_int
+    PagedKV = ctypes.POINTER(_PagedKV)
     sig = {
         "dg_denoise_workspace_bytes": (sz, [i64, i32, i64, ctypes.c_int]),
         "dg_denoise_step": (st, [P, ctypes.c_int, i64, i64, i32, i64, P, u64] + [P] * 11 + [P, sz, P]),
@@ -84,6 +92,12 @@ def load(path: str | None = None):
         "dg_attention_workspace_bytes": (sz, [i32, i32]),
         "dg_attention": (st, [P, P, P, P, P, P, P, P, i32, i32, i64, i64, i32, i32, i32, i32, ctypes.c_float,
                               P, sz, P]),
+        "dg_kv_append": (st, [P, i64, P, i64, P, i64, P, P, i32, i64, i32, i32, i32, P, i32, i32, PagedKV, P]),
+        "dg_paged_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "dg_paged_attention": (st, [P, PagedKV, P, P, P, P, i32, i32, i64, i32, i32, i32, i32, ctypes.c_float,
+                                    P, sz, P]),
+        "dg_adjust_logits": (st, [P, ctypes.c_int, i64, P, i64, i64, i32, i64, P, P, P, i64, P, P, P, P, i64,
+                                  P, i64, i32, P, P]),
         "dg_embed_canvas": (st, [P, i64, i64, P, i32, P, ctypes.c_float, P, P]),
         "dg_commit": (st, [P, P, P, i64, i32, P, P, P, P, P]),
         "dg_philox_words": (st, [u64, u32, u32, u32, u32, u32, i64, P, P]),
@@ -113,7 +127,8 @@ def exported_symbols() -> list[str]:
                         "dg_self_cond_mlp", "dg_self_cond_probs_workspace_bytes",
                         "dg_self_cond_probs", "dg_gemm_workspace_bytes", "dg_gemm_bf16",
                         "dg_gemm_bf16_noalloc", "dg_choice_probs", "dg_embed_canvas", "dg_commit", "dg_attention",
-                        "dg_attention_workspace_bytes",
+                        "dg_attention_workspace_bytes", "dg_kv_append", "dg_paged_attention",
+                        "dg_paged_attention_workspace_bytes", "dg_adjust_logits",
                         "dg_philox_words", "dg_get_device_status", "dg_clear_device_status",
                         "dg_probe_bounded_wait",
                         "dg_status_string", "dg_version", "dg_launch_count") if hasattr(lib, n)]
@@ -406,6 +421,171 @@ def dg_attention(q, k, v, o, cu_q, cu_kv, causal, max_q_len: int, *, lse=None, w
                              workspace.numel(), _s(stream))
     if check:
         _check("dg_attention", rc)
+    return rc
+
+
+def _want(fn, **tensors):
+    """Each tensor has its dtype and shape (None = any extent), is contiguous, and lies on the current
+    device; name=(tensor, dtype, shape).  A tensor of None is skipped."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+        if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+            raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+        _here(fn, name, t)
+
+
+def _here(fn, name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{fn}: {name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+
+
+def _rows(fn, name, t, heads, d):
+    """Row stride of t [tokens, heads, d], whose rows hold [heads][d] without gaps."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{fn}: {name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{fn}: {name} must have shape (tokens, {heads}, {d}), got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{fn}: {name}'s heads must follow each other")
+    _here(fn, name, t)
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def _paged_kv(fn, k_cache, v_cache, page_table, kv_len):
+    """dg_paged_kv of k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides of the first three) and
+    page_table [n_seq, max_pages], kv_len [n_seq] int32."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{fn}: {name} must be bfloat16, got {t.dtype}")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{fn}: {name} must be [n_pages, page_size, Hkv, D] with contiguous heads")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError(f"{fn}: k_cache and v_cache must have one layout")
+    n_pages, page_size, Hkv, D = k_cache.shape
+    n = kv_len.numel()
+    _want(fn, page_table=(page_table, torch.int32, (n, None)), kv_len=(kv_len, torch.int32, (n,)))
+    _here(fn, "k_cache", k_cache)
+    _here(fn, "v_cache", v_cache)
+    # the stride of an extent of one says nothing: any valid one will do
+    ps, ss, hs = (s if e > 1 else D for e, s in zip(k_cache.shape[:3], k_cache.stride()[:3]))
+    kv = _PagedKV(_p(k_cache), _p(v_cache), _p(page_table), _p(kv_len), n_pages, ps, ss, hs, page_size,
+                  page_table.shape[1])
+    return kv, n, Hkv, D
+
+
+def _scratch(fn, nbytes, workspace, device, stream):
+    """The caller's workspace, or one for this call; a fresh one lives until the call's stream passes it."""
+    if workspace is None:
+        workspace = torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
+        if stream is not None and _s(stream) != torch.cuda.current_stream().cuda_stream:
+            # the allocator orders memory along the current stream: order the call's stream after it and
+            # keep the memory until that stream is done with it
+            st = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+            st.wait_stream(torch.cuda.current_stream())
+            workspace.record_stream(st)
+        return workspace, nbytes
+    _here(fn, "workspace", workspace)
+    if not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def dg_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, *, inv_freq=None, interleaved=False, q=None,
+                 q_out=None, stream=None, check=True) -> int:
+    """Append k, v [total, Hkv, D] (rows of any stride) to the paged cache, keys rotated by position *
+    inv_freq [rot_dim / 2] float64; q [total, Hq, D] is rotated into q_out (contiguous).  The cache:
+    k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides but the last), page_table [n_seq,
+    max_pages], kv_len [n_seq] and cu_q [n_seq + 1] int32."""
+    fn = "dg_kv_append"
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{fn}: q and q_out come together")
+    kv, n, Hkv, D = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
+    total = k.shape[0]
+    ldk, ldv = _rows(fn, "k", k, Hkv, D), _rows(fn, "v", v, Hkv, D)
+    Hq, ldq = Hkv, 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        ldq = _rows(fn, "q", q, Hq, D)
+        _want(fn, q_out=(q_out, torch.bfloat16, (total, Hq, D)))
+    if v.shape[0] != total or (q is not None and q.shape[0] != total):
+        raise ValueError(f"{fn}: q, k and v must have as many rows")
+    _want(fn, cu_q=(cu_q, torch.int32, (n + 1,)), inv_freq=(inv_freq, torch.float64, (None,)))
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    rc = load().dg_kv_append(_p(k), ldk, _p(v), ldv, _p(q), ldq, _p(q_out), _p(cu_q), n, total, Hq, Hkv, D,
+                             _p(inv_freq), rot, int(bool(interleaved)), ctypes.byref(kv), _s(stream))
+    if check:
+        _check(fn, rc)
+    return rc
+
+
+def dg_paged_attention_workspace_bytes(n_seq: int, max_q_len: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().dg_paged_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D))
+
+
+def dg_paged_attention(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal, max_q_len: int, *, lse=None,
+                       window: int = -1, scale: float | None = None, workspace=None, stream=None,
+                       check=True) -> int:
+    """dg_attention over the paged cache of dg_kv_append: q, o [total_q, Hq, D] bf16, cu_q [n + 1] and
+    kv_len [n] int32, causal [n] uint8, lse [total_q, Hq] float32."""
+    fn = "dg_paged_attention"
+    kv, n, Hkv, D = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
+    total, Hq = (q.shape[0], q.shape[1]) if q.dim() == 3 else (0, 0)
+    _want(fn, q=(q, torch.bfloat16, (total, Hq, D)), o=(o, torch.bfloat16, (total, Hq, D)),
+          lse=(lse, torch.float32, (total, Hq)), cu_q=(cu_q, torch.int32, (n + 1,)),
+          causal=(causal, torch.uint8, (n,)))
+    scale = 1.0 / float(D) ** 0.5 if scale is None else float(scale)
+    need = dg_paged_attention_workspace_bytes(n, int(max_q_len), Hq, Hkv, D)
+    workspace, ws_bytes = _scratch(fn, need, workspace, q.device, stream)
+    rc = load().dg_paged_attention(_p(q), ctypes.byref(kv), _p(o), _p(lse), _p(cu_q), _p(causal), n,
+                                   int(max_q_len), total, Hq, Hkv, D, int(window), scale, _p(workspace),
+                                   ws_bytes, _s(stream))
+    if check:
+        _check(fn, rc)
+    return rc
+
+
+def dg_adjust_logits(logits, params, out=None, *, history=None, cu_history=None, penalties=None,
+                     bias_tokens=None, bias_values=None, cu_bias=None, masks=None, mask_index=None, V=None,
+                     stream=None, check=True) -> int:
+    """Penalties for the tokens of history (penalties [n, 3]: repetition, frequency, presence), biases and
+    masks (int32 words, bit set = allowed; mask_index [n, L], -1 = none) on logits [n, L, ld], into out
+    (in place when None).  history / bias lists are packed, canvas c's at cu[c] .. cu[c + 1]."""
+    fn = "dg_adjust_logits"
+    out = logits if out is None else out
+    if logits.dim() != 3 or out.dim() != 3 or out.shape[:2] != logits.shape[:2]:
+        raise ValueError(f"{fn}: logits and out must be [n, L, ld]")
+    dt = _dtype_code(logits)
+    if out.dtype != logits.dtype:
+        raise TypeError(f"{fn}: out must be {logits.dtype}, got {out.dtype}")
+    n, L, ld = logits.shape
+    V = ld if V is None else V
+    if (history is None) != (cu_history is None) or (history is None) != (penalties is None):
+        raise ValueError(f"{fn}: history, cu_history and penalties come together")
+    if (bias_tokens is None) != (bias_values is None) or (bias_tokens is None) != (cu_bias is None):
+        raise ValueError(f"{fn}: bias_tokens, bias_values and cu_bias come together")
+    if (masks is None) != (mask_index is None):
+        raise ValueError(f"{fn}: masks and mask_index come together")
+    nh = 0 if history is None else history.numel()
+    nb = 0 if bias_tokens is None else bias_tokens.numel()
+    _want(fn, logits=(logits, logits.dtype, (n, L, ld)), out=(out, out.dtype, (n, L, None)),
+          history=(history, torch.int32, (nh,)), cu_history=(cu_history, torch.int32, (n + 1,)),
+          penalties=(penalties, torch.float32, (n, 3)), bias_tokens=(bias_tokens, torch.int32, (nb,)),
+          bias_values=(bias_values, torch.float32, (nb,)), cu_bias=(cu_bias, torch.int32, (n + 1,)),
+          masks=(masks, torch.int32, (None, None)), mask_index=(mask_index, torch.int32, (n, L)))
+    _want(fn, params=(params, torch.uint8, (n * PARAM_BYTES,)))
+    n_masks, words = (0, 0) if masks is None else masks.shape
+    rc = load().dg_adjust_logits(_p(logits), dt, ld, _p(out), out.shape[2], n, L, V, _p(params), _p(history),
+                                 _p(cu_history), nh, _p(penalties), _p(bias_tokens), _p(bias_values),
+                                 _p(cu_bias), nb, _p(masks), words, n_masks, _p(mask_index), _s(stream))
+    if check:
+        _check(fn, rc)
     return rc
 
 

@@ -1,0 +1,262 @@
+// dg_adjust.cu -- a request's edits of its logits before the step reads them: penalties for the
+// tokens of its history, a bias per token, a grammar's mask.
+//
+// Every edit is a function of (canvas, token) but the mask, which is one of (position, token).  So a
+// block owns one canvas's slice of the vocabulary for a group of positions, a thread 16 bytes of it:
+// the block counts the slice's tokens in the canvas's lists once (shared memory), each thread turns
+// its tokens' counts and biases into one fp32 addend a token that stays in registers, and the rows
+// stream by with one mask byte a vector.  Nothing is sorted, gathered or kept between launches, and
+// the lists are read from L2 once a block.
+// Memory-bound: in place only vectors with an edited or excluded token are touched, and a vector
+// that is excluded whole is written without being read.
+#include <cuda_runtime.h>
+
+#include <math.h>
+
+#include <algorithm>
+
+#include "dg_common.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 8;   // rows in flight a thread
+
+struct AdjustArgs {
+    const unsigned char* x;
+    unsigned char* out;
+    int64_t ld_bytes, ld_out_bytes;
+    int32_t L, V, rows;   // rows: positions of a block
+    const dg_canvas_params* params;
+    const int32_t *history, *cu_history;
+    const dg_penalties* penalties;
+    const int32_t* bias_tokens;
+    const float* bias_values;
+    const int32_t* cu_bias;
+    const uint32_t* masks;
+    const int32_t* mask_index;
+    int64_t total_history, total_bias, mask_stride;
+    int32_t n_masks;
+    unsigned* status;
+};
+
+DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+
+// Bytes: 2 (bf16) or 4 (fp32) a logit; PerVec tokens in 16 bytes.
+template <int Bytes>
+__global__ void __launch_bounds__(kThreads) k_adjust(const AdjustArgs a) {
+    constexpr int PerVec = 16 / Bytes;
+    constexpr int kSlice = kThreads * PerVec;   // tokens of a block
+    constexpr uint32_t kAll = (1u << PerVec) - 1u;
+    __shared__ int32_t n_hist[kSlice];          // occurrences in the history
+    __shared__ int32_t n_bias[kSlice];          // entries in the bias list
+    __shared__ int32_t first_bias[kSlice];      // the first of them
+    dg::pdl_wait();
+    dg::pdl_release();
+    const int tid = threadIdx.x;
+    const int64_t c = blockIdx.z;
+    if (!(a.params[c].flags & DG_ACTIVE)) return;
+    const int slice0 = (int)blockIdx.x * kSlice;
+    const int v0 = slice0 + tid * PerVec;
+    const bool reports = blockIdx.x == 0 && blockIdx.y == 0 && tid == 0;
+
+    // the lists, and whether they are sound (the same for every block of the canvas)
+    int h0 = 0, h1 = 0, b0 = 0, b1 = 0;
+    dg_penalties pen = {1.f, 0.f, 0.f};
+    bool sound = true;
+    if (a.history) {
+        h0 = a.cu_history[c];
+        h1 = a.cu_history[c + 1];
+        pen = a.penalties[c];
+        sound = h0 >= 0 && h1 >= h0 && h1 <= a.total_history && pen.repetition > 0.f && isfinite(pen.repetition) &&
+                isfinite(pen.frequency) && isfinite(pen.presence);
+    }
+    if (a.bias_tokens) {
+        b0 = a.cu_bias[c];
+        b1 = a.cu_bias[c + 1];
+        sound = sound && b0 >= 0 && b1 >= b0 && b1 <= a.total_bias;
+    }
+    if (!sound) {
+        if (reports) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+        return;
+    }
+    float add[PerVec];
+    uint32_t penalised = 0, edited = 0;   // tokens with a count / with a count or a bias
+#pragma unroll
+    for (int e = 0; e < PerVec; ++e) add[e] = 0.f;
+    if (h1 > h0 || b1 > b0) {
+#pragma unroll
+        for (int e = 0; e < PerVec; ++e) {
+            n_hist[tid * PerVec + e] = 0;
+            n_bias[tid * PerVec + e] = 0;
+            first_bias[tid * PerVec + e] = 0x7fffffff;
+        }
+        __syncthreads();
+        const int end = min(kSlice, a.V - slice0);
+        for (int i = h0 + tid; i < h1; i += kThreads) {
+            const int64_t t = (int64_t)a.history[i] - slice0;
+            if (t >= 0 && t < end) atomicAdd(&n_hist[t], 1);
+        }
+        for (int i = b0 + tid; i < b1; i += kThreads) {
+            const int64_t t = (int64_t)a.bias_tokens[i] - slice0;
+            if (t >= 0 && t < end) {
+                atomicAdd(&n_bias[t], 1);
+                atomicMin(&first_bias[t], i);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < PerVec; ++e) {
+            const int nh = n_hist[tid * PerVec + e];
+            int nb = n_bias[tid * PerVec + e];
+            float b = 0.f;
+            for (int i = first_bias[tid * PerVec + e]; nb > 0; ++i)   // in list order
+                if (a.bias_tokens[i] == v0 + e) {
+                    b += a.bias_values[i];
+                    --nb;
+                    edited |= 1u << e;
+                }
+            if (nh > 0) {
+                penalised |= 1u << e;
+                b -= pen.frequency * (float)nh + pen.presence;
+            }
+            add[e] = b;
+        }
+        edited |= penalised;
+    }
+    if (v0 >= a.V) return;
+    const int n_mine = min(PerVec, a.V - v0);                  // tokens of the vector inside the vocabulary
+    const uint32_t mine = (1u << n_mine) - 1u;
+    const bool in_place = a.out == a.x;
+    constexpr uint32_t kNegInf = Bytes == 2 ? 0xff80ff80u : 0xff800000u;
+
+    const int r0 = (int)blockIdx.y * a.rows, r1 = min(a.L, r0 + a.rows);
+    for (int r = r0; r < r1; r += kUnroll) {
+        uint32_t keep[kUnroll];   // allowed tokens
+        uint4 x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            keep[u] = mine;
+            if (a.masks && r + u < r1) {
+                const int m = a.mask_index[c * a.L + r + u];
+                if (m >= 0 && m < a.n_masks) {
+                    const uint32_t w = reinterpret_cast<const unsigned char*>(a.masks + m * a.mask_stride)[v0 >> 3];
+                    keep[u] = mine & (w >> (v0 & 7));
+                } else if (m != -1 && tid == 0 && blockIdx.x == 0) {
+                    dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (r + u < r1 && keep[u] != 0 && !(in_place && keep[u] == mine && edited == 0))
+                x[u] = *reinterpret_cast<const uint4*>(a.x + (c * a.L + r + u) * a.ld_bytes + (int64_t)v0 * Bytes);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (r + u >= r1 || (in_place && keep[u] == mine && edited == 0)) continue;
+            unsigned char* dst = a.out + (c * a.L + r + u) * a.ld_out_bytes + (int64_t)v0 * Bytes;
+            uint4 y = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+            if (keep[u] != 0) {
+                y = x[u];
+                uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                for (int e = 0; e < PerVec; ++e) {
+                    const int i = Bytes == 2 ? e / 2 : e;
+                    const bool high = Bytes == 2 && (e & 1);
+                    uint32_t bits = w[i];
+                    if (edited >> e & 1) {
+                        float v = Bytes == 4 ? __uint_as_float(bits)
+                                             : __uint_as_float(high ? bits & 0xffff0000u : bits << 16);
+                        if (penalised >> e & 1) v = v > 0.f ? v / pen.repetition : v * pen.repetition;
+                        v += add[e];
+                        if (Bytes == 4) {
+                            bits = __float_as_uint(v);
+                        } else {
+                            const uint32_t p = pack_bf16x2(v, v);
+                            bits = high ? (bits & 0xffffu) | (p & 0xffff0000u) : (bits & 0xffff0000u) | (p & 0xffffu);
+                        }
+                    }
+                    if (!(keep[u] >> e & 1)) {
+                        if (Bytes == 4)
+                            bits = 0xff800000u;
+                        else
+                            bits = high ? (bits & 0xffffu) | 0xff800000u : (bits & 0xffff0000u) | 0xff80u;
+                    }
+                    w[i] = bits;
+                }
+            }
+            if (n_mine == PerVec) {
+                *reinterpret_cast<uint4*>(dst) = y;
+            } else {   // the row's last vector: nothing past column V is written
+#pragma unroll
+                for (int e = 0; e < PerVec; ++e) {
+                    if (e >= n_mine) break;
+                    const uint32_t w = reinterpret_cast<const uint32_t*>(&y)[Bytes == 2 ? e / 2 : e];
+                    if (Bytes == 2)
+                        reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(e & 1 ? w >> 16 : w);
+                    else
+                        reinterpret_cast<uint32_t*>(dst)[e] = w;
+                }
+            }
+        }
+    }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+extern "C" dg_status dg_adjust_logits(const void* logits, dg_dtype dtype, int64_t ld, void* out, int64_t ld_out,
+                                      int64_t n_canvas, int32_t L, int64_t V, const dg_canvas_params* params,
+                                      const int32_t* history, const int32_t* cu_history, int64_t total_history,
+                                      const dg_penalties* penalties, const int32_t* bias_tokens,
+                                      const float* bias_values, const int32_t* cu_bias, int64_t total_bias,
+                                      const uint32_t* masks, int64_t mask_stride, int32_t n_masks,
+                                      const int32_t* mask_index, dg_stream_t stream) {
+    if (dtype != DG_BF16 && dtype != DG_FP32) return DG_ERR_INVALID_ARG;
+    if (n_canvas < 0 || n_canvas > 65535 || L < 1 || L > 1024 || V < 2 || V > 0x7fffffffLL || ld < V || ld_out < V ||
+        total_history < 0 || total_history > 0x7fffffffLL || total_bias < 0 || total_bias > 0x7fffffffLL)
+        return DG_ERR_INVALID_ARG;
+    if (n_canvas == 0) return DG_OK;
+    if (!logits || !out || !params) return DG_ERR_INVALID_ARG;
+    if (history && (!cu_history || !penalties)) return DG_ERR_INVALID_ARG;
+    if (bias_tokens && (!bias_values || !cu_bias)) return DG_ERR_INVALID_ARG;
+    if (masks && (!mask_index || n_masks < 1 || mask_stride < (V + 31) / 32 || mask_stride > 0x7fffffffLL))
+        return DG_ERR_INVALID_ARG;
+    if (out == logits && ld_out != ld) return DG_ERR_INVALID_ARG;
+    const int64_t es = dtype == DG_BF16 ? 2 : 4;
+    if (!aligned(logits, 16) || !aligned(out, 16) || (ld * es) % 16 || (ld_out * es) % 16) return DG_ERR_ALIGNMENT;
+    if (V * es > 0x7fffffffLL) return DG_ERR_UNSUPPORTED;
+    AdjustArgs a;
+    a.x = static_cast<const unsigned char*>(logits);
+    a.out = static_cast<unsigned char*>(out);
+    a.ld_bytes = ld * es;
+    a.ld_out_bytes = ld_out * es;
+    a.L = L;
+    a.V = (int32_t)V;
+    a.rows = 64;
+    a.params = params;
+    a.history = history;
+    a.cu_history = cu_history;
+    a.penalties = penalties;
+    a.bias_tokens = bias_tokens;
+    a.bias_values = bias_values;
+    a.cu_bias = cu_bias;
+    a.masks = masks;
+    a.mask_index = mask_index;
+    a.total_history = total_history;
+    a.total_bias = total_bias;
+    a.mask_stride = mask_stride;
+    a.n_masks = n_masks;
+    a.status = dghost::status_word();
+    const int64_t slice = kThreads * (16 / es);
+    const dim3 grid((unsigned)((V + slice - 1) / slice), (unsigned)((L + a.rows - 1) / a.rows), (unsigned)n_canvas);
+    const cudaError_t e = dghost::launch_pdl(es == 2 ? k_adjust<2> : k_adjust<4>, grid, dim3(kThreads), 0,
+                                             (cudaStream_t)stream, a);
+    dghost::count_launch();
+    return dghost::cuda_status(e);
+}

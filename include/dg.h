@@ -362,6 +362,135 @@ DG_API dg_status dg_attention(const uint16_t* q, const uint16_t* k, const uint16
                               dg_stream_t stream);
 
 /* ------------------------------------------------------------------------------------ */
+/* A paged key / value cache: what a pass appends to it and the attention that reads it.  */
+/* The pages keep their context between passes ([DG "DiffusionGemmaModelState와            */
+/* DiffusionSampler"]: prefill and commit passes write it, denoising passes read it); its  */
+/* layout, and the rotation of positions, are readings: the pages describe neither.        */
+/* ------------------------------------------------------------------------------------ */
+
+/* The cache as the calls see it.  Token p of sequence s lies in slot p % page_size of page
+ * page_table[s][p / page_size]; its key for head h starts at
+ *   k + page * page_stride + slot * slot_stride + h * head_stride   (elements),
+ * its value at the same place of v, so that tokens may lie side by side ([page][slot][head][D])
+ * or heads ([page][head][slot][D]).
+ *   k, v        (device) bf16, 16-byte aligned.
+ *   page_table  (device) [n_seq][max_pages] int32; entries that no call needs may hold anything.
+ *   kv_len      (device) [n_seq] int32: the sequence's tokens, those of this pass included.
+ *               0 marks an empty slot of a padded batch.
+ * page_size is a power of two in [8, 65536]; n_pages < 2^31; strides are multiples of 8, at least
+ * D and below 2^39, and n_pages * page_stride < 2^60. */
+typedef struct {
+    uint16_t* k;
+    uint16_t* v;
+    const int32_t* page_table;
+    const int32_t* kv_len;
+    int64_t n_pages;
+    int64_t page_stride, slot_stride, head_stride;
+    int32_t page_size;
+    int32_t max_pages;
+} dg_paged_kv;
+
+/* Appends a pass's keys and values to the cache and rotates its queries and keys on the way.
+ * Sequence s owns rows cu_q[s] .. cu_q[s+1]-1 of q, k and v, its last q_len tokens: row i of it
+ * has the position p = kv_len[s] - q_len + i.  The first rot_dim dimensions of every query and key
+ * head turn in pairs, pair j by the angle p * inv_freq[j]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos),
+ * a and b at dimensions j and j + rot_dim / 2, or 2 j and 2 j + 1 when `interleaved` is not 0; the
+ * others are copied.  Keys and values go to slot p of the sequence, queries to q_out.  A denoising
+ * pass writes its canvas's slots anew each time.  Angles are reduced exactly (64-bit fixed point
+ * turns), so far positions are as exact as near ones; sines, cosines and the rotation are in fp32
+ * with one rounding to bf16.
+ *   k, v      (device) bf16 [total_q] rows of [Hkv][D], ldk / ldv elements apart (multiples of 8,
+ *             at least Hkv * D: they may be parts of one fused projection's rows).
+ *   q         (device, may be NULL) bf16 [total_q] rows of [Hq][D], ldq apart.
+ *   q_out     (device, out, NULL iff q is) bf16 [total_q][Hq][D]; may be q itself when
+ *             ldq = Hq * D, else must not overlap q.
+ *   cu_q      (device) [n_seq + 1] int32 offsets (non-decreasing).
+ *   inv_freq  (device, may be NULL when rot_dim = 0) [rot_dim / 2] double, radians per position.
+ *   cache     (host) the cache; the pages of positions kv_len - q_len .. kv_len - 1 must not be
+ *             shared with another sequence.
+ * Rows before cu_q[0] and behind cu_q[n_seq] are left out; so are the rows of a sequence with kv_len 0.  A
+ * sequence whose offsets lie outside [0, total_q], with kv_len < 0, 0 < kv_len < q_len or kv_len >
+ * max_pages * page_size raises DG_DEV_BAD_PARAM and is skipped, as is a token whose page is outside
+ * [0, n_pages): nothing of it is written.
+ * D is 64, 128 or 256 (else DG_ERR_UNSUPPORTED); rot_dim a multiple of 16 in [0, D]; Hq, Hkv in
+ * [1, 65535]; n_seq in [0, 65535]; 0 <= total_q < 2^31.  Errors: DG_ERR_INVALID_ARG,
+ * DG_ERR_ALIGNMENT (bf16 pointers not 16-byte aligned, strides not multiples of 8),
+ * DG_ERR_UNSUPPORTED, DG_ERR_CUDA.  One kernel. */
+DG_API dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q,
+                              int64_t ldq, uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q,
+                              int32_t Hq, int32_t Hkv, int32_t D, const double* inv_freq, int32_t rot_dim,
+                              int32_t interleaved, const dg_paged_kv* cache, dg_stream_t stream);
+
+/* dg_attention with its keys and values in the cache: o[i][h] = softmax over the allowed keys of
+ * (scale * q[i][h] . k[j][h']) applied to v, h' = h / (Hq / Hkv); queries, positions, causal and window as
+ * there, with kv_len[s] keys for sequence s.
+ *   q, o, lse, cu_q, causal, max_q_len, window, scale: as dg_attention (lse may be NULL).
+ *   cache     (host) the cache (only read).  Slots past kv_len and pages that hold no key some query may see
+ *             may hold anything, NaN included (their table entries too); a value that some
+ *             queries may see and others not must be finite.
+ *   workspace (device) >= dg_paged_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D),
+ *             16-byte aligned, no initial contents; calls that overlap on the GPU need their own.
+ * A sequence with kv_len 0 sees no key: its rows of o are 0 and its lse -inf.  A sequence whose
+ * offsets lie outside [0, total_q], with kv_len < 0, 0 < kv_len < q_len or kv_len > max_pages *
+ * page_size raises DG_DEV_BAD_PARAM and is skipped (its rows are not written); one with more than max_q_len
+ * queries raises it too and gets at least its first max_q_len rows; one that needs a page
+ * outside [0, n_pages) raises it and its rows are unspecified.  Rows of no sequence are not written.
+ * Limits and errors as dg_attention and dg_kv_append. */
+DG_API size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D);
+DG_API dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
+                                    const int32_t* cu_q, const uint8_t* causal, int32_t n_seq, int32_t max_q_len,
+                                    int64_t total_q, int32_t Hq, int32_t Hkv, int32_t D, int32_t window, float scale,
+                                    void* workspace, size_t workspace_bytes, dg_stream_t stream);
+
+/* ------------------------------------------------------------------------------------ */
+/* A request's own edits of its logits, before the step reads them: penalties for tokens  */
+/* it has already produced, a bias per token and a grammar's mask.  The pages describe     */
+/* none of them; the reading is the usual definition of such sampling parameters.           */
+/* ------------------------------------------------------------------------------------ */
+
+/* Penalties of one canvas. */
+typedef struct {
+    float repetition; /* > 0; 1 = none */
+    float frequency;  /* per occurrence; 0 = none */
+    float presence;   /* 0 = none */
+} dg_penalties;
+
+/* For every position of every DG_ACTIVE canvas c and every token t < V, with x the logit, n_t the
+ * number of times t occurs in the canvas's history and b_t the sum of its biases:
+ *   y = n_t > 0 ? (x > 0 ? x / repetition : x * repetition) : x,
+ *   y = y + (b_t - (n_t > 0 ? frequency * n_t + presence : 0))   if n_t > 0 or t has a bias,
+ *   y = -inf                                                    if the position's mask excludes t.
+ * fp32 with one rounding to the logits' type; a token with neither history, bias nor mask keeps its
+ * bits.  A bias of -inf excludes its token.  A mask that excludes every token leaves a row of -inf,
+ * which dg_denoise_step reports with DG_DEV_EMPTY_ROW.  Repeated tokens in a canvas's bias list add up, in list order.
+ *   logits      (device) [n_canvas][L][ld] of dtype, as in dg_denoise_step; out (device, out) the
+ *               same with ld_out; may be logits itself when ld_out = ld (then only what changes
+ *               is written), else must not overlap it.  Columns past V are not written.
+ *   params      (device) [n_canvas]: only DG_ACTIVE is read; other canvases are not written.
+ *   history     (device, may be NULL = none) [total_history] int32 tokens, canvas c's at
+ *               cu_history[c] .. cu_history[c+1]-1; cu_history (device) [n_canvas + 1] int32 and
+ *               penalties (device) [n_canvas] are given with it.
+ *   bias_tokens, bias_values (device, may be NULL = none) [total_bias] int32 / float; canvas c's
+ *               at cu_bias[c] .. cu_bias[c+1]-1.
+ *   masks       (device, may be NULL = none) [n_masks] rows of mask_stride 32-bit words: bit t % 32
+ *               of word t / 32 set = token t allowed.  mask_index (device) [n_canvas][L] int32: the
+ *               mask row of each position, -1 = none.
+ * Tokens outside [0, V) in the lists are ignored (-1 pads them).  A canvas with offsets outside its
+ * list, a penalty that is not finite or a repetition <= 0 raises DG_DEV_BAD_PARAM and is skipped; a
+ * mask index outside [-1, n_masks) raises it and counts as -1.
+ * Limits: those of dg_denoise_step; ld * sizeof(dtype) and ld_out * sizeof(dtype) multiples of 16;
+ * mask_stride >= ceil(V / 32); list lengths < 2^31.  Errors: DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT,
+ * DG_ERR_UNSUPPORTED (a row of 2^31 bytes or more), DG_ERR_CUDA.  One kernel, no workspace. */
+DG_API dg_status dg_adjust_logits(const void* logits, dg_dtype dtype, int64_t ld, void* out, int64_t ld_out,
+                                  int64_t n_canvas, int32_t L, int64_t V, const dg_canvas_params* params,
+                                  const int32_t* history, const int32_t* cu_history, int64_t total_history,
+                                  const dg_penalties* penalties, const int32_t* bias_tokens,
+                                  const float* bias_values, const int32_t* cu_bias, int64_t total_bias,
+                                  const uint32_t* masks, int64_t mask_stride, int32_t n_masks,
+                                  const int32_t* mask_index, dg_stream_t stream);
+
+/* ------------------------------------------------------------------------------------ */
 /* Self-conditioning [DG "자기 조건화"]:                                                  */
 /*   pe    = P . E,  P = softmax(logits / T) per position, E the token embedding table;  */
 /*   delta = W_down (gelu_tanh(W_gate pe) * (W_up pe)), no bias (gated MLP).            */
