@@ -1,5 +1,4 @@
-// dg_paged.cu -- the paged key / value cache: appending a pass's rotated keys and its values, and
-// attention of a few queries a sequence over the pages.
+// dg_paged.cu -- the paged key / value cache: appending a pass's rotated keys and its values.
 #include <cuda_runtime.h>
 
 #include <math.h>
@@ -159,80 +158,6 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendArgs a
     *reinterpret_cast<uint4*>(dst + e0 + dist) = y;
 }
 
-// ------------------------------------------------------------------ attention, a query head per block
-struct PagedAttnArgs {
-    const uint16_t* q;
-    uint16_t* o;
-    float* lse;
-    const int32_t* cu_q;
-    const uint8_t* causal;
-    int64_t total_q;
-    int32_t n_seq, max_q_len, Hq, Hkv, D, window;
-    float scale;
-    dg::PagedKV kv;
-    unsigned* status;
-};
-
-// One block per (row, query head): its warps take every fourth key, a lane D / 32 dimensions of
-// it; running maximum and sum per warp, joined at the end.
-__global__ void __launch_bounds__(128) k_paged_row(const PagedAttnArgs a) {
-    __shared__ float sm[4], sl[4], so[4][256];
-    dg::pdl_wait();
-    dg::pdl_release();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = (int)blockIdx.x, h = (int)blockIdx.y;
-    const int s = dg::warp_owner(a.cu_q, a.n_seq, t);
-    if (s >= a.n_seq || a.cu_q[s] > t) return;
-    const dg::PagedSeq q = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
-    if (threadIdx.x == 0 && (!q.ok || q.ql > a.max_q_len)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-    if (!q.ok) return;
-    const int pos = q.kl - q.ql + (t - q.q0);
-    const int64_t W = a.window;
-    const int lo = W >= 0 ? (int)max((int64_t)0, pos - W) : 0;
-    const int hi = q.kl == 0 ? -1 : a.causal[s] ? pos : (int)(W >= 0 ? min((int64_t)q.kl - 1, pos + W) : q.kl - 1);
-    const int per = a.D / 32;
-    float qv[8], acc[8];
-    const uint16_t* qr = a.q + ((int64_t)t * a.Hq + h) * a.D + lane * per;
-    for (int e = 0; e < 8; ++e) {
-        qv[e] = e < per ? __uint_as_float((uint32_t)qr[e] << 16) * a.scale : 0.f;
-        acc[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    const int64_t head = (h / (a.Hq / a.Hkv)) * a.kv.head_stride + lane * per;
-    for (int j = lo + warp; j <= hi; j += 4) {
-        const int32_t page = a.kv.page_table[(int64_t)s * a.kv.max_pages + (j >> a.kv.page_shift)];
-        if (page < 0 || page >= a.kv.n_pages) {
-            if (lane == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-            continue;
-        }
-        const int64_t at = page * a.kv.page_stride + (j & ((1 << a.kv.page_shift) - 1)) * a.kv.slot_stride + head;
-        float x = 0.f;
-        for (int e = 0; e < per; ++e) x += qv[e] * __uint_as_float((uint32_t)a.kv.k[at + e] << 16);
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        const float mn = fmaxf(m, x);
-        const float f = m == -INFINITY ? 0.f : expf(m - mn);
-        const float w = mn == -INFINITY ? 0.f : expf(x - mn);
-        l = l * f + w;
-        for (int e = 0; e < per; ++e) acc[e] = acc[e] * f + w * __uint_as_float((uint32_t)a.kv.v[at + e] << 16);
-        m = mn;
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    for (int e = 0; e < per; ++e) so[warp][lane * per + e] = acc[e];
-    __syncthreads();
-    float M = -INFINITY, total = 0.f;
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w]);
-    for (int w = 0; w < 4; ++w) total += sm[w] == -INFINITY ? 0.f : sl[w] * expf(sm[w] - M);
-    for (int d = threadIdx.x; d < a.D; d += 128) {
-        float o = 0.f;
-        for (int w = 0; w < 4; ++w) o += sm[w] == -INFINITY ? 0.f : so[w][d] * expf(sm[w] - M);
-        a.o[((int64_t)t * a.Hq + h) * a.D + d] = (uint16_t)(pack_bf16x2(total > 0.f ? o / total : 0.f, 0.f) & 0xffffu);
-    }
-    if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)t * a.Hq + h] = total > 0.f ? M + logf(total) : -INFINITY;
-}
-
 }  // namespace
 
 namespace dghost {
@@ -308,46 +233,6 @@ extern "C" dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t
     if (blocks > 0x7fffffffLL) return DG_ERR_INVALID_ARG;
     const cudaError_t e = dghost::launch_pdl(interleaved ? k_kv_append<true> : k_kv_append<false>,
                                              dim3((unsigned)blocks), dim3(kAppendThreads), 0, (cudaStream_t)stream, a);
-    dghost::count_launch();
-    return dghost::cuda_status(e);
-}
-
-extern "C" size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv,
-                                                     int32_t D) {
-    return 0;
-}
-
-extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
-                                        const int32_t* cu_q, const uint8_t* causal, int32_t n_seq, int32_t max_q_len,
-                                        int64_t total_q, int32_t Hq, int32_t Hkv, int32_t D, int32_t window,
-                                        float scale, void* workspace, size_t workspace_bytes, dg_stream_t stream) {
-    if (n_seq < 0 || n_seq > 65535 || Hq < 1 || Hq > 65535 || Hkv < 1 || Hq % Hkv != 0 || window < -1 ||
-        !(scale == scale) || scale == INFINITY || scale == -INFINITY)
-        return DG_ERR_INVALID_ARG;
-    if (D != 64 && D != 128 && D != 256) return DG_ERR_UNSUPPORTED;
-    if (max_q_len < 1 || max_q_len > (1 << 30) || total_q < 0 || total_q >= (1LL << 31)) return DG_ERR_INVALID_ARG;
-    if (n_seq == 0 || total_q == 0) return DG_OK;
-    if (!q || !o || !cu_q || !causal) return DG_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(o)) return DG_ERR_ALIGNMENT;
-    PagedAttnArgs a;
-    const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
-    if (ok != DG_OK) return ok;
-    a.q = q;
-    a.o = o;
-    a.lse = lse;
-    a.cu_q = cu_q;
-    a.causal = causal;
-    a.total_q = total_q;
-    a.n_seq = n_seq;
-    a.max_q_len = max_q_len;
-    a.Hq = Hq;
-    a.Hkv = Hkv;
-    a.D = D;
-    a.window = window;
-    a.scale = scale;
-    a.status = dghost::status_word();
-    const cudaError_t e = dghost::launch_pdl(k_paged_row, dim3((unsigned)total_q, (unsigned)Hq), dim3(128), 0,
-                                             (cudaStream_t)stream, a);
     dghost::count_launch();
     return dghost::cuda_status(e);
 }

@@ -1,0 +1,616 @@
+// dg_paged_attn.cu -- attention of a few query rows a sequence over the paged key / value cache.
+//
+// With few query rows the keys and values are read once and each value is used for a handful of
+// multiplications, so the call is bound by memory.  A row here is one (query, query head); the rows that
+// share a key head (Hq / Hkv of every query) make one item of up to 8 NB rows, and an item visits
+// the 64-key tiles that some query of its sequence may see.  All tiles of all items, in order,
+// form one line that is cut into equal runs, one for each of a fixed number of resident CTAs (as many as
+// the SMs hold): every CTA streams the same number of keys whatever the lengths are, and a
+// long sequence is split over as many CTAs as its share of the line takes.  A run's first and last items
+// may be pieces; pieces go to the workspace as (maximum, sum, unnormalised output) and a second
+// kernel joins them in the order of the line.
+//
+// Within a CTA each warp owns 16 keys of a tile and runs on its own: its own ring of stages filled
+// by cp.async, its own running maximum and sum; warps meet only at the end of an item.  The
+// products are taken transposed, S^T = K Q^T and O^T = V^T P^T, with keys (or
+// dimensions) as the 16 rows of mma.m16n8k16 and the query rows as its 8 columns: eight rows fill the
+// instruction, and P^T comes out of the first product's layout by two 8 x 8 register transposes.
+// (The warp instruction, not tcgen05: at 8 rows the products need a few percent of either,
+// and a tile of TMEM would only add a round trip between the two products.)
+#include <cuda_runtime.h>
+
+#include <math.h>
+
+#include <algorithm>
+
+#include "dg_paged.cuh"
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 16;                  // keys of a warp's step
+constexpr int kTileKeys = kWarps * kStep;  // keys of a tile
+constexpr int kMaxCtas = 512;              // grid bound the workspace is sized for
+constexpr float kRescaleAbove = 8.f;       // log2 units the maximum may grow before it moves: P <= 2^8
+
+struct SplitArgs {
+    const uint16_t* q;
+    uint16_t* o;
+    float* lse;
+    const int32_t* cu_q;
+    const uint8_t* causal;
+    int64_t total_q;
+    int32_t n_seq, max_q_len, Hq, Hkv, group, window;
+    float scale_log2;
+    dg::PagedKV kv;
+    float* part_o;    // [grid][2][rows][D]
+    float* part_ml;   // [grid][2][rows][2]
+    int4* desc;       // [grid]: sequence, item of the sequence, CTAs that follow (0: nothing to join)
+    unsigned* status;
+};
+
+template <int D>
+struct SplitCfg {
+    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
+    static constexpr uint32_t kHalf = kStep * D * 2;       // the keys of a step (or its values)
+    static constexpr uint32_t kStage = 2 * kHalf;
+    static constexpr uint32_t kRing = kStages * kStage;    // a warp's ring
+    static constexpr size_t kSmem = (size_t)kWarps * kRing;
+};
+
+DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+DG_DEVINL float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 16 bytes, or zeros when !ok (nothing is read then).
+DG_DEVINL void cp_async16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+DG_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+DG_DEVINL void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+DG_DEVINL void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+DG_DEVINL void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+DG_DEVINL uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+DG_DEVINL void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The keys a query at position pos may see: [lo, hi], empty when hi < lo.
+DG_DEVINL void key_range(int pos, int kl, int window, bool causal, int& lo, int& hi) {
+    const int64_t W = window;
+    lo = W >= 0 ? (int)max((int64_t)0, (int64_t)pos - W) : 0;
+    hi = causal ? min(pos, kl - 1) : W >= 0 ? (int)min((int64_t)kl - 1, (int64_t)pos + W) : kl - 1;
+}
+
+// A sequence on the line: its row tiles, and the key tiles each of its items visits (one when it
+// has queries and no keys, so that its rows get their zeros).
+struct SeqPlan {
+    dg::PagedSeq seq;
+    int row_tiles, tile0, tiles;
+    bool causal;
+    DG_DEVINL int64_t cost(int Hkv) const { return (int64_t)row_tiles * tiles * Hkv; }
+};
+
+template <int Rows>
+DG_DEVINL SeqPlan seq_plan(const SplitArgs& a, int s) {
+    SeqPlan p;
+    p.seq = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+    p.causal = a.causal[s] != 0;
+    p.row_tiles = p.seq.ok ? (int)(((int64_t)p.seq.ql * a.group + Rows - 1) / Rows) : 0;
+    p.tile0 = 0;
+    p.tiles = 1;
+    if (p.row_tiles > 0 && p.seq.kl > 0) {
+        int lo, hi, first, last;
+        key_range(p.seq.kl - p.seq.ql, p.seq.kl, a.window, p.causal, first, hi);
+        key_range(p.seq.kl - 1, p.seq.kl, a.window, p.causal, lo, last);
+        p.tile0 = first / kTileKeys;
+        p.tiles = last / kTileKeys - p.tile0 + 1;
+    }
+    return p;
+}
+
+DG_DEVINL int64_t warp_sum(int64_t v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The line's length and where a CTA's run starts on it.
+struct Run {
+    int64_t total, per_cta, start, end;
+    int seq;            // the sequence at `start`
+    int64_t seq_start;  // and where it begins
+};
+
+template <int Rows>
+DG_DEVINL Run find_run(const SplitArgs& a) {
+    __shared__ int64_t sums[kWarps];
+    __shared__ int64_t found_start;
+    __shared__ int found_seq;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t mine = 0, first_cost = 0;
+    for (int s = tid; s < a.n_seq; s += kThreads) {
+        const SeqPlan p = seq_plan<Rows>(a, s);
+        const int64_t c = p.cost(a.Hkv);
+        if (s == tid) first_cost = c;
+        mine += c;
+        if (blockIdx.x == 0 && (!p.seq.ok || p.seq.ql > a.max_q_len)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+    }
+    mine = warp_sum(mine);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    Run r;
+    r.total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) r.total += sums[w];
+    r.per_cta = max((int64_t)1, (r.total + gridDim.x - 1) / gridDim.x);
+    r.start = min(r.total, (int64_t)blockIdx.x * r.per_cta);
+    r.end = min(r.total, r.start + r.per_cta);
+    r.seq = 0;
+    r.seq_start = 0;
+    if (r.start >= r.end) return r;   // the same for the whole CTA
+    int64_t base = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += kThreads) {
+        const int s = s0 + tid;
+        const int64_t c = s0 == 0 ? first_cost : s < a.n_seq ? seq_plan<Rows>(a, s).cost(a.Hkv) : 0;
+        int64_t incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        __syncthreads();   // the last round's readers of sums are done
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        int64_t before = base, all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += sums[w];
+            all += sums[w];
+        }
+        incl += before;
+        if (c > 0 && incl - c <= r.start && r.start < incl) {
+            found_seq = s;
+            found_start = incl - c;
+        }
+        base += all;
+        if (base > r.start) break;   // the same for the whole CTA
+    }
+    __syncthreads();
+    r.seq = found_seq;
+    r.seq_start = found_start;
+    return r;
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_split(const SplitArgs a) {
+    using C = SplitCfg<D>;
+    constexpr int Rows = 8 * NB;
+    constexpr int KK = D / 16;              // 16-dimension blocks of a head
+    constexpr int Chunks = D / 8;           // 16-byte chunks of a head
+    constexpr int PerLoad = 32 / Chunks;    // key rows a warp's load instruction covers
+    constexpr int Pad = D + 4;              // floats of a row of the meeting buffer: no bank conflicts
+    static_assert(Rows * Pad * 4 <= C::kRing, "a warp's output fits its ring");
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float s_m[kWarps][Rows], s_l[kWarps][Rows];
+    dg::pdl_wait();
+    dg::pdl_release();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Run run = find_run<Rows>(a);
+    if (run.start >= run.end) {
+        if (tid == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    unsigned char* ring = smem + (size_t)warp * C::kRing;
+    const uint32_t ring_s = dg::smem_u32(ring);
+    const int page_mask = (1 << a.kv.page_shift) - 1;
+    const int ch = lane % Chunks, rsub = lane / Chunks;
+    int4 desc = make_int4(0, 0, 0, 0);
+
+    int64_t at = run.start;             // on the line
+    int64_t seq_start = run.seq_start;
+    int s = run.seq;
+    SeqPlan p = seq_plan<Rows>(a, s);
+    while (true) {
+        while (at >= seq_start + p.cost(a.Hkv)) {   // the next sequence that has work
+            seq_start += p.cost(a.Hkv);
+            p = seq_plan<Rows>(a, ++s);
+        }
+        // the piece: tiles t0 .. t1 - 1 of one item
+        const int item = (int)((at - seq_start) / p.tiles);
+        const int t0 = (int)(at - seq_start - (int64_t)item * p.tiles);
+        const int t1 = (int)min((int64_t)p.tiles, t0 + (run.end - at));
+        const int hk = item / p.row_tiles, row0 = (item - hk * p.row_tiles) * Rows;
+        const int n_rows = min(Rows, p.seq.ql * a.group - row0);
+        const int pos0 = p.seq.kl - p.seq.ql;
+        int klo, khi, unused;
+        key_range(pos0 + row0 / a.group, p.seq.kl, a.window, p.causal, klo, unused);
+        key_range(pos0 + (row0 + n_rows - 1) / a.group, p.seq.kl, a.window, p.causal, unused, khi);
+
+        // Q^T as the second operand: lane holds column lane / 4, dimensions 2 (lane % 4) + {0, 1} (+ 8)
+        uint32_t qf[NB][KK][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int r = row0 + nb * 8 + lane / 4;
+            const bool ok = nb * 8 + lane / 4 < n_rows;
+            const int qi = ok ? r / a.group : 0;
+            const uint16_t* src = a.q + ((int64_t)(p.seq.q0 + qi) * a.Hq + hk * a.group + (ok ? r - qi * a.group : 0)) * D +
+                                  (lane & 3) * 2;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                qf[nb][kk][0] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
+                qf[nb][kk][1] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
+            }
+        }
+        // the ranges of this lane's rows of S^T (columns 2 (lane % 4) + {0, 1}); the item's own
+        // narrowest one decides whether a step needs its mask
+        int rlo[NB][2], rhi[NB][2], all_lo, all_hi;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = min(nb * 8 + (lane & 3) * 2 + e, n_rows - 1);
+                key_range(pos0 + (row0 + r) / a.group, p.seq.kl, a.window, p.causal, rlo[nb][e], rhi[nb][e]);
+            }
+        key_range(pos0 + (row0 + n_rows - 1) / a.group, p.seq.kl, a.window, p.causal, all_lo, unused);
+        key_range(pos0 + row0 / a.group, p.seq.kl, a.window, p.causal, unused, all_hi);
+
+        float acc[KK][NB][4];
+#pragma unroll
+        for (int mt = 0; mt < KK; ++mt)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][nb][e] = 0.f;
+        float m[NB][2], l[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
+
+        const int32_t* table = a.kv.page_table + (int64_t)s * a.kv.max_pages;
+        const int64_t head_at = hk * a.kv.head_stride + ch * 8;
+        const int steps = t1 - t0;
+        const int key0 = (p.tile0 + t0) * kTileKeys + warp * kStep;   // first key of this warp's first step
+        // the pages of a step's first and second eight keys (one page when pages hold 16 or more)
+        auto entry = [&](int step, int half) -> int32_t {
+            const int j = key0 + step * kTileKeys + half * 8;
+            return step < steps && j <= khi && j + 7 >= klo ? table[j >> a.kv.page_shift] : -1;
+        };
+        int32_t e0 = entry(0, 0), e1 = entry(0, 1);
+        auto issue = [&](int step) {   // the step's keys and values into its stage; then the next step's pages
+            if (step < steps) {
+                const int j0 = key0 + step * kTileKeys;
+                const uint32_t dst = ring_s + (uint32_t)(step % C::kStages) * C::kStage;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int32_t page = half ? e1 : e0;
+                    const bool good = page >= 0 && page < a.kv.n_pages;
+                    const int jh = j0 + half * 8;
+                    if (!good && jh <= khi && jh + 7 >= klo && lane == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+                    const int64_t off = good ? page * a.kv.page_stride + (int64_t)((jh & page_mask) + rsub) * a.kv.slot_stride + head_at : 0;
+                    const uint16_t* ks = a.kv.k + off;
+                    const uint16_t* vs = a.kv.v + off;
+                    const int64_t hop = good ? PerLoad * a.kv.slot_stride : 0;
+#pragma unroll
+                    for (int i = 0; i < 8 / PerLoad; ++i) {
+                        const int row = half * 8 + i * PerLoad + rsub;
+                        const bool ok = good && j0 + row >= klo && j0 + row <= khi;
+                        const uint32_t d = dst + (uint32_t)row * (D * 2) + (uint32_t)((ch ^ (row & 7)) * 16);
+                        cp_async16(d, ks, ok);
+                        cp_async16(d + C::kHalf, vs, ok);
+                        ks += hop;
+                        vs += hop;
+                    }
+                }
+                e0 = entry(step + 1, 0);
+                e1 = entry(step + 1, 1);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+
+        const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_col = (lane >> 4) & 1;
+        const int v_row = (lane & 7) + ((lane >> 4) & 1) * 8, v_col = (lane >> 3) & 1;
+        for (int step = 0; step < steps; ++step) {
+            cp_async_wait<C::kStages - 2>();
+            __syncwarp();   // every lane's part has landed, and the stage refilled now has been read
+            issue(step + C::kStages - 1);
+            const int j0 = key0 + step * kTileKeys;
+            if (j0 > khi || j0 + kStep - 1 < klo) continue;   // no key of the item
+            const uint32_t st = ring_s + (uint32_t)(step % C::kStages) * C::kStage;
+            float c[NB][2][4];   // S^T, even and odd 16-dimension blocks apart: two chains
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[nb][0][e] = c[nb][1][e] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                uint32_t kf[4];
+                ldmatrix4(kf, st + (uint32_t)k_row * (D * 2) + (uint32_t)(((kk * 2 + k_col) ^ (lane & 7)) * 16));
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma(c[nb][kk & 1], kf, qf[nb][kk][0], qf[nb][kk][1]);
+            }
+            const bool whole = j0 >= all_lo && j0 + kStep - 1 <= all_hi;
+            float x[NB][4];   // [key lane / 4 (+ 8 for 2, 3)][row 2 (lane % 4) + (0, 1)], in log2 units
+            bool grown = false;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[nb][e] = (c[nb][0][e] + c[nb][1][e]) * a.scale_log2;
+                    if (!whole) {
+                        const int j = j0 + lane / 4 + (e & 2) * 4;
+                        if (j < rlo[nb][e & 1] || j > rhi[nb][e & 1]) x[nb][e] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grown = grown || fmaxf(x[nb][e], x[nb][e + 2]) > m[nb][e] + kRescaleAbove;
+            }
+            if (__any_sync(0xffffffffu, grown)) {   // some row's maximum moves: new references, old sums rescaled
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(x[nb][e], x[nb][e + 2]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        mx = fmaxf(mx, m[nb][e]);
+                        const float f = mx == -INFINITY ? 1.f : ex2(m[nb][e] - mx);
+                        l[nb][e] *= f;
+#pragma unroll
+                        for (int mt = 0; mt < KK; ++mt) {
+                            acc[mt][nb][e] *= f;
+                            acc[mt][nb][e + 2] *= f;
+                        }
+                        m[nb][e] = mx;
+                    }
+            }
+            uint32_t pf[NB][2];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float r0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], r1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
+                const float p0 = ex2(x[nb][0] - r0), p1 = ex2(x[nb][1] - r1);
+                const float p2 = ex2(x[nb][2] - r0), p3 = ex2(x[nb][3] - r1);
+                l[nb][0] += p0 + p2;
+                l[nb][1] += p1 + p3;
+                pf[nb][0] = transpose8x8(pack_bf16x2(p0, p1));
+                pf[nb][1] = transpose8x8(pack_bf16x2(p2, p3));
+            }
+#pragma unroll
+            for (int mt = 0; mt < KK; ++mt) {
+                uint32_t vf[4];
+                ldmatrix4_trans(vf, st + C::kHalf + (uint32_t)v_row * (D * 2) + (uint32_t)(((mt * 2 + v_col) ^ (lane & 7)) * 16));
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma(acc[mt][nb], vf, pf[nb][0], pf[nb][1]);
+            }
+        }
+
+        // the warps meet: each leaves its unnormalised output in its own ring, and its statistics
+        cp_async_wait<0>();
+        __syncwarp();
+        float* mo = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nb][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane < 4) {
+                    s_m[warp][nb * 8 + lane * 2 + e] = m[nb][e];
+                    s_l[warp][nb * 8 + lane * 2 + e] = sum;
+                }
+#pragma unroll
+                for (int mt = 0; mt < KK; ++mt) {
+                    const int at_row = (nb * 8 + (lane & 3) * 2 + e) * Pad + mt * 16 + lane / 4;
+                    mo[at_row] = acc[mt][nb][e];
+                    mo[at_row + 8] = acc[mt][nb][e + 2];
+                }
+            }
+        }
+        __syncthreads();
+        const bool starts = t0 == 0, ends = t1 == p.tiles;
+        const int64_t slot = (int64_t)blockIdx.x * 2 + (starts ? 1 : 0);
+        for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+            float L = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - M);
+                L += s_l[w][r] * f;
+                const float4 v = *reinterpret_cast<const float4*>(smem + (size_t)w * C::kRing + ((size_t)r * Pad + d) * 4);
+                o.x += v.x * f;
+                o.y += v.y * f;
+                o.z += v.z * f;
+                o.w += v.w * f;
+            }
+            if (starts && ends) {
+                const int rr = row0 + r, qi = rr / a.group;
+                const int64_t out = (int64_t)(p.seq.q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
+                const float inv = L > 0.f ? 1.f / L : 0.f;
+                *reinterpret_cast<uint2*>(a.o + out * D + d) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                if (d == 0 && a.lse) a.lse[out] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+            } else {
+                *reinterpret_cast<float4*>(a.part_o + (slot * Rows + r) * D + d) = o;
+                if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * Rows + r) * 2) = make_float2(M, L);
+            }
+        }
+        if (starts && !ends) {
+            const int64_t last = (at + p.tiles - 1) / run.per_cta;   // the CTA that has the item's last tile
+            desc = make_int4(s, item, (int)(last - blockIdx.x), 0);
+        }
+        at += steps;
+        if (at >= run.end) break;
+        __syncthreads();   // the meeting buffers are the next piece's rings
+    }
+    if (tid == 0) a.desc[blockIdx.x] = desc;
+}
+
+// Joins an item's pieces: the last one of CTA c (slot 1) and the first ones (slot 0) of the CTAs
+// that follow it, in that order.  blockIdx.x = c, blockIdx.y = 64 of the dimensions.
+template <int D, int NB>
+__global__ void __launch_bounds__(128) k_paged_join(const SplitArgs a) {
+    constexpr int Rows = 8 * NB;
+    __shared__ float w[kMaxCtas][Rows];   // the pieces' weights
+    __shared__ float s_l[Rows], s_m[Rows];
+    dg::pdl_wait();
+    dg::pdl_release();
+    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int4 desc = a.desc[c];
+    if (desc.z == 0) return;
+    const int n = desc.z + 1;
+    const SeqPlan p = seq_plan<Rows>(a, desc.x);
+    const int hk = desc.y / p.row_tiles, row0 = (desc.y - hk * p.row_tiles) * Rows;
+    const int n_rows = min(Rows, p.seq.ql * a.group - row0);
+    auto slot = [&](int i) -> int64_t { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
+    for (int r = warp; r < n_rows; r += 4) {
+        float M = -INFINITY;
+        for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[(slot(i) * Rows + r) * 2]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float L = 0.f;
+        for (int i = lane; i < n; i += 32) {
+            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot(i) * Rows + r) * 2);
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            w[i][r] = f;
+            L += ml.y * f;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) {
+            s_l[r] = L;
+            s_m[r] = M;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < n_rows * 16; i += 128) {
+        const int r = i / 16, d = (int)blockIdx.y * 64 + (i & 15) * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(a.part_o + (slot(k) * Rows + r) * D + d);
+            const float f = w[k][r];
+            o.x += v.x * f;
+            o.y += v.y * f;
+            o.z += v.z * f;
+            o.w += v.w * f;
+        }
+        const float L = s_l[r], inv = L > 0.f ? 1.f / L : 0.f;
+        const int rr = row0 + r, qi = rr / a.group;
+        const int64_t out = (int64_t)(p.seq.q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
+        *reinterpret_cast<uint2*>(a.o + out * D + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (d == 0 && a.lse) a.lse[out] = L > 0.f ? (s_m[r] + log2f(L)) * kLn2 : -INFINITY;
+    }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Rows of an item: 8 when the call's queries and a group fit them, else 16.
+int item_rows(int32_t max_q_len, int32_t group) { return (int64_t)max_q_len * group <= 8 ? 8 : 16; }
+
+size_t split_bytes(int rows, int32_t D) {
+    return (size_t)kMaxCtas * 16 + (size_t)kMaxCtas * 2 * rows * ((size_t)D + 2) * 4;
+}
+
+template <int D, int NB>
+dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
+    using C = SplitCfg<D>;
+    const int sms = dghost::sm_count();
+    if (sms <= 0) return DG_ERR_CUDA;
+    if (cudaFuncSetAttribute(k_paged_split<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
+        cudaSuccess)
+        return DG_ERR_CUDA;
+    const unsigned grid = (unsigned)std::min(sms * C::kCtasPerSm, kMaxCtas);
+    cudaError_t e = dghost::launch_pdl(k_paged_split<D, NB>, dim3(grid), dim3(kThreads), C::kSmem, stream, a);
+    dghost::count_launch();
+    if (e != cudaSuccess) return DG_ERR_CUDA;
+    e = dghost::launch_pdl(k_paged_join<D, NB>, dim3(grid, D / 64), dim3(128), 0, stream, a);
+    dghost::count_launch();
+    return dghost::cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv,
+                                                     int32_t D) {
+    if (n_seq < 1 || max_q_len < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
+    return split_bytes(item_rows(max_q_len, Hq / Hkv), D);
+}
+
+extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
+                                        const int32_t* cu_q, const uint8_t* causal, int32_t n_seq, int32_t max_q_len,
+                                        int64_t total_q, int32_t Hq, int32_t Hkv, int32_t D, int32_t window,
+                                        float scale, void* workspace, size_t workspace_bytes, dg_stream_t stream) {
+    if (n_seq < 0 || n_seq > 65535 || Hq < 1 || Hq > 65535 || Hkv < 1 || Hq % Hkv != 0 || window < -1 ||
+        !(scale == scale) || scale == INFINITY || scale == -INFINITY)
+        return DG_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return DG_ERR_UNSUPPORTED;
+    if (max_q_len < 1 || max_q_len > (1 << 30) || total_q < 0 || total_q >= (1LL << 31)) return DG_ERR_INVALID_ARG;
+    if (n_seq == 0 || total_q == 0) return DG_OK;
+    if (!q || !o || !cu_q || !causal) return DG_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o)) return DG_ERR_ALIGNMENT;
+    SplitArgs a;
+    const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
+    if (ok != DG_OK) return ok;
+    const int rows = item_rows(max_q_len, Hq / Hkv);
+    if (!workspace || workspace_bytes < split_bytes(rows, D)) return DG_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
+    a.q = q;
+    a.o = o;
+    a.lse = lse;
+    a.cu_q = cu_q;
+    a.causal = causal;
+    a.total_q = total_q;
+    a.n_seq = n_seq;
+    a.max_q_len = max_q_len;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.group = Hq / Hkv;
+    a.window = window;
+    a.scale_log2 = scale * kLog2e;
+    a.desc = static_cast<int4*>(workspace);
+    a.part_o = reinterpret_cast<float*>(a.desc + kMaxCtas);
+    a.part_ml = a.part_o + (size_t)kMaxCtas * 2 * rows * D;
+    a.status = dghost::status_word();
+    cudaStream_t st = (cudaStream_t)stream;
+    if (D == 64) return rows == 8 ? launch_split<64, 1>(a, st) : launch_split<64, 2>(a, st);
+    if (D == 128) return rows == 8 ? launch_split<128, 1>(a, st) : launch_split<128, 2>(a, st);
+    return rows == 8 ? launch_split<256, 1>(a, st) : launch_split<256, 2>(a, st);
+}
