@@ -424,66 +424,82 @@ def dg_attention(q, k, v, o, cu_q, cu_kv, causal, max_q_len: int, *, lse=None, w
     return rc
 
 
-def _want(fn, **tensors):
-    """Each tensor has its dtype and shape (None = any extent), is contiguous, and lies on the current
-    device; name=(tensor, dtype, shape).  A tensor of None is skipped."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
-        if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
-            raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be contiguous")
-        _here(fn, name, t)
+def _refuse(fn, name, t, dtype, shape, dev):
+    """Why a tensor is not a contiguous one of dtype and shape (None = any extent) on device dev."""
+    if t.dtype != dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+    raise ValueError(f"{fn}: {name} is on {t.device}, other tensors of the call on device {dev}")
 
 
-def _here(fn, name, t):
-    if not t.is_cuda:
-        raise ValueError(f"{fn}: {name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: {name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+def _whole(fn, name, t, dtype, shape, dev):
+    """The address of a contiguous tensor of dtype and shape on device dev; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(fn, name, t, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _rows(fn, name, t, heads, d):
-    """Row stride of t [tokens, heads, d], whose rows hold [heads][d] without gaps."""
-    if t.dtype != torch.bfloat16:
+def _on(fn, dev, stream):
+    """The raw stream of a call whose tensors are on device dev, the current one."""
+    if dev < 0:
+        raise ValueError(f"{fn}: device tensors expected")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{fn}: the tensors are on device {dev}, the current device is {torch.cuda.current_device()}")
+    return _s(stream)
+
+
+def _rows(fn, name, t, heads, d, dev):
+    """Address and row stride of t [tokens, heads, d], whose rows hold [heads][d] without gaps."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{fn}: {name} must be bfloat16, got {t.dtype}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
         raise ValueError(f"{fn}: {name} must have shape (tokens, {heads}, {d}), got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != d):
         raise ValueError(f"{fn}: {name}'s heads must follow each other")
-    _here(fn, name, t)
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    if t.get_device() != dev:
+        _refuse(fn, name, t, t.dtype, t.shape, dev)
+    return t.data_ptr(), row if t.shape[0] > 1 else heads * d
 
 
 def _paged_kv(fn, k_cache, v_cache, page_table, kv_len):
     """dg_paged_kv of k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides of the first three) and
-    page_table [n_seq, max_pages], kv_len [n_seq] int32."""
+    page_table [n_seq, max_pages], kv_len [n_seq] int32; n_seq, Hkv, D and the device."""
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise TypeError(f"{fn}: {name} must be bfloat16, got {t.dtype}")
         if t.dim() != 4 or t.stride(3) != 1:
             raise ValueError(f"{fn}: {name} must be [n_pages, page_size, Hkv, D] with contiguous heads")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    strides = k_cache.stride()
+    n_pages, page_size, Hkv, D = shape = k_cache.shape
+    if v_cache.shape != shape or v_cache.stride() != strides:
         raise ValueError(f"{fn}: k_cache and v_cache must have one layout")
-    n_pages, page_size, Hkv, D = k_cache.shape
+    dev = k_cache.get_device()
+    if v_cache.get_device() != dev:
+        _refuse(fn, "v_cache", v_cache, v_cache.dtype, (None,) * 4, dev)
     n = kv_len.numel()
-    _want(fn, page_table=(page_table, torch.int32, (n, None)), kv_len=(kv_len, torch.int32, (n,)))
-    _here(fn, "k_cache", k_cache)
-    _here(fn, "v_cache", v_cache)
+    if page_table.dim() != 2:
+        _refuse(fn, "page_table", page_table, torch.int32, (n, None), dev)
+    cols = page_table.shape[1]
+    table = _whole(fn, "page_table", page_table, torch.int32, (n, cols), dev)
+    lens = _whole(fn, "kv_len", kv_len, torch.int32, (n,), dev)
     # the stride of an extent of one says nothing: any valid one will do
-    ps, ss, hs = (s if e > 1 else D for e, s in zip(k_cache.shape[:3], k_cache.stride()[:3]))
-    kv = _PagedKV(_p(k_cache), _p(v_cache), _p(page_table), _p(kv_len), n_pages, ps, ss, hs, page_size,
-                  page_table.shape[1])
-    return kv, n, Hkv, D
+    ps = strides[0] if n_pages > 1 else D
+    ss = strides[1] if page_size > 1 else D
+    hs = strides[2] if Hkv > 1 else D
+    return _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), table, lens, n_pages, ps, ss, hs, page_size, cols), n, Hkv, D, dev
 
 
-def _scratch(fn, nbytes, workspace, device, stream):
-    """The caller's workspace, or one for this call; a fresh one lives until the call's stream passes it."""
+def _scratch(fn, nbytes, workspace, dev, stream):
+    """Address and size of the caller's workspace, or of one for this call; a fresh one lives until the
+    call's stream passes it."""
     if workspace is None:
-        workspace = torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
+        workspace = torch.empty(max(1, nbytes), dtype=torch.uint8, device=dev)
         if stream is not None and _s(stream) != torch.cuda.current_stream().cuda_stream:
             # the allocator orders memory along the current stream: order the call's stream after it and
             # keep the memory until that stream is done with it
@@ -491,9 +507,8 @@ def _scratch(fn, nbytes, workspace, device, stream):
             st.wait_stream(torch.cuda.current_stream())
             workspace.record_stream(st)
         return workspace, nbytes
-    _here(fn, "workspace", workspace)
-    if not workspace.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be contiguous")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(fn, "workspace", workspace, workspace.dtype, workspace.shape, dev)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -506,20 +521,22 @@ def dg_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, *, inv_freq=N
     fn = "dg_kv_append"
     if (q is None) != (q_out is None):
         raise ValueError(f"{fn}: q and q_out come together")
-    kv, n, Hkv, D = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
+    kv, n, Hkv, D, dev = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
     total = k.shape[0]
-    ldk, ldv = _rows(fn, "k", k, Hkv, D), _rows(fn, "v", v, Hkv, D)
-    Hq, ldq = Hkv, 0
+    kp, ldk = _rows(fn, "k", k, Hkv, D, dev)
+    vp, ldv = _rows(fn, "v", v, Hkv, D, dev)
+    Hq, qp, ldq, op = Hkv, None, 0, None
     if q is not None:
         Hq = q.shape[1] if q.dim() == 3 else 0
-        ldq = _rows(fn, "q", q, Hq, D)
-        _want(fn, q_out=(q_out, torch.bfloat16, (total, Hq, D)))
+        qp, ldq = _rows(fn, "q", q, Hq, D, dev)
+        op = _whole(fn, "q_out", q_out, torch.bfloat16, (total, Hq, D), dev)
     if v.shape[0] != total or (q is not None and q.shape[0] != total):
         raise ValueError(f"{fn}: q, k and v must have as many rows")
-    _want(fn, cu_q=(cu_q, torch.int32, (n + 1,)), inv_freq=(inv_freq, torch.float64, (None,)))
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    rc = load().dg_kv_append(_p(k), ldk, _p(v), ldv, _p(q), ldq, _p(q_out), _p(cu_q), n, total, Hq, Hkv, D,
-                             _p(inv_freq), rot, int(bool(interleaved)), ctypes.byref(kv), _s(stream))
+    cu = _whole(fn, "cu_q", cu_q, torch.int32, (n + 1,), dev)
+    half = 0 if inv_freq is None else inv_freq.numel()
+    wp = _whole(fn, "inv_freq", inv_freq, torch.float64, (half,), dev)
+    rc = load().dg_kv_append(kp, ldk, vp, ldv, qp, ldq, op, cu, n, total, Hq, Hkv, D, wp, 2 * half,
+                             1 if interleaved else 0, ctypes.byref(kv), _on(fn, dev, stream))
     if check:
         _check(fn, rc)
     return rc
@@ -535,17 +552,20 @@ def dg_paged_attention(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal,
     """dg_attention over the paged cache of dg_kv_append: q, o [total_q, Hq, D] bf16, cu_q [n + 1] and
     kv_len [n] int32, causal [n] uint8, lse [total_q, Hq] float32."""
     fn = "dg_paged_attention"
-    kv, n, Hkv, D = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
+    kv, n, Hkv, D, dev = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
     total, Hq = (q.shape[0], q.shape[1]) if q.dim() == 3 else (0, 0)
-    _want(fn, q=(q, torch.bfloat16, (total, Hq, D)), o=(o, torch.bfloat16, (total, Hq, D)),
-          lse=(lse, torch.float32, (total, Hq)), cu_q=(cu_q, torch.int32, (n + 1,)),
-          causal=(causal, torch.uint8, (n,)))
+    bf = torch.bfloat16
+    qp = _whole(fn, "q", q, bf, (total, Hq, D), dev)
+    op = _whole(fn, "o", o, bf, (total, Hq, D), dev)
+    lp = _whole(fn, "lse", lse, torch.float32, (total, Hq), dev)
+    cu = _whole(fn, "cu_q", cu_q, torch.int32, (n + 1,), dev)
+    cz = _whole(fn, "causal", causal, torch.uint8, (n,), dev)
     scale = 1.0 / float(D) ** 0.5 if scale is None else float(scale)
-    need = dg_paged_attention_workspace_bytes(n, int(max_q_len), Hq, Hkv, D)
-    workspace, ws_bytes = _scratch(fn, need, workspace, q.device, stream)
-    rc = load().dg_paged_attention(_p(q), ctypes.byref(kv), _p(o), _p(lse), _p(cu_q), _p(causal), n,
-                                   int(max_q_len), total, Hq, Hkv, D, int(window), scale, _p(workspace),
-                                   ws_bytes, _s(stream))
+    st = _on(fn, dev, stream)
+    need = 0 if workspace is not None else load().dg_paged_attention_workspace_bytes(n, int(max_q_len), Hq, Hkv, D)
+    workspace, ws_bytes = _scratch(fn, need, workspace, dev, stream)
+    rc = load().dg_paged_attention(qp, ctypes.byref(kv), op, lp, cu, cz, n, int(max_q_len), total, Hq, Hkv, D,
+                                   int(window), scale, workspace.data_ptr(), ws_bytes, st)
     if check:
         _check(fn, rc)
     return rc
@@ -559,12 +579,11 @@ def dg_adjust_logits(logits, params, out=None, *, history=None, cu_history=None,
     (in place when None).  history / bias lists are packed, canvas c's at cu[c] .. cu[c + 1]."""
     fn = "dg_adjust_logits"
     out = logits if out is None else out
-    if logits.dim() != 3 or out.dim() != 3 or out.shape[:2] != logits.shape[:2]:
+    if logits.dim() != 3 or out.dim() != 3:
         raise ValueError(f"{fn}: logits and out must be [n, L, ld]")
-    dt = _dtype_code(logits)
-    if out.dtype != logits.dtype:
-        raise TypeError(f"{fn}: out must be {logits.dtype}, got {out.dtype}")
+    dt, dtype = _dtype_code(logits), logits.dtype
     n, L, ld = logits.shape
+    ldo = out.shape[2]
     V = ld if V is None else V
     if (history is None) != (cu_history is None) or (history is None) != (penalties is None):
         raise ValueError(f"{fn}: history, cu_history and penalties come together")
@@ -572,18 +591,23 @@ def dg_adjust_logits(logits, params, out=None, *, history=None, cu_history=None,
         raise ValueError(f"{fn}: bias_tokens, bias_values and cu_bias come together")
     if (masks is None) != (mask_index is None):
         raise ValueError(f"{fn}: masks and mask_index come together")
+    i32, f32, dev = torch.int32, torch.float32, logits.get_device()
     nh = 0 if history is None else history.numel()
     nb = 0 if bias_tokens is None else bias_tokens.numel()
-    _want(fn, logits=(logits, logits.dtype, (n, L, ld)), out=(out, out.dtype, (n, L, None)),
-          history=(history, torch.int32, (nh,)), cu_history=(cu_history, torch.int32, (n + 1,)),
-          penalties=(penalties, torch.float32, (n, 3)), bias_tokens=(bias_tokens, torch.int32, (nb,)),
-          bias_values=(bias_values, torch.float32, (nb,)), cu_bias=(cu_bias, torch.int32, (n + 1,)),
-          masks=(masks, torch.int32, (None, None)), mask_index=(mask_index, torch.int32, (n, L)))
-    _want(fn, params=(params, torch.uint8, (n * PARAM_BYTES,)))
-    n_masks, words = (0, 0) if masks is None else masks.shape
-    rc = load().dg_adjust_logits(_p(logits), dt, ld, _p(out), out.shape[2], n, L, V, _p(params), _p(history),
-                                 _p(cu_history), nh, _p(penalties), _p(bias_tokens), _p(bias_values),
-                                 _p(cu_bias), nb, _p(masks), words, n_masks, _p(mask_index), _s(stream))
+    n_masks, words = (0, 0) if masks is None else masks.shape if masks.dim() == 2 else (-1, -1)
+    xp = _whole(fn, "logits", logits, dtype, (n, L, ld), dev)
+    op = _whole(fn, "out", out, dtype, (n, L, ldo), dev)
+    pp = _whole(fn, "params", params, torch.uint8, (n * PARAM_BYTES,), dev)
+    hp = _whole(fn, "history", history, i32, (nh,), dev)
+    ch = _whole(fn, "cu_history", cu_history, i32, (n + 1,), dev)
+    pen = _whole(fn, "penalties", penalties, f32, (n, 3), dev)
+    bt = _whole(fn, "bias_tokens", bias_tokens, i32, (nb,), dev)
+    bv = _whole(fn, "bias_values", bias_values, f32, (nb,), dev)
+    cb = _whole(fn, "cu_bias", cu_bias, i32, (n + 1,), dev)
+    mp = _whole(fn, "masks", masks, i32, (n_masks, words), dev)
+    mi = _whole(fn, "mask_index", mask_index, i32, (n, L), dev)
+    rc = load().dg_adjust_logits(xp, dt, ld, op, ldo, n, L, V, pp, hp, ch, nh, pen, bt, bv, cb, nb, mp, words,
+                                 n_masks, mi, _on(fn, dev, stream))
     if check:
         _check(fn, rc)
     return rc

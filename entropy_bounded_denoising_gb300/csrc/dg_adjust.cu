@@ -20,7 +20,8 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 8;   // rows in flight a thread
+constexpr int kUnroll = 4;   // rows in flight a thread
+constexpr int kMaxRows = 64; // rows of a block, at most
 
 struct AdjustArgs {
     const unsigned char* x;
@@ -46,15 +47,53 @@ DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
     return v;
 }
 
+// The penalties and biases of a vector's edited tokens: one fma each, by 1 / repetition or repetition
+// (1 for a token without a count) and the token's addend.
+template <int Bytes>
+DG_DEVINL void edit(uint4& y, uint32_t edited, uint32_t penalised, float down, float up, const float (&add)[16 / Bytes]) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+    for (int e = 0; e < 16 / Bytes; ++e) {
+        const int i = Bytes == 2 ? e / 2 : e;
+        const bool high = Bytes == 2 && (e & 1);
+        const float v = __uint_as_float(Bytes == 4 ? w[i] : high ? w[i] & 0xffff0000u : w[i] << 16);
+        const float f = !(penalised >> e & 1) ? 1.f : v > 0.f ? down : up;
+        const float z = fmaf(v, f, add[e]);
+        const uint32_t p = Bytes == 4 ? __float_as_uint(z) : pack_bf16x2(z, z);
+        const uint32_t bits = Bytes == 4 ? p : high ? (w[i] & 0xffffu) | (p & 0xffff0000u) : (w[i] & 0xffff0000u) | (p & 0xffffu);
+        if (edited >> e & 1) w[i] = bits;
+    }
+}
+
+// -inf for the tokens whose bit of `keep` is clear.
+template <int Bytes>
+DG_DEVINL void exclude(uint4& y, uint32_t keep, const uint2* expand) {
+    if (Bytes == 2) {
+        const uint2 a = expand[keep & 15u], b = expand[keep >> 4];
+        y.x = (y.x & a.x) | (0xff80ff80u & ~a.x);
+        y.y = (y.y & a.y) | (0xff80ff80u & ~a.y);
+        y.z = (y.z & b.x) | (0xff80ff80u & ~b.x);
+        y.w = (y.w & b.y) | (0xff80ff80u & ~b.y);
+    } else {
+        y.x = keep & 1u ? y.x : 0xff800000u;
+        y.y = keep & 2u ? y.y : 0xff800000u;
+        y.z = keep & 4u ? y.z : 0xff800000u;
+        y.w = keep & 8u ? y.w : 0xff800000u;
+    }
+}
+
 // Bytes: 2 (bf16) or 4 (fp32) a logit; PerVec tokens in 16 bytes.
 template <int Bytes>
-__global__ void __launch_bounds__(kThreads) k_adjust(const AdjustArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
     constexpr int PerVec = 16 / Bytes;
     constexpr int kSlice = kThreads * PerVec;   // tokens of a block
-    constexpr uint32_t kAll = (1u << PerVec) - 1u;
+    constexpr uint32_t kAll = 0xffu;            // a mask byte
     __shared__ int32_t n_hist[kSlice];          // occurrences in the history
     __shared__ int32_t n_bias[kSlice];          // entries in the bias list
     __shared__ int32_t first_bias[kSlice];      // the first of them
+    __shared__ int32_t row_mask[kMaxRows];
+    __shared__ uint2 expand[16];
+    constexpr uint32_t kNegInf = Bytes == 2 ? 0xff80ff80u : 0xff800000u;
     dg::pdl_wait();
     dg::pdl_release();
     const int tid = threadIdx.x;
@@ -97,10 +136,12 @@ __global__ void __launch_bounds__(kThreads) k_adjust(const AdjustArgs a) {
         }
         __syncthreads();
         const int end = min(kSlice, a.V - slice0);
+#pragma unroll 4
         for (int i = h0 + tid; i < h1; i += kThreads) {
             const int64_t t = (int64_t)a.history[i] - slice0;
             if (t >= 0 && t < end) atomicAdd(&n_hist[t], 1);
         }
+#pragma unroll 4
         for (int i = b0 + tid; i < b1; i += kThreads) {
             const int64_t t = (int64_t)a.bias_tokens[i] - slice0;
             if (t >= 0 && t < end) {
@@ -128,78 +169,70 @@ __global__ void __launch_bounds__(kThreads) k_adjust(const AdjustArgs a) {
         }
         edited |= penalised;
     }
+    // what keeps an excluded token's logit: words of ones where four tokens' bits are set (bf16 pairs)
+    if (Bytes == 2 && tid < 16)
+        expand[tid] = make_uint2(((tid & 1) ? 0xffffu : 0u) | ((tid & 2) ? 0xffff0000u : 0u),
+                                 ((tid & 4) ? 0xffffu : 0u) | ((tid & 8) ? 0xffff0000u : 0u));
+    const int r0 = (int)blockIdx.y * a.rows, r1 = min(a.L, r0 + a.rows);
+    for (int r = tid; r < a.rows; r += kThreads) {   // the rows' masks; -1 = none
+        int m = -1;
+        if (a.masks && r0 + r < r1) {
+            m = a.mask_index[c * a.L + r0 + r];
+            if (m < -1 || m >= a.n_masks) {
+                if (blockIdx.x == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+                m = -1;
+            }
+        }
+        row_mask[r] = m;
+    }
+    __syncthreads();
     if (v0 >= a.V) return;
     const int n_mine = min(PerVec, a.V - v0);                  // tokens of the vector inside the vocabulary
     const uint32_t mine = (1u << n_mine) - 1u;
+    const float down = 1.f / pen.repetition;
     const bool in_place = a.out == a.x;
-    constexpr uint32_t kNegInf = Bytes == 2 ? 0xff80ff80u : 0xff800000u;
+    const bool quiet = in_place && edited == 0;                // nothing to write where nothing is excluded
+    const unsigned char* mask_at = reinterpret_cast<const unsigned char*>(a.masks) + (v0 >> 3);
+    const int64_t mask_pitch = a.mask_stride * 4;
+    const unsigned char* src = a.x + (c * a.L + r0) * a.ld_bytes + (int64_t)v0 * Bytes;
+    unsigned char* dst = a.out + (c * a.L + r0) * a.ld_out_bytes + (int64_t)v0 * Bytes;
 
-    const int r0 = (int)blockIdx.y * a.rows, r1 = min(a.L, r0 + a.rows);
-    for (int r = r0; r < r1; r += kUnroll) {
+    for (int r = 0; r < r1 - r0; r += kUnroll, src += kUnroll * a.ld_bytes, dst += kUnroll * a.ld_out_bytes) {
         uint32_t keep[kUnroll];   // allowed tokens
         uint4 x[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            keep[u] = mine;
-            if (a.masks && r + u < r1) {
-                const int m = a.mask_index[c * a.L + r + u];
-                if (m >= 0 && m < a.n_masks) {
-                    const uint32_t w = reinterpret_cast<const unsigned char*>(a.masks + m * a.mask_stride)[v0 >> 3];
-                    keep[u] = mine & (w >> (v0 & 7));
-                } else if (m != -1 && tid == 0 && blockIdx.x == 0) {
-                    dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-                }
-            }
+        for (int u = 0; u < kUnroll; ++u) {   // rows is a multiple of kUnroll: row_mask covers r + u
+            const int m = row_mask[r + u];
+            keep[u] = kAll;
+            if (m >= 0) keep[u] = (uint32_t)mask_at[m * mask_pitch];
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            if (r + u < r1 && keep[u] != 0 && !(in_place && keep[u] == mine && edited == 0))
-                x[u] = *reinterpret_cast<const uint4*>(a.x + (c * a.L + r + u) * a.ld_bytes + (int64_t)v0 * Bytes);
+        for (int u = 0; u < kUnroll; ++u) {
+            keep[u] = (Bytes == 4 ? keep[u] >> (v0 & 4) : keep[u]) & mine;
+            if (r + u < r1 - r0 && keep[u] != 0 && !(quiet && keep[u] == mine))
+                x[u] = *reinterpret_cast<const uint4*>(src + u * a.ld_bytes);
+        }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (r + u >= r1 || (in_place && keep[u] == mine && edited == 0)) continue;
-            unsigned char* dst = a.out + (c * a.L + r + u) * a.ld_out_bytes + (int64_t)v0 * Bytes;
+            if (r + u >= r1 - r0 || (quiet && keep[u] == mine)) continue;
             uint4 y = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
             if (keep[u] != 0) {
                 y = x[u];
-                uint32_t* w = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-                for (int e = 0; e < PerVec; ++e) {
-                    const int i = Bytes == 2 ? e / 2 : e;
-                    const bool high = Bytes == 2 && (e & 1);
-                    uint32_t bits = w[i];
-                    if (edited >> e & 1) {
-                        float v = Bytes == 4 ? __uint_as_float(bits)
-                                             : __uint_as_float(high ? bits & 0xffff0000u : bits << 16);
-                        if (penalised >> e & 1) v = v > 0.f ? v / pen.repetition : v * pen.repetition;
-                        v += add[e];
-                        if (Bytes == 4) {
-                            bits = __float_as_uint(v);
-                        } else {
-                            const uint32_t p = pack_bf16x2(v, v);
-                            bits = high ? (bits & 0xffffu) | (p & 0xffff0000u) : (bits & 0xffff0000u) | (p & 0xffffu);
-                        }
-                    }
-                    if (!(keep[u] >> e & 1)) {
-                        if (Bytes == 4)
-                            bits = 0xff800000u;
-                        else
-                            bits = high ? (bits & 0xffffu) | 0xff800000u : (bits & 0xffff0000u) | 0xff80u;
-                    }
-                    w[i] = bits;
-                }
+                if (edited) edit<Bytes>(y, edited, penalised, down, pen.repetition, add);
+                exclude<Bytes>(y, keep[u], expand);
             }
+            unsigned char* at = dst + u * a.ld_out_bytes;
             if (n_mine == PerVec) {
-                *reinterpret_cast<uint4*>(dst) = y;
+                *reinterpret_cast<uint4*>(at) = y;
             } else {   // the row's last vector: nothing past column V is written
 #pragma unroll
                 for (int e = 0; e < PerVec; ++e) {
                     if (e >= n_mine) break;
                     const uint32_t w = reinterpret_cast<const uint32_t*>(&y)[Bytes == 2 ? e / 2 : e];
                     if (Bytes == 2)
-                        reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(e & 1 ? w >> 16 : w);
+                        reinterpret_cast<uint16_t*>(at)[e] = (uint16_t)(e & 1 ? w >> 16 : w);
                     else
-                        reinterpret_cast<uint32_t*>(dst)[e] = w;
+                        reinterpret_cast<uint32_t*>(at)[e] = w;
                 }
             }
         }
@@ -238,7 +271,6 @@ extern "C" dg_status dg_adjust_logits(const void* logits, dg_dtype dtype, int64_
     a.ld_out_bytes = ld_out * es;
     a.L = L;
     a.V = (int32_t)V;
-    a.rows = 64;
     a.params = params;
     a.history = history;
     a.cu_history = cu_history;
@@ -253,8 +285,14 @@ extern "C" dg_status dg_adjust_logits(const void* logits, dg_dtype dtype, int64_
     a.mask_stride = mask_stride;
     a.n_masks = n_masks;
     a.status = dghost::status_word();
-    const int64_t slice = kThreads * (16 / es);
-    const dim3 grid((unsigned)((V + slice - 1) / slice), (unsigned)((L + a.rows - 1) / a.rows), (unsigned)n_canvas);
+    const int sms = dghost::sm_count();
+    if (sms <= 0) return DG_ERR_CUDA;
+    const int64_t slice = kThreads * (16 / es), slices = (V + slice - 1) / slice;
+    // rows of a block: as many as leave eight blocks an SM (a block's lists are then read for up to 64
+    // rows), and at least what a thread keeps in flight
+    const int64_t rows = slices * n_canvas * L / (8 * (int64_t)sms) / kUnroll * kUnroll;
+    a.rows = (int32_t)std::max<int64_t>(kUnroll, std::min<int64_t>(kMaxRows, rows));
+    const dim3 grid((unsigned)slices, (unsigned)((L + a.rows - 1) / a.rows), (unsigned)n_canvas);
     const cudaError_t e = dghost::launch_pdl(es == 2 ? k_adjust<2> : k_adjust<4>, grid, dim3(kThreads), 0,
                                              (cudaStream_t)stream, a);
     dghost::count_launch();
