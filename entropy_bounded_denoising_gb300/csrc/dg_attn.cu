@@ -35,7 +35,7 @@
 
 #include <algorithm>
 
-#include "dg_common.cuh"
+#include "dg_paged.cuh"
 
 namespace {
 
@@ -61,6 +61,11 @@ struct AttnArgs {
     int64_t total_q, total_kv;
     float scale_log2;       // scale * log2(e)
     unsigned* status;
+    // keys in pages (dg_paged_attention): the cache in place of cu_kv; the products' sign flips when the
+    // scale is negative (scale_log2 is then its magnitude, so that the largest score stays the largest)
+    dg::PagedKV kv;
+    int32_t n_seq;
+    int32_t negate;
 };
 
 struct __align__(8) AttnShared {
@@ -111,25 +116,27 @@ constexpr int kThreads = 192;
 struct TileRange {
     int q0, ql, k0, kl;   // sequence offsets and lengths
     int pmin, pmax;       // positions of the tile's first and last real query
+    int jlo, jhi;         // first and last key some query of the tile may see
     int jt_lo, nt;        // first key tile and count
     bool causal;
 };
 
+template <bool Paged>
 DG_DEVINL TileRange tile_range(const AttnArgs& a, int s, int t) {
     TileRange r;
     r.q0 = a.cu_q[s];
     r.ql = a.cu_q[s + 1] - r.q0;
-    r.k0 = a.cu_kv[s];
-    r.kl = a.cu_kv[s + 1] - r.k0;
+    r.k0 = Paged ? 0 : a.cu_kv[s];
+    r.kl = Paged ? a.kv.kv_len[s] : a.cu_kv[s + 1] - r.k0;
     r.causal = a.causal[s] != 0;
     const int off = r.kl - r.ql;
     r.pmin = off + t * kTile;
     r.pmax = off + min(r.ql, t * kTile + kTile) - 1;
     const int64_t W = a.window;
-    const int jlo = W >= 0 ? (int)max((int64_t)0, (int64_t)r.pmin - W) : 0;
-    const int jhi = r.causal ? r.pmax : (W >= 0 ? (int)min((int64_t)r.kl - 1, (int64_t)r.pmax + W) : r.kl - 1);
-    r.jt_lo = jlo / kKeys;
-    r.nt = jhi >= jlo ? jhi / kKeys - r.jt_lo + 1 : 0;
+    r.jlo = W >= 0 ? (int)max((int64_t)0, (int64_t)r.pmin - W) : 0;
+    r.jhi = r.causal ? r.pmax : (W >= 0 ? (int)min((int64_t)r.kl - 1, (int64_t)r.pmax + W) : r.kl - 1);
+    r.jt_lo = r.jlo / kKeys;
+    r.nt = r.jhi >= r.jlo ? r.jhi / kKeys - r.jt_lo + 1 : 0;
     return r;
 }
 
@@ -264,6 +271,7 @@ DG_DEVINL void do_abort(AttnShared& sh, unsigned* status) {
 constexpr int kCostBuckets = 1024;
 constexpr int kPlanHeader = 4;  // ints before the items: the item count, a one-cost flag, a 64-bit work counter
 
+template <bool Paged>
 __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_seq, int32_t max_q_tiles,
                                                     int32_t* __restrict__ plan) {
     __shared__ int count[kCostBuckets];
@@ -275,7 +283,16 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
     const int64_t pairs = (int64_t)n_seq * max_q_tiles;
     auto item_key = [&](int64_t f, int& key) -> bool {  // false: no item (past the queries or bad)
         const int s = (int)(f / max_q_tiles), t = (int)(f % max_q_tiles);
-        const TileRange r = tile_range(a, s, t);
+        if constexpr (Paged) {
+            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+            if (t == 0 && (!p.ok || p.ql > (int64_t)max_q_tiles * kTile)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+            if (!p.ok || p.kl == 0 || (int64_t)t * kTile >= p.ql) return false;
+        }
+        const TileRange r = tile_range<Paged>(a, s, t);
+        if constexpr (Paged) {
+            key = kCostBuckets - 1 - min(r.nt, kCostBuckets - 1);
+            return true;
+        }
         const bool bad = r.q0 < 0 || r.k0 < 0 || r.ql < 0 || (int64_t)r.q0 + r.ql > a.total_q ||
                          (int64_t)r.k0 + r.kl > a.total_kv || r.ql > r.kl;
         if (t == 0 && (bad || r.ql > max_q_tiles * kTile)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
@@ -329,7 +346,12 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
 // above).  Every ring, buffer and barrier phase is counted over the CTA's whole run (g: its key
 // tiles so far, k: its items so far), so the next item's Q and K / V loads and its first S MMA
 // overlap the current item's last tiles and its epilogue.
-template <int D>
+//
+// With Paged the key and value tiles come page by page (one TMA box of min(page, 64) slots each,
+// zeros where no query sees the page), the rows of the value tiles that no query of the item sees
+// are zeroed before the product (what their slots hold is nobody's; their weights are 0, but 0 * NaN is not),
+// and the sequences without keys get their rows of zeros from the CTAs on their way in.
+template <int D, bool Paged>
 __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     k_attention(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const AttnArgs a, const int32_t* __restrict__ plan) {
@@ -344,6 +366,17 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     AttnShared& sh = *reinterpret_cast<AttnShared*>(smem + kOffBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t n_work = (int64_t)plan[0] * a.Hq;
+    if constexpr (Paged) {
+        for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
+            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+            if (!p.ok || p.kl != 0) continue;
+            const int64_t first = (int64_t)p.q0 * a.Hq, rows = (int64_t)p.ql * a.Hq;
+            for (int64_t i = threadIdx.x; i < rows * (kHead / 8); i += kThreads)
+                reinterpret_cast<uint4*>(a.o + first * kHead)[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse)
+                for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[first + i] = -INFINITY;
+        }
+    }
     if ((int64_t)blockIdx.x >= n_work) return;  // the whole CTA: no work
     const int2* items = reinterpret_cast<const int2*>(plan + kPlanHeader);
     const int group = a.Hq / a.Hkv;
@@ -436,19 +469,49 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
                 if (w < 0) break;
                 const int2 it = items[w / a.Hq];
                 const int hk = (int)(w % a.Hq) / group;
-                const TileRange r = tile_range(a, it.x, it.y);
+                const TileRange r = tile_range<Paged>(a, it.x, it.y);
                 for (int i = 0; i < r.nt; ++i, ++g) {
                     const int st = (int)(g & 1u);
+                    int32_t pages[8];  // of the tile's boxes, read before the wait; n_pages reads zeros
+                    const int box_shift = Paged ? min(a.kv.page_shift, 6) : 6, boxes = kKeys >> box_shift;
+                    const int j0 = (r.jt_lo + i) * kKeys;
+                    if constexpr (Paged) {
+                        const int32_t* table = a.kv.page_table + (int64_t)it.x * a.kv.max_pages;
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const int j = j0 + (b << box_shift);
+                            if (b < boxes) {
+                                const bool seen = j <= r.jhi && r.jlo - j < (1 << box_shift);
+                                pages[b] = seen ? table[j >> a.kv.page_shift] : (int32_t)a.kv.n_pages;
+                                if (pages[b] < 0 || pages[b] >= a.kv.n_pages) {
+                                    if (seen) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+                                    pages[b] = (int32_t)a.kv.n_pages;
+                                }
+                            }
+                        }
+                    }
                     if (!attn_wait(&empty[st], ((g >> 1) & 1u) ^ 1u)) {
                         ok = false;
                         break;
                     }
                     dg::mbar_arrive_expect_tx(&full[st], kKVBytes);
-                    const int krow = r.k0 + (r.jt_lo + i) * kKeys;
                     unsigned char* dst = ring + st * kKVBytes;
+                    if constexpr (Paged) {
 #pragma unroll
-                    for (int c = 0; c < kHead / kSub; ++c)
-                        dg::tma_load_2d(dst + c * kKSub, tm, hk * kHead + c * kSub, krow, &full[st]);
+                        for (int b = 0; b < 8; ++b) {
+                            if (b >= boxes) break;
+                            const int row = b << box_shift;
+                            const int slot = (j0 + row) & ((1 << a.kv.page_shift) - 1);
+#pragma unroll
+                            for (int c = 0; c < kHead / kSub; ++c)
+                                dg::tma_load_4d(dst + c * kKSub + row * kSub * 2, tm, c * kSub, slot, hk, pages[b], &full[st]);
+                        }
+                    } else {
+                        const int krow = r.k0 + j0;
+#pragma unroll
+                        for (int c = 0; c < kHead / kSub; ++c)
+                            dg::tma_load_2d(dst + c * kKSub, tm, hk * kHead + c * kSub, krow, &full[st]);
+                    }
                     ++issued[st];
                 }
             }
@@ -469,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
                 const int64_t w = round_robin ? rr_item(kq) : take_item(sh, kq, ok);
                 if (w < 0) break;
                 const int2 it = items[w / a.Hq];
-                const TileRange r = tile_range(a, it.x, it.y);
+                const TileRange r = tile_range<Paged>(a, it.x, it.y);
                 if (!attn_wait(&sh.qfull, kq & 1u)) {
                     ok = false;
                     break;
@@ -537,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
             if (w < 0) break;
             const int2 it = items[w / a.Hq];
             const int h = (int)(w % a.Hq);
-            const TileRange r = tile_range(a, it.x, it.y);
+            const TileRange r = tile_range<Paged>(a, it.x, it.y);
             const int t = it.y;
             const int pos = r.kl - r.ql + t * kTile + row;
             const bool row_valid = t * kTile + row < r.ql;
@@ -566,6 +629,27 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
                 if (lane == 0) dg::mbar_arrive(&sh.sempty);  // S free for the next tile's S
                 const int jt = r.jt_lo + i;
                 const int j0 = jt * kKeys;
+                if constexpr (Paged) {
+                    if (a.negate) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[c][e] = -x[c][e];
+                    }
+                    if (j0 < r.jlo || j0 + kKeys - 1 > r.jhi) {  // the value rows nobody sees
+                        if (!attn_wait_warp(&sh.vfull[gi & 1u], (gi >> 1) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        unsigned char* vt = smem + kOffV + (gi & 1u) * kKVBytes;
+                        for (int z = row; z < kKeys * (int)(kKVBytes / kKSub) * 8; z += 128) {  // 16-byte chunks
+                            const int kx = (z >> 3) & (kKeys - 1);
+                            if (j0 + kx < r.jlo || j0 + kx > r.jhi)
+                                reinterpret_cast<uint4*>(vt)[z] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        dg::fence_proxy_async_smem();  // before the P V product reads them (pfull below)
+                    }
+                }
                 if (!tile_full(r, a.window, jt)) {
                     // masked entries: -inf, which 2^x maps to 0.  The keys a query at position pos may
                     // see form one range: j < kv_len, j <= pos if causal, and with a window W also
@@ -738,7 +822,7 @@ extern "C" dg_status dg_attention(const uint16_t* q, const uint16_t* k, const ui
     if (!tmap_heads(&tq, q, total_q, Hq, D, kTile) || !tmap_heads(&tk, k, total_kv, Hkv, D, kKeys) ||
         !tmap_heads(&tv, v, total_kv, Hkv, D, kKeys))
         return DG_ERR_CUDA;
-    AttnArgs a;
+    AttnArgs a = {};
     a.cu_q = cu_q;
     a.cu_kv = cu_kv;
     a.causal = causal;
@@ -753,7 +837,7 @@ extern "C" dg_status dg_attention(const uint16_t* q, const uint16_t* k, const ui
     a.status = dghost::status_word();
     int32_t* plan = static_cast<int32_t*>(workspace);
     cudaStream_t st = (cudaStream_t)stream;
-    k_attn_plan<<<1, 1024, 0, st>>>(a, n_seq, max_q_tiles, plan);
+    k_attn_plan<false><<<1, 1024, 0, st>>>(a, n_seq, max_q_tiles, plan);
     dghost::count_launch();
     if (cudaGetLastError() != cudaSuccess) return DG_ERR_CUDA;
     // persistent CTAs (two or one per SM by D), fewer when there is less work (the device knows
@@ -767,7 +851,66 @@ extern "C" dg_status dg_attention(const uint16_t* q, const uint16_t* k, const ui
         dghost::count_launch();
         return dghost::cuda_status(cudaGetLastError());
     };
-    if (D == 64) return launch(k_attention<64>, AttnCfg<64>::kSmem, AttnCfg<64>::kCtasPerSm);
-    if (D == 128) return launch(k_attention<128>, AttnCfg<128>::kSmem, AttnCfg<128>::kCtasPerSm);
-    return launch(k_attention<256>, AttnCfg<256>::kSmem, AttnCfg<256>::kCtasPerSm);
+    if (D == 64) return launch(k_attention<64, false>, AttnCfg<64>::kSmem, AttnCfg<64>::kCtasPerSm);
+    if (D == 128) return launch(k_attention<128, false>, AttnCfg<128>::kSmem, AttnCfg<128>::kCtasPerSm);
+    return launch(k_attention<256, false>, AttnCfg<256>::kSmem, AttnCfg<256>::kCtasPerSm);
 }
+
+namespace dghost {
+
+size_t attention_pages_bytes(int32_t n_seq, int32_t max_q_len) {
+    return plan_bytes(n_seq, ((int64_t)max_q_len + kTile - 1) / kTile);
+}
+
+// dg_paged_attention for calls with many query rows (arguments checked by it).
+dg_status attention_pages(const uint16_t* q, const dg::PagedKV& kv, uint16_t* o, float* lse, const int32_t* cu_q,
+                          const uint8_t* causal, int32_t n_seq, int32_t max_q_len, int64_t total_q, int32_t Hq,
+                          int32_t Hkv, int32_t D, int32_t window, float scale, void* workspace, cudaStream_t st) {
+    const int P = sm_count();
+    if (P <= 0) return DG_ERR_CUDA;
+    const int64_t max_q_tiles = ((int64_t)max_q_len + kTile - 1) / kTile;
+    CUtensorMap tq, tk, tv;
+    // a page as the copies see it: 64 columns of a head, up to 64 of its slots
+    auto tmap_pages = [&](CUtensorMap* tm, uint16_t* base) {
+        const uint64_t dims[4] = {(uint64_t)D, 1ull << kv.page_shift, (uint64_t)Hkv, (uint64_t)kv.n_pages};
+        const uint64_t strides[3] = {(uint64_t)kv.slot_stride * 2, (uint64_t)kv.head_stride * 2,
+                                     (uint64_t)kv.page_stride * 2};
+        const uint32_t box[4] = {(uint32_t)kSub, 1u << std::min(kv.page_shift, 6), 1u, 1u};
+        return encode_tmap(tm, 0, 4, base, dims, strides, box, 128);
+    };
+    if (!tmap_heads(&tq, q, total_q, Hq, D, kTile) || !tmap_pages(&tk, kv.k) || !tmap_pages(&tv, kv.v))
+        return DG_ERR_CUDA;
+    AttnArgs a = {};
+    a.cu_q = cu_q;
+    a.causal = causal;
+    a.o = o;
+    a.lse = lse;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.window = window;
+    a.total_q = total_q;
+    // a scale of 0 weighs every key alike: the smallest one that keeps masked scores (-inf) what they are
+    a.scale_log2 = std::max(fabsf(scale) * kLog2e, 1e-30f);
+    a.status = status_word();
+    a.kv = kv;
+    a.n_seq = n_seq;
+    a.negate = scale < 0.f;
+    int32_t* plan = static_cast<int32_t*>(workspace);
+    k_attn_plan<true><<<1, 1024, 0, st>>>(a, n_seq, (int32_t)max_q_tiles, plan);
+    count_launch();
+    if (cudaGetLastError() != cudaSuccess) return DG_ERR_CUDA;
+    const int64_t work_bound = (int64_t)n_seq * max_q_tiles * Hq;
+    auto launch = [&](auto kern, size_t smem, int per_sm) -> dg_status {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return DG_ERR_CUDA;
+        const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((int64_t)per_sm * P, work_bound));
+        kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, a, plan);
+        count_launch();
+        return cuda_status(cudaGetLastError());
+    };
+    if (D == 64) return launch(k_attention<64, true>, AttnCfg<64>::kSmem, AttnCfg<64>::kCtasPerSm);
+    if (D == 128) return launch(k_attention<128, true>, AttnCfg<128>::kSmem, AttnCfg<128>::kCtasPerSm);
+    return launch(k_attention<256, true>, AttnCfg<256>::kSmem, AttnCfg<256>::kCtasPerSm);
+}
+
+}  // namespace dghost

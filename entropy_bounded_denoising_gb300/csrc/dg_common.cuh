@@ -268,6 +268,14 @@ DG_DEVINL void tma_load_3d(void* dst, const void* tmap, int32_t c0, int32_t c1, 
         : "memory");
 }
 
+DG_DEVINL void tma_load_4d(void* dst, const void* tmap, int32_t c0, int32_t c1, int32_t c2, int32_t c3, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
 DG_DEVINL void prefetch_tmap(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }

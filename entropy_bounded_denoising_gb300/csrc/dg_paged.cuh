@@ -57,4 +57,10 @@ DG_DEVINL int warp_owner(const int32_t* cu_q, int n, int t) {
 namespace dghost {
 // Checks shared by the calls that take a dg_paged_kv; fills `c` when it returns DG_OK.
 dg_status paged_kv(const dg_paged_kv* cache, int32_t D, dg::PagedKV* c);
+
+// Attention over pages with the query tiles of dg_attention (dg_attn.cu), and its workspace.
+size_t attention_pages_bytes(int32_t n_seq, int32_t max_q_len);
+dg_status attention_pages(const uint16_t* q, const dg::PagedKV& kv, uint16_t* o, float* lse, const int32_t* cu_q,
+                          const uint8_t* causal, int32_t n_seq, int32_t max_q_len, int64_t total_q, int32_t Hq,
+                          int32_t Hkv, int32_t D, int32_t window, float scale, void* workspace, cudaStream_t stream);
 }  // namespace dghost

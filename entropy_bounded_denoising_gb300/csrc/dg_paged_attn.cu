@@ -545,6 +545,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Rows of an item: 8 when the call's queries and a group fit them, else 16.
 int item_rows(int32_t max_q_len, int32_t group) { return (int64_t)max_q_len * group <= 8 ? 8 : 16; }
 
+// Calls of more rows than this take dg_attention's query tiles.
+#ifndef DG_SPLIT_ROWS
+#define DG_SPLIT_ROWS 32
+#endif
+bool split_path(int32_t max_q_len, int32_t group) { return max_q_len == 1 || (int64_t)max_q_len * group <= DG_SPLIT_ROWS; }
+
 size_t split_bytes(int rows, int32_t D) {
     return (size_t)kMaxCtas * 16 + (size_t)kMaxCtas * 2 * rows * ((size_t)D + 2) * 4;
 }
@@ -571,6 +577,7 @@ dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
 extern "C" size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv,
                                                      int32_t D) {
     if (n_seq < 1 || max_q_len < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
+    if (!split_path(max_q_len, Hq / Hkv)) return dghost::attention_pages_bytes(n_seq, max_q_len);
     return split_bytes(item_rows(max_q_len, Hq / Hkv), D);
 }
 
@@ -590,8 +597,13 @@ extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* ca
     const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
     if (ok != DG_OK) return ok;
     const int rows = item_rows(max_q_len, Hq / Hkv);
-    if (!workspace || workspace_bytes < split_bytes(rows, D)) return DG_ERR_WORKSPACE;
+    const bool split = split_path(max_q_len, Hq / Hkv);
+    if (!workspace || workspace_bytes < dg_paged_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D))
+        return DG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
+    if (!split)
+        return dghost::attention_pages(q, a.kv, o, lse, cu_q, causal, n_seq, max_q_len, total_q, Hq, Hkv, D, window, scale,
+                                       workspace, (cudaStream_t)stream);
     a.q = q;
     a.o = o;
     a.lse = lse;
