@@ -33,10 +33,30 @@ struct AppendArgs {
     const int32_t* cu_q;
     const double* inv_freq;
     int64_t total_q;
-    int32_t n_seq, Hq, Hkv, D, rot, tasks;  // tasks: per row
+    int32_t n_seq, Hq, Hkv, D, rot, tasks, head_shift;  // tasks: per row; 2^head_shift of them a head
+    bool narrow;        // fewer than 2^31 tasks
     dg::PagedKV kv;
     unsigned* status;
 };
+
+struct Task {
+    int row, head;   // row of the unit; heads in order: key heads, value heads, query heads
+    int at, dist;    // the first chunk's dimension, and how far behind it the second one lies
+    bool turn;       // of the rotated part
+};
+
+DG_DEVINL Task task_of(const AppendArgs& a, int i) {
+    Task k;
+    k.row = i / a.tasks;
+    const int t = i - k.row * a.tasks;
+    k.head = t >> a.head_shift;
+    const int tt = t & ((1 << a.head_shift) - 1);
+    const bool value = k.head >= a.Hkv && k.head < 2 * a.Hkv;
+    k.turn = !value && tt < a.rot / 16;
+    k.at = value || k.turn ? tt * 8 : a.rot + (tt - a.rot / 16) * 8;
+    k.dist = value ? a.D / 2 : k.turn ? a.rot / 2 : (a.D - a.rot) / 2;
+    return k;
+}
 
 DG_DEVINL void rotate_halves(uint4& x, uint4& y, const float2* cs) {
     uint32_t* a = reinterpret_cast<uint32_t*>(&x);
@@ -60,102 +80,129 @@ DG_DEVINL void rotate_neighbours(uint4& x, const float2* cs) {
     }
 }
 
-template <bool Interleaved>
-__global__ void __launch_bounds__(kAppendThreads) k_kv_append(const AppendArgs a) {
-    // rows of the block: where each goes, and the sines and cosines of its angles
-    constexpr int kRows = kAppendThreads / 8 + 2;  // at least 8 tasks a row (one key head of 64)
-    __shared__ int64_t place[kRows];               // cache offset of the row's slot, -1 = skipped
+// w radians as a fraction of a turn in 64-bit fixed point: floor(w / (2 pi) 2^64) mod 2^64, within a few
+// units of the last place for |w| < 2^40.  In integers: w = m 2^(e - 1075) and 4 / (2 pi) = 2 / pi =
+// 0.A2F9836E4E441529... in base 16, so the turns are m times those 64 bits, shifted by e - 1077.  (The
+// doubles' own operations run at a small fraction of this rate here.)
+DG_DEVINL uint64_t turns_of(double w) {
+    const uint64_t bits = (uint64_t)__double_as_longlong(w);
+    const int e = (int)(bits >> 52) & 0x7ff;
+    const uint64_t m = (bits & 0xfffffffffffffull) | (e ? 1ull << 52 : 0ull);
+    const uint64_t lo = m * 0xA2F9836E4E441529ull, hi = __umul64hi(m, 0xA2F9836E4E441529ull);
+    const int down = 1077 - max(e, 1);
+    uint64_t f = 0;
+    if (down >= 64 && down < 128)
+        f = hi >> (down - 64);
+    else if (down > 0 && down < 64)
+        f = (lo >> down) | (hi << (64 - down));
+    return bits >> 63 ? 0ull - f : f;
+}
+
+// The sequence that owns a row, and the row's position in it (-1: none).
+DG_DEVINL int row_position(const AppendArgs& a, int t, int s) {
+    if (s >= a.n_seq) return -1;
+    const dg::PagedSeq q = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+    if (q.q0 > t) return -1;
+    if (!q.ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+    return q.ok && q.kl > 0 ? q.kl - q.ql + (t - q.q0) : -1;
+}
+
+// A block's rows are looked up and its sines computed while its data is on the way: every thread
+// first asks for the 64 bytes it will store.
+// PerThread: a thread's tasks.  One, with the most threads an SM holds, while every task has a
+// place at once; four where there are several rounds of blocks (more bytes on the way and fewer lookups
+// a byte): 64 rows of 32 heads of 128 take 3.3 us with one and 4.8 with four, 2048 rows 9.3 and 8.9,
+// 30k rows of 32 heads of 256 149 and 138.
+template <bool Interleaved, int PerThread>
+__global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_append(const AppendArgs a) {
+    constexpr int kPerThread = PerThread, kUnit = kAppendThreads * PerThread;   // tasks of a block
+    constexpr int kRows = kUnit / 8 + 2;       // rows of a unit: at least 8 tasks each (one key head of 64)
+    __shared__ int64_t place[kRows];           // cache offset of a row's slot, -1 = skipped
     __shared__ int32_t position[kRows];
-    __shared__ float2 cs[kAppendThreads * 4 + 2 * 128];
+    __shared__ float2 cs[kUnit * 4 + 2 * 128]; // cosine and sine of its angles
     dg::pdl_wait();
     dg::pdl_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t first = (int64_t)blockIdx.x * kAppendThreads;
-    const int64_t row0 = first / a.tasks;
-    const int rows = (int)(min(a.total_q - 1, (first + kAppendThreads - 1) / a.tasks) - row0) + 1;
     const int half = a.rot / 2;
+    const int64_t first = (int64_t)blockIdx.x * kUnit;
+    const int64_t row0 = a.narrow ? (int64_t)((uint32_t)first / (uint32_t)a.tasks) : first / a.tasks;
+    const int skip = (int)(first - row0 * a.tasks);   // tasks of row0 before the unit
+    const int rows = (int)min(a.total_q - row0, (int64_t)((skip + kUnit - 1) / a.tasks + 1));
 
-    for (int r = warp; r < rows; r += kAppendThreads / 32) {
-        const int t = (int)(row0 + r);
-        const int s = dg::warp_owner(a.cu_q, a.n_seq, t);
-        if (lane == 0) {
-            int64_t at = -1;
-            int p = 0;
-            if (s < a.n_seq && a.cu_q[s] <= t) {
-                const dg::PagedSeq q = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
-                if (!q.ok) {
-                    dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-                } else if (q.kl > 0) {
-                    p = q.kl - q.ql + (t - q.q0);
-                    const int32_t page = a.kv.page_table[(int64_t)s * a.kv.max_pages + (p >> a.kv.page_shift)];
-                    if (page < 0 || page >= a.kv.n_pages)
-                        dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-                    else
-                        at = page * a.kv.page_stride + (p & ((1 << a.kv.page_shift) - 1)) * a.kv.slot_stride;
-                }
-            }
-            place[r] = at;
-            position[r] = p;
+    uint4 x[kPerThread], y[kPerThread];
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u) {
+        const Task k = task_of(a, skip + u * kAppendThreads + tid);
+        if (k.row < rows) {
+            const int64_t row = row0 + k.row;
+            const uint16_t* src = k.head < a.Hkv       ? a.k + row * a.ldk + (int64_t)k.head * a.D
+                                  : k.head < 2 * a.Hkv ? a.v + row * a.ldv + (int64_t)(k.head - a.Hkv) * a.D
+                                                       : a.q + row * a.ldq + (int64_t)(k.head - 2 * a.Hkv) * a.D;
+            x[u] = *reinterpret_cast<const uint4*>(src + k.at);
+            y[u] = *reinterpret_cast<const uint4*>(src + k.at + k.dist);
         }
     }
+    int mine = -1, owner = 0;   // the row this thread looks up
+    if (rows <= kAppendThreads / 32) {   // a warp a row: two dependent reads for up to 1024 sequences
+        if (warp < rows) {
+            owner = dg::warp_owner(a.cu_q, a.n_seq, (int)(row0 + warp));
+            if (lane == 0) mine = warp;
+        }
+    } else if (tid < rows) {             // narrow rows: a thread each, by bisection
+        mine = tid;
+        int hi = a.n_seq;
+        while (owner < hi) {
+            const int mid = (owner + hi) / 2;
+            if (a.cu_q[mid + 1] <= (int)(row0 + tid))
+                owner = mid + 1;
+            else
+                hi = mid;
+        }
+    }
+    int p = -1;
+    if (mine >= 0) {
+        p = row_position(a, (int)(row0 + mine), owner);
+        position[mine] = p;
+    }
     __syncthreads();
-    // turns of pair j at position p: p * inv_freq / 2 pi modulo 1, exact in 64-bit fixed point
-    // once the frequency is rounded to 2^-64 turns (or to its 53 bits)
+    if (mine >= 0) {
+        int64_t at = -1;
+        if (p >= 0) {
+            const int32_t page = a.kv.page_table[(int64_t)owner * a.kv.max_pages + (p >> a.kv.page_shift)];
+            if (page < 0 || page >= a.kv.n_pages)
+                dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+            else
+                at = page * a.kv.page_stride + (p & ((1 << a.kv.page_shift) - 1)) * a.kv.slot_stride;
+        }
+        place[mine] = at;
+    }
     for (int i = tid; i < rows * half; i += kAppendThreads) {
-        const double turns = a.inv_freq[i % half] * 0.15915494309189533577;
-        const uint64_t f = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-        const int64_t u = (int64_t)(f * (uint64_t)position[i / half]);
+        const int r = i / half;
+        const int64_t u = (int64_t)(turns_of(a.inv_freq[i - r * half]) * (uint64_t)position[r]);
         float sn, c;
         sincospif((float)u * 1.0842021724855044e-19f, &sn, &c);  // 2^-63: half turns in [-1, 1]
         cs[i] = make_float2(c, sn);
     }
     __syncthreads();
-    const int64_t id = first + tid;
-    const int64_t row = id / a.tasks;
-    if (row >= a.total_q) return;
-    const int r = (int)(row - row0);
-    if (place[r] < 0) return;
-    const int per_head = a.D / 16;
-    const int task = (int)(id - row * a.tasks);
-    const int head = task / per_head;
-    const int tt = task - head * per_head;
-    // heads in order: key heads, value heads, query heads
-    const bool is_v = head >= a.Hkv && head < 2 * a.Hkv;
-    int e0 = tt * 8, dist = a.D / 2;
-    const bool turn = !is_v && tt < a.rot / 16;
-    if (!is_v) {
-        if (turn) {
-            dist = half;
-        } else {
-            e0 = a.rot + (tt - a.rot / 16) * 8;
-            dist = (a.D - a.rot) / 2;
+#pragma unroll
+    for (int u = 0; u < kPerThread; ++u) {
+        const Task k = task_of(a, skip + u * kAppendThreads + tid);
+        if (k.row >= rows || place[k.row] < 0) continue;
+        if (k.turn) {
+            const float2* c = cs + k.row * half;
+            if (Interleaved) {
+                rotate_neighbours(x[u], c + k.at / 2);
+                rotate_neighbours(y[u], c + half / 2 + k.at / 2);
+            } else {
+                rotate_halves(x[u], y[u], c + k.at);
+            }
         }
+        uint16_t* dst = k.head < a.Hkv       ? a.kv.k + place[k.row] + k.head * a.kv.head_stride
+                        : k.head < 2 * a.Hkv ? a.kv.v + place[k.row] + (k.head - a.Hkv) * a.kv.head_stride
+                                             : a.q_out + ((row0 + k.row) * a.Hq + (k.head - 2 * a.Hkv)) * a.D;
+        *reinterpret_cast<uint4*>(dst + k.at) = x[u];
+        *reinterpret_cast<uint4*>(dst + k.at + k.dist) = y[u];
     }
-    const uint16_t* src;
-    uint16_t* dst;
-    if (head < a.Hkv) {
-        src = a.k + row * a.ldk + (int64_t)head * a.D;
-        dst = a.kv.k + place[r] + head * a.kv.head_stride;
-    } else if (is_v) {
-        src = a.v + row * a.ldv + (int64_t)(head - a.Hkv) * a.D;
-        dst = a.kv.v + place[r] + (head - a.Hkv) * a.kv.head_stride;
-    } else {
-        src = a.q + row * a.ldq + (int64_t)(head - 2 * a.Hkv) * a.D;
-        dst = a.q_out + (row * a.Hq + (head - 2 * a.Hkv)) * a.D;
-    }
-    uint4 x = *reinterpret_cast<const uint4*>(src + e0);
-    uint4 y = *reinterpret_cast<const uint4*>(src + e0 + dist);
-    if (turn) {
-        const float2* c = cs + r * half;
-        if (Interleaved) {
-            rotate_neighbours(x, c + tt * 4);
-            rotate_neighbours(y, c + half / 2 + tt * 4);
-        } else {
-            rotate_halves(x, y, c + tt * 8);
-        }
-    }
-    *reinterpret_cast<uint4*>(dst + e0) = x;
-    *reinterpret_cast<uint4*>(dst + e0 + dist) = y;
 }
 
 }  // namespace
@@ -228,10 +275,17 @@ extern "C" dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t
     a.D = D;
     a.rot = rot_dim;
     a.tasks = ((q ? Hq : 0) + 2 * Hkv) * (D / 16);
+    a.head_shift = D == 64 ? 2 : D == 128 ? 3 : 4;
     a.status = dghost::status_word();
-    const int64_t blocks = (total_q * a.tasks + kAppendThreads - 1) / kAppendThreads;
+    a.narrow = total_q * a.tasks < (1LL << 31);
+    const int sms = dghost::sm_count();
+    if (sms <= 0) return DG_ERR_CUDA;
+    const bool one = total_q * a.tasks <= (int64_t)sms * 2048;
+    const int64_t unit = one ? kAppendThreads : kAppendThreads * 4;
+    const int64_t blocks = (total_q * a.tasks + unit - 1) / unit;
     if (blocks > 0x7fffffffLL) return DG_ERR_INVALID_ARG;
-    const cudaError_t e = dghost::launch_pdl(interleaved ? k_kv_append<true> : k_kv_append<false>,
+    const cudaError_t e = dghost::launch_pdl(one ? (interleaved ? k_kv_append<true, 1> : k_kv_append<false, 1>)
+                                                 : (interleaved ? k_kv_append<true, 4> : k_kv_append<false, 4>),
                                              dim3((unsigned)blocks), dim3(kAppendThreads), 0, (cudaStream_t)stream, a);
     dghost::count_launch();
     return dghost::cuda_status(e);
