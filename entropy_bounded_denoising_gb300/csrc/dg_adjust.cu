@@ -48,12 +48,14 @@ DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // The penalties and biases of a vector's edited tokens: one fma each, by 1 / repetition or repetition
-// (1 for a token without a count) and the token's addend.
+// (1 for a token without a count) and the token's addend.  `any`: the places of a vector that some lane of
+// the warp has edited; lists are short beside the vocabulary, so most places are skipped by all.
 template <int Bytes>
-DG_DEVINL void edit(uint4& y, uint32_t edited, uint32_t penalised, float down, float up, const float (&add)[16 / Bytes]) {
+DG_DEVINL void edit(uint4& y, uint32_t any, uint32_t edited, uint32_t penalised, float down, float up, const float (&add)[16 / Bytes]) {
     uint32_t* w = reinterpret_cast<uint32_t*>(&y);
 #pragma unroll
     for (int e = 0; e < 16 / Bytes; ++e) {
+        if (!(any >> e & 1)) continue;
         const int i = Bytes == 2 ? e / 2 : e;
         const bool high = Bytes == 2 && (e & 1);
         const float v = __uint_as_float(Bytes == 4 ? w[i] : high ? w[i] & 0xffff0000u : w[i] << 16);
@@ -82,12 +84,30 @@ DG_DEVINL void exclude(uint4& y, uint32_t keep, const uint2* expand) {
     }
 }
 
+// A vector's first n tokens (all but in a row's last vector: nothing past column V is written).
+template <int Bytes>
+DG_DEVINL void store(unsigned char* at, const uint4& y, int n) {
+    constexpr int PerVec = 16 / Bytes;
+    if (n == PerVec) {
+        *reinterpret_cast<uint4*>(at) = y;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < PerVec; ++e) {
+        if (e >= n) break;
+        const uint32_t w = reinterpret_cast<const uint32_t*>(&y)[Bytes == 2 ? e / 2 : e];
+        if (Bytes == 2)
+            reinterpret_cast<uint16_t*>(at)[e] = (uint16_t)(e & 1 ? w >> 16 : w);
+        else
+            reinterpret_cast<uint32_t*>(at)[e] = w;
+    }
+}
+
 // Bytes: 2 (bf16) or 4 (fp32) a logit; PerVec tokens in 16 bytes.
 template <int Bytes>
 __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
     constexpr int PerVec = 16 / Bytes;
     constexpr int kSlice = kThreads * PerVec;   // tokens of a block
-    constexpr uint32_t kAll = 0xffu;            // a mask byte
     __shared__ int32_t n_hist[kSlice];          // occurrences in the history
     __shared__ int32_t n_bias[kSlice];          // entries in the bias list
     __shared__ int32_t first_bias[kSlice];      // the first of them
@@ -98,43 +118,89 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
     dg::pdl_release();
     const int tid = threadIdx.x;
     const int64_t c = blockIdx.z;
-    if (!(a.params[c].flags & DG_ACTIVE)) return;
     const int slice0 = (int)blockIdx.x * kSlice;
     const int v0 = slice0 + tid * PerVec;
+    const int r0 = (int)blockIdx.y * a.rows, rows = min(a.L - r0, a.rows);
     const bool reports = blockIdx.x == 0 && blockIdx.y == 0 && tid == 0;
 
-    // the lists, and whether they are sound (the same for every block of the canvas)
+    // everything that depends on nothing else is read at once: the canvas's flag, its lists' bounds and
+    // penalties, the rows' masks
+    const uint32_t flags = a.params[c].flags;
     int h0 = 0, h1 = 0, b0 = 0, b1 = 0;
     dg_penalties pen = {1.f, 0.f, 0.f};
-    bool sound = true;
     if (a.history) {
         h0 = a.cu_history[c];
         h1 = a.cu_history[c + 1];
         pen = a.penalties[c];
-        sound = h0 >= 0 && h1 >= h0 && h1 <= a.total_history && pen.repetition > 0.f && isfinite(pen.repetition) &&
-                isfinite(pen.frequency) && isfinite(pen.presence);
     }
     if (a.bias_tokens) {
         b0 = a.cu_bias[c];
         b1 = a.cu_bias[c + 1];
-        sound = sound && b0 >= 0 && b1 >= b0 && b1 <= a.total_bias;
     }
+    int m = -1;   // kMaxRows <= kThreads: a thread a row; -1 = none
+    if (a.masks && tid < rows) m = a.mask_index[c * a.L + r0 + tid];
+    if (!(flags & DG_ACTIVE)) return;
+    const bool sound = h0 >= 0 && h1 >= h0 && h1 <= a.total_history && b0 >= 0 && b1 >= b0 && b1 <= a.total_bias &&
+                       pen.repetition > 0.f && isfinite(pen.repetition) && isfinite(pen.frequency) &&
+                       isfinite(pen.presence);
     if (!sound) {
         if (reports) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
         return;
     }
+    if (m < -1 || m >= a.n_masks) {
+        if (blockIdx.x == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+        m = -1;
+    }
+    if (tid < kMaxRows) row_mask[tid] = m;
+    // what keeps an excluded token's logit: words of ones where four tokens' bits are set (bf16 pairs)
+    if (Bytes == 2 && tid < 16)
+        expand[tid] = make_uint2(((tid & 1) ? 0xffffu : 0u) | ((tid & 2) ? 0xffff0000u : 0u),
+                                 ((tid & 4) ? 0xffffu : 0u) | ((tid & 8) ? 0xffff0000u : 0u));
+    const bool listed = h1 > h0 || b1 > b0;
+    if (listed) {
+#pragma unroll
+        for (int e = 0; e < PerVec; ++e) {
+            n_hist[e * kThreads + tid] = 0;
+            if (b1 > b0) {
+                n_bias[e * kThreads + tid] = 0;
+                first_bias[e * kThreads + tid] = 0x7fffffff;
+            }
+        }
+    }
+    __syncthreads();
+    // the first rows' masks and data are on their way while the lists are counted
+    const bool in_place = a.out == a.x;
+    const int n_mine = max(0, min(PerVec, a.V - v0));          // tokens of the vector inside the vocabulary
+    const uint32_t mine = (1u << n_mine) - 1u;
+    const unsigned char* mask_at = reinterpret_cast<const unsigned char*>(a.masks) + (v0 >> 3);
+    const int64_t mask_pitch = a.mask_stride * 4;
+    const unsigned char* src = a.x + (c * a.L + r0) * a.ld_bytes + (int64_t)v0 * Bytes;
+    unsigned char* dst = a.out + (c * a.L + r0) * a.ld_out_bytes + (int64_t)v0 * Bytes;
+    uint32_t keep[kUnroll], next[kUnroll];   // allowed tokens of the vector, for kUnroll rows
+    uint4 x[kUnroll];
+    auto masks_of = [&](int r) {             // row_mask is -1 past the last row
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int row = r + u < kMaxRows ? row_mask[r + u] : -1;
+            next[u] = row >= 0 && n_mine > 0 ? (uint32_t)mask_at[row * mask_pitch] : 0xffu;
+        }
+    };
+    auto load = [&](int r, bool only_mixed) {   // a vector that goes whole, or stays whole in place, is not read
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            keep[u] = (Bytes == 4 ? next[u] >> (v0 & 4) : next[u]) & mine;
+            x[u] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+            if (r + u < rows && keep[u] != 0 && !(only_mixed && keep[u] == mine))
+                x[u] = *reinterpret_cast<const uint4*>(src + u * a.ld_bytes);
+        }
+    };
+    masks_of(0);
+    load(0, in_place && !listed);
     float add[PerVec];
     uint32_t penalised = 0, edited = 0;   // tokens with a count / with a count or a bias
 #pragma unroll
     for (int e = 0; e < PerVec; ++e) add[e] = 0.f;
-    if (h1 > h0 || b1 > b0) {
-#pragma unroll
-        for (int e = 0; e < PerVec; ++e) {
-            n_hist[tid * PerVec + e] = 0;
-            n_bias[tid * PerVec + e] = 0;
-            first_bias[tid * PerVec + e] = 0x7fffffff;
-        }
-        __syncthreads();
+    if (listed) {
         const int end = min(kSlice, a.V - slice0);
 #pragma unroll 4
         for (int i = h0 + tid; i < h1; i += kThreads) {
@@ -153,9 +219,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
 #pragma unroll
         for (int e = 0; e < PerVec; ++e) {
             const int nh = n_hist[tid * PerVec + e];
-            int nb = n_bias[tid * PerVec + e];
+            int nb = b1 > b0 ? n_bias[tid * PerVec + e] : 0;
             float b = 0.f;
-            for (int i = first_bias[tid * PerVec + e]; nb > 0; ++i)   // in list order
+            for (int i = nb > 0 ? first_bias[tid * PerVec + e] : 0; nb > 0; ++i)   // in list order
                 if (a.bias_tokens[i] == v0 + e) {
                     b += a.bias_values[i];
                     --nb;
@@ -169,73 +235,24 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
         }
         edited |= penalised;
     }
-    // what keeps an excluded token's logit: words of ones where four tokens' bits are set (bf16 pairs)
-    if (Bytes == 2 && tid < 16)
-        expand[tid] = make_uint2(((tid & 1) ? 0xffffu : 0u) | ((tid & 2) ? 0xffff0000u : 0u),
-                                 ((tid & 4) ? 0xffffu : 0u) | ((tid & 8) ? 0xffff0000u : 0u));
-    const int r0 = (int)blockIdx.y * a.rows, r1 = min(a.L, r0 + a.rows);
-    for (int r = tid; r < a.rows; r += kThreads) {   // the rows' masks; -1 = none
-        int m = -1;
-        if (a.masks && r0 + r < r1) {
-            m = a.mask_index[c * a.L + r0 + r];
-            if (m < -1 || m >= a.n_masks) {
-                if (blockIdx.x == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-                m = -1;
-            }
-        }
-        row_mask[r] = m;
-    }
-    __syncthreads();
-    if (v0 >= a.V) return;
-    const int n_mine = min(PerVec, a.V - v0);                  // tokens of the vector inside the vocabulary
-    const uint32_t mine = (1u << n_mine) - 1u;
+    const uint32_t any = __reduce_or_sync(0xffffffffu, edited);
+    if (n_mine == 0) return;
+    const bool still = in_place && edited == 0;   // nothing to write where nothing is excluded
     const float down = 1.f / pen.repetition;
-    const bool in_place = a.out == a.x;
-    const bool quiet = in_place && edited == 0;                // nothing to write where nothing is excluded
-    const unsigned char* mask_at = reinterpret_cast<const unsigned char*>(a.masks) + (v0 >> 3);
-    const int64_t mask_pitch = a.mask_stride * 4;
-    const unsigned char* src = a.x + (c * a.L + r0) * a.ld_bytes + (int64_t)v0 * Bytes;
-    unsigned char* dst = a.out + (c * a.L + r0) * a.ld_out_bytes + (int64_t)v0 * Bytes;
-
-    for (int r = 0; r < r1 - r0; r += kUnroll, src += kUnroll * a.ld_bytes, dst += kUnroll * a.ld_out_bytes) {
-        uint32_t keep[kUnroll];   // allowed tokens
-        uint4 x[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {   // rows is a multiple of kUnroll: row_mask covers r + u
-            const int m = row_mask[r + u];
-            keep[u] = kAll;
-            if (m >= 0) keep[u] = (uint32_t)mask_at[m * mask_pitch];
-        }
+    for (int r = 0;;) {
+        masks_of(r + kUnroll);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            keep[u] = (Bytes == 4 ? keep[u] >> (v0 & 4) : keep[u]) & mine;
-            if (r + u < r1 - r0 && keep[u] != 0 && !(quiet && keep[u] == mine))
-                x[u] = *reinterpret_cast<const uint4*>(src + u * a.ld_bytes);
+            if (r + u >= rows || (still && keep[u] == mine)) continue;
+            if (any) edit<Bytes>(x[u], any, edited, penalised, down, pen.repetition, add);
+            exclude<Bytes>(x[u], keep[u], expand);
+            store<Bytes>(dst + u * a.ld_out_bytes, x[u], n_mine);
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (r + u >= r1 - r0 || (quiet && keep[u] == mine)) continue;
-            uint4 y = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
-            if (keep[u] != 0) {
-                y = x[u];
-                if (edited) edit<Bytes>(y, edited, penalised, down, pen.repetition, add);
-                exclude<Bytes>(y, keep[u], expand);
-            }
-            unsigned char* at = dst + u * a.ld_out_bytes;
-            if (n_mine == PerVec) {
-                *reinterpret_cast<uint4*>(at) = y;
-            } else {   // the row's last vector: nothing past column V is written
-#pragma unroll
-                for (int e = 0; e < PerVec; ++e) {
-                    if (e >= n_mine) break;
-                    const uint32_t w = reinterpret_cast<const uint32_t*>(&y)[Bytes == 2 ? e / 2 : e];
-                    if (Bytes == 2)
-                        reinterpret_cast<uint16_t*>(at)[e] = (uint16_t)(e & 1 ? w >> 16 : w);
-                    else
-                        reinterpret_cast<uint32_t*>(at)[e] = w;
-                }
-            }
-        }
+        r += kUnroll;
+        if (r >= rows) break;
+        src += kUnroll * a.ld_bytes;
+        dst += kUnroll * a.ld_out_bytes;
+        load(r, still);
     }
 }
 
@@ -288,10 +305,11 @@ extern "C" dg_status dg_adjust_logits(const void* logits, dg_dtype dtype, int64_
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
     const int64_t slice = kThreads * (16 / es), slices = (V + slice - 1) / slice;
-    // rows of a block: as many as leave eight blocks an SM (a block's lists are then read for up to 64
-    // rows), and at least what a thread keeps in flight
-    const int64_t rows = slices * n_canvas * L / (8 * (int64_t)sms) / kUnroll * kUnroll;
-    a.rows = (int32_t)std::max<int64_t>(kUnroll, std::min<int64_t>(kMaxRows, rows));
+    // rows of a block: up to 64, so that its lists are read for many rows, but few enough that the blocks
+    // fill the four places an SM has for them
+    const int64_t places = 4 * (int64_t)sms;
+    const int64_t rows = (slices * n_canvas * L + places - 1) / places;
+    a.rows = (int32_t)std::min<int64_t>(kMaxRows, (rows + kUnroll - 1) / kUnroll * kUnroll);
     const dim3 grid((unsigned)slices, (unsigned)((L + a.rows - 1) / a.rows), (unsigned)n_canvas);
     const cudaError_t e = dghost::launch_pdl(es == 2 ? k_adjust<2> : k_adjust<4>, grid, dim3(kThreads), 0,
                                              (cudaStream_t)stream, a);
