@@ -86,6 +86,7 @@ struct __align__(8) AttnShared {
     uint64_t wfull[4];        // the item queue: slot k % 4 holds the CTA's k-th work index
     uint64_t wempty[4];       // (-1: no more), taken by its 7 readers
     int64_t item_w[4];
+    int32_t pages[2][8];      // pages of the tile that the K / V producer is loading (one thread's own)
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -300,9 +301,12 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
         key = kCostBuckets - 1 - min(r.nt, kCostBuckets - 1);  // longest first
         return true;
     };
+    int my_key = -1;   // of pair tid, kept for the second pass
     for (int64_t f = tid; f < pairs; f += blockDim.x) {
         int key;
-        if (item_key(f, key)) atomicAdd(&count[key], 1);
+        if (!item_key(f, key)) continue;
+        if (f == tid) my_key = key;
+        atomicAdd(&count[key], 1);
     }
     __syncthreads();
     // exclusive prefix over the buckets (one per thread): warp scans, then the warp totals
@@ -335,8 +339,8 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
     __syncthreads();
     int2* items = reinterpret_cast<int2*>(plan + kPlanHeader);
     for (int64_t f = tid; f < pairs; f += blockDim.x) {
-        int key;
-        if (item_key(f, key)) items[atomicAdd(&count[key], 1)] = make_int2((int)(f / max_q_tiles), (int)(f % max_q_tiles));
+        int key = my_key;
+        if (f == tid ? key >= 0 : item_key(f, key)) items[atomicAdd(&count[key], 1)] = make_int2((int)(f / max_q_tiles), (int)(f % max_q_tiles));
     }
 }
 
@@ -472,23 +476,28 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
                 const TileRange r = tile_range<Paged>(a, it.x, it.y);
                 for (int i = 0; i < r.nt; ++i, ++g) {
                     const int st = (int)(g & 1u);
-                    int32_t pages[8];  // of the tile's boxes, read before the wait; n_pages reads zeros
+                    // the pages of the tile's boxes, read before the wait; n_pages reads zeros
                     const int box_shift = Paged ? min(a.kv.page_shift, 6) : 6, boxes = kKeys >> box_shift;
                     const int j0 = (r.jt_lo + i) * kKeys;
                     if constexpr (Paged) {
                         const int32_t* table = a.kv.page_table + (int64_t)it.x * a.kv.max_pages;
+                        int32_t entry[8];
+                        bool bad = false;
 #pragma unroll
                         for (int b = 0; b < 8; ++b) {
                             const int j = j0 + (b << box_shift);
-                            if (b < boxes) {
-                                const bool seen = j <= r.jhi && r.jlo - j < (1 << box_shift);
-                                pages[b] = seen ? table[j >> a.kv.page_shift] : (int32_t)a.kv.n_pages;
-                                if (pages[b] < 0 || pages[b] >= a.kv.n_pages) {
-                                    if (seen) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-                                    pages[b] = (int32_t)a.kv.n_pages;
-                                }
-                            }
+                            entry[b] = (int32_t)a.kv.n_pages;
+                            if (b < boxes && j <= r.jhi && r.jlo - j < (1 << box_shift)) entry[b] = table[j >> a.kv.page_shift];
                         }
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const int j = j0 + (b << box_shift);
+                            const bool seen = b < boxes && j <= r.jhi && r.jlo - j < (1 << box_shift);
+                            const bool out = entry[b] < 0 || entry[b] >= a.kv.n_pages;
+                            bad = bad || (seen && out);
+                            sh.pages[lane][b] = out ? (int32_t)a.kv.n_pages : entry[b];
+                        }
+                        if (bad) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
                     }
                     if (!attn_wait(&empty[st], ((g >> 1) & 1u) ^ 1u)) {
                         ok = false;
@@ -497,14 +506,13 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
                     dg::mbar_arrive_expect_tx(&full[st], kKVBytes);
                     unsigned char* dst = ring + st * kKVBytes;
                     if constexpr (Paged) {
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            if (b >= boxes) break;
-                            const int row = b << box_shift;
+#pragma unroll 1
+                        for (int b = 0; b < boxes; ++b) {
+                            const int row = b << box_shift, page = sh.pages[lane][b];
                             const int slot = (j0 + row) & ((1 << a.kv.page_shift) - 1);
 #pragma unroll
                             for (int c = 0; c < kHead / kSub; ++c)
-                                dg::tma_load_4d(dst + c * kKSub + row * kSub * 2, tm, c * kSub, slot, hk, pages[b], &full[st]);
+                                dg::tma_load_4d(dst + c * kKSub + row * kSub * 2, tm, c * kSub, slot, hk, page, &full[st]);
                         }
                     } else {
                         const int krow = r.k0 + j0;
@@ -524,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         if (lane == 0) {
-            constexpr uint32_t idS = dg::instr_desc(kTile, kKeys, false);  // S = Q K^T: K tile K-major
+            // S = Q K^T: K tile K-major; bit 13 negates Q
+            const uint32_t idS = dg::instr_desc(kTile, kKeys, false) | (Paged && a.negate ? 1u << 13 : 0u);
             constexpr uint32_t idO = dg::instr_desc(kTile, kHead, true);   // O += P V: V rows are N-major
             uint32_t g = 0, kq = 0;
             bool ok = true;
@@ -630,12 +639,6 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
                 const int jt = r.jt_lo + i;
                 const int j0 = jt * kKeys;
                 if constexpr (Paged) {
-                    if (a.negate) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[c][e] = -x[c][e];
-                    }
                     if (j0 < r.jlo || j0 + kKeys - 1 > r.jhi) {  // the value rows nobody sees
                         if (!attn_wait_warp(&sh.vfull[gi & 1u], (gi >> 1) & 1u)) {
                             ok = false;
