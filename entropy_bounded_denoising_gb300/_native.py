@@ -446,14 +446,15 @@ def _whole(fn, name, t, dtype, shape, dev):
 
 # the current stream's handle without building a Stream object (3 us of a 15 us call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _on(fn, dev, stream):
     """The raw stream of a call whose tensors are on device dev, the current one."""
     if dev < 0:
         raise ValueError(f"{fn}: device tensors expected")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{fn}: the tensors are on device {dev}, the current device is {torch.cuda.current_device()}")
+    if dev != _device():
+        raise ValueError(f"{fn}: the tensors are on device {dev}, the current device is {_device()}")
     return _raw_stream(dev) if stream is None else _s(stream)
 
 
@@ -472,31 +473,34 @@ def _rows(fn, name, t, heads, d, dev):
     return t.data_ptr(), row if shape[0] > 1 else heads * d
 
 
-def _paged_kv(fn, k_cache, v_cache, page_table, kv_len):
-    """dg_paged_kv of k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides of the first three) and
-    page_table [n_seq, max_pages], kv_len [n_seq] int32; n_seq, Hkv, D and the device."""
+def _refuse_cache(fn, k_cache, v_cache):
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype is not torch.bfloat16:
+        if t.dtype != torch.bfloat16:
             raise TypeError(f"{fn}: {name} must be bfloat16, got {t.dtype}")
         if t.dim() != 4 or t.stride(3) != 1:
             raise ValueError(f"{fn}: {name} must be [n_pages, page_size, Hkv, D] with contiguous heads")
-    strides = k_cache.stride()
-    n_pages, page_size, Hkv, D = shape = k_cache.shape
-    if v_cache.shape != shape or v_cache.stride() != strides:
-        raise ValueError(f"{fn}: k_cache and v_cache must have one layout")
+    raise ValueError(f"{fn}: k_cache and v_cache must have one layout")
+
+
+def _paged_kv(fn, k_cache, v_cache, page_table, kv_len):
+    """dg_paged_kv of k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides of the first three) and
+    page_table [n_seq, max_pages], kv_len [n_seq] int32; n_seq, Hkv, D and the device."""
+    shape, strides = k_cache.shape, k_cache.stride()
+    if (k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16 or len(shape) != 4
+            or strides[3] != 1 or v_cache.shape != shape or v_cache.stride() != strides):
+        _refuse_cache(fn, k_cache, v_cache)
+    n_pages, page_size, Hkv, D = shape
     dev = k_cache.get_device()
     if v_cache.get_device() != dev:
         _refuse(fn, "v_cache", v_cache, v_cache.dtype, (None,) * 4, dev)
     n = kv_len.numel()
-    if page_table.dim() != 2:
-        _refuse(fn, "page_table", page_table, torch.int32, (n, None), dev)
-    cols = page_table.shape[1]
+    cols = page_table.shape[-1] if page_table.dim() == 2 else None
     table = _whole(fn, "page_table", page_table, torch.int32, (n, cols), dev)
     lens = _whole(fn, "kv_len", kv_len, torch.int32, (n,), dev)
     # the stride of an extent of one says nothing: any valid one will do
-    ps = strides[0] if n_pages > 1 else D
-    ss = strides[1] if page_size > 1 else D
-    hs = strides[2] if Hkv > 1 else D
+    ps, ss, hs, _ = strides
+    if n_pages == 1 or page_size == 1 or Hkv == 1:
+        ps, ss, hs = (s if e > 1 else D for e, s in zip(shape, (ps, ss, hs)))
     return _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), table, lens, n_pages, ps, ss, hs, page_size, cols), n, Hkv, D, dev
 
 
@@ -514,7 +518,7 @@ def _scratch(fn, nbytes, workspace, dev, stream):
         return workspace, nbytes
     if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse(fn, "workspace", workspace, workspace.dtype, workspace.shape, dev)
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.nbytes
 
 
 def dg_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, *, inv_freq=None, interleaved=False, q=None,
@@ -559,17 +563,18 @@ def dg_paged_attention(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal,
     fn = "dg_paged_attention"
     kv, n, Hkv, D, dev = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
     total, Hq = (q.shape[0], q.shape[1]) if q.dim() == 3 else (0, 0)
-    bf = torch.bfloat16
-    qp = _whole(fn, "q", q, bf, (total, Hq, D), dev)
-    op = _whole(fn, "o", o, bf, (total, Hq, D), dev)
+    rows = (total, Hq, D)
+    qp = _whole(fn, "q", q, torch.bfloat16, rows, dev)
+    op = _whole(fn, "o", o, torch.bfloat16, rows, dev)
     lp = _whole(fn, "lse", lse, torch.float32, (total, Hq), dev)
     cu = _whole(fn, "cu_q", cu_q, torch.int32, (n + 1,), dev)
     cz = _whole(fn, "causal", causal, torch.uint8, (n,), dev)
     scale = 1.0 / float(D) ** 0.5 if scale is None else float(scale)
     st = _on(fn, dev, stream)
-    need = 0 if workspace is not None else load().dg_paged_attention_workspace_bytes(n, int(max_q_len), Hq, Hkv, D)
+    lib = load()
+    need = 0 if workspace is not None else lib.dg_paged_attention_workspace_bytes(n, int(max_q_len), Hq, Hkv, D)
     workspace, ws_bytes = _scratch(fn, need, workspace, dev, stream)
-    rc = load().dg_paged_attention(qp, ctypes.byref(kv), op, lp, cu, cz, n, int(max_q_len), total, Hq, Hkv, D,
+    rc = lib.dg_paged_attention(qp, ctypes.byref(kv), op, lp, cu, cz, n, int(max_q_len), total, Hq, Hkv, D,
                                    int(window), scale, workspace.data_ptr(), ws_bytes, st)
     if check:
         _check(fn, rc)

@@ -22,6 +22,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "dg_paged.cuh"
 
@@ -48,7 +49,7 @@ struct SplitArgs {
     dg::PagedKV kv;
     float* part_o;    // [grid][2][rows][D]
     float* part_ml;   // [grid][2][rows][2]
-    int4* desc;       // [grid]: sequence, item of the sequence, CTAs that follow (0: nothing to join)
+    int4* desc;       // [grid][2]: CTAs that follow (0: nothing to join), rows, first row of q, key head; first row
     unsigned* status;
 };
 
@@ -213,79 +214,203 @@ DG_DEVINL Run find_run(const SplitArgs& a) {
     return r;
 }
 
+// A run's part of one item.
+struct Piece {
+    int32_t s, hk;            // sequence, key head
+    int32_t row0, n_rows;     // rows of the item
+    int32_t q0, kl, pos0;     // the sequence's first row of q, keys, position of its first query
+    int32_t klo, khi;         // the keys that some row of the item may see
+    int32_t tile0, steps;     // first tile and tiles of the piece
+    int32_t tiles;            // of the item
+    bool causal, starts, ends;
+    int64_t at;               // where the piece begins on the line
+};
+
+// Walks a run piece by piece.
+template <int Rows>
+struct Walk {
+    int64_t at, seq_start, end;
+    int s;
+    SeqPlan p;
+
+    DG_DEVINL bool next(const SplitArgs& a, Piece& z) {
+        if (at >= end) return false;
+        while (at >= seq_start + p.cost(a.Hkv)) {   // the next sequence that has work
+            seq_start += p.cost(a.Hkv);
+            p = seq_plan<Rows>(a, ++s);
+        }
+        const int item = (int)((at - seq_start) / p.tiles);
+        const int t0 = (int)(at - seq_start - (int64_t)item * p.tiles);
+        z.s = s;
+        z.hk = item / p.row_tiles;
+        z.row0 = (item - z.hk * p.row_tiles) * Rows;
+        z.n_rows = min(Rows, p.seq.ql * a.group - z.row0);
+        z.q0 = p.seq.q0;
+        z.kl = p.seq.kl;
+        z.pos0 = p.seq.kl - p.seq.ql;
+        z.causal = p.causal;
+        int unused;
+        key_range(z.pos0 + z.row0 / a.group, z.kl, a.window, z.causal, z.klo, unused);
+        key_range(z.pos0 + (z.row0 + z.n_rows - 1) / a.group, z.kl, a.window, z.causal, unused, z.khi);
+        z.tile0 = p.tile0 + t0;
+        z.steps = (int)min((int64_t)(p.tiles - t0), end - at);
+        z.tiles = p.tiles;
+        z.starts = t0 == 0;
+        z.ends = t0 + z.steps == p.tiles;
+        z.at = at;
+        at += z.steps;
+        return true;
+    }
+};
+
 template <int D, int NB>
 __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_split(const SplitArgs a) {
     using C = SplitCfg<D>;
     constexpr int Rows = 8 * NB;
+    constexpr int S = C::kStages;
     constexpr int KK = D / 16;              // 16-dimension blocks of a head
     constexpr int Chunks = D / 8;           // 16-byte chunks of a head
     constexpr int PerLoad = 32 / Chunks;    // key rows a warp's load instruction covers
-    constexpr int Pad = D + 4;              // floats of a row of the meeting buffer: no bank conflicts
-    static_assert(Rows * Pad * 4 <= C::kRing, "a warp's output fits its ring");
+    static_assert(Rows * D * 4 <= (int)C::kStage, "a warp's output fits a stage of its ring");
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_m[kWarps][Rows], s_l[kWarps][Rows];
+    __shared__ Piece s_piece[2];   // the run's current piece and the next one (two places used in turn)
     dg::pdl_wait();
     dg::pdl_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Run run = find_run<Rows>(a);
     if (run.start >= run.end) {
-        if (tid == 0) a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (tid == 0) a.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
     unsigned char* ring = smem + (size_t)warp * C::kRing;
     const uint32_t ring_s = dg::smem_u32(ring);
     const int page_mask = (1 << a.kv.page_shift) - 1;
     const int ch = lane % Chunks, rsub = lane / Chunks;
-    int4 desc = make_int4(0, 0, 0, 0);
+    int4 desc0 = make_int4(0, 0, 0, 0), desc1 = desc0;
 
-    int64_t at = run.start;             // on the line
-    int64_t seq_start = run.seq_start;
-    int s = run.seq;
-    SeqPlan p = seq_plan<Rows>(a, s);
-    while (true) {
-        while (at >= seq_start + p.cost(a.Hkv)) {   // the next sequence that has work
-            seq_start += p.cost(a.Hkv);
-            p = seq_plan<Rows>(a, ++s);
+    // Loads run ahead of the products by up to S steps, past the end of a piece into the next one.
+    // Steps are counted over the run: step g lies in stage g % S, and is one cp.async group.
+    uint32_t issued = 0, consumed = 0;
+    struct {                       // the piece the loads are in
+        const int32_t* table;
+        int64_t head_at;
+        int klo, khi, key0, steps, step;
+        int32_t e0, e1;            // pages of the next step's first and second eight keys
+    } in = {};
+    auto entry = [&](int half) -> int32_t {
+        if (in.step >= in.steps) return -1;
+        const int j = in.key0 + in.step * kTileKeys + half * 8;
+        return j <= in.khi && j + 7 >= in.klo ? in.table[j >> a.kv.page_shift] : -1;
+    };
+    auto open = [&](const Piece& z) {
+        in.table = a.kv.page_table + (int64_t)z.s * a.kv.max_pages;
+        in.head_at = z.hk * a.kv.head_stride + ch * 8;
+        in.klo = z.klo;
+        in.khi = z.khi;
+        in.key0 = z.tile0 * kTileKeys + warp * kStep;
+        in.steps = z.steps;
+        in.step = 0;
+        in.e0 = entry(0);
+        in.e1 = entry(1);
+    };
+    auto issue = [&]() {   // one step's keys and values into its stage; then the next step's pages
+        const int j0 = in.key0 + in.step * kTileKeys;
+        const uint32_t dst = ring_s + (issued % S) * C::kStage;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int32_t page = half ? in.e1 : in.e0;
+            const bool good = page >= 0 && page < a.kv.n_pages;
+            const int jh = j0 + half * 8;
+            if (!good && jh <= in.khi && jh + 7 >= in.klo && lane == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+            const int64_t off = good ? page * a.kv.page_stride + (int64_t)((jh & page_mask) + rsub) * a.kv.slot_stride + in.head_at : 0;
+            const uint16_t* ks = a.kv.k + off;
+            const uint16_t* vs = a.kv.v + off;
+            const int64_t hop = good ? PerLoad * a.kv.slot_stride : 0;
+#pragma unroll
+            for (int i = 0; i < 8 / PerLoad; ++i) {
+                const int row = half * 8 + i * PerLoad + rsub;
+                const bool ok = good && j0 + row >= in.klo && j0 + row <= in.khi;
+                const uint32_t d = dst + (uint32_t)row * (D * 2) + (uint32_t)((ch ^ (row & 7)) * 16);
+                cp_async16(d, ks, ok);
+                cp_async16(d + C::kHalf, vs, ok);
+                ks += hop;
+                vs += hop;
+            }
         }
-        // the piece: tiles t0 .. t1 - 1 of one item
-        const int item = (int)((at - seq_start) / p.tiles);
-        const int t0 = (int)(at - seq_start - (int64_t)item * p.tiles);
-        const int t1 = (int)min((int64_t)p.tiles, t0 + (run.end - at));
-        const int hk = item / p.row_tiles, row0 = (item - hk * p.row_tiles) * Rows;
-        const int n_rows = min(Rows, p.seq.ql * a.group - row0);
-        const int pos0 = p.seq.kl - p.seq.ql;
-        int klo, khi, unused;
-        key_range(pos0 + row0 / a.group, p.seq.kl, a.window, p.causal, klo, unused);
-        key_range(pos0 + (row0 + n_rows - 1) / a.group, p.seq.kl, a.window, p.causal, unused, khi);
+        cp_async_commit();
+        ++issued;
+        ++in.step;
+        in.e0 = entry(0);
+        in.e1 = entry(1);
+    };
 
-        // Q^T as the second operand: lane holds column lane / 4, dimensions 2 (lane % 4) + {0, 1} (+ 8)
-        uint32_t qf[NB][KK][2];
+    Walk<Rows> walk{run.start, run.seq_start, run.end, run.seq, seq_plan<Rows>(a, run.seq)};
+    int place = 0;                 // of the current piece in s_piece
+    bool more;                     // there is a next one
+    bool ahead = false;            // the loads are in it
+    {
+        Piece z;
+        walk.next(a, z);
+        open(z);
+        if (tid == 0) s_piece[0] = z;
+        more = walk.next(a, z);
+        if (more && tid == 0) s_piece[1] = z;
+    }
+    __syncthreads();
+    // Fills the ring up to `limit` steps ahead of the products.
+    auto fill = [&](uint32_t limit) {
+        while (issued - consumed < limit) {
+            if (in.step < in.steps) {
+                issue();
+            } else if (more && !ahead) {
+                open(s_piece[place ^ 1]);
+                ahead = true;
+            } else {
+                break;
+            }
+        }
+    };
+    // Q^T as the second operand: lane holds column lane / 4, dimensions 2 (lane % 4) + {0, 1} (+ 8)
+    uint32_t qf[NB][KK][2];
+    auto load_q = [&](const Piece& z) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int r = row0 + nb * 8 + lane / 4;
-            const bool ok = nb * 8 + lane / 4 < n_rows;
-            const int qi = ok ? r / a.group : 0;
-            const uint16_t* src = a.q + ((int64_t)(p.seq.q0 + qi) * a.Hq + hk * a.group + (ok ? r - qi * a.group : 0)) * D +
-                                  (lane & 3) * 2;
+            const bool ok = nb * 8 + lane / 4 < z.n_rows;
+            const int r = z.row0 + nb * 8 + (ok ? lane / 4 : 0);
+            const int qi = r / a.group;
+            const uint16_t* src = a.q + ((int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (r - qi * a.group)) * D + (lane & 3) * 2;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 qf[nb][kk][0] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
                 qf[nb][kk][1] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
             }
         }
-        // the ranges of this lane's rows of S^T (columns 2 (lane % 4) + {0, 1}); the item's own
-        // narrowest one decides whether a step needs its mask
-        int rlo[NB][2], rhi[NB][2], all_lo, all_hi;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = min(nb * 8 + (lane & 3) * 2 + e, n_rows - 1);
-                key_range(pos0 + (row0 + r) / a.group, p.seq.kl, a.window, p.causal, rlo[nb][e], rhi[nb][e]);
-            }
-        key_range(pos0 + (row0 + n_rows - 1) / a.group, p.seq.kl, a.window, p.causal, all_lo, unused);
-        key_range(pos0 + row0 / a.group, p.seq.kl, a.window, p.causal, unused, all_hi);
+    };
+    fill(S - 1);
+    load_q(s_piece[0]);
 
+    const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_col = (lane >> 4) & 1;
+    const int v_row = (lane & 7) + ((lane >> 4) & 1) * 8, v_col = (lane >> 3) & 1;
+    while (true) {
+        // the ranges of this lane's rows of S^T (columns 2 (lane % 4) + {0, 1}), and the narrowest: it
+        // decides whether a step needs its mask
+        const int klo = s_piece[place].klo, khi = s_piece[place].khi, steps = s_piece[place].steps;
+        const int key0 = s_piece[place].tile0 * kTileKeys + warp * kStep;
+        int rlo[NB][2], rhi[NB][2], all_lo, all_hi;
+        {
+            const Piece& z = s_piece[place];
+            int unused;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = min(nb * 8 + (lane & 3) * 2 + e, z.n_rows - 1);
+                    key_range(z.pos0 + (z.row0 + r) / a.group, z.kl, a.window, z.causal, rlo[nb][e], rhi[nb][e]);
+                }
+            key_range(z.pos0 + (z.row0 + z.n_rows - 1) / a.group, z.kl, a.window, z.causal, all_lo, unused);
+            key_range(z.pos0 + z.row0 / a.group, z.kl, a.window, z.causal, unused, all_hi);
+        }
         float acc[KK][NB][4];
 #pragma unroll
         for (int mt = 0; mt < KK; ++mt)
@@ -297,58 +422,17 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
 
-        const int32_t* table = a.kv.page_table + (int64_t)s * a.kv.max_pages;
-        const int64_t head_at = hk * a.kv.head_stride + ch * 8;
-        const int steps = t1 - t0;
-        const int key0 = (p.tile0 + t0) * kTileKeys + warp * kStep;   // first key of this warp's first step
-        // the pages of a step's first and second eight keys (one page when pages hold 16 or more)
-        auto entry = [&](int step, int half) -> int32_t {
-            const int j = key0 + step * kTileKeys + half * 8;
-            return step < steps && j <= khi && j + 7 >= klo ? table[j >> a.kv.page_shift] : -1;
-        };
-        int32_t e0 = entry(0, 0), e1 = entry(0, 1);
-        auto issue = [&](int step) {   // the step's keys and values into its stage; then the next step's pages
-            if (step < steps) {
-                const int j0 = key0 + step * kTileKeys;
-                const uint32_t dst = ring_s + (uint32_t)(step % C::kStages) * C::kStage;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int32_t page = half ? e1 : e0;
-                    const bool good = page >= 0 && page < a.kv.n_pages;
-                    const int jh = j0 + half * 8;
-                    if (!good && jh <= khi && jh + 7 >= klo && lane == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-                    const int64_t off = good ? page * a.kv.page_stride + (int64_t)((jh & page_mask) + rsub) * a.kv.slot_stride + head_at : 0;
-                    const uint16_t* ks = a.kv.k + off;
-                    const uint16_t* vs = a.kv.v + off;
-                    const int64_t hop = good ? PerLoad * a.kv.slot_stride : 0;
-#pragma unroll
-                    for (int i = 0; i < 8 / PerLoad; ++i) {
-                        const int row = half * 8 + i * PerLoad + rsub;
-                        const bool ok = good && j0 + row >= klo && j0 + row <= khi;
-                        const uint32_t d = dst + (uint32_t)row * (D * 2) + (uint32_t)((ch ^ (row & 7)) * 16);
-                        cp_async16(d, ks, ok);
-                        cp_async16(d + C::kHalf, vs, ok);
-                        ks += hop;
-                        vs += hop;
-                    }
-                }
-                e0 = entry(step + 1, 0);
-                e1 = entry(step + 1, 1);
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < C::kStages - 1; ++i) issue(i);
-
-        const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_col = (lane >> 4) & 1;
-        const int v_row = (lane & 7) + ((lane >> 4) & 1) * 8, v_col = (lane >> 3) & 1;
         for (int step = 0; step < steps; ++step) {
-            cp_async_wait<C::kStages - 2>();
+            if (issued - consumed == (uint32_t)(S - 1))
+                cp_async_wait<S - 2>();
+            else
+                cp_async_wait<0>();
             __syncwarp();   // every lane's part has landed, and the stage refilled now has been read
-            issue(step + C::kStages - 1);
+            fill(S);
+            const uint32_t st = ring_s + (consumed % S) * C::kStage;
+            ++consumed;
             const int j0 = key0 + step * kTileKeys;
             if (j0 > khi || j0 + kStep - 1 < klo) continue;   // no key of the item
-            const uint32_t st = ring_s + (uint32_t)(step % C::kStages) * C::kStage;
             float c[NB][2][4];   // S^T, even and odd 16-dimension blocks apart: two chains
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -416,10 +500,12 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
             }
         }
 
-        // the warps meet: each leaves its unnormalised output in its own ring, and its statistics
-        cp_async_wait<0>();
+        // The warps meet: each leaves its unnormalised output in the stage it read last (the others are
+        // already being filled for the next piece), its rows' dimensions turned so that the lanes' banks
+        // differ, and its statistics.
+        const uint32_t met = ((consumed - 1u) % S) * C::kStage;
         __syncwarp();
-        float* mo = reinterpret_cast<float*>(ring);
+        float* mo = reinterpret_cast<float*>(ring + met);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -431,18 +517,19 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
                     s_m[warp][nb * 8 + lane * 2 + e] = m[nb][e];
                     s_l[warp][nb * 8 + lane * 2 + e] = sum;
                 }
+                const int r = nb * 8 + (lane & 3) * 2 + e, turn = (lane & 3) << 3;
 #pragma unroll
                 for (int mt = 0; mt < KK; ++mt) {
-                    const int at_row = (nb * 8 + (lane & 3) * 2 + e) * Pad + mt * 16 + lane / 4;
-                    mo[at_row] = acc[mt][nb][e];
-                    mo[at_row + 8] = acc[mt][nb][e + 2];
+                    mo[r * D + ((mt * 16 + lane / 4) ^ turn)] = acc[mt][nb][e];
+                    mo[r * D + ((mt * 16 + 8 + lane / 4) ^ turn)] = acc[mt][nb][e + 2];
                 }
             }
         }
+        if (more) load_q(s_piece[place ^ 1]);   // on its way while the warps meet
         __syncthreads();
-        const bool starts = t0 == 0, ends = t1 == p.tiles;
-        const int64_t slot = (int64_t)blockIdx.x * 2 + (starts ? 1 : 0);
-        for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
+        const Piece z = s_piece[place];
+        const int64_t slot = (int64_t)blockIdx.x * 2 + (z.starts ? 1 : 0);
+        for (int i = tid; i < z.n_rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
             float M = -INFINITY;
 #pragma unroll
@@ -453,15 +540,16 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
             for (int w = 0; w < kWarps; ++w) {
                 const float f = s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - M);
                 L += s_l[w][r] * f;
-                const float4 v = *reinterpret_cast<const float4*>(smem + (size_t)w * C::kRing + ((size_t)r * Pad + d) * 4);
+                const float4 v = *reinterpret_cast<const float4*>(smem + (size_t)w * C::kRing + met +
+                                                                  ((size_t)r * D + (d ^ (((r >> 1) & 3) << 3))) * 4);
                 o.x += v.x * f;
                 o.y += v.y * f;
                 o.z += v.z * f;
                 o.w += v.w * f;
             }
-            if (starts && ends) {
-                const int rr = row0 + r, qi = rr / a.group;
-                const int64_t out = (int64_t)(p.seq.q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
+            if (z.starts && z.ends) {
+                const int rr = z.row0 + r, qi = rr / a.group;
+                const int64_t out = (int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (rr - qi * a.group);
                 const float inv = L > 0.f ? 1.f / L : 0.f;
                 *reinterpret_cast<uint2*>(a.o + out * D + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -471,15 +559,27 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
                 if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * Rows + r) * 2) = make_float2(M, L);
             }
         }
-        if (starts && !ends) {
-            const int64_t last = (at + p.tiles - 1) / run.per_cta;   // the CTA that has the item's last tile
-            desc = make_int4(s, item, (int)(last - blockIdx.x), 0);
+        if (z.starts && !z.ends) {
+            const int64_t last = (z.at + z.tiles - 1) / run.per_cta;   // the CTA that has the item's last tile
+            desc0 = make_int4((int)(last - blockIdx.x), z.n_rows, z.q0, z.hk);
+            desc1 = make_int4(z.row0, 0, 0, 0);
         }
-        at += steps;
-        if (at >= run.end) break;
-        __syncthreads();   // the meeting buffers are the next piece's rings
+        if (!more) break;
+        __syncthreads();   // the meeting buffers and the piece's place are free
+        // on to the next piece; the loads are in it already, or begin with it
+        if (!ahead) open(s_piece[place ^ 1]);
+        ahead = false;
+        Piece w;
+        more = walk.next(a, w);
+        if (more && tid == 0) s_piece[place] = w;
+        place ^= 1;
+        __syncthreads();   // the next piece's successor is in its place
+        fill(S - 1);
     }
-    if (tid == 0) a.desc[blockIdx.x] = desc;
+    if (tid == 0) {
+        a.desc[2 * blockIdx.x] = desc0;
+        a.desc[2 * blockIdx.x + 1] = desc1;
+    }
 }
 
 // Joins an item's pieces: the last one of CTA c (slot 1) and the first ones (slot 0) of the CTAs
@@ -492,12 +592,9 @@ __global__ void __launch_bounds__(128) k_paged_join(const SplitArgs a) {
     dg::pdl_wait();
     dg::pdl_release();
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int4 desc = a.desc[c];
-    if (desc.z == 0) return;
-    const int n = desc.z + 1;
-    const SeqPlan p = seq_plan<Rows>(a, desc.x);
-    const int hk = desc.y / p.row_tiles, row0 = (desc.y - hk * p.row_tiles) * Rows;
-    const int n_rows = min(Rows, p.seq.ql * a.group - row0);
+    const int4 desc0 = a.desc[2 * c], desc1 = a.desc[2 * c + 1];
+    if (desc0.x == 0) return;
+    const int n = desc0.x + 1, n_rows = desc0.y, q0 = desc0.z, hk = desc0.w, row0 = desc1.x;
     auto slot = [&](int i) -> int64_t { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
     for (int r = warp; r < n_rows; r += 4) {
         float M = -INFINITY;
@@ -533,7 +630,7 @@ __global__ void __launch_bounds__(128) k_paged_join(const SplitArgs a) {
         }
         const float L = s_l[r], inv = L > 0.f ? 1.f / L : 0.f;
         const int rr = row0 + r, qi = rr / a.group;
-        const int64_t out = (int64_t)(p.seq.q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
+        const int64_t out = (int64_t)(q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
         *reinterpret_cast<uint2*>(a.o + out * D + d) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (d == 0 && a.lse) a.lse[out] = L > 0.f ? (s_m[r] + log2f(L)) * kLn2 : -INFINITY;
@@ -552,7 +649,7 @@ int item_rows(int32_t max_q_len, int32_t group) { return (int64_t)max_q_len * gr
 bool split_path(int32_t max_q_len, int32_t group) { return max_q_len == 1 || (int64_t)max_q_len * group <= DG_SPLIT_ROWS; }
 
 size_t split_bytes(int rows, int32_t D) {
-    return (size_t)kMaxCtas * 16 + (size_t)kMaxCtas * 2 * rows * ((size_t)D + 2) * 4;
+    return (size_t)kMaxCtas * 32 + (size_t)kMaxCtas * 2 * rows * ((size_t)D + 2) * 4;
 }
 
 template <int D, int NB>
@@ -560,9 +657,16 @@ dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
     using C = SplitCfg<D>;
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
-    if (cudaFuncSetAttribute(k_paged_split<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
-        cudaSuccess)
-        return DG_ERR_CUDA;
+    // the attribute once a device: 0.4 us of a call that takes the host 4
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DG_ERR_CUDA;
+    if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+        if (cudaFuncSetAttribute(k_paged_split<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
+            cudaSuccess)
+            return DG_ERR_CUDA;
+        if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     const unsigned grid = (unsigned)std::min(sms * C::kCtasPerSm, kMaxCtas);
     cudaError_t e = dghost::launch_pdl(k_paged_split<D, NB>, dim3(grid), dim3(kThreads), C::kSmem, stream, a);
     dghost::count_launch();
@@ -618,7 +722,7 @@ extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* ca
     a.window = window;
     a.scale_log2 = scale * kLog2e;
     a.desc = static_cast<int4*>(workspace);
-    a.part_o = reinterpret_cast<float*>(a.desc + kMaxCtas);
+    a.part_o = reinterpret_cast<float*>(a.desc + 2 * kMaxCtas);
     a.part_ml = a.part_o + (size_t)kMaxCtas * 2 * rows * D;
     a.status = dghost::status_word();
     cudaStream_t st = (cudaStream_t)stream;
