@@ -32,8 +32,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 16;                  // keys of a warp's step
-constexpr int kTileKeys = kWarps * kStep;  // keys of a tile
 constexpr int kMaxCtas = 512;              // grid bound the workspace is sized for
 constexpr float kRescaleAbove = 8.f;       // log2 units the maximum may grow before it moves: P <= 2^8
 
@@ -55,7 +53,9 @@ struct SplitArgs {
 
 template <int D>
 struct SplitCfg {
-    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr int kStep = D == 64 ? 32 : 16;        // keys of a warp's step
+    static constexpr int kTileKeys = kWarps * kStep;       // keys of a tile
+    static constexpr int kStages = 3;
     static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
     static constexpr uint32_t kHalf = kStep * D * 2;       // the keys of a step (or its values)
     static constexpr uint32_t kStage = 2 * kHalf;
@@ -123,7 +123,7 @@ struct SeqPlan {
     DG_DEVINL int64_t cost(int Hkv) const { return (int64_t)row_tiles * tiles * Hkv; }
 };
 
-template <int Rows>
+template <int Rows, int Tile>
 DG_DEVINL SeqPlan seq_plan(const SplitArgs& a, int s) {
     SeqPlan p;
     p.seq = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
@@ -135,8 +135,8 @@ DG_DEVINL SeqPlan seq_plan(const SplitArgs& a, int s) {
         int lo, hi, first, last;
         key_range(p.seq.kl - p.seq.ql, p.seq.kl, a.window, p.causal, first, hi);
         key_range(p.seq.kl - 1, p.seq.kl, a.window, p.causal, lo, last);
-        p.tile0 = first / kTileKeys;
-        p.tiles = last / kTileKeys - p.tile0 + 1;
+        p.tile0 = first / Tile;
+        p.tiles = last / Tile - p.tile0 + 1;
     }
     return p;
 }
@@ -154,37 +154,60 @@ struct Run {
     int64_t seq_start;  // and where it begins
 };
 
-template <int Rows>
+template <int Rows, int Tile>
 DG_DEVINL Run find_run(const SplitArgs& a) {
     __shared__ int64_t sums[kWarps];
     __shared__ int64_t found_start;
     __shared__ int found_seq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Run r;
+    auto cut = [&](int64_t total) {
+        r.total = total;
+        r.per_cta = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
+        r.start = min(total, (int64_t)blockIdx.x * r.per_cta);
+        r.end = min(total, r.start + r.per_cta);
+        r.seq = 0;
+        r.seq_start = 0;
+    };
+    auto cost_of = [&](int s) -> int64_t {
+        const SeqPlan p = seq_plan<Rows, Tile>(a, s);
+        if (blockIdx.x == 0 && (!p.seq.ok || p.seq.ql > a.max_q_len)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+        return p.cost(a.Hkv);
+    };
+    if (a.n_seq <= 32) {   // every warp by itself: nothing to wait for
+        const int64_t c = lane < a.n_seq ? cost_of(lane) : 0;
+        int64_t incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        cut(__shfl_sync(0xffffffffu, incl, 31));
+        const uint32_t hit = __ballot_sync(0xffffffffu, c > 0 && incl - c <= r.start && r.start < incl);
+        if (hit) {
+            r.seq = __ffs(hit) - 1;
+            r.seq_start = __shfl_sync(0xffffffffu, incl - c, r.seq);
+        }
+        return r;
+    }
     int64_t mine = 0, first_cost = 0;
     for (int s = tid; s < a.n_seq; s += kThreads) {
-        const SeqPlan p = seq_plan<Rows>(a, s);
-        const int64_t c = p.cost(a.Hkv);
+        const int64_t c = cost_of(s);
         if (s == tid) first_cost = c;
         mine += c;
-        if (blockIdx.x == 0 && (!p.seq.ok || p.seq.ql > a.max_q_len)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
     }
     mine = warp_sum(mine);
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
-    Run r;
-    r.total = 0;
+    int64_t total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) r.total += sums[w];
-    r.per_cta = max((int64_t)1, (r.total + gridDim.x - 1) / gridDim.x);
-    r.start = min(r.total, (int64_t)blockIdx.x * r.per_cta);
-    r.end = min(r.total, r.start + r.per_cta);
-    r.seq = 0;
-    r.seq_start = 0;
+    for (int w = 0; w < kWarps; ++w) total += sums[w];
+    cut(total);
     if (r.start >= r.end) return r;   // the same for the whole CTA
     int64_t base = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += kThreads) {
         const int s = s0 + tid;
-        const int64_t c = s0 == 0 ? first_cost : s < a.n_seq ? seq_plan<Rows>(a, s).cost(a.Hkv) : 0;
+        const int64_t c = s0 == 0 ? first_cost : s < a.n_seq ? seq_plan<Rows, Tile>(a, s).cost(a.Hkv) : 0;
         int64_t incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -227,7 +250,7 @@ struct Piece {
 };
 
 // Walks a run piece by piece.
-template <int Rows>
+template <int Rows, int Tile>
 struct Walk {
     int64_t at, seq_start, end;
     int s;
@@ -237,7 +260,7 @@ struct Walk {
         if (at >= end) return false;
         while (at >= seq_start + p.cost(a.Hkv)) {   // the next sequence that has work
             seq_start += p.cost(a.Hkv);
-            p = seq_plan<Rows>(a, ++s);
+            p = seq_plan<Rows, Tile>(a, ++s);
         }
         const int item = (int)((at - seq_start) / p.tiles);
         const int t0 = (int)(at - seq_start - (int64_t)item * p.tiles);
@@ -267,7 +290,8 @@ template <int D, int NB>
 __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_split(const SplitArgs a) {
     using C = SplitCfg<D>;
     constexpr int Rows = 8 * NB;
-    constexpr int S = C::kStages;
+    constexpr int S = C::kStages, Tile = C::kTileKeys;
+    constexpr int KB = C::kStep / 16;       // 16-key blocks of a step
     constexpr int KK = D / 16;              // 16-dimension blocks of a head
     constexpr int Chunks = D / 8;           // 16-byte chunks of a head
     constexpr int PerLoad = 32 / Chunks;    // key rows a warp's load instruction covers
@@ -278,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
     dg::pdl_wait();
     dg::pdl_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Run run = find_run<Rows>(a);
+    const Run run = find_run<Rows, Tile>(a);
     if (run.start >= run.end) {
         if (tid == 0) a.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
@@ -296,11 +320,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
         const int32_t* table;
         int64_t head_at;
         int klo, khi, key0, steps, step;
-        int32_t e0, e1;            // pages of the next step's first and second eight keys
+        int32_t e[2 * KB];         // the pages of the next step's keys, eight at a time
     } in = {};
     auto entry = [&](int half) -> int32_t {
         if (in.step >= in.steps) return -1;
-        const int j = in.key0 + in.step * kTileKeys + half * 8;
+        const int j = in.key0 + in.step * Tile + half * 8;
         return j <= in.khi && j + 7 >= in.klo ? in.table[j >> a.kv.page_shift] : -1;
     };
     auto open = [&](const Piece& z) {
@@ -308,18 +332,18 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
         in.head_at = z.hk * a.kv.head_stride + ch * 8;
         in.klo = z.klo;
         in.khi = z.khi;
-        in.key0 = z.tile0 * kTileKeys + warp * kStep;
+        in.key0 = z.tile0 * Tile + warp * C::kStep;
         in.steps = z.steps;
         in.step = 0;
-        in.e0 = entry(0);
-        in.e1 = entry(1);
+#pragma unroll
+        for (int b = 0; b < 2 * KB; ++b) in.e[b] = entry(b);
     };
     auto issue = [&]() {   // one step's keys and values into its stage; then the next step's pages
-        const int j0 = in.key0 + in.step * kTileKeys;
+        const int j0 = in.key0 + in.step * Tile;
         const uint32_t dst = ring_s + (issued % S) * C::kStage;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int32_t page = half ? in.e1 : in.e0;
+        for (int half = 0; half < 2 * KB; ++half) {
+            const int32_t page = in.e[half];
             const bool good = page >= 0 && page < a.kv.n_pages;
             const int jh = j0 + half * 8;
             if (!good && jh <= in.khi && jh + 7 >= in.klo && lane == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
@@ -341,11 +365,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
         cp_async_commit();
         ++issued;
         ++in.step;
-        in.e0 = entry(0);
-        in.e1 = entry(1);
+#pragma unroll
+        for (int b = 0; b < 2 * KB; ++b) in.e[b] = entry(b);
     };
 
-    Walk<Rows> walk{run.start, run.seq_start, run.end, run.seq, seq_plan<Rows>(a, run.seq)};
+    Walk<Rows, Tile> walk{run.start, run.seq_start, run.end, run.seq, seq_plan<Rows, Tile>(a, run.seq)};
     int place = 0;                 // of the current piece in s_piece
     bool more;                     // there is a next one
     bool ahead = false;            // the loads are in it
@@ -396,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
         // the ranges of this lane's rows of S^T (columns 2 (lane % 4) + {0, 1}), and the narrowest: it
         // decides whether a step needs its mask
         const int klo = s_piece[place].klo, khi = s_piece[place].khi, steps = s_piece[place].steps;
-        const int key0 = s_piece[place].tile0 * kTileKeys + warp * kStep;
+        const int key0 = s_piece[place].tile0 * Tile + warp * C::kStep;
         int rlo[NB][2], rhi[NB][2], all_lo, all_hi;
         {
             const Piece& z = s_piece[place];
@@ -431,42 +455,61 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
             fill(S);
             const uint32_t st = ring_s + (consumed % S) * C::kStage;
             ++consumed;
-            const int j0 = key0 + step * kTileKeys;
-            if (j0 > khi || j0 + kStep - 1 < klo) continue;   // no key of the item
-            float c[NB][2][4];   // S^T, even and odd 16-dimension blocks apart: two chains
+            const int j0 = key0 + step * Tile;
+            if (j0 > khi || j0 + C::kStep - 1 < klo) continue;   // no key of the item
+            float x[KB][NB][4];   // S^T: [key lane / 4 (+ 8 for 2, 3)][row 2 (lane % 4) + (0, 1)]
+            {
+                float c[KB][NB][2][4];   // even and odd 16-dimension blocks apart: two chains a block of keys
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[kb][nb][0][e] = c[kb][nb][1][e] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        uint32_t kf[4];
+                        ldmatrix4(kf, st + (uint32_t)(kb * 16 + k_row) * (D * 2) + (uint32_t)(((kk * 2 + k_col) ^ (lane & 7)) * 16));
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) mma(c[kb][nb][kk & 1], kf, qf[nb][kk][0], qf[nb][kk][1]);
+                    }
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[kb][nb][e] = (c[kb][nb][0][e] + c[kb][nb][1][e]) * a.scale_log2;
+            }
+            if (j0 < all_lo || j0 + C::kStep - 1 > all_hi) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = j0 + kb * 16 + lane / 4 + (e & 2) * 4;
+                            if (j < rlo[nb][e & 1] || j > rhi[nb][e & 1]) x[kb][nb][e] = -INFINITY;
+                        }
+            }
+            float top[NB][2];   // this lane's largest score of each of its rows
+            bool grown = false;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[nb][0][e] = c[nb][1][e] = 0.f;
+                for (int e = 0; e < 2; ++e) {
+                    top[nb][e] = fmaxf(x[0][nb][e], x[0][nb][e + 2]);
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                uint32_t kf[4];
-                ldmatrix4(kf, st + (uint32_t)k_row * (D * 2) + (uint32_t)(((kk * 2 + k_col) ^ (lane & 7)) * 16));
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma(c[nb][kk & 1], kf, qf[nb][kk][0], qf[nb][kk][1]);
-            }
-            const bool whole = j0 >= all_lo && j0 + kStep - 1 <= all_hi;
-            float x[NB][4];   // [key lane / 4 (+ 8 for 2, 3)][row 2 (lane % 4) + (0, 1)], in log2 units
-            bool grown = false;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[nb][e] = (c[nb][0][e] + c[nb][1][e]) * a.scale_log2;
-                    if (!whole) {
-                        const int j = j0 + lane / 4 + (e & 2) * 4;
-                        if (j < rlo[nb][e & 1] || j > rhi[nb][e & 1]) x[nb][e] = -INFINITY;
-                    }
+                    for (int kb = 1; kb < KB; ++kb) top[nb][e] = fmaxf(top[nb][e], fmaxf(x[kb][nb][e], x[kb][nb][e + 2]));
+                    grown = grown || top[nb][e] > m[nb][e] + kRescaleAbove;
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) grown = grown || fmaxf(x[nb][e], x[nb][e + 2]) > m[nb][e] + kRescaleAbove;
-            }
             if (__any_sync(0xffffffffu, grown)) {   // some row's maximum moves: new references, old sums rescaled
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(x[nb][e], x[nb][e + 2]);
+                        float mx = top[nb][e];
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                         mx = fmaxf(mx, m[nb][e]);
@@ -480,24 +523,29 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
                         m[nb][e] = mx;
                     }
             }
-            uint32_t pf[NB][2];
+            uint32_t pf[KB][NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const float r0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], r1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
-                const float p0 = ex2(x[nb][0] - r0), p1 = ex2(x[nb][1] - r1);
-                const float p2 = ex2(x[nb][2] - r0), p3 = ex2(x[nb][3] - r1);
-                l[nb][0] += p0 + p2;
-                l[nb][1] += p1 + p3;
-                pf[nb][0] = transpose8x8(pack_bf16x2(p0, p1));
-                pf[nb][1] = transpose8x8(pack_bf16x2(p2, p3));
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const float p0 = ex2(x[kb][nb][0] - r0), p1 = ex2(x[kb][nb][1] - r1);
+                    const float p2 = ex2(x[kb][nb][2] - r0), p3 = ex2(x[kb][nb][3] - r1);
+                    l[nb][0] += p0 + p2;
+                    l[nb][1] += p1 + p3;
+                    pf[kb][nb][0] = transpose8x8(pack_bf16x2(p0, p1));
+                    pf[kb][nb][1] = transpose8x8(pack_bf16x2(p2, p3));
+                }
             }
 #pragma unroll
-            for (int mt = 0; mt < KK; ++mt) {
-                uint32_t vf[4];
-                ldmatrix4_trans(vf, st + C::kHalf + (uint32_t)v_row * (D * 2) + (uint32_t)(((mt * 2 + v_col) ^ (lane & 7)) * 16));
+            for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma(acc[mt][nb], vf, pf[nb][0], pf[nb][1]);
-            }
+                for (int mt = 0; mt < KK; ++mt) {
+                    uint32_t vf[4];
+                    ldmatrix4_trans(vf, st + C::kHalf + (uint32_t)(kb * 16 + v_row) * (D * 2) + (uint32_t)(((mt * 2 + v_col) ^ (lane & 7)) * 16));
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma(acc[mt][nb], vf, pf[kb][nb][0], pf[kb][nb][1]);
+                }
         }
 
         // The warps meet: each leaves its unnormalised output in the stage it read last (the others are
@@ -583,12 +631,21 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
 }
 
 // Joins an item's pieces: the last one of CTA c (slot 1) and the first ones (slot 0) of the CTAs
-// that follow it, in that order.  blockIdx.x = c, blockIdx.y = 64 of the dimensions.
+// that follow it.  blockIdx.x = c, blockIdx.y = 64 of the dimensions; most blocks find nothing to join.
+// A thread owns four dimensions of a row for every kGroups-th piece (a long context of one head is joined
+// from dozens: reading them one after another took most of the kernel); the groups add up in
+// shared memory in a fixed order.  The first pieces are on their way while the weights are worked out.
+constexpr int kJoinThreads = 512;
+
 template <int D, int NB>
-__global__ void __launch_bounds__(128) k_paged_join(const SplitArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const SplitArgs a) {
     constexpr int Rows = 8 * NB;
-    __shared__ float w[kMaxCtas][Rows];   // the pieces' weights
+    constexpr int kPlaces = Rows * 16;               // float4s of 64 dimensions of the rows
+    constexpr int kGroups = kJoinThreads / kPlaces;  // 4 or 2
+    constexpr int kEarly = 4;                        // pieces a thread asks for before it knows their weights
+    __shared__ float w[kMaxCtas][Rows];              // the pieces' maxima, then their weights
     __shared__ float s_l[Rows], s_m[Rows];
+    __shared__ float4 part[kGroups > 1 ? kGroups - 1 : 1][kPlaces];
     dg::pdl_wait();
     dg::pdl_release();
     const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -596,45 +653,63 @@ __global__ void __launch_bounds__(128) k_paged_join(const SplitArgs a) {
     if (desc0.x == 0) return;
     const int n = desc0.x + 1, n_rows = desc0.y, q0 = desc0.z, hk = desc0.w, row0 = desc1.x;
     auto slot = [&](int i) -> int64_t { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
-    for (int r = warp; r < n_rows; r += 4) {
+    const int group = tid / kPlaces, place = tid - group * kPlaces;
+    const int r = place / 16, d = (int)blockIdx.y * 64 + (place & 15) * 4;
+    const bool mine = r < n_rows;
+    auto piece = [&](int k) { return *reinterpret_cast<const float4*>(a.part_o + (slot(k) * Rows + r) * D + d); };
+    float4 early[kEarly];
+#pragma unroll
+    for (int e = 0; e < kEarly; ++e)
+        if (mine && group + e * kGroups < n) early[e] = piece(group + e * kGroups);
+    // weights: a row a warp
+    for (int q = warp; q < n_rows; q += kJoinThreads / 32) {
         float M = -INFINITY;
-        for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[(slot(i) * Rows + r) * 2]);
+        for (int i = lane; i < n; i += 32) {
+            const float v = a.part_ml[(slot(i) * Rows + q) * 2];
+            w[i][q] = v;
+            M = fmaxf(M, v);
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float L = 0.f;
         for (int i = lane; i < n; i += 32) {
-            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot(i) * Rows + r) * 2);
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-            w[i][r] = f;
-            L += ml.y * f;
+            const float m = w[i][q], f = m == -INFINITY ? 0.f : ex2(m - M);
+            w[i][q] = f;
+            L += a.part_ml[(slot(i) * Rows + q) * 2 + 1] * f;
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         if (lane == 0) {
-            s_l[r] = L;
-            s_m[r] = M;
+            s_l[q] = L;
+            s_m[q] = M;
         }
     }
     __syncthreads();
-    for (int i = tid; i < n_rows * 16; i += 128) {
-        const int r = i / 16, d = (int)blockIdx.y * 64 + (i & 15) * 4;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& v, float f) {
+        o.x += v.x * f;
+        o.y += v.y * f;
+        o.z += v.z * f;
+        o.w += v.w * f;
+    };
+    if (mine) {
+#pragma unroll
+        for (int e = 0; e < kEarly; ++e)
+            if (group + e * kGroups < n) add(early[e], w[group + e * kGroups][r]);
 #pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float4 v = *reinterpret_cast<const float4*>(a.part_o + (slot(k) * Rows + r) * D + d);
-            const float f = w[k][r];
-            o.x += v.x * f;
-            o.y += v.y * f;
-            o.z += v.z * f;
-            o.w += v.w * f;
-        }
-        const float L = s_l[r], inv = L > 0.f ? 1.f / L : 0.f;
-        const int rr = row0 + r, qi = rr / a.group;
-        const int64_t out = (int64_t)(q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
-        *reinterpret_cast<uint2*>(a.o + out * D + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (d == 0 && a.lse) a.lse[out] = L > 0.f ? (s_m[r] + log2f(L)) * kLn2 : -INFINITY;
+        for (int k = group + kEarly * kGroups; k < n; k += kGroups) add(piece(k), w[k][r]);
     }
+    if (group > 0) part[group - 1][place] = o;
+    __syncthreads();
+    if (group > 0 || !mine) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) add(part[g - 1][place], 1.f);
+    const float L = s_l[r], inv = L > 0.f ? 1.f / L : 0.f;
+    const int rr = row0 + r, qi = rr / a.group;
+    const int64_t out = (int64_t)(q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
+    *reinterpret_cast<uint2*>(a.o + out * D + d) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (d == 0 && a.lse) a.lse[out] = L > 0.f ? (s_m[r] + log2f(L)) * kLn2 : -INFINITY;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -671,7 +746,7 @@ dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
     cudaError_t e = dghost::launch_pdl(k_paged_split<D, NB>, dim3(grid), dim3(kThreads), C::kSmem, stream, a);
     dghost::count_launch();
     if (e != cudaSuccess) return DG_ERR_CUDA;
-    e = dghost::launch_pdl(k_paged_join<D, NB>, dim3(grid, D / 64), dim3(128), 0, stream, a);
+    e = dghost::launch_pdl(k_paged_join<D, NB>, dim3(grid, D / 64), dim3(kJoinThreads), 0, stream, a);
     dghost::count_launch();
     return dghost::cuda_status(e);
 }
