@@ -424,6 +424,11 @@ def dg_attention(q, k, v, o, cu_q, cu_kv, causal, max_q_len: int, *, lse=None, w
     return rc
 
 
+# The serving calls below are made once a token: their checks are written out, with few calls, because a
+# call of a few microseconds on the device waits for the host.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _refuse(fn, name, t, dtype, shape, dev):
     """Why a tensor is not a contiguous one of dtype and shape (None = any extent) on device dev."""
     if t.dtype != dtype:
@@ -460,7 +465,7 @@ def _on(fn, dev, stream):
 
 def _rows(fn, name, t, heads, d, dev):
     """Address and row stride of t [tokens, heads, d], whose rows hold [heads][d] without gaps."""
-    if t.dtype is not torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{fn}: {name} must be bfloat16, got {t.dtype}")
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != d:
@@ -486,7 +491,7 @@ def _paged_kv(fn, k_cache, v_cache, page_table, kv_len):
     """dg_paged_kv of k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides of the first three) and
     page_table [n_seq, max_pages], kv_len [n_seq] int32; n_seq, Hkv, D and the device."""
     shape, strides = k_cache.shape, k_cache.stride()
-    if (k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16 or len(shape) != 4
+    if (k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16 or len(shape) != 4
             or strides[3] != 1 or v_cache.shape != shape or v_cache.stride() != strides):
         _refuse_cache(fn, k_cache, v_cache)
     n_pages, page_size, Hkv, D = shape
@@ -494,14 +499,18 @@ def _paged_kv(fn, k_cache, v_cache, page_table, kv_len):
     if v_cache.get_device() != dev:
         _refuse(fn, "v_cache", v_cache, v_cache.dtype, (None,) * 4, dev)
     n = kv_len.numel()
-    cols = page_table.shape[-1] if page_table.dim() == 2 else None
-    table = _whole(fn, "page_table", page_table, torch.int32, (n, cols), dev)
-    lens = _whole(fn, "kv_len", kv_len, torch.int32, (n,), dev)
+    if kv_len.dtype is not _I32 or kv_len.dim() != 1 or not kv_len.is_contiguous() or kv_len.get_device() != dev:
+        _refuse(fn, "kv_len", kv_len, _I32, (n,), dev)
+    ts = page_table.shape
+    if (page_table.dtype is not _I32 or len(ts) != 2 or ts[0] != n or not page_table.is_contiguous()
+            or page_table.get_device() != dev):
+        _refuse(fn, "page_table", page_table, _I32, (n, None), dev)
     # the stride of an extent of one says nothing: any valid one will do
     ps, ss, hs, _ = strides
     if n_pages == 1 or page_size == 1 or Hkv == 1:
         ps, ss, hs = (s if e > 1 else D for e, s in zip(shape, (ps, ss, hs)))
-    return _PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), table, lens, n_pages, ps, ss, hs, page_size, cols), n, Hkv, D, dev
+    return (_PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), n_pages, ps, ss,
+                     hs, page_size, ts[1]), n, Hkv, D, dev)
 
 
 def _scratch(fn, nbytes, workspace, dev, stream):
@@ -535,18 +544,24 @@ def dg_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, *, inv_freq=N
     kp, ldk = _rows(fn, "k", k, Hkv, D, dev)
     vp, ldv = _rows(fn, "v", v, Hkv, D, dev)
     Hq, qp, ldq, op = Hkv, None, 0, None
+    if v.shape[0] != total or (q is not None and q.shape[0] != total):
+        raise ValueError(f"{fn}: q, k and v must have as many rows")
     if q is not None:
         Hq = q.shape[1] if q.dim() == 3 else 0
         qp, ldq = _rows(fn, "q", q, Hq, D, dev)
-        op = _whole(fn, "q_out", q_out, torch.bfloat16, (total, Hq, D), dev)
-    if v.shape[0] != total or (q is not None and q.shape[0] != total):
-        raise ValueError(f"{fn}: q, k and v must have as many rows")
-    cu = _whole(fn, "cu_q", cu_q, torch.int32, (n + 1,), dev)
-    half = 0 if inv_freq is None else inv_freq.numel()
-    wp = _whole(fn, "inv_freq", inv_freq, torch.float64, (half,), dev)
-    rc = load().dg_kv_append(kp, ldk, vp, ldv, qp, ldq, op, cu, n, total, Hq, Hkv, D, wp, 2 * half,
-                             1 if interleaved else 0, ctypes.byref(kv), _on(fn, dev, stream))
-    if check:
+        if (q_out.dtype is not _BF16 or q_out.shape != q.shape or not q_out.is_contiguous()
+                or q_out.get_device() != dev):
+            _refuse(fn, "q_out", q_out, _BF16, (total, Hq, D), dev)
+        op = q_out.data_ptr()
+    if cu_q.dtype is not _I32 or cu_q.shape != (n + 1,) or not cu_q.is_contiguous() or cu_q.get_device() != dev:
+        _refuse(fn, "cu_q", cu_q, _I32, (n + 1,), dev)
+    half, wp = 0, None
+    if inv_freq is not None:
+        half = inv_freq.numel()
+        wp = _whole(fn, "inv_freq", inv_freq, torch.float64, (half,), dev)
+    rc = load().dg_kv_append(kp, ldk, vp, ldv, qp, ldq, op, cu_q.data_ptr(), n, total, Hq, Hkv, D, wp, 2 * half,
+                             1 if interleaved else 0, kv, _on(fn, dev, stream))
+    if check and rc:
         _check(fn, rc)
     return rc
 
@@ -562,21 +577,25 @@ def dg_paged_attention(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal,
     kv_len [n] int32, causal [n] uint8, lse [total_q, Hq] float32."""
     fn = "dg_paged_attention"
     kv, n, Hkv, D, dev = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
-    total, Hq = (q.shape[0], q.shape[1]) if q.dim() == 3 else (0, 0)
-    rows = (total, Hq, D)
-    qp = _whole(fn, "q", q, torch.bfloat16, rows, dev)
-    op = _whole(fn, "o", o, torch.bfloat16, rows, dev)
-    lp = _whole(fn, "lse", lse, torch.float32, (total, Hq), dev)
-    cu = _whole(fn, "cu_q", cu_q, torch.int32, (n + 1,), dev)
+    rows = q.shape
+    if q.dtype is not _BF16 or len(rows) != 3 or rows[2] != D or not q.is_contiguous() or q.get_device() != dev:
+        _refuse(fn, "q", q, _BF16, (None, None, D), dev)
+    total, Hq, _ = rows
+    if o.dtype is not _BF16 or o.shape != rows or not o.is_contiguous() or o.get_device() != dev:
+        _refuse(fn, "o", o, _BF16, rows, dev)
+    if cu_q.dtype is not _I32 or cu_q.shape != (n + 1,) or not cu_q.is_contiguous() or cu_q.get_device() != dev:
+        _refuse(fn, "cu_q", cu_q, _I32, (n + 1,), dev)
     cz = _whole(fn, "causal", causal, torch.uint8, (n,), dev)
-    scale = 1.0 / float(D) ** 0.5 if scale is None else float(scale)
+    lp = None if lse is None else _whole(fn, "lse", lse, _F32, (total, Hq), dev)
     st = _on(fn, dev, stream)
     lib = load()
-    need = 0 if workspace is not None else lib.dg_paged_attention_workspace_bytes(n, int(max_q_len), Hq, Hkv, D)
+    max_q_len = int(max_q_len)
+    scale = D ** -0.5 if scale is None else float(scale)
+    need = 0 if workspace is not None else lib.dg_paged_attention_workspace_bytes(n, max_q_len, Hq, Hkv, D)
     workspace, ws_bytes = _scratch(fn, need, workspace, dev, stream)
-    rc = lib.dg_paged_attention(qp, ctypes.byref(kv), op, lp, cu, cz, n, int(max_q_len), total, Hq, Hkv, D,
-                                   int(window), scale, workspace.data_ptr(), ws_bytes, st)
-    if check:
+    rc = lib.dg_paged_attention(q.data_ptr(), kv, o.data_ptr(), lp, cu_q.data_ptr(), cz, n, max_q_len, total, Hq, Hkv,
+                                D, int(window), scale, workspace.data_ptr(), ws_bytes, st)
+    if check and rc:
         _check(fn, rc)
     return rc
 
@@ -618,7 +637,7 @@ def dg_adjust_logits(logits, params, out=None, *, history=None, cu_history=None,
     mi = _whole(fn, "mask_index", mask_index, i32, (n, L), dev)
     rc = load().dg_adjust_logits(xp, dt, ld, op, ldo, n, L, V, pp, hp, ch, nh, pen, bt, bv, cb, nb, mp, words,
                                  n_masks, mi, _on(fn, dev, stream))
-    if check:
+    if check and rc:
         _check(fn, rc)
     return rc
 

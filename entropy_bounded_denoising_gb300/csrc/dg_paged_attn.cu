@@ -30,8 +30,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 512;              // grid bound the workspace is sized for
 constexpr float kRescaleAbove = 8.f;       // log2 units the maximum may grow before it moves: P <= 2^8
 
@@ -51,11 +49,18 @@ struct SplitArgs {
     unsigned* status;
 };
 
-template <int D>
+template <int D, int NB>
 struct SplitCfg {
+    // Warps, keys of a warp's step, stages of its ring and CTAs an SM, measured on contexts from 1k to 128k
+    // keys, one to 256 requests: for heads of 64 (8, 16, 3, 2), (4, 16, 3, 4) and (8, 16, 2, 3) come within 3 % of
+    // (4, 32, 3, 2) either way; for 128 and eight rows (4, 16, 3, 2) takes 228 us where (6, 16, 2, 2) takes 218
+    // and (8, 16, 3, 1) 233 (64 requests over 8k keys), but 16 rows need the registers of eight warps: 64 us
+    // against 70 (32 requests of 5 drafts over 4k); for 256 (4, 16, 3, 1) takes 85 us where (7, 16, 2, 1) takes
+    // 76.5 (128 requests over 1.2k keys), and the same on one long context.
+    static constexpr int kWarps = D == 64 ? 4 : D == 256 ? 7 : NB == 1 ? 6 : 4, kThreads = kWarps * 32;
     static constexpr int kStep = D == 64 ? 32 : 16;        // keys of a warp's step
     static constexpr int kTileKeys = kWarps * kStep;       // keys of a tile
-    static constexpr int kStages = 3;
+    static constexpr int kStages = D == 256 || (D == 128 && NB == 1) ? 2 : 3;
     static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
     static constexpr uint32_t kHalf = kStep * D * 2;       // the keys of a step (or its values)
     static constexpr uint32_t kStage = 2 * kHalf;
@@ -154,9 +159,10 @@ struct Run {
     int64_t seq_start;  // and where it begins
 };
 
-template <int Rows, int Tile>
+template <int Rows, int Tile, int kWarps>
 DG_DEVINL Run find_run(const SplitArgs& a) {
-    __shared__ int64_t sums[kWarps];
+    constexpr int kThreads = kWarps * 32;
+    __shared__ int64_t sums[4 * kWarps];
     __shared__ int64_t found_start;
     __shared__ int found_seq;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -174,20 +180,56 @@ DG_DEVINL Run find_run(const SplitArgs& a) {
         if (blockIdx.x == 0 && (!p.seq.ok || p.seq.ql > a.max_q_len)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
         return p.cost(a.Hkv);
     };
-    if (a.n_seq <= 32) {   // every warp by itself: nothing to wait for
-        const int64_t c = lane < a.n_seq ? cost_of(lane) : 0;
+    auto scan = [&](int64_t c) {
         int64_t incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
+        return incl;
+    };
+    if (a.n_seq <= 32) {   // every warp by itself: nothing to wait for
+        const int64_t c = lane < a.n_seq ? cost_of(lane) : 0, incl = scan(c);
         cut(__shfl_sync(0xffffffffu, incl, 31));
-        const uint32_t hit = __ballot_sync(0xffffffffu, c > 0 && incl - c <= r.start && r.start < incl);
+        const uint32_t hit = __ballot_sync(0xffffffffu, incl - c <= r.start && r.start < incl);
         if (hit) {
             r.seq = __ffs(hit) - 1;
             r.seq_start = __shfl_sync(0xffffffffu, incl - c, r.seq);
         }
+        return r;
+    }
+    constexpr int kFew = 4;
+    if (a.n_seq <= kFew * kThreads) {   // up to four sequences a thread, read at once
+        int64_t c[kFew], incl[kFew];
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) c[k] = k * kThreads + tid < a.n_seq ? cost_of(k * kThreads + tid) : 0;
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            incl[k] = scan(c[k]);
+            if (lane == 31) sums[k * kWarps + warp] = incl[k];
+        }
+        __syncthreads();
+        int64_t total = 0, before[kFew];
+#pragma unroll
+        for (int k = 0; k < kFew; ++k)
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) before[k] = total;
+                total += sums[k * kWarps + w];
+            }
+        cut(total);
+#pragma unroll
+        for (int k = 0; k < kFew; ++k) {
+            const int64_t to = before[k] + incl[k];
+            if (to - c[k] <= r.start && r.start < to) {
+                found_seq = k * kThreads + tid;
+                found_start = to - c[k];
+            }
+        }
+        __syncthreads();
+        r.seq = found_seq;
+        r.seq_start = found_start;
         return r;
     }
     int64_t mine = 0, first_cost = 0;
@@ -208,12 +250,7 @@ DG_DEVINL Run find_run(const SplitArgs& a) {
     for (int s0 = 0; s0 < a.n_seq; s0 += kThreads) {
         const int s = s0 + tid;
         const int64_t c = s0 == 0 ? first_cost : s < a.n_seq ? seq_plan<Rows, Tile>(a, s).cost(a.Hkv) : 0;
-        int64_t incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
+        int64_t incl = scan(c);
         __syncthreads();   // the last round's readers of sums are done
         if (lane == 31) sums[warp] = incl;
         __syncthreads();
@@ -262,8 +299,9 @@ struct Walk {
             seq_start += p.cost(a.Hkv);
             p = seq_plan<Rows, Tile>(a, ++s);
         }
-        const int item = (int)((at - seq_start) / p.tiles);
-        const int t0 = (int)(at - seq_start - (int64_t)item * p.tiles);
+        const int64_t off = at - seq_start;
+        const int item = off < (1LL << 31) ? (int)((uint32_t)off / (uint32_t)p.tiles) : (int)(off / p.tiles);
+        const int t0 = (int)(off - (int64_t)item * p.tiles);
         z.s = s;
         z.hk = item / p.row_tiles;
         z.row0 = (item - z.hk * p.row_tiles) * Rows;
@@ -287,10 +325,10 @@ struct Walk {
 };
 
 template <int D, int NB>
-__global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_split(const SplitArgs a) {
-    using C = SplitCfg<D>;
+__global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kCtasPerSm) k_paged_split(const SplitArgs a) {
+    using C = SplitCfg<D, NB>;
     constexpr int Rows = 8 * NB;
-    constexpr int S = C::kStages, Tile = C::kTileKeys;
+    constexpr int S = C::kStages, Tile = C::kTileKeys, kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int KB = C::kStep / 16;       // 16-key blocks of a step
     constexpr int KK = D / 16;              // 16-dimension blocks of a head
     constexpr int Chunks = D / 8;           // 16-byte chunks of a head
@@ -298,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
     static_assert(Rows * D * 4 <= (int)C::kStage, "a warp's output fits a stage of its ring");
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_m[kWarps][Rows], s_l[kWarps][Rows];
-    __shared__ Piece s_piece[2];   // the run's current piece and the next one (two places used in turn)
+    __shared__ Piece s_piece[4];   // the run's current piece and the two behind it (piece k in place k % 4)
     dg::pdl_wait();
     dg::pdl_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Run run = find_run<Rows, Tile>(a);
+    const Run run = find_run<Rows, Tile, kWarps>(a);
     if (run.start >= run.end) {
         if (tid == 0) a.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
@@ -371,30 +409,31 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
 
     Walk<Rows, Tile> walk{run.start, run.seq_start, run.end, run.seq, seq_plan<Rows, Tile>(a, run.seq)};
     int place = 0;                 // of the current piece in s_piece
-    bool more;                     // there is a next one
-    bool ahead = false;            // the loads are in it
-    {
-        Piece z;
-        walk.next(a, z);
-        open(z);
-        if (tid == 0) s_piece[0] = z;
-        more = walk.next(a, z);
-        if (more && tid == 0) s_piece[1] = z;
-    }
-    __syncthreads();
+    bool more = false, more2 = false;   // there is a next one, and one behind it
+    bool ahead = false;                 // the loads are in the next one
     // Fills the ring up to `limit` steps ahead of the products.
     auto fill = [&](uint32_t limit) {
         while (issued - consumed < limit) {
             if (in.step < in.steps) {
                 issue();
             } else if (more && !ahead) {
-                open(s_piece[place ^ 1]);
+                open(s_piece[(place + 1) & 3]);
                 ahead = true;
             } else {
                 break;
             }
         }
     };
+    {
+        Piece z;
+        walk.next(a, z);
+        open(z);
+        fill(S - 1);   // on their way before the next piece is worked out
+        if (tid == 0) s_piece[0] = z;
+        more = walk.next(a, z);
+        if (more && tid == 0) s_piece[1] = z;
+    }
+    __syncthreads();
     // Q^T as the second operand: lane holds column lane / 4, dimensions 2 (lane % 4) + {0, 1} (+ 8)
     uint32_t qf[NB][KK][2];
     auto load_q = [&](const Piece& z) {
@@ -411,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
             }
         }
     };
-    fill(S - 1);
     load_q(s_piece[0]);
+    fill(S - 1);
 
     const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_col = (lane >> 4) & 1;
     const int v_row = (lane & 7) + ((lane >> 4) & 1) * 8, v_col = (lane >> 3) & 1;
@@ -446,6 +485,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
 
+        {   // the piece behind the next one, while loads are on their way (others see it after the meeting)
+            Piece z;
+            more2 = more && walk.next(a, z);
+            if (more2 && tid == 0) s_piece[(place + 2) & 3] = z;
+        }
         for (int step = 0; step < steps; ++step) {
             if (issued - consumed == (uint32_t)(S - 1))
                 cp_async_wait<S - 2>();
@@ -573,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
                 }
             }
         }
-        if (more) load_q(s_piece[place ^ 1]);   // on its way while the warps meet
+        if (more) load_q(s_piece[(place + 1) & 3]);   // on its way while the warps meet
         __syncthreads();
         const Piece z = s_piece[place];
         const int64_t slot = (int64_t)blockIdx.x * 2 + (z.starts ? 1 : 0);
@@ -613,15 +657,12 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D>::kCtasPerSm) k_paged_spl
             desc1 = make_int4(z.row0, 0, 0, 0);
         }
         if (!more) break;
-        __syncthreads();   // the meeting buffers and the piece's place are free
+        __syncthreads();   // the meeting buffers are free
         // on to the next piece; the loads are in it already, or begin with it
-        if (!ahead) open(s_piece[place ^ 1]);
+        place = (place + 1) & 3;
+        if (!ahead) open(s_piece[place]);
         ahead = false;
-        Piece w;
-        more = walk.next(a, w);
-        if (more && tid == 0) s_piece[place] = w;
-        place ^= 1;
-        __syncthreads();   // the next piece's successor is in its place
+        more = more2;
         fill(S - 1);
     }
     if (tid == 0) {
@@ -717,11 +758,20 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Rows of an item: 8 when the call's queries and a group fit them, else 16.
 int item_rows(int32_t max_q_len, int32_t group) { return (int64_t)max_q_len * group <= 8 ? 8 : 16; }
 
-// Calls of more rows than this take dg_attention's query tiles.
-#ifndef DG_SPLIT_ROWS
-#define DG_SPLIT_ROWS 32
-#endif
-bool split_path(int32_t max_q_len, int32_t group) { return max_q_len == 1 || (int64_t)max_q_len * group <= DG_SPLIT_ROWS; }
+// Whether a call takes this file's path or dg_attention's query tiles over pages (dg_attn.cu).  An item here
+// (up to 16 rows of a key head) and a tile there (128 queries of a query head) pass over the keys in about the same
+// time, 75 to 82 us for 256 of them on 4k keys at heads of 128, and tiles below the number of CTAs take
+// as long as that number does.  So: whichever has fewer passes.  Measured (us here / there): 32 requests over
+// 4k keys, 16 query over 8 key heads, 8 queries 92 / 150, 16 queries 168 / 150, 32 queries 327 / 152; 8 requests
+// over 2.3k keys, 16 queries 29 / 43, 32 queries 49 / 43, 64 queries 72 / 45; one request, 128 queries 27 / 40.
+// Over 216 shapes (heads of 64, 128, 256, 1 to 16 query heads a key head, 1 to 256 queries) the rule loses
+// 0.7 % to the better path on average, 22 % at most.
+bool split_path(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D) {
+    const int64_t tile_ctas = D == 256 ? 152 : 304;
+    const int64_t here = (int64_t)n_seq * Hkv * (((int64_t)max_q_len * (Hq / Hkv) + 15) / 16);
+    const int64_t there = (int64_t)n_seq * Hq * (((int64_t)max_q_len + 127) / 128);
+    return max_q_len == 1 || here <= std::max(there, tile_ctas);
+}
 
 size_t split_bytes(int rows, int32_t D) {
     return (size_t)kMaxCtas * 32 + (size_t)kMaxCtas * 2 * rows * ((size_t)D + 2) * 4;
@@ -729,7 +779,7 @@ size_t split_bytes(int rows, int32_t D) {
 
 template <int D, int NB>
 dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
-    using C = SplitCfg<D>;
+    using C = SplitCfg<D, NB>;
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
     // the attribute once a device: 0.4 us of a call that takes the host 4
@@ -743,7 +793,7 @@ dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
         if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     const unsigned grid = (unsigned)std::min(sms * C::kCtasPerSm, kMaxCtas);
-    cudaError_t e = dghost::launch_pdl(k_paged_split<D, NB>, dim3(grid), dim3(kThreads), C::kSmem, stream, a);
+    cudaError_t e = dghost::launch_pdl(k_paged_split<D, NB>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, a);
     dghost::count_launch();
     if (e != cudaSuccess) return DG_ERR_CUDA;
     e = dghost::launch_pdl(k_paged_join<D, NB>, dim3(grid, D / 64), dim3(kJoinThreads), 0, stream, a);
@@ -756,7 +806,7 @@ dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
 extern "C" size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv,
                                                      int32_t D) {
     if (n_seq < 1 || max_q_len < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
-    if (!split_path(max_q_len, Hq / Hkv)) return dghost::attention_pages_bytes(n_seq, max_q_len);
+    if (!split_path(n_seq, max_q_len, Hq, Hkv, D)) return dghost::attention_pages_bytes(n_seq, max_q_len);
     return split_bytes(item_rows(max_q_len, Hq / Hkv), D);
 }
 
@@ -776,7 +826,7 @@ extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* ca
     const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
     if (ok != DG_OK) return ok;
     const int rows = item_rows(max_q_len, Hq / Hkv);
-    const bool split = split_path(max_q_len, Hq / Hkv);
+    const bool split = split_path(n_seq, max_q_len, Hq, Hkv, D);
     if (!workspace || workspace_bytes < dg_paged_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D))
         return DG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
