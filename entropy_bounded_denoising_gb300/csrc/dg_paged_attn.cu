@@ -44,7 +44,7 @@ struct SplitArgs {
     float scale_log2;
     dg::PagedKV kv;
     float* part_o;    // [grid][2][rows][D]
-    float* part_ml;   // [grid][2][rows][2]
+    float4* part_ml;  // [grid][2][rows]: maximum, sum, sum of the rounded weights, -
     int4* desc;       // [grid][2]: CTAs that follow (0: nothing to join), rows, first row of q, key head; first row
     unsigned* status;
 };
@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
     constexpr int PerLoad = 32 / Chunks;    // key rows a warp's load instruction covers
     static_assert(Rows * D * 4 <= (int)C::kStage, "a warp's output fits a stage of its ring");
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_m[kWarps][Rows], s_l[kWarps][Rows];
+    __shared__ float s_m[kWarps][Rows];
+    __shared__ float2 s_l[kWarps][Rows];
     __shared__ Piece s_piece[4];   // the run's current piece and the two behind it (piece k in place k % 4)
     dg::pdl_wait();
     dg::pdl_release();
@@ -481,9 +482,11 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[mt][nb][e] = 0.f;
-        float m[NB][2], l[NB][2];
+        // running maximum; sum of the weights (for lse) and of the weights as the product with V has them,
+        // rounded to bf16, which the output is divided by: a row that one key decides is then exact
+        float m[NB][2], l[NB][2], lr[NB][2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
+        for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = lr[nb][0] = lr[nb][1] = 0.f;
 
         {   // the piece behind the next one, while loads are on their way (others see it after the meeting)
             Piece z;
@@ -559,6 +562,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                         mx = fmaxf(mx, m[nb][e]);
                         const float f = mx == -INFINITY ? 1.f : ex2(m[nb][e] - mx);
                         l[nb][e] *= f;
+                        lr[nb][e] *= f;
 #pragma unroll
                         for (int mt = 0; mt < KK; ++mt) {
                             acc[mt][nb][e] *= f;
@@ -577,8 +581,11 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                     const float p2 = ex2(x[kb][nb][2] - r0), p3 = ex2(x[kb][nb][3] - r1);
                     l[nb][0] += p0 + p2;
                     l[nb][1] += p1 + p3;
-                    pf[kb][nb][0] = transpose8x8(pack_bf16x2(p0, p1));
-                    pf[kb][nb][1] = transpose8x8(pack_bf16x2(p2, p3));
+                    const uint32_t w0 = pack_bf16x2(p0, p1), w1 = pack_bf16x2(p2, p3);
+                    lr[nb][0] += __uint_as_float(w0 << 16) + __uint_as_float(w1 << 16);
+                    lr[nb][1] += __uint_as_float(w0 & 0xffff0000u) + __uint_as_float(w1 & 0xffff0000u);
+                    pf[kb][nb][0] = transpose8x8(w0);
+                    pf[kb][nb][1] = transpose8x8(w1);
                 }
             }
 #pragma unroll
@@ -602,12 +609,15 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = l[nb][e];
+                float sum = l[nb][e], sum_r = lr[nb][e];
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                for (int o = 4; o < 32; o <<= 1) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    sum_r += __shfl_xor_sync(0xffffffffu, sum_r, o);
+                }
                 if (lane < 4) {
                     s_m[warp][nb * 8 + lane * 2 + e] = m[nb][e];
-                    s_l[warp][nb * 8 + lane * 2 + e] = sum;
+                    s_l[warp][nb * 8 + lane * 2 + e] = make_float2(sum, sum_r);
                 }
                 const int r = nb * 8 + (lane & 3) * 2 + e, turn = (lane & 3) << 3;
 #pragma unroll
@@ -626,12 +636,13 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
-            float L = 0.f;
+            float L = 0.f, Lr = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float f = s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - M);
-                L += s_l[w][r] * f;
+                L += s_l[w][r].x * f;
+                Lr += s_l[w][r].y * f;
                 const float4 v = *reinterpret_cast<const float4*>(smem + (size_t)w * C::kRing + met +
                                                                   ((size_t)r * D + (d ^ (((r >> 1) & 3) << 3))) * 4);
                 o.x += v.x * f;
@@ -642,13 +653,13 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
             if (z.starts && z.ends) {
                 const int rr = z.row0 + r, qi = rr / a.group;
                 const int64_t out = (int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (rr - qi * a.group);
-                const float inv = L > 0.f ? 1.f / L : 0.f;
+                const float inv = Lr > 0.f ? 1.f / Lr : 0.f;
                 *reinterpret_cast<uint2*>(a.o + out * D + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
                 if (d == 0 && a.lse) a.lse[out] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
             } else {
                 *reinterpret_cast<float4*>(a.part_o + (slot * Rows + r) * D + d) = o;
-                if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * Rows + r) * 2) = make_float2(M, L);
+                if (d == 0) a.part_ml[slot * Rows + r] = make_float4(M, L, Lr, 0.f);
             }
         }
         if (z.starts && !z.ends) {
@@ -685,7 +696,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const SplitArgs a) 
     constexpr int kGroups = kJoinThreads / kPlaces;  // 4 or 2
     constexpr int kEarly = 4;                        // pieces a thread asks for before it knows their weights
     __shared__ float w[kMaxCtas][Rows];              // the pieces' maxima, then their weights
-    __shared__ float s_l[Rows], s_m[Rows];
+    __shared__ float s_l[Rows], s_lr[Rows], s_m[Rows];
     __shared__ float4 part[kGroups > 1 ? kGroups - 1 : 1][kPlaces];
     dg::pdl_wait();
     dg::pdl_release();
@@ -706,22 +717,28 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const SplitArgs a) 
     for (int q = warp; q < n_rows; q += kJoinThreads / 32) {
         float M = -INFINITY;
         for (int i = lane; i < n; i += 32) {
-            const float v = a.part_ml[(slot(i) * Rows + q) * 2];
+            const float v = a.part_ml[slot(i) * Rows + q].x;
             w[i][q] = v;
             M = fmaxf(M, v);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float L = 0.f;
+        float L = 0.f, Lr = 0.f;
         for (int i = lane; i < n; i += 32) {
             const float m = w[i][q], f = m == -INFINITY ? 0.f : ex2(m - M);
+            const float4 ml = a.part_ml[slot(i) * Rows + q];
             w[i][q] = f;
-            L += a.part_ml[(slot(i) * Rows + q) * 2 + 1] * f;
+            L += ml.y * f;
+            Lr += ml.z * f;
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        for (int o = 16; o; o >>= 1) {
+            L += __shfl_xor_sync(0xffffffffu, L, o);
+            Lr += __shfl_xor_sync(0xffffffffu, Lr, o);
+        }
         if (lane == 0) {
             s_l[q] = L;
+            s_lr[q] = Lr;
             s_m[q] = M;
         }
     }
@@ -745,7 +762,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const SplitArgs a) 
     if (group > 0 || !mine) return;
 #pragma unroll
     for (int g = 1; g < kGroups; ++g) add(part[g - 1][place], 1.f);
-    const float L = s_l[r], inv = L > 0.f ? 1.f / L : 0.f;
+    const float L = s_l[r], inv = s_lr[r] > 0.f ? 1.f / s_lr[r] : 0.f;
     const int rr = row0 + r, qi = rr / a.group;
     const int64_t out = (int64_t)(q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
     *reinterpret_cast<uint2*>(a.o + out * D + d) =
@@ -774,7 +791,7 @@ bool split_path(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32
 }
 
 size_t split_bytes(int rows, int32_t D) {
-    return (size_t)kMaxCtas * 32 + (size_t)kMaxCtas * 2 * rows * ((size_t)D + 2) * 4;
+    return (size_t)kMaxCtas * 32 + (size_t)kMaxCtas * 2 * rows * ((size_t)D + 4) * 4;
 }
 
 template <int D, int NB>
@@ -848,7 +865,7 @@ extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* ca
     a.scale_log2 = scale * kLog2e;
     a.desc = static_cast<int4*>(workspace);
     a.part_o = reinterpret_cast<float*>(a.desc + 2 * kMaxCtas);
-    a.part_ml = a.part_o + (size_t)kMaxCtas * 2 * rows * D;
+    a.part_ml = reinterpret_cast<float4*>(a.part_o + (size_t)kMaxCtas * 2 * rows * D);
     a.status = dghost::status_word();
     cudaStream_t st = (cudaStream_t)stream;
     if (D == 64) return rows == 8 ? launch_split<64, 1>(a, st) : launch_split<64, 2>(a, st);
