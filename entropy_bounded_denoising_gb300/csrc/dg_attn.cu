@@ -278,12 +278,18 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
     __shared__ int count[kCostBuckets];
     __shared__ int warp_sum[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if constexpr (Paged) {
+        dg::pdl_wait();
+        dg::pdl_release();   // the attention kernel sets itself up beside this one
+    }
     for (int b = tid; b < kCostBuckets; b += blockDim.x) count[b] = 0;
     if (tid == 0) *reinterpret_cast<unsigned long long*>(plan + 2) = 0ull;  // the attention kernel's work counter
     __syncthreads();
     const int64_t pairs = (int64_t)n_seq * max_q_tiles;
+    const bool narrow = pairs < (1LL << 31);
     auto item_key = [&](int64_t f, int& key) -> bool {  // false: no item (past the queries or bad)
-        const int s = (int)(f / max_q_tiles), t = (int)(f % max_q_tiles);
+        const int s = narrow ? (int)((uint32_t)f / (uint32_t)max_q_tiles) : (int)(f / max_q_tiles);
+        const int t = (int)(f - (int64_t)s * max_q_tiles);
         if constexpr (Paged) {
             const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
             if (t == 0 && (!p.ok || p.ql > (int64_t)max_q_tiles * kTile)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
@@ -369,27 +375,11 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(attn_smem_raw) + 1023) & ~uintptr_t(1023));
     AttnShared& sh = *reinterpret_cast<AttnShared*>(smem + kOffBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t n_work = (int64_t)plan[0] * a.Hq;
-    if constexpr (Paged) {
-        for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
-            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
-            if (!p.ok || p.kl != 0) continue;
-            const int64_t first = (int64_t)p.q0 * a.Hq, rows = (int64_t)p.ql * a.Hq;
-            for (int64_t i = threadIdx.x; i < rows * (kHead / 8); i += kThreads)
-                reinterpret_cast<uint4*>(a.o + first * kHead)[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (a.lse)
-                for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[first + i] = -INFINITY;
-        }
+    // With pages the CTA sets up its barriers and tensor memory before it waits for the plan kernel (which
+    // lets it start); without, the CTAs beyond the work leave first.
+    if constexpr (!Paged) {
+        if ((int64_t)blockIdx.x >= (int64_t)plan[0] * a.Hq) return;  // the whole CTA: no work
     }
-    if ((int64_t)blockIdx.x >= n_work) return;  // the whole CTA: no work
-    const int2* items = reinterpret_cast<const int2*>(plan + kPlanHeader);
-    const int group = a.Hq / a.Hkv;
-    const bool round_robin = plan[1] != 0;
-    auto rr_item = [&](uint32_t k) -> int64_t {
-        const int64_t w = (int64_t)blockIdx.x + (int64_t)k * gridDim.x;
-        return w < n_work ? w : -1;
-    };
-
     if (threadIdx.x == 0) {
         dg::mbar_init(&sh.qfull, 1);
         dg::mbar_init(&sh.qempty, 1);
@@ -421,6 +411,32 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     __syncthreads();
     dg::tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
+    const int32_t* list = plan;
+    if constexpr (Paged) {
+        dg::pdl_wait();
+        dg::pdl_release();
+        asm volatile("" : "+l"(list)::"memory");  // no read of the list moves up past the wait
+    }
+    const int64_t n_work = (int64_t)list[0] * a.Hq;
+    if constexpr (Paged) {
+        for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
+            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+            if (!p.ok || p.kl != 0) continue;
+            const int64_t first = (int64_t)p.q0 * a.Hq, rows = (int64_t)p.ql * a.Hq;
+            for (int64_t i = threadIdx.x; i < rows * (kHead / 8); i += kThreads)
+                reinterpret_cast<uint4*>(a.o + first * kHead)[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse)
+                for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[first + i] = -INFINITY;
+        }
+    }
+    const int2* items = reinterpret_cast<const int2*>(list + kPlanHeader);
+    const int group = a.Hq / a.Hkv;
+    const bool round_robin = list[1] != 0;
+    auto rr_item = [&](uint32_t k) -> int64_t {
+        const int64_t w = (int64_t)blockIdx.x + (int64_t)k * gridDim.x;
+        return w < n_work ? w : -1;
+    };
+
     const uint32_t sQ = dg::smem_u32(smem + kOffQ);
 
     if (warp == 0) {
@@ -428,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         // the V ring, lane 2 the Q tile of each item (once the last item's last S has read it)
         if (lane == 2) {
             dg::prefetch_tmap(&tmQ);
-            unsigned long long* counter = reinterpret_cast<unsigned long long*>(const_cast<int32_t*>(plan) + 2);
+            unsigned long long* counter = reinterpret_cast<unsigned long long*>(const_cast<int32_t*>(list) + 2);
             uint32_t kq = 0;
             bool ok = true;
             for (;; ++kq) {
@@ -899,17 +915,17 @@ dg_status attention_pages(const uint16_t* q, const dg::PagedKV& kv, uint16_t* o,
     a.n_seq = n_seq;
     a.negate = scale < 0.f;
     int32_t* plan = static_cast<int32_t*>(workspace);
-    k_attn_plan<true><<<1, 1024, 0, st>>>(a, n_seq, (int32_t)max_q_tiles, plan);
+    cudaError_t e = launch_pdl(k_attn_plan<true>, dim3(1), dim3(1024), 0, st, a, n_seq, (int32_t)max_q_tiles, plan);
     count_launch();
-    if (cudaGetLastError() != cudaSuccess) return DG_ERR_CUDA;
+    if (e != cudaSuccess) return DG_ERR_CUDA;
     const int64_t work_bound = (int64_t)n_seq * max_q_tiles * Hq;
     auto launch = [&](auto kern, size_t smem, int per_sm) -> dg_status {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return DG_ERR_CUDA;
         const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((int64_t)per_sm * P, work_bound));
-        kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, a, plan);
+        e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, tq, tk, tv, a, plan);
         count_launch();
-        return cuda_status(cudaGetLastError());
+        return cuda_status(e);
     };
     if (D == 64) return launch(k_attention<64, true>, AttnCfg<64>::kSmem, AttnCfg<64>::kCtasPerSm);
     if (D == 128) return launch(k_attention<128, true>, AttnCfg<128>::kSmem, AttnCfg<128>::kCtasPerSm);
