@@ -374,7 +374,9 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(attn_smem_raw) + 1023) & ~uintptr_t(1023));
     AttnShared& sh = *reinterpret_cast<AttnShared*>(smem + kOffBar);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (with pages a broadcast tells the compiler that the branches on the warp are uniform)
+    const int warp = Paged ? __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0) : (int)(threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
     // With pages the CTA sets up its barriers and tensor memory before it waits for the plan kernel (which
     // lets it start); without, the CTAs beyond the work leave first.
     if constexpr (!Paged) {
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if (Paged ? dg::elect_leader() : lane == 0) {
             // S = Q K^T: K tile K-major; bit 13 negates Q
             const uint32_t idS = dg::instr_desc(kTile, kKeys, false) | (Paged && a.negate ? 1u << 13 : 0u);
             constexpr uint32_t idO = dg::instr_desc(kTile, kHead, true);   // O += P V: V rows are N-major
