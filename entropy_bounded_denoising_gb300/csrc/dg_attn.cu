@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     dg::tc_fence_before();
     __syncthreads();
     dg::tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = Paged ? __shfl_sync(0xffffffffu, sh.tmem_base, 0) : sh.tmem_base;
     const int32_t* list = plan;
     if constexpr (Paged) {
         dg::pdl_wait();
