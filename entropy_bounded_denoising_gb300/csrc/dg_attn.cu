@@ -122,14 +122,13 @@ struct TileRange {
     bool causal;
 };
 
-template <bool Paged>
-DG_DEVINL TileRange tile_range(const AttnArgs& a, int s, int t) {
+DG_DEVINL TileRange range_of(const AttnArgs& a, int t, int q0, int ql, int k0, int kl, bool causal) {
     TileRange r;
-    r.q0 = a.cu_q[s];
-    r.ql = a.cu_q[s + 1] - r.q0;
-    r.k0 = Paged ? 0 : a.cu_kv[s];
-    r.kl = Paged ? a.kv.kv_len[s] : a.cu_kv[s + 1] - r.k0;
-    r.causal = a.causal[s] != 0;
+    r.q0 = q0;
+    r.ql = ql;
+    r.k0 = k0;
+    r.kl = kl;
+    r.causal = causal;
     const int off = r.kl - r.ql;
     r.pmin = off + t * kTile;
     r.pmax = off + min(r.ql, t * kTile + kTile) - 1;
@@ -139,6 +138,12 @@ DG_DEVINL TileRange tile_range(const AttnArgs& a, int s, int t) {
     r.jt_lo = r.jlo / kKeys;
     r.nt = r.jhi >= r.jlo ? r.jhi / kKeys - r.jt_lo + 1 : 0;
     return r;
+}
+
+template <bool Paged>
+DG_DEVINL TileRange tile_range(const AttnArgs& a, int s, int t) {
+    const int q0 = a.cu_q[s], ql = a.cu_q[s + 1] - q0, k0 = Paged ? 0 : a.cu_kv[s];
+    return range_of(a, t, q0, ql, k0, Paged ? a.kv.kv_len[s] : a.cu_kv[s + 1] - k0, a.causal[s] != 0);
 }
 
 DG_DEVINL bool tile_full(const TileRange& r, int window, int jt) {
@@ -263,6 +268,24 @@ DG_DEVINL void do_abort(AttnShared& sh, unsigned* status) {
     dg::raise_status(status, DG_DEV_TIMEOUT);
 }
 
+// A work item as the roles use it.  With pages the list holds all of it, 32 bytes an item, so that a CTA's
+// first copies wait for one read and not for two.
+struct Item {
+    int s, t;      // sequence, query tile
+    TileRange r;
+};
+
+template <bool Paged>
+DG_DEVINL Item read_item(const AttnArgs& a, const int32_t* list, int64_t i) {
+    if constexpr (Paged) {
+        const int4 x = reinterpret_cast<const int4*>(list)[2 * i], y = reinterpret_cast<const int4*>(list)[2 * i + 1];
+        return Item{x.x, x.y, range_of(a, x.y, x.z, x.w, 0, y.x, y.y != 0)};
+    } else {
+        const int2 x = reinterpret_cast<const int2*>(list)[i];
+        return Item{x.x, x.y, tile_range<false>(a, x.x, x.y)};
+    }
+}
+
 // ------------------------------------------------------------------ the plan
 // Work items are (sequence, 128-query tile) pairs with at least one query.  One CTA lists them
 // by decreasing cost (key tiles visited; a counting sort over kCostBuckets), so that the
@@ -343,10 +366,18 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
     __syncthreads();
     if (tid < kCostBuckets) count[tid] = warp_sum[warp] + incl - c;
     __syncthreads();
-    int2* items = reinterpret_cast<int2*>(plan + kPlanHeader);
     for (int64_t f = tid; f < pairs; f += blockDim.x) {
         int key = my_key;
-        if (f == tid ? key >= 0 : item_key(f, key)) items[atomicAdd(&count[key], 1)] = make_int2((int)(f / max_q_tiles), (int)(f % max_q_tiles));
+        if (!(f == tid ? key >= 0 : item_key(f, key))) continue;
+        const int at = atomicAdd(&count[key], 1);
+        const int s = (int)(f / max_q_tiles), q_tile = (int)(f % max_q_tiles);
+        if constexpr (Paged) {
+            int4* item = reinterpret_cast<int4*>(plan + kPlanHeader) + 2 * (int64_t)at;
+            item[0] = make_int4(s, q_tile, a.cu_q[s], a.cu_q[s + 1] - a.cu_q[s]);
+            item[1] = make_int4(a.kv.kv_len[s], a.causal[s] != 0, 0, 0);
+        } else {
+            reinterpret_cast<int2*>(plan + kPlanHeader)[at] = make_int2(s, q_tile);
+        }
     }
 }
 
@@ -360,7 +391,7 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
 // With Paged the key and value tiles come page by page (one TMA box of min(page, 64) slots each,
 // zeros where no query sees the page), the rows of the value tiles that no query of the item sees
 // are zeroed before the product (what their slots hold is nobody's; their weights are 0, but 0 * NaN is not),
-// and the sequences without keys get their rows of zeros from the CTAs on their way in.
+// and the sequences without keys get their rows of zeros from the CTAs on their way out.
 template <int D, bool Paged>
 __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     k_attention(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -420,18 +451,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         asm volatile("" : "+l"(list)::"memory");  // no read of the list moves up past the wait
     }
     const int64_t n_work = (int64_t)list[0] * a.Hq;
-    if constexpr (Paged) {
-        for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
-            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
-            if (!p.ok || p.kl != 0) continue;
-            const int64_t first = (int64_t)p.q0 * a.Hq, rows = (int64_t)p.ql * a.Hq;
-            for (int64_t i = threadIdx.x; i < rows * (kHead / 8); i += kThreads)
-                reinterpret_cast<uint4*>(a.o + first * kHead)[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (a.lse)
-                for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[first + i] = -INFINITY;
-        }
-    }
-    const int2* items = reinterpret_cast<const int2*>(list + kPlanHeader);
+    const int32_t* items = list + kPlanHeader;
     const int group = a.Hq / a.Hkv;
     const bool round_robin = list[1] != 0;
     auto rr_item = [&](uint32_t k) -> int64_t {
@@ -466,9 +486,9 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
                     dg::mbar_arrive(&sh.wfull[slot]);  // releases the index to the readers
                 }
                 if (w < 0 || aborted(sh)) break;
-                const int2 it = items[w / a.Hq];
+                const Item it = read_item<Paged>(a, items, w / a.Hq);
                 const int h = (int)(w % a.Hq);
-                const int qrow = a.cu_q[it.x] + it.y * kTile;
+                const int qrow = it.r.q0 + it.t * kTile;
                 dg::mbar_arrive_expect_tx(&sh.qfull, kQBytes);
 #pragma unroll
                 for (int c = 0; c < kHead / kSub; ++c)
@@ -489,16 +509,16 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
             for (uint32_t k = 0; ok && !aborted(sh); ++k) {
                 const int64_t w = round_robin ? rr_item(k) : take_item(sh, k, ok);
                 if (w < 0) break;
-                const int2 it = items[w / a.Hq];
+                const Item it = read_item<Paged>(a, items, w / a.Hq);
                 const int hk = (int)(w % a.Hq) / group;
-                const TileRange r = tile_range<Paged>(a, it.x, it.y);
+                const TileRange& r = it.r;
                 for (int i = 0; i < r.nt; ++i, ++g) {
                     const int st = (int)(g & 1u);
                     // the pages of the tile's boxes, read before the wait; n_pages reads zeros
                     const int box_shift = Paged ? min(a.kv.page_shift, 6) : 6, boxes = kKeys >> box_shift;
                     const int j0 = (r.jt_lo + i) * kKeys;
                     if constexpr (Paged) {
-                        const int32_t* table = a.kv.page_table + (int64_t)it.x * a.kv.max_pages;
+                        const int32_t* table = a.kv.page_table + (int64_t)it.s * a.kv.max_pages;
                         int32_t entry[8];
                         bool bad = false;
 #pragma unroll
@@ -558,8 +578,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
             for (; ok && !aborted(sh); ++kq) {
                 const int64_t w = round_robin ? rr_item(kq) : take_item(sh, kq, ok);
                 if (w < 0) break;
-                const int2 it = items[w / a.Hq];
-                const TileRange r = tile_range<Paged>(a, it.x, it.y);
+                const TileRange r = read_item<Paged>(a, items, w / a.Hq).r;
                 if (!attn_wait(&sh.qfull, kq & 1u)) {
                     ok = false;
                     break;
@@ -625,10 +644,10 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         for (; ok; ++kq) {
             const int64_t w = round_robin ? rr_item(kq) : take_item_warp(sh, kq, ok);
             if (w < 0) break;
-            const int2 it = items[w / a.Hq];
+            const Item it = read_item<Paged>(a, items, w / a.Hq);
             const int h = (int)(w % a.Hq);
-            const TileRange r = tile_range<Paged>(a, it.x, it.y);
-            const int t = it.y;
+            const TileRange& r = it.r;
+            const int t = it.t;
             const int pos = r.kl - r.ql + t * kTile + row;
             const bool row_valid = t * kTile + row < r.ql;
             float m_ref = -INFINITY, l = 0.f;
@@ -784,6 +803,18 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         if (!ok) do_abort(sh, a.status);
     }
 
+    if constexpr (Paged) {  // the sequences without keys, after the work: their rows of zeros
+        for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
+            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+            if (!p.ok || p.kl != 0) continue;
+            const int64_t first = (int64_t)p.q0 * a.Hq, rows = (int64_t)p.ql * a.Hq;
+            for (int64_t i = threadIdx.x; i < rows * (kHead / 8); i += kThreads)
+                reinterpret_cast<uint4*>(a.o + first * kHead)[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse)
+                for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[first + i] = -INFINITY;
+        }
+    }
+
     dg::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -807,9 +838,9 @@ bool tmap_heads(CUtensorMap* tm, const void* base, int64_t rows, int32_t heads, 
     return dghost::encode_tmap(tm, 0, 2, const_cast<void*>(base), dims, strides, box, 128);
 }
 
-// Plan: a header and one (sequence, query tile) entry per possible item.
-size_t plan_bytes(int64_t n_seq, int64_t max_q_tiles) {
-    return ((size_t)kPlanHeader * 4 + (size_t)n_seq * (size_t)max_q_tiles * 8 + 255) / 256 * 256;
+// Plan: a header and one entry per possible item, (sequence, query tile) or, with pages, 32 bytes.
+size_t plan_bytes(int64_t n_seq, int64_t max_q_tiles, size_t entry = 8) {
+    return ((size_t)kPlanHeader * 4 + (size_t)n_seq * (size_t)max_q_tiles * entry + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -880,7 +911,7 @@ extern "C" dg_status dg_attention(const uint16_t* q, const uint16_t* k, const ui
 namespace dghost {
 
 size_t attention_pages_bytes(int32_t n_seq, int32_t max_q_len) {
-    return plan_bytes(n_seq, ((int64_t)max_q_len + kTile - 1) / kTile);
+    return plan_bytes(n_seq, ((int64_t)max_q_len + kTile - 1) / kTile, 32);
 }
 
 // dg_paged_attention for calls with many query rows (arguments checked by it).
