@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
             const int nh = n_hist[tid * PerVec + e];
             int nb = b1 > b0 ? n_bias[tid * PerVec + e] : 0;
             float b = 0.f;
-            for (int i = nb > 0 ? first_bias[tid * PerVec + e] : 0; nb > 0; ++i)   // in list order
+            for (int i = nb > 0 ? first_bias[tid * PerVec + e] : 0; nb > 0 && i < b1; ++i)   // in list order
                 if (a.bias_tokens[i] == v0 + e) {
                     b += a.bias_values[i];
                     --nb;

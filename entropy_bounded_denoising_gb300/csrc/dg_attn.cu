@@ -64,7 +64,7 @@ struct AttnArgs {
     // keys in pages (dg_paged_attention): the cache in place of cu_kv; the products' sign flips when the
     // scale is negative (scale_log2 is then its magnitude, so that the largest score stays the largest)
     dg::PagedKV kv;
-    int32_t n_seq;
+    int32_t n_seq, max_q_len;
     int32_t negate;
 };
 
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
         const int t = (int)(f - (int64_t)s * max_q_tiles);
         if constexpr (Paged) {
             const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
-            if (t == 0 && (!p.ok || p.ql > (int64_t)max_q_tiles * kTile)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+            if (t == 0 && (!p.ok || p.ql > a.max_q_len)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
             if (!p.ok || p.kl == 0 || (int64_t)t * kTile >= p.ql) return false;
         }
         const TileRange r = tile_range<Paged>(a, s, t);
@@ -946,6 +946,7 @@ dg_status attention_pages(const uint16_t* q, const dg::PagedKV& kv, uint16_t* o,
     a.status = status_word();
     a.kv = kv;
     a.n_seq = n_seq;
+    a.max_q_len = max_q_len;
     a.negate = scale < 0.f;
     int32_t* plan = static_cast<int32_t*>(workspace);
     cudaError_t e = launch_pdl(k_attn_plan<true>, dim3(1), dim3(1024), 0, st, a, n_seq, (int32_t)max_q_tiles, plan);

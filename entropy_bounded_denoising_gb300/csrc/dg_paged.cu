@@ -103,8 +103,9 @@ DG_DEVINL int row_position(const AppendArgs& a, int t, int s) {
     if (s >= a.n_seq) return -1;
     const dg::PagedSeq q = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
     if (q.q0 > t) return -1;
-    if (!q.ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-    return q.ok && q.kl > 0 ? q.kl - q.ql + (t - q.q0) : -1;
+    const bool ok = q.ok && t - q.q0 < q.ql;   // (the search says little when the offsets are not in order)
+    if (!ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+    return ok && q.kl > 0 ? q.kl - q.ql + (t - q.q0) : -1;
 }
 
 // A block's rows are looked up and its sines computed while its data is on the way: every thread

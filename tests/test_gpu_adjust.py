@@ -230,3 +230,50 @@ def test_edits_in_front_of_the_step():
     p = torch.softmax(y.double(), -1)
     H = -(p * torch.where(p > 0, p, torch.ones_like(p)).log()).sum(-1)
     assert torch.allclose(s.entropy.double(), H, rtol=1e-5, atol=1e-9)
+
+
+def test_the_run_in_one_graph():
+    """A served pass captured once (append, attention, logits, edits) and replayed with other lengths and
+    inputs gives what the calls give one by one."""
+    n, L, V, Hq, Hkv, D = 3, 16, 2048, 4, 2, 64
+    b = ref.Batch([(L, 90 + L, 0), (L, 40 + L, 1), (L, 300 + L, 0)], Hq, Hkv, D, 16, seed=3).fill_keys()
+    w = 10000.0 ** (-torch.arange(D // 2, dtype=torch.float64, device=DEV) / (D // 2))
+    qkv = torch.randn((n * L, (Hq + 2 * Hkv) * D), generator=torch.Generator().manual_seed(5)).to(ref.BF16).to(DEV)
+    q, k, v = (qkv[:, a * D:e * D].unflatten(1, (e - a, D)) for a, e in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+    W = synth.lm_head_weights_int(V, Hq * D, seed=4, device=DEV)
+    params = _params(n)
+    hist, cu = _ints([[1, 2, 3, 1], [0], [7] * 9])
+    pen = torch.tensor([[1.2, 0.5, 0.25]] * n, device=DEV)
+    qr, o = torch.empty((n * L, Hq, D), dtype=ref.BF16, device=DEV), torch.empty((n * L, Hq, D), dtype=ref.BF16, device=DEV)
+    x = torch.empty((n, L, V), dtype=ref.BF16, device=DEV)
+
+    def run():
+        dg.dg_kv_append(k, v, b.k_cache, b.v_cache, b.table, b.cu, b.kv_len, inv_freq=w, q=q, q_out=qr)
+        dg.dg_paged_attention(qr, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, L)
+        dg.dg_lm_head_logits(o.view(n, L, Hq * D), W, params, x)
+        dg.dg_adjust_logits(x, params, history=hist, cu_history=cu, penalties=pen)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for lens in ([90 + L, 40 + L, 300 + L], [L, 3 + L, 0], [1 + L, 0, 200 + L]):
+        b.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        qkv.mul_(-1)
+        for t in (qr, o, x):
+            t.zero_()
+        kc, vc = b.k_cache.clone(), b.v_cache.clone()
+        run()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (qr, o, x, b.k_cache, b.v_cache)]
+        b.k_cache.copy_(kc)
+        b.v_cache.copy_(vc)
+        for t in (qr, o, x):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for got, t in zip((qr, o, x, b.k_cache, b.v_cache), want):
+            assert torch.equal(got.view(torch.int16), t.view(torch.int16))
+        assert torch.isfinite(x).all()
+    assert dg.dg_get_device_status() == 0

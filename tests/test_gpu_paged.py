@@ -270,6 +270,99 @@ def test_attention_refused_sequences_and_rows():
     dg.dg_clear_device_status()
 
 
+def _tiles(D, seqs=None, **kw):
+    """A batch of many rows a key head, which takes the query tiles."""
+    seqs = [(130, 200, 1), (140, 500, 0), (1, 1, 1), (133, 133, 1), (0, 40, 0), (257, 300, 0), (131, 0, 1)] if seqs is None else seqs
+    return ref.Batch(seqs, 8, 8, D, 16, seed=D + len(seqs), before=1, after=2, **kw).fill_keys()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_tiles_scales_and_refusals(D):
+    """The query tiles with every sign of the scale, with refused sequences, a page outside the pool, more
+    queries than the call says, and nothing but sequences without keys."""
+    bad = dg.DG_DEV_BAD_PARAM
+    b = _tiles(D)
+    for scale in (None, 0.0, -0.1, 1.0):
+        _attend(b, scale=scale)
+    b = _tiles(D)
+    b.kv_len[1] = 139
+    _attend(b, status=bad, skip=(1,))
+    b = _tiles(D, extra_columns=0)
+    b.kv_len[1] = 32 * 16 + 1
+    _attend(b, status=bad, skip=(1,))
+    b = _tiles(D)
+    b.kv_len[3] = -5
+    b.cu[7] = b.total + 1
+    b.cu[6] = 3
+    _attend(b, status=bad, skip=(3, 5, 6))
+    for page in (-1, b.n_pages, 2 ** 31 - 1):
+        b = _tiles(D)
+        b.table[1, 7] = page
+        o = torch.full(b.q.shape, 7.0, dtype=ref.BF16, device=DEV)
+        dg.dg_clear_device_status()
+        dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, 257)
+        torch.cuda.synchronize()
+        assert dg.dg_get_device_status() == bad
+        ref.check_attention(b, o, None, skip=(1,))
+    b = _tiles(D)
+    dg.dg_clear_device_status()
+    o = torch.zeros_like(b.q)
+    dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, 256)
+    torch.cuda.synchronize()
+    assert dg.dg_get_device_status() == bad
+    ref.check_attention(b, o, None, skip=(5,))
+    b = _tiles(D, [(200, 0, 1)] * 6)
+    _attend(b)
+
+
+def test_attention_tiles_hide_what_no_query_sees():
+    """Slots of a sequence before its window, and its own stale slots past kv_len, hold NaN: windows that end
+    inside a page and a tile, page sizes below and above the tile's, table entries of dropped pages invalid."""
+    for page in (8, 32, 128):
+        b = ref.Batch([(150, 1000, c) for c in (0, 1, 0, 1, 1, 0)], 8, 8, 128, page, seed=page).fill_keys()
+        want, lse = _attend(b, 90)
+        for s, (a, kl, _) in enumerate(b.seqs):
+            first = kl - a - 90
+            gone = b.slots(s, range(first))
+            b.k_cache[gone] = math.nan
+            b.v_cache[gone] = math.nan
+            b.table[s, :first // page] = -3
+        o = torch.empty_like(want)
+        dg.dg_clear_device_status()
+        dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, 150, window=90)
+        torch.cuda.synchronize()
+        assert dg.dg_get_device_status() == 0 and torch.equal(o, want)
+
+
+def test_attention_thousands_of_sequences():
+    """More sequences than a block reads at once, most of them empty or short."""
+    seqs = [(1, (7 * i) % 40, 1) if i % 3 else (0, 9, 1) for i in range(3000)]
+    b = ref.Batch(seqs, 2, 1, 64, 8, seed=6, after=1).fill_keys()
+    o = torch.full(b.q.shape, 7.0, dtype=ref.BF16, device=DEV)
+    dg.dg_clear_device_status()
+    dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, 1)
+    torch.cuda.synchronize()
+    assert dg.dg_get_device_status() == 0
+    pick = set(range(0, 3000, 37)) | {0, 1, 2, 2998, 2999}
+    ref.check_attention(b, o, None, skip=[s for s in range(3000) if s not in pick])
+
+
+def test_offsets_out_of_order_are_refused():
+    """Offsets that go back: the rows they claim are left alone or belong to a sound sequence; nothing outside
+    the tables is read."""
+    b = ref.Batch([(4, 20, 1), (5, 16, 1), (3, 30, 1)], 2, 1, 64, 16, seed=2, extra_columns=0).fill_keys()
+    for cu in ([0, 9, 4, 12], [0, -5, 9, 12], [5, 4, 3, 2], [0, 2 ** 31 - 1, 9, 12], [-7, 4, 9, 12]):
+        b.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+        q, o = b.q.clone(), torch.zeros_like(b.q)
+        dg.dg_clear_device_status()
+        dg.dg_kv_append(q[:, :1].contiguous(), q[:, 1:].contiguous(), b.k_cache.clone(), b.v_cache.clone(), b.table, b.cu,
+                        b.kv_len, inv_freq=_inv_freq(64), q=q, q_out=o)
+        dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, 5)
+        torch.cuda.synchronize()
+        assert dg.dg_get_device_status() == dg.DG_DEV_BAD_PARAM
+    dg.dg_clear_device_status()
+
+
 def test_attention_repeats_bit_for_bit():
     for seqs in (TOKENS * 5, [(1, 50000, 1)], MIXED):
         b = ref.Batch(seqs, 8, 4, 128, 16, seed=4).fill_keys()
@@ -304,9 +397,10 @@ def test_attention_workspace_needs_no_contents_and_is_checked():
             _attend_only(b, torch.empty(need + 8, dtype=torch.uint8, device=DEV)[8:])
 
 
-@pytest.mark.parametrize("q", [1, 100])
+@pytest.mark.parametrize("q", [1, 100, 400])
 def test_attention_on_streams_and_in_graphs(q):
-    """Two calls at once on two streams, and a captured call replayed after its inputs changed."""
+    """Two calls at once on two streams, and a captured call replayed after its inputs changed: one token,
+    and rows for the split keys (100) and for the query tiles (400)."""
     bs = [ref.Batch([(q, 5000 + 500 * i, 1)] * 3, 8, 4, 128, 16, seed=i).fill_keys() for i in range(2)]
     want = [_attend(b) for b in bs]
     streams = [torch.cuda.Stream() for _ in bs]
