@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
         const int s = narrow ? (int)((uint32_t)f / (uint32_t)max_q_tiles) : (int)(f / max_q_tiles);
         const int t = (int)(f - (int64_t)s * max_q_tiles);
         if constexpr (Paged) {
-            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
             if (t == 0 && (!p.ok || p.ql > a.max_q_len)) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
             if (!p.ok || p.kl == 0 || (int64_t)t * kTile >= p.ql) return false;
         }
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
 
     if constexpr (Paged) {  // the sequences without keys, after the work: their rows of zeros
         for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
-            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
             if (!p.ok || p.kl != 0) continue;
             const int64_t first = (int64_t)p.q0 * a.Hq, rows = (int64_t)p.ql * a.Hq;
             for (int64_t i = threadIdx.x; i < rows * (kHead / 8); i += kThreads)

@@ -101,7 +101,7 @@ DG_DEVINL uint64_t turns_of(double w) {
 // The sequence that owns a row, and the row's position in it (-1: none).
 DG_DEVINL int row_position(const AppendArgs& a, int t, int s) {
     if (s >= a.n_seq) return -1;
-    const dg::PagedSeq q = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+    const dg::PagedSeq q = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, 0x7fffffff);
     if (q.q0 > t) return -1;
     const bool ok = q.ok && t - q.q0 < q.ql;   // (the search says little when the offsets are not in order)
     if (!ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);

@@ -18,6 +18,9 @@ struct PagedKV {
     DG_DEVINL int64_t capacity() const { return (int64_t)max_pages << page_shift; }
 };
 
+// Keys of a sequence of an attention call, at most: an index a tile past the last key still fits 32 bits.
+constexpr int32_t kMaxKeys = 0x7fff0000;
+
 // A sequence of a paged call: its rows of q and its keys.  `ok` is false where the offsets or
 // lengths are out of range (the caller raises DG_DEV_BAD_PARAM and leaves the sequence out).
 struct PagedSeq {
@@ -25,12 +28,13 @@ struct PagedSeq {
     bool ok;
 };
 
-DG_DEVINL PagedSeq paged_seq(const PagedKV& c, const int32_t* cu_q, int64_t total_q, int s) {
+DG_DEVINL PagedSeq paged_seq(const PagedKV& c, const int32_t* cu_q, int64_t total_q, int s, int32_t max_keys) {
     PagedSeq r;
     r.q0 = cu_q[s];
     const int32_t q1 = cu_q[s + 1];
     r.kl = c.kv_len[s];
-    r.ok = r.q0 >= 0 && q1 >= r.q0 && (int64_t)q1 <= total_q && r.kl >= 0 && (int64_t)r.kl <= c.capacity();
+    r.ok = r.q0 >= 0 && q1 >= r.q0 && (int64_t)q1 <= total_q && r.kl >= 0 && r.kl <= max_keys &&
+           (int64_t)r.kl <= c.capacity();
     r.ql = r.ok ? q1 - r.q0 : 0;
     if (r.kl > 0 && r.ql > r.kl) r.ok = false;
     return r;

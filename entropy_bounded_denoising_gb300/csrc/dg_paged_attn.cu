@@ -131,7 +131,7 @@ struct SeqPlan {
 template <int Rows, int Tile>
 DG_DEVINL SeqPlan seq_plan(const SplitArgs& a, int s) {
     SeqPlan p;
-    p.seq = dg::paged_seq(a.kv, a.cu_q, a.total_q, s);
+    p.seq = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
     p.causal = a.causal[s] != 0;
     p.row_tiles = p.seq.ok ? (int)(((int64_t)p.seq.ql * a.group + Rows - 1) / Rows) : 0;
     p.tile0 = 0;
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                 const float inv = Lr > 0.f ? 1.f / Lr : 0.f;
                 *reinterpret_cast<uint2*>(a.o + out * D + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-                if (d == 0 && a.lse) a.lse[out] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+                if (d == 0 && a.lse) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;  // (a NaN stays one)
             } else {
                 *reinterpret_cast<float4*>(a.part_o + (slot * Rows + r) * D + d) = o;
                 if (d == 0) a.part_ml[slot * Rows + r] = make_float4(M, L, Lr, 0.f);
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const SplitArgs a) 
     const int64_t out = (int64_t)(q0 + qi) * a.Hq + hk * a.group + (rr - qi * a.group);
     *reinterpret_cast<uint2*>(a.o + out * D + d) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (d == 0 && a.lse) a.lse[out] = L > 0.f ? (s_m[r] + log2f(L)) * kLn2 : -INFINITY;
+    if (d == 0 && a.lse) a.lse[out] = L == 0.f ? -INFINITY : (s_m[r] + log2f(L)) * kLn2;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

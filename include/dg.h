@@ -401,7 +401,7 @@ typedef struct {
  * turns), so far positions are as exact as near ones; sines, cosines and the rotation are in fp32
  * with one rounding to bf16.
  *   k, v      (device) bf16 [total_q] rows of [Hkv][D], ldk / ldv elements apart (multiples of 8,
- *             at least Hkv * D: they may be parts of one fused projection's rows).
+ *             at least Hkv * D, below 2^31: they may be parts of one fused projection's rows).
  *   q         (device, may be NULL) bf16 [total_q] rows of [Hq][D], ldq apart.
  *   q_out     (device, out, NULL iff q is) bf16 [total_q][Hq][D]; may be q itself when
  *             ldq = Hq * D, else must not overlap q.
@@ -432,11 +432,12 @@ DG_API dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v,
  *   workspace (device) >= dg_paged_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D),
  *             16-byte aligned, no initial contents; calls that overlap on the GPU need their own.
  * A sequence with kv_len 0 sees no key: its rows of o are 0 and its lse -inf.  A sequence whose
- * offsets lie outside [0, total_q], with kv_len < 0, 0 < kv_len < q_len or kv_len > max_pages *
- * page_size raises DG_DEV_BAD_PARAM and is skipped (its rows are not written); one with more than max_q_len
- * queries raises it too and gets at least its first max_q_len rows; one that needs a page
- * outside [0, n_pages) raises it and its rows are unspecified.  Rows of no sequence are not written.
- * Limits and errors as dg_attention and dg_kv_append. */
+ * offsets lie outside [0, total_q], with kv_len < 0, 0 < kv_len < q_len, kv_len > max_pages *
+ * page_size or kv_len > 2^31 - 2^16 raises DG_DEV_BAD_PARAM and is skipped (its rows are not
+ * written); one with more than max_q_len queries raises it too and gets at least its first max_q_len
+ * rows; one that needs a page outside [0, n_pages) raises it and its rows are unspecified.  Rows of no
+ * sequence are not written.
+ * Limits and errors as dg_attention and dg_kv_append.  Two kernels. */
 DG_API size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D);
 DG_API dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
                                     const int32_t* cu_q, const uint8_t* causal, int32_t n_seq, int32_t max_q_len,

@@ -363,6 +363,66 @@ def test_offsets_out_of_order_are_refused():
     dg.dg_clear_device_status()
 
 
+def test_longest_sequences():
+    """Sequences at the limit of kv_len, of which a window shows the last two pages: appended to and read by
+    either path; one key more is refused by the attention."""
+    last, page, D, H, W = (1 << 31) - (1 << 16), 65536, 64, 8, 100
+    for rows in (1, 640):
+        b = ref.Batch([(rows, rows + W, 1)], H, H, D, 1024, seed=rows)
+        kc, vc = (torch.zeros((2, page, H, D), dtype=ref.BF16, device=DEV) for _ in range(2))
+        table = torch.full((1, last // page + 1), -1, dtype=torch.int32, device=DEV)
+        table[0, last // page - 2:last // page] = torch.tensor([0, 1])
+        g = torch.Generator(device=DEV).manual_seed(rows)
+        k, v = (torch.randn((rows + W, H, D), generator=g, device=DEV).to(ref.BF16) for _ in range(2))
+        cu = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+        cu_all = torch.tensor([0, rows + W], dtype=torch.int32, device=DEV)
+        causal = torch.ones(1, dtype=torch.uint8, device=DEV)
+        for kl, status in ((last, 0), (last + 1, dg.DG_DEV_BAD_PARAM)):
+            kv_len = torch.tensor([kl], dtype=torch.int32, device=DEV)
+            o, lse = torch.full((rows, H, D), 7.0, dtype=ref.BF16, device=DEV), torch.full((rows, H), 7.0, device=DEV)
+            dg.dg_clear_device_status()
+            if not status:
+                dg.dg_kv_append(k, v, kc, vc, table, cu_all, kv_len)
+            dg.dg_paged_attention(b.q, kc, vc, o, table, cu, kv_len, causal, rows, lse=lse, window=W)
+            torch.cuda.synchronize()
+            assert dg.dg_get_device_status() == status
+            if status:
+                assert (o == 7.0).all() and (lse == 7.0).all()
+                continue
+            assert torch.equal(kc[1, -(rows + W):], k) and torch.equal(vc[1, -(rows + W):], v)
+            ro, rl, bound, lbound = ref.attention(b.q, k, v, True, W, 1 / 8)
+            assert ((o.double() - ro).abs() <= bound).all() and ((lse.double() - rl).abs() <= lbound).all()
+    dg.dg_clear_device_status()
+
+
+@pytest.mark.parametrize("rows", [1, 640])
+def test_attention_past_32_bit_offsets(rows):
+    """The last pages of a cache of more than 2^32 bytes and 2^31 elements, by either path."""
+    D, H, page = 64, 8, 64
+    n_pages = (1 << 31) // (D * H * page) + 16
+    small = ref.Batch([(rows, 700, 1)], H, H, D, page, seed=1, extra_columns=0).fill_keys()
+    kc, vc = (torch.full((n_pages, page, H, D), math.nan, dtype=ref.BF16, device=DEV) for _ in range(2))
+    used = small.table.flatten().long()
+    far = torch.arange(n_pages - used.numel(), n_pages, dtype=torch.int32, device=DEV)
+    kc[far.long()], vc[far.long()] = small.k_cache[used], small.v_cache[used]
+    o = torch.zeros_like(small.q)
+    dg.dg_paged_attention(small.q, kc, vc, o, far[None], small.cu, small.kv_len, small.causal, rows)
+    ref.check_attention(small, o, None)
+
+
+@pytest.mark.parametrize("rows", [5, 640])
+def test_attention_nan_queries_stay_in_their_rows(rows):
+    """A query of NaN: its rows of o and lse are NaN, by either path; all others are right."""
+    b = ref.Batch([(rows, 700, 1), (1, 900, 1)], 8, 8, 64, 16, seed=rows).fill_keys()
+    o0, l0 = _attend(b)
+    q = b.q[2, 3].clone()
+    b.q[2, 3] = math.nan
+    o, lse = _attend_only(b)
+    assert torch.isnan(o[2, 3]).all() and torch.isnan(lse[2, 3])
+    b.q[2, 3], o[2, 3], lse[2, 3] = q, o0[2, 3], l0[2, 3]
+    ref.check_attention(b, o, lse)
+
+
 def test_attention_repeats_bit_for_bit():
     for seqs in (TOKENS * 5, [(1, 50000, 1)], MIXED):
         b = ref.Batch(seqs, 8, 4, 128, 16, seed=4).fill_keys()
