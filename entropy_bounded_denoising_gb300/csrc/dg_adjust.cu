@@ -22,6 +22,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;   // rows in flight a thread
 constexpr int kMaxRows = 64; // rows of a block, at most
+constexpr int kEarly = 2;    // entries of each list that a thread reads before anything else
 
 struct AdjustArgs {
     const unsigned char* x;
@@ -108,9 +109,10 @@ template <int Bytes>
 __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
     constexpr int PerVec = 16 / Bytes;
     constexpr int kSlice = kThreads * PerVec;   // tokens of a block
-    __shared__ int32_t n_hist[kSlice];          // occurrences in the history
-    __shared__ int32_t n_bias[kSlice];          // entries in the bias list
-    __shared__ int32_t first_bias[kSlice];      // the first of them
+    __shared__ __align__(16) int32_t n_hist[kSlice];       // occurrences in the history
+    __shared__ __align__(16) int32_t n_bias[kSlice];       // entries in the bias list
+    __shared__ int32_t first_bias[kSlice];                 // the first of them
+    __shared__ float one_bias[kSlice];                     // and the value when it is the only one
     __shared__ int32_t row_mask[kMaxRows];
     __shared__ uint2 expand[16];
     constexpr uint32_t kNegInf = Bytes == 2 ? 0xff80ff80u : 0xff800000u;
@@ -157,14 +159,25 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
         expand[tid] = make_uint2(((tid & 1) ? 0xffffu : 0u) | ((tid & 2) ? 0xffff0000u : 0u),
                                  ((tid & 4) ? 0xffffu : 0u) | ((tid & 8) ? 0xffff0000u : 0u));
     const bool listed = h1 > h0 || b1 > b0;
+    // a thread's first entries of the lists are on their way meanwhile
+    int32_t early_h[kEarly], early_b[kEarly];
+    float early_v[kEarly];
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k) {
+        const int64_t i = (int64_t)h0 + tid + k * kThreads, j = (int64_t)b0 + tid + k * kThreads;
+        early_h[k] = i < h1 ? a.history[i] : -1;
+        early_b[k] = j < b1 ? a.bias_tokens[j] : -1;
+        early_v[k] = j < b1 ? a.bias_values[j] : 0.f;
+    }
     if (listed) {
 #pragma unroll
-        for (int e = 0; e < PerVec; ++e) {
-            n_hist[e * kThreads + tid] = 0;
-            if (b1 > b0) {
-                n_bias[e * kThreads + tid] = 0;
-                first_bias[e * kThreads + tid] = 0x7fffffff;
-            }
+        for (int e = 0; e < PerVec / 4; ++e) {
+            reinterpret_cast<int4*>(n_hist)[e * kThreads + tid] = make_int4(0, 0, 0, 0);
+            if (b1 > b0) reinterpret_cast<int4*>(n_bias)[e * kThreads + tid] = make_int4(0, 0, 0, 0);
+        }
+        if (b1 > b0) {
+#pragma unroll
+            for (int e = 0; e < PerVec; ++e) first_bias[e * kThreads + tid] = 0x7fffffff;
         }
     }
     __syncthreads();
@@ -194,42 +207,64 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
                 x[u] = *reinterpret_cast<const uint4*>(src + u * a.ld_bytes);
         }
     };
+    const int end = min(kSlice, a.V - slice0);
+    auto count = [&](int32_t token) {
+        const int64_t t = (int64_t)token - slice0;
+        if (t >= 0 && t < end) atomicAdd(&n_hist[t], 1);
+    };
+    auto note = [&](int32_t token, float value, int i) {
+        const int64_t t = (int64_t)token - slice0;
+        if (t < 0 || t >= end) return;
+        atomicAdd(&n_bias[t], 1);
+        atomicMin(&first_bias[t], i);
+        one_bias[t] = value;
+    };
     masks_of(0);
+    if (listed) {
+#pragma unroll
+        for (int k = 0; k < kEarly; ++k) {
+            count(early_h[k]);
+            note(early_b[k], early_v[k], b0 + tid + k * kThreads);
+        }
+    }
     load(0, in_place && !listed);
+    if (listed) {
+#pragma unroll 4
+        for (int64_t i = (int64_t)h0 + kEarly * kThreads + tid; i < h1; i += kThreads) count(a.history[i]);
+#pragma unroll 4
+        for (int64_t i = (int64_t)b0 + kEarly * kThreads + tid; i < b1; i += kThreads)
+            note(a.bias_tokens[i], a.bias_values[i], (int)i);
+    }
     float add[PerVec];
     uint32_t penalised = 0, edited = 0;   // tokens with a count / with a count or a bias
 #pragma unroll
     for (int e = 0; e < PerVec; ++e) add[e] = 0.f;
     if (listed) {
-        const int end = min(kSlice, a.V - slice0);
-#pragma unroll 4
-        for (int i = h0 + tid; i < h1; i += kThreads) {
-            const int64_t t = (int64_t)a.history[i] - slice0;
-            if (t >= 0 && t < end) atomicAdd(&n_hist[t], 1);
-        }
-#pragma unroll 4
-        for (int i = b0 + tid; i < b1; i += kThreads) {
-            const int64_t t = (int64_t)a.bias_tokens[i] - slice0;
-            if (t >= 0 && t < end) {
-                atomicAdd(&n_bias[t], 1);
-                atomicMin(&first_bias[t], i);
-            }
-        }
         __syncthreads();
+        int nh[PerVec], nb[PerVec];
+#pragma unroll
+        for (int e = 0; e < PerVec; e += 4) {
+            *reinterpret_cast<int4*>(&nh[e]) = *reinterpret_cast<const int4*>(&n_hist[tid * PerVec + e]);
+            *reinterpret_cast<int4*>(&nb[e]) =
+                b1 > b0 ? *reinterpret_cast<const int4*>(&n_bias[tid * PerVec + e]) : make_int4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int e = 0; e < PerVec; ++e) {
-            const int nh = n_hist[tid * PerVec + e];
-            int nb = b1 > b0 ? n_bias[tid * PerVec + e] : 0;
             float b = 0.f;
-            for (int i = nb > 0 ? first_bias[tid * PerVec + e] : 0; nb > 0 && i < b1; ++i)   // in list order
-                if (a.bias_tokens[i] == v0 + e) {
-                    b += a.bias_values[i];
-                    --nb;
-                    edited |= 1u << e;
-                }
-            if (nh > 0) {
+            if (nb[e] == 1) {
+                b = one_bias[tid * PerVec + e];
+            } else if (nb[e] > 1) {   // in list order
+                int left = nb[e];
+                for (int i = first_bias[tid * PerVec + e]; left > 0 && i < b1; ++i)
+                    if (a.bias_tokens[i] == v0 + e) {
+                        b += a.bias_values[i];
+                        --left;
+                    }
+            }
+            if (nb[e] > 0) edited |= 1u << e;
+            if (nh[e] > 0) {
                 penalised |= 1u << e;
-                b -= pen.frequency * (float)nh + pen.presence;
+                b -= pen.frequency * (float)nh[e] + pen.presence;
             }
             add[e] = b;
         }
