@@ -8,6 +8,8 @@ built (run ``entropy_bounded_denoising_gb300.build.build()``).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 
@@ -27,6 +29,7 @@ _PARAM_FMT = "<fffiiiiII"
 PARAM_BYTES = struct.calcsize(_PARAM_FMT)   # 36, sizeof(dg_canvas_params)
 
 _lib = None
+_bind = None   # dg_bind.so, connected to _lib
 
 
 class _PagedKV(ctypes.Structure):   # dg_paged_kv
@@ -47,14 +50,15 @@ def library_path() -> str:
 
 
 def load(path: str | None = None):
-    """Load libdg.so (built in-tree).  Raises if it is missing."""
-    global _lib
+    """Load libdg.so and dg_bind.so (built in-tree).  Raises if either is missing."""
+    global _lib, _bind
     if _lib is not None:
         return _lib
     path = path or _build.LIB
-    if not os.path.exists(path):
-        raise RuntimeError(f"libdg.so not found at {path}: build it with "
-                           "entropy_bounded_denoising_gb300.build.build()")
+    for p in (path, _build.BIND):
+        if not os.path.exists(p):
+            raise RuntimeError(f"{os.path.basename(p)} not found at {p}: build it with "
+                               "entropy_bounded_denoising_gb300.build.build()")
     lib = ctypes.CDLL(path)
     P, i32, i64, u32, u64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                                   ctypes.c_uint64, ctypes.c_size_t)
@@ -112,7 +116,12 @@ def load(path: str | None = None):
         f = getattr(lib, name)
         f.restype = res
         f.argtypes = args
-    _lib = lib
+    names = ("dg_kv_append", "dg_paged_attention", "dg_paged_attention_workspace_bytes", "dg_adjust_logits")
+    loader = importlib.machinery.ExtensionFileLoader("dg_bind", _build.BIND)
+    bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("dg_bind", loader))
+    loader.exec_module(bind)
+    bind.connect(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+    _lib, _bind = lib, bind
     return lib
 
 
@@ -424,110 +433,24 @@ def dg_attention(q, k, v, o, cu_q, cu_kv, causal, max_q_len: int, *, lse=None, w
     return rc
 
 
-# The serving calls below are made once a token: their checks are written out, with few calls, because a
+# The serving calls below are made once a token: dg_bind.so checks and marshals their arguments, because a
 # call of a few microseconds on the device waits for the host.
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+def _serving():
+    if _bind is None:
+        load()
+    return _bind
 
 
-def _refuse(fn, name, t, dtype, shape, dev):
-    """Why a tensor is not a contiguous one of dtype and shape (None = any extent) on device dev."""
-    if t.dtype != dtype:
-        raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
-        raise ValueError(f"{fn}: {name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be contiguous")
-    raise ValueError(f"{fn}: {name} is on {t.device}, other tensors of the call on device {dev}")
-
-
-def _whole(fn, name, t, dtype, shape, dev):
-    """The address of a contiguous tensor of dtype and shape on device dev; None for None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(fn, name, t, dtype, shape, dev)
-    return t.data_ptr()
-
-
-# the current stream's handle without building a Stream object (3 us of a 15 us call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _on(fn, dev, stream):
-    """The raw stream of a call whose tensors are on device dev, the current one."""
-    if dev < 0:
-        raise ValueError(f"{fn}: device tensors expected")
-    if dev != _device():
-        raise ValueError(f"{fn}: the tensors are on device {dev}, the current device is {_device()}")
-    return _raw_stream(dev) if stream is None else _s(stream)
-
-
-def _rows(fn, name, t, heads, d, dev):
-    """Address and row stride of t [tokens, heads, d], whose rows hold [heads][d] without gaps."""
-    if t.dtype is not _BF16:
-        raise TypeError(f"{fn}: {name} must be bfloat16, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
-        raise ValueError(f"{fn}: {name} must have shape (tokens, {heads}, {d}), got {tuple(shape)}")
-    row, head, one = t.stride()
-    if one != 1 or (heads > 1 and head != d):
-        raise ValueError(f"{fn}: {name}'s heads must follow each other")
-    if t.get_device() != dev:
-        _refuse(fn, name, t, t.dtype, shape, dev)
-    return t.data_ptr(), row if shape[0] > 1 else heads * d
-
-
-def _refuse_cache(fn, k_cache, v_cache):
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{fn}: {name} must be bfloat16, got {t.dtype}")
-        if t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError(f"{fn}: {name} must be [n_pages, page_size, Hkv, D] with contiguous heads")
-    raise ValueError(f"{fn}: k_cache and v_cache must have one layout")
-
-
-def _paged_kv(fn, k_cache, v_cache, page_table, kv_len):
-    """dg_paged_kv of k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides of the first three) and
-    page_table [n_seq, max_pages], kv_len [n_seq] int32; n_seq, Hkv, D and the device."""
-    shape, strides = k_cache.shape, k_cache.stride()
-    if (k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16 or len(shape) != 4
-            or strides[3] != 1 or v_cache.shape != shape or v_cache.stride() != strides):
-        _refuse_cache(fn, k_cache, v_cache)
-    n_pages, page_size, Hkv, D = shape
-    dev = k_cache.get_device()
-    if v_cache.get_device() != dev:
-        _refuse(fn, "v_cache", v_cache, v_cache.dtype, (None,) * 4, dev)
-    n = kv_len.numel()
-    if kv_len.dtype is not _I32 or kv_len.dim() != 1 or not kv_len.is_contiguous() or kv_len.get_device() != dev:
-        _refuse(fn, "kv_len", kv_len, _I32, (n,), dev)
-    ts = page_table.shape
-    if (page_table.dtype is not _I32 or len(ts) != 2 or ts[0] != n or not page_table.is_contiguous()
-            or page_table.get_device() != dev):
-        _refuse(fn, "page_table", page_table, _I32, (n, None), dev)
-    # the stride of an extent of one says nothing: any valid one will do
-    ps, ss, hs, _ = strides
-    if n_pages == 1 or page_size == 1 or Hkv == 1:
-        ps, ss, hs = (s if e > 1 else D for e, s in zip(shape, (ps, ss, hs)))
-    return (_PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), n_pages, ps, ss,
-                     hs, page_size, ts[1]), n, Hkv, D, dev)
-
-
-def _scratch(fn, nbytes, workspace, dev, stream):
-    """Address and size of the caller's workspace, or of one for this call; a fresh one lives until the
-    call's stream passes it."""
-    if workspace is None:
-        workspace = torch.empty(max(1, nbytes), dtype=torch.uint8, device=dev)
-        if stream is not None and _s(stream) != torch.cuda.current_stream().cuda_stream:
-            # the allocator orders memory along the current stream: order the call's stream after it and
-            # keep the memory until that stream is done with it
-            st = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-            st.wait_stream(torch.cuda.current_stream())
-            workspace.record_stream(st)
-        return workspace, nbytes
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        _refuse(fn, "workspace", workspace, workspace.dtype, workspace.shape, dev)
-    return workspace, workspace.nbytes
+def _scratch(nbytes, dev, stream):
+    """A workspace for one call; it lives until the call's stream passes it."""
+    workspace = torch.empty(max(1, nbytes), dtype=torch.uint8, device=dev)
+    if stream is not None and _s(stream) != torch.cuda.current_stream().cuda_stream:
+        # the allocator orders memory along the current stream: order the call's stream after it and
+        # keep the memory until that stream is done with it
+        st = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        st.wait_stream(torch.cuda.current_stream())
+        workspace.record_stream(st)
+    return workspace
 
 
 def dg_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, *, inv_freq=None, interleaved=False, q=None,
@@ -536,33 +459,10 @@ def dg_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, *, inv_freq=N
     inv_freq [rot_dim / 2] float64; q [total, Hq, D] is rotated into q_out (contiguous).  The cache:
     k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides but the last), page_table [n_seq,
     max_pages], kv_len [n_seq] and cu_q [n_seq + 1] int32."""
-    fn = "dg_kv_append"
-    if (q is None) != (q_out is None):
-        raise ValueError(f"{fn}: q and q_out come together")
-    kv, n, Hkv, D, dev = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
-    total = k.shape[0]
-    kp, ldk = _rows(fn, "k", k, Hkv, D, dev)
-    vp, ldv = _rows(fn, "v", v, Hkv, D, dev)
-    Hq, qp, ldq, op = Hkv, None, 0, None
-    if v.shape[0] != total or (q is not None and q.shape[0] != total):
-        raise ValueError(f"{fn}: q, k and v must have as many rows")
-    if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        qp, ldq = _rows(fn, "q", q, Hq, D, dev)
-        if (q_out.dtype is not _BF16 or q_out.shape != q.shape or not q_out.is_contiguous()
-                or q_out.get_device() != dev):
-            _refuse(fn, "q_out", q_out, _BF16, (total, Hq, D), dev)
-        op = q_out.data_ptr()
-    if cu_q.dtype is not _I32 or cu_q.shape != (n + 1,) or not cu_q.is_contiguous() or cu_q.get_device() != dev:
-        _refuse(fn, "cu_q", cu_q, _I32, (n + 1,), dev)
-    half, wp = 0, None
-    if inv_freq is not None:
-        half = inv_freq.numel()
-        wp = _whole(fn, "inv_freq", inv_freq, torch.float64, (half,), dev)
-    rc = load().dg_kv_append(kp, ldk, vp, ldv, qp, ldq, op, cu_q.data_ptr(), n, total, Hq, Hkv, D, wp, 2 * half,
-                             1 if interleaved else 0, kv, _on(fn, dev, stream))
+    rc = _serving().kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, inv_freq, interleaved, q, q_out,
+                              None if stream is None else _s(stream))
     if check and rc:
-        _check(fn, rc)
+        _check("dg_kv_append", rc)
     return rc
 
 
@@ -575,28 +475,13 @@ def dg_paged_attention(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal,
                        check=True) -> int:
     """dg_attention over the paged cache of dg_kv_append: q, o [total_q, Hq, D] bf16, cu_q [n + 1] and
     kv_len [n] int32, causal [n] uint8, lse [total_q, Hq] float32."""
-    fn = "dg_paged_attention"
-    kv, n, Hkv, D, dev = _paged_kv(fn, k_cache, v_cache, page_table, kv_len)
-    rows = q.shape
-    if q.dtype is not _BF16 or len(rows) != 3 or rows[2] != D or not q.is_contiguous() or q.get_device() != dev:
-        _refuse(fn, "q", q, _BF16, (None, None, D), dev)
-    total, Hq, _ = rows
-    if o.dtype is not _BF16 or o.shape != rows or not o.is_contiguous() or o.get_device() != dev:
-        _refuse(fn, "o", o, _BF16, rows, dev)
-    if cu_q.dtype is not _I32 or cu_q.shape != (n + 1,) or not cu_q.is_contiguous() or cu_q.get_device() != dev:
-        _refuse(fn, "cu_q", cu_q, _I32, (n + 1,), dev)
-    cz = _whole(fn, "causal", causal, torch.uint8, (n,), dev)
-    lp = None if lse is None else _whole(fn, "lse", lse, _F32, (total, Hq), dev)
-    st = _on(fn, dev, stream)
-    lib = load()
-    max_q_len = int(max_q_len)
-    scale = D ** -0.5 if scale is None else float(scale)
-    need = 0 if workspace is not None else lib.dg_paged_attention_workspace_bytes(n, max_q_len, Hq, Hkv, D)
-    workspace, ws_bytes = _scratch(fn, need, workspace, dev, stream)
-    rc = lib.dg_paged_attention(q.data_ptr(), kv, o.data_ptr(), lp, cu_q.data_ptr(), cz, n, max_q_len, total, Hq, Hkv,
-                                D, int(window), scale, workspace.data_ptr(), ws_bytes, st)
+    call, st = _serving().paged_attention, None if stream is None else _s(stream)
+    rc = call(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal, max_q_len, lse, window, scale, workspace, st)
+    if workspace is None:   # rc: the bytes it needs; nothing has run
+        rc = call(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal, max_q_len, lse, window, scale,
+                  _scratch(rc[0], q.device, stream), st)
     if check and rc:
-        _check(fn, rc)
+        _check("dg_paged_attention", rc)
     return rc
 
 
@@ -606,39 +491,10 @@ def dg_adjust_logits(logits, params, out=None, *, history=None, cu_history=None,
     """Penalties for the tokens of history (penalties [n, 3]: repetition, frequency, presence), biases and
     masks (int32 words, bit set = allowed; mask_index [n, L], -1 = none) on logits [n, L, ld], into out
     (in place when None).  history / bias lists are packed, canvas c's at cu[c] .. cu[c + 1]."""
-    fn = "dg_adjust_logits"
-    out = logits if out is None else out
-    if logits.dim() != 3 or out.dim() != 3:
-        raise ValueError(f"{fn}: logits and out must be [n, L, ld]")
-    dt, dtype = _dtype_code(logits), logits.dtype
-    n, L, ld = logits.shape
-    ldo = out.shape[2]
-    V = ld if V is None else V
-    if (history is None) != (cu_history is None) or (history is None) != (penalties is None):
-        raise ValueError(f"{fn}: history, cu_history and penalties come together")
-    if (bias_tokens is None) != (bias_values is None) or (bias_tokens is None) != (cu_bias is None):
-        raise ValueError(f"{fn}: bias_tokens, bias_values and cu_bias come together")
-    if (masks is None) != (mask_index is None):
-        raise ValueError(f"{fn}: masks and mask_index come together")
-    i32, f32, dev = torch.int32, torch.float32, logits.get_device()
-    nh = 0 if history is None else history.numel()
-    nb = 0 if bias_tokens is None else bias_tokens.numel()
-    n_masks, words = (0, 0) if masks is None else masks.shape if masks.dim() == 2 else (-1, -1)
-    xp = _whole(fn, "logits", logits, dtype, (n, L, ld), dev)
-    op = _whole(fn, "out", out, dtype, (n, L, ldo), dev)
-    pp = _whole(fn, "params", params, torch.uint8, (n * PARAM_BYTES,), dev)
-    hp = _whole(fn, "history", history, i32, (nh,), dev)
-    ch = _whole(fn, "cu_history", cu_history, i32, (n + 1,), dev)
-    pen = _whole(fn, "penalties", penalties, f32, (n, 3), dev)
-    bt = _whole(fn, "bias_tokens", bias_tokens, i32, (nb,), dev)
-    bv = _whole(fn, "bias_values", bias_values, f32, (nb,), dev)
-    cb = _whole(fn, "cu_bias", cu_bias, i32, (n + 1,), dev)
-    mp = _whole(fn, "masks", masks, i32, (n_masks, words), dev)
-    mi = _whole(fn, "mask_index", mask_index, i32, (n, L), dev)
-    rc = load().dg_adjust_logits(xp, dt, ld, op, ldo, n, L, V, pp, hp, ch, nh, pen, bt, bv, cb, nb, mp, words,
-                                 n_masks, mi, _on(fn, dev, stream))
+    rc = _serving().adjust_logits(logits, params, out, history, cu_history, penalties, bias_tokens, bias_values, cu_bias,
+                                  masks, mask_index, V, None if stream is None else _s(stream), PARAM_BYTES)
     if check and rc:
-        _check(fn, rc)
+        _check("dg_adjust_logits", rc)
     return rc
 
 

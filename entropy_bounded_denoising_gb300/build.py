@@ -1,8 +1,9 @@
 """Build libdg.so (the CUDA kernels behind include/dg.h) in-tree for sm_103a.
 
 Each translation unit is compiled by its own nvcc process, in parallel, then linked into
-``entropy_bounded_denoising_gb300/_build/libdg.so``.  Objects are rebuilt only when a source
-or header is newer than the library.
+``entropy_bounded_denoising_gb300/_build/libdg.so``; beside it ``dg_bind.so``, the serving calls'
+Python module (host code against PyTorch's headers).  Objects are rebuilt only when a source or
+header is newer than the libraries.
 """
 from __future__ import annotations
 
@@ -11,12 +12,18 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libdg.so")
+BIND = os.path.join(OUT, "dg_bind.so")
+BIND_SRC = os.path.join(CSRC, "dg_bind.cpp")
+TORCH = os.path.dirname(os.path.abspath(torch.__file__))
 HEADER = os.path.join(ROOT, "include", "dg.h")
 
 NVCC_FLAGS = [
@@ -27,8 +34,12 @@ NVCC_FLAGS = [
 ]
 
 
+def _cuda() -> str:
+    return os.environ.get("CUDA_HOME", "/usr/local/cuda")
+
+
 def _nvcc() -> str:
-    cand = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "bin", "nvcc")
+    cand = os.path.join(_cuda(), "bin", "nvcc")
     return cand if os.path.exists(cand) else "nvcc"
 
 
@@ -37,11 +48,25 @@ def sources() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER, __file__]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [BIND_SRC, HEADER, __file__]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _build_bind() -> None:
+    tmp = BIND + f".tmp{os.getpid()}"
+    lib = os.path.join(TORCH, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(TORCH, "include"), "-isystem", os.path.join(_cuda(), "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), BIND_SRC, "-o", tmp,
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -60,8 +85,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(sources()))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources()) + 1) as ex:
+        bind = ex.submit(_build_bind)
         objs = list(ex.map(compile_one, sources()))
+        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-o", tmp, *objs,
            "-Xcompiler", "-fPIC", "-lcudart"]

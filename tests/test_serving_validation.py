@@ -128,6 +128,46 @@ def test_python_checks_come_before_the_device():
         dg.dg_adjust_logits(x, p)
 
 
+def test_python_refuses_what_is_not_a_tensor_or_does_not_fit():
+    bf = torch.bfloat16
+    k, c = torch.zeros((4, 2, 64), dtype=bf), torch.zeros((3, 8, 2, 64), dtype=bf)
+    table, cu, kl = torch.zeros((1, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    q, causal = torch.zeros((4, 4, 64), dtype=bf), torch.zeros(1, dtype=torch.uint8)
+    good = dict(k=k, v=k, k_cache=c, v_cache=c, page_table=table, cu_q=cu, kv_len=kl)
+    for name, bad, kind in (("k", None, TypeError), ("v", 3, TypeError), ("k_cache", [c], TypeError), ("v_cache", c[0], ValueError),
+                            ("page_table", None, TypeError), ("kv_len", None, TypeError), ("cu_q", kl, ValueError),
+                            ("k", k[0], ValueError), ("v", k[:, :1], ValueError), ("v", k.transpose(0, 1), ValueError),
+                            ("v", k[:3], ValueError), ("k", torch.zeros((4, 4, 64), dtype=bf)[:, ::2], ValueError),
+                            ("k_cache", c.to_sparse(), TypeError), ("kv_len", torch.zeros((1, 1), dtype=torch.int32), ValueError)):
+        with pytest.raises(kind):
+            dg.dg_kv_append(**{**good, name: bad})
+    for kw in (dict(inv_freq=torch.zeros(8)), dict(inv_freq=3), dict(q=q, q_out=q.float()), dict(q=q.float(), q_out=q)):
+        with pytest.raises(TypeError):
+            dg.dg_kv_append(**good, **kw)
+    for kw in (dict(q=q[:3], q_out=q[:3]), dict(q=q, q_out=q[:, :2]), dict(q=q, q_out=q.transpose(0, 1)),
+               dict(inv_freq=torch.zeros((1, 8), dtype=torch.float64))):
+        with pytest.raises(ValueError):
+            dg.dg_kv_append(**good, **kw)
+    good = dict(q=q, k_cache=c, v_cache=c, o=q, page_table=table, cu_q=cu, kv_len=kl, causal=causal, max_q_len=4)
+    for name, bad, kind in (("q", None, TypeError), ("o", q[:3], ValueError), ("q", q.transpose(0, 1), ValueError),
+                            ("causal", kl, TypeError), ("max_q_len", 1.5, TypeError), ("max_q_len", 1 << 31, ValueError),
+                            ("lse", torch.zeros(4), ValueError), ("window", 1 << 40, ValueError), ("scale", "1", TypeError)):
+        with pytest.raises(kind):
+            dg.dg_paged_attention(**{**good, name: bad})
+    x, p = torch.zeros((1, 4, 64)), torch.zeros(36, dtype=torch.uint8)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    f32 = torch.zeros
+    for args, kw, kind in (((x.double(), p), {}, TypeError), ((x[0], p), {}, ValueError), ((x, p[:35]), {}, ValueError),
+                           ((x, None), {}, TypeError), ((None, p), {}, TypeError), ((x, p), dict(V=1.5), TypeError),
+                           ((x, p, x[:, :3]), {}, ValueError), ((x, p), dict(masks=i32(2), mask_index=i32(1, 4)), ValueError),
+                           ((x, p), dict(masks=i32(1, 2), mask_index=i32(4)), ValueError),
+                           ((x, p), dict(history=i32(3), cu_history=i32(2), penalties=f32(3)), ValueError),
+                           ((x, p), dict(history=i32(3).long(), cu_history=i32(2), penalties=f32(1, 3)), TypeError),
+                           ((x, p), dict(bias_tokens=i32(3), bias_values=f32(2), cu_bias=i32(2)), ValueError)):
+        with pytest.raises(kind):
+            dg.dg_adjust_logits(*args, **kw)
+
+
 def test_paged_attention_form_matches_the_attention_oracle():
     """The fp64 form reads the pages as the oracle of dg_attention reads packed keys."""
     b = ref.Batch([(3, 20, True), (5, 13, False), (1, 9, True)], 4, 2, 64, 8, seed=1, device="cpu").fill_keys()
