@@ -109,11 +109,13 @@ DG_DEVINL int row_position(const AppendArgs& a, int t, int s) {
 }
 
 // A block's rows are looked up and its sines computed while its data is on the way: every thread
-// first asks for the 64 bytes it will store.
+// first asks for the 32 bytes a task that it will store.
+// Bound by memory from a few thousand rows on: 30k rows of 32 heads of 256 (907 MB to and fro) take 138 us,
+// 6.6 TB/s.  Below, by its chain of dependent reads (offsets, lengths, page) and the launch: 64 rows of 32 heads of
+// 128 take 3.1 us, 2048 rows 9.1, where a copy of their 34 MB takes 6.6.
 // PerThread: a thread's tasks.  One, with the most threads an SM holds, while every task has a
 // place at once; four where there are several rounds of blocks (more bytes on the way and fewer lookups
-// a byte): 64 rows of 32 heads of 128 take 3.3 us with one and 4.8 with four, 2048 rows 9.3 and 8.9,
-// 30k rows of 32 heads of 256 149 and 138.
+// a byte): 64 rows take 3.3 us with one and 4.8 with four, 2048 rows 9.3 and 8.9, the 30k rows 149 and 138.
 template <bool Interleaved, int PerThread>
 __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_append(const AppendArgs a) {
     constexpr int kPerThread = PerThread, kUnit = kAppendThreads * PerThread;   // tasks of a block
@@ -143,6 +145,7 @@ __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_a
             y[u] = *reinterpret_cast<const uint4*>(src + k.at + k.dist);
         }
     }
+    const double w0 = tid < rows * half ? a.inv_freq[tid % half] : 0.0;   // of this thread's first angle
     int mine = -1, owner = 0;   // the row this thread looks up
     if (rows <= kAppendThreads / 32) {   // a warp a row: two dependent reads for up to 1024 sequences
         if (warp < rows) {
@@ -179,7 +182,8 @@ __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_a
     }
     for (int i = tid; i < rows * half; i += kAppendThreads) {
         const int r = i / half;
-        const int64_t u = (int64_t)(turns_of(a.inv_freq[i - r * half]) * (uint64_t)position[r]);
+        const double w = i == tid ? w0 : a.inv_freq[i - r * half];
+        const int64_t u = (int64_t)(turns_of(w) * (uint64_t)position[r]);
         float sn, c;
         sincospif((float)u * 1.0842021724855044e-19f, &sn, &c);  // 2^-63: half turns in [-1, 1]
         cs[i] = make_float2(c, sn);
