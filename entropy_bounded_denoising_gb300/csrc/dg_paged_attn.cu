@@ -57,7 +57,10 @@ struct SplitCfg {
     // and (8, 16, 3, 1) 233 (64 requests over 8k keys), but 16 rows need the registers of eight warps: 64 us
     // against 70 (32 requests of 5 drafts over 4k); for 256 (4, 16, 3, 1) takes 85 us where (7, 16, 2, 1) takes
     // 76.5 (128 requests over 1.2k keys), and the same on one long context.
-    static constexpr int kWarps = D == 64 ? 4 : D == 256 ? 7 : NB == 1 ? 6 : 4, kThreads = kWarps * 32;
+    // 16 rows of 256 with their queries in registers, (7, 16, 2, 1), spill: 41.7 and 243 us (16 requests of 5 drafts
+    // over 3k keys, 64 of 4 over 8k) against 38.1 and 234 with six warps and the queries in shared memory.
+    static constexpr bool kSharedQ = D == 256 && NB == 2;
+    static constexpr int kWarps = D == 64 ? 4 : D == 256 ? (NB == 1 ? 7 : 6) : NB == 1 ? 6 : 4, kThreads = kWarps * 32;
     static constexpr int kStep = D == 64 ? 32 : 16;        // keys of a warp's step
     static constexpr int kTileKeys = kWarps * kStep;       // keys of a tile
     static constexpr int kStages = D == 256 || (D == 128 && NB == 1) ? 2 : 3;
@@ -65,7 +68,8 @@ struct SplitCfg {
     static constexpr uint32_t kHalf = kStep * D * 2;       // the keys of a step (or its values)
     static constexpr uint32_t kStage = 2 * kHalf;
     static constexpr uint32_t kRing = kStages * kStage;    // a warp's ring
-    static constexpr size_t kSmem = (size_t)kWarps * kRing;
+    static constexpr size_t kOffQ = (size_t)kWarps * kRing;  // two pieces' queries, when they lie in shared memory
+    static constexpr size_t kSmem = kOffQ + (kSharedQ ? 2 * 8 * NB * D * 2 : 0);
 };
 
 DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
@@ -435,24 +439,40 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
         if (more && tid == 0) s_piece[1] = z;
     }
     __syncthreads();
-    // Q^T as the second operand: lane holds column lane / 4, dimensions 2 (lane % 4) + {0, 1} (+ 8)
-    uint32_t qf[NB][KK][2];
-    auto load_q = [&](const Piece& z) {
+    // Q^T as the second operand: lane holds column lane / 4, dimensions 2 (lane % 4) + {0, 1} (+ 8); in shared
+    // memory two pieces' worth, [piece % 2][KK][NB][lane] (a piece's is seen after the meeting before it)
+    uint32_t qf[C::kSharedQ ? 1 : NB][C::kSharedQ ? 1 : KK][2];
+    uint2* const q_shared = reinterpret_cast<uint2*>(smem + C::kOffQ);
+    auto load_q = [&](const Piece& z, int p) {
+        if constexpr (C::kSharedQ) {
+            for (int i = tid; i < KK * NB * 32; i += kThreads) {
+                const int l = i & 31, nb = (i >> 5) % NB, kk = (i >> 5) / NB;
+                const bool ok = nb * 8 + l / 4 < z.n_rows;
+                const int r = z.row0 + nb * 8 + (ok ? l / 4 : 0);
+                const int qi = r / a.group;
+                const uint16_t* src = a.q + ((int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (r - qi * a.group)) * D + (l & 3) * 2 + kk * 16;
+                q_shared[(p & 1) * (KK * NB * 32) + i] =
+                    ok ? make_uint2(*reinterpret_cast<const uint32_t*>(src), *reinterpret_cast<const uint32_t*>(src + 8))
+                       : make_uint2(0u, 0u);
+            }
+        } else {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            const bool ok = nb * 8 + lane / 4 < z.n_rows;
-            const int r = z.row0 + nb * 8 + (ok ? lane / 4 : 0);
-            const int qi = r / a.group;
-            const uint16_t* src = a.q + ((int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (r - qi * a.group)) * D + (lane & 3) * 2;
+            for (int nb = 0; nb < NB; ++nb) {
+                const bool ok = nb * 8 + lane / 4 < z.n_rows;
+                const int r = z.row0 + nb * 8 + (ok ? lane / 4 : 0);
+                const int qi = r / a.group;
+                const uint16_t* src = a.q + ((int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (r - qi * a.group)) * D + (lane & 3) * 2;
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                qf[nb][kk][0] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
-                qf[nb][kk][1] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
+                for (int kk = 0; kk < KK; ++kk) {
+                    qf[nb][kk][0] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
+                    qf[nb][kk][1] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
+                }
             }
         }
     };
-    load_q(s_piece[0]);
+    load_q(s_piece[0], 0);
     fill(S - 1);
+    if constexpr (C::kSharedQ) __syncthreads();
 
     const int k_row = (lane & 7) + ((lane >> 3) & 1) * 8, k_col = (lane >> 4) & 1;
     const int v_row = (lane & 7) + ((lane >> 4) & 1) * 8, v_col = (lane >> 3) & 1;
@@ -520,7 +540,14 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                         uint32_t kf[4];
                         ldmatrix4(kf, st + (uint32_t)(kb * 16 + k_row) * (D * 2) + (uint32_t)(((kk * 2 + k_col) ^ (lane & 7)) * 16));
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) mma(c[kb][nb][kk & 1], kf, qf[nb][kk][0], qf[nb][kk][1]);
+                        for (int nb = 0; nb < NB; ++nb) {
+                            if constexpr (C::kSharedQ) {
+                                const uint2 q = q_shared[((place & 1) * KK + kk) * (NB * 32) + nb * 32 + lane];
+                                mma(c[kb][nb][kk & 1], kf, q.x, q.y);
+                            } else {
+                                mma(c[kb][nb][kk & 1], kf, qf[nb][kk][0], qf[nb][kk][1]);
+                            }
+                        }
                     }
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
@@ -627,7 +654,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                 }
             }
         }
-        if (more) load_q(s_piece[(place + 1) & 3]);   // on its way while the warps meet
+        if (more) load_q(s_piece[(place + 1) & 3], place + 1);   // on its way while the warps meet
         __syncthreads();
         const Piece z = s_piece[place];
         const int64_t slot = (int64_t)blockIdx.x * 2 + (z.starts ? 1 : 0);
