@@ -2,7 +2,8 @@
 
 The hot path (per-position softmax / entropy / argmax / Gumbel-max sample, entropy-bound
 acceptance, renoise, convergence, and the self-conditioning feedback on tcgen05 tensor cores)
-lives in ``libdg.so`` behind the C ABI in ``include/dg.h``; this package is its thin Python
+lives in ``libdg.so`` behind the C ABI in ``include/dg.h``, with the serving calls around it (a
+paged key / value cache, attention over it, edited logits); this package is its thin Python
 binding (``_native``), the in-tree build (``build``) and the seeded input generator
 (``synth``).
 """

@@ -28,6 +28,12 @@
 //               O is rescaled in TMEM (tcgen05.ld, multiply, tcgen05.st) after the last P V.
 //               At the end O / l goes out in bf16 with the row's lse.
 // Only key tiles holding an allowed key for some query of the tile are visited.
+//
+// The same kernel serves dg_paged_attention's calls with many query rows (k_attention<D, true>): key and
+// value tiles come page by page, and its set-up runs beside the plan kernel.  Its MMAs are issued by the elected
+// lane of a uniform warp.  8 canvases of 256 queries over 2.3k keys, 16 query over 8 key heads of 128: 50 us,
+// 770 TFLOP/s; 32 of them over 4k keys 173 us, 970 TFLOP/s (the first has 256 items for 304 CTAs, so half the
+// SMs work two while the others work one; per tile the softmax's chain of dependent steps bounds both).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

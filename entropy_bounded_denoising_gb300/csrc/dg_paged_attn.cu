@@ -2,21 +2,29 @@
 //
 // With few query rows the keys and values are read once and each value is used for a handful of
 // multiplications, so the call is bound by memory.  A row here is one (query, query head); the rows that
-// share a key head (Hq / Hkv of every query) make one item of up to 8 NB rows, and an item visits
-// the 64-key tiles that some query of its sequence may see.  All tiles of all items, in order,
-// form one line that is cut into equal runs, one for each of a fixed number of resident CTAs (as many as
-// the SMs hold): every CTA streams the same number of keys whatever the lengths are, and a
-// long sequence is split over as many CTAs as its share of the line takes.  A run's first and last items
-// may be pieces; pieces go to the workspace as (maximum, sum, unnormalised output) and a second
-// kernel joins them in the order of the line.
+// share a key head (Hq / Hkv of every query) make items of 8 NB rows (8, or 16 when a call's do not fit 8),
+// and an item visits the key tiles that some query of its sequence may see.  All tiles of all items, in
+// order, form one line that is cut into equal runs, one for each of a fixed number of resident CTAs (as many
+// as the SMs hold): every CTA streams the same number of keys whatever the lengths are, and a long sequence
+// is split over as many CTAs as its share of the line takes.  A run's first and last items may be
+// pieces; pieces go to the workspace as (maximum, sums, unnormalised output) and a second kernel joins
+// them in the order of the line.
 //
-// Within a CTA each warp owns 16 keys of a tile and runs on its own: its own ring of stages filled
-// by cp.async, its own running maximum and sum; warps meet only at the end of an item.  The
-// products are taken transposed, S^T = K Q^T and O^T = V^T P^T, with keys (or
-// dimensions) as the 16 rows of mma.m16n8k16 and the query rows as its 8 columns: eight rows fill the
-// instruction, and P^T comes out of the first product's layout by two 8 x 8 register transposes.
-// (The warp instruction, not tcgen05: at 8 rows the products need a few percent of either,
-// and a tile of TMEM would only add a round trip between the two products.)
+// Within a CTA each warp owns 16 or 32 keys of a tile and runs on its own: its own ring of stages filled by
+// cp.async (a step's keys and values each, past the end of a piece into the next one), its own running
+// maximum and sums; warps meet only at the end of a piece.  The products are taken transposed, S^T = K Q^T
+// and O^T = V^T P^T, with keys (or dimensions) as the 16 rows of mma.m16n8k16 and the query rows as its 8
+// columns: eight rows fill the instruction, and P^T comes out of the first product's layout by two 8 x 8
+// register transposes.  (The warp instruction, not tcgen05: at 8 rows the products need a few percent of
+// either -- the tensor pipe is 9 % busy over 8k keys -- and a tile of TMEM would only add a round trip between
+// the two products.)
+//
+// Measured: 64 tokens over up to 8k keys, 8 key heads of 128: 223 us, 6.6 TB/s, 97 % of the rate of a copy;
+// one token over 128k keys, 4 key heads of 256: 88 us, 90 %.  Short of that: one sequence over 1k keys takes
+// 7.9 us, two launches and five reads that wait for one another (lengths, pages, keys; list, pieces); 250
+// windows of 1000 keys at 8 heads of 64 take 97.5 us, 76 %, because tokens of heads of 64 side by side are read
+// in pieces of 128 bytes (5.6 TB/s where heads side by side give 6.5), and items of few keys cost a CTA their
+// latency: 1288 items of 3 keys, heads of 256, 35 us.
 #include <cuda_runtime.h>
 
 #include <math.h>
