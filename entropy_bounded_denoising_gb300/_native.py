@@ -29,7 +29,7 @@ _PARAM_FMT = "<fffiiiiII"
 PARAM_BYTES = struct.calcsize(_PARAM_FMT)   # 36, sizeof(dg_canvas_params)
 
 _lib = None
-_bind = None   # dg_bind.so, connected to _lib
+_bind = None   # the dg_bind module, connected to _lib
 
 
 class _PagedKV(ctypes.Structure):   # dg_paged_kv
@@ -50,7 +50,7 @@ def library_path() -> str:
 
 
 def load(path: str | None = None):
-    """Load libdg.so and dg_bind.so (built in-tree).  Raises if either is missing."""
+    """Load libdg.so and its dg_bind module (built in-tree).  Raises if either is missing."""
     global _lib, _bind
     if _lib is not None:
         return _lib
@@ -433,7 +433,7 @@ def dg_attention(q, k, v, o, cu_q, cu_kv, causal, max_q_len: int, *, lse=None, w
     return rc
 
 
-# The serving calls below are made once a token: dg_bind.so checks and marshals their arguments, because a
+# The serving calls below are made once a token: the dg_bind module checks and marshals their arguments, because a
 # call of a few microseconds on the device waits for the host.
 def _serving():
     if _bind is None:

@@ -1,7 +1,7 @@
 """Build libdg.so (the CUDA kernels behind include/dg.h) in-tree for sm_103a.
 
 Each translation unit is compiled by its own nvcc process, in parallel, then linked into
-``entropy_bounded_denoising_gb300/_build/libdg.so``; beside it ``dg_bind.so``, the serving calls'
+``entropy_bounded_denoising_gb300/_build/libdg.so``; beside it ``dg_bind-*.so``, the serving calls'
 Python module (host code against PyTorch's headers).  Objects are rebuilt only when a source or
 header is newer than the libraries.
 """
@@ -21,7 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libdg.so")
-BIND = os.path.join(OUT, "dg_bind.so")
+BIND = os.path.join(OUT, f"dg_bind-{torch.__version__}-{sys.implementation.cache_tag}.so")   # of one PyTorch and Python
 BIND_SRC = os.path.join(CSRC, "dg_bind.cpp")
 TORCH = os.path.dirname(os.path.abspath(torch.__file__))
 HEADER = os.path.join(ROOT, "include", "dg.h")
