@@ -22,9 +22,8 @@
 // Measured: 64 tokens over up to 8k keys, 8 key heads of 128: 223 us, 6.6 TB/s, 97 % of the rate of a copy;
 // one token over 128k keys, 4 key heads of 256: 88 us, 90 %.  Short of that: one sequence over 1k keys takes
 // 7.9 us, two launches and five reads that wait for one another (lengths, pages, keys; list, pieces); 250
-// windows of 1000 keys at 8 heads of 64 take 97.5 us, 76 %, because tokens of heads of 64 side by side are read
-// in pieces of 128 bytes (5.6 TB/s where heads side by side give 6.5), and items of few keys cost a CTA their
-// latency: 1288 items of 3 keys, heads of 256, 35 us.
+// windows of 1000 keys at 8 heads of 64 take 85 us, 87 %, of which start and join are 8; and items of few keys
+// cost a CTA their latency: 1288 items of 3 keys, heads of 256, 35 us.
 #include <cuda_runtime.h>
 
 #include <math.h>
@@ -336,10 +335,13 @@ struct Walk {
     }
 };
 
-template <int D, int NB>
+// Pair: two neighbouring key heads of D / 2 as one of D.  Every query row is multiplied with the keys of
+// both and takes the scores of its own; its output is its own half.  Half of the products go to waste, of which
+// there are plenty; there are half as many items, and where tokens lie side by side the reads are twice as wide.
+template <int D, int NB, bool Pair>
 __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kCtasPerSm) k_paged_split(const SplitArgs a) {
     using C = SplitCfg<D, NB>;
-    constexpr int Rows = 8 * NB;
+    constexpr int Rows = 8 * NB, HD = Pair ? D / 2 : D;   // HD: of a query head
     constexpr int S = C::kStages, Tile = C::kTileKeys, kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int KB = C::kStep / 16;       // 16-key blocks of a step
     constexpr int KK = D / 16;              // 16-dimension blocks of a head
@@ -380,7 +382,8 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
     };
     auto open = [&](const Piece& z) {
         in.table = a.kv.page_table + (int64_t)z.s * a.kv.max_pages;
-        in.head_at = z.hk * a.kv.head_stride + ch * 8;
+        in.head_at = Pair ? (z.hk * 2 + ch / (Chunks / 2)) * a.kv.head_stride + ch % (Chunks / 2) * 8
+                          : z.hk * a.kv.head_stride + ch * 8;
         in.klo = z.klo;
         in.khi = z.khi;
         in.key0 = z.tile0 * Tile + warp * C::kStep;
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
     __syncthreads();
     // Q^T as the second operand: lane holds column lane / 4, dimensions 2 (lane % 4) + {0, 1} (+ 8); in shared
     // memory two pieces' worth, [piece % 2][KK][NB][lane] (a piece's is seen after the meeting before it)
-    uint32_t qf[C::kSharedQ ? 1 : NB][C::kSharedQ ? 1 : KK][2];
+    uint32_t qf[C::kSharedQ ? 1 : NB][C::kSharedQ ? 1 : HD / 16][2];
     uint2* const q_shared = reinterpret_cast<uint2*>(smem + C::kOffQ);
     auto load_q = [&](const Piece& z, int p) {
         if constexpr (C::kSharedQ) {
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                 const bool ok = nb * 8 + l / 4 < z.n_rows;
                 const int r = z.row0 + nb * 8 + (ok ? l / 4 : 0);
                 const int qi = r / a.group;
-                const uint16_t* src = a.q + ((int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (r - qi * a.group)) * D + (l & 3) * 2 + kk * 16;
+                const uint16_t* src = a.q + ((int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (r - qi * a.group)) * HD + (l & 3) * 2 + kk * 16;
                 q_shared[(p & 1) * (KK * NB * 32) + i] =
                     ok ? make_uint2(*reinterpret_cast<const uint32_t*>(src), *reinterpret_cast<const uint32_t*>(src + 8))
                        : make_uint2(0u, 0u);
@@ -469,9 +472,9 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                 const bool ok = nb * 8 + lane / 4 < z.n_rows;
                 const int r = z.row0 + nb * 8 + (ok ? lane / 4 : 0);
                 const int qi = r / a.group;
-                const uint16_t* src = a.q + ((int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (r - qi * a.group)) * D + (lane & 3) * 2;
+                const uint16_t* src = a.q + ((int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (r - qi * a.group)) * HD + (lane & 3) * 2;
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
+                for (int kk = 0; kk < HD / 16; ++kk) {
                     qf[nb][kk][0] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
                     qf[nb][kk][1] = ok ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
                 }
@@ -490,6 +493,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
         const int klo = s_piece[place].klo, khi = s_piece[place].khi, steps = s_piece[place].steps;
         const int key0 = s_piece[place].tile0 * Tile + warp * C::kStep;
         int rlo[NB][2], rhi[NB][2], all_lo, all_hi;
+        bool upper[NB][2];   // of the pair's second head
         {
             const Piece& z = s_piece[place];
             int unused;
@@ -497,8 +501,9 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = min(nb * 8 + (lane & 3) * 2 + e, z.n_rows - 1);
-                    key_range(z.pos0 + (z.row0 + r) / a.group, z.kl, a.window, z.causal, rlo[nb][e], rhi[nb][e]);
+                    const int r = min(nb * 8 + (lane & 3) * 2 + e, z.n_rows - 1), qi = (z.row0 + r) / a.group;
+                    key_range(z.pos0 + qi, z.kl, a.window, z.causal, rlo[nb][e], rhi[nb][e]);
+                    if constexpr (Pair) upper[nb][e] = z.row0 + r - qi * a.group >= a.group / 2;
                 }
             key_range(z.pos0 + (z.row0 + z.n_rows - 1) / a.group, z.kl, a.window, z.causal, all_lo, unused);
             key_range(z.pos0 + z.row0 / a.group, z.kl, a.window, z.causal, unused, all_hi);
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
             if (j0 > khi || j0 + C::kStep - 1 < klo) continue;   // no key of the item
             float x[KB][NB][4];   // S^T: [key lane / 4 (+ 8 for 2, 3)][row 2 (lane % 4) + (0, 1)]
             {
-                float c[KB][NB][2][4];   // even and odd 16-dimension blocks apart: two chains a block of keys
+                float c[KB][NB][2][4];   // even and odd 16-dimension blocks (a pair: its heads) apart: two chains a block of keys
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -553,7 +558,8 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                                 const uint2 q = q_shared[((place & 1) * KK + kk) * (NB * 32) + nb * 32 + lane];
                                 mma(c[kb][nb][kk & 1], kf, q.x, q.y);
                             } else {
-                                mma(c[kb][nb][kk & 1], kf, qf[nb][kk][0], qf[nb][kk][1]);
+                                constexpr int QK = HD / 16;
+                                mma(c[kb][nb][Pair ? kk / QK : kk & 1], kf, qf[nb][kk % QK][0], qf[nb][kk % QK][1]);
                             }
                         }
                     }
@@ -562,7 +568,9 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[kb][nb][e] = (c[kb][nb][0][e] + c[kb][nb][1][e]) * a.scale_log2;
+                        for (int e = 0; e < 4; ++e)
+                            x[kb][nb][e] = (Pair ? (upper[nb][e & 1] ? c[kb][nb][1][e] : c[kb][nb][0][e])
+                                                 : c[kb][nb][0][e] + c[kb][nb][1][e]) * a.scale_log2;
             }
             if (j0 < all_lo || j0 + C::kStep - 1 > all_hi) {
 #pragma unroll
@@ -666,8 +674,10 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
         __syncthreads();
         const Piece z = s_piece[place];
         const int64_t slot = (int64_t)blockIdx.x * 2 + (z.starts ? 1 : 0);
-        for (int i = tid; i < z.n_rows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+        for (int i = tid; i < z.n_rows * (HD / 4); i += kThreads) {
+            const int r = i / (HD / 4), d = (i - r * (HD / 4)) * 4;
+            const int rr = z.row0 + r, qi = rr / a.group, head = rr - qi * a.group;
+            const int col = Pair && head >= a.group / 2 ? HD + d : d;   // of the rows in shared memory
             float M = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
@@ -679,21 +689,20 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
                 L += s_l[w][r].x * f;
                 Lr += s_l[w][r].y * f;
                 const float4 v = *reinterpret_cast<const float4*>(smem + (size_t)w * C::kRing + met +
-                                                                  ((size_t)r * D + (d ^ (((r >> 1) & 3) << 3))) * 4);
+                                                                  ((size_t)r * D + (col ^ (((r >> 1) & 3) << 3))) * 4);
                 o.x += v.x * f;
                 o.y += v.y * f;
                 o.z += v.z * f;
                 o.w += v.w * f;
             }
             if (z.starts && z.ends) {
-                const int rr = z.row0 + r, qi = rr / a.group;
-                const int64_t out = (int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + (rr - qi * a.group);
+                const int64_t out = (int64_t)(z.q0 + qi) * a.Hq + z.hk * a.group + head;
                 const float inv = Lr > 0.f ? 1.f / Lr : 0.f;
-                *reinterpret_cast<uint2*>(a.o + out * D + d) =
+                *reinterpret_cast<uint2*>(a.o + out * HD + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
                 if (d == 0 && a.lse) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;  // (a NaN stays one)
             } else {
-                *reinterpret_cast<float4*>(a.part_o + (slot * Rows + r) * D + d) = o;
+                *reinterpret_cast<float4*>(a.part_o + (slot * Rows + r) * HD + d) = o;
                 if (d == 0) a.part_ml[slot * Rows + r] = make_float4(M, L, Lr, 0.f);
             }
         }
@@ -810,6 +819,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Rows of an item: 8 when the call's queries and a group fit them, else 16.
 int item_rows(int32_t max_q_len, int32_t group) { return (int64_t)max_q_len * group <= 8 ? 8 : 16; }
 
+// Whether two key heads of 64 go as one of 128: when the rows of both fit eight.  250 windows of 1000 keys, 8 / 8
+// heads, 97.5 us head by head and 84.9 in pairs; 64 requests over 8k keys 130 / 113 (tokens side by side), 117 / 111
+// (heads side by side); 200 over 300 keys, 16 / 8 heads, 39.7 / 28.0; 256 over 60 keys 25.2 / 16.8; one over 1k keys
+// 7.9 / 7.3.  Not with 16 rows (32 requests of 8 queries over 3k keys 29.3 / 30.2, 26 of 8 over 54 keys 6.8 / 7.4,
+// though 24.5 / 21.0 for 200 with 8 query heads a key head over 300), nor heads of 128 as 256 (64 over 8k keys 223 /
+// 221, but 256 over 60 keys 27.6 / 28.4, one over 1k 7.9 / 8.6).
+bool in_pairs(int32_t max_q_len, int32_t group, int32_t Hkv, int32_t D) {
+    return D == 64 && Hkv % 2 == 0 && (int64_t)max_q_len * group * 2 <= 8;
+}
+
 // Whether a call takes this file's path or dg_attention's query tiles over pages (dg_attn.cu).  An item here
 // (up to 16 rows of a key head) and a tile there (128 queries of a query head) pass over the keys in about the same
 // time, 75 to 82 us for 256 of them on 4k keys at heads of 128, and tiles below the number of CTAs take
@@ -829,8 +848,9 @@ size_t split_bytes(int rows, int32_t D) {
     return (size_t)kMaxCtas * 32 + (size_t)kMaxCtas * 2 * rows * ((size_t)D + 4) * 4;
 }
 
-template <int D, int NB>
+template <int D, int NB, bool Pair = false>
 dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
+    constexpr int HD = Pair ? D / 2 : D;
     using C = SplitCfg<D, NB>;
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
@@ -839,16 +859,16 @@ dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return DG_ERR_CUDA;
     if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
-        if (cudaFuncSetAttribute(k_paged_split<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
+        if (cudaFuncSetAttribute(k_paged_split<D, NB, Pair>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
             cudaSuccess)
             return DG_ERR_CUDA;
         if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     const unsigned grid = (unsigned)std::min(sms * C::kCtasPerSm, kMaxCtas);
-    cudaError_t e = dghost::launch_pdl(k_paged_split<D, NB>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, a);
+    cudaError_t e = dghost::launch_pdl(k_paged_split<D, NB, Pair>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, a);
     dghost::count_launch();
     if (e != cudaSuccess) return DG_ERR_CUDA;
-    e = dghost::launch_pdl(k_paged_join<D, NB>, dim3(grid, D / 64), dim3(kJoinThreads), 0, stream, a);
+    e = dghost::launch_pdl(k_paged_join<HD, NB>, dim3(grid, HD / 64), dim3(kJoinThreads), 0, stream, a);
     dghost::count_launch();
     return dghost::cuda_status(e);
 }
@@ -903,6 +923,11 @@ extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* ca
     a.part_ml = reinterpret_cast<float4*>(a.part_o + (size_t)kMaxCtas * 2 * rows * D);
     a.status = dghost::status_word();
     cudaStream_t st = (cudaStream_t)stream;
+    if (in_pairs(max_q_len, a.group, Hkv, D)) {
+        a.Hkv /= 2;
+        a.group *= 2;
+        return launch_split<128, 1, true>(a, st);
+    }
     if (D == 64) return rows == 8 ? launch_split<64, 1>(a, st) : launch_split<64, 2>(a, st);
     if (D == 128) return rows == 8 ? launch_split<128, 1>(a, st) : launch_split<128, 2>(a, st);
     return rows == 8 ? launch_split<256, 1>(a, st) : launch_split<256, 2>(a, st);

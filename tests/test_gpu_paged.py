@@ -423,6 +423,29 @@ def test_attention_nan_queries_stay_in_their_rows(rows):
     ref.check_attention(b, o, lse)
 
 
+@pytest.mark.parametrize("rows,D,Hq,Hkv", [(1, 64, 8, 8), (2, 64, 8, 4), (1, 64, 3, 3), (8, 64, 2, 2), (1, 128, 8, 4), (300, 64, 16, 8)])
+def test_attention_heads_do_not_meet(rows, D, Hq, Hkv):
+    """NaN keys and infinite values that one key head may see: its query heads alone show them."""
+    b = ref.Batch([(rows, 700, 0), (1, 90, 1)], Hq, Hkv, D, 16, seed=rows + D).fill_keys()
+    want, lse = _attend(b)
+    bad, group = Hkv - 1 if Hkv == 3 else 1, Hq // Hkv
+    at = b.slots(0, [0, 100, 699])
+    b.k_cache[at[0], at[1], bad] = math.nan
+    b.v_cache[at[0], at[1], bad] = math.inf
+    o, l = _attend_only(b)
+    mine = slice(bad * group, (bad + 1) * group)
+    assert not torch.isfinite(o[:rows, mine]).any() and torch.isnan(l[:rows, mine]).all()
+    o[:rows, mine], l[:rows, mine] = want[:rows, mine], lse[:rows, mine]
+    b.k_cache[at[0], at[1], bad] = 0
+    for s in range(2):   # the other heads against fp64
+        sl = slice(int(b.cu[s]), int(b.cu[s + 1]))
+        k, v = (t.nan_to_num(0, 0, 0) for t in b.keys(s))
+        ro, rl, bound, lbound = ref.attention(b.q[sl], k, v, bool(b.causal[s]), -1, D ** -0.5)
+        clean = [h for h in range(Hq) if s or not mine.start <= h < mine.stop]
+        assert ((o[sl].double() - ro).abs() <= bound)[:, clean].all()
+        assert ((l[sl].double() - rl).abs() <= lbound)[:, clean].all()
+
+
 def test_attention_repeats_bit_for_bit():
     for seqs in (TOKENS * 5, [(1, 50000, 1)], MIXED):
         b = ref.Batch(seqs, 8, 4, 128, 16, seed=4).fill_keys()
