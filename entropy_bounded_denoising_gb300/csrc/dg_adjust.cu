@@ -10,9 +10,9 @@
 // Bound by memory: in place only vectors with an edited or excluded token are touched, and a vector that is
 // excluded whole is written without being read.  8 canvases of 256 positions, fp32, 152k tokens, half of them
 // excluded: 283 us; nearly every vector has an allowed token, so 0.95 GB are read and 0.88 written, 270 us
-// at a copy's rate.  A grammar that leaves 1 % of 262k bf16 tokens, in place: 255 us for 1.01 GB written and
-// 0.55 read (a vector with an allowed token is read, and DRAM gives 128 bytes around it; writing only the
-// excluded tokens of such vectors without reading them took 420).  One canvas over 32k tokens: 9.3 us, of
+// at a copy's rate.  A grammar that leaves 1 % of 262k bf16 tokens, in place: 242 us for 1.01 GB written and
+// 0.33 read (a vector with an allowed token is read, and 64 bytes come with it; writing only the excluded
+// tokens of such vectors without reading them took 420).  One canvas over 32k tokens: 9.3 us, of
 // which a copy of the logits takes 6.6 and the mask alone 7.5; the rest is the wait for the lists.
 #include <cuda_runtime.h>
 
@@ -50,6 +50,15 @@ struct AdjustArgs {
 DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
     uint32_t v;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+
+// 16 bytes, fetching no more than the 64 around them: a mask that leaves few tokens has few vectors read, and 128
+// around each were half of the row (1 % of 262k bf16 tokens left, in place: 256 us without the hint, 242 with it;
+// where most are read it makes no difference).
+DG_DEVINL uint4 load16(const unsigned char* p) {
+    uint4 v;
+    asm volatile("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
             keep[u] = (Bytes == 4 ? next[u] >> (v0 & 4) : next[u]) & mine;
             x[u] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
             if (r + u < rows && keep[u] != 0 && !(only_mixed && keep[u] == mine))
-                x[u] = *reinterpret_cast<const uint4*>(src + u * a.ld_bytes);
+                x[u] = load16(src + u * a.ld_bytes);
         }
     };
     const int end = min(kSlice, a.V - slice0);
