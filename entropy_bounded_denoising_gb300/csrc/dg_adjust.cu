@@ -10,7 +10,7 @@
 // Bound by memory: in place only vectors with an edited or excluded token are touched, and a vector that is
 // excluded whole is written without being read.  8 canvases of 256 positions, fp32, 152k tokens, half of them
 // excluded: 283 us; nearly every vector has an allowed token, so 0.95 GB are read and 0.88 written, 270 us
-// at a copy's rate.  A grammar that leaves 1 % of 262k bf16 tokens, in place: 242 us for 1.01 GB written and
+// at a copy's rate.  A grammar that leaves 1 % of 262k bf16 tokens, in place: 222 us for 1.01 GB written and
 // 0.33 read (a vector with an allowed token is read, and 64 bytes come with it; writing only the excluded
 // tokens of such vectors without reading them took 420).  One canvas over 32k tokens: 9.3 us, of
 // which a copy of the logits takes 6.6 and the mask alone 7.5; the rest is the wait for the lists.
@@ -25,7 +25,11 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;   // rows in flight a thread
+constexpr int kBlocksPerSm = 4;
+// Rows in flight a thread: the registers of the lists' addends hold four rows more when a call gives no lists.
+// Masks alone, in place, bf16, 1 % of 250k tokens left: 277 us with four, 260 with six, 238 with eight (half of
+// 131k fp32 tokens left: 318, 320, 327).
+constexpr int unroll_of(bool lists) { return lists ? 4 : 8; }
 constexpr int kMaxRows = 64; // rows of a block, at most
 constexpr int kEarly = 2;    // entries of each list that a thread reads before anything else
 
@@ -55,10 +59,11 @@ DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
 
 // 16 bytes, fetching no more than the 64 around them: a mask that leaves few tokens has few vectors read, and 128
 // around each were half of the row (1 % of 262k bf16 tokens left, in place: 256 us without the hint, 242 with it;
-// where most are read it makes no difference).
+// where most are read it makes no difference).  Not volatile: a row is read before its own store and after no
+// other's.
 DG_DEVINL uint4 load16(const unsigned char* p) {
     uint4 v;
-    asm volatile("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 
@@ -100,11 +105,16 @@ DG_DEVINL void exclude(uint4& y, uint32_t keep, const uint2* expand) {
 }
 
 // A vector's first n tokens (all but in a row's last vector: nothing past column V is written).
-template <int Bytes>
+template <int Bytes, bool Lists>
 DG_DEVINL void store(unsigned char* at, const uint4& y, int n) {
     constexpr int PerVec = 16 / Bytes;
     if (n == PerVec) {
-        *reinterpret_cast<uint4*>(at) = y;
+        // (a plain store of fp32 without lists was compiled into four of 4 bytes: 422 us for 204; with lists it is
+        // the quicker one, 9.2 us for 9.7 on one canvas)
+        if constexpr (Lists)
+            *reinterpret_cast<uint4*>(at) = y;
+        else
+            __stcg(reinterpret_cast<uint4*>(at), y);
         return;
     }
 #pragma unroll
@@ -118,15 +128,17 @@ DG_DEVINL void store(unsigned char* at, const uint4& y, int n) {
     }
 }
 
-// Bytes: 2 (bf16) or 4 (fp32) a logit; PerVec tokens in 16 bytes.
-template <int Bytes>
-__global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
+// Bytes: 2 (bf16) or 4 (fp32) a logit; PerVec tokens in 16 bytes.  Lists: the call gives a history or biases.
+template <int Bytes, bool Lists>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustArgs a) {
+    constexpr int kUnroll = unroll_of(Lists);
     constexpr int PerVec = 16 / Bytes;
     constexpr int kSlice = kThreads * PerVec;   // tokens of a block
-    __shared__ __align__(16) int32_t n_hist[kSlice];       // occurrences in the history
-    __shared__ __align__(16) int32_t n_bias[kSlice];       // entries in the bias list
-    __shared__ int32_t first_bias[kSlice];                 // the first of them
-    __shared__ float one_bias[kSlice];                     // and the value when it is the only one
+    constexpr int kCounts = Lists ? kSlice : 4;
+    __shared__ __align__(16) int32_t n_hist[kCounts];       // occurrences in the history
+    __shared__ __align__(16) int32_t n_bias[kCounts];       // entries in the bias list
+    __shared__ int32_t first_bias[kCounts];                 // the first of them
+    __shared__ float one_bias[kCounts];                     // and the value when it is the only one
     __shared__ int32_t row_mask[kMaxRows];
     __shared__ uint2 expand[16];
     constexpr uint32_t kNegInf = Bytes == 2 ? 0xff80ff80u : 0xff800000u;
@@ -144,12 +156,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
     const uint32_t flags = a.params[c].flags;
     int h0 = 0, h1 = 0, b0 = 0, b1 = 0;
     dg_penalties pen = {1.f, 0.f, 0.f};
-    if (a.history) {
+    if (Lists && a.history) {
         h0 = a.cu_history[c];
         h1 = a.cu_history[c + 1];
         pen = a.penalties[c];
     }
-    if (a.bias_tokens) {
+    if (Lists && a.bias_tokens) {
         b0 = a.cu_bias[c];
         b1 = a.cu_bias[c + 1];
     }
@@ -172,12 +184,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
     if (Bytes == 2 && tid < 16)
         expand[tid] = make_uint2(((tid & 1) ? 0xffffu : 0u) | ((tid & 2) ? 0xffff0000u : 0u),
                                  ((tid & 4) ? 0xffffu : 0u) | ((tid & 8) ? 0xffff0000u : 0u));
-    const bool listed = h1 > h0 || b1 > b0;
+    const bool listed = Lists && (h1 > h0 || b1 > b0);
     // a thread's first entries of the lists are on their way meanwhile
     int32_t early_h[kEarly], early_b[kEarly];
     float early_v[kEarly];
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k) {
+    for (int k = 0; Lists && k < kEarly; ++k) {
         const int64_t i = (int64_t)h0 + tid + k * kThreads, j = (int64_t)b0 + tid + k * kThreads;
         early_h[k] = i < h1 ? a.history[i] : -1;
         early_b[k] = j < b1 ? a.bias_tokens[j] : -1;
@@ -203,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
     const int64_t mask_pitch = a.mask_stride * 4;
     const unsigned char* src = a.x + (c * a.L + r0) * a.ld_bytes + (int64_t)v0 * Bytes;
     unsigned char* dst = a.out + (c * a.L + r0) * a.ld_out_bytes + (int64_t)v0 * Bytes;
+    asm volatile("" : "+l"(src));   // no read of a row moves up past pdl_wait
     uint32_t keep[kUnroll], next[kUnroll];   // allowed tokens of the vector, for kUnroll rows
     uint4 x[kUnroll];
     auto masks_of = [&](int r) {             // row_mask is -1 past the last row
@@ -284,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
         }
         edited |= penalised;
     }
-    const uint32_t any = __reduce_or_sync(0xffffffffu, edited);
+    const uint32_t any = Lists ? __reduce_or_sync(0xffffffffu, edited) : 0u;
     if (n_mine == 0) return;
     const bool still = in_place && edited == 0;   // nothing to write where nothing is excluded
     const float down = 1.f / pen.repetition;
@@ -295,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_adjust(const AdjustArgs a) {
             if (r + u >= rows || (still && keep[u] == mine)) continue;
             if (any) edit<Bytes>(x[u], any, edited, penalised, down, pen.repetition, add);
             exclude<Bytes>(x[u], keep[u], expand);
-            store<Bytes>(dst + u * a.ld_out_bytes, x[u], n_mine);
+            store<Bytes, Lists>(dst + u * a.ld_out_bytes, x[u], n_mine);
         }
         r += kUnroll;
         if (r >= rows) break;
@@ -355,12 +368,14 @@ extern "C" dg_status dg_adjust_logits(const void* logits, dg_dtype dtype, int64_
     if (sms <= 0) return DG_ERR_CUDA;
     const int64_t slice = kThreads * (16 / es), slices = (V + slice - 1) / slice;
     // rows of a block: up to 64, so that its lists are read for many rows, but few enough that the blocks
-    // fill the four places an SM has for them
-    const int64_t places = 4 * (int64_t)sms;
+    // fill the places an SM has for them
+    const bool lists = history || bias_tokens;
+    const int64_t places = kBlocksPerSm * (int64_t)sms;
     const int64_t rows = (slices * n_canvas * L + places - 1) / places;
-    a.rows = (int32_t)std::min<int64_t>(kMaxRows, (rows + kUnroll - 1) / kUnroll * kUnroll);
+    a.rows = (int32_t)std::min<int64_t>(kMaxRows, (rows + 3) / 4 * 4);
     const dim3 grid((unsigned)slices, (unsigned)((L + a.rows - 1) / a.rows), (unsigned)n_canvas);
-    const cudaError_t e = dghost::launch_pdl(es == 2 ? k_adjust<2> : k_adjust<4>, grid, dim3(kThreads), 0,
+    const cudaError_t e = dghost::launch_pdl(es == 2 ? (lists ? k_adjust<2, true> : k_adjust<2, false>)
+                                                     : (lists ? k_adjust<4, true> : k_adjust<4, false>), grid, dim3(kThreads), 0,
                                              (cudaStream_t)stream, a);
     dghost::count_launch();
     return dghost::cuda_status(e);
