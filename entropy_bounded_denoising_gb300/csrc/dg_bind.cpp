@@ -300,6 +300,7 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         if (a[9] != Py_None) {
             n_masks = THPVariable_Unpack(a[9]).size(0);
             words = THPVariable_Unpack(a[9]).size(1);
+            if (n_masks < 1 || words < 1) refuse(PyExc_ValueError, c.named("masks") + " must have rows and words");
         }
         const void* mi = c.whole(a[10], "mask_index", at::kInt, {n, L});
         if (L > INT32_MAX || n_masks > INT32_MAX) refuse(PyExc_ValueError, std::string(fn) + ": an extent is out of range");

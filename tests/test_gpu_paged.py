@@ -511,6 +511,35 @@ def test_attention_on_streams_and_in_graphs(q):
     ref.check_attention(b, o, lse)
 
 
+def test_calls_from_two_threads_at_once():
+    """Threads that append to their own caches and attend, each on its own stream, without workspaces."""
+    import threading
+    bs = [ref.Batch([(q, 1500 + 100 * q, 1)] * 5, 8, 4, 64, 16, seed=q).fill_keys() for q in (1, 3, 300)]
+    want = [_attend(b) for b in bs]
+    got, streams = [None] * 3, [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+
+    def run(i):
+        b = bs[i]
+        rows = torch.cat([torch.arange(kl - a, kl) for a, kl, _ in b.seqs])
+        at = b.table[torch.arange(5, device=DEV).repeat_interleave(b.seqs[0][0]), rows.to(DEV) // 16].long(), rows.to(DEV) % 16
+        with torch.cuda.stream(streams[i]):
+            k, v = b.k_cache[at], b.v_cache[at]      # what the cache holds: appended again, it stays the same
+            for _ in range(30):
+                dg.dg_kv_append(k, v, b.k_cache, b.v_cache, b.table, b.cu, b.kv_len)
+                got[i] = _attend_only(b)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert dg.dg_get_device_status() == 0
+    for (o, lse), (o0, l0) in zip(got, want):
+        assert torch.equal(o, o0) and torch.equal(lse, l0)
+
+
 def test_append_then_attend_step_by_step():
     """Tokens appended one by one and read back, as a decoding loop does, against the packed form."""
     n, Hq, Hkv, D, page, steps = 3, 4, 2, 64, 8, 20

@@ -161,6 +161,7 @@ def test_python_refuses_what_is_not_a_tensor_or_does_not_fit():
                            ((x, None), {}, TypeError), ((None, p), {}, TypeError), ((x, p), dict(V=1.5), TypeError),
                            ((x, p, x[:, :3]), {}, ValueError), ((x, p), dict(masks=i32(2), mask_index=i32(1, 4)), ValueError),
                            ((x, p), dict(masks=i32(1, 2), mask_index=i32(4)), ValueError),
+                           ((x, p), dict(masks=i32(0, 2), mask_index=i32(1, 4)), ValueError),
                            ((x, p), dict(history=i32(3), cu_history=i32(2), penalties=f32(3)), ValueError),
                            ((x, p), dict(history=i32(3).long(), cu_history=i32(2), penalties=f32(1, 3)), TypeError),
                            ((x, p), dict(bias_tokens=i32(3), bias_values=f32(2), cu_bias=i32(2)), ValueError)):
