@@ -731,13 +731,11 @@ __global__ void __launch_bounds__(SplitCfg<D, NB>::kThreads, SplitCfg<D, NB>::kC
 // A thread owns four dimensions of a row for every kGroups-th piece (a long context of one head is joined
 // from dozens: reading them one after another took most of the kernel); the groups add up in
 // shared memory in a fixed order.  The first pieces are on their way while the weights are worked out.
-constexpr int kJoinThreads = 512;
-
-template <int D, int NB>
+template <int D, int NB, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const SplitArgs a) {
     constexpr int Rows = 8 * NB;
     constexpr int kPlaces = Rows * 16;               // float4s of 64 dimensions of the rows
-    constexpr int kGroups = kJoinThreads / kPlaces;  // 4 or 2
+    constexpr int kGroups = kJoinThreads / kPlaces;  // 4, 2 or 1
     constexpr int kEarly = 4;                        // pieces a thread asks for before it knows their weights
     __shared__ float w[kMaxCtas][Rows];              // the pieces' maxima, then their weights
     __shared__ float s_l[Rows], s_lr[Rows], s_m[Rows];
@@ -868,7 +866,13 @@ dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
     cudaError_t e = dghost::launch_pdl(k_paged_split<D, NB, Pair>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, a);
     dghost::count_launch();
     if (e != cudaSuccess) return DG_ERR_CUDA;
-    e = dghost::launch_pdl(k_paged_join<HD, NB>, dim3(grid, HD / 64), dim3(kJoinThreads), 0, stream, a);
+    // Many items are joined from a few pieces each, if at all, and half the threads a block come and go sooner;
+    // few have many pieces.  42 items of 2 keys: 6.6 us with 512, 6.1 with 256; 256 of 5 drafts over 4k keys 65.1 /
+    // 64.0; 4 of 128k keys 86.9 / 87.5, 8 of 1k 7.1 / 7.4.
+    if (8 * (int64_t)a.n_seq * a.Hkv >= grid)
+        e = dghost::launch_pdl(k_paged_join<HD, NB, 256>, dim3(grid, HD / 64), dim3(256), 0, stream, a);
+    else
+        e = dghost::launch_pdl(k_paged_join<HD, NB, 512>, dim3(grid, HD / 64), dim3(512), 0, stream, a);
     dghost::count_launch();
     return dghost::cuda_status(e);
 }
