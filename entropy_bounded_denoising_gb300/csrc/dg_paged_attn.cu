@@ -19,7 +19,7 @@
 // either -- the tensor pipe is 9 % busy over 8k keys -- and a tile of TMEM would only add a round trip between
 // the two products.)
 //
-// Measured: 64 tokens over up to 8k keys, 8 key heads of 128: 223 us, 6.6 TB/s, 97 % of the rate of a copy;
+// Measured: 64 tokens over up to 8k keys, 8 key heads of 128: 221 us, 6.7 TB/s, 98 % of the rate of a copy;
 // one token over 128k keys, 4 key heads of 256: 88 us, 90 %.  Short of that: one sequence over 1k keys takes
 // 7.9 us, two launches and five reads that wait for one another (lengths, pages, keys; list, pieces); 250
 // windows of 1000 keys at 8 heads of 64 take 85 us, 87 %, of which start and join are 8; and items of few keys
