@@ -30,9 +30,10 @@
 // Only key tiles holding an allowed key for some query of the tile are visited.
 //
 // The same kernel serves dg_paged_attention's calls with many query rows (k_attention<D, true>): key and
-// value tiles come page by page, and its set-up runs beside the plan kernel.  Its MMAs are issued by the elected
-// lane of a uniform warp.  8 canvases of 256 queries over 2.3k keys, 16 query over 8 key heads of 128: 50 us,
-// 770 TFLOP/s; 32 of them over 4k keys 173 us, 970 TFLOP/s (the first has 256 items for 304 CTAs, so half the
+// value tiles come page by page, and its set-up runs beside the plan kernel, or the caller's last one when there
+// is no plan.  Its MMAs are issued by the elected
+// lane of a uniform warp.  8 canvases of 256 queries over 2.3k keys, 16 query over 8 key heads of 128: 46 us,
+// 850 TFLOP/s; 32 of them over 4k keys 173 to 181 us, 970 to 1000 TFLOP/s (the first has 256 items for 304 CTAs, so half the
 // SMs work two while the others work one; per tile the softmax's chain of dependent steps bounds both).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -275,7 +276,8 @@ DG_DEVINL void do_abort(AttnShared& sh, unsigned* status) {
 }
 
 // A work item as the roles use it.  With pages the list holds all of it, 32 bytes an item, so that a CTA's
-// first copies wait for one read and not for two.
+// first copies wait for one read and not for two; without a list (null) item i is tile i % max_q_tiles of
+// sequence i / max_q_tiles.
 struct Item {
     int s, t;      // sequence, query tile
     TileRange r;
@@ -284,6 +286,10 @@ struct Item {
 template <bool Paged>
 DG_DEVINL Item read_item(const AttnArgs& a, const int32_t* list, int64_t i) {
     if constexpr (Paged) {
+        if (!list) {
+            const int tiles = (a.max_q_len + kTile - 1) / kTile, s = (int)i / tiles;
+            return Item{s, (int)i - s * tiles, tile_range<true>(a, s, (int)i - s * tiles)};
+        }
         const int4 x = reinterpret_cast<const int4*>(list)[2 * i], y = reinterpret_cast<const int4*>(list)[2 * i + 1];
         return Item{x.x, x.y, range_of(a, x.y, x.z, x.w, 0, y.x, y.y != 0)};
     } else {
@@ -456,10 +462,21 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         dg::pdl_release();
         asm volatile("" : "+l"(list)::"memory");  // no read of the list moves up past the wait
     }
-    const int64_t n_work = (int64_t)list[0] * a.Hq;
-    const int32_t* items = list + kPlanHeader;
+    const bool direct = Paged && !list;   // without a list: one item a CTA, or none
+    int64_t n_work;
+    bool round_robin = true;
+    if (direct) {
+        const int tiles = (a.max_q_len + kTile - 1) / kTile, f = (int)blockIdx.x / a.Hq, s = f / tiles;
+        const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
+        if (threadIdx.x == 0 && (int)blockIdx.x == s * tiles * a.Hq && (!p.ok || p.ql > a.max_q_len))
+            dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+        n_work = p.ok && p.kl > 0 && (f - s * tiles) * kTile < p.ql ? (int64_t)blockIdx.x + 1 : 0;
+    } else {
+        n_work = (int64_t)list[0] * a.Hq;
+        round_robin = list[1] != 0;
+    }
+    const int32_t* items = direct ? nullptr : list + kPlanHeader;
     const int group = a.Hq / a.Hkv;
-    const bool round_robin = list[1] != 0;
     auto rr_item = [&](uint32_t k) -> int64_t {
         const int64_t w = (int64_t)blockIdx.x + (int64_t)k * gridDim.x;
         return w < n_work ? w : -1;
@@ -954,12 +971,19 @@ dg_status attention_pages(const uint16_t* q, const dg::PagedKV& kv, uint16_t* o,
     a.n_seq = n_seq;
     a.max_q_len = max_q_len;
     a.negate = scale < 0.f;
-    int32_t* plan = static_cast<int32_t*>(workspace);
-    cudaError_t e = launch_pdl(k_attn_plan<true>, dim3(1), dim3(1024), 0, st, a, n_seq, (int32_t)max_q_tiles, plan);
-    count_launch();
-    if (e != cudaSuccess) return DG_ERR_CUDA;
     const int64_t work_bound = (int64_t)n_seq * max_q_tiles * Hq;
     auto launch = [&](auto kern, size_t smem, int per_sm) -> dg_status {
+        // No more items than CTAs: nothing to order, and every CTA finds its item by itself.  Listed / by itself: 8
+        // canvases of 256 over 2.3k keys, 16 heads of 128, 49.5 / 45.7 us; 6 of 256 over 265 keys, heads of 64,
+        // 15.6 / 12.9; 19 of 128 of which 1, 3 or 10 have 8k keys and the others 300, 129 / 113, 131 / 117 to 127,
+        // 141 / 134.
+        int32_t* plan = work_bound <= (int64_t)per_sm * P ? nullptr : static_cast<int32_t*>(workspace);
+        cudaError_t e = cudaSuccess;
+        if (plan) {
+            e = launch_pdl(k_attn_plan<true>, dim3(1), dim3(1024), 0, st, a, n_seq, (int32_t)max_q_tiles, plan);
+            count_launch();
+            if (e != cudaSuccess) return DG_ERR_CUDA;
+        }
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return DG_ERR_CUDA;
         const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((int64_t)per_sm * P, work_bound));

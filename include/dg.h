@@ -437,7 +437,7 @@ DG_API dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v,
  * written); one with more than max_q_len queries raises it too and gets at least its first max_q_len
  * rows; one that needs a page outside [0, n_pages) raises it and its rows are unspecified.  Rows of no
  * sequence are not written.
- * Limits and errors as dg_attention and dg_kv_append.  Two kernels. */
+ * Limits and errors as dg_attention and dg_kv_append.  One or two kernels. */
 DG_API size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D);
 DG_API dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
                                     const int32_t* cu_q, const uint8_t* causal, int32_t n_seq, int32_t max_q_len,
