@@ -827,18 +827,18 @@ bool in_pairs(int32_t max_q_len, int32_t group, int32_t Hkv, int32_t D) {
     return D == 64 && Hkv % 2 == 0 && (int64_t)max_q_len * group * 2 <= 8;
 }
 
-// Whether a call takes this file's path or dg_attention's query tiles over pages (dg_attn.cu).  An item here
-// (up to 16 rows of a key head) and a tile there (128 queries of a query head) pass over the keys in about the same
-// time, 75 to 82 us for 256 of them on 4k keys at heads of 128, and tiles below the number of CTAs take
-// as long as that number does.  So: whichever has fewer passes.  Measured (us here / there): 32 requests over
-// 4k keys, 16 query over 8 key heads, 8 queries 92 / 150, 16 queries 168 / 150, 32 queries 327 / 152; 8 requests
-// over 2.3k keys, 16 queries 29 / 43, 32 queries 49 / 43, 64 queries 72 / 45; one request, 128 queries 27 / 40.
-// Over 216 shapes (heads of 64, 128, 256, 1 to 16 query heads a key head, 1 to 256 queries) the rule loses
-// 0.7 % to the better path on average, 22 % at most.
+// Whether a call takes this file's path or dg_attention's query tiles over pages (dg_attn.cu).  A tile there (128
+// queries of a query head) passes over the keys in the time of an item of 8 rows here, or of two for heads of
+// 64, and tiles below the number of CTAs take as long as that number does.  So: whichever has fewer passes.
+// Measured (us here / there), 16 query over 8 key heads of 128: 32 requests over 4k keys, 8 queries 90 / 137, 16
+// queries 167 / 137; 8 requests over 2.3k keys, 16 queries 32 / 35, 24 queries 40 / 35, 64 queries 86 / 36; one over 2k
+// keys, 256 queries 44 / 33.  Heads of 64, 16 queries of 8 heads, 32 requests over 4k keys 55 / 65.  Over 216 shapes
+// (heads of 64, 128, 256, 1 to 16 query heads a key head, 1 to 256 queries) the rule loses 0.1 % to the better
+// path on average, 24 % at most.
 bool split_path(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D) {
     const int64_t tile_ctas = D == 256 ? 152 : 304;
-    const int64_t here = (int64_t)n_seq * Hkv * (((int64_t)max_q_len * (Hq / Hkv) + 15) / 16);
-    const int64_t there = (int64_t)n_seq * Hq * (((int64_t)max_q_len + 127) / 128);
+    const int64_t here = (int64_t)n_seq * Hkv * (((int64_t)max_q_len * (Hq / Hkv) + 7) / 8);
+    const int64_t there = (int64_t)n_seq * Hq * (((int64_t)max_q_len + 127) / 128) * (D == 64 ? 2 : 1);
     return max_q_len == 1 || here <= std::max(there, tile_ctas);
 }
 
