@@ -41,6 +41,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dg_paged.cuh"
 
@@ -68,12 +69,17 @@ struct AttnArgs {
     int64_t total_q, total_kv;
     float scale_log2;       // scale * log2(e)
     unsigned* status;
-    // keys in pages (dg_paged_attention): the cache in place of cu_kv; the products' sign flips when the
-    // scale is negative (scale_log2 is then its magnitude, so that the largest score stays the largest)
+};
+
+// Keys in pages (dg_paged_attention): the cache in place of cu_kv; the products' sign flips when the scale is
+// negative (scale_log2 is then its magnitude, so that the largest score stays the largest).
+struct PagedArgs : AttnArgs {
     dg::PagedKV kv;
     int32_t n_seq, max_q_len;
     int32_t negate;
 };
+template <bool Paged>
+using Args = std::conditional_t<Paged, PagedArgs, AttnArgs>;
 
 struct __align__(8) AttnShared {
     uint64_t qfull;
@@ -148,9 +154,14 @@ DG_DEVINL TileRange range_of(const AttnArgs& a, int t, int q0, int ql, int k0, i
 }
 
 template <bool Paged>
-DG_DEVINL TileRange tile_range(const AttnArgs& a, int s, int t) {
-    const int q0 = a.cu_q[s], ql = a.cu_q[s + 1] - q0, k0 = Paged ? 0 : a.cu_kv[s];
-    return range_of(a, t, q0, ql, k0, Paged ? a.kv.kv_len[s] : a.cu_kv[s + 1] - k0, a.causal[s] != 0);
+DG_DEVINL TileRange tile_range(const Args<Paged>& a, int s, int t) {
+    const int q0 = a.cu_q[s], ql = a.cu_q[s + 1] - q0;
+    if constexpr (Paged) {
+        return range_of(a, t, q0, ql, 0, a.kv.kv_len[s], a.causal[s] != 0);
+    } else {
+        const int k0 = a.cu_kv[s];
+        return range_of(a, t, q0, ql, k0, a.cu_kv[s + 1] - k0, a.causal[s] != 0);
+    }
 }
 
 DG_DEVINL bool tile_full(const TileRange& r, int window, int jt) {
@@ -275,27 +286,21 @@ DG_DEVINL void do_abort(AttnShared& sh, unsigned* status) {
     dg::raise_status(status, DG_DEV_TIMEOUT);
 }
 
-// A work item as the roles use it.  With pages the list holds all of it, 32 bytes an item, so that a CTA's
+// A work item with keys in pages, as the roles use it.  The list holds all of it, 32 bytes an item, so that a CTA's
 // first copies wait for one read and not for two; without a list (null) item i is tile i % max_q_tiles of
-// sequence i / max_q_tiles.
+// sequence i / max_q_tiles.  (With packed keys the roles read the list's (sequence, tile) themselves.)
 struct Item {
     int s, t;      // sequence, query tile
     TileRange r;
 };
 
-template <bool Paged>
-DG_DEVINL Item read_item(const AttnArgs& a, const int32_t* list, int64_t i) {
-    if constexpr (Paged) {
-        if (!list) {
-            const int tiles = (a.max_q_len + kTile - 1) / kTile, s = (int)i / tiles;
-            return Item{s, (int)i - s * tiles, tile_range<true>(a, s, (int)i - s * tiles)};
-        }
-        const int4 x = reinterpret_cast<const int4*>(list)[2 * i], y = reinterpret_cast<const int4*>(list)[2 * i + 1];
-        return Item{x.x, x.y, range_of(a, x.y, x.z, x.w, 0, y.x, y.y != 0)};
-    } else {
-        const int2 x = reinterpret_cast<const int2*>(list)[i];
-        return Item{x.x, x.y, tile_range<false>(a, x.x, x.y)};
+DG_DEVINL Item paged_item(const PagedArgs& a, const int32_t* list, int64_t i) {
+    if (!list) {
+        const int tiles = (a.max_q_len + kTile - 1) / kTile, s = (int)i / tiles;
+        return Item{s, (int)i - s * tiles, tile_range<true>(a, s, (int)i - s * tiles)};
     }
+    const int4 x = reinterpret_cast<const int4*>(list)[2 * i], y = reinterpret_cast<const int4*>(list)[2 * i + 1];
+    return Item{x.x, x.y, range_of(a, x.y, x.z, x.w, 0, y.x, y.y != 0)};
 }
 
 // ------------------------------------------------------------------ the plan
@@ -308,7 +313,7 @@ constexpr int kCostBuckets = 1024;
 constexpr int kPlanHeader = 4;  // ints before the items: the item count, a one-cost flag, a 64-bit work counter
 
 template <bool Paged>
-__global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_seq, int32_t max_q_tiles,
+__global__ void __launch_bounds__(1024) k_attn_plan(const Args<Paged> a, int32_t n_seq, int32_t max_q_tiles,
                                                     int32_t* __restrict__ plan) {
     __shared__ int count[kCostBuckets];
     __shared__ int warp_sum[32];
@@ -403,11 +408,13 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const AttnArgs a, int32_t n_
 // With Paged the key and value tiles come page by page (one TMA box of min(page, 64) slots each,
 // zeros where no query sees the page), the rows of the value tiles that no query of the item sees
 // are zeroed before the product (what their slots hold is nobody's; their weights are 0, but 0 * NaN is not),
-// and the sequences without keys get their rows of zeros from the CTAs on their way out.
+// and the sequences without keys get their rows of zeros from the CTAs on their way out.  Where there are no pages
+// each role reads its items and their ranges by itself, in its own code: from a function common to both cases the
+// compiler made a kernel for heads of 128 that takes 289 us for 281 (32 canvases of 256 over 4k keys).
 template <int D, bool Paged>
 __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     k_attention(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const AttnArgs a, const int32_t* __restrict__ plan) {
+                const __grid_constant__ CUtensorMap tmV, const Args<Paged> a, const int32_t* __restrict__ plan) {
     using C = AttnCfg<D>;
     constexpr int kHead = D;
     constexpr uint32_t kQBytes = C::kQBytes, kKVBytes = C::kKVBytes;
@@ -421,10 +428,20 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
     const int warp = Paged ? __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0) : (int)(threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     // With pages the CTA sets up its barriers and tensor memory before it waits for the plan kernel (which
-    // lets it start); without, the CTAs beyond the work leave first.
+    // lets it start).  Without, it reads the list first, and the CTAs beyond the work leave: read behind the
+    // set-up it costs 1 us a call (one canvas of 256 over 2.3k keys, 45.3 / 46.3 us).
+    int64_t n_work = 0;
+    bool round_robin = true;
     if constexpr (!Paged) {
-        if ((int64_t)blockIdx.x >= (int64_t)plan[0] * a.Hq) return;  // the whole CTA: no work
+        n_work = (int64_t)plan[0] * a.Hq;
+        if ((int64_t)blockIdx.x >= n_work) return;  // the whole CTA: no work
+        round_robin = plan[1] != 0;
     }
+    const int group = a.Hq / a.Hkv;
+    auto rr_item = [&](uint32_t k) -> int64_t {
+        const int64_t w = (int64_t)blockIdx.x + (int64_t)k * gridDim.x;
+        return w < n_work ? w : -1;
+    };
     if (threadIdx.x == 0) {
         dg::mbar_init(&sh.qfull, 1);
         dg::mbar_init(&sh.qempty, 1);
@@ -463,24 +480,19 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         asm volatile("" : "+l"(list)::"memory");  // no read of the list moves up past the wait
     }
     const bool direct = Paged && !list;   // without a list: one item a CTA, or none
-    int64_t n_work;
-    bool round_robin = true;
-    if (direct) {
-        const int tiles = (a.max_q_len + kTile - 1) / kTile, f = (int)blockIdx.x / a.Hq, s = f / tiles;
-        const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
-        if (threadIdx.x == 0 && (int)blockIdx.x == s * tiles * a.Hq && (!p.ok || p.ql > a.max_q_len))
-            dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-        n_work = p.ok && p.kl > 0 && (f - s * tiles) * kTile < p.ql ? (int64_t)blockIdx.x + 1 : 0;
-    } else {
-        n_work = (int64_t)list[0] * a.Hq;
-        round_robin = list[1] != 0;
+    if constexpr (Paged) {
+        if (direct) {
+            const int tiles = (a.max_q_len + kTile - 1) / kTile, f = (int)blockIdx.x / a.Hq, s = f / tiles;
+            const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
+            if (threadIdx.x == 0 && (int)blockIdx.x == s * tiles * a.Hq && (!p.ok || p.ql > a.max_q_len))
+                dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+            n_work = p.ok && p.kl > 0 && (f - s * tiles) * kTile < p.ql ? (int64_t)blockIdx.x + 1 : 0;
+        } else {
+            n_work = (int64_t)list[0] * a.Hq;
+            round_robin = list[1] != 0;
+        }
     }
     const int32_t* items = direct ? nullptr : list + kPlanHeader;
-    const int group = a.Hq / a.Hkv;
-    auto rr_item = [&](uint32_t k) -> int64_t {
-        const int64_t w = (int64_t)blockIdx.x + (int64_t)k * gridDim.x;
-        return w < n_work ? w : -1;
-    };
 
     const uint32_t sQ = dg::smem_u32(smem + kOffQ);
 
@@ -509,9 +521,15 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
                     dg::mbar_arrive(&sh.wfull[slot]);  // releases the index to the readers
                 }
                 if (w < 0 || aborted(sh)) break;
-                const Item it = read_item<Paged>(a, items, w / a.Hq);
                 const int h = (int)(w % a.Hq);
-                const int qrow = it.r.q0 + it.t * kTile;
+                int qrow;
+                if constexpr (Paged) {
+                    const Item it = paged_item(a, items, w / a.Hq);
+                    qrow = it.r.q0 + it.t * kTile;
+                } else {
+                    const int2 it = reinterpret_cast<const int2*>(items)[w / a.Hq];
+                    qrow = a.cu_q[it.x] + it.y * kTile;
+                }
                 dg::mbar_arrive_expect_tx(&sh.qfull, kQBytes);
 #pragma unroll
                 for (int c = 0; c < kHead / kSub; ++c)
@@ -532,16 +550,26 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
             for (uint32_t k = 0; ok && !aborted(sh); ++k) {
                 const int64_t w = round_robin ? rr_item(k) : take_item(sh, k, ok);
                 if (w < 0) break;
-                const Item it = read_item<Paged>(a, items, w / a.Hq);
                 const int hk = (int)(w % a.Hq) / group;
-                const TileRange& r = it.r;
+                int seq;
+                TileRange r;
+                if constexpr (Paged) {
+                    const Item it = paged_item(a, items, w / a.Hq);
+                    seq = it.s;
+                    r = it.r;
+                } else {
+                    const int2 it = reinterpret_cast<const int2*>(items)[w / a.Hq];
+                    r = tile_range<false>(a, it.x, it.y);
+                }
                 for (int i = 0; i < r.nt; ++i, ++g) {
                     const int st = (int)(g & 1u);
                     // the pages of the tile's boxes, read before the wait; n_pages reads zeros
-                    const int box_shift = Paged ? min(a.kv.page_shift, 6) : 6, boxes = kKeys >> box_shift;
+                    int box_shift = 6;
+                    if constexpr (Paged) box_shift = min(a.kv.page_shift, 6);
+                    const int boxes = kKeys >> box_shift;
                     const int j0 = (r.jt_lo + i) * kKeys;
                     if constexpr (Paged) {
-                        const int32_t* table = a.kv.page_table + (int64_t)it.s * a.kv.max_pages;
+                        const int32_t* table = a.kv.page_table + (int64_t)seq * a.kv.max_pages;
                         int32_t entry[8];
                         bool bad = false;
 #pragma unroll
@@ -594,14 +622,21 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         // ------------------------------------------------ MMA issuer
         if (Paged ? dg::elect_leader() : lane == 0) {
             // S = Q K^T: K tile K-major; bit 13 negates Q
-            const uint32_t idS = dg::instr_desc(kTile, kKeys, false) | (Paged && a.negate ? 1u << 13 : 0u);
+            uint32_t idS = dg::instr_desc(kTile, kKeys, false);
+            if constexpr (Paged) idS |= a.negate ? 1u << 13 : 0u;
             constexpr uint32_t idO = dg::instr_desc(kTile, kHead, true);   // O += P V: V rows are N-major
             uint32_t g = 0, kq = 0;
             bool ok = true;
             for (; ok && !aborted(sh); ++kq) {
                 const int64_t w = round_robin ? rr_item(kq) : take_item(sh, kq, ok);
                 if (w < 0) break;
-                const TileRange r = read_item<Paged>(a, items, w / a.Hq).r;
+                TileRange r;
+                if constexpr (Paged) {
+                    r = paged_item(a, items, w / a.Hq).r;
+                } else {
+                    const int2 it = reinterpret_cast<const int2*>(items)[w / a.Hq];
+                    r = tile_range<false>(a, it.x, it.y);
+                }
                 if (!attn_wait(&sh.qfull, kq & 1u)) {
                     ok = false;
                     break;
@@ -667,10 +702,18 @@ __global__ void __launch_bounds__(kThreads, AttnCfg<D>::kCtasPerSm)
         for (; ok; ++kq) {
             const int64_t w = round_robin ? rr_item(kq) : take_item_warp(sh, kq, ok);
             if (w < 0) break;
-            const Item it = read_item<Paged>(a, items, w / a.Hq);
             const int h = (int)(w % a.Hq);
-            const TileRange& r = it.r;
-            const int t = it.t;
+            int t;
+            TileRange r;
+            if constexpr (Paged) {
+                const Item it = paged_item(a, items, w / a.Hq);
+                t = it.t;
+                r = it.r;
+            } else {
+                const int2 it = reinterpret_cast<const int2*>(items)[w / a.Hq];
+                t = it.y;
+                r = tile_range<false>(a, it.x, it.y);
+            }
             const int pos = r.kl - r.ql + t * kTile + row;
             const bool row_valid = t * kTile + row < r.ql;
             float m_ref = -INFINITY, l = 0.f;
@@ -955,7 +998,7 @@ dg_status attention_pages(const uint16_t* q, const dg::PagedKV& kv, uint16_t* o,
     };
     if (!tmap_heads(&tq, q, total_q, Hq, D, kTile) || !tmap_pages(&tk, kv.k) || !tmap_pages(&tv, kv.v))
         return DG_ERR_CUDA;
-    AttnArgs a = {};
+    PagedArgs a = {};
     a.cu_q = cu_q;
     a.causal = causal;
     a.o = o;
