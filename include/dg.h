@@ -410,9 +410,10 @@ typedef struct {
  *   cache     (host) the cache; the pages of positions kv_len - q_len .. kv_len - 1 must not be
  *             shared with another sequence.
  * Rows before cu_q[0] and behind cu_q[n_seq] are left out; so are the rows of a sequence with kv_len 0.  A
- * sequence whose offsets lie outside [0, total_q], with kv_len < 0, 0 < kv_len < q_len or kv_len >
- * max_pages * page_size raises DG_DEV_BAD_PARAM and is skipped, as is a token whose page is outside
- * [0, n_pages): nothing of it is written.
+ * sequence, with rows or without, whose offsets lie outside [0, total_q] or go back, with kv_len < 0, 0 <
+ * kv_len < q_len or kv_len > max_pages * page_size raises DG_DEV_BAD_PARAM and is skipped, as is a token
+ * whose page is outside [0, n_pages): nothing of it is written.  Where offsets go back, rows of other
+ * sequences may be left out too.  (With n_seq or total_q 0 nothing runs and nothing is reported.)
  * D is 64, 128 or 256 (else DG_ERR_UNSUPPORTED); rot_dim a multiple of 16 in [0, D]; Hq, Hkv in
  * [1, 65535]; n_seq in [0, 65535]; 0 <= total_q < 2^31.  Errors: DG_ERR_INVALID_ARG,
  * DG_ERR_ALIGNMENT (bf16 pointers not 16-byte aligned, strides not multiples of 8),

@@ -1,0 +1,105 @@
+"""GPU tests of the serving calls (dg_kv_append, dg_paged_attention, dg_adjust_logits) where their arguments
+are at the edge of what include/dg.h allows, or past it: what is reported, what is left alone."""
+import pytest
+import torch
+
+import entropy_bounded_denoising_gb300 as dg
+
+import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BAD = dg.DG_DEV_BAD_PARAM
+
+
+# ------------------------------------------------------------------ sequences that are refused
+def _three(seqs=((4, 20, 1), (5, 16, 1), (3, 30, 1))):
+    return ref.Batch(list(seqs), 2, 1, 64, 16, seed=2, extra_columns=0).fill_keys()
+
+
+def _claims(b):
+    """Per row of q: the sound sequences that claim it."""
+    cu, kl = b.cu.tolist(), b.kv_len.tolist()
+    cap = b.table.shape[1] * b.page_size
+    claims = [[] for _ in range(b.total)]
+    for s, n in enumerate(kl):
+        q0, q1 = cu[s], cu[s + 1]
+        if 0 <= q0 <= q1 <= b.total and 0 < n <= cap and q1 - q0 <= n:
+            for t in range(q0, q1):
+                claims[t].append(s)
+    return claims
+
+
+def _append_copies(b):
+    """Appends random rows without rotation; every row goes to the slot of a sound sequence that claims it or,
+    where the offsets go back, nowhere; nothing else changes.  Returns the status."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    q, k, v = (torch.randn((b.total, h, 64), generator=g, device=DEV).to(ref.BF16) for h in (2, 1, 1))
+    o = torch.full_like(q, 7.0)
+    before = b.k_cache.clone(), b.v_cache.clone()
+    dg.dg_clear_device_status()
+    dg.dg_kv_append(k, v, b.k_cache, b.v_cache, b.table, b.cu, b.kv_len, q=q, q_out=o)
+    torch.cuda.synchronize()
+    status = dg.dg_get_device_status()
+    cu, kl = b.cu.tolist(), b.kv_len.tolist()
+    ordered = all(x <= y for x, y in zip(cu, cu[1:]))
+    same = lambda x, y: torch.equal(x.view(torch.int16), y.view(torch.int16))  # noqa: E731
+    free = torch.ones(b.k_cache.shape[:2], dtype=torch.bool, device=DEV)   # slots that no row may write
+    for t, claims in enumerate(_claims(b)):
+        written = not same(o[t], torch.full_like(o[t], 7.0))
+        assert not written or same(o[t], q[t])
+        assert written == bool(claims) if ordered else claims or not written
+        at = [b.slots(s, [kl[s] - (cu[s + 1] - cu[s]) + t - cu[s]]) for s in claims]
+        if written:
+            assert any(same(b.k_cache[x][0], k[t]) and same(b.v_cache[x][0], v[t]) for x in at)
+        for x in at:
+            free[x] = False
+    for now, was in zip((b.k_cache, b.v_cache), before):
+        assert same(now[free], was[free])
+    return status
+
+
+@pytest.mark.parametrize("cu", [[5, 4, 3, 2], [0, 9, 4, 12], [0, -5, 9, 12], [0, 4, 12, 62], [-7, 4, 9, 12],
+                                [0, 2 ** 31 - 1, 9, 12], [12, 0, 0, 0]])
+def test_bad_offsets_are_reported_by_each_call(cu):
+    b = _three()
+    b.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+    assert _append_copies(b) == BAD
+    o = torch.full(b.q.shape, 7.0, dtype=ref.BF16, device=DEV)
+    dg.dg_clear_device_status()
+    dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, 9)
+    torch.cuda.synchronize()
+    assert dg.dg_get_device_status() == BAD
+    for t, claims in enumerate(_claims(b)):
+        if not claims:
+            assert (o[t] == 7.0).all(), t
+        elif len(claims) == 1:
+            s = claims[0]
+            at = b.slots(s, range(int(b.kv_len[s])))
+            rows = slice(int(b.cu[s]), int(b.cu[s + 1]))
+            ro, _, bound, _ = ref.attention(b.q[rows], b.k_cache[at], b.v_cache[at], True, -1, 1 / 8)
+            assert ((o[t].double() - ro[t - rows.start]).abs() <= bound[t - rows.start]).all(), t
+    dg.dg_clear_device_status()
+
+
+@pytest.mark.parametrize("kv_len", [-1, 33, 2 ** 31 - 1])
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_append_reports_bad_lengths_of_sequences_without_rows(which, kv_len):
+    seqs = [(4, 20, 1), (5, 16, 1), (3, 30, 1)]
+    seqs[which] = (0, 16, 1)
+    b = _three(seqs)
+    assert _append_copies(b) == 0
+    b.kv_len[which] = kv_len
+    assert _append_copies(b) == BAD
+    dg.dg_clear_device_status()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_append_checks_thousands_of_sequences(rows):
+    """More sequences than the grid has threads, of which the last ones have no rows."""
+    for bad in (None, 0, 1, 2999, 5555, 5999):
+        b = ref.Batch([(rows, 50, 1)] + [(0, 3, 1)] * 5999, 2, 1, 64, 64, seed=2, extra_columns=0).fill_keys()
+        if bad is not None:
+            b.kv_len[bad] = -1
+        assert _append_copies(b) == (0 if bad is None else BAD), bad
+    dg.dg_clear_device_status()
