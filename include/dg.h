@@ -397,16 +397,17 @@ typedef struct {
  *   (a, b) -> (a cos - b sin, a sin + b cos),
  * a and b at dimensions j and j + rot_dim / 2, or 2 j and 2 j + 1 when `interleaved` is not 0; the
  * others are copied.  Keys and values go to slot p of the sequence, queries to q_out.  A denoising
- * pass writes its canvas's slots anew each time.  Angles are reduced exactly (64-bit fixed point
- * turns), so far positions are as exact as near ones; sines, cosines and the rotation are in fp32
- * with one rounding to bf16.
+ * pass writes its canvas's slots anew each time.  Angles are reduced in 64-bit fixed-point turns,
+ * with at most two units of 2^-64 of a turn off for each position, so far positions are as exact as
+ * near ones; sines, cosines and the rotation are in fp32 with one rounding to bf16.
  *   k, v      (device) bf16 [total_q] rows of [Hkv][D], ldk / ldv elements apart (multiples of 8,
  *             at least Hkv * D, below 2^31: they may be parts of one fused projection's rows).
  *   q         (device, may be NULL) bf16 [total_q] rows of [Hq][D], ldq apart.
  *   q_out     (device, out, NULL iff q is) bf16 [total_q][Hq][D]; may be q itself when
  *             ldq = Hq * D, else must not overlap q.
  *   cu_q      (device) [n_seq + 1] int32 offsets (non-decreasing).
- *   inv_freq  (device, may be NULL when rot_dim = 0) [rot_dim / 2] double, radians per position.
+ *   inv_freq  (device, may be NULL when rot_dim = 0) [rot_dim / 2] double, radians per position, of
+ *             magnitude below 2^53; another one, or a NaN, raises DG_DEV_BAD_PARAM and counts as 0.
  *   cache     (host) the cache; the pages of positions kv_len - q_len .. kv_len - 1 must not be
  *             shared with another sequence.
  * Rows before cu_q[0] and behind cu_q[n_seq] are left out; so are the rows of a sequence with kv_len 0.  A

@@ -1,5 +1,7 @@
 """GPU tests of the serving calls (dg_kv_append, dg_paged_attention, dg_adjust_logits) where their arguments
 are at the edge of what include/dg.h allows, or past it: what is reported, what is left alone."""
+import math
+
 import pytest
 import torch
 
@@ -102,4 +104,71 @@ def test_append_checks_thousands_of_sequences(rows):
         if bad is not None:
             b.kv_len[bad] = -1
         assert _append_copies(b) == (0 if bad is None else BAD), bad
+    dg.dg_clear_device_status()
+
+
+# ------------------------------------------------------------------ angles
+def _pi(bits):
+    """floor(pi 2^bits): 16 atan(1 / 5) - 4 atan(1 / 239), in integers with 64 bits to spare."""
+    one = 1 << (bits + 64)
+
+    def atan(n):
+        total, power, k = 0, one // n, 1
+        while power:
+            total += power // k if k % 4 == 1 else -(power // k)
+            power //= n * n
+            k += 2
+        return total
+
+    return (16 * atan(5) - 4 * atan(239)) >> 64
+
+
+def _angle(w, p):
+    """w p modulo a turn, in radians: the double w taken exactly."""
+    n, d = w.as_integer_ratio()
+    turn = 2 * _pi(400)                       # of 2^-400 radians
+    r = ((n * p) << 400) // d % turn
+    return r / (1 << 400)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("size", [1e-3, 1.0, 3.9999, 4.0, 100.0, 1e6, 1e12, 2.0 ** 52])
+def test_far_positions_with_frequencies_of_many_turns(size, interleaved):
+    """Positions near 2^31 and frequencies up to 2^53 of either sign: the bound is that of near positions."""
+    D, page, far = 64, 65536, (1 << 31) - 3
+    table = torch.full((1, far // page + 1), -1, dtype=torch.int32, device=DEV)
+    table[0, (far - 5) // page:] = 0
+    cache = [torch.zeros((1, page, 1, D), dtype=ref.BF16, device=DEV) for _ in range(2)]
+    k = torch.randn((5, 1, D), generator=torch.Generator().manual_seed(3)).to(ref.BF16).to(DEV)
+    w = [size * (1 + (j * 0.6180339887498949) % 1 * 0.999) * (-1) ** (j // 2) for j in range(D // 2)]
+    dg.dg_clear_device_status()
+    dg.dg_kv_append(k, k, *cache, table, torch.tensor([0, 5], dtype=torch.int32, device=DEV),
+                    torch.tensor([far], dtype=torch.int32, device=DEV),
+                    inv_freq=torch.tensor(w, dtype=torch.float64, device=DEV), interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert dg.dg_get_device_status() == 0
+    for i in range(5):
+        p = far - 5 + i
+        ang = torch.tensor([_angle(x, p) for x in w], dtype=torch.float64, device=DEV)
+        want = ref.rotate(k[i:i + 1].double(), torch.ones(1, device=DEV), ang, interleaved)[0, 0]
+        got = cache[0][0, p % page, 0].double()
+        # two units of 2^-64 of a turn a position: 2 pi 2^-32 radians at most, next to 2^-22 for sine and cosine
+        slack = ref.rotation_bound(k[i:i + 1].double(), ang, interleaved)[0, 0] * (1 + 2 * math.pi * 2.0 ** -32 * 2.0 ** 21)
+        assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + slack).all(), i
+
+
+def test_frequencies_without_an_angle_are_refused():
+    """Frequencies of 2^53 and more, infinite ones and NaN raise the status and turn nothing; those beside them do."""
+    w = [0.5, 2.0 ** 53, -2.0 ** 53, 1e300, math.inf, -math.inf, math.nan, 2.0 ** 53 - 1]
+    b = ref.Batch([(3, 40, 1), (1, 9, 1)], 2, 1, 64, 16, seed=4).fill_keys()
+    k = torch.randn((4, 1, 64), generator=torch.Generator().manual_seed(1)).to(ref.BF16).to(DEV)
+    for j in range(8):
+        f = torch.zeros(8, dtype=torch.float64, device=DEV)
+        f[j] = w[j]
+        dg.dg_clear_device_status()
+        dg.dg_kv_append(k, k, b.k_cache, b.v_cache, b.table, b.cu, b.kv_len, inv_freq=f)
+        torch.cuda.synchronize()
+        assert dg.dg_get_device_status() == (0 if j in (0, 7) else BAD), w[j]
+        got = b.k_cache[b.slots(1, [8])][0]
+        assert torch.equal(got, k[3]) != (j in (0, 7)), w[j]
     dg.dg_clear_device_status()
