@@ -41,6 +41,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <limits>
 #include <type_traits>
 
 #include "dg_paged.cuh"
@@ -1007,8 +1008,9 @@ dg_status attention_pages(const uint16_t* q, const dg::PagedKV& kv, uint16_t* o,
     a.Hkv = Hkv;
     a.window = window;
     a.total_q = total_q;
-    // a scale of 0 weighs every key alike: the smallest one that keeps masked scores (-inf) what they are
-    a.scale_log2 = std::max(fabsf(scale) * kLog2e, 1e-30f);
+    // a scale of 0 weighs every key alike: the smallest float keeps masked scores (-inf) what they are and moves
+    // no finite score by more than 5e-7
+    a.scale_log2 = std::max(fabsf(scale) * kLog2e, std::numeric_limits<float>::denorm_min());
     a.status = status_word();
     a.kv = kv;
     a.n_seq = n_seq;

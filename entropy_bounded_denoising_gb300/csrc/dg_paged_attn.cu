@@ -891,7 +891,7 @@ extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* ca
                                         int64_t total_q, int32_t Hq, int32_t Hkv, int32_t D, int32_t window,
                                         float scale, void* workspace, size_t workspace_bytes, dg_stream_t stream) {
     if (n_seq < 0 || n_seq > 65535 || Hq < 1 || Hq > 65535 || Hkv < 1 || Hq % Hkv != 0 || window < -1 ||
-        !(scale == scale) || scale == INFINITY || scale == -INFINITY)
+        !(fabsf(scale) <= 0x1p127f))   // (past it log2(e) scale is infinite)
         return DG_ERR_INVALID_ARG;
     if (D != 64 && D != 128 && D != 256) return DG_ERR_UNSUPPORTED;
     if (max_q_len < 1 || max_q_len > (1 << 30) || total_q < 0 || total_q >= (1LL << 31)) return DG_ERR_INVALID_ARG;

@@ -427,7 +427,8 @@ DG_API dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v,
 /* dg_attention with its keys and values in the cache: o[i][h] = softmax over the allowed keys of
  * (scale * q[i][h] . k[j][h']) applied to v, h' = h / (Hq / Hkv); queries, positions, causal and window as
  * there, with kv_len[s] keys for sequence s.
- *   q, o, lse, cu_q, causal, max_q_len, window, scale: as dg_attention (lse may be NULL).
+ *   q, o, lse, cu_q, causal, max_q_len, window: as dg_attention (lse may be NULL); scale: any of magnitude up
+ *             to 2^127, 0 and negative ones too.
  *   cache     (host) the cache (only read).  Slots past kv_len and pages that hold no key some query may see
  *             may hold anything, NaN included (their table entries too); a value that some
  *             queries may see and others not must be finite.

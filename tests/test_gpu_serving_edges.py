@@ -172,3 +172,22 @@ def test_frequencies_without_an_angle_are_refused():
         got = b.k_cache[b.slots(1, [8])][0]
         assert torch.equal(got, k[3]) != (j in (0, 7)), w[j]
     dg.dg_clear_device_status()
+
+
+# ------------------------------------------------------------------ scores
+@pytest.mark.parametrize("rows,n", [(1, 2), (300, 2), (256, 24)])
+@pytest.mark.parametrize("size", [2.0 ** 56, 2.0 ** 60, 1.0])
+def test_scales_that_undo_large_queries_and_keys(rows, n, size):
+    """Queries and keys of 2^56 and a scale of 2^-114 are scores like any others; scales of 0 and next to it weigh
+    every key alike."""
+    b = ref.Batch([(rows, 500, 0)] * n, 8, 8, 64, 16, seed=rows).fill_keys()
+    b.q.mul_(size)
+    b.k_cache.mul_(size)
+    for scale in (2.0 ** -2 / size ** 2, -2.0 ** -2 / size ** 2, 2.0 ** -140, 0.0):
+        o = torch.full(b.q.shape, 7.0, dtype=ref.BF16, device=DEV)
+        lse = torch.full(b.q.shape[:2], 7.0, device=DEV)
+        dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, rows, lse=lse, scale=scale)
+        for s in (0, n - 1):
+            sl = slice(int(b.cu[s]), int(b.cu[s + 1]))
+            ro, rl, bound, lbound = ref.attention(b.q[sl], *b.keys(s), False, -1, scale)
+            assert ((o[sl].double() - ro).abs() <= bound).all() and ((lse[sl].double() - rl).abs() <= lbound).all(), scale
