@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustA
     if (a.masks && tid < rows) m = a.mask_index[c * a.L + r0 + tid];
     if (!(flags & DG_ACTIVE)) return;
     const bool sound = h0 >= 0 && h1 >= h0 && h1 <= a.total_history && b0 >= 0 && b1 >= b0 && b1 <= a.total_bias &&
-                       pen.repetition > 0.f && isfinite(pen.repetition) && isfinite(pen.frequency) &&
-                       isfinite(pen.presence);
+                       pen.repetition >= 0x1p-126f && pen.repetition <= 0x1p126f &&   // its reciprocal is a normal number
+                       isfinite(pen.frequency) && isfinite(pen.presence);
     if (!sound) {
         if (reports) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
         return;

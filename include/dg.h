@@ -455,7 +455,7 @@ DG_API dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache,
 
 /* Penalties of one canvas. */
 typedef struct {
-    float repetition; /* > 0; 1 = none */
+    float repetition; /* in [2^-126, 2^126]; 1 = none */
     float frequency;  /* per occurrence; 0 = none */
     float presence;   /* 0 = none */
 } dg_penalties;
@@ -481,7 +481,7 @@ typedef struct {
  *               of word t / 32 set = token t allowed.  mask_index (device) [n_canvas][L] int32: the
  *               mask row of each position, -1 = none.
  * Tokens outside [0, V) in the lists are ignored (-1 pads them).  A canvas with offsets outside its
- * list, a penalty that is not finite or a repetition <= 0 raises DG_DEV_BAD_PARAM and is skipped; a
+ * list, a penalty that is not finite or a repetition out of its range raises DG_DEV_BAD_PARAM and is skipped; a
  * mask index outside [-1, n_masks) raises it and counts as -1.
  * Limits: those of dg_denoise_step; ld * sizeof(dtype) and ld_out * sizeof(dtype) multiples of 16;
  * mask_stride >= ceil(V / 32); list lengths < 2^31.  Errors: DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT,

@@ -2,6 +2,7 @@
 are at the edge of what include/dg.h allows, or past it: what is reported, what is left alone."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -191,3 +192,40 @@ def test_scales_that_undo_large_queries_and_keys(rows, n, size):
             sl = slice(int(b.cu[s]), int(b.cu[s + 1]))
             ro, rl, bound, lbound = ref.attention(b.q[sl], *b.keys(s), False, -1, scale)
             assert ((o[sl].double() - ro).abs() <= bound).all() and ((lse[sl].double() - rl).abs() <= lbound).all(), scale
+
+
+# ------------------------------------------------------------------ logit edits
+def _active(n):
+    p = np.zeros((n, dg.PARAM_BYTES // 4), np.int32)
+    p[:, 0] = np.float32(1.0).view(np.int32)
+    p[:, -1] = dg.DG_ACTIVE
+    return torch.from_numpy(p.view(np.uint8).reshape(-1)).to(DEV)
+
+
+def _ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def test_repetitions_without_a_normal_reciprocal_are_refused():
+    """x / repetition is x times the rounded reciprocal: right to 2^-23 where that is a normal number, refused
+    where it is not."""
+    x = torch.tensor([[[1e-30, 3.0, 1e30, -1e-30, -3.0, -1e30, 0.0, 7.0]]], device=DEV)
+    for rep, sound in ((2.0 ** -126, 1), (2.0 ** 126, 1), (1e-37, 1), (8e37, 1), (1.7, 1), (2.0 ** -127, 0), (1e-39, 0),
+                       (2.0 ** 126 * (1 + 2.0 ** -23), 0), (3e38, 0), (math.inf, 0), (math.nan, 0), (0.0, 0), (-2.0, 0)):
+        out = torch.full_like(x, 9.0)
+        dg.dg_clear_device_status()
+        dg.dg_adjust_logits(x, _active(1), out, history=_ints(*range(7)), cu_history=_ints(0, 7),
+                            penalties=torch.tensor([[rep, 0.0, 0.0]], device=DEV))
+        torch.cuda.synchronize()
+        assert dg.dg_get_device_status() == (0 if sound else BAD), rep
+        if not sound:
+            assert (out == 9.0).all(), rep
+            continue
+        r = float(torch.tensor(rep, dtype=torch.float32))
+        for t, v in enumerate(x[0, 0].tolist()):
+            want = v if t == 7 else v / r if v > 0 else v * r
+            got = float(out[0, 0, t])
+            # fp32: beyond its range infinity, below it steps of 2^-149
+            assert got == want or (abs(want) >= 3.4e38 and got == math.copysign(math.inf, want)) or \
+                abs(got - want) <= 2.0 ** -23 * abs(want) + 2.0 ** -149, (rep, v, got)
+    dg.dg_clear_device_status()
