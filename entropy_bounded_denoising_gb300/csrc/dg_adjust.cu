@@ -32,6 +32,7 @@ constexpr int kBlocksPerSm = 4;
 constexpr int unroll_of(bool lists) { return lists ? 4 : 8; }
 constexpr int kMaxRows = 64; // rows of a block, at most
 constexpr int kEarly = 2;    // entries of each list that a thread reads before anything else
+constexpr int kAgain = 8;    // entries of a bias list with repeated tokens that a lane reads at a time
 
 struct AdjustArgs {
     const unsigned char* x;
@@ -128,6 +129,36 @@ DG_DEVINL void store(unsigned char* at, const uint4& y, int n) {
     }
 }
 
+// Adds up the biases of the warp's own tokens that have more than one, in list order: the warp reads the list,
+// 256 entries at a time, and takes the entries of such tokens one after another.  (A thread that looked for its
+// tokens' entries by itself took as many dependent reads as lay between them: 4000 tokens given twice 1170 us, this
+// way 41.)  A call, so that its registers are not the kernel's.
+template <int PerVec>
+__device__ __noinline__ void add_repeats(const int32_t* tokens, const float* values, int b0, int b1, int slice0, int end,
+                                         const int32_t* n_bias, float* sums) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int own0 = (tid - lane) * PerVec, own1 = min(own0 + 32 * PerVec, end);   // the warp's tokens, of the slice
+    for (int64_t j0 = b0; j0 < b1; j0 += 32 * kAgain) {
+        int64_t token[kAgain];
+        float value[kAgain];
+#pragma unroll
+        for (int u = 0; u < kAgain; ++u) {
+            const int64_t j = j0 + u * 32 + lane;
+            token[u] = j < b1 ? (int64_t)tokens[j] - slice0 : -1;
+            value[u] = j < b1 ? values[j] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kAgain; ++u) {
+            const bool own = token[u] >= own0 && token[u] < own1;
+            for (uint32_t hits = __ballot_sync(0xffffffffu, own && n_bias[own ? token[u] : 0] > 1); hits; hits &= hits - 1) {
+                const int t = __shfl_sync(0xffffffffu, (int)token[u], __ffs(hits) - 1);
+                const float v = __shfl_sync(0xffffffffu, value[u], __ffs(hits) - 1);
+                if (t / PerVec == tid) sums[t] += v;
+            }
+        }
+    }
+}
+
 // Bytes: 2 (bf16) or 4 (fp32) a logit; PerVec tokens in 16 bytes.  Lists: the call gives a history or biases.
 template <int Bytes, bool Lists>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustArgs a) {
@@ -137,8 +168,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustA
     constexpr int kCounts = Lists ? kSlice : 4;
     __shared__ __align__(16) int32_t n_hist[kCounts];       // occurrences in the history
     __shared__ __align__(16) int32_t n_bias[kCounts];       // entries in the bias list
-    __shared__ int32_t first_bias[kCounts];                 // the first of them
-    __shared__ float one_bias[kCounts];                     // and the value when it is the only one
+    __shared__ float one_bias[kCounts];                     // the value of the only one, else their sum
     __shared__ int32_t row_mask[kMaxRows];
     __shared__ uint2 expand[16];
     constexpr uint32_t kNegInf = Bytes == 2 ? 0xff80ff80u : 0xff800000u;
@@ -201,10 +231,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustA
             reinterpret_cast<int4*>(n_hist)[e * kThreads + tid] = make_int4(0, 0, 0, 0);
             if (b1 > b0) reinterpret_cast<int4*>(n_bias)[e * kThreads + tid] = make_int4(0, 0, 0, 0);
         }
-        if (b1 > b0) {
-#pragma unroll
-            for (int e = 0; e < PerVec; ++e) first_bias[e * kThreads + tid] = 0x7fffffff;
-        }
     }
     __syncthreads();
     // the first rows' masks and data are on their way while the lists are counted
@@ -239,11 +265,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustA
         const int64_t t = (int64_t)token - slice0;
         if (t >= 0 && t < end) atomicAdd(&n_hist[t], 1);
     };
-    auto note = [&](int32_t token, float value, int i) {
+    auto note = [&](int32_t token, float value) {
         const int64_t t = (int64_t)token - slice0;
         if (t < 0 || t >= end) return;
         atomicAdd(&n_bias[t], 1);
-        atomicMin(&first_bias[t], i);
         one_bias[t] = value;
     };
     masks_of(0);
@@ -251,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustA
 #pragma unroll
         for (int k = 0; k < kEarly; ++k) {
             count(early_h[k]);
-            note(early_b[k], early_v[k], b0 + tid + k * kThreads);
+            note(early_b[k], early_v[k]);
         }
     }
     load(0, in_place && !listed);
@@ -260,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustA
         for (int64_t i = (int64_t)h0 + kEarly * kThreads + tid; i < h1; i += kThreads) count(a.history[i]);
 #pragma unroll 4
         for (int64_t i = (int64_t)b0 + kEarly * kThreads + tid; i < b1; i += kThreads)
-            note(a.bias_tokens[i], a.bias_values[i], (int)i);
+            note(a.bias_tokens[i], a.bias_values[i]);
     }
     float add[PerVec];
     uint32_t penalised = 0, edited = 0;   // tokens with a count / with a count or a bias
@@ -275,19 +300,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adjust(const AdjustA
             *reinterpret_cast<int4*>(&nb[e]) =
                 b1 > b0 ? *reinterpret_cast<const int4*>(&n_bias[tid * PerVec + e]) : make_int4(0, 0, 0, 0);
         }
+        bool several = false;   // some token of the thread has more than one bias
+#pragma unroll
+        for (int e = 0; e < PerVec; ++e) several |= nb[e] > 1;
+        if (__any_sync(0xffffffffu, several)) {
+#pragma unroll
+            for (int e = 0; e < PerVec; ++e)
+                if (nb[e] > 1) one_bias[tid * PerVec + e] = 0.f;
+            add_repeats<PerVec>(a.bias_tokens, a.bias_values, b0, b1, slice0, end, n_bias, one_bias);
+        }
 #pragma unroll
         for (int e = 0; e < PerVec; ++e) {
-            float b = 0.f;
-            if (nb[e] == 1) {
-                b = one_bias[tid * PerVec + e];
-            } else if (nb[e] > 1) {   // in list order
-                int left = nb[e];
-                for (int i = first_bias[tid * PerVec + e]; left > 0 && i < b1; ++i)
-                    if (a.bias_tokens[i] == v0 + e) {
-                        b += a.bias_values[i];
-                        --left;
-                    }
-            }
+            float b = nb[e] > 0 ? one_bias[tid * PerVec + e] : 0.f;
             if (nb[e] > 0) edited |= 1u << e;
             if (nh[e] > 0) {
                 penalised |= 1u << e;

@@ -229,3 +229,59 @@ def test_repetitions_without_a_normal_reciprocal_are_refused():
             assert got == want or (abs(want) >= 3.4e38 and got == math.copysign(math.inf, want)) or \
                 abs(got - want) <= 2.0 ** -23 * abs(want) + 2.0 ** -149, (rep, v, got)
     dg.dg_clear_device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,lens,kinds", [(2, [1, 2, 700], 2), (5000, [1023, 1024, 1025, 0, 3000], 40), (5000, [4097, 2], 5000),
+                                          (70001, [2, 9000, 2048], 4500), (3001, [6000, 6000, 1], 1)])
+def test_repeated_biases_add_up_in_list_order(V, lens, kinds, dtype):
+    """Lists in which tokens come many times, anywhere: the fp32 sum in list order, bit for bit."""
+    n, L = len(lens), 3
+    g = torch.Generator().manual_seed(V + kinds)
+    cu = np.cumsum([0] + lens)
+    pool = torch.randperm(V + 2, generator=g)[:kinds] - 1                   # -1 and V among them: ignored
+    tok = pool[torch.randint(0, len(pool), (int(cu[-1]),), generator=g)].to(torch.int32)
+    val = (torch.randn(int(cu[-1]), generator=g) * 10.0 ** torch.randint(-3, 4, (int(cu[-1]),), generator=g)).float()
+    ld = -(-V // 8) * 8
+    x = torch.randn((n, L, ld), generator=g).to(dtype)
+    for in_place in (False, True):
+        xd = x.to(DEV)
+        out = xd if in_place else torch.full_like(xd, 9.0)
+        dg.dg_clear_device_status()
+        dg.dg_adjust_logits(xd, _active(n), None if in_place else out, bias_tokens=tok.to(DEV), bias_values=val.to(DEV),
+                            cu_bias=torch.from_numpy(cu.astype(np.int32)).to(DEV), V=V)
+        torch.cuda.synchronize()
+        assert dg.dg_get_device_status() == 0
+        for c in range(n):
+            s = np.zeros(V, np.float32)
+            for t, v in zip(tok[cu[c]:cu[c + 1]].tolist(), val[cu[c]:cu[c + 1]].numpy()):
+                if 0 <= t < V:
+                    s[t] = np.float32(s[t] + v)
+            seen = torch.zeros(V, dtype=torch.bool)
+            seen[[t for t in tok[cu[c]:cu[c + 1]].tolist() if 0 <= t < V]] = True
+            want = torch.where(seen, x[c, :, :V].float() + torch.from_numpy(s), x[c, :, :V].float()).to(dtype)
+            assert torch.equal(out[c, :, :V].cpu(), want), c
+
+
+def test_repeated_biases_take_no_more_than_a_few_times_as_long():
+    """4000 tokens given twice against 8000 given once: the entries of a token lie 4000 apart."""
+    V, L = 32768, 16
+    x = torch.randn((1, L, V), device=DEV)
+    out, params, cu = torch.empty_like(x), _active(1), _ints(0, 8000)
+    tok = torch.randperm(V, device=DEV)[:8000].to(torch.int32)
+    val = torch.randn(8000, device=DEV)
+
+    def best(tokens):
+        times = []
+        for _ in range(8):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            dg.dg_adjust_logits(x, params, out, bias_tokens=tokens, bias_values=val, cu_bias=cu)
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end))
+        return min(times)
+
+    once, twice = best(tok), best(tok[:4000].repeat(2))
+    print(f"once {once * 1000:.1f} us, twice {twice * 1000:.1f} us")
+    assert twice < 10 * once, (once, twice)   # 80 times before such lists were read by the whole block
