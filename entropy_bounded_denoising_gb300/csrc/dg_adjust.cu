@@ -366,6 +366,10 @@ extern "C" dg_status dg_adjust_logits(const void* logits, dg_dtype dtype, int64_
     if (out == logits && ld_out != ld) return DG_ERR_INVALID_ARG;
     const int64_t es = dtype == DG_BF16 ? 2 : 4;
     if (!aligned(logits, 16) || !aligned(out, 16) || (ld * es) % 16 || (ld_out * es) % 16) return DG_ERR_ALIGNMENT;
+    for (const void* p : {(const void*)params, (const void*)history, (const void*)cu_history, (const void*)penalties,
+                          (const void*)bias_tokens, (const void*)bias_values, (const void*)cu_bias, (const void*)masks,
+                          (const void*)mask_index})
+        if (!aligned(p, 4)) return DG_ERR_ALIGNMENT;   // (records handed over as bytes may lie anywhere)
     if (V * es > 0x7fffffffLL) return DG_ERR_UNSUPPORTED;
     AdjustArgs a;
     a.x = static_cast<const unsigned char*>(logits);

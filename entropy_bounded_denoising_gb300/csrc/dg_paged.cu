@@ -250,7 +250,8 @@ dg_status paged_kv(const dg_paged_kv* cache, int32_t D, dg::PagedKV* c) {
     for (int64_t s : strides)
         if (s < D || s >= (1LL << 39)) return DG_ERR_INVALID_ARG;
     if (cache->n_pages > (1LL << 60) / cache->page_stride) return DG_ERR_INVALID_ARG;
-    if (!aligned16(cache->k) || !aligned16(cache->v)) return DG_ERR_ALIGNMENT;
+    if (!aligned16(cache->k) || !aligned16(cache->v) || !on_multiple(cache->page_table, 4) || !on_multiple(cache->kv_len, 4))
+        return DG_ERR_ALIGNMENT;
     for (int64_t s : strides)
         if (s % 8) return DG_ERR_ALIGNMENT;
     c->k = cache->k;
@@ -284,7 +285,7 @@ extern "C" dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t
     if (ldk >= (1LL << 31) || ldv >= (1LL << 31) || (q && ldq >= (1LL << 31))) return DG_ERR_INVALID_ARG;
     if (q && q_out == q && ldq != (int64_t)Hq * D) return DG_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))) || ldk % 8 || ldv % 8 ||
-        (q && ldq % 8))
+        (q && ldq % 8) || !dghost::on_multiple(cu_q, 4) || !dghost::on_multiple(inv_freq, 8))
         return DG_ERR_ALIGNMENT;
     AppendArgs a;
     const dg_status ok = dghost::paged_kv(cache, D, &a.kv);

@@ -59,6 +59,9 @@ DG_DEVINL int warp_owner(const int32_t* cu_q, int n, int t) {
 }  // namespace dg
 
 namespace dghost {
+// Whether a pointer (null too) lies on a multiple of n bytes, a power of two.
+inline bool on_multiple(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 // Checks shared by the calls that take a dg_paged_kv; fills `c` when it returns DG_OK.
 dg_status paged_kv(const dg_paged_kv* cache, int32_t D, dg::PagedKV* c);
 

@@ -897,7 +897,8 @@ extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* ca
     if (max_q_len < 1 || max_q_len > (1 << 30) || total_q < 0 || total_q >= (1LL << 31)) return DG_ERR_INVALID_ARG;
     if (n_seq == 0 || total_q == 0) return DG_OK;
     if (!q || !o || !cu_q || !causal) return DG_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(o)) return DG_ERR_ALIGNMENT;
+    if (!aligned16(q) || !aligned16(o) || !dghost::on_multiple(cu_q, 4) || !dghost::on_multiple(lse, 4))
+        return DG_ERR_ALIGNMENT;
     SplitArgs a;
     const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
     if (ok != DG_OK) return ok;

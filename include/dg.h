@@ -417,8 +417,8 @@ typedef struct {
  * sequences may be left out too.  (With n_seq or total_q 0 nothing runs and nothing is reported.)
  * D is 64, 128 or 256 (else DG_ERR_UNSUPPORTED); rot_dim a multiple of 16 in [0, D]; Hq, Hkv in
  * [1, 65535]; n_seq in [0, 65535]; 0 <= total_q < 2^31.  Errors: DG_ERR_INVALID_ARG,
- * DG_ERR_ALIGNMENT (bf16 pointers not 16-byte aligned, strides not multiples of 8),
- * DG_ERR_UNSUPPORTED, DG_ERR_CUDA.  One kernel. */
+ * DG_ERR_ALIGNMENT (bf16 pointers not 16-byte aligned, others not a multiple of their elements'
+ * size, strides not multiples of 8), DG_ERR_UNSUPPORTED, DG_ERR_CUDA.  One kernel. */
 DG_API dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q,
                               int64_t ldq, uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q,
                               int32_t Hq, int32_t Hkv, int32_t D, const double* inv_freq, int32_t rot_dim,
@@ -484,8 +484,9 @@ typedef struct {
  * list, a penalty that is not finite or a repetition out of its range raises DG_DEV_BAD_PARAM and is skipped; a
  * mask index outside [-1, n_masks) raises it and counts as -1.
  * Limits: those of dg_denoise_step; ld * sizeof(dtype) and ld_out * sizeof(dtype) multiples of 16;
- * mask_stride >= ceil(V / 32); list lengths < 2^31.  Errors: DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT,
- * DG_ERR_UNSUPPORTED (a row of 2^31 bytes or more), DG_ERR_CUDA.  One kernel, no workspace. */
+ * mask_stride >= ceil(V / 32); list lengths < 2^31.  Errors: DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT (logits
+ * not 16-byte aligned; params, lists or masks not 4-byte aligned), DG_ERR_UNSUPPORTED (a row of 2^31 bytes
+ * or more), DG_ERR_CUDA.  One kernel, no workspace. */
 DG_API dg_status dg_adjust_logits(const void* logits, dg_dtype dtype, int64_t ld, void* out, int64_t ld_out,
                                   int64_t n_canvas, int32_t L, int64_t V, const dg_canvas_params* params,
                                   const int32_t* history, const int32_t* cu_history, int64_t total_history,

@@ -29,3 +29,28 @@ def test_scales_whose_log2_form_is_infinite_are_refused():
         assert _attention(scale=scale) == dg.DG_ERR_INVALID_ARG
     for scale in (2.0 ** 127, -2.0 ** 127, 0.0):   # past this check: the workspace's is next
         assert _attention(scale=scale, ws=None) == dg.DG_ERR_WORKSPACE
+
+
+def _append(k=16, ldk=128, v=16, ldv=128, q=16, ldq=256, qo=32, cu=16, n=1, total=4, Hq=2, Hkv=1, D=128, w=16, rot=128,
+            kv=None):
+    c = _kv() if kv is None else kv
+    return dg.load().dg_kv_append(k, ldk, v, ldv, q, ldq, qo, cu, n, total, Hq, Hkv, D, w, rot, 0, ctypes.byref(c), None)
+
+
+def _adjust(x=16, dt=0, ld=64, out=32, ldo=64, n=1, L=4, V=64, p=16, h=16, cuh=16, nh=5, pen=16, bt=16, bv=16, cub=16,
+            nb=5, m=16, ms=2, nm=1, mi=16):
+    return dg.load().dg_adjust_logits(x, dt, ld, out, ldo, n, L, V, p, h, cuh, nh, pen, bt, bv, cub, nb, m, ms, nm, mi,
+                                      None)
+
+
+def test_pointers_between_their_elements_are_refused():
+    """A kernel's read of a word that does not lie on a multiple of its size ends the context; records given as
+    bytes, and pointers through the C ABI, may lie anywhere."""
+    for off in (1, 2, 3):
+        for name in ("p", "h", "cuh", "pen", "bt", "bv", "cub", "m", "mi"):
+            assert _adjust(**{name: 16 + off}) == dg.DG_ERR_ALIGNMENT, name
+        for kw in (dict(cu=16 + off), dict(lse=16 + off), dict(kv=_kv(page_table=16 + off)), dict(kv=_kv(kv_len=16 + off))):
+            assert _attention(**kw) == dg.DG_ERR_ALIGNMENT, kw
+        for kw in (dict(cu=16 + off), dict(w=16 + 4), dict(w=16 + off), dict(kv=_kv(page_table=16 + off)),
+                   dict(kv=_kv(kv_len=16 + off))):
+            assert _append(**kw) == dg.DG_ERR_ALIGNMENT, kw
