@@ -882,8 +882,9 @@ dg_status launch_split(const SplitArgs& a, cudaStream_t stream) {
 extern "C" size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv,
                                                      int32_t D) {
     if (n_seq < 1 || max_q_len < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
-    if (!split_path(n_seq, max_q_len, Hq, Hkv, D)) return dghost::attention_pages_bytes(n_seq, max_q_len);
-    return split_bytes(item_rows(max_q_len, Hq / Hkv), D);
+    // what either path needs, so that a workspace for a program's largest call serves its smaller ones, whichever
+    // way they go
+    return std::max(split_bytes(item_rows(max_q_len, Hq / Hkv), D), dghost::attention_pages_bytes(n_seq, max_q_len));
 }
 
 extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,

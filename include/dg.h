@@ -433,7 +433,10 @@ DG_API dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v,
  *             may hold anything, NaN included (their table entries too); a value that some
  *             queries may see and others not must be finite.
  *   workspace (device) >= dg_paged_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D),
- *             16-byte aligned, no initial contents; calls that overlap on the GPU need their own.
+ *             16-byte aligned, no initial contents; calls that overlap on the GPU need their own.  With
+ *             the same heads the size never falls as n_seq or max_q_len grow: one workspace for a
+ *             program's largest call serves all of them (2 MB to 17 MB, or 32 bytes for every 128 of
+ *             a sequence's max_q_len queries where that is more).
  * A sequence with kv_len 0 sees no key: its rows of o are 0 and its lse -inf.  A sequence whose
  * offsets lie outside [0, total_q], with kv_len < 0, 0 < kv_len < q_len, kv_len > max_pages *
  * page_size or kv_len > 2^31 - 2^16 raises DG_DEV_BAD_PARAM and is skipped (its rows are not

@@ -285,3 +285,15 @@ def test_repeated_biases_take_no_more_than_a_few_times_as_long():
     once, twice = best(tok), best(tok[:4000].repeat(2))
     print(f"once {once * 1000:.1f} us, twice {twice * 1000:.1f} us")
     assert twice < 10 * once, (once, twice)   # 80 times before such lists were read by the whole block
+
+
+# ------------------------------------------------------------------ workspaces
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_one_workspace_serves_a_programs_calls(D):
+    """A buffer of the size of the largest call, for tokens, drafts and canvases one after another."""
+    ws = torch.empty(dg.dg_paged_attention_workspace_bytes(70, 300, 16, 8, D), dtype=torch.uint8, device=DEV)
+    for n, rows in ((70, 1), (1, 1), (5, 5), (3, 40), (2, 300), (70, 2), (24, 200)):
+        b = ref.Batch([(rows, rows + 90, 1)] * n, 16, 8, D, 16, seed=n).fill_keys()
+        o, lse = torch.full_like(b.q, 7.0), torch.full(b.q.shape[:2], 7.0, device=DEV)
+        dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, rows, lse=lse, workspace=ws)
+        ref.check_attention(b, o, lse, skip=range(3, n))

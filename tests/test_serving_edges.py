@@ -54,3 +54,17 @@ def test_pointers_between_their_elements_are_refused():
         for kw in (dict(cu=16 + off), dict(w=16 + 4), dict(w=16 + off), dict(kv=_kv(page_table=16 + off)),
                    dict(kv=_kv(kv_len=16 + off))):
             assert _append(**kw) == dg.DG_ERR_ALIGNMENT, kw
+
+
+def test_the_workspace_for_a_larger_call_serves_the_smaller_ones():
+    """With the same heads the size never falls as the sequences or their queries grow."""
+    counts = [1, 2, 3, 8, 17, 64, 150, 256, 1000, 65535]
+    queries = [1, 2, 3, 4, 5, 8, 9, 16, 17, 64, 128, 129, 256, 300, 2048, 1 << 20]
+    for D in (64, 128, 256):
+        for Hq, Hkv in ((1, 1), (8, 8), (16, 8), (32, 4), (40, 1), (71, 1)):
+            size = {(n, q): dg.dg_paged_attention_workspace_bytes(n, q, Hq, Hkv, D) for n in counts for q in queries}
+            for i, n in enumerate(counts):
+                for j, q in enumerate(queries):
+                    assert size[n, q] > 0
+                    assert i == 0 or size[n, q] >= size[counts[i - 1], q], (n, q, Hq, Hkv, D)
+                    assert j == 0 or size[n, q] >= size[n, queries[j - 1]], (n, q, Hq, Hkv, D)
