@@ -29,7 +29,7 @@ _PARAM_FMT = "<fffiiiiII"
 PARAM_BYTES = struct.calcsize(_PARAM_FMT)   # 36, sizeof(dg_canvas_params)
 
 _lib = None
-_bind = None   # the dg_bind module, connected to _lib
+_bind = None   # the dg_bind module, connected to _lib by the first serving call
 
 
 class _PagedKV(ctypes.Structure):   # dg_paged_kv
@@ -50,15 +50,14 @@ def library_path() -> str:
 
 
 def load(path: str | None = None):
-    """Load libdg.so and its dg_bind module (built in-tree).  Raises if either is missing."""
-    global _lib, _bind
+    """Load libdg.so (built in-tree).  Raises if it is missing."""
+    global _lib
     if _lib is not None:
         return _lib
     path = path or _build.LIB
-    for p in (path, _build.BIND):
-        if not os.path.exists(p):
-            raise RuntimeError(f"{os.path.basename(p)} not found at {p}: build it with "
-                               "entropy_bounded_denoising_gb300.build.build()")
+    if not os.path.exists(path):
+        raise RuntimeError(f"libdg.so not found at {path}: build it with "
+                           "entropy_bounded_denoising_gb300.build.build()")
     lib = ctypes.CDLL(path)
     P, i32, i64, u32, u64, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                                   ctypes.c_uint64, ctypes.c_size_t)
@@ -116,12 +115,7 @@ def load(path: str | None = None):
         f = getattr(lib, name)
         f.restype = res
         f.argtypes = args
-    names = ("dg_kv_append", "dg_paged_attention", "dg_paged_attention_workspace_bytes", "dg_adjust_logits")
-    loader = importlib.machinery.ExtensionFileLoader("dg_bind", _build.BIND)
-    bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("dg_bind", loader))
-    loader.exec_module(bind)
-    bind.connect(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
-    _lib, _bind = lib, bind
+    _lib = lib
     return lib
 
 
@@ -434,10 +428,21 @@ def dg_attention(q, k, v, o, cu_q, cu_kv, causal, max_q_len: int, *, lse=None, w
 
 
 # The serving calls below are made once a token: the dg_bind module checks and marshals their arguments, because a
-# call of a few microseconds on the device waits for the host.
+# call of a few microseconds on the device waits for the host.  It is loaded by the first of them; nothing else
+# needs it.
 def _serving():
+    global _bind
     if _bind is None:
-        load()
+        lib = load()
+        if not os.path.exists(_build.BIND):
+            raise RuntimeError(f"{os.path.basename(_build.BIND)}, which the serving calls need, not found at "
+                               f"{_build.BIND}: build it with entropy_bounded_denoising_gb300.build.build_bind()")
+        loader = importlib.machinery.ExtensionFileLoader("dg_bind", _build.BIND)
+        bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("dg_bind", loader))
+        loader.exec_module(bind)
+        names = ("dg_kv_append", "dg_paged_attention", "dg_paged_attention_workspace_bytes", "dg_adjust_logits")
+        bind.connect(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+        _bind = bind
     return _bind
 
 

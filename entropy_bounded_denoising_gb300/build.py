@@ -2,17 +2,20 @@
 
 Each translation unit is compiled by its own nvcc process, in parallel, then linked into
 ``entropy_bounded_denoising_gb300/_build/libdg.so``; beside it ``dg_bind-*.so``, the serving calls'
-Python module (host code against PyTorch's headers).  Objects are rebuilt only when a source or
-header is newer than the libraries.
+Python module (host code against Python's and PyTorch's headers; where they are missing the library is
+built all the same, with a warning, and only the serving calls' Python forms are closed).  Either is
+rebuilt only when one of its sources or headers is newer.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import contextlib
 import glob
 import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 import torch
 
@@ -47,15 +50,14 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [BIND_SRC, HEADER, __file__]
-    return any(os.path.getmtime(p) > t for p in deps)
+def _stale(target: str, deps: list[str]) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(p) > os.path.getmtime(target)
+                                             for p in deps + [HEADER, __file__])
 
 
-def _build_bind() -> None:
+def build_bind() -> str:
+    """The serving calls' Python module; raises with the compiler's message where it cannot be built."""
+    os.makedirs(OUT, exist_ok=True)
     tmp = BIND + f".tmp{os.getpid()}"
     lib = os.path.join(TORCH, "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -63,14 +65,30 @@ def _build_bind() -> None:
            "-isystem", os.path.join(TORCH, "include"), "-isystem", os.path.join(_cuda(), "include"),
            "-isystem", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), BIND_SRC, "-o", tmp,
            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"g++ failed for {BIND_SRC}: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BIND)
+    return BIND
+
+
+def _try_bind() -> None:
+    try:
+        build_bind()
+    except RuntimeError as e:
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(BIND)   # an older one, whose calls may not be the library's
+        warnings.warn(f"the serving calls' Python module was not built: {e}", stacklevel=3)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    bind_stale = force or _stale(BIND, [BIND_SRC])
+    if not force and not _stale(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh"))):
+        if bind_stale:
+            _try_bind()
         return LIB
     os.makedirs(OUT, exist_ok=True)
     nvcc = _nvcc()
@@ -86,9 +104,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources()) + 1) as ex:
-        bind = ex.submit(_build_bind)
+        bind = ex.submit(_try_bind) if bind_stale else None
         objs = list(ex.map(compile_one, sources()))
-        bind.result()
+        if bind:
+            bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-o", tmp, *objs,
            "-Xcompiler", "-fPIC", "-lcudart"]

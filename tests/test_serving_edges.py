@@ -1,12 +1,15 @@
 """Host tests of the serving calls (dg_kv_append, dg_paged_attention, dg_adjust_logits) at the edge of what
 include/dg.h allows; nothing is launched."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import entropy_bounded_denoising_gb300 as dg
-from entropy_bounded_denoising_gb300 import _native
+from entropy_bounded_denoising_gb300 import _native, build
 
 
 def _kv(**kw):
@@ -68,3 +71,48 @@ def test_the_workspace_for_a_larger_call_serves_the_smaller_ones():
                     assert size[n, q] > 0
                     assert i == 0 or size[n, q] >= size[counts[i - 1], q], (n, q, Hq, Hkv, D)
                     assert j == 0 or size[n, q] >= size[n, queries[j - 1]], (n, q, Hq, Hkv, D)
+
+
+def test_the_step_needs_the_library_alone():
+    """Without the serving calls' Python module the library loads and the other calls work; a serving call says what
+    is missing."""
+    code = ("import entropy_bounded_denoising_gb300 as dg, torch\n"
+            "from entropy_bounded_denoising_gb300 import _native\n"
+            "_native._build.BIND = '/nonexistent/dg_bind.so'\n"
+            "lib = dg.load()\n"
+            "assert dg.dg_denoise_workspace_bytes(1, 16, 1024) > 0 and dg.version() >= 100\n"
+            "assert lib.dg_denoise_step(None, 0, 8, 1, 16, 8, None, 0, *([None] * 11), None, 0, None) == dg.DG_ERR_INVALID_ARG\n"
+            "assert dg.dg_paged_attention_workspace_bytes(1, 1, 8, 8, 64) > 0\n"
+            "x = torch.zeros((1, 4, 64))\n"
+            "try:\n"
+            "    dg.dg_adjust_logits(x, torch.zeros(36, dtype=torch.uint8))\n"
+            "except RuntimeError as e:\n"
+            "    assert 'build_bind' in str(e)\n"
+            "else:\n"
+            "    raise AssertionError('no error')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("how", ["no compiler", "no headers"])
+def test_the_library_builds_without_what_the_python_module_needs(monkeypatch, tmp_path, how):
+    build.build()
+    run, old = subprocess.run, tmp_path / "dg_bind.so"
+    old.write_bytes(b"of another source")
+    os.utime(old, (0, 0))
+
+    def fails(cmd, **kw):
+        if cmd[0] != "g++":
+            return run(cmd, **kw)
+        if how == "no compiler":
+            raise FileNotFoundError("g++")
+        return subprocess.CompletedProcess(cmd, 1, "", "Python.h: No such file or directory")
+
+    monkeypatch.setattr(build, "BIND", str(old))
+    monkeypatch.setattr(build.subprocess, "run", fails)
+    with pytest.warns(UserWarning, match="serving calls"):
+        assert build.build() == build.LIB
+    assert not old.exists()              # a stale one is not left to be loaded
+    with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
+        build.build_bind()
