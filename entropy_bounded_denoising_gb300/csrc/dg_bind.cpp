@@ -139,8 +139,9 @@ struct Cache {
             if (t->dim() != 4 || t->stride(3) != 1)
                 refuse(PyExc_ValueError, c.named(t == &k ? "k_cache" : "v_cache") +
                                              " must be [n_pages, page_size, Hkv, D] with contiguous heads");
-        if (k.sizes() != v.sizes() || k.strides() != v.strides())
-            refuse(PyExc_ValueError, std::string(c.fn) + ": k_cache and v_cache must have one layout");
+        bool alike = k.sizes() == v.sizes();
+        for (int i = 0; alike && i < 3; ++i) alike = k.size(i) == 1 || k.stride(i) == v.stride(i);
+        if (!alike) refuse(PyExc_ValueError, std::string(c.fn) + ": k_cache and v_cache must have one layout");
         kv.kv_len = static_cast<const int32_t*>(c.whole(len, "kv_len", at::kInt, {-1}));
         if (len == Py_None) refuse(PyExc_TypeError, c.named("kv_len") + " must be a tensor");
         n_seq = THPVariable_Unpack(len).size(0);

@@ -297,3 +297,17 @@ def test_one_workspace_serves_a_programs_calls(D):
         o, lse = torch.full_like(b.q, 7.0), torch.full(b.q.shape[:2], 7.0, device=DEV)
         dg.dg_paged_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, b.causal, rows, lse=lse, workspace=ws)
         ref.check_attention(b, o, lse, skip=range(3, n))
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+def test_caches_whose_strides_differ_where_the_extent_is_one(rows):
+    b = ref.Batch([(rows, 400, 1)] * 3, 8, 1, 64, 16, seed=rows).fill_keys()
+    ends = []
+    for v in (b.v_cache, b.v_cache.transpose(1, 2).contiguous().transpose(1, 2)):
+        b.v_cache = v
+        assert _append_copies(b) == 0
+        o = torch.zeros_like(b.q)
+        dg.dg_paged_attention(b.q, b.k_cache, v, o, b.table, b.cu, b.kv_len, b.causal, rows)
+        ref.check_attention(b, o, None)
+        ends.append(o)
+    assert torch.equal(*ends)

@@ -116,3 +116,16 @@ def test_the_library_builds_without_what_the_python_module_needs(monkeypatch, tm
     assert not old.exists()              # a stale one is not left to be loaded
     with pytest.raises(RuntimeError, match="g\\+\\+ failed"):
         build.build_bind()
+
+
+@pytest.mark.parametrize("shape,order,alike", [((3, 8, 1, 64), (0, 2, 1, 3), True), ((1, 8, 2, 64), (1, 0, 2, 3), True),
+                                               ((1, 8, 1, 64), (2, 1, 0, 3), True), ((3, 8, 2, 64), (0, 2, 1, 3), False)])
+def test_strides_of_extents_of_one_may_differ(shape, order, alike):
+    """The stride of an extent of one says nothing: caches that differ in it alone have one layout."""
+    k = torch.zeros(shape, dtype=torch.bfloat16)
+    v = torch.zeros([shape[i] for i in order], dtype=torch.bfloat16).permute(order)
+    assert v.shape == k.shape and v.stride() != k.stride()
+    x = torch.zeros((4, shape[2], 64), dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError, match="device tensors" if alike else "one layout"):   # the check that comes next
+        dg.dg_kv_append(x, x, k, v, i32(1, 3), i32(2), i32(1))
