@@ -835,11 +835,12 @@ bool in_pairs(int32_t max_q_len, int32_t group, int32_t Hkv, int32_t D) {
 // keys, 256 queries 44 / 33.  Heads of 64, 16 queries of 8 heads, 32 requests over 4k keys 55 / 65.  Over 216 shapes
 // (heads of 64, 128, 256, 1 to 16 query heads a key head, 1 to 256 queries) the rule loses 0.1 % to the better
 // path on average, 24 % at most.
-bool split_path(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D) {
-    const int64_t tile_ctas = D == 256 ? 152 : 304;
-    const int64_t here = (int64_t)n_seq * Hkv * (((int64_t)max_q_len * (Hq / Hkv) + 7) / 8);
-    const int64_t there = (int64_t)n_seq * Hq * (((int64_t)max_q_len + 127) / 128) * (D == 64 ? 2 : 1);
-    return max_q_len == 1 || here <= std::max(there, tile_ctas);
+bool split_path(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D, int sms) {
+    const int64_t tile_ctas = D == 256 ? sms : 2 * sms;
+    // passes a sequence, which fit 64 bits for every call that the checks let through
+    const int64_t here = Hkv * (((int64_t)max_q_len * (Hq / Hkv) + 7) / 8);
+    const int64_t there = Hq * (((int64_t)max_q_len + 127) / 128) * (D == 64 ? 2 : 1);
+    return here <= std::max(there, tile_ctas / n_seq);
 }
 
 size_t split_bytes(int rows, int32_t D) {
@@ -904,11 +905,12 @@ extern "C" dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* ca
     const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
     if (ok != DG_OK) return ok;
     const int rows = item_rows(max_q_len, Hq / Hkv);
-    const bool split = split_path(n_seq, max_q_len, Hq, Hkv, D);
     if (!workspace || workspace_bytes < dg_paged_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D))
         return DG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
-    if (!split)
+    const int sms = dghost::sm_count();
+    if (sms <= 0) return DG_ERR_CUDA;
+    if (!split_path(n_seq, max_q_len, Hq, Hkv, D, sms))
         return dghost::attention_pages(q, a.kv, o, lse, cu_q, causal, n_seq, max_q_len, total_q, Hq, Hkv, D, window, scale,
                                        workspace, (cudaStream_t)stream);
     a.q = q;
