@@ -9,10 +9,10 @@
 // the lists are read from L2 once a block.
 // Bound by memory: in place only vectors with an edited or excluded token are touched, and a vector that is
 // excluded whole is written without being read.  8 canvases of 256 positions, fp32, 152k tokens, half of them
-// excluded: 283 us; nearly every vector has an allowed token, so 0.95 GB are read and 0.88 written, 270 us
+// excluded: 282 us; nearly every vector has an allowed token, so 0.95 GB are read and 0.88 written, 270 us
 // at a copy's rate.  A grammar that leaves 1 % of 262k bf16 tokens, in place: 222 us for 1.01 GB written and
 // 0.33 read (a vector with an allowed token is read, and 64 bytes come with it; writing only the excluded
-// tokens of such vectors without reading them took 420).  One canvas over 32k tokens: 9.3 us, of
+// tokens of such vectors without reading them took 420).  One canvas over 32k tokens: 9.6 us, of
 // which a copy of the logits takes 6.6 and the mask alone 7.5; the rest is the wait for the lists.
 #include <cuda_runtime.h>
 
@@ -27,8 +27,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 4;
 // Rows in flight a thread: the registers of the lists' addends hold four rows more when a call gives no lists.
-// Masks alone, in place, bf16, 1 % of 250k tokens left: 277 us with four, 260 with six, 238 with eight (half of
-// 131k fp32 tokens left: 318, 320, 327).
+// Masks alone, in place, 8 canvases of 256, four / six / eight rows: bf16, 1 % of 250k tokens left, 278 / 261 / 239 us,
+// of 262k 231 / 220 / 222; fp32, half of 131k left, 322 / 320 / 326.
 constexpr int unroll_of(bool lists) { return lists ? 4 : 8; }
 constexpr int kMaxRows = 64; // rows of a block, at most
 constexpr int kEarly = 2;    // entries of each list that a thread reads before anything else
@@ -59,7 +59,7 @@ DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
 }
 
 // 16 bytes, fetching no more than the 64 around them: a mask that leaves few tokens has few vectors read, and 128
-// around each were half of the row (1 % of 262k bf16 tokens left, in place: 256 us without the hint, 242 with it;
+// around each were half of the row (1 % of 262k bf16 tokens left, in place: 249 us without the hint, 222 with it;
 // where most are read it makes no difference).  Not volatile: a row is read before its own store and after no
 // other's.
 DG_DEVINL uint4 load16(const unsigned char* p) {

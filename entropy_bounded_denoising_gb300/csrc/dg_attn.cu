@@ -33,8 +33,13 @@
 // value tiles come page by page, and its set-up runs beside the plan kernel, or the caller's last one when there
 // is no plan.  Its MMAs are issued by the elected
 // lane of a uniform warp.  8 canvases of 256 queries over 2.3k keys, 16 query over 8 key heads of 128: 46 us,
-// 850 TFLOP/s; 32 of them over 4k keys 173 to 181 us, 970 to 1000 TFLOP/s (the first has 256 items for 304 CTAs, so half the
+// 840 TFLOP/s; 32 of them over 4096 keys 254 us, 1080 TFLOP/s (the first has 256 items for 304 CTAs, so half the
 // SMs work two while the others work one; per tile the softmax's chain of dependent steps bounds both).
+//
+// Weights are rounded to bf16 for the product with V, which takes bf16; scores, maxima and sums stay in fp32, and O
+// is divided by the sum of the unrounded weights, so a row that few keys decide is off by up to half a step of their
+// weights, 2^-8.  (Dividing by the sum of the rounded ones, as dg_paged_attn.cu does, cancels that, and costs 13 %
+// here: 44.5 / 50.3 us for the 8 canvases over pages, 254 / 277 for the 32.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -89,8 +89,7 @@ DG_DEVINL void rotate_neighbours(uint4& x, const float2* cs) {
 DG_DEVINL int exponent_of(double w) { return (int)(__double2hiint(w) >> 20) & 0x7ff; }
 DG_DEVINL bool has_angle(double w) { return exponent_of(w) < 1023 + 53; }
 
-// A call of its own: such frequencies are rare, and in line their instructions take 0.25 us more of 64 rows
-// (3.25 / 3.07) and 6 more of 30k (144.5 / 138.0).
+// A call of its own: such frequencies are rare, and in line their instructions cost 64 rows 0.2 us and 30k rows 6.
 __device__ __noinline__ uint64_t far_turns(uint64_t m, int e) {   // (top, mid, low) 2^(e - 1205) turns, 66 <= down <= 116
     const uint64_t lo = m * 0xA2F9836E4E441529ull, hi = __umul64hi(m, 0xA2F9836E4E441529ull);
     const uint64_t mid = lo + __umul64hi(m, 0xFC2757D1F534DDC0ull), top = hi + (mid < lo ? 1ull : 0ull);
@@ -126,12 +125,13 @@ DG_DEVINL int row_position(const AppendArgs& a, int t, int s) {
 
 // A block's rows are looked up and its sines computed while its data is on the way: every thread
 // first asks for the 32 bytes a task that it will store.
-// Bound by memory from a few thousand rows on: 30k rows of 32 heads of 256 (907 MB to and fro) take 138 us,
-// 6.6 TB/s.  Below, by its chain of dependent reads (offsets, lengths, page) and the launch: 64 rows of 32 heads of
-// 128 take 3.1 us, 2048 rows 9.1, where a copy of their 34 MB takes 6.6.
+// Bound by memory from a few thousand rows on: 30k rows of 32 heads of 256 (907 MB to and fro) take 139 us,
+// 6.5 TB/s.  Below, by its chain of dependent reads (offsets, lengths, page) and the launch: 64 rows of 32 heads of
+// 128 take 3.4 us, 2048 rows 9.1, where a copy of their 34 MB takes 6.6.
 // PerThread: a thread's tasks.  One, with the most threads an SM holds, while every task has a
 // place at once; four where there are several rounds of blocks (more bytes on the way and fewer lookups
-// a byte): 64 rows take 3.3 us with one and 4.8 with four, 2048 rows 9.3 and 8.9, the 30k rows 149 and 138.
+// a byte).  One against four, the same rows again and again: 64 rows 3.4 and 5.1 us, 2048 rows 8.4 and 8.2, the 30k
+// rows 154 and 138.
 template <bool Interleaved, int PerThread>
 __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_append(const AppendArgs a) {
     constexpr int kPerThread = PerThread, kUnit = kAppendThreads * PerThread;   // tasks of a block
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_a
     dg::pdl_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // Every sequence is checked, whether a row finds it or not, and every frequency: a thread each, in blocks of
-    // their own (64 rows 3.0 us; with the sequences checked in the first block, before its lookups, 3.2).
+    // their own (0.05 us of 64 rows' 3.4; in the first block, before its lookups, the sequences alone cost 0.25).
     if (blockIdx.x >= a.row_blocks) {
         const int s = (int)(blockIdx.x - a.row_blocks) * kAppendThreads + tid;
         if ((s < a.n_seq && !dg::paged_seq(a.kv, a.cu_q, a.total_q, s, 0x7fffffff).ok) ||

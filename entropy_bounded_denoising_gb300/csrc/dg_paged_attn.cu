@@ -19,10 +19,10 @@
 // either -- the tensor pipe is 9 % busy over 8k keys -- and a tile of TMEM would only add a round trip between
 // the two products.)
 //
-// Measured: 64 tokens over up to 8k keys, 8 key heads of 128: 221 us, 6.7 TB/s, 98 % of the rate of a copy;
+// Measured: 64 tokens over up to 8k keys, 8 key heads of 128: 216 to 222 us, 6.7 TB/s, 98 % of the rate of a copy;
 // one token over 128k keys, 4 key heads of 256: 88 us, 90 %.  Short of that: one sequence over 1k keys takes
-// 7.9 us, two launches and five reads that wait for one another (lengths, pages, keys; list, pieces); 250
-// windows of 1000 keys at 8 heads of 64 take 85 us, 87 %, of which start and join are 8; and items of few keys
+// 8.3 us, two launches and five reads that wait for one another (lengths, pages, keys; list, pieces); 250
+// windows of 1000 keys at 8 heads of 64 take 84 us, 88 %, of which start and join are 8; and items of few keys
 // cost a CTA their latency: 1288 items of 3 keys, heads of 256, 35 us.
 #include <cuda_runtime.h>
 
@@ -833,8 +833,10 @@ bool in_pairs(int32_t max_q_len, int32_t group, int32_t Hkv, int32_t D) {
 // Measured (us here / there), 16 query over 8 key heads of 128: 32 requests over 4k keys, 8 queries 90 / 137, 16
 // queries 167 / 137; 8 requests over 2.3k keys, 16 queries 32 / 35, 24 queries 40 / 35, 64 queries 86 / 36; one over 2k
 // keys, 256 queries 44 / 33.  Heads of 64, 16 queries of 8 heads, 32 requests over 4k keys 55 / 65.  Over 216 shapes
-// (heads of 64, 128, 256, 1 to 16 query heads a key head, 1 to 256 queries) the rule loses 0.1 % to the better
-// path on average, 24 % at most.
+// (heads of 64, 128, 256, 1 to 16 query heads a key head, 1 to 256 queries, the same number in every sequence) the
+// rule loses 0.1 % to the better path on average, 24 % at most.  A call that mixes lengths goes by its longest, and
+// its single tokens then cost a tile each: 63 tokens over 8k keys beside a prompt of 512 take 484 us, in two calls 331;
+// one over 128k beside a canvas 1595, in two calls 128.
 bool split_path(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D, int sms) {
     const int64_t tile_ctas = D == 256 ? sms : 2 * sms;
     // passes a sequence, which fit 64 bits for every call that the checks let through

@@ -441,9 +441,16 @@ DG_API dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v,
  * offsets lie outside [0, total_q], with kv_len < 0, 0 < kv_len < q_len, kv_len > max_pages *
  * page_size or kv_len > 2^31 - 2^16 raises DG_DEV_BAD_PARAM and is skipped (its rows are not
  * written); one with more than max_q_len queries raises it too and gets at least its first max_q_len
- * rows; one that needs a page outside [0, n_pages) raises it and its rows are unspecified.  Rows of no
- * sequence are not written.
- * Limits and errors as dg_attention and dg_kv_append.  One or two kernels. */
+ * rows; one that needs a page outside [0, n_pages) raises it and its rows are unspecified, as are rows that
+ * two sequences claim (offsets that go back).  Rows of no sequence are not written.  (With n_seq or total_q 0
+ * nothing runs and nothing is reported.)
+ * Scores, maxima and sums are in fp32; the weights are rounded to bf16 for the product with v, as in
+ * dg_attention.  A call of few queries a sequence divides by the sum of the rounded weights (a row that one key
+ * decides is its value), one of many by the sum of the unrounded ones.  Which of the two forms a
+ * call takes goes by max_q_len: single tokens over long contexts are better in a call of their own than beside
+ * a prompt or a canvas, whose form reads their keys once a query head and does not split them.
+ * Limits and errors as dg_attention and dg_kv_append, natural alignment of lse, cu_q and the cache's tables
+ * included.  One or two kernels. */
 DG_API size_t dg_paged_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D);
 DG_API dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
                                     const int32_t* cu_q, const uint8_t* causal, int32_t n_seq, int32_t max_q_len,
@@ -470,7 +477,9 @@ typedef struct {
  *   y = -inf                                                    if the position's mask excludes t.
  * fp32 with one rounding to the logits' type; a token with neither history, bias nor mask keeps its
  * bits.  A bias of -inf excludes its token.  A mask that excludes every token leaves a row of -inf,
- * which dg_denoise_step reports with DG_DEV_EMPTY_ROW.  Repeated tokens in a canvas's bias list add up, in list order.
+ * which dg_denoise_step reports with DG_DEV_EMPTY_ROW.  Repeated tokens in a canvas's bias list add up, in list
+ * order.  Edits come between dg_lm_head_logits and dg_denoise_step: dg_lm_head_denoise_step takes its
+ * statistics while it makes the logits, before any edit, and cannot be used for canvases that have some.
  *   logits      (device) [n_canvas][L][ld] of dtype, as in dg_denoise_step; out (device, out) the
  *               same with ld_out; may be logits itself when ld_out = ld (then only what changes
  *               is written), else must not overlap it.  Columns past V are not written.
