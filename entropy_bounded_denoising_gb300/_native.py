@@ -101,6 +101,14 @@ def load(path: str | None = None):
                                     P, sz, P]),
         "dg_adjust_logits": (st, [P, ctypes.c_int, i64, P, i64, i64, i32, i64, P, P, P, i64, P, P, P, P, i64,
                                   P, i64, i32, P, P]),
+        "dg_kv_append_norm": (st, [P, i64, P, i64, P, i64, P, P, i32, i64, i32, i32, i32, P, P, ctypes.c_float, P, P, i32,
+                                   i32, PagedKV, P]),
+        "dg_tree_attention_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
+        "dg_tree_attention": (st, [P, PagedKV, P, P, P, P, i32, P, i32, i32, i64, i32, i32, i32, i32, i32,
+                                   ctypes.c_float, P, sz, P]),
+        "dg_sink_attention": (st, [P, PagedKV, P, P, P, i32, i32, i64, i32, i32, i32, i32, i32, ctypes.c_float, P, sz, P]),
+        "dg_verify_drafts": (st, [P, ctypes.c_int, i64, P, P, P, i64, P, i32, i64, i64, P, P, P, P, P, P, P]),
+        "dg_kv_keep": (st, [PagedKV, i32, i64, P, i32, i64, i32, i32, P, P, P, P]),
         "dg_embed_canvas": (st, [P, i64, i64, P, i32, P, ctypes.c_float, P, P]),
         "dg_commit": (st, [P, P, P, i64, i32, P, P, P, P, P]),
         "dg_philox_words": (st, [u64, u32, u32, u32, u32, u32, i64, P, P]),
@@ -131,7 +139,9 @@ def exported_symbols() -> list[str]:
                         "dg_self_cond_probs", "dg_gemm_workspace_bytes", "dg_gemm_bf16",
                         "dg_gemm_bf16_noalloc", "dg_choice_probs", "dg_embed_canvas", "dg_commit", "dg_attention",
                         "dg_attention_workspace_bytes", "dg_kv_append", "dg_paged_attention",
-                        "dg_paged_attention_workspace_bytes", "dg_adjust_logits",
+                        "dg_paged_attention_workspace_bytes", "dg_adjust_logits", "dg_kv_append_norm",
+                        "dg_tree_attention", "dg_tree_attention_workspace_bytes", "dg_sink_attention",
+                        "dg_verify_drafts", "dg_kv_keep",
                         "dg_philox_words", "dg_get_device_status", "dg_clear_device_status",
                         "dg_probe_bounded_wait",
                         "dg_status_string", "dg_version", "dg_launch_count") if hasattr(lib, n)]
@@ -440,7 +450,9 @@ def _serving():
         loader = importlib.machinery.ExtensionFileLoader("dg_bind", _build.BIND)
         bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("dg_bind", loader))
         loader.exec_module(bind)
-        names = ("dg_kv_append", "dg_paged_attention", "dg_paged_attention_workspace_bytes", "dg_adjust_logits")
+        names = ("dg_kv_append", "dg_paged_attention", "dg_paged_attention_workspace_bytes", "dg_adjust_logits",
+                 "dg_kv_append_norm", "dg_tree_attention", "dg_tree_attention_workspace_bytes", "dg_sink_attention",
+                 "dg_verify_drafts", "dg_kv_keep")
         bind.connect(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
         _bind = bind
     return _bind
@@ -487,6 +499,79 @@ def dg_paged_attention(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal,
                   _scratch(rc[0], q.device, stream), st)
     if check and rc:
         _check("dg_paged_attention", rc)
+    return rc
+
+
+def dg_kv_append_norm(k, v, k_cache, v_cache, page_table, cu_q, kv_len, *, inv_freq=None, interleaved=False, q=None,
+                      q_out=None, q_norm=None, k_norm=None, eps: float = 1e-6, positions=None, stream=None,
+                      check=True) -> int:
+    """dg_kv_append with every query and key head x turned to x * w / sqrt(mean(x^2) + eps) before the rotation
+    (q_norm, k_norm: w [D] float32, None = as it is) and rotated by positions [total] int32 (None: the
+    slots' numbers)."""
+    rc = _serving().kv_append_norm(k, v, k_cache, v_cache, page_table, cu_q, kv_len, inv_freq, interleaved, q, q_out,
+                                   None if stream is None else _s(stream), q_norm, k_norm, eps, positions)
+    if check and rc:
+        _check("dg_kv_append_norm", rc)
+    return rc
+
+
+def dg_tree_attention_workspace_bytes(n_seq: int, max_q_len: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load().dg_tree_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D))
+
+
+def dg_tree_attention(q, k_cache, v_cache, o, page_table, cu_q, kv_len, tree_mask, max_q_len: int, *, positions=None,
+                      lse=None, window: int = -1, sinks: int = 0, scale: float | None = None, workspace=None,
+                      stream=None, check=True) -> int:
+    """Attention of drafted trees over the paged cache: a sequence's last q_len keys are its nodes, seen by query i
+    where bit j of tree_mask [total_q, words] (int32 words) is set; the context before them is seen whole, or with
+    window >= 0 from positions [total_q] (int32) - window on and its first `sinks` tokens.  Other arguments as
+    dg_paged_attention."""
+    call, st = _serving().tree_attention, None if stream is None else _s(stream)
+    rc = call(q, k_cache, v_cache, o, page_table, cu_q, kv_len, max_q_len, lse, window, sinks, scale, workspace, st,
+              tree_mask, positions)
+    if workspace is None:   # rc: the bytes it needs; nothing has run
+        rc = call(q, k_cache, v_cache, o, page_table, cu_q, kv_len, max_q_len, lse, window, sinks, scale,
+                  _scratch(rc[0], q.device, stream), st, tree_mask, positions)
+    if check and rc:
+        _check("dg_tree_attention", rc)
+    return rc
+
+
+def dg_sink_attention(q, k_cache, v_cache, o, page_table, cu_q, kv_len, max_q_len: int, *, window: int, sinks: int,
+                      lse=None, scale: float | None = None, workspace=None, stream=None, check=True) -> int:
+    """Causal attention over the paged cache where the query at position p sees keys p - window .. p and the first
+    `sinks`.  Other arguments as dg_paged_attention; the workspace is dg_tree_attention's."""
+    call, st = _serving().sink_attention, None if stream is None else _s(stream)
+    rc = call(q, k_cache, v_cache, o, page_table, cu_q, kv_len, max_q_len, lse, window, sinks, scale, workspace, st)
+    if workspace is None:   # rc: the bytes it needs; nothing has run
+        rc = call(q, k_cache, v_cache, o, page_table, cu_q, kv_len, max_q_len, lse, window, sinks, scale,
+                  _scratch(rc[0], q.device, stream), st)
+    if check and rc:
+        _check("dg_sink_attention", rc)
+    return rc
+
+
+def dg_verify_drafts(logits, tokens, cu_q, temperature, uniforms, next_uniforms, n_accept, path, out_tokens, *,
+                     parents=None, draft_probs=None, V=None, stream=None, check=True) -> int:
+    """Verify drafted tokens against softmax(logits / temperature): logits [total, >= V] (bf16 or fp32, row i predicts the
+    token behind node i), nodes packed by cu_q [n + 1], each sequence's root first; parents [total] (None:
+    chains) or draft_probs [total, >= V] float32.  Writes n_accept [n], path [total] (accepted nodes, the root first) and
+    out_tokens [total] (accepted tokens and the next one), -1 behind them."""
+    rc = _serving().verify_drafts(logits, tokens, cu_q, temperature, uniforms, next_uniforms, n_accept, path, out_tokens,
+                                  parents, draft_probs, V, None if stream is None else _s(stream))
+    if check and rc:
+        _check("dg_verify_drafts", rc)
+    return rc
+
+
+def dg_kv_keep(k_cache, v_cache, page_table, cu_q, kv_len, path, n_accept, new_len, *, stream=None, check=True) -> int:
+    """Move the accepted nodes (path [total], n_accept [n], of dg_verify_drafts) to the slots behind the context, in every
+    layer of k_cache, v_cache [n_pages, page_size, Hkv, D] or [n_layers, n_pages, ...]; new_len [n] int32 gets
+    the lengths (not in place of kv_len)."""
+    rc = _serving().kv_keep(k_cache, v_cache, page_table, cu_q, kv_len, path, n_accept, new_len,
+                            None if stream is None else _s(stream))
+    if check and rc:
+        _check("dg_kv_keep", rc)
     return rc
 
 

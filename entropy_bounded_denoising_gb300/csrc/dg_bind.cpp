@@ -1,5 +1,6 @@
 // dg_bind.cpp -- the checks and the marshalling of the serving calls (dg_kv_append, dg_paged_attention,
-// dg_adjust_logits) for Python.
+// dg_adjust_logits, and for drafted tokens dg_kv_append_norm, dg_tree_attention, dg_sink_attention,
+// dg_verify_drafts, dg_kv_keep) for Python.
 //
 // These calls are made once a token and a layer, and take 3 to 9 us on the device for a few sequences.
 // Checked in Python and passed through ctypes they took the host 10.5 to 12.9 us, which a decoding loop waited
@@ -24,6 +25,12 @@ decltype(&dg_kv_append) g_append = nullptr;
 decltype(&dg_paged_attention) g_attention = nullptr;
 decltype(&dg_paged_attention_workspace_bytes) g_attention_bytes = nullptr;
 decltype(&dg_adjust_logits) g_adjust = nullptr;
+decltype(&dg_kv_append_norm) g_append_norm = nullptr;
+decltype(&dg_tree_attention) g_tree = nullptr;
+decltype(&dg_tree_attention_workspace_bytes) g_tree_bytes = nullptr;
+decltype(&dg_sink_attention) g_sink = nullptr;
+decltype(&dg_verify_drafts) g_verify = nullptr;
+decltype(&dg_kv_keep) g_keep = nullptr;
 
 struct Raised {};   // a Python error is set
 
@@ -127,20 +134,36 @@ int64_t integer(PyObject* o, int64_t lo, int64_t hi, const char* fn, const char*
 int64_t int32(PyObject* o, const char* fn, const char* name) { return integer(o, INT32_MIN, INT32_MAX, fn, name); }
 
 // dg_paged_kv of k_cache, v_cache [n_pages, page_size, Hkv, D] (any strides of the first three) and
-// page_table [n_seq, max_pages], kv_len [n_seq].
+// page_table [n_seq, max_pages], kv_len [n_seq]; where `layers` allows it, of [n_layers, n_pages, ...] too.
 struct Cache {
     dg_paged_kv kv;
-    int64_t n_seq, Hkv, D;
+    int64_t n_seq, Hkv, D, n_layers = 1, layer_stride = 0;
 
-    Cache(Call& c, PyObject* ko, PyObject* vo, PyObject* table, PyObject* len) {
-        const at::Tensor& k = c.tensor(ko, "k_cache", at::kBFloat16);
-        const at::Tensor& v = c.tensor(vo, "v_cache", at::kBFloat16);
-        for (const at::Tensor* t : {&k, &v})
-            if (t->dim() != 4 || t->stride(3) != 1)
-                refuse(PyExc_ValueError, c.named(t == &k ? "k_cache" : "v_cache") +
-                                             " must be [n_pages, page_size, Hkv, D] with contiguous heads");
-        bool alike = k.sizes() == v.sizes();
+    Cache(Call& c, PyObject* ko, PyObject* vo, PyObject* table, PyObject* len, bool layers = false) {
+        const at::Tensor& kt = c.tensor(ko, "k_cache", at::kBFloat16);
+        const at::Tensor& vt = c.tensor(vo, "v_cache", at::kBFloat16);
+        for (const at::Tensor* t : {&kt, &vt})
+            if ((t->dim() != 4 && !(layers && t->dim() == 5)) || t->stride(t->dim() - 1) != 1)
+                refuse(PyExc_ValueError, c.named(t == &kt ? "k_cache" : "v_cache") + " must be [" +
+                                             (layers ? "n_layers (or not), " : "") +
+                                             "n_pages, page_size, Hkv, D] with contiguous heads");
+        const int skip = kt.dim() == 5 ? 1 : 0;
+        struct View {   // the four extents and strides of a layer
+            const at::Tensor& t;
+            int skip;
+            int64_t size(int i) const { return t.size(i + skip); }
+            int64_t stride(int i) const { return t.stride(i + skip); }
+            void* data_ptr() const { return t.data_ptr(); }
+        };
+        const View k{kt, skip}, v{vt, skip};
+        bool alike = kt.sizes() == vt.sizes();
         for (int i = 0; alike && i < 3; ++i) alike = k.size(i) == 1 || k.stride(i) == v.stride(i);
+        if (alike && skip) {
+            n_layers = kt.size(0);
+            layer_stride = n_layers > 1 ? kt.stride(0) : 0;
+            alike = n_layers <= 1 || kt.stride(0) == vt.stride(0);
+            if (n_layers > INT32_MAX) refuse(PyExc_ValueError, std::string(c.fn) + ": an extent of the cache is out of range");
+        }
         if (!alike) refuse(PyExc_ValueError, std::string(c.fn) + ": k_cache and v_cache must have one layout");
         kv.kv_len = static_cast<const int32_t*>(c.whole(len, "kv_len", at::kInt, {-1}));
         if (len == Py_None) refuse(PyExc_TypeError, c.named("kv_len") + " must be a tensor");
@@ -181,13 +204,16 @@ bool takes(Py_ssize_t n, Py_ssize_t want) {
     return false;
 }
 
-// k, v, k_cache, v_cache, page_table, cu_q, kv_len, inv_freq, interleaved, q, q_out, stream -> status
+// k, v, k_cache, v_cache, page_table, cu_q, kv_len, inv_freq, interleaved, q, q_out, stream -> status;
+// with norms q_norm, k_norm, eps, positions follow
+template <bool Norm>
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!takes(n, 12)) return nullptr;
+    if (!takes(n, Norm ? 16 : 12)) return nullptr;
     return guarded([&]() -> PyObject* {
-        Call c{"dg_kv_append"};
+        const std::string fn = Norm ? "dg_kv_append_norm" : "dg_kv_append";
+        Call c{fn.c_str()};
         PyObject *q = a[9], *q_out = a[10];
-        if ((q == Py_None) != (q_out == Py_None)) refuse(PyExc_ValueError, "dg_kv_append: q and q_out come together");
+        if ((q == Py_None) != (q_out == Py_None)) refuse(PyExc_ValueError, fn + ": q and q_out come together");
         const Cache kv(c, a[2], a[3], a[4], a[6]);
         int64_t total, ldk, v_rows, ldv, q_rows = 0, ldq = 0, Hq = kv.Hkv;
         const void* kp = c.rows(a[0], "k", kv.Hkv, kv.D, total, ldk);
@@ -200,18 +226,34 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             op = c.whole(q_out, "q_out", at::kBFloat16, {q_rows, Hq, kv.D});
         }
         if (v_rows != total || (q != Py_None && q_rows != total))
-            refuse(PyExc_ValueError, "dg_kv_append: q, k and v must have as many rows");
-        if (Hq > INT32_MAX) refuse(PyExc_ValueError, "dg_kv_append: too many heads");
+            refuse(PyExc_ValueError, fn + ": q, k and v must have as many rows");
+        if (Hq > INT32_MAX) refuse(PyExc_ValueError, fn + ": too many heads");
         const void* cu = c.whole(a[5], "cu_q", at::kInt, {kv.n_seq + 1});
         const void* w = c.whole(a[7], "inv_freq", at::kDouble, {-1});
         const int64_t half = w || a[7] != Py_None ? THPVariable_Unpack(a[7]).size(0) : 0;
-        if (half > INT32_MAX / 2) refuse(PyExc_ValueError, "dg_kv_append: inv_freq is too long");
+        if (half > INT32_MAX / 2) refuse(PyExc_ValueError, fn + ": inv_freq is too long");
         const int interleaved = PyObject_IsTrue(a[8]);
         if (interleaved < 0) throw Raised();
+        const void *qn = nullptr, *kn = nullptr, *pos = nullptr;
+        double eps = 0.0;
+        if constexpr (Norm) {
+            qn = c.whole(a[12], "q_norm", at::kFloat, {kv.D});
+            kn = c.whole(a[13], "k_norm", at::kFloat, {kv.D});
+            if (a[12] != Py_None && q == Py_None) refuse(PyExc_ValueError, fn + ": q_norm comes with q");
+            eps = PyFloat_AsDouble(a[14]);
+            if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+            pos = c.whole(a[15], "positions", at::kInt, {total});
+        }
         const dg_stream_t st = c.stream(a[11]);
         dg_status rc;
         Py_BEGIN_ALLOW_THREADS;
-        rc = g_append((const uint16_t*)kp, ldk, (const uint16_t*)vp, ldv, (const uint16_t*)qp, ldq, (uint16_t*)op,
+        if constexpr (Norm)
+            rc = g_append_norm((const uint16_t*)kp, ldk, (const uint16_t*)vp, ldv, (const uint16_t*)qp, ldq, (uint16_t*)op,
+                               (const int32_t*)cu, (int32_t)kv.n_seq, total, (int32_t)Hq, (int32_t)kv.Hkv, (int32_t)kv.D,
+                               (const float*)qn, (const float*)kn, (float)eps, (const int32_t*)pos, (const double*)w,
+                               (int32_t)(2 * half), interleaved, &kv.kv, st);
+        else
+            rc = g_append((const uint16_t*)kp, ldk, (const uint16_t*)vp, ldv, (const uint16_t*)qp, ldq, (uint16_t*)op,
                       (const int32_t*)cu, (int32_t)kv.n_seq, total, (int32_t)Hq, (int32_t)kv.Hkv, (int32_t)kv.D,
                       (const double*)w, (int32_t)(2 * half), interleaved, &kv.kv, st);
         Py_END_ALLOW_THREADS;
@@ -256,6 +298,141 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         rc = g_attention((const uint16_t*)q, &kv.kv, (uint16_t*)o, (float*)lse, (const int32_t*)cu, (const uint8_t*)causal,
                          (int32_t)kv.n_seq, (int32_t)max_q, total, (int32_t)Hq, (int32_t)kv.Hkv, (int32_t)kv.D,
                          (int32_t)window, (float)scale, wp, bytes, st);
+        Py_END_ALLOW_THREADS;
+        return PyLong_FromLong(rc);
+    });
+}
+
+// q, k_cache, v_cache, o, page_table, cu_q, kv_len, max_q_len, lse, window, sinks, scale, workspace, stream and, of a tree,
+// tree_mask, positions -> status; without a workspace nothing runs, and the bytes it needs come back as a 1-tuple
+template <bool Tree>
+PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!takes(n, Tree ? 16 : 14)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const char* fn = Tree ? "dg_tree_attention" : "dg_sink_attention";
+        Call c{fn};
+        const Cache kv(c, a[1], a[2], a[4], a[6]);
+        const void* q = c.whole(a[0], "q", at::kBFloat16, {-1, -1, kv.D});
+        if (a[0] == Py_None) refuse(PyExc_TypeError, c.named("q") + " must be a tensor");
+        const at::Tensor& qt = THPVariable_Unpack(a[0]);
+        const int64_t total = qt.size(0), Hq = qt.size(1);
+        if (Hq > INT32_MAX) refuse(PyExc_ValueError, c.named("q") + " has too many heads");
+        void* o = c.whole(a[3], "o", at::kBFloat16, {total, Hq, kv.D});
+        const void* cu = c.whole(a[5], "cu_q", at::kInt, {kv.n_seq + 1});
+        void* lse = c.whole(a[8], "lse", at::kFloat, {total, Hq});
+        const int64_t max_q = int32(a[7], fn, "max_q_len"), window = int32(a[9], fn, "window"), sinks = int32(a[10], fn, "sinks");
+        double scale = kv.D > 0 ? 1.0 / std::sqrt((double)kv.D) : 0.0;
+        if (a[11] != Py_None) {
+            scale = PyFloat_AsDouble(a[11]);
+            if (scale == -1.0 && PyErr_Occurred()) throw Raised();
+        }
+        const void *mask = nullptr, *pos = nullptr;
+        int64_t words = 0;
+        if constexpr (Tree) {
+            mask = c.whole(a[14], "tree_mask", at::kInt, {total, -1});
+            if (a[14] == Py_None) refuse(PyExc_TypeError, c.named("tree_mask") + " must be a tensor");
+            words = THPVariable_Unpack(a[14]).size(1);
+            if (words > INT32_MAX) refuse(PyExc_ValueError, c.named("tree_mask") + " has too many words");
+            pos = c.whole(a[15], "positions", at::kInt, {total});
+        }
+        const dg_stream_t st = c.stream(a[13]);
+        if (a[12] == Py_None)
+            return Py_BuildValue("(n)", (Py_ssize_t)g_tree_bytes((int32_t)kv.n_seq, (int32_t)max_q, (int32_t)Hq,
+                                                                 (int32_t)kv.Hkv, (int32_t)kv.D));
+        if (!THPVariable_Check(a[12])) refuse(PyExc_TypeError, c.named("workspace") + " must be a tensor");
+        const at::Tensor& ws = c.tensor(a[12], "workspace", THPVariable_Unpack(a[12]).scalar_type());
+        if (!ws.is_contiguous()) refuse(PyExc_ValueError, c.named("workspace") + " must be contiguous");
+        void* wp = ws.data_ptr();
+        const size_t bytes = ws.nbytes();
+        dg_status rc;
+        Py_BEGIN_ALLOW_THREADS;
+        if constexpr (Tree)
+            rc = g_tree((const uint16_t*)q, &kv.kv, (uint16_t*)o, (float*)lse, (const int32_t*)cu, (const uint32_t*)mask,
+                        (int32_t)words, (const int32_t*)pos, (int32_t)kv.n_seq, (int32_t)max_q, total, (int32_t)Hq,
+                        (int32_t)kv.Hkv, (int32_t)kv.D, (int32_t)window, (int32_t)sinks, (float)scale, wp, bytes, st);
+        else
+            rc = g_sink((const uint16_t*)q, &kv.kv, (uint16_t*)o, (float*)lse, (const int32_t*)cu, (int32_t)kv.n_seq,
+                        (int32_t)max_q, total, (int32_t)Hq, (int32_t)kv.Hkv, (int32_t)kv.D, (int32_t)window,
+                        (int32_t)sinks, (float)scale, wp, bytes, st);
+        Py_END_ALLOW_THREADS;
+        return PyLong_FromLong(rc);
+    });
+}
+
+// logits, tokens, cu_q, temperature, uniforms, next_uniforms, n_accept, path, out_tokens, parents, draft_probs, V, stream
+// -> status
+PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    if (!takes(n_args, 13)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const char* fn = "dg_verify_drafts";
+        Call c{fn};
+        if (!THPVariable_Check(a[0])) refuse(PyExc_TypeError, c.named("logits") + " must be a tensor");
+        const at::ScalarType type = THPVariable_Unpack(a[0]).scalar_type();
+        if (type != at::kBFloat16 && type != at::kFloat) refuse(PyExc_TypeError, "logits must be bfloat16 or float32");
+        // rows of any stride: the last dimension's elements follow each other
+        auto rows = [&](PyObject* o, const char* name, at::ScalarType t, int64_t& ld) -> const at::Tensor& {
+            const at::Tensor& x = c.tensor(o, name, t);
+            if (x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1))
+                refuse(PyExc_ValueError, c.named(name) + " must be [total, columns] with contiguous rows");
+            ld = x.size(0) > 1 ? x.stride(0) : x.size(1);
+            return x;
+        };
+        int64_t ld, ldq = 0;
+        const at::Tensor& x = rows(a[0], "logits", type, ld);
+        const int64_t total = x.size(0), V = a[11] == Py_None ? x.size(1) : integer(a[11], INT64_MIN, INT64_MAX, fn, "V");
+        if (V > x.size(1)) refuse(PyExc_ValueError, c.named("V") + " is more than the logits' columns");
+        for (int i : {1, 2, 3, 4, 5, 6, 7, 8})
+            if (a[i] == Py_None) refuse(PyExc_TypeError, std::string(fn) + ": an argument is None");
+        c.whole(a[3], "temperature", at::kFloat, {-1});
+        const int64_t n = THPVariable_Unpack(a[3]).size(0);
+        if (n > INT32_MAX) refuse(PyExc_ValueError, std::string(fn) + ": too many sequences");
+        const void* temperature = c.whole(a[3], "temperature", at::kFloat, {n});
+        const void* tokens = c.whole(a[1], "tokens", at::kInt, {total});
+        const void* cu = c.whole(a[2], "cu_q", at::kInt, {n + 1});
+        const void* u = c.whole(a[4], "uniforms", at::kFloat, {total});
+        const void* un = c.whole(a[5], "next_uniforms", at::kFloat, {n});
+        void* count = c.whole(a[6], "n_accept", at::kInt, {n});
+        void* path = c.whole(a[7], "path", at::kInt, {total});
+        void* out = c.whole(a[8], "out_tokens", at::kInt, {total});
+        const void* parents = c.whole(a[9], "parents", at::kInt, {total});
+        const void* probs = nullptr;
+        if (a[10] != Py_None) {
+            const at::Tensor& p = rows(a[10], "draft_probs", at::kFloat, ldq);
+            if (p.size(0) != total || p.size(1) < V)
+                refuse(PyExc_ValueError, c.named("draft_probs") + " must have the logits' rows and at least V columns");
+            if (a[9] != Py_None) refuse(PyExc_ValueError, std::string(fn) + ": parents and draft_probs do not go together");
+            probs = p.data_ptr();
+        }
+        const dg_stream_t st = c.stream(a[12]);
+        dg_status rc;
+        Py_BEGIN_ALLOW_THREADS;
+        rc = g_verify(x.data_ptr(), type == at::kBFloat16 ? DG_BF16 : DG_FP32, ld, (const int32_t*)tokens,
+                      (const int32_t*)parents, (const float*)probs, ldq, (const int32_t*)cu, (int32_t)n, total, V,
+                      (const float*)temperature, (const float*)u, (const float*)un, (int32_t*)count, (int32_t*)path,
+                      (int32_t*)out, st);
+        Py_END_ALLOW_THREADS;
+        return PyLong_FromLong(rc);
+    });
+}
+
+// k_cache, v_cache, page_table, cu_q, kv_len, path, n_accept, new_len, stream -> status
+PyObject* kv_keep(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!takes(n, 9)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        Call c{"dg_kv_keep"};
+        const Cache kv(c, a[0], a[1], a[2], a[4], true);
+        for (int i : {3, 5, 6, 7})
+            if (a[i] == Py_None) refuse(PyExc_TypeError, std::string(c.fn) + ": an argument is None");
+        const void* cu = c.whole(a[3], "cu_q", at::kInt, {kv.n_seq + 1});
+        const void* path = c.whole(a[5], "path", at::kInt, {-1});
+        const int64_t total = THPVariable_Unpack(a[5]).size(0);
+        const void* count = c.whole(a[6], "n_accept", at::kInt, {kv.n_seq});
+        void* len = c.whole(a[7], "new_len", at::kInt, {kv.n_seq});
+        const dg_stream_t st = c.stream(a[8]);
+        dg_status rc;
+        Py_BEGIN_ALLOW_THREADS;
+        rc = g_keep(&kv.kv, (int32_t)kv.n_layers, kv.layer_stride, (const int32_t*)cu, (int32_t)kv.n_seq, total,
+                    (int32_t)kv.Hkv, (int32_t)kv.D, (const int32_t*)path, (const int32_t*)count, (int32_t*)len, st);
         Py_END_ALLOW_THREADS;
         return PyLong_FromLong(rc);
     });
@@ -317,11 +494,13 @@ PyObject* adjust_logits(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
-// The addresses of dg_kv_append, dg_paged_attention, its workspace query and dg_adjust_logits.
+// The addresses of dg_kv_append, dg_paged_attention, its workspace query, dg_adjust_logits, dg_kv_append_norm,
+// dg_tree_attention, its workspace query, dg_sink_attention, dg_verify_drafts and dg_kv_keep.
 PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!takes(n, 4)) return nullptr;
-    void* p[4];
-    for (int i = 0; i < 4; ++i) {
+    constexpr int kCalls = 10;
+    if (!takes(n, kCalls)) return nullptr;
+    void* p[kCalls];
+    for (int i = 0; i < kCalls; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an entry point is missing");
@@ -332,6 +511,12 @@ PyObject* connect(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_attention = reinterpret_cast<decltype(g_attention)>(p[1]);
     g_attention_bytes = reinterpret_cast<decltype(g_attention_bytes)>(p[2]);
     g_adjust = reinterpret_cast<decltype(g_adjust)>(p[3]);
+    g_append_norm = reinterpret_cast<decltype(g_append_norm)>(p[4]);
+    g_tree = reinterpret_cast<decltype(g_tree)>(p[5]);
+    g_tree_bytes = reinterpret_cast<decltype(g_tree_bytes)>(p[6]);
+    g_sink = reinterpret_cast<decltype(g_sink)>(p[7]);
+    g_verify = reinterpret_cast<decltype(g_verify)>(p[8]);
+    g_keep = reinterpret_cast<decltype(g_keep)>(p[9]);
     Py_RETURN_NONE;
 }
 
@@ -341,7 +526,12 @@ PyCFunction fast() {
 }
 
 PyMethodDef kMethods[] = {{"connect", fast<connect>(), METH_FASTCALL, nullptr},
-                          {"kv_append", fast<kv_append>(), METH_FASTCALL, nullptr},
+                          {"kv_append", fast<kv_append<false>>(), METH_FASTCALL, nullptr},
+                          {"kv_append_norm", fast<kv_append<true>>(), METH_FASTCALL, nullptr},
+                          {"tree_attention", fast<tree_attention<true>>(), METH_FASTCALL, nullptr},
+                          {"sink_attention", fast<tree_attention<false>>(), METH_FASTCALL, nullptr},
+                          {"verify_drafts", fast<verify_drafts>(), METH_FASTCALL, nullptr},
+                          {"kv_keep", fast<kv_keep>(), METH_FASTCALL, nullptr},
                           {"paged_attention", fast<paged_attention>(), METH_FASTCALL, nullptr},
                           {"adjust_logits", fast<adjust_logits>(), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};

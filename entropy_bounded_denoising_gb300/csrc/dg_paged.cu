@@ -1,9 +1,11 @@
-// dg_paged.cu -- the paged key / value cache: appending a pass's rotated keys and its values.
+// dg_paged.cu -- the paged key / value cache: appending a pass's rotated keys and its values, its queries
+// and keys normed before where a call says so.
 #include <cuda_runtime.h>
 
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dg_paged.cuh"
 
@@ -39,6 +41,15 @@ struct AppendArgs {
     dg::PagedKV kv;
     unsigned* status;
 };
+
+// With norms of the heads and rows' own positions (dg_kv_append_norm).
+struct NormArgs : AppendArgs {
+    const float* norm[2];      // of queries and of keys; null: not normed
+    const int32_t* positions;  // null: the slots' numbers
+    float eps;
+};
+template <bool Norm>
+using ArgsOf = std::conditional_t<Norm, NormArgs, AppendArgs>;
 
 struct Task {
     int row, head;   // row of the unit; heads in order: key heads, value heads, query heads
@@ -79,6 +90,50 @@ DG_DEVINL void rotate_neighbours(uint4& x, const float2* cs) {
         const float u = lo_f(a[e]), w = hi_f(a[e]);
         a[e] = pack_bf16x2(u * c.x - w * c.y, u * c.y + w * c.x);
     }
+}
+
+// The sixteen values of a task as floats, and back.
+DG_DEVINL void unpack16(const uint4& x, const uint4& y, float (&f)[16]) {
+    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[2 * e] = lo_f(w[e]);
+        f[2 * e + 1] = hi_f(w[e]);
+    }
+}
+DG_DEVINL void pack16(const float (&f)[16], uint4& x, uint4& y) {
+    x = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    y = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
+}
+
+// The sum over a head's 2^head_shift lanes, which lie side by side.
+DG_DEVINL float head_sum(float v, int head_shift) {
+    for (int o = 1; o < (1 << head_shift); o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// f / sqrt(mean f^2 + eps) over a head.  A sum of squares past fp32 (values from 2^60 on) is taken of values 2^-70 as large,
+// beside which eps is nothing.  (Whole warp; squares below fp32 are below eps, which is at least 2^-126.)
+DG_DEVINL void norm_head(float (&f)[16], int head_shift, int D, float eps) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
+    ss = head_sum(ss, head_shift);
+    const bool large = !(ss <= 0x1p120f);   // (a NaN is rid of nothing here)
+    if (__any_sync(0xffffffffu, large)) {
+        const float s = large ? 0x1p-70f : 1.f;
+        eps = large ? eps * 0x1p-140f : eps;
+        ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            f[e] *= s;
+            ss = fmaf(f[e], f[e], ss);
+        }
+        ss = head_sum(ss, head_shift);
+    }
+    const float r = rsqrtf(ss / (float)D + eps);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] *= r;
 }
 
 // w radians as a fraction of a turn in 64-bit fixed point: floor(w / (2 pi) 2^64) mod 2^64, within two units of the
@@ -132,13 +187,18 @@ DG_DEVINL int row_position(const AppendArgs& a, int t, int s) {
 // place at once; four where there are several rounds of blocks (more bytes on the way and fewer lookups
 // a byte).  One against four, the same rows again and again: 64 rows 3.4 and 5.1 us, 2048 rows 8.4 and 8.2, the 30k
 // rows 154 and 138.
-template <bool Interleaved, int PerThread>
-__global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_append(const AppendArgs a) {
+//
+// Norm (dg_kv_append_norm): a head's D / 16 lanes add up its squares; its values stay in fp32 from the norm through the
+// rotation.
+template <bool Interleaved, int PerThread, bool Norm>
+__global__ void __launch_bounds__(kAppendThreads, Norm || PerThread == 4 ? 4 : 8) k_kv_append(const ArgsOf<Norm> a) {
     constexpr int kPerThread = PerThread, kUnit = kAppendThreads * PerThread;   // tasks of a block
     constexpr int kRows = kUnit / 8 + 2;       // rows of a unit: at least 8 tasks each (one key head of 64)
     __shared__ int64_t place[kRows];           // cache offset of a row's slot, -1 = skipped
     __shared__ int32_t position[kRows];
     __shared__ float2 cs[kUnit * 4 + 2 * 128]; // cosine and sine of its angles
+    __shared__ int32_t turn_by[Norm ? kRows : 1];            // its position as the rotation takes it
+    __shared__ __align__(16) float weight[Norm ? 512 : 4];   // of queries, of keys
     dg::pdl_wait();
     dg::pdl_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -192,6 +252,13 @@ __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_a
     if (mine >= 0) {
         p = row_position(a, (int)(row0 + mine), owner);
         position[mine] = p;
+        if constexpr (Norm) turn_by[mine] = a.positions ? a.positions[row0 + mine] : p;
+    }
+    if constexpr (Norm) {
+        for (int i = tid; i < 2 * a.D; i += kAppendThreads) {
+            const float* w = a.norm[i >= a.D];
+            weight[i] = w ? w[i >= a.D ? i - a.D : i] : 0.f;
+        }
     }
     __syncthreads();
     if (mine >= 0) {
@@ -208,7 +275,7 @@ __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_a
     for (int i = tid; i < rows * half; i += kAppendThreads) {
         const int r = i / half;
         const double w = i == tid ? w0 : a.inv_freq[i - r * half];
-        const int64_t u = (int64_t)(turns_of(w) * (uint64_t)position[r]);
+        const int64_t u = (int64_t)(turns_of(w) * (uint64_t)(Norm ? turn_by : position)[r]);
         float sn, c;
         sincospif((float)u * 1.0842021724855044e-19f, &sn, &c);  // 2^-63: half turns in [-1, 1]
         cs[i] = make_float2(c, sn);
@@ -217,8 +284,50 @@ __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_a
 #pragma unroll
     for (int u = 0; u < kPerThread; ++u) {
         const Task k = task_of(a, skip + u * kAppendThreads + tid);
+        if constexpr (Norm) {   // (a head's lanes have one row and are of one head: they go the same ways)
+            const bool key = k.head < a.Hkv, in = k.row < rows && (key || k.head >= 2 * a.Hkv);
+            const bool normed = in && a.norm[key ? 1 : 0];
+            if (__any_sync(0xffffffffu, in)) {
+                float f[16];
+                unpack16(x[u], y[u], f);
+                if (!in) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) f[e] = 0.f;
+                }
+                if (__any_sync(0xffffffffu, normed)) {
+                    float n[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) n[e] = f[e];
+                    norm_head(n, a.head_shift, a.D, a.eps);
+                    const float4* w = reinterpret_cast<const float4*>(weight + (key ? a.D : 0));
+                    if (normed) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 v = w[(k.at + (c < 2 ? 0 : k.dist)) / 4 + (c & 1)];
+                            f[4 * c] = n[4 * c] * v.x;
+                            f[4 * c + 1] = n[4 * c + 1] * v.y;
+                            f[4 * c + 2] = n[4 * c + 2] * v.z;
+                            f[4 * c + 3] = n[4 * c + 3] * v.w;
+                        }
+                    }
+                }
+                if (in && k.turn) {
+                    const float2* c = cs + k.row * half + (Interleaved ? k.at / 2 : k.at);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // pair e: dimensions e of both chunks, or two neighbours of the first (4 pairs) or second chunk
+                        const int i = Interleaved ? 2 * e : e, j = Interleaved ? 2 * e + 1 : e + 8;
+                        const float2 z = Interleaved && e >= 4 ? c[half / 2 + e - 4] : c[e];
+                        const float p0 = f[i], p1 = f[j];
+                        f[i] = p0 * z.x - p1 * z.y;
+                        f[j] = p0 * z.y + p1 * z.x;
+                    }
+                }
+                if (normed || (in && k.turn)) pack16(f, x[u], y[u]);
+            }
+        }
         if (k.row >= rows || place[k.row] < 0) continue;
-        if (k.turn) {
+        if (!Norm && k.turn) {
             const float2* c = cs + k.row * half;
             if (Interleaved) {
                 rotate_neighbours(x[u], c + k.at / 2);
@@ -270,24 +379,31 @@ dg_status paged_kv(const dg_paged_kv* cache, int32_t D, dg::PagedKV* c) {
 
 }  // namespace dghost
 
-extern "C" dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q,
-                                  int64_t ldq, uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q,
-                                  int32_t Hq, int32_t Hkv, int32_t D, const double* inv_freq, int32_t rot_dim,
-                                  int32_t interleaved, const dg_paged_kv* cache, dg_stream_t stream) {
+namespace {
+
+// Checks and launch shared by dg_kv_append and dg_kv_append_norm.
+template <bool Norm>
+dg_status append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q, int64_t ldq,
+                 uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q, int32_t Hq, int32_t Hkv,
+                 int32_t D, const float* q_norm, const float* k_norm, float eps, const int32_t* positions,
+                 const double* inv_freq, int32_t rot_dim, int32_t interleaved, const dg_paged_kv* cache,
+                 dg_stream_t stream) {
     if (n_seq < 0 || n_seq > 65535 || total_q < 0 || total_q >= (1LL << 31) || Hq < 1 || Hq > 65535 || Hkv < 1 ||
         Hkv > 65535)
         return DG_ERR_INVALID_ARG;
     if (D != 64 && D != 128 && D != 256) return DG_ERR_UNSUPPORTED;
     if (rot_dim < 0 || rot_dim > D || rot_dim % 16 || (rot_dim > 0 && !inv_freq)) return DG_ERR_INVALID_ARG;
+    if ((q_norm || k_norm) && !(eps >= 0x1p-126f && eps < INFINITY)) return DG_ERR_INVALID_ARG;
     if (n_seq == 0 || total_q == 0) return DG_OK;
-    if (!k || !v || !cu_q || (q != nullptr) != (q_out != nullptr)) return DG_ERR_INVALID_ARG;
+    if (!k || !v || !cu_q || (q != nullptr) != (q_out != nullptr) || (q_norm && !q)) return DG_ERR_INVALID_ARG;
     if (ldk < (int64_t)Hkv * D || ldv < (int64_t)Hkv * D || (q && ldq < (int64_t)Hq * D)) return DG_ERR_INVALID_ARG;
     if (ldk >= (1LL << 31) || ldv >= (1LL << 31) || (q && ldq >= (1LL << 31))) return DG_ERR_INVALID_ARG;
     if (q && q_out == q && ldq != (int64_t)Hq * D) return DG_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))) || ldk % 8 || ldv % 8 ||
-        (q && ldq % 8) || !dghost::on_multiple(cu_q, 4) || !dghost::on_multiple(inv_freq, 8))
+        (q && ldq % 8) || !dghost::on_multiple(cu_q, 4) || !dghost::on_multiple(inv_freq, 8) ||
+        !dghost::on_multiple(q_norm, 4) || !dghost::on_multiple(k_norm, 4) || !dghost::on_multiple(positions, 4))
         return DG_ERR_ALIGNMENT;
-    AppendArgs a;
+    ArgsOf<Norm> a;
     const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
     if (ok != DG_OK) return ok;
     a.k = k;
@@ -309,6 +425,12 @@ extern "C" dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t
     a.head_shift = D == 64 ? 2 : D == 128 ? 3 : 4;
     a.status = dghost::status_word();
     a.narrow = total_q * a.tasks < (1LL << 31);
+    if constexpr (Norm) {
+        a.norm[0] = q_norm;
+        a.norm[1] = k_norm;
+        a.positions = positions;
+        a.eps = eps;
+    }
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
     const bool one = total_q * a.tasks <= (int64_t)sms * 2048;
@@ -317,9 +439,29 @@ extern "C" dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t
     const int64_t blocks = row_blocks + (n_seq + kAppendThreads - 1) / kAppendThreads;
     if (blocks > 0x7fffffffLL) return DG_ERR_INVALID_ARG;
     a.row_blocks = (uint32_t)row_blocks;
-    const cudaError_t e = dghost::launch_pdl(one ? (interleaved ? k_kv_append<true, 1> : k_kv_append<false, 1>)
-                                                 : (interleaved ? k_kv_append<true, 4> : k_kv_append<false, 4>),
-                                             dim3((unsigned)blocks), dim3(kAppendThreads), 0, (cudaStream_t)stream, a);
+    const cudaError_t e =
+        dghost::launch_pdl(one ? (interleaved ? k_kv_append<true, 1, Norm> : k_kv_append<false, 1, Norm>)
+                               : (interleaved ? k_kv_append<true, 4, Norm> : k_kv_append<false, 4, Norm>),
+                           dim3((unsigned)blocks), dim3(kAppendThreads), 0, (cudaStream_t)stream, a);
     dghost::count_launch();
     return dghost::cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q,
+                                  int64_t ldq, uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q,
+                                  int32_t Hq, int32_t Hkv, int32_t D, const double* inv_freq, int32_t rot_dim,
+                                  int32_t interleaved, const dg_paged_kv* cache, dg_stream_t stream) {
+    return append<false>(k, ldk, v, ldv, q, ldq, q_out, cu_q, n_seq, total_q, Hq, Hkv, D, nullptr, nullptr, 0.f, nullptr,
+                         inv_freq, rot_dim, interleaved, cache, stream);
+}
+
+extern "C" dg_status dg_kv_append_norm(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q,
+                                       int64_t ldq, uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q,
+                                       int32_t Hq, int32_t Hkv, int32_t D, const float* q_norm, const float* k_norm,
+                                       float eps, const int32_t* positions, const double* inv_freq, int32_t rot_dim,
+                                       int32_t interleaved, const dg_paged_kv* cache, dg_stream_t stream) {
+    return append<true>(k, ldk, v, ldv, q, ldq, q_out, cu_q, n_seq, total_q, Hq, Hkv, D, q_norm, k_norm, eps, positions,
+                        inv_freq, rot_dim, interleaved, cache, stream);
 }

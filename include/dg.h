@@ -458,6 +458,124 @@ DG_API dg_status dg_paged_attention(const uint16_t* q, const dg_paged_kv* cache,
                                     void* workspace, size_t workspace_bytes, dg_stream_t stream);
 
 /* ------------------------------------------------------------------------------------ */
+/* Drafted tokens over the paged cache.  Before it commits, a pass may look at several        */
+/* continuations at once: a request's last certain token (the root, node 0) and drafts behind  */
+/* it, each the child of an earlier node.  Appended with a rotation by their depth, seen       */
+/* through an ancestor mask, verified against the target's logits and kept along the accepted  */
+/* path.  The pages describe none of it; the reading is the usual definition of speculative    */
+/* sampling and of its trees.                                                                  */
+/* ------------------------------------------------------------------------------------ */
+
+/* dg_kv_append with a norm of every query and key head before the rotation, and positions of the
+ * rows' own:
+ *   y = x * w / sqrt(mean(x^2) + eps)   over the D dimensions of a head, w = q_norm or k_norm,
+ * then y is rotated as there, by the angles positions[row] * inv_freq[j] (p * inv_freq[j] without
+ * positions: the slot's number).  Row i of a sequence still goes to slot kv_len - q_len + i, so the nodes of a
+ * tree lie one behind the other and turn by their depth.  Sums, norm and rotation are in fp32 with one rounding to
+ * bf16; a sum of squares that fp32 does not hold is taken of scaled values.  A head that is
+ * neither normed nor rotated, and values, are copied bit for bit.
+ *   q_norm, k_norm (device, may be NULL = not normed) [D] float; q_norm only with q.
+ *   eps            in [2^-126, inf) when a norm is given, else ignored.
+ *   positions      (device, may be NULL) [total_q] int32, of any value; only rows that a sequence owns are used.
+ * Everything else, errors included, as dg_kv_append.  One kernel. */
+DG_API dg_status dg_kv_append_norm(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q,
+                                   int64_t ldq, uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q,
+                                   int32_t Hq, int32_t Hkv, int32_t D, const float* q_norm, const float* k_norm,
+                                   float eps, const int32_t* positions, const double* inv_freq, int32_t rot_dim,
+                                   int32_t interleaved, const dg_paged_kv* cache, dg_stream_t stream);
+
+/* Attention of drafted trees over the paged cache.  A sequence's last q_len = cu_q[s+1] - cu_q[s] keys are its
+ * nodes, the c = kv_len - q_len before them its context.  Query i sees
+ *   node j     when bit j of its mask is set (bit j % 32 of word j / 32 of row cu_q[s] + i; bits from q_len on
+ *              are ignored): its ancestors and itself, as a rule;
+ *   context j  when window < 0, or j >= positions[cu_q[s] + i] - window, or j < sinks.
+ * o = softmax of scale * q . k over what it sees, applied to v; h' = h / (Hq / Hkv), as dg_paged_attention.
+ *   tree_mask (device) [total_q][mask_words] uint32, 4-byte aligned; mask_words >= ceil(max_q_len / 32).
+ *   positions (device, may be NULL when window < 0) [total_q] int32: the nodes' positions (c + depth).
+ *   sinks     >= 0: first tokens of the context that stay visible to a window; ignored without one.
+ *   q, o, lse, cu_q, max_q_len, scale, cache, workspace: as dg_paged_attention.  A sequence with more than max_q_len
+ *             queries raises DG_DEV_BAD_PARAM and is skipped; the other refusals are the same.
+ * A row that sees no key at all gets 0 and an lse of -inf.  A node that no query of its sequence sees, and context
+ * that no query sees, may hold anything; a value that some queries see and others not must be finite.
+ * Scores, maxima and sums are in fp32; the weights are rounded to bf16 for the product with v, which is divided by
+ * the sum of the unrounded ones.
+ *   workspace (device) >= dg_tree_attention_workspace_bytes(), 16-byte aligned, no initial contents; calls that
+ *             overlap on the GPU need their own.  The size never falls as n_seq or max_q_len grow.
+ * Limits and errors as dg_paged_attention; max_q_len <= 65536.  At most two kernels. */
+DG_API size_t dg_tree_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D);
+DG_API dg_status dg_tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
+                                   const int32_t* cu_q, const uint32_t* tree_mask, int32_t mask_words,
+                                   const int32_t* positions, int32_t n_seq, int32_t max_q_len, int64_t total_q, int32_t Hq,
+                                   int32_t Hkv, int32_t D, int32_t window, int32_t sinks, float scale, void* workspace,
+                                   size_t workspace_bytes, dg_stream_t stream);
+
+/* Causal attention over the paged cache through a sliding window with first tokens that stay visible: the query at
+ * position p (kv_len - q_len + i) sees key j when j <= p and (j >= p - window or j < sinks).
+ *   window >= 0, sinks >= 0; everything else as dg_tree_attention (its workspace too), except that max_q_len may be
+ *   up to 2^30. */
+DG_API dg_status dg_sink_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
+                                   const int32_t* cu_q, int32_t n_seq, int32_t max_q_len, int64_t total_q, int32_t Hq,
+                                   int32_t Hkv, int32_t D, int32_t window, int32_t sinks, float scale, void* workspace,
+                                   size_t workspace_bytes, dg_stream_t stream);
+
+/* Verification of drafts against the target model's distribution, from given random numbers.  Sequence s owns nodes
+ * cu_q[s] .. cu_q[s+1]-1, the root first; row i of the logits predicts the token behind node i, p_i =
+ * softmax(logits[i] / temperature[s]).  The walk starts at the root.  At node v its children c are tried in order,
+ * x_c = tokens[c], u_c = uniforms[c]:
+ *   with draft_probs (chains only: node i's parent is i - 1), c is accepted iff u_c * draft_probs[c][x_c] < p_v(x_c);
+ *     rejected, it leaves max(p_v - draft_probs[c], 0) of p_v (all of p_v where that is 0 everywhere);
+ *   without, c is accepted iff u_c * m < p_v(x_c), m what the children rejected before it leave of p_v's mass; rejected, it
+ *     leaves p_v without x_c (a token tried before has nothing left; all of p_v where nothing is left).
+ * An accepted child is the next v.  Where none is, the walk ends, and the next token is the smallest t with
+ * sum_{t' <= t} left(t') > next_uniforms[s] * sum left.  With temperature 0 a child is accepted iff its token is the
+ * smallest argmax of the row, which is also the next token; the random numbers are not read.  Of draft
+ * distributions so verified the produced tokens have the target's.
+ *   logits    (device) [total][ld] of dtype, 16-byte aligned, ld >= V, ld * sizeof(dtype) a multiple of 16; columns
+ *             from V on do not count.  Only rows that the walk comes to are read.
+ *   tokens    (device) [total] int32, the roots' unused; one outside [0, V) is never accepted.
+ *   parents   (device, may be NULL = chains) [total] int32, of node i >= 1 the index within its sequence of an
+ *             earlier node, roots' unused; not together with draft_probs.
+ *   draft_probs (device, may be NULL) [total][ldq] float, 16-byte aligned, ldq >= V, a multiple of 4: row c the
+ *             distribution that tokens[c] was drawn from; entries below 0 and NaN count as 0, above 1 as 1.
+ *   temperature (device) [n_seq] float; uniforms [total], next_uniforms [n_seq] (device) float in [0, 1).
+ *   n_accept  (device, out) [n_seq] int32: accepted drafts.
+ *   path      (device, out) [total] int32: path[cu_q[s] + i], i <= n_accept: the i-th node of the path, the root (0) first;
+ *             -1 behind them.
+ *   out_tokens (device, out) [total] int32: the accepted tokens and, at cu_q[s] + n_accept, the next one; -1 behind them.
+ * Probabilities are fp32 where that decides, else within 2^-31 of the formula's, summed in 64-bit fixed point; so
+ * results do not depend on order, and repeated calls are bit-identical.
+ * A sequence without nodes, or one that is refused (offsets outside [0, total], more than 1024 nodes, a parent or
+ * temperature out of range (negative, not finite or below 2^-64 but not 0), a uniform outside [0, 1)) has n_accept = -1, and -1 in its rows of path and
+ * out_tokens where its offsets are good; refusals raise DG_DEV_BAD_PARAM.  A row on the walk that holds NaN or +inf raises
+ * DG_DEV_NAN_INF_ROW, one all -inf DG_DEV_EMPTY_ROW: the walk ends there with next token -1.
+ * Limits: n_seq in [0, 65535], 2 <= V < 2^30, total < 2^31, V * sizeof(dtype) < 2^31.  Errors:
+ * DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT, DG_ERR_UNSUPPORTED, DG_ERR_CUDA.  One kernel, no workspace. */
+DG_API dg_status dg_verify_drafts(const void* logits, dg_dtype dtype, int64_t ld, const int32_t* tokens,
+                                  const int32_t* parents, const float* draft_probs, int64_t ldq, const int32_t* cu_q,
+                                  int32_t n_seq, int64_t total, int64_t V, const float* temperature, const float* uniforms,
+                                  const float* next_uniforms, int32_t* n_accept, int32_t* path, int32_t* out_tokens,
+                                  dg_stream_t stream);
+
+/* Keeps an accepted path in the cache: the keys and values of sequence s's nodes path[0] < path[1] < ... <
+ * path[n_accept[s]] (of its rows of path, as dg_verify_drafts leaves them) move to the slots c, c + 1, ... behind the
+ * context, c = kv_len - q_len, in every layer, and
+ *   new_len[s] = c + n_accept[s] + 1.
+ * Slots past it keep what they hold.  n_accept -1 leaves a sequence as it is, with new_len = kv_len.
+ *   cache     (host) layer 0's cache; layer l's lies l * layer_stride elements behind it (n_layers >= 1; layer_stride a
+ *             multiple of 8 below 2^55, ignored for one layer), all with one page table.  The nodes' pages must not be
+ *             shared with another sequence.
+ *   path (device) [total_q] int32, n_accept (device) [n_seq] int32.
+ *   new_len   (device, out) [n_seq] int32; must not overlap kv_len or n_accept, which other blocks still read.
+ * A sequence whose offsets lie outside [0, total_q], with kv_len < q_len, kv_len > max_pages * page_size, n_accept
+ * outside [-1, q_len), a path that does not ascend within [0, q_len), or a page it needs outside [0, n_pages) raises
+ * DG_DEV_BAD_PARAM; nothing of it moves, and new_len = kv_len.
+ * D is 64, 128 or 256 (else DG_ERR_UNSUPPORTED); Hkv in [1, 65535], n_layers in [1, 65535]; other limits and errors as
+ * dg_kv_append.  One kernel. */
+DG_API dg_status dg_kv_keep(const dg_paged_kv* cache, int32_t n_layers, int64_t layer_stride, const int32_t* cu_q,
+                            int32_t n_seq, int64_t total_q, int32_t Hkv, int32_t D, const int32_t* path,
+                            const int32_t* n_accept, int32_t* new_len, dg_stream_t stream);
+
+/* ------------------------------------------------------------------------------------ */
 /* A request's own edits of its logits, before the step reads them: penalties for tokens  */
 /* it has already produced, a bias per token and a grammar's mask.  The pages describe     */
 /* none of them; the reading is the usual definition of such sampling parameters.           */
