@@ -1,10 +1,30 @@
 // dg_tree_attn.cu -- attention of drafted trees, and through a sliding window with first tokens that stay
-// visible, over the paged key / value cache.
+// visible, over the paged key / value cache, on the tensor cores (tcgen05 + TMEM + TMA, sm_103a).
+//
+// An item is (sequence, key head, up to 128 rows), a row one (query, query head of that key head): the rows that share
+// keys share a tile, so keys and values are read once for 128 / (Hq / Hkv) queries.  It visits tiles of 64 keys: those of
+// the first tokens that stay visible, then those from the window's (or the context's) first to its last key.  All
+// tiles of all items, in order, form one line that is cut into equal runs, one for each of the resident CTAs; a
+// run's first and last items may be pieces, which go to the workspace as (maximum, sum, unnormalised output)
+// and are joined by a second kernel in the order of the line.  Where there are many items a run takes whole ones.
+//
+// A CTA (two an SM; one for heads of 256):
+//   warp 0      lane 2 walks the run, publishes its pieces in a ring and copies their queries; lanes 0 and 1
+//               copy keys and values (two tiles each), page by page;
+//   warp 1      issues the products: S = Q K^T (128 x 64) into TMEM, O += P V with P from TMEM;
+//   warps 2..5  the softmax, a row a thread.
+// A tile that not all rows see whole gets each row's 64-bit mask: the window's and the context's ranges, and the row's
+// words of the tree mask, shifted to the tile.  Keys of it that no row sees have their values zeroed in shared
+// memory before the product (what they hold is nobody's, and 0 * NaN is not 0).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
+#include <limits>
+#include <utility>
 
 #include "dg_paged.cuh"
 
@@ -12,79 +32,886 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTile = 128;      // rows of an item
+constexpr int kKeys = 64;       // keys of a tile
+constexpr int kSub = 64;        // columns of a 128-byte swizzle atom
+constexpr uint32_t kQSub = kTile * kSub * 2, kKSub = kKeys * kSub * 2;
+constexpr float kRescaleAbove = 8.f;   // log2 units a row's maximum may grow before it moves: P <= 2^8
+constexpr int kThreads = 192;
+constexpr int kRing = 4;        // pieces published ahead
+constexpr int kReaders = 7;     // of a piece: two copies, the products, four softmax warps (the walker reads none)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct TreeArgs {
-    const uint16_t* q;
     uint16_t* o;
     float* lse;
     const int32_t* cu_q;
     const uint32_t* mask;       // null: causal
     const int32_t* positions;
     int64_t total_q;
-    int32_t n_seq, max_q_len, Hq, Hkv, mask_words, window, sinks;
+    int32_t n_seq, max_q_len, Hq, Hkv, group, mask_words, window, sinks;
+    int32_t hpt, qpt, head_tiles;   // heads and queries of an item; items a query's heads take
+    int32_t rows;               // of a piece in the workspace (multiple of 32)
+    int32_t negate;             // the products' sign: scale_log2 is the scale's magnitude, so the largest score stays the largest
     float scale_log2;
     dg::PagedKV kv;
+    float4* part_o;             // [grid][2][D / 4][rows]
+    float2* part_ml;            // [grid][2][rows]: maximum, sum
+    int4* desc;                 // [grid][2]: CTAs that follow (0: nothing to join), first query's row, first head, queries; heads
     unsigned* status;
 };
 
-DG_DEVINL float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
-// A warp owns a query of one head, a lane D / 32 of its dimensions; keys one after another.
 template <int D>
-__global__ void __launch_bounds__(128) k_tree_simple(const TreeArgs a) {
-    constexpr int E = D / 32;
+struct TreeCfg {
+    static constexpr uint32_t kQBytes = (D / kSub) * kQSub, kKVBytes = (D / kSub) * kKSub;
+    static constexpr uint32_t kOffQ = 0, kOffK = kQBytes, kOffV = kOffK + 2 * kKVBytes, kOffBar = kOffV + 2 * kKVBytes;
+    static constexpr uint32_t kColS = 0, kColO = 64, kColP = 64 + D;
+    static constexpr uint32_t kTmemCols = D == 256 ? 512 : 256;
+    static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
+    static constexpr int kMaxCtas = D == 256 ? 256 : 512;   // grid bound the workspace is sized for
+};
+
+DG_DEVINL uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+DG_DEVINL float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Packed fp32 pairs (one rounding per element, as the scalar forms).
+DG_DEVINL uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+DG_DEVINL void f2_split(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+DG_DEVINL uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+DG_DEVINL uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// A run's part of one item.
+struct Piece {
+    int32_t s, hk, h0, nh;       // sequence, key head, first query head and heads
+    int32_t qrow, qi0, nq;       // first query: row of q and index in the sequence; queries
+    int32_t ql, kl;
+    int32_t sink_end, ns;        // keys below sink_end stay visible; tiles of them before the body's
+    int32_t jlo, jhi;            // the body's keys that some row may see
+    int32_t t0, nt;              // tiles of the piece, of the item's
+    int32_t last;                // the CTA that has the item's last tile
+    uint32_t flags;              // kStarts, kEnds
+    // the tile that comes i-th
+    DG_DEVINL int tile(int i) const { return t0 + i < ns ? t0 + i : jlo / kKeys + t0 + i - ns; }
+};
+constexpr uint32_t kStarts = 1, kEnds = 2;
+
+struct __align__(8) TreeShared {
+    uint64_t qfull, qempty, oempty;
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2];   // separate rings: a K buffer is free once its S is done
+    uint64_t sfull, sempty;
+    uint64_t pfull[2], pvdone[2];
+    uint64_t mmadone;
+    uint64_t wfull[kRing], wempty[kRing];
+    uint64_t met;                 // the four softmax warps' own barrier (bounded, unlike bar.sync)
+    uint64_t seen[2][4];          // of a masked tile, by warp: the keys some row sees
+    int64_t sums[kThreads / 32];
+    int64_t found_start;
+    Piece piece[kRing];           // nt 0: no more
+    int32_t pages[2][8];          // of the tile that a copying lane is at
+    int32_t top_position[2][4];
+    int32_t found_seq;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+template <int D>
+constexpr size_t tree_smem() {
+    return 1024 + TreeCfg<D>::kOffBar + sizeof(TreeShared) + 64;
+}
+
+DG_DEVINL bool try_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(dg::smem_u32(bar)), "r"(parity), "r"(200u)
+        : "memory");
+    return ok != 0;
+}
+DG_DEVINL bool wait(uint64_t* bar, uint32_t parity) {   // bounded, as every wait of the library
+    for (uint32_t i = 0; i < 4u * dg::kWaitPolls; ++i)
+        if (try_wait(bar, parity)) return true;
+    return false;
+}
+DG_DEVINL bool wait_warp(uint64_t* bar, uint32_t parity) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = wait(bar, parity) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+DG_DEVINL bool aborted(const TreeShared& sh) { return *(volatile const int*)&sh.abort_flag != 0; }
+DG_DEVINL void do_abort(TreeShared& sh, unsigned* status) {
+    *(volatile int*)&sh.abort_flag = 1;
+    dg::raise_status(status, DG_DEV_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ the line
+// A sequence on it: its items (query tiles x heads' tiles x key heads) and the line's length an item has, at least its
+// tiles.  Of a tree every item visits the same tiles, and of a single query tile the length is exact; the query tiles of
+// a longer causal sequence get the most that one of them may have.
+struct SeqLine {
+    dg::PagedSeq seq;
+    int q_tiles;
+    int64_t len;
+    DG_DEVINL int64_t cost(const TreeArgs& a) const { return (int64_t)q_tiles * a.head_tiles * a.Hkv * len; }
+};
+
+struct Range {
+    int sink_end, ns, jlo, jhi, nt;
+};
+// The tiles of query tile qt.
+DG_DEVINL Range range_of(const TreeArgs& a, const dg::PagedSeq& q, int qt) {
+    Range r;
+    const int ctx = q.kl - q.ql;
+    const int64_t first = a.mask ? ctx : (int64_t)ctx + (int64_t)qt * a.qpt;
+    r.jhi = a.mask ? q.kl - 1 : ctx + (int)min((int64_t)q.ql, ((int64_t)qt + 1) * a.qpt) - 1;
+    r.jlo = a.window < 0 ? 0 : (int)max((int64_t)0, first - a.window);
+    r.sink_end = min(a.sinks, r.jlo);
+    r.ns = min((r.sink_end + kKeys - 1) / kKeys, r.jlo / kKeys);
+    r.nt = r.ns + r.jhi / kKeys - r.jlo / kKeys + 1;
+    return r;
+}
+
+DG_DEVINL SeqLine seq_line(const TreeArgs& a, int s) {
+    SeqLine p;
+    p.seq = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
+    if (p.seq.ql > a.max_q_len) p.seq.ok = false;
+    p.q_tiles = p.seq.ok && p.seq.kl > 0 ? (int)(((int64_t)p.seq.ql + a.qpt - 1) / a.qpt) : 0;
+    p.len = 0;
+    if (p.q_tiles == 1 || (p.q_tiles > 0 && a.mask)) {
+        p.len = range_of(a, p.seq, 0).nt;
+    } else if (p.q_tiles > 0) {
+        p.len = min((int64_t)((p.seq.kl - 1) / kKeys + 1),
+                    ((int64_t)a.window + a.qpt + kKeys - 2) / kKeys + 1 + ((int64_t)a.sinks + kKeys - 1) / kKeys);
+    }
+    return p;
+}
+
+struct Run {
+    int64_t per_cta, start, end, seq_start;
+    int seq;
+    bool whole;      // items are not cut: a run has those that begin in it
+};
+
+DG_DEVINL int64_t warp_sum(int64_t v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Runs shorter than this many tiles cost more in pieces than they gain.
+constexpr int kMinRun = 2;
+
+// Whole CTA.  Two passes over the sequences' costs, the second up to the one that the run begins in; what a thread
+// worked out in the first round of the first pass it keeps.
+DG_DEVINL Run find_run(const TreeArgs& a, TreeShared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t mine = 0, first = 0, items = 0;
+    for (int s = tid; s < a.n_seq; s += kThreads) {
+        const SeqLine p = seq_line(a, s);
+        if (blockIdx.x == 0 && !p.seq.ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+        const int64_t c = p.cost(a);
+        if (s == tid) first = c;
+        mine += c;
+        items += p.q_tiles;
+    }
+    // (items of a call stay below 2^31 / 8 a thread; costs below 2^55 in all)
+    mine = warp_sum(mine);
+    items = warp_sum(items);
+    if (lane == 0) sh.sums[warp] = mine;
+    __syncthreads();
+    Run r;
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) total += sh.sums[w];
+    __syncthreads();
+    if (lane == 0) sh.sums[warp] = items;
+    __syncthreads();
+    items = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) items += sh.sums[w];
+    items *= (int64_t)a.head_tiles * a.Hkv;
+    __syncthreads();
+    r.per_cta = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x);
+    r.start = min(total, (int64_t)blockIdx.x * r.per_cta);
+    r.end = min(total, r.start + r.per_cta);
+    r.whole = items >= 8 * (int64_t)gridDim.x;
+    r.seq = 0;
+    r.seq_start = 0;
+    if (r.start >= r.end) return r;   // the same for the whole CTA
+    int64_t base = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += kThreads) {
+        const int s = s0 + tid;
+        const int64_t c = s0 == 0 ? first : s < a.n_seq ? seq_line(a, s).cost(a) : 0;
+        int64_t incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sh.sums[warp] = incl;
+        __syncthreads();
+        int64_t before = base, all = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sh.sums[w];
+            all += sh.sums[w];
+        }
+        incl += before;
+        if (c > 0 && incl - c <= r.start && r.start < incl) {
+            sh.found_seq = s;
+            sh.found_start = incl - c;
+        }
+        base += all;
+        __syncthreads();
+        if (base > r.start) break;   // the same for the whole CTA
+    }
+    r.seq = sh.found_seq;
+    r.seq_start = sh.found_start;
+    return r;
+}
+
+// Walks a run piece by piece (one thread).
+struct Walk {
+    int64_t at, seq_start, end, per_cta;
+    int s;
+    bool whole;
+    SeqLine p;
+
+    DG_DEVINL bool next(const TreeArgs& a, Piece& z) {
+        while (at < end) {
+            while (at >= seq_start + p.cost(a)) {   // the next sequence that has work
+                if (s + 1 >= a.n_seq) return false;
+                seq_start += p.cost(a);
+                p = seq_line(a, ++s);
+            }
+            const int64_t off = at - seq_start, item = off / p.len;
+            const int64_t begin = seq_start + item * p.len;
+            const int t0 = (int)(at - begin);
+            const int64_t per_head = (int64_t)p.q_tiles * a.head_tiles;
+            const int hk = (int)(item / per_head);
+            const int64_t x = item - hk * per_head;
+            const int qt = (int)(x / a.head_tiles), ht = (int)(x - (int64_t)qt * a.head_tiles);
+            const Range r = range_of(a, p.seq, qt);
+            const int64_t to = whole ? begin + p.len : min(end, begin + p.len);
+            at = to;
+            if (whole ? t0 != 0 : t0 >= r.nt) continue;
+            z.s = s;
+            z.hk = hk;
+            z.h0 = hk * a.group + ht * a.hpt;
+            z.nh = min(a.hpt, a.group - ht * a.hpt);
+            z.qi0 = qt * a.qpt;
+            z.qrow = p.seq.q0 + z.qi0;
+            z.nq = min(a.qpt, p.seq.ql - z.qi0);
+            z.ql = p.seq.ql;
+            z.kl = p.seq.kl;
+            z.sink_end = r.sink_end;
+            z.ns = r.ns;
+            z.jlo = r.jlo;
+            z.jhi = r.jhi;
+            z.t0 = t0;
+            z.nt = (int)min((int64_t)r.nt, to - begin) - t0;
+            z.last = (int)((begin + r.nt - 1) / per_cta);
+            z.flags = (t0 == 0 ? kStarts : 0u) | (t0 + z.nt == r.nt ? kEnds : 0u);
+            return true;
+        }
+        return false;
+    }
+};
+
+// The k-th piece of the run, for a thread or a whole warp; nt = 0 at the end.
+DG_DEVINL Piece take(TreeShared& sh, uint32_t k, bool& ok) {
+    const int slot = (int)(k % kRing);
+    if (!wait(&sh.wfull[slot], (k / kRing) & 1u)) {
+        ok = false;
+        Piece z;
+        z.nt = 0;
+        return z;
+    }
+    const Piece z = sh.piece[slot];
+    dg::mbar_arrive(&sh.wempty[slot]);
+    return z;
+}
+DG_DEVINL Piece take_warp(TreeShared& sh, uint32_t k, bool& ok) {
+    const int slot = (int)(k % kRing);
+    if (!wait_warp(&sh.wfull[slot], (k / kRing) & 1u)) {
+        ok = false;
+        Piece z;
+        z.nt = 0;
+        return z;
+    }
+    const Piece z = sh.piece[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) dg::mbar_arrive(&sh.wempty[slot]);
+    return z;
+}
+
+// Bits below n.
+DG_DEVINL uint64_t below(int64_t n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// The keys j0 .. j0 + 63 that a row sees: `pos` its position, `row` its query's row.
+DG_DEVINL uint64_t seen_keys(const TreeArgs& a, const Piece& z, int j0, int pos, int64_t row) {
+    const int ctx = z.kl - z.ql;
+    uint64_t m = below((int64_t)(a.mask ? ctx : pos + 1) - j0);
+    if (a.window >= 0) m &= ~below((int64_t)pos - a.window - j0) | below((int64_t)a.sinks - j0);
+    if (a.mask && j0 + kKeys > ctx) {
+        const uint32_t* w = a.mask + row * a.mask_words;
+        const int n0 = j0 - ctx;             // node of bit 0, from -63 on
+        auto word = [&](int i) -> uint64_t { return i >= 0 && i < a.mask_words ? w[i] : 0u; };
+        const int i = n0 >> 5, sh = n0 & 31;   // (floors)
+        uint64_t bits = (word(i) >> sh) | (word(i + 1) << (32 - sh));
+        if (sh) bits |= word(i + 2) << (64 - sh);
+        m |= bits & below((int64_t)z.kl - j0) & ~below(-(int64_t)n0);
+    }
+    return m;
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int D>
+__global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
+    k_tree(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+           const __grid_constant__ CUtensorMap tmV, const TreeArgs a) {
+    using C = TreeCfg<D>;
+    constexpr uint32_t kKVBytes = C::kKVBytes;
+    constexpr uint32_t kColS = C::kColS, kColO = C::kColO, kColP = C::kColP, kTmemCols = C::kTmemCols;
+    extern __shared__ __align__(1024) unsigned char tree_smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tree_smem_raw) + 1023) & ~uintptr_t(1023));
+    TreeShared& sh = *reinterpret_cast<TreeShared*>(smem + C::kOffBar);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        dg::mbar_init(&sh.qfull, 1);
+        dg::mbar_init(&sh.qempty, 1);
+        dg::mbar_init(&sh.oempty, 4);
+        for (int i = 0; i < 2; ++i) {
+            dg::mbar_init(&sh.kfull[i], 1);
+            dg::mbar_init(&sh.kempty[i], 1);
+            dg::mbar_init(&sh.vfull[i], 1);
+            dg::mbar_init(&sh.vempty[i], 1);
+            dg::mbar_init(&sh.pfull[i], 4);
+            dg::mbar_init(&sh.pvdone[i], 1);
+        }
+        dg::mbar_init(&sh.sfull, 1);
+        dg::mbar_init(&sh.sempty, 4);
+        dg::mbar_init(&sh.mmadone, 1);
+        dg::mbar_init(&sh.met, 4);
+        for (int i = 0; i < kRing; ++i) {
+            dg::mbar_init(&sh.wfull[i], 1);
+            dg::mbar_init(&sh.wempty[i], kReaders);
+        }
+        sh.abort_flag = 0;
+        dg::fence_mbar_init();
+    }
+    if (warp == 1) {
+        dg::tmem_alloc(&sh.tmem_base, kTmemCols);
+        dg::tmem_relinquish();
+    }
+    dg::tc_fence_before();
+    __syncthreads();
+    dg::tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
     dg::pdl_wait();
     dg::pdl_release();
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (w < a.n_seq && lane == 0) {
-        const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, (int)w, dg::kMaxKeys);
-        if (!p.ok || p.ql > a.max_q_len) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-    }
-    const int64_t row = w / a.Hq;
-    const int h = (int)(w - row * a.Hq);
-    if (row >= a.total_q) return;
-    const int s = dg::warp_owner(a.cu_q, a.n_seq, (int)row);
-    if (s >= a.n_seq) return;
-    const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
-    if (!p.ok || p.ql > a.max_q_len || row < p.q0 || row - p.q0 >= p.ql) return;
-    const int i = (int)row - p.q0, ctx = p.kl > 0 ? p.kl - p.ql : 0;
-    const int64_t pos = a.positions ? a.positions[row] : ctx + i;
-    const uint16_t* q = a.q + (row * a.Hq + h) * D + lane * E;
-    float qf[E], acc[E] = {};
-    for (int e = 0; e < E; ++e) qf[e] = bf(q[e]) * a.scale_log2;
-    float m = -INFINITY, l = 0.f;
-    const int64_t head_at = (h / (a.Hq / a.Hkv)) * a.kv.head_stride + lane * E;
-    for (int j = 0; j < p.kl; ++j) {
-        bool seen = a.window < 0 || (int64_t)j >= pos - a.window || j < a.sinks;
-        if (!a.mask)
-            seen = seen && j <= ctx + i;
-        else if (j >= ctx)
-            seen = a.mask[row * a.mask_words + (j - ctx) / 32] >> ((j - ctx) & 31) & 1u;
-        if (!seen) continue;
-        const int32_t page = a.kv.page_table[(int64_t)s * a.kv.max_pages + (j >> a.kv.page_shift)];
-        if (page < 0 || page >= a.kv.n_pages) {
-            if (lane == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-            continue;
+    const Run run = find_run(a, sh);
+    const bool any = run.start < run.end;
+    const uint32_t sQ = dg::smem_u32(smem + C::kOffQ);
+
+    if (!any) {
+        // nothing: straight to the end
+    } else if (warp == 0) {
+        if (lane == 2) {
+            // ------------------------------------------------ the walk, and the queries
+            dg::prefetch_tmap(&tmQ);
+            Walk walk{run.start, run.seq_start, run.end, run.per_cta, run.seq, run.whole, seq_line(a, run.seq)};
+            const uint32_t bytes = (uint32_t)(a.hpt * a.qpt) * kSub * 2 * (D / kSub);
+            bool ok = true, more = true;
+            uint32_t k = 0, copies = 0;
+            for (; more; ++k) {
+                const int slot = (int)(k % kRing);
+                Piece z;
+                more = !aborted(sh) && walk.next(a, z);
+                if (!more) z.nt = 0;
+                if (!wait(&sh.wempty[slot], ((k / kRing) & 1u) ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                sh.piece[slot] = z;
+                dg::mbar_arrive(&sh.wfull[slot]);   // releases the piece to its readers
+                if (!more) break;
+                if (!wait(&sh.qempty, (k & 1u) ^ 1u)) {   // the last piece's last S has read its queries
+                    ok = false;
+                    break;
+                }
+                dg::mbar_arrive_expect_tx(&sh.qfull, bytes);
+#pragma unroll
+                for (int c = 0; c < D / kSub; ++c)
+                    dg::tma_load_3d(smem + C::kOffQ + c * kQSub, &tmQ, c * kSub, z.h0, z.qrow, &sh.qfull);
+                ++copies;
+            }
+            if (!ok) do_abort(sh, a.status);
+            if (aborted(sh) && copies > 0) (void)wait(&sh.qfull, (copies - 1u) & 1u);   // the last copy landed
+        } else if (lane < 2) {
+            // ------------------------------------------------ keys (lane 0) and values (lane 1)
+            const bool is_k = lane == 0;
+            const CUtensorMap* tm = is_k ? &tmK : &tmV;
+            uint64_t* full = is_k ? sh.kfull : sh.vfull;
+            uint64_t* empty = is_k ? sh.kempty : sh.vempty;
+            unsigned char* ring = smem + (is_k ? C::kOffK : C::kOffV);
+            dg::prefetch_tmap(tm);
+            const int box_shift = min(a.kv.page_shift, 6), boxes = kKeys >> box_shift, size = 1 << box_shift;
+            uint32_t g = 0;
+            int issued[2] = {0, 0};
+            bool ok = true;
+            for (uint32_t k = 0; ok && !aborted(sh); ++k) {
+                const Piece z = take(sh, k, ok);
+                if (z.nt == 0) break;
+                const int32_t* table = a.kv.page_table + (int64_t)z.s * a.kv.max_pages;
+                for (int i = 0; i < z.nt; ++i, ++g) {
+                    const int st = (int)(g & 1u), j0 = z.tile(i) * kKeys;
+                    // the pages of the tile's boxes, read before the wait; n_pages reads zeros
+                    int32_t entry[8];
+                    bool bad = false;
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) {
+                        const int j = j0 + (b << box_shift);
+                        entry[b] = (int32_t)a.kv.n_pages;
+                        if (b < boxes && j <= z.jhi && (j + (size - 1) >= z.jlo || j < z.sink_end)) {
+                            entry[b] = table[j >> a.kv.page_shift];
+                            bad = bad || entry[b] < 0 || entry[b] >= a.kv.n_pages;
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        sh.pages[lane][b] = entry[b] < 0 || entry[b] >= a.kv.n_pages ? (int32_t)a.kv.n_pages : entry[b];
+                    if (bad) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+                    if (!wait(&empty[st], ((g >> 1) & 1u) ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    dg::mbar_arrive_expect_tx(&full[st], kKVBytes);
+                    unsigned char* dst = ring + st * kKVBytes;
+#pragma unroll 1
+                    for (int b = 0; b < boxes; ++b) {
+                        const int row = b << box_shift, page = sh.pages[lane][b];
+                        const int slot = (j0 + row) & ((1 << a.kv.page_shift) - 1);
+#pragma unroll
+                        for (int c = 0; c < D / kSub; ++c)
+                            dg::tma_load_4d(dst + c * kKSub + row * kSub * 2, tm, c * kSub, slot, z.hk, page, &full[st]);
+                    }
+                    ++issued[st];
+                }
+            }
+            if (!ok) do_abort(sh, a.status);
+            if (aborted(sh)) {   // never leave with a copy still landing in shared memory
+                for (int st = 0; st < 2; ++st)
+                    if (issued[st] > 0) (void)wait(&full[st], (uint32_t)(issued[st] - 1) & 1u);
+            }
         }
-        const int64_t at = page * a.kv.page_stride + (j & ((1 << a.kv.page_shift) - 1)) * a.kv.slot_stride + head_at;
-        float x = 0.f;
-        for (int e = 0; e < E; ++e) x = fmaf(qf[e], bf(a.kv.k[at + e]), x);
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        const float top = fmaxf(m, x), f = m == -INFINITY ? 0.f : exp2f(m - top), w2 = exp2f(x - top);
-        l = l * f + w2;
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + w2 * bf(a.kv.v[at + e]);
-        m = top;
+    } else if (warp == 1) {
+        // ------------------------------------------------ the products
+        if (dg::elect_leader()) {
+            // S = Q K^T: both K-major, bit 13 negates Q; O += P V: the values' rows are N-major
+            const uint32_t idS = dg::instr_desc(kTile, kKeys, false) | (a.negate ? 1u << 13 : 0u);
+            constexpr uint32_t idO = dg::instr_desc(kTile, D, true);
+            uint32_t g = 0;
+            bool ok = true;
+            for (uint32_t k = 0; ok && !aborted(sh); ++k) {
+                const int nt = take(sh, k, ok).nt;
+                if (nt == 0) break;
+                if (!wait(&sh.qfull, k & 1u)) {
+                    ok = false;
+                    break;
+                }
+                for (int i = 0; i <= nt; ++i) {
+                    if (i < nt) {   // S of tile g + i, once the softmax has read the last S
+                        const uint32_t gs = g + (uint32_t)i;
+                        const int st = (int)(gs & 1u);
+                        if (!wait(&sh.kfull[st], (gs >> 1) & 1u) || !wait(&sh.sempty, (gs & 1u) ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        dg::tc_fence_after();
+                        const uint32_t sK = dg::smem_u32(smem + C::kOffK + st * kKVBytes);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t offq = (uint32_t)(kk >> 2) * kQSub + (uint32_t)(kk & 3) * 32u;
+                            const uint32_t offk = (uint32_t)(kk >> 2) * kKSub + (uint32_t)(kk & 3) * 32u;
+                            dg::tc_mma_f16(tmem + kColS, dg::smem_desc(sQ + offq, 16, 1024, 128),
+                                           dg::smem_desc(sK + offk, 16, 1024, 128), idS, kk > 0 ? 1u : 0u);
+                        }
+                        dg::tc_commit(&sh.sfull);
+                        dg::tc_commit(&sh.kempty[st]);
+                        if (i == nt - 1) dg::tc_commit(&sh.qempty);   // the queries, after the piece's last S
+                    }
+                    if (i >= 1) {   // O += P V of tile g + i - 1 once the softmax has written P
+                        const uint32_t gp = g + (uint32_t)i - 1u;
+                        const int st = (int)(gp & 1u);
+                        if (!wait(&sh.pfull[st], (gp >> 1) & 1u) || !wait(&sh.vfull[st], (gp >> 1) & 1u) ||
+                            (i == 1 && !wait(&sh.oempty, (k & 1u) ^ 1u))) {   // the last piece's O read out
+                            ok = false;
+                            break;
+                        }
+                        dg::tc_fence_after();
+                        const uint32_t sV = dg::smem_u32(smem + C::kOffV + st * kKVBytes);
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            dg::tc_mma_f16_ts(tmem + kColO, tmem + kColP + (uint32_t)(st * 32 + kk * 8),
+                                              dg::smem_desc(sV + (uint32_t)kk * 16u * 128u, kKSub, 1024, 128), idO,
+                                              (i > 1 || kk > 0) ? 1u : 0u);
+                        dg::tc_commit(&sh.pvdone[st]);
+                        dg::tc_commit(&sh.vempty[st]);
+                    }
+                }
+                g += (uint32_t)nt;
+            }
+            if (!ok) do_abort(sh, a.status);
+            dg::tc_commit(&sh.mmadone);   // every product has completed before the tensor memory is released
+            (void)wait(&sh.mmadone, 0);
+        }
+    } else {
+        // ------------------------------------------------ softmax, a row a thread
+        const int q = warp & 3;   // the quarter of TMEM's lanes this warp may access
+        const int row = q * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        uint32_t g = 0, masked = 0, meetings = 0;
+        bool ok = true, to_join = false;
+        // Each warp has left something for the others.  (What it leaves next but one is behind another meeting: two places
+        // of each kind are enough.)
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) dg::mbar_arrive(&sh.met);
+            return wait_warp(&sh.met, meetings++ & 1u);
+        };
+        for (uint32_t k = 0; ok; ++k) {
+            const Piece z = take_warp(sh, k, ok);
+            if (z.nt == 0) break;
+            const int ctx = z.kl - z.ql;
+            const int qi = row / a.hpt, hi = row - qi * a.hpt;
+            const bool valid = qi < z.nq && hi < z.nh;
+            const bool idle = !__any_sync(0xffffffffu, valid);   // no row of this warp's: only its arrivals
+            const int64_t qrow = (int64_t)z.qrow + (valid ? qi : 0);
+            int pos = ctx + z.qi0 + (valid ? qi : 0), top = ctx + z.qi0 + z.nq - 1;
+            if (a.mask && a.window >= 0) {   // the nodes' own positions, and the last of the item's
+                pos = max(a.positions[qrow], ctx);
+                const int w = __reduce_max_sync(0xffffffffu, pos);
+                int32_t* tops = sh.top_position[k & 1u];
+                if (lane == 0) tops[q] = w;
+                if (!meet()) {
+                    ok = false;
+                    break;
+                }
+                top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+            }
+            const int all_hi = a.mask ? ctx - 1 : ctx + z.qi0;   // every row sees keys up to it,
+            const int64_t all_lo = a.window < 0 ? 0 : (int64_t)top - a.window;   // from here on
+            float m_ref = -INFINITY, l = 0.f;
+            for (int i = 0; i < z.nt; ++i) {
+                const uint32_t gi = g + (uint32_t)i;
+                if (!wait_warp(&sh.sfull, gi & 1u)) {
+                    ok = false;
+                    break;
+                }
+                dg::tc_fence_after();
+                float x[2][32];
+                if (!idle) {
+                    uint32_t raw[2][32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) dg::tmem_ld32_nowait(tmem + lane_base + kColS + (uint32_t)(c * 32), raw[c]);
+                    dg::tmem_ld_wait_dep(raw[0]);
+                    dg::tmem_ld_wait_dep(raw[1]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[c][e] = __uint_as_float(raw[c][e]);
+                }
+                dg::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) dg::mbar_arrive(&sh.sempty);
+                const int j0 = z.tile(i) * kKeys, j1 = j0 + kKeys - 1;
+                if (j1 > all_hi || (j0 < all_lo && j1 >= a.sinks)) {   // not all of it is seen by all
+                    const uint64_t m = valid ? seen_keys(a, z, j0, pos, qrow) : 0ull;
+                    const uint32_t w0 = __reduce_or_sync(0xffffffffu, (uint32_t)m);
+                    const uint32_t w1 = __reduce_or_sync(0xffffffffu, (uint32_t)(m >> 32));
+                    uint64_t* seen = sh.seen[masked & 1u];
+                    ++masked;
+                    if (lane == 0) seen[q] = (uint64_t)w1 << 32 | w0;
+                    if (!meet()) {
+                        ok = false;
+                        break;
+                    }
+                    const uint64_t any_row = seen[0] | seen[1] | seen[2] | seen[3];
+                    if (~any_row) {   // the values nobody sees
+                        if (!wait_warp(&sh.vfull[gi & 1u], (gi >> 1) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        unsigned char* vt = smem + C::kOffV + (gi & 1u) * kKVBytes;
+                        for (int c = row; c < kKeys * (D / kSub) * 8; c += 128) {   // 16-byte chunks
+                            if (!(any_row >> ((c >> 3) & (kKeys - 1)) & 1u))
+                                reinterpret_cast<uint4*>(vt)[c] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        dg::fence_proxy_async_smem();   // before the product reads them (pfull below)
+                    }
+                    if (!idle) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t w = c ? (uint32_t)(m >> 32) : (uint32_t)m;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[c][e] = w >> e & 1u ? x[c][e] : -INFINITY;
+                        }
+                    }
+                }
+                if (!idle) {
+                    float mx[16];   // the tile's maximum of the raw scores
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        mx[e] = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
+#pragma unroll
+                    for (int wd = 8; wd >= 1; wd >>= 1)
+#pragma unroll
+                        for (int e = 0; e < wd; ++e) mx[e] = fmaxf(mx[e], mx[e + wd]);
+                    const float tmax = mx[0] * a.scale_log2;   // (-inf stays: the scale is above 0)
+                    const bool rescale = __any_sync(0xffffffffu, valid && tmax > m_ref + kRescaleAbove);
+                    // O is rescaled after this piece's last P V only; else P's buffer must have been read by the
+                    // product two tiles back, which may be the last piece's
+                    if ((rescale && i > 0) || gi > 1) {
+                        const uint32_t gj = (rescale && i > 0) ? gi - 1 : gi - 2;
+                        if (!wait_warp(&sh.pvdone[gj & 1u], (gj >> 1) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        dg::tc_fence_after();
+                    }
+                    if (rescale) {
+                        const float m_new = fmaxf(m_ref, tmax);
+                        const float alpha = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);
+                        l *= alpha;
+                        if (i > 0) {
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                const uint32_t ta = tmem + lane_base + kColO + (uint32_t)(c * 32);
+                                dg::tmem_ld32(ta, o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                                dg::tmem_st32(ta, o);
+                                dg::tmem_st_wait();   // before the next chunk's load may reuse the registers
+                            }
+                        }
+                        m_ref = m_new;
+                    }
+                    const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const uint64_t cc = f2(a.scale_log2, a.scale_log2), mm = f2(neg_m, neg_m);
+                    uint64_t acc = f2(0.f, 0.f);
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float z0, z1;
+                            f2_split(f2_fma(f2(x[c][e], x[c][e + 1]), cc, mm), z0, z1);
+                            const float p0 = ex2(z0), p1 = ex2(z1);
+                            acc = f2_add(acc, f2(p0, p1));
+                            pk[c * 16 + e / 2] = pack_bf16x2(p0, p1);
+                        }
+                    }
+                    float sa, sb;
+                    f2_split(acc, sa, sb);
+                    dg::tmem_st32u(tmem + lane_base + kColP + (gi & 1u) * 32u, pk);
+                    dg::tmem_st_wait();
+                    l += sa + sb;
+                }
+                dg::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) dg::mbar_arrive(&sh.pfull[gi & 1u]);
+            }
+            if (!ok) break;
+            const uint32_t gl = g + (uint32_t)z.nt - 1u;   // the piece's last P V
+            if (!wait_warp(&sh.pvdone[gl & 1u], (gl >> 1) & 1u)) {
+                ok = false;
+                break;
+            }
+            dg::tc_fence_after();
+            if (!idle) {
+                const bool whole = z.flags == (kStarts | kEnds);
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const int64_t out = qrow * a.Hq + z.h0 + (valid ? hi : 0);
+                const int64_t slot = (int64_t)blockIdx.x * 2 + (z.flags & kStarts ? 1 : 0);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    dg::tmem_ld32(tmem + lane_base + kColO + (uint32_t)(c * 32), o);
+                    if (!valid) continue;
+                    if (whole) {
+                        if (!(l > 0.f)) {   // a row that sees nothing
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = l == 0.f ? 0.f : o[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(a.o + out * D + c * 32 + e) = make_uint4(
+                                pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
+                                pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv), pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            a.part_o[(slot * (D / 4) + c * 8 + e / 4) * a.rows + row] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                if (valid && whole && a.lse) a.lse[out] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+                if (valid && !whole) a.part_ml[slot * a.rows + row] = make_float2(m_ref, l);
+            }
+            if (row == 0 && (z.flags & kStarts) && !(z.flags & kEnds)) {
+                a.desc[2 * blockIdx.x] = make_int4(z.last - (int)blockIdx.x, z.qrow, z.h0, z.nq);
+                a.desc[2 * blockIdx.x + 1] = make_int4(z.nh, 0, 0, 0);
+                to_join = true;
+            }
+            dg::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) dg::mbar_arrive(&sh.oempty);   // O read out: the next piece may overwrite it
+            g += (uint32_t)z.nt;
+        }
+        if (!ok) do_abort(sh, a.status);
+        if (row == 0 && !to_join) a.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int e = 0; e < E; e += 2) {
-        uint32_t r;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(acc[e + 1] * inv), "f"(acc[e] * inv));
-        *reinterpret_cast<uint32_t*>(a.o + (row * a.Hq + h) * D + lane * E + e) = r;
+    if (!any && threadIdx.x == 0) a.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+
+    // the sequences without keys: their rows of zeros
+    for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
+        const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
+        if (!p.ok || p.kl != 0 || p.ql > a.max_q_len) continue;
+        const int64_t first = (int64_t)p.q0 * a.Hq, rows = (int64_t)p.ql * a.Hq;
+        for (int64_t i = threadIdx.x; i < rows * (D / 8); i += kThreads)
+            reinterpret_cast<uint4*>(a.o + first * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse)
+            for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[first + i] = -INFINITY;
     }
-    if (lane == 0 && a.lse) a.lse[row * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+
+    dg::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        dg::tc_fence_after();
+        dg::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins an item's pieces: the last one of CTA c (slot 1) and the first ones (slot 0) of the CTAs that follow
+// it.  blockIdx.x = c, blockIdx.y = 16 of the dimensions; a thread owns a row's, most blocks find nothing to join.
+constexpr int kJoinDims = 16;
+template <int D>
+__global__ void __launch_bounds__(kTile) k_tree_join(const TreeArgs a) {
+    dg::pdl_wait();
+    dg::pdl_release();
+    const int c = blockIdx.x, row = threadIdx.x;
+    const int4 d0 = a.desc[2 * c];
+    if (d0.x == 0) return;
+    const int n = d0.x + 1, nh = a.desc[2 * c + 1].x;
+    const int qi = row / a.hpt, hi = row - qi * a.hpt;
+    if (qi >= d0.w || hi >= nh) return;
+    auto slot = [&](int i) -> int64_t { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) M = fmaxf(M, a.part_ml[slot(i) * a.rows + row].x);
+    float L = 0.f;
+    float4 o[kJoinDims / 4];
+#pragma unroll
+    for (int e = 0; e < kJoinDims / 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float2 ml = a.part_ml[slot(i) * a.rows + row];
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        L += ml.y * f;
+#pragma unroll
+        for (int e = 0; e < kJoinDims / 4; ++e) {
+            const float4 v = a.part_o[(slot(i) * (D / 4) + blockIdx.y * (kJoinDims / 4) + e) * a.rows + row];
+            if (f != 0.f) {   // (a piece of which the row saw nothing adds nothing, whatever its values)
+                o[e].x += v.x * f;
+                o[e].y += v.y * f;
+                o[e].z += v.z * f;
+                o[e].w += v.w * f;
+            }
+        }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int64_t out = ((int64_t)d0.y + qi) * a.Hq + d0.z + hi;
+    uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + blockIdx.y * kJoinDims);
+#pragma unroll
+    for (int e = 0; e < kJoinDims / 4; e += 2)
+        dst[e / 2] = make_uint4(pack_bf16x2(o[e].x * inv, o[e].y * inv), pack_bf16x2(o[e].z * inv, o[e].w * inv),
+                                pack_bf16x2(o[e + 1].x * inv, o[e + 1].y * inv), pack_bf16x2(o[e + 1].z * inv, o[e + 1].w * inv));
+    if (blockIdx.y == 0 && a.lse) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// ------------------------------------------------------------------ host side
+// Rows of a piece in the workspace.
+int piece_rows(int32_t max_q_len, int32_t group) {
+    return (int)std::min<int64_t>(kTile, ((int64_t)max_q_len * group + 31) / 32 * 32);
+}
+size_t piece_bytes(int32_t D, int rows) {
+    const size_t ctas = D == 256 ? TreeCfg<256>::kMaxCtas : TreeCfg<128>::kMaxCtas;
+    return ctas * 32 + ctas * 2 * rows * ((size_t)D * 4 + 8);
+}
+
+template <int D>
+dg_status launch_tree(TreeArgs& a, const uint16_t* q, void* workspace, cudaStream_t stream) {
+    using C = TreeCfg<D>;
+    const int sms = dghost::sm_count();
+    if (sms <= 0) return DG_ERR_CUDA;
+    CUtensorMap tq, tk, tv;
+    {   // queries: 64 columns x the item's heads x its queries
+        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.total_q};
+        const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)a.Hq * D * 2};
+        const uint32_t box[3] = {(uint32_t)kSub, (uint32_t)a.hpt, (uint32_t)a.qpt};
+        if (!dghost::encode_tmap(&tq, 0, 3, const_cast<uint16_t*>(q), dims, strides, box, 128)) return DG_ERR_CUDA;
+    }
+    for (auto [tm, base] : {std::pair<CUtensorMap*, uint16_t*>{&tk, a.kv.k}, {&tv, a.kv.v}}) {
+        // a page: 64 columns of a head, up to 64 of its slots
+        const uint64_t dims[4] = {(uint64_t)D, 1ull << a.kv.page_shift, (uint64_t)a.Hkv, (uint64_t)a.kv.n_pages};
+        const uint64_t strides[3] = {(uint64_t)a.kv.slot_stride * 2, (uint64_t)a.kv.head_stride * 2,
+                                     (uint64_t)a.kv.page_stride * 2};
+        const uint32_t box[4] = {(uint32_t)kSub, 1u << std::min(a.kv.page_shift, 6), 1u, 1u};
+        if (!dghost::encode_tmap(tm, 0, 4, base, dims, strides, box, 128)) return DG_ERR_CUDA;
+    }
+    // the attribute once a device
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DG_ERR_CUDA;
+    if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+        if (cudaFuncSetAttribute(k_tree<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tree_smem<D>()) != cudaSuccess)
+            return DG_ERR_CUDA;
+        if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    const unsigned grid = (unsigned)std::min(sms * C::kCtasPerSm, C::kMaxCtas);
+    a.desc = static_cast<int4*>(workspace);
+    a.part_o = reinterpret_cast<float4*>(a.desc + 2 * C::kMaxCtas);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)C::kMaxCtas * 2 * (D / 4) * a.rows);
+    cudaError_t e = dghost::launch_pdl(k_tree<D>, dim3(grid), dim3(kThreads), tree_smem<D>(), stream, tq, tk, tv, a);
+    dghost::count_launch();
+    if (e != cudaSuccess) return DG_ERR_CUDA;
+    e = dghost::launch_pdl(k_tree_join<D>, dim3(grid, D / kJoinDims), dim3(kTile), 0, stream, a);
+    dghost::count_launch();
+    return dghost::cuda_status(e);
 }
 
 dg_status tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse, const int32_t* cu_q,
@@ -109,7 +936,6 @@ dg_status tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* 
     if (!workspace || workspace_bytes < dg_tree_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D))
         return DG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
-    a.q = q;
     a.o = o;
     a.lse = lse;
     a.cu_q = cu_q;
@@ -123,21 +949,26 @@ dg_status tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* 
     a.mask_words = mask_words;
     a.window = window;
     a.sinks = window < 0 ? 0 : sinks;
-    a.scale_log2 = scale * kLog2e;
+    a.group = Hq / Hkv;
+    a.hpt = std::min(a.group, kTile);
+    a.qpt = kTile / a.hpt;
+    a.head_tiles = (a.group + kTile - 1) / kTile;
+    a.rows = piece_rows(max_q_len, a.group);
+    // a scale of 0 weighs every key alike: the smallest float keeps masked scores (-inf) what they are and moves
+    // no finite score by more than 5e-7
+    a.scale_log2 = std::max(fabsf(scale) * kLog2e, std::numeric_limits<float>::denorm_min());
+    a.negate = scale < 0.f;
     a.status = dghost::status_word();
-    const int64_t blocks = (std::max<int64_t>(total_q * Hq, n_seq) + 3) / 4;
-    if (blocks > 0x7fffffffLL) return DG_ERR_INVALID_ARG;
-    auto kern = D == 64 ? k_tree_simple<64> : D == 128 ? k_tree_simple<128> : k_tree_simple<256>;
-    const cudaError_t e = dghost::launch_pdl(kern, dim3((unsigned)blocks), dim3(128), 0, (cudaStream_t)stream, a);
-    dghost::count_launch();
-    return dghost::cuda_status(e);
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (D == 64) return launch_tree<64>(a, q, workspace, st);
+    return D == 128 ? launch_tree<128>(a, q, workspace, st) : launch_tree<256>(a, q, workspace, st);
 }
 
 }  // namespace
 
 extern "C" size_t dg_tree_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D) {
     if (n_seq < 1 || max_q_len < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
-    return 16;
+    return piece_bytes(D, piece_rows(max_q_len, Hq / Hkv));
 }
 
 extern "C" dg_status dg_tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,

@@ -491,7 +491,8 @@ DG_API dg_status dg_kv_append_norm(const uint16_t* k, int64_t ldk, const uint16_
  *   context j  when window < 0, or j >= positions[cu_q[s] + i] - window, or j < sinks.
  * o = softmax of scale * q . k over what it sees, applied to v; h' = h / (Hq / Hkv), as dg_paged_attention.
  *   tree_mask (device) [total_q][mask_words] uint32, 4-byte aligned; mask_words >= ceil(max_q_len / 32).
- *   positions (device, may be NULL when window < 0) [total_q] int32: the nodes' positions (c + depth).
+ *   positions (device, may be NULL when window < 0) [total_q] int32: the nodes' positions, c + depth (one below c
+ *             counts as c).
  *   sinks     >= 0: first tokens of the context that stay visible to a window; ignored without one.
  *   q, o, lse, cu_q, max_q_len, scale, cache, workspace: as dg_paged_attention.  A sequence with more than max_q_len
  *             queries raises DG_DEV_BAD_PARAM and is skipped; the other refusals are the same.
