@@ -28,16 +28,18 @@ struct PagedSeq {
     bool ok;
 };
 
-DG_DEVINL PagedSeq paged_seq(const PagedKV& c, const int32_t* cu_q, int64_t total_q, int s, int32_t max_keys) {
+DG_DEVINL PagedSeq paged_seq_of(const PagedKV& c, int64_t total_q, int32_t q0, int32_t q1, int32_t kl, int32_t max_keys) {
     PagedSeq r;
-    r.q0 = cu_q[s];
-    const int32_t q1 = cu_q[s + 1];
-    r.kl = c.kv_len[s];
+    r.q0 = q0;
+    r.kl = kl;
     r.ok = r.q0 >= 0 && q1 >= r.q0 && (int64_t)q1 <= total_q && r.kl >= 0 && r.kl <= max_keys &&
            (int64_t)r.kl <= c.capacity();
     r.ql = r.ok ? q1 - r.q0 : 0;
     if (r.kl > 0 && r.ql > r.kl) r.ok = false;
     return r;
+}
+DG_DEVINL PagedSeq paged_seq(const PagedKV& c, const int32_t* cu_q, int64_t total_q, int s, int32_t max_keys) {
+    return paged_seq_of(c, total_q, cu_q[s], cu_q[s + 1], c.kv_len[s], max_keys);
 }
 
 // The number of sequences that end at or before row t (cu_q[1 .. n] <= t): the index of the

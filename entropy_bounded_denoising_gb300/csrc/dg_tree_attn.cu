@@ -9,8 +9,8 @@
 // and are joined by a second kernel in the order of the line.  Where there are many items a run takes whole ones.
 //
 // A CTA (two an SM; one for heads of 256):
-//   warp 0      lane 2 walks the run, publishes its pieces in a ring and copies their queries; lanes 0 and 1
-//               copy keys and values (two tiles each), page by page;
+//   warp 0      walks the run, publishes its pieces in a ring and copies their queries, keys and values (two tiles
+//               each), page by page, a box a lane;
 //   warp 1      issues the products: S = Q K^T (128 x 64) into TMEM, O += P V with P from TMEM;
 //   warps 2..5  the softmax, a row a thread.
 // A tile that not all rows see whole gets each row's 64-bit mask: the window's and the context's ranges, and the row's
@@ -39,7 +39,7 @@ constexpr uint32_t kQSub = kTile * kSub * 2, kKSub = kKeys * kSub * 2;
 constexpr float kRescaleAbove = 8.f;   // log2 units a row's maximum may grow before it moves: P <= 2^8
 constexpr int kThreads = 192;
 constexpr int kRing = 4;        // pieces published ahead
-constexpr int kReaders = 7;     // of a piece: two copies, the products, four softmax warps (the walker reads none)
+constexpr int kReaders = 5;     // of a piece: the products, four softmax warps
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -124,12 +124,11 @@ struct __align__(8) TreeShared {
     uint64_t wfull[kRing], wempty[kRing];
     uint64_t met;                 // the four softmax warps' own barrier (bounded, unlike bar.sync)
     uint64_t seen[2][4];          // of a masked tile, by warp: the keys some row sees
-    int64_t sums[kThreads / 32];
+    int64_t sums[kThreads / 32], items[kThreads / 32];
     int64_t found_start;
     Piece piece[kRing];           // nt 0: no more
-    int32_t pages[2][8];          // of the tile that a copying lane is at
     int32_t top_position[2][4];
-    int32_t found_seq;
+    int32_t found_seq, zeros;     // zeros: some sequence has queries and no keys
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -193,11 +192,19 @@ DG_DEVINL Range range_of(const TreeArgs& a, const dg::PagedSeq& q, int qt) {
     return r;
 }
 
-DG_DEVINL SeqLine seq_line(const TreeArgs& a, int s) {
+// What a sequence's line is worked out from, asked for ahead of its use.
+struct RawSeq {
+    int32_t q0, q1, kl;
+};
+DG_DEVINL RawSeq raw_seq(const TreeArgs& a, int s) {
+    return s < a.n_seq ? RawSeq{a.cu_q[s], a.cu_q[s + 1], a.kv.kv_len[s]} : RawSeq{0, 0, 0};
+}
+
+DG_DEVINL SeqLine seq_line(const TreeArgs& a, const RawSeq& x) {
     SeqLine p;
-    p.seq = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
+    p.seq = dg::paged_seq_of(a.kv, a.total_q, x.q0, x.q1, x.kl, dg::kMaxKeys);
     if (p.seq.ql > a.max_q_len) p.seq.ok = false;
-    p.q_tiles = p.seq.ok && p.seq.kl > 0 ? (int)(((int64_t)p.seq.ql + a.qpt - 1) / a.qpt) : 0;
+    p.q_tiles = p.seq.ok && p.seq.kl > 0 ? (p.seq.ql <= a.qpt ? (p.seq.ql > 0 ? 1 : 0) : (int)(((int64_t)p.seq.ql + a.qpt - 1) / a.qpt)) : 0;
     p.len = 0;
     if (p.q_tiles == 1 || (p.q_tiles > 0 && a.mask)) {
         p.len = range_of(a, p.seq, 0).nt;
@@ -212,6 +219,7 @@ struct Run {
     int64_t per_cta, start, end, seq_start;
     int seq;
     bool whole;      // items are not cut: a run has those that begin in it
+    bool zeros;      // some sequence has queries and no keys
 };
 
 DG_DEVINL int64_t warp_sum(int64_t v) {
@@ -219,57 +227,107 @@ DG_DEVINL int64_t warp_sum(int64_t v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+DG_DEVINL int64_t warp_scan(int64_t v) {   // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
+}
 
 // Runs shorter than this many tiles cost more in pieces than they gain.
 constexpr int kMinRun = 2;
 
-// Whole CTA.  Two passes over the sequences' costs, the second up to the one that the run begins in; what a thread
-// worked out in the first round of the first pass it keeps.
-DG_DEVINL Run find_run(const TreeArgs& a, TreeShared& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t mine = 0, first = 0, items = 0;
-    for (int s = tid; s < a.n_seq; s += kThreads) {
-        const SeqLine p = seq_line(a, s);
-        if (blockIdx.x == 0 && !p.seq.ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-        const int64_t c = p.cost(a);
-        if (s == tid) first = c;
-        mine += c;
-        items += p.q_tiles;
-    }
-    // (items of a call stay below 2^31 / 8 a thread; costs below 2^55 in all)
-    mine = warp_sum(mine);
-    items = warp_sum(items);
-    if (lane == 0) sh.sums[warp] = mine;
-    __syncthreads();
-    Run r;
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) total += sh.sums[w];
-    __syncthreads();
-    if (lane == 0) sh.sums[warp] = items;
-    __syncthreads();
-    items = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) items += sh.sums[w];
-    items *= (int64_t)a.head_tiles * a.Hkv;
-    __syncthreads();
-    r.per_cta = max((int64_t)kMinRun, (total + gridDim.x - 1) / gridDim.x);
+DG_DEVINL void cut(Run& r, int64_t total, int64_t items) {
+    r.per_cta = max((int64_t)kMinRun, total < (1LL << 31) ? (int64_t)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
+                                                          : (total + gridDim.x - 1) / gridDim.x);
     r.start = min(total, (int64_t)blockIdx.x * r.per_cta);
     r.end = min(total, r.start + r.per_cta);
     r.whole = items >= 8 * (int64_t)gridDim.x;
     r.seq = 0;
     r.seq_start = 0;
+}
+
+// The run of a call of few sequences, found by one warp while the others wait for its pieces.
+constexpr int kFew = 4;
+DG_DEVINL Run find_run_warp(const TreeArgs& a) {
+    const int lane = threadIdx.x & 31;
+    int64_t c[kFew];
+    int64_t sum = 0;
+    int items = 0;    // (query tiles of 128 sequences: below 2^31 together, as their queries are)
+    bool zeros = false;
+    RawSeq raw[kFew];
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) raw[k] = raw_seq(a, k * 32 + lane);
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+        c[k] = 0;
+        if (k * 32 >= a.n_seq) continue;
+        const SeqLine p = seq_line(a, raw[k]);
+        if (blockIdx.x == 0 && !p.seq.ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+        c[k] = p.cost(a);
+        zeros = zeros || (p.seq.ok && p.seq.kl == 0 && p.seq.ql > 0);
+        sum += c[k];
+        items += p.q_tiles;
+    }
+    Run r;
+    cut(r, warp_sum(sum), (int64_t)__reduce_add_sync(0xffffffffu, items) * a.head_tiles * a.Hkv);
+    r.zeros = __any_sync(0xffffffffu, zeros);
+    int64_t base = 0;
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) {
+        if (k * 32 >= a.n_seq) break;
+        const int64_t incl = base + warp_scan(c[k]);
+        const uint32_t hit = __ballot_sync(0xffffffffu, incl - c[k] <= r.start && r.start < incl);
+        if (hit) {
+            r.seq = k * 32 + __ffs(hit) - 1;
+            r.seq_start = __shfl_sync(0xffffffffu, incl - c[k], __ffs(hit) - 1);
+        }
+        base = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return r;
+}
+
+// Of many: the whole CTA.  Two passes over the sequences' costs, the second up to the one that the run begins in.
+DG_DEVINL Run find_run(const TreeArgs& a, TreeShared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t mine = 0, first = 0, items = 0;
+    bool zeros = false;
+#pragma unroll 4
+    for (int s = tid; s < a.n_seq; s += kThreads) {
+        const SeqLine p = seq_line(a, raw_seq(a, s));
+        if (blockIdx.x == 0 && !p.seq.ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+        const int64_t c = p.cost(a);
+        zeros = zeros || (p.seq.ok && p.seq.kl == 0 && p.seq.ql > 0);
+        if (s == tid) first = c;
+        mine += c;
+        items += p.q_tiles;
+    }
+    mine = warp_sum(mine);
+    items = warp_sum(items);
+    if (lane == 0) {
+        sh.sums[warp] = mine;
+        sh.items[warp] = items;
+    }
+    Run r;
+    r.zeros = __syncthreads_or(zeros);
+    int64_t total = 0;
+    items = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        total += sh.sums[w];
+        items += sh.items[w];
+    }
+    __syncthreads();
+    cut(r, total, items * a.head_tiles * a.Hkv);
     if (r.start >= r.end) return r;   // the same for the whole CTA
     int64_t base = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += kThreads) {
         const int s = s0 + tid;
-        const int64_t c = s0 == 0 ? first : s < a.n_seq ? seq_line(a, s).cost(a) : 0;
-        int64_t incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
+        const int64_t c = s0 == 0 ? first : seq_line(a, raw_seq(a, s)).cost(a);
+        int64_t incl = warp_scan(c);
         if (lane == 31) sh.sums[warp] = incl;
         __syncthreads();
         int64_t before = base, all = 0;
@@ -292,49 +350,88 @@ DG_DEVINL Run find_run(const TreeArgs& a, TreeShared& sh) {
     return r;
 }
 
-// Walks a run piece by piece (one thread).
+// Walks a run piece by piece (a warp, uniformly).  From item to item by counting: a division or a read that is waited for
+// costs the copies behind it a tile.
 struct Walk {
-    int64_t at, seq_start, end, per_cta;
-    int s;
+    int64_t begin, at, end, per_cta;   // of the item on the line; where the run is in it
+    int s, hk, qt, ht;
     bool whole;
     SeqLine p;
+    RawSeq next_raw;                   // of the sequence behind it
+
+    DG_DEVINL void start(const TreeArgs& a, const Run& r) {
+        end = r.end;
+        at = r.start;
+        per_cta = r.per_cta;
+        whole = r.whole;
+        s = r.seq;
+        hk = qt = ht = 0;
+        begin = r.seq_start;
+        const RawSeq raw = raw_seq(a, s);
+        next_raw = raw_seq(a, s + 1);
+        p = seq_line(a, raw);
+        if (at >= end) return;
+        const int64_t off = at - begin, per_head = (int64_t)p.q_tiles * a.head_tiles;
+        const int64_t item = off < (1LL << 31) ? (uint32_t)off / (uint32_t)p.len : off / p.len;
+        begin += item * p.len;
+        if (item < (1LL << 31) && per_head < (1LL << 31)) {
+            hk = (int)((uint32_t)item / (uint32_t)per_head);
+            const uint32_t x = (uint32_t)item - (uint32_t)hk * (uint32_t)per_head;
+            qt = a.head_tiles == 1 ? (int)x : (int)(x / (uint32_t)a.head_tiles);
+            ht = (int)(x - (uint32_t)qt * (uint32_t)a.head_tiles);
+        } else {
+            hk = (int)(item / per_head);
+            const int64_t x = item - hk * per_head;
+            qt = (int)(x / a.head_tiles);
+            ht = (int)(x - (int64_t)qt * a.head_tiles);
+        }
+    }
 
     DG_DEVINL bool next(const TreeArgs& a, Piece& z) {
         while (at < end) {
-            while (at >= seq_start + p.cost(a)) {   // the next sequence that has work
-                if (s + 1 >= a.n_seq) return false;
-                seq_start += p.cost(a);
-                p = seq_line(a, ++s);
-            }
-            const int64_t off = at - seq_start, item = off / p.len;
-            const int64_t begin = seq_start + item * p.len;
-            const int t0 = (int)(at - begin);
-            const int64_t per_head = (int64_t)p.q_tiles * a.head_tiles;
-            const int hk = (int)(item / per_head);
-            const int64_t x = item - hk * per_head;
-            const int qt = (int)(x / a.head_tiles), ht = (int)(x - (int64_t)qt * a.head_tiles);
-            const Range r = range_of(a, p.seq, qt);
             const int64_t to = whole ? begin + p.len : min(end, begin + p.len);
+            const int t0 = (int)(at - begin);
+            const Range r = range_of(a, p.seq, qt);
+            const bool skip = whole ? t0 != 0 : t0 >= r.nt;
+            if (!skip) {
+                z.s = s;
+                z.hk = hk;
+                z.h0 = hk * a.group + ht * a.hpt;
+                z.nh = min(a.hpt, a.group - ht * a.hpt);
+                z.qi0 = qt * a.qpt;
+                z.qrow = p.seq.q0 + z.qi0;
+                z.nq = min(a.qpt, p.seq.ql - z.qi0);
+                z.ql = p.seq.ql;
+                z.kl = p.seq.kl;
+                z.sink_end = r.sink_end;
+                z.ns = r.ns;
+                z.jlo = r.jlo;
+                z.jhi = r.jhi;
+                z.t0 = t0;
+                z.nt = (int)min((int64_t)r.nt, to - begin) - t0;
+                z.flags = (t0 == 0 ? kStarts : 0u) | (t0 + z.nt == r.nt ? kEnds : 0u);
+                z.last = z.flags == kStarts ? (int)((begin + r.nt - 1) / per_cta) : 0;
+            }
+            begin += p.len;
             at = to;
-            if (whole ? t0 != 0 : t0 >= r.nt) continue;
-            z.s = s;
-            z.hk = hk;
-            z.h0 = hk * a.group + ht * a.hpt;
-            z.nh = min(a.hpt, a.group - ht * a.hpt);
-            z.qi0 = qt * a.qpt;
-            z.qrow = p.seq.q0 + z.qi0;
-            z.nq = min(a.qpt, p.seq.ql - z.qi0);
-            z.ql = p.seq.ql;
-            z.kl = p.seq.kl;
-            z.sink_end = r.sink_end;
-            z.ns = r.ns;
-            z.jlo = r.jlo;
-            z.jhi = r.jhi;
-            z.t0 = t0;
-            z.nt = (int)min((int64_t)r.nt, to - begin) - t0;
-            z.last = (int)((begin + r.nt - 1) / per_cta);
-            z.flags = (t0 == 0 ? kStarts : 0u) | (t0 + z.nt == r.nt ? kEnds : 0u);
-            return true;
+            if (++ht == a.head_tiles) {
+                ht = 0;
+                if (++qt == p.q_tiles) {
+                    qt = 0;
+                    if (++hk == a.Hkv) {
+                        hk = 0;
+                        do {   // the next sequence that has work
+                            if (++s >= a.n_seq) {
+                                at = end;
+                                break;
+                            }
+                            p = seq_line(a, next_raw);
+                            next_raw = raw_seq(a, s + 1);
+                        } while (p.q_tiles == 0);
+                    }
+                }
+            }
+            if (!skip) return true;
         }
         return false;
     }
@@ -353,18 +450,11 @@ DG_DEVINL Piece take(TreeShared& sh, uint32_t k, bool& ok) {
     dg::mbar_arrive(&sh.wempty[slot]);
     return z;
 }
-DG_DEVINL Piece take_warp(TreeShared& sh, uint32_t k, bool& ok) {
-    const int slot = (int)(k % kRing);
-    if (!wait_warp(&sh.wfull[slot], (k / kRing) & 1u)) {
-        ok = false;
-        Piece z;
-        z.nt = 0;
-        return z;
-    }
-    const Piece z = sh.piece[slot];
+// For a whole warp: the piece stays where it is until the warp leaves it.
+DG_DEVINL bool await_piece(TreeShared& sh, uint32_t k) { return wait_warp(&sh.wfull[k % kRing], (k / kRing) & 1u); }
+DG_DEVINL void leave_piece(TreeShared& sh, uint32_t k) {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) dg::mbar_arrive(&sh.wempty[slot]);
-    return z;
+    if ((threadIdx.x & 31) == 0) dg::mbar_arrive(&sh.wempty[k % kRing]);
 }
 
 // Bits below n.
@@ -433,100 +523,124 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
     dg::pdl_wait();
     dg::pdl_release();
-    const Run run = find_run(a, sh);
-    const bool any = run.start < run.end;
+    // With few sequences warp 0 finds the run by itself.
+    const bool few = a.n_seq <= 32 * kFew;
+    Run run;
+    if (!few) run = find_run(a, sh);
     const uint32_t sQ = dg::smem_u32(smem + C::kOffQ);
 
-    if (!any) {
-        // nothing: straight to the end
-    } else if (warp == 0) {
-        if (lane == 2) {
-            // ------------------------------------------------ the walk, and the queries
+    if (warp == 0) {
+        // ------------------------------------------------ the walk and the copies, a whole warp
+        // Tile n's keys, then tile n - 1's values, in the order in which the products free their places; behind a piece's
+        // first keys its queries, whose place the same product frees as that of the second tile's keys.  A lane copies a
+        // box of a page's slots x 64 columns; the lanes hold the page numbers of the tiles to come, and ask for
+        // the next ones (the next piece's first ones too) before they are needed.
+        if (lane == 0) {
             dg::prefetch_tmap(&tmQ);
-            Walk walk{run.start, run.seq_start, run.end, run.per_cta, run.seq, run.whole, seq_line(a, run.seq)};
-            const uint32_t bytes = (uint32_t)(a.hpt * a.qpt) * kSub * 2 * (D / kSub);
-            bool ok = true, more = true;
-            uint32_t k = 0, copies = 0;
-            for (; more; ++k) {
-                const int slot = (int)(k % kRing);
-                Piece z;
-                more = !aborted(sh) && walk.next(a, z);
-                if (!more) z.nt = 0;
-                if (!wait(&sh.wempty[slot], ((k / kRing) & 1u) ^ 1u)) {
-                    ok = false;
-                    break;
-                }
-                sh.piece[slot] = z;
-                dg::mbar_arrive(&sh.wfull[slot]);   // releases the piece to its readers
-                if (!more) break;
-                if (!wait(&sh.qempty, (k & 1u) ^ 1u)) {   // the last piece's last S has read its queries
-                    ok = false;
-                    break;
-                }
-                dg::mbar_arrive_expect_tx(&sh.qfull, bytes);
-#pragma unroll
-                for (int c = 0; c < D / kSub; ++c)
-                    dg::tma_load_3d(smem + C::kOffQ + c * kQSub, &tmQ, c * kSub, z.h0, z.qrow, &sh.qfull);
-                ++copies;
+            dg::prefetch_tmap(&tmK);
+            dg::prefetch_tmap(&tmV);
+        }
+        constexpr int kCols = D / kSub;
+        const int box_shift = min(a.kv.page_shift, 6), size = 1 << box_shift, boxes = kKeys >> box_shift;
+        const int ahead = 32 / boxes;                       // tiles whose pages the warp holds
+        const int my_tile = lane / boxes, my_box = lane - my_tile * boxes;   // as a holder
+        const int box = lane / kCols, col = lane - box * kCols;              // as a copier
+        const uint32_t q_bytes = (uint32_t)(a.hpt * a.qpt) * kSub * 2 * kCols;
+        if (few) run = find_run_warp(a);
+        if (lane == 0) sh.zeros = run.zeros;
+        Walk walk;
+        walk.start(a, run);
+        Piece z, zn;
+        auto entries = [&](const Piece& x, int i) -> int32_t {   // of tiles i .. i + ahead - 1; n_pages reads zeros
+            const int ti = i + my_tile;
+            if (ti >= x.nt) return (int32_t)a.kv.n_pages;
+            const int j = x.tile(ti) * kKeys + (my_box << box_shift);
+            if (j > x.jhi || (j + (size - 1) < x.jlo && j >= x.sink_end)) return (int32_t)a.kv.n_pages;
+            const int32_t page = a.kv.page_table[(int64_t)x.s * a.kv.max_pages + (j >> a.kv.page_shift)];
+            if (page >= 0 && page < a.kv.n_pages) return page;
+            dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+            return (int32_t)a.kv.n_pages;
+        };
+        bool ok = true, more = walk.next(a, zn);
+        int32_t en = more ? entries(zn, 0) : 0;
+        uint32_t n_keys = 0, n_values = 0, n_queries = 0;   // copies asked for
+        int v_page = 0, v_slot = 0, v_hk = 0;               // of the last tile's values
+        auto copy = [&](const CUtensorMap* tm, unsigned char* dst, uint64_t* full, int slot, int hk, int page) {
+            if (lane == 0) dg::mbar_arrive_expect_tx(full, kKVBytes);
+            __syncwarp();
+            if (box < boxes)
+                dg::tma_load_4d(dst + col * kKSub + (box << box_shift) * kSub * 2, tm, col * kSub, slot, hk, page, full);
+        };
+        auto values = [&]() {                               // of the tile before
+            const int st = (int)(n_values & 1u);
+            if (!wait_warp(&sh.vempty[st], ((n_values >> 1) & 1u) ^ 1u)) return false;
+            copy(&tmV, smem + C::kOffV + st * kKVBytes, &sh.vfull[st], v_slot, v_hk, v_page);
+            ++n_values;
+            return true;
+        };
+        for (uint32_t k = 0; ok; ++k) {
+            const int slot = (int)(k % kRing);
+            if (!wait_warp(&sh.wempty[slot], ((k / kRing) & 1u) ^ 1u)) {
+                ok = false;
+                break;
             }
-            if (!ok) do_abort(sh, a.status);
-            if (aborted(sh) && copies > 0) (void)wait(&sh.qfull, (copies - 1u) & 1u);   // the last copy landed
-        } else if (lane < 2) {
-            // ------------------------------------------------ keys (lane 0) and values (lane 1)
-            const bool is_k = lane == 0;
-            const CUtensorMap* tm = is_k ? &tmK : &tmV;
-            uint64_t* full = is_k ? sh.kfull : sh.vfull;
-            uint64_t* empty = is_k ? sh.kempty : sh.vempty;
-            unsigned char* ring = smem + (is_k ? C::kOffK : C::kOffV);
-            dg::prefetch_tmap(tm);
-            const int box_shift = min(a.kv.page_shift, 6), boxes = kKeys >> box_shift, size = 1 << box_shift;
-            uint32_t g = 0;
-            int issued[2] = {0, 0};
-            bool ok = true;
-            for (uint32_t k = 0; ok && !aborted(sh); ++k) {
-                const Piece z = take(sh, k, ok);
-                if (z.nt == 0) break;
-                const int32_t* table = a.kv.page_table + (int64_t)z.s * a.kv.max_pages;
-                for (int i = 0; i < z.nt; ++i, ++g) {
-                    const int st = (int)(g & 1u), j0 = z.tile(i) * kKeys;
-                    // the pages of the tile's boxes, read before the wait; n_pages reads zeros
-                    int32_t entry[8];
-                    bool bad = false;
-#pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        const int j = j0 + (b << box_shift);
-                        entry[b] = (int32_t)a.kv.n_pages;
-                        if (b < boxes && j <= z.jhi && (j + (size - 1) >= z.jlo || j < z.sink_end)) {
-                            entry[b] = table[j >> a.kv.page_shift];
-                            bad = bad || entry[b] < 0 || entry[b] >= a.kv.n_pages;
-                        }
-                    }
-#pragma unroll
-                    for (int b = 0; b < 8; ++b)
-                        sh.pages[lane][b] = entry[b] < 0 || entry[b] >= a.kv.n_pages ? (int32_t)a.kv.n_pages : entry[b];
-                    if (bad) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-                    if (!wait(&empty[st], ((g >> 1) & 1u) ^ 1u)) {
+            z = zn;
+            if (!more || aborted(sh)) z.nt = 0;
+            z.nt = __shfl_sync(0xffffffffu, z.nt, 0);
+            if (lane == 0) {
+                sh.piece[slot] = z;
+                dg::mbar_arrive(&sh.wfull[slot]);           // releases the piece to its readers
+            }
+            if (z.nt == 0) break;
+            int32_t e = en, e_next = entries(z, ahead);
+            int held = 0;                                   // the tile that e's first entries are of
+            for (int i = 0; i < z.nt; ++i) {
+                if (i == held + ahead) {
+                    held = i;
+                    e = e_next;
+                    e_next = entries(z, i + ahead);
+                }
+                const int st = (int)(n_keys & 1u), j0 = z.tile(i) * kKeys;
+                const int page = __shfl_sync(0xffffffffu, e, ((i - held) * boxes + box) & 31);
+                const int at = (j0 + (box << box_shift)) & ((1 << a.kv.page_shift) - 1);
+                if (!wait_warp(&sh.kempty[st], ((n_keys >> 1) & 1u) ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                copy(&tmK, smem + C::kOffK + st * kKVBytes, &sh.kfull[st], at, z.hk, page);
+                ++n_keys;
+                if (n_keys > 1 && !values()) {
+                    ok = false;
+                    break;
+                }
+                v_page = page;
+                v_slot = at;
+                v_hk = z.hk;
+                if (i == 0) {
+                    if (!wait_warp(&sh.qempty, (k & 1u) ^ 1u)) {   // the last piece's last S has read its queries
                         ok = false;
                         break;
                     }
-                    dg::mbar_arrive_expect_tx(&full[st], kKVBytes);
-                    unsigned char* dst = ring + st * kKVBytes;
-#pragma unroll 1
-                    for (int b = 0; b < boxes; ++b) {
-                        const int row = b << box_shift, page = sh.pages[lane][b];
-                        const int slot = (j0 + row) & ((1 << a.kv.page_shift) - 1);
-#pragma unroll
-                        for (int c = 0; c < D / kSub; ++c)
-                            dg::tma_load_4d(dst + c * kKSub + row * kSub * 2, tm, c * kSub, slot, z.hk, page, &full[st]);
-                    }
-                    ++issued[st];
+                    if (lane == 0) dg::mbar_arrive_expect_tx(&sh.qfull, q_bytes);
+                    __syncwarp();
+                    if (lane < kCols)
+                        dg::tma_load_3d(smem + C::kOffQ + lane * kQSub, &tmQ, lane * kSub, z.h0, z.qrow, &sh.qfull);
+                    ++n_queries;
+                }
+                if (i == min(1, z.nt - 1)) {   // the next piece, and its first pages, behind copies on their way
+                    more = walk.next(a, zn);
+                    en = more ? entries(zn, 0) : 0;
                 }
             }
-            if (!ok) do_abort(sh, a.status);
-            if (aborted(sh)) {   // never leave with a copy still landing in shared memory
-                for (int st = 0; st < 2; ++st)
-                    if (issued[st] > 0) (void)wait(&full[st], (uint32_t)(issued[st] - 1) & 1u);
+        }
+        if (ok && n_keys > 0) ok = values();
+        if (!ok && lane == 0) do_abort(sh, a.status);
+        if (__any_sync(0xffffffffu, !ok || aborted(sh))) {   // never leave with a copy still landing in shared memory
+            for (uint32_t b = 1; b <= 2; ++b) {
+                if (n_keys >= b) (void)wait_warp(&sh.kfull[(n_keys - b) & 1u], ((n_keys - b) >> 1) & 1u);
+                if (n_values >= b) (void)wait_warp(&sh.vfull[(n_values - b) & 1u], ((n_values - b) >> 1) & 1u);
             }
+            if (n_queries > 0) (void)wait_warp(&sh.qfull, (n_queries - 1u) & 1u);
         }
     } else if (warp == 1) {
         // ------------------------------------------------ the products
@@ -604,8 +718,13 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             return wait_warp(&sh.met, meetings++ & 1u);
         };
         for (uint32_t k = 0; ok; ++k) {
-            const Piece z = take_warp(sh, k, ok);
-            if (z.nt == 0) break;
+            if (!await_piece(sh, k)) {
+                ok = false;
+                break;
+            }
+            const Piece& z = sh.piece[k % kRing];   // (read again where it is needed: kept in registers it spills them)
+            const int nt = z.nt;
+            if (nt == 0) break;
             const int ctx = z.kl - z.ql;
             const int qi = row / a.hpt, hi = row - qi * a.hpt;
             const bool valid = qi < z.nq && hi < z.nh;
@@ -626,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             const int all_hi = a.mask ? ctx - 1 : ctx + z.qi0;   // every row sees keys up to it,
             const int64_t all_lo = a.window < 0 ? 0 : (int64_t)top - a.window;   // from here on
             float m_ref = -INFINITY, l = 0.f;
-            for (int i = 0; i < z.nt; ++i) {
+            for (int i = 0; i < nt; ++i) {
                 const uint32_t gi = g + (uint32_t)i;
                 if (!wait_warp(&sh.sfull, gi & 1u)) {
                     ok = false;
@@ -708,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                         const float alpha = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);
                         l *= alpha;
                         if (i > 0) {
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 float o[32];
                                 const uint32_t ta = tmem + lane_base + kColO + (uint32_t)(c * 32);
@@ -747,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                 if (lane == 0) dg::mbar_arrive(&sh.pfull[gi & 1u]);
             }
             if (!ok) break;
-            const uint32_t gl = g + (uint32_t)z.nt - 1u;   // the piece's last P V
+            const uint32_t gl = g + (uint32_t)nt - 1u;   // the piece's last P V
             if (!wait_warp(&sh.pvdone[gl & 1u], (gl >> 1) & 1u)) {
                 ok = false;
                 break;
@@ -758,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 const int64_t out = qrow * a.Hq + z.h0 + (valid ? hi : 0);
                 const int64_t slot = (int64_t)blockIdx.x * 2 + (z.flags & kStarts ? 1 : 0);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
                     dg::tmem_ld32(tmem + lane_base + kColO + (uint32_t)(c * 32), o);
@@ -790,13 +909,20 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             dg::tc_fence_before();
             __syncwarp();
             if (lane == 0) dg::mbar_arrive(&sh.oempty);   // O read out: the next piece may overwrite it
-            g += (uint32_t)z.nt;
+            leave_piece(sh, k);
+            g += (uint32_t)nt;
         }
         if (!ok) do_abort(sh, a.status);
         if (row == 0 && !to_join) a.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     }
-    if (!any && threadIdx.x == 0) a.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
 
+    dg::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        dg::tc_fence_after();
+        dg::tmem_dealloc(tmem, kTmemCols);
+    }
+    if (!sh.zeros) return;
     // the sequences without keys: their rows of zeros
     for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x) {
         const dg::PagedSeq p = dg::paged_seq(a.kv, a.cu_q, a.total_q, s, dg::kMaxKeys);
@@ -806,13 +932,6 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             reinterpret_cast<uint4*>(a.o + first * D)[i] = make_uint4(0u, 0u, 0u, 0u);
         if (a.lse)
             for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse[first + i] = -INFINITY;
-    }
-
-    dg::tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        dg::tc_fence_after();
-        dg::tmem_dealloc(tmem, kTmemCols);
     }
 }
 
