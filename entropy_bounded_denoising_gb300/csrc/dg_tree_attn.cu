@@ -26,7 +26,7 @@
 #include <limits>
 #include <utility>
 
-#include "dg_paged.cuh"
+#include "dg_tree.cuh"
 
 namespace {
 
@@ -992,17 +992,45 @@ size_t piece_bytes(int32_t D, int rows) {
     return ctas * 32 + ctas * 2 * rows * ((size_t)D * 4 + 8);
 }
 
+// Whether a call takes the kernels for few rows (dg_tree_split.cu).
+bool few_rows(int32_t max_q_len, int32_t group) { return (int64_t)max_q_len * group <= 16; }
+
 template <int D>
-dg_status launch_tree(TreeArgs& a, const uint16_t* q, void* workspace, cudaStream_t stream) {
+dg_status launch_tree(const dghost::TreeCall& c, void* workspace, cudaStream_t stream) {
     using C = TreeCfg<D>;
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
+    TreeArgs a;
+    a.o = c.o;
+    a.lse = c.lse;
+    a.cu_q = c.cu_q;
+    a.mask = c.mask;
+    a.positions = c.positions;
+    a.total_q = c.total_q;
+    a.n_seq = c.n_seq;
+    a.max_q_len = c.max_q_len;
+    a.Hq = c.Hq;
+    a.Hkv = c.Hkv;
+    a.group = c.Hq / c.Hkv;
+    a.mask_words = c.mask_words;
+    a.window = c.window;
+    a.sinks = c.sinks;
+    a.hpt = std::min(a.group, kTile);
+    a.qpt = kTile / a.hpt;
+    a.head_tiles = (a.group + kTile - 1) / kTile;
+    a.rows = piece_rows(c.max_q_len, a.group);
+    // a scale of 0 weighs every key alike: the smallest float keeps masked scores (-inf) what they are and moves
+    // no finite score by more than 5e-7
+    a.scale_log2 = std::max(fabsf(c.scale) * kLog2e, std::numeric_limits<float>::denorm_min());
+    a.negate = c.scale < 0.f;
+    a.kv = c.kv;
+    a.status = dghost::status_word();
     CUtensorMap tq, tk, tv;
     {   // queries: 64 columns x the item's heads x its queries
         const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.total_q};
         const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)a.Hq * D * 2};
         const uint32_t box[3] = {(uint32_t)kSub, (uint32_t)a.hpt, (uint32_t)a.qpt};
-        if (!dghost::encode_tmap(&tq, 0, 3, const_cast<uint16_t*>(q), dims, strides, box, 128)) return DG_ERR_CUDA;
+        if (!dghost::encode_tmap(&tq, 0, 3, const_cast<uint16_t*>(c.q), dims, strides, box, 128)) return DG_ERR_CUDA;
     }
     for (auto [tm, base] : {std::pair<CUtensorMap*, uint16_t*>{&tk, a.kv.k}, {&tv, a.kv.v}}) {
         // a page: 64 columns of a head, up to 64 of its slots
@@ -1049,45 +1077,39 @@ dg_status tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* 
     if (!aligned16(q) || !aligned16(o) || !dghost::on_multiple(cu_q, 4) || !dghost::on_multiple(lse, 4) ||
         !dghost::on_multiple(mask, 4) || !dghost::on_multiple(positions, 4))
         return DG_ERR_ALIGNMENT;
-    TreeArgs a;
-    const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
+    dghost::TreeCall c;
+    const dg_status ok = dghost::paged_kv(cache, D, &c.kv);
     if (ok != DG_OK) return ok;
     if (!workspace || workspace_bytes < dg_tree_attention_workspace_bytes(n_seq, max_q_len, Hq, Hkv, D))
         return DG_ERR_WORKSPACE;
     if (!aligned16(workspace)) return DG_ERR_ALIGNMENT;
-    a.o = o;
-    a.lse = lse;
-    a.cu_q = cu_q;
-    a.mask = mask;
-    a.positions = positions;
-    a.total_q = total_q;
-    a.n_seq = n_seq;
-    a.max_q_len = max_q_len;
-    a.Hq = Hq;
-    a.Hkv = Hkv;
-    a.mask_words = mask_words;
-    a.window = window;
-    a.sinks = window < 0 ? 0 : sinks;
-    a.group = Hq / Hkv;
-    a.hpt = std::min(a.group, kTile);
-    a.qpt = kTile / a.hpt;
-    a.head_tiles = (a.group + kTile - 1) / kTile;
-    a.rows = piece_rows(max_q_len, a.group);
-    // a scale of 0 weighs every key alike: the smallest float keeps masked scores (-inf) what they are and moves
-    // no finite score by more than 5e-7
-    a.scale_log2 = std::max(fabsf(scale) * kLog2e, std::numeric_limits<float>::denorm_min());
-    a.negate = scale < 0.f;
-    a.status = dghost::status_word();
+    c.q = q;
+    c.o = o;
+    c.lse = lse;
+    c.cu_q = cu_q;
+    c.mask = mask;
+    c.positions = positions;
+    c.total_q = total_q;
+    c.n_seq = n_seq;
+    c.max_q_len = max_q_len;
+    c.Hq = Hq;
+    c.Hkv = Hkv;
+    c.mask_words = mask_words;
+    c.window = window;
+    c.sinks = window < 0 ? 0 : sinks;
+    c.scale = scale;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (D == 64) return launch_tree<64>(a, q, workspace, st);
-    return D == 128 ? launch_tree<128>(a, q, workspace, st) : launch_tree<256>(a, q, workspace, st);
+    if (few_rows(max_q_len, Hq / Hkv)) return dghost::tree_split(c, D, workspace, st);
+    if (D == 64) return launch_tree<64>(c, workspace, st);
+    return D == 128 ? launch_tree<128>(c, workspace, st) : launch_tree<256>(c, workspace, st);
 }
 
 }  // namespace
 
 extern "C" size_t dg_tree_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D) {
     if (n_seq < 1 || max_q_len < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
-    return piece_bytes(D, piece_rows(max_q_len, Hq / Hkv));
+    // what either path needs, so that a workspace for a program's largest call serves its smaller ones
+    return std::max(piece_bytes(D, piece_rows(max_q_len, Hq / Hkv)), dghost::tree_split_bytes(max_q_len, Hq / Hkv, D));
 }
 
 extern "C" dg_status dg_tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
