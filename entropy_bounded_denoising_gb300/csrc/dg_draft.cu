@@ -6,6 +6,8 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "dg_paged.cuh"
 
@@ -13,40 +15,54 @@ namespace cg = cooperative_groups;
 
 namespace {
 
+// Arrives on a barrier of another CTA of the cluster (or this one), after what this thread has written there.
+DG_DEVINL void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ------------------------------------------------------------------ verification
 // A cluster of CTAs owns a sequence and walks its tree, so that only the rows on the walk are read: all of a
-// cluster's threads take the statistics of one row, its first CTA decides which child goes on and tells the
-// others.  The token after the path is drawn by inversion: the weights of the last row, as 64-bit fixed point, are
-// summed by warps (each of which owns a contiguous part of the row), the first CTA finds the CTA in whose part the
-// threshold falls, and there a warp walks its part again.
+// cluster's threads take the statistics of one row, its first CTA (the lead) decides which child goes on and tells the
+// others.  CTAs leave their parts in the lead's shared memory and arrive on its barrier, the lead leaves its command in
+// theirs: bounded waits between two CTAs, not barriers of all threads.  The token after the path is drawn by inversion:
+// the weights of the last row, as 64-bit fixed point, are summed by warps (each of which owns a contiguous part of the
+// row), the lead finds the CTA in whose part the threshold falls, and there the warps halve the part of the owner
+// between them until one vector is left.
 //
 // Precision.  A token is drawn wrongly when an error of the cumulated probability moves a token's border past
 // the random number: with errors e, about e times the number of tokens.  Weights in plain fp32 (2^-25 each) would
-// miss one draw in a thousand on 262144 tokens; here a weight is 2^(j / 64) from a table of 62 bits times 2^g, |g| <= 1/128,
-// by its Taylor polynomial, within 2^-31 of the exact one, and the sums are exact, whatever their order.
-// Acceptance compares with fp32 sums, unless they come within their own bound of the border: then the row
-// is summed like the last one (`kSum`) and compared again.
-constexpr int kVThreads = 512, kVWarps = kVThreads / 32;
+// miss one draw in a thousand on 262144 tokens; here a weight is 2^(j / 32) from a table times 2^g, |g| <= 1/64, by its
+// Taylor polynomial, in two floats within 2^-31 of the exact one (2^-32 as a rule).  The two are added up over a vector
+// of 16 bytes so that nothing is lost (multiples of 2^-20 exactly, what is left within 2^-43), turned into fixed point, and
+// added exactly from there on, whatever the order.
+// Acceptance compares fp32 sums, unless they come within their own bound of the border: then the row is summed
+// like the last one (kSum) and compared again.
+constexpr int kVThreads = 256, kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxNodes = 1024;
+constexpr int kSegments = 64;      // that a part is searched in at a time
 
-// 2^(j / 64) 2^62, rounded.
-__constant__ uint64_t kPow[64] = {
-    0x4000000000000000ull, 0x40b268f9de0183baull, 0x4166c34c5615d0ecull, 0x421d1461d66f2023ull, 0x42d561b3e6243d8aull,
-    0x438fb0cb4f468808ull, 0x444c0740496d4294ull, 0x450a6abaa4b77ecdull, 0x45cae0f1f545eb73ull, 0x468d6fadbf2dd4f3ull,
-    0x47521cc5a2e6a9e0ull, 0x4818ee218a3358eeull, 0x48e1e9b9d588e19bull, 0x49ad159789f37496ull, 0x4a7a77d47f7b84b1ull,
-    0x4b4a169b900c2d00ull, 0x4c1bf828c6dc54b8ull, 0x4cf022c9905bfd32ull, 0x4dc69cdceaa72a9cull, 0x4e9f6cd3967fdba8ull,
-    0x4f7a993048d088d7ull, 0x50582887dcb8a7e1ull, 0x513821818624b40cull, 0x521a8ad704f3404full, 0x52ff6b54d8a89c75ull,
-    0x53e6c9da74b29ab5ull, 0x54d0ad5a753e077cull, 0x55bd1cdad49f699cull, 0x56ac1f752150a563ull, 0x579dbc56b48521baull,
-    0x5891fac0e95612c8ull, 0x5988e20954889245ull, 0x5a827999fcef3242ull, 0x5b7ec8f19468bbc9ull, 0x5c7dd7a3b17dcf75ull,
-    0x5d7fad59099f22feull, 0x5e8451cfac061b5full, 0x5f8bccdb3d398841ull, 0x6096266533384a2bull, 0x61a3666d124bb204ull,
-    0x62b39508aa836d6full, 0x63c6ba6455dcd8aeull, 0x64dcdec3371793d1ull, 0x65f60a7f79393e2eull, 0x6712460a8fc24072ull,
-    0x683199ed779592caull, 0x69540ec8f895722dull, 0x6a79ad55e7f6fd10ull, 0x6ba27e656b4eb57aull, 0x6cce8ae13c57ebdbull,
-    0x6dfddbcbed791babull, 0x6f307a412f074892ull, 0x70666f76154a7089ull, 0x719fc4b95f452d29ull, 0x72dc8373be41a454ull,
-    0x741cb5281e25ee34ull, 0x75606373ee921c97ull, 0x76a7980f6cca15c2ull, 0x77f25ccdee6d7ae6ull, 0x7940bb9e2cffd89dull,
-    0x7a92be8a92436616ull, 0x7be86fb985689ddcull, 0x7d41d96db915019dull, 0x7e9f06067a4360baull};
+// 2^(j / 32), rounded, and what the rounding left out, relative.
+__constant__ float kPow[32] = {
+    0x1.0000000000000p+0f, 0x1.059b0e0000000p+0f, 0x1.0b55860000000p+0f, 0x1.11301e0000000p+0f,
+    0x1.172b840000000p+0f, 0x1.1d48740000000p+0f, 0x1.2387a60000000p+0f, 0x1.29e9e00000000p+0f,
+    0x1.306fe00000000p+0f, 0x1.371a740000000p+0f, 0x1.3dea640000000p+0f, 0x1.44e0860000000p+0f,
+    0x1.4bfdae0000000p+0f, 0x1.5342b60000000p+0f, 0x1.5ab07e0000000p+0f, 0x1.6247ec0000000p+0f,
+    0x1.6a09e60000000p+0f, 0x1.71f75e0000000p+0f, 0x1.7a11480000000p+0f, 0x1.82589a0000000p+0f,
+    0x1.8ace540000000p+0f, 0x1.93737c0000000p+0f, 0x1.9c49180000000p+0f, 0x1.a5503c0000000p+0f,
+    0x1.ae89fa0000000p+0f, 0x1.b7f7700000000p+0f, 0x1.c199be0000000p+0f, 0x1.cb720e0000000p+0f,
+    0x1.d5818e0000000p+0f, 0x1.dfc9740000000p+0f, 0x1.ea4afa0000000p+0f, 0x1.f507660000000p+0f};
+__constant__ float kPowRest[32] = {
+    0x0.0p+0f, -0x1.9474140000000p-25f, 0x1.8d96d40000000p-25f, -0x1.dda2fc0000000p-25f,
+    -0x1.9c0c220000000p-27f, -0x1.a2fbb20000000p-25f, 0x1.9649040000000p-25f, -0x1.2b0dbc0000000p-25f,
+    0x1.1250020000000p-25f, -0x1.cde8ce0000000p-26f, 0x1.370be40000000p-25f, 0x1.336de20000000p-30f,
+    -0x1.0a35500000000p-25f, -0x1.c541b40000000p-26f, -0x1.00d8ac0000000p-27f, -0x1.6cb2840000000p-25f,
+    0x1.26055c0000000p-26f, 0x1.8b2bb80000000p-26f, -0x1.05cb440000000p-25f, -0x1.1c21420000000p-26f,
+    0x1.67a1ca0000000p-28f, -0x1.348e560000000p-25f, 0x1.a3b5e40000000p-28f, -0x1.0b7ec80000000p-25f,
+    -0x1.f9c3040000000p-27f, -0x1.e4c8860000000p-26f, -0x1.6961b40000000p-28f, -0x1.b5151e0000000p-28f,
+    -0x1.a5217c0000000p-28f, -0x1.ab71320000000p-26f, 0x1.61428e0000000p-28f, -0x1.2ad5f80000000p-27f};
 
 struct VerifyArgs {
     const void* logits;
@@ -63,7 +79,7 @@ struct VerifyArgs {
 
 enum : int { kStats, kSum, kLeft, kFind, kExit };
 
-// What the first CTA tells the others to do with a row.
+// What the lead tells the others to do with a row.
 struct Command {
     int op;
     int node;          // row of the sequence
@@ -71,12 +87,12 @@ struct Command {
     int draft;         // kLeft, and kFind after it: the rejected draft (else -1)
     int cta;           // kFind: the CTA that finds the token,
     float top;         // the row's maximum
-    uint64_t total;    // kLeft: the row's sum
+    float w_hi, w_lo;  // kLeft: the row's sum, in units of the largest weight
     uint64_t target;   // kFind: the sum to pass, counted from that CTA's part
     int64_t out;       // and the place of the token
 };
 
-struct Partial {       // of one CTA: kStats: maximum, sum, its place, 0 / 1: a NaN or +inf; kSum, kLeft: sum
+struct Partial {       // of one CTA: kStats: maximum, sum, its place, a NaN or +inf; kSum, kLeft: sum
     float top, sum;
     int arg, bad;
     uint64_t fixed;
@@ -84,16 +100,21 @@ struct Partial {       // of one CTA: kStats: maximum, sum, its place, 0 / 1: a 
 
 struct __align__(16) VShared {
     Command cmd;
-    Partial part[kMaxCluster];        // in the first CTA: everyone's
+    Partial part[kMaxCluster];        // in the lead: everyone's
+    uint64_t told, parts;             // barriers: a command is here; (the lead's) every part is
     uint64_t warp_sum[kVWarps];       // fixed-point sums of the warps' parts
+    uint64_t segment[kSegments];
     float w_top[kVWarps], w_sum[kVWarps];
     int w_arg[kVWarps], w_bad[kVWarps];
-    float c_hi, c_lo;                 // log2(e) / temperature
+    float pow[32], rest[32];
+    float c_hi, c_lo, d_min;          // log2(e) / temperature, and the difference whose weight is 2^-120
     int n_gone;                       // rejected tokens of the last node that lie in this CTA's part
+    int child, last;                  // what the lead's first warp decided
     int gone[kMaxNodes];
-    int path[kMaxNodes];              // the first CTA's
+    int path[kMaxNodes];              // the lead's, as the rest:
     int rejected[kMaxNodes];
-    uint64_t pow[64];
+    int token[kMaxNodes], parent[kMaxNodes];
+    float uniform[kMaxNodes];
 };
 
 template <typename T>
@@ -119,6 +140,13 @@ DG_DEVINL void unpack(const uint4& r, int64_t v, int64_t V, float (&x)[Vec<T>::k
             if (v * N + e >= V) x[e] = -INFINITY;
     }
 }
+template <typename T>
+DG_DEVINL float logit(const T* row, int64_t t) {
+    if constexpr (sizeof(T) == 2)
+        return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[t] << 16);
+    else
+        return reinterpret_cast<const float*>(row)[t];
+}
 
 DG_DEVINL float ex2(float x) {
     float y;
@@ -126,60 +154,131 @@ DG_DEVINL float ex2(float x) {
     return y;
 }
 
-// 2^((x - top) c) as mantissa m in [2^62, 2^63) (a little above at most) and exponent n <= 0: m 2^(n - 62).  The exponent
-// in two floats: the difference (its own rounding kept where both are fp32), its product with c; then 2^(j / 64)
-// 2^g with the polynomial's terms up to g^4 (the next is below 2^-44).
-template <typename T>
-DG_DEVINL uint64_t weight(float x, float top, float c_hi, float c_lo, const uint64_t* pow, int& n) {
-    const float d = x - top;
-    float hi = d * c_hi;
-    float lo = fmaf(d, c_hi, -hi);
-    lo = fmaf(d, c_lo, lo);
-    if constexpr (sizeof(T) == 4) {   // and what x - top lost
-        const float z = d - x;
-        lo = fmaf((x - (d - z)) - (top + z), c_hi, lo);
-    }
-    if (!(hi > -200.f)) {             // nothing at any place after the point (and no index out of the table)
-        n = -200;
-        return 1ull << 62;
-    }
-    const float t = fmaf(hi, 64.f, 12582912.f);   // 1.5 2^23: rounds to a whole number
-    const int k = __float_as_int(t) - 0x4b400000;
-    float g = fmaf(t - 12582912.f, -0.015625f, hi);
-    g += lo;
-    const float e = g * fmaf(g, fmaf(g, fmaf(g, 9.6181291e-3f, 5.5504109e-2f), 0.24022651f), 0.69314718f);
-    const uint64_t h = pow[k & 63];
-    const float hf = (float)(uint32_t)(h >> 32);  // in units of 2^-30
-    const int s = __float2int_rn(hf * e * 128.f); // |e| < 2^-7: units of 2^-37, below 2^31
-    n = k >> 6;
-    return h + ((uint64_t)(int64_t)s << 25);
+// Two floats at a time (one rounding each, as the scalar forms).
+DG_DEVINL uint64_t f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
+DG_DEVINL void f2_split(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+DG_DEVINL uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+DG_DEVINL uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+DG_DEVINL uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+DG_DEVINL uint64_t f2_sub(uint64_t a, uint64_t b) { return f2_fma(b, f2(-1.f, -1.f), a); }
 
-// The same with `frac` bits after the point, rounded.
+// 2^((x - top) c) of two logits, each as hi + lo.  The exponent in two floats: the difference (with what its rounding left
+// out where logits are fp32; of bf16 logits it is exact unless one is 2^16 times the other), its product with c.  Then
+// 2^(j / 32) 2^g with the terms up to g^4 (the next is below 2^-39).  Differences below d_min, -inf and NaN among
+// them, weigh 2^-120: nothing at any place after the point.
 template <typename T>
-DG_DEVINL uint64_t fixed_weight(float x, float top, float c_hi, float c_lo, const uint64_t* pow, int frac) {
-    int n;
-    const uint64_t m = weight<T>(x, top, c_hi, c_lo, pow, n);
-    const int s = 62 - frac - n;      // >= 18
-    return s > 63 ? 0ull : (m + (1ull << (s - 1))) >> s;
+DG_DEVINL void weights2(const VShared& sh, float x0, float x1, float top, uint64_t& hi, uint64_t& lo) {
+    const uint64_t x = f2(x0, x1), nt = f2(-top, -top);
+    uint64_t d = f2_add(x, nt), left = 0;
+    if constexpr (sizeof(T) == 4) {
+        const uint64_t z = f2_sub(d, x);
+        left = f2_add(f2_sub(x, f2_sub(d, z)), f2_sub(nt, z));
+    }
+    float d0, d1;
+    f2_split(d, d0, d1);
+    const bool low0 = !(d0 > sh.d_min), low1 = !(d1 > sh.d_min);
+    d = f2(low0 ? sh.d_min : d0, low1 ? sh.d_min : d1);
+    const uint64_t c = f2(sh.c_hi, sh.c_hi), cl = f2(sh.c_lo, sh.c_lo);
+    const uint64_t p = f2_mul(d, c);
+    uint64_t q = f2_fma(d, c, f2_mul(p, f2(-1.f, -1.f)));
+    q = f2_fma(d, cl, q);
+    if constexpr (sizeof(T) == 4) {
+        float l0, l1;
+        f2_split(left, l0, l1);
+        q = f2_fma(f2(low0 ? 0.f : l0, low1 ? 0.f : l1), c, q);
+    }
+    const uint64_t magic = f2(12582912.f, 12582912.f);       // 1.5 2^23: rounds to a whole number
+    const uint64_t t = f2_fma(p, f2(32.f, 32.f), magic);
+    uint64_t g = f2_fma(f2_sub(t, magic), f2(-0.03125f, -0.03125f), p);
+    g = f2_add(g, q);
+    uint64_t e = f2_fma(g, f2(9.6181291e-3f, 9.6181291e-3f), f2(5.5504109e-2f, 5.5504109e-2f));
+    e = f2_fma(g, e, f2(0.24022651f, 0.24022651f));
+    e = f2_fma(g, e, f2(0.69314718f, 0.69314718f));
+    float t0, t1;
+    f2_split(t, t0, t1);
+    const int k0 = __float_as_int(t0), k1 = __float_as_int(t1);   // (whole number in the low bits, the rest of the magic above)
+    const int j0 = k0 & 31, j1 = k1 & 31;
+    e = f2_fma(g, e, f2(sh.rest[j0], sh.rest[j1]));
+    const uint64_t w = f2(__int_as_float(__float_as_int(sh.pow[j0]) + ((k0 << 18) & 0xff800000)),
+                          __int_as_float(__float_as_int(sh.pow[j1]) + ((k1 << 18) & 0xff800000)));
+    hi = f2_fma(w, e, w);
+    lo = f2_fma(w, e, f2_sub(w, hi));
 }
 
 DG_DEVINL float unit(float q) { return fminf(fmaxf(q, 0.f), 1.f); }   // (a NaN is 0)
 
-// w - q total, or 0: q in [0, 1] a float, so the product is a 24-bit number times the total, shifted.
-DG_DEVINL uint64_t left_of(uint64_t w, float q, uint64_t total) {
-    q = unit(q);
-    const uint32_t b = __float_as_uint(q), e = b >> 23;
-    if (e >= 127) return 0;           // 1: more than any weight
-    const uint64_t m = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
-    const int s = 150 - (e ? (int)e : 1);   // 24 .. 149
-    const uint64_t lo = m * total, hi = __umul64hi(m, total);
-    uint64_t p;
-    if (s < 64)
-        p = (lo >> s) | (hi << (64 - s));
-    else
-        p = s < 128 ? hi >> (s - 64) : 0;
-    return w > p ? w - p : 0;
+// The sum of a vector's weights in fixed point; with q_row of what q times the row's sum leaves of them.  Elements whose
+// bit of `out` is set are left out.
+template <typename T>
+DG_DEVINL uint64_t vector_sum(const VShared& sh, const VerifyArgs& a, const Command& c, const uint4& r, int64_t v,
+                              const float* q_row, uint32_t out) {
+    constexpr int N = Vec<T>::kN;
+    float x[N];
+    unpack<T>(r, v, a.V, x);
+    float q[N];
+    if (q_row) {
+#pragma unroll
+        for (int h = 0; h < N / 4; ++h) {   // (four that begin before V end within the row)
+            const float4 f = v * N + 4 * h < a.V ? __ldg(reinterpret_cast<const float4*>(q_row + v * N) + h) : make_float4(1.f, 1.f, 1.f, 1.f);
+            q[4 * h] = unit(f.x);
+            q[4 * h + 1] = unit(f.y);
+            q[4 * h + 2] = unit(f.z);
+            q[4 * h + 3] = unit(f.w);
+        }
+    }
+    const uint64_t grid = f2(12.f, 12.f);       // 1.5 2^3: rounds to multiples of 2^-20
+    uint64_t coarse = 0, fine = 0;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        uint64_t hi, lo;
+        weights2<T>(sh, x[e], x[e + 1], c.top, hi, lo);
+        if (q_row) {                            // hi + lo - q (w_hi + w_lo), or 0
+            const uint64_t qq = f2(q[e], q[e + 1]), wh = f2(c.w_hi, c.w_hi);
+            const uint64_t p = f2_mul(qq, wh);
+            const uint64_t pl = f2_fma(qq, f2(c.w_lo, c.w_lo), f2_fma(qq, wh, f2_mul(p, f2(-1.f, -1.f))));
+            const uint64_t d = f2_sub(hi, p), z = f2_sub(d, hi);
+            const uint64_t err = f2_sub(f2_sub(hi, f2_sub(d, z)), f2_add(p, z));
+            const uint64_t l = f2_add(err, f2_sub(lo, pl));
+            const uint64_t h = f2_add(d, l);
+            lo = f2_add(f2_sub(d, h), l);
+            float h0, h1, l0, l1;
+            f2_split(h, h0, h1);
+            f2_split(lo, l0, l1);
+            hi = f2(h0 > 0.f ? h0 : 0.f, h1 > 0.f ? h1 : 0.f);
+            lo = f2(h0 > 0.f ? l0 : 0.f, h1 > 0.f ? l1 : 0.f);
+        }
+        if (out >> e & 3u) {
+            float h0, h1, l0, l1;
+            f2_split(hi, h0, h1);
+            f2_split(lo, l0, l1);
+            hi = f2(out >> e & 1u ? 0.f : h0, out >> e & 2u ? 0.f : h1);
+            lo = f2(out >> e & 1u ? 0.f : l0, out >> e & 2u ? 0.f : l1);
+        }
+        const uint64_t m = f2_sub(f2_add(hi, grid), grid);
+        coarse = f2_add(coarse, m);
+        fine = f2_add(f2_add(fine, f2_sub(hi, m)), lo);
+    }
+    float c0, c1, g0, g1;
+    f2_split(coarse, c0, c1);
+    f2_split(fine, g0, g1);
+    const int64_t whole = __float2int_rn((c0 + c1) * 1048576.f);
+    return (uint64_t)((whole << (a.frac - 20)) + __float2int_rn((g0 + g1) * __int_as_float((a.frac + 127) << 23)));
 }
 
 DG_DEVINL uint64_t warp_add(uint64_t v) {
@@ -188,28 +287,25 @@ DG_DEVINL uint64_t warp_add(uint64_t v) {
     return v;
 }
 
-// The part of a row that a warp of the cluster owns, in vectors.
+// The part of a row that a warp of the cluster owns, in vectors, a multiple of 32 except at the row's end.
+template <typename T>
+DG_DEVINL int64_t part_size(int64_t V, int n_cta) {
+    const int64_t nv = (V + Vec<T>::kN - 1) / Vec<T>::kN;
+    return (nv + (int64_t)n_cta * kVThreads - 1) / ((int64_t)n_cta * kVThreads) * 32;
+}
 struct Part {
     int64_t from, to;
 };
 template <typename T>
 DG_DEVINL Part part_of(int64_t V, int cta, int n_cta, int warp) {
-    const int64_t nv = (V + Vec<T>::kN - 1) / Vec<T>::kN;
-    const int64_t each = (nv + (int64_t)n_cta * kVWarps * 32 - 1) / ((int64_t)n_cta * kVWarps * 32) * 32;
+    const int64_t nv = (V + Vec<T>::kN - 1) / Vec<T>::kN, each = part_size<T>(V, n_cta);
     const int64_t from = ((int64_t)cta * kVWarps + warp) * each;
     return Part{min(from, nv), min(from + each, nv)};
 }
-// and who owns a token.
-template <typename T>
-DG_DEVINL int part_with(int64_t V, int n_cta, int64_t token) {
-    const int64_t nv = (V + Vec<T>::kN - 1) / Vec<T>::kN;
-    const int64_t each = (nv + (int64_t)n_cta * kVWarps * 32 - 1) / ((int64_t)n_cta * kVWarps * 32) * 32;
-    return (int)(token / Vec<T>::kN / each);
-}
 
-// A row's maximum, its smallest place, and (with Sum) sum of 2^((x - maximum) c), of this CTA's part.
+// A row's maximum, its smallest place (without Sum), and with Sum the sum of 2^((x - maximum) c), of this CTA's part.
 template <typename T, bool Sum>
-DG_DEVINL void row_stats(VShared& sh, const T* row, int64_t V, int cta, int n_cta, Partial* to) {
+DG_DEVINL Partial row_stats(VShared& sh, const T* row, int64_t V, int cta, int n_cta) {
     constexpr int N = Vec<T>::kN, kDeep = 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Part p = part_of<T>(V, cta, n_cta, warp);
@@ -274,199 +370,201 @@ DG_DEVINL void row_stats(VShared& sh, const T* row, int64_t V, int cta, int n_ct
         sh.w_bad[warp] = bad;
     }
     __syncthreads();
+    Partial q{-INFINITY, 0.f, 0x7fffffff, 0, 0};
     if (tid == 0) {
-        Partial q{-INFINITY, 0.f, 0x7fffffff, 0, 0};
         for (int w = 0; w < kVWarps; ++w) q.top = fmaxf(q.top, sh.w_top[w]);
         const float at = q.top == -INFINITY ? 0.f : q.top;
         for (int w = 0; w < kVWarps; ++w) {
-            q.sum += sh.w_sum[w] * ex2((sh.w_top[w] - at) * c);
+            if constexpr (Sum) q.sum += sh.w_sum[w] * ex2((sh.w_top[w] - at) * c);
             if (sh.w_top[w] == q.top) q.arg = min(q.arg, sh.w_arg[w]);
             q.bad |= sh.w_bad[w];
         }
-        *to = q;
     }
+    return q;
 }
 
-// The fixed-point weights of a vector.
+// The elements of vector v that are left out.
 template <typename T>
-DG_DEVINL void vector_weights(const VShared& sh, const uint4& r, int64_t v, int64_t V, float top, int frac,
-                              const float* q_row, uint64_t total, uint64_t (&w)[Vec<T>::kN]) {
-    constexpr int N = Vec<T>::kN;
-    float x[N];
-    unpack<T>(r, v, V, x);
-#pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = fixed_weight<T>(x[e], top, sh.c_hi, sh.c_lo, sh.pow, frac);
-    if (q_row) {   // (four probabilities that begin before V end within the row; weights from V on are 0)
-#pragma unroll
-        for (int h = 0; h < N / 4; ++h) {
-            if (v * N + 4 * h >= V) continue;
-            const float4 q = __ldg(reinterpret_cast<const float4*>(q_row + v * N) + h);
-            w[4 * h] = left_of(w[4 * h], q.x, total);
-            w[4 * h + 1] = left_of(w[4 * h + 1], q.y, total);
-            w[4 * h + 2] = left_of(w[4 * h + 2], q.z, total);
-            w[4 * h + 3] = left_of(w[4 * h + 3], q.w, total);
-        }
+DG_DEVINL uint32_t left_out(const VShared& sh, int64_t v) {
+    uint32_t out = 0;
+    for (int i = 0; i < min(sh.n_gone, kMaxNodes); ++i)
+        if (sh.gone[i] / Vec<T>::kN == v) out |= 1u << (sh.gone[i] % Vec<T>::kN);
+    return out;
+}
+
+// A warp's sum of the vectors from .. to - 1.
+template <typename T>
+DG_DEVINL uint64_t range_sum(const VShared& sh, const VerifyArgs& a, const Command& c, const uint4* src, const float* q_row,
+                             int64_t from, int64_t to) {
+    uint64_t sum = 0;
+    int64_t v = from + (threadIdx.x & 31);
+    uint4 r = v < to ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+    while (v < to) {
+        const int64_t nv = v + 32;
+        const uint4 next = nv < to ? __ldg(src + nv) : r;
+        sum += vector_sum<T>(sh, a, c, r, v, q_row, sh.n_gone ? left_out<T>(sh, v) : 0u);
+        r = next;
+        v = nv;
     }
+    return warp_add(sum);
 }
 
 // Sums of the weights by warp (q_row: of what a draft's distribution leaves of them), and the CTA's.
 template <typename T>
-DG_DEVINL void row_sums(VShared& sh, const T* row, const VerifyArgs& a, const Command& c, const float* q_row, int cta,
-                        int n_cta, int q0, int ql, Partial* to) {
-    constexpr int N = Vec<T>::kN;
+DG_DEVINL Partial row_sums(VShared& sh, const T* row, const VerifyArgs& a, const Command& c, const float* q_row, int cta,
+                           int n_cta, int q0, int ql) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Part p = part_of<T>(a.V, cta, n_cta, warp);
-    const uint4* src = reinterpret_cast<const uint4*>(row);
-    uint64_t sum = 0;
-    for (int64_t v = p.from + lane; v < p.to; v += 32) {
-        uint64_t w[N];
-        vector_weights<T>(sh, __ldg(src + v), v, a.V, c.top, a.frac, q_row, c.total, w);
-#pragma unroll
-        for (int e = 0; e < N; ++e) sum += w[e];
-    }
-    sum = warp_add(sum);
-    if (lane == 0) sh.warp_sum[warp] = sum;
     if (tid == 0) sh.n_gone = 0;
     __syncthreads();
-    if (c.minus > 0) {   // the rejected children's tokens in this CTA's part, each once
+    if (c.minus > 0) {   // the rejected children's tokens in this CTA's part
+        const int64_t part = part_size<T>(a.V, n_cta) * kVWarps;
         for (int i = c.node + 1 + tid; i < ql; i += kVThreads) {
             const int32_t t = a.tokens[q0 + i];
-            if ((a.parents ? a.parents[q0 + i] : i - 1) != c.node || t < 0 || t >= a.V) continue;
-            const int owner = part_with<T>(a.V, n_cta, t);
-            if (owner / kVWarps != cta) continue;
-            bool again = false;
-            for (int k = c.node + 1; k < i && !again; ++k)
-                again = a.tokens[q0 + k] == t && (a.parents ? a.parents[q0 + k] : k - 1) == c.node;
-            if (again) continue;
-            float x;
-            if constexpr (sizeof(T) == 2)
-                x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[t] << 16);
-            else
-                x = reinterpret_cast<const float*>(row)[t];
-            const uint64_t w = fixed_weight<T>(x, c.top, sh.c_hi, sh.c_lo, sh.pow, a.frac);
-            atomicAdd((unsigned long long*)&sh.warp_sum[owner % kVWarps], (unsigned long long)(0 - w));
-            const int at = atomicAdd(&sh.n_gone, 1);   // (in any order: the list is searched)
+            if ((a.parents ? a.parents[q0 + i] : i - 1) != c.node || t < 0 || t >= a.V || t / Vec<T>::kN / part != cta) continue;
+            const int at = atomicAdd(&sh.n_gone, 1);   // (in any order, and the same one twice: a list that is searched)
             if (at < kMaxNodes) sh.gone[at] = t;
         }
         __syncthreads();
     }
-    if (tid == 0) {
-        Partial q{};
+    const Part p = part_of<T>(a.V, cta, n_cta, warp);
+    const uint64_t sum = range_sum<T>(sh, a, c, reinterpret_cast<const uint4*>(row), q_row, p.from, p.to);
+    if (lane == 0) sh.warp_sum[warp] = sum;
+    __syncthreads();
+    Partial q{};
+    if (tid == 0)
         for (int w = 0; w < kVWarps; ++w) q.fixed += sh.warp_sum[w];
-        *to = q;
-    }
+    return q;
 }
 
 // The token whose cumulated weight passes the target, which lies in this CTA's part (warp_sum and gone are as row_sums left
-// them for these weights).
+// them for these weights).  The CTA's warps sum up to 64 segments of what is left, until that is 32 vectors.
 template <typename T>
 DG_DEVINL void find_token(VShared& sh, const T* row, const VerifyArgs& a, const Command& c, const float* q_row, int cta, int n_cta) {
     constexpr int N = Vec<T>::kN;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint4* src = reinterpret_cast<const uint4*>(row);
     uint64_t target = c.target;
     int owner = 0;
     while (owner < kVWarps - 1 && target >= sh.warp_sum[owner]) target -= sh.warp_sum[owner++];
-    if (warp != owner) return;
-    const Part p = part_of<T>(a.V, cta, n_cta, warp);
-    const uint4* src = reinterpret_cast<const uint4*>(row);
-    for (int64_t v0 = p.from; v0 < p.to; v0 += 32) {
-        const int64_t v = v0 + lane;
-        uint64_t w[N], mine = 0;
-#pragma unroll
-        for (int e = 0; e < N; ++e) w[e] = 0;
-        if (v < p.to) {
-            vector_weights<T>(sh, __ldg(src + v), v, a.V, c.top, a.frac, q_row, c.total, w);
-            if (c.minus > 0)
-                for (int i = 0; i < min(sh.n_gone, kMaxNodes); ++i)
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        if (v * N + e == sh.gone[i]) w[e] = 0;
-#pragma unroll
-            for (int e = 0; e < N; ++e) mine += w[e];
+    Part p = part_of<T>(a.V, cta, n_cta, owner);
+    while (p.to - p.from > 32) {
+        const int64_t tiles = (p.to - p.from + 31) / 32, each = (tiles + kSegments - 1) / kSegments * 32;
+        const int n = (int)((p.to - p.from + each - 1) / each);
+        for (int i = warp; i < n; i += kVWarps) {
+            const int64_t from = p.from + i * each;
+            const uint64_t s = range_sum<T>(sh, a, c, src, q_row, from, min(from + each, p.to));
+            if (lane == 0) sh.segment[i] = s;
         }
-        uint64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, incl > target);
-        if (past) {
-            if (lane == __ffs(past) - 1) {
-                uint64_t s = incl - mine;
-                int at = 0;
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    s += w[e];
-                    if (s <= target) at = e + 1;
-                }
-                a.out_tokens[c.out] = (int32_t)(v * N + at);
-            }
-            return;
-        }
-        target -= __shfl_sync(0xffffffffu, incl, 31);
+        __syncthreads();
+        int i = 0;
+        while (i < n - 1 && target >= sh.segment[i]) target -= sh.segment[i++];
+        p = Part{p.from + i * each, min(p.from + (i + 1) * each, p.to)};
+        __syncthreads();   // (the next round writes the segments)
     }
+    if (warp != 0) return;
+    const int64_t v = p.from + lane;
+    const bool in = v < p.to;
+    uint4 r = make_uint4(0, 0, 0, 0);
+    uint32_t out = 0;
+    uint64_t mine = 0;
+    if (in) {
+        r = __ldg(src + v);
+        out = sh.n_gone ? left_out<T>(sh, v) : 0u;
+        mine = vector_sum<T>(sh, a, c, r, v, q_row, out);
+    }
+    uint64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, in && incl > target);
+    if (past ? lane != __ffs(past) - 1 : lane != 0) return;
+    const uint64_t before = incl - mine;
+    int at = N - 1;
+    for (int e = 0; e < N - 1; ++e)   // the first e whose sum up to it passes
+        if (before + vector_sum<T>(sh, a, c, r, v, q_row, out | (0xffffffffu << (e + 1))) > target) {
+            at = e;
+            break;
+        }
+    a.out_tokens[c.out] = (int32_t)min(v * N + at, a.V - 1);
 }
 
-// The first CTA's first warp: tries the children of `node` in order.  The row's maximum and sum are given (fixed point when
-// `exact`).  Returns the accepted child, -1: none, -2: too near to say with an fp32 sum.  `last`: the rejected draft.
+// What the lead's first warp knows of a child before the row's statistics are there.
+struct Child {
+    bool is;
+    int32_t token;
+    float x, u, q;
+};
 template <typename T>
+DG_DEVINL Child child_of(const VShared& sh, const VerifyArgs& a, const T* row, int q0, int ql, int node, int c, float T_) {
+    Child k{false, -1, -INFINITY, 0.f, 1.f};
+    if (c >= ql || (a.parents ? sh.parent[c] != node : c != node + 1)) return k;
+    k.is = true;
+    k.token = sh.token[c];
+    if (T_ > 0.f) {
+        k.u = sh.uniform[c];
+        if (k.token >= 0 && k.token < a.V) {
+            k.x = logit<T>(row, k.token);
+            if (a.probs) k.q = unit(a.probs[(int64_t)(q0 + c) * a.ldq + k.token]);
+        }
+    }
+    return k;
+}
+
+// The lead's first warp: tries the children of `node` in order (`k`: the first 32 nodes' behind it).  The row's maximum and
+// sum are given (fixed point when Exact).  Returns the accepted child, -1: none, -2: too near to say with an fp32 sum.
+// `last`: the rejected draft.
+template <typename T, bool Exact>
 DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int ql, int node, float T_, const Partial& st,
-                     bool exact, int n_cta, int& last) {
+                     int n_cta, Child k, int& last) {
+    using F = std::conditional_t<Exact, double, float>;
     const int lane = threadIdx.x & 31;
     last = -1;
     // The sum's bound: its exponents' roundings (2^-23 of each, weighted by weights that fall faster than exponents
-    // grow), the exponentials (2^-22), the joins, and 2^-24 an addition of a thread.
-    const double sum = exact ? ldexp((double)st.fixed, -a.frac) : (double)st.sum;
-    const double slack = exact ? 0.0 : sum * (0x1p-17 + (double)a.V / (n_cta * kVThreads) * 0x1p-24);
-    double left = sum;
+    // grow), the exponentials (2^-22), the joins, this comparison, and 2^-24 an addition of a thread.
+    const F sum = Exact ? (F)ldexp((double)st.fixed, -a.frac) : (F)st.sum;
+    const F slack = Exact ? (F)0 : sum * ((F)0x1p-15f + (F)a.V / (F)(n_cta * kVThreads) * (F)0x1p-23f);
+    F left = sum;
     int n_rejected = 0;
     const int end = a.parents ? ql : min(ql, node + 2);
     for (int base = node + 1; base < end; base += 32) {
-        const int c = base + lane;
-        const bool child = c < end && (a.parents ? a.parents[q0 + c] == node : true);
-        int32_t token = -1;
-        double w = 0.0, u = 0.0, q = 1.0;
-        if (child) {
-            token = a.tokens[q0 + c];
-            if (T_ > 0.f) {
-                u = a.uniforms[q0 + c];
-                if (token >= 0 && token < a.V) {
-                    float x;
-                    if constexpr (sizeof(T) == 2)
-                        x = __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[token] << 16);
-                    else
-                        x = reinterpret_cast<const float*>(row)[token];
-                    int n;
-                    const uint64_t m = weight<T>(x, st.top, sh.c_hi, sh.c_lo, sh.pow, n);
-                    w = n <= -200 ? 0.0 : ldexp((double)m, n - 62);
-                    if (a.probs) q = unit(a.probs[(int64_t)(q0 + c) * a.ldq + token]);
-                }
+        if (base > node + 1) k = child_of<T>(sh, a, row, q0, ql, node, base + lane, T_);
+        F w = 0;
+        if (T_ > 0.f && k.is && k.token >= 0 && k.token < a.V) {
+            if constexpr (Exact) {
+                uint64_t hi, lo;
+                weights2<T>(sh, k.x, k.x, st.top, hi, lo);
+                float h, l, unused;
+                f2_split(hi, h, unused);
+                f2_split(lo, l, unused);
+                w = h > 0x1p-119f ? (F)h + (F)l : (F)0;
+            } else {
+                w = ex2((k.x - st.top) * sh.c_hi);
             }
         }
-        uint32_t todo = __ballot_sync(0xffffffffu, child);
+        uint32_t todo = __ballot_sync(0xffffffffu, k.is);
         while (todo) {
             const int from = __ffs(todo) - 1;
             todo &= todo - 1;
-            const int32_t t = __shfl_sync(0xffffffffu, token, from);
+            const int32_t t = __shfl_sync(0xffffffffu, k.token, from);
             if (T_ == 0.f) {
                 if (t == st.arg) return base + from;
                 last = base + from;
                 continue;
             }
-            const double wt = __shfl_sync(0xffffffffu, w, from), ut = __shfl_sync(0xffffffffu, u, from);
-            const double qt = __shfl_sync(0xffffffffu, q, from);
+            const F wt = __shfl_sync(0xffffffffu, w, from), ut = __shfl_sync(0xffffffffu, k.u, from);
             if (a.probs) {
-                const double lhs = ut * qt * sum;
-                if (fabs(lhs - wt) < ut * qt * slack) return -2;
+                const F m = ut * (F)__shfl_sync(0xffffffffu, k.q, from), lhs = m * sum;
+                if (!Exact && fabsf((float)(lhs - wt)) <= (float)(m * slack) && (lhs > 0 || wt > 0)) return -2;
                 if (lhs < wt) return base + from;
             } else {
                 bool again = false;
                 for (int i = lane; i < n_rejected; i += 32) again = again || sh.rejected[i] == t;
                 again = __any_sync(0xffffffffu, again);
                 if (!again) {
-                    const double lhs = ut * fmax(left, 0.0);
-                    if (fabs(lhs - wt) < ut * slack) return -2;
+                    const F lhs = ut * (left > 0 ? left : (F)0);
+                    if (!Exact && fabsf((float)(lhs - wt)) <= (float)(ut * slack) && (ut > 0 || wt > 0)) return -2;
                     if (lhs < wt) return base + from;
                     left -= wt;
                     if (lane == 0) sh.rejected[n_rejected] = t;
@@ -484,80 +582,108 @@ template <typename T>
 __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
     __shared__ VShared sh;
     cg::cluster_group cluster = cg::this_cluster();
+    const int n_cta = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
+    const int s = (int)(blockIdx.x / n_cta), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        dg::mbar_init(&sh.told, 1);
+        dg::mbar_init(&sh.parts, (uint32_t)n_cta);
+        dg::fence_mbar_init();
+    }
+    if (tid < 32) {
+        sh.pow[tid] = kPow[tid];
+        sh.rest[tid] = kPowRest[tid];
+    }
+    __syncthreads();
+    auto arrived = cluster.barrier_arrive();   // everyone runs, with its barriers, before anyone reaches into another CTA
     dg::pdl_wait();
     dg::pdl_release();
-    const int n_cta = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
-    const int s = (int)(blockIdx.x / n_cta), tid = threadIdx.x, warp = tid >> 5;
-    VShared* lead = cluster.map_shared_rank(&sh, 0);
-    const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], ql = q1 - q0;
+    const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1];
     const float T_ = a.temperature[s];
-    if (tid < 64) sh.pow[tid] = kPow[tid];
+    const bool offsets = q0 >= 0 && q1 >= q0 && (int64_t)q1 <= a.total;
+    const int ql = offsets ? q1 - q0 : 0;
     if (tid == 0) {
         const double c = T_ > 0.f ? 1.4426950408889634 / (double)T_ : 1.0;
         sh.c_hi = (float)c;
         sh.c_lo = (float)(c - (double)sh.c_hi);
+        sh.d_min = -120.f / sh.c_hi;
+        sh.n_gone = 0;
     }
-    // The first CTA alone looks at what decides how often the cluster meets.
-    int node = 0, accepted = 0;
+    // The lead alone looks at what decides how often the cluster meets.
+    int accepted = 0;
     bool walks = false;
     if (cta == 0) {
-        const bool offsets = q0 >= 0 && q1 >= q0 && (int64_t)q1 <= a.total;
         bool good = offsets && ql <= kMaxNodes;
         if (good && ql > 0) {
-            good = T_ == 0.f || (T_ >= 0x1p-64f && T_ < INFINITY);
+            good = T_ == 0.f || (T_ >= 0x1p-64f && T_ <= 0x1p64f);
             if (T_ != 0.f) good = good && a.next_uniforms[s] >= 0.f && a.next_uniforms[s] < 1.f;
-            for (int i = 1 + tid; good && i < ql; i += kVThreads) {
-                if (a.parents) good = good && a.parents[q0 + i] >= 0 && a.parents[q0 + i] < i;
-                if (T_ != 0.f) good = good && a.uniforms[q0 + i] >= 0.f && a.uniforms[q0 + i] < 1.f;
+            for (int i = tid; i < ql; i += kVThreads) {
+                const int32_t up = a.parents ? a.parents[q0 + i] : i - 1, t = a.tokens[q0 + i];
+                const float u = T_ != 0.f ? a.uniforms[q0 + i] : 0.f;
+                sh.parent[i] = up;
+                sh.token[i] = t;
+                sh.uniform[i] = u;
+                if (i > 0) good = good && up >= 0 && up < i && u >= 0.f && u < 1.f;
             }
         }
         good = !__syncthreads_or(!good);
         walks = good && ql > 0;
         if (!walks) {
-            if (offsets)
-                for (int i = tid; i < ql; i += kVThreads) a.path[q0 + i] = a.out_tokens[q0 + i] = -1;
+            for (int i = tid; i < ql; i += kVThreads) a.path[q0 + i] = a.out_tokens[q0 + i] = -1;
             if (tid == 0) {
                 a.n_accept[s] = -1;
                 if (!good) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
             }
         }
+    } else {
+        __syncthreads();
     }
-    cluster.sync();   // everyone runs before anyone writes to its shared memory
 
-    auto tell = [&](const Command& c) {   // the first CTA's first threads: one command to every CTA
-        if (tid < n_cta) *reinterpret_cast<Command*>(&cluster.map_shared_rank(&sh, tid)->cmd) = c;
-    };
-    // The first CTA's state between commands (the same in all its threads).
-    Command next{kStats, 0, 0, -1, 0, 0.f, 0, 0, 0};
-    if (cta == 0 && !walks) next.op = kExit;
-    __shared__ int s_child, s_last;
-    Partial stats{};            // of the row at `node`
+    // The first command is known to all: the root's statistics.  (A sequence that is refused gives its CTAs nothing to
+    // read; the lead's command to leave is on its way.)
+    Command c{kStats, 0, 0, -1, 0, 0.f, 0.f, 0.f, 0, 0};
+    Partial stats{};            // of the row at `node` (the lead's)
     int rejected = -1;          // the draft rejected there
-    uint64_t total = 0;
-    while (true) {
-        if (cta == 0) tell(next);
-        cluster.sync();
-        const Command c = sh.cmd;
-        if (c.op == kExit) return;
+    for (uint32_t meeting = 0;; ++meeting) {
         const T* row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + c.node) * a.ld;
         const float* q_row = c.draft >= 0 ? a.probs + (int64_t)(q0 + c.draft) * a.ldq : nullptr;
-        if (c.op == kFind) {
-            if (cta == c.cta) find_token<T>(sh, row, a, c, q_row, cta, n_cta);
-            return;
-        }
+        Child k{false, -1, 0.f, 0.f, 0.f};
+        if (cta == 0 && warp == 0 && walks) k = child_of<T>(sh, a, row, q0, ql, c.node, c.node + 1 + lane, T_);
+        Partial mine{-INFINITY, 0.f, 0x7fffffff, 0, 0};
         if (c.op == kStats) {
-            if (T_ > 0.f)
-                row_stats<T, true>(sh, row, a.V, cta, n_cta, &lead->part[cta]);
-            else
-                row_stats<T, false>(sh, row, a.V, cta, n_cta, &lead->part[cta]);
+            if (ql > 0) mine = T_ > 0.f ? row_stats<T, true>(sh, row, a.V, cta, n_cta) : row_stats<T, false>(sh, row, a.V, cta, n_cta);
         } else {
-            row_sums<T>(sh, row, a, c, q_row, cta, n_cta, q0, ql, &lead->part[cta]);
+            mine = row_sums<T>(sh, row, a, c, q_row, cta, n_cta, q0, ql);
         }
-        cluster.sync();
-        if (cta != 0) continue;
+        if (meeting == 0) cluster.barrier_wait(std::move(arrived));
+        if (tid == 0) {   // this CTA's part to the lead
+            cluster.map_shared_rank(&sh, 0)->part[cta] = mine;
+            arrive_cluster(dg::mapa_shared(&sh.parts, 0));
+        }
+        if (cta != 0) {
+            if (!dg::mbar_wait_cluster(&sh.told, meeting & 1u)) {
+                if (tid == 0) dg::raise_status(a.status, DG_DEV_TIMEOUT);
+                break;
+            }
+            c = sh.cmd;
+            if (c.op == kExit) break;
+            if (c.op == kFind) {
+                if (cta == c.cta) {
+                    row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + c.node) * a.ld;
+                    find_token<T>(sh, row, a, c, c.draft >= 0 ? a.probs + (int64_t)(q0 + c.draft) * a.ldq : nullptr, cta, n_cta);
+                }
+                break;
+            }
+            continue;
+        }
 
-        // The first CTA decides what comes next.
-        bool finish = false, no_token = false;
+        // The lead decides what comes next.
+        Command next{kExit, c.node, 0, -1, 0, stats.top, 0.f, 0.f, 0, 0};
+        bool finish = !walks, no_token = false;
+        if (!dg::mbar_wait_cluster(&sh.parts, meeting & 1u)) {   // (bounded; the others' waits run out as well)
+            if (tid == 0) dg::raise_status(a.status, DG_DEV_TIMEOUT);
+            finish = true;
+            walks = false;
+        }
         auto draw_from = [&](uint64_t sum) {   // the token past next_uniforms * sum
             const float u = a.next_uniforms[s];
             const uint64_t U = (uint64_t)__float2ull_rz(u * 0x1p32f) << 32 |
@@ -565,17 +691,18 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
             uint64_t target = __umul64hi(sum, U);
             int owner = 0;
             while (owner < n_cta - 1 && target >= sh.part[owner].fixed) target -= sh.part[owner++].fixed;
+            next = c;
             next.op = kFind;
             next.cta = owner;
             next.target = target;
             next.out = q0 + accepted;
         };
-        if (c.op == kStats) {
+        if (walks && c.op == kStats) {
             Partial t{-INFINITY, 0.f, 0x7fffffff, 0, 0};
             for (int i = 0; i < n_cta; ++i) t.top = fmaxf(t.top, sh.part[i].top);
             const float at = t.top == -INFINITY ? 0.f : t.top;
             for (int i = 0; i < n_cta; ++i) {
-                t.sum += sh.part[i].sum * ex2((sh.part[i].top - at) * sh.c_hi);
+                if (T_ > 0.f) t.sum += sh.part[i].sum * ex2((sh.part[i].top - at) * sh.c_hi);
                 if (sh.part[i].top == t.top) t.arg = min(t.arg, sh.part[i].arg);
                 t.bad |= sh.part[i].bad;
             }
@@ -585,36 +712,34 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
                 if (tid == 0) dg::raise_status(a.status, nan ? DG_DEV_NAN_INF_ROW : DG_DEV_EMPTY_ROW);
                 finish = no_token = true;
             }
-        } else {
+        } else if (walks) {
             uint64_t f = 0;
             for (int i = 0; i < n_cta; ++i) f += sh.part[i].fixed;
             stats.fixed = f;
         }
         if (!finish && (c.op == kStats || (c.op == kSum && c.minus < 0))) {   // (minus -1: a sum asked for by a decision)
-            __syncthreads();
             if (warp == 0) {
                 int last;
-                const int child = decide<T>(sh, a, row, q0, ql, c.node, T_, stats, c.op == kSum, n_cta, last);
-                if (tid == 0) {
-                    s_child = child;
-                    s_last = last;
+                const int child = c.op == kSum ? decide<T, true>(sh, a, row, q0, ql, c.node, T_, stats, n_cta, k, last)
+                                               : decide<T, false>(sh, a, row, q0, ql, c.node, T_, stats, n_cta, k, last);
+                if (lane == 0) {
+                    sh.child = child;
+                    sh.last = last;
                 }
             }
             __syncthreads();
-            const int child = s_child;
-            next = Command{kStats, c.node, 0, -1, 0, stats.top, 0, 0, 0};
+            const int child = sh.child;
+            next.op = kStats;
+            next.top = stats.top;
             if (child == -2) {
                 next.op = kSum;
                 next.minus = -1;
             } else if (child >= 0) {
-                if (tid == 0) {
-                    sh.path[accepted] = child;
-                }
-                node = child;
+                if (tid == 0) sh.path[accepted] = child;
                 ++accepted;
                 next.node = child;
             } else {
-                rejected = s_last;
+                rejected = sh.last;
                 if (T_ == 0.f) {
                     if (tid == 0) a.out_tokens[q0 + accepted] = stats.arg;
                     finish = true;
@@ -624,37 +749,51 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
                 }
             }
         } else if (!finish && c.op == kSum) {
-            total = stats.fixed;
             if (a.probs && rejected >= 0) {
+                const double w = ldexp((double)stats.fixed, -a.frac);
                 next.op = kLeft;
                 next.draft = rejected;
-                next.total = total;
-            } else if (c.minus > 0 && total == 0) {
-                next.minus = 0;          // nothing is left: all of the row again
+                next.w_hi = (float)w;
+                next.w_lo = (float)(w - (double)next.w_hi);
+            } else if (c.minus > 0 && stats.fixed == 0) {
+                next.op = kSum;          // nothing is left: all of the row again
             } else {
-                draw_from(total);
+                draw_from(stats.fixed);
             }
         } else if (!finish) {            // kLeft
             if (stats.fixed == 0) {      // nothing is left: the row itself, whose sums are made again
                 rejected = -1;
-                next = Command{kSum, c.node, 0, -1, 0, stats.top, 0, 0, 0};
+                next.op = kSum;
             } else {
                 draw_from(stats.fixed);
             }
         }
-        if (finish || next.op == kFind) {   // the walk's outputs
-            __syncthreads();
+        if (finish) next.op = kExit;
+        __syncthreads();   // the parts are read: the next ones may come
+        if (tid > 0 && tid < n_cta) {
+            VShared* to = cluster.map_shared_rank(&sh, tid);
+            to->cmd = next;
+            arrive_cluster(dg::mapa_shared(&sh.told, (uint32_t)tid));
+        }
+        if (walks && (next.op == kExit || next.op == kFind)) {   // the walk's outputs
             for (int i = tid; i < ql; i += kVThreads) {
                 a.path[q0 + i] = i == 0 ? 0 : i <= accepted ? sh.path[i - 1] : -1;
                 if (i < accepted)
-                    a.out_tokens[q0 + i] = a.tokens[q0 + sh.path[i]];
+                    a.out_tokens[q0 + i] = sh.token[sh.path[i]];
                 else if (i > accepted || no_token)
                     a.out_tokens[q0 + i] = -1;
             }
             if (tid == 0) a.n_accept[s] = accepted;
-            if (finish) next.op = kExit;
         }
-        __syncthreads();
+        if (next.op == kExit) break;
+        if (next.op == kFind) {
+            if (next.cta == 0) {
+                row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + next.node) * a.ld;
+                find_token<T>(sh, row, a, next, next.draft >= 0 ? a.probs + (int64_t)(q0 + next.draft) * a.ldq : nullptr, 0, n_cta);
+            }
+            break;
+        }
+        c = next;
     }
 }
 
@@ -787,7 +926,10 @@ extern "C" dg_status dg_verify_drafts(const void* logits, dg_dtype dtype, int64_
     while ((1LL << bits) < V) ++bits;
     a.frac = std::min(44, 62 - bits);
     a.status = dghost::status_word();
-    const int cluster = 8;
+    const int sms = dghost::sm_count();
+    if (sms <= 0) return DG_ERR_CUDA;
+    int cluster = 8;
+    while (cluster > 1 && (int64_t)n_seq * cluster > 2 * (int64_t)sms) cluster /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)n_seq * cluster);
     cfg.blockDim = dim3(kVThreads);

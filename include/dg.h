@@ -546,7 +546,7 @@ DG_API dg_status dg_sink_attention(const uint16_t* q, const dg_paged_kv* cache, 
  * Probabilities are fp32 where that decides, else within 2^-31 of the formula's, summed in 64-bit fixed point; so
  * results do not depend on order, and repeated calls are bit-identical.
  * A sequence without nodes, or one that is refused (offsets outside [0, total], more than 1024 nodes, a parent or
- * temperature out of range (negative, not finite or below 2^-64 but not 0), a uniform outside [0, 1)) has n_accept = -1, and -1 in its rows of path and
+ * temperature out of range (neither 0 nor in [2^-64, 2^64]), a uniform outside [0, 1)) has n_accept = -1, and -1 in its rows of path and
  * out_tokens where its offsets are good; refusals raise DG_DEV_BAD_PARAM.  A row on the walk that holds NaN or +inf raises
  * DG_DEV_NAN_INF_ROW, one all -inf DG_DEV_EMPTY_ROW: the walk ends there with next token -1.
  * Limits: n_seq in [0, 65535], 2 <= V < 2^30, total < 2^31, V * sizeof(dtype) < 2^31.  Errors:
