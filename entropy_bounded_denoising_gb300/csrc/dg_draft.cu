@@ -15,9 +15,12 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-// Arrives on a barrier of another CTA of the cluster (or this one), after what this thread has written there.
-DG_DEVINL void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// 16 bytes into the shared memory of a CTA of the cluster, counted by the barrier there once they lie in their place (one
+// trip; a store, and an arrival that waits for it, take two).
+DG_DEVINL void send16(uint32_t to, const uint4& v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
+                 : "memory");
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -43,6 +46,7 @@ constexpr int kVThreads = 256, kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxNodes = 1024;
 constexpr int kSegments = 64;      // that a part is searched in at a time
+constexpr int kDeep = 5;           // vectors a lane has on their way
 
 // 2^(j / 32), rounded, and what the rounding left out, relative.
 __constant__ float kPow[32] = {
@@ -80,7 +84,7 @@ struct VerifyArgs {
 enum : int { kStats, kSum, kLeft, kFind, kExit };
 
 // What the lead tells the others to do with a row.
-struct Command {
+struct __align__(16) Command {
     int op;
     int node;          // row of the sequence
     int minus;         // kSum, and kFind after it: 1: leave out the tokens of the node's children; -1: for a decision
@@ -91,11 +95,16 @@ struct Command {
     uint64_t target;   // kFind: the sum to pass, counted from that CTA's part
     int64_t out;       // and the place of the token
 };
+static_assert(sizeof(Command) == 48, "sent 16 bytes at a time");
 
-struct Partial {       // of one CTA: kStats: maximum, sum, its place, a NaN or +inf; kSum, kLeft: sum
+struct __align__(16) Partial {       // of one CTA: kStats: maximum, sum, its place, a NaN or +inf
     float top, sum;
     int arg, bad;
-    uint64_t fixed;
+    DG_DEVINL uint64_t fixed() const { return (uint32_t)arg | (uint64_t)(uint32_t)bad << 32; }   // kSum, kLeft: the sum
+    DG_DEVINL void set_fixed(uint64_t v) {
+        arg = (int)(uint32_t)v;
+        bad = (int)(uint32_t)(v >> 32);
+    }
 };
 
 struct __align__(16) VShared {
@@ -108,13 +117,42 @@ struct __align__(16) VShared {
     int w_arg[kVWarps], w_bad[kVWarps];
     float pow[32], rest[32];
     float c_hi, c_lo, d_min;          // log2(e) / temperature, and the difference whose weight is 2^-120
+    int64_t V;
+    int frac;
     int n_gone;                       // rejected tokens of the last node that lie in this CTA's part
     int child, last;                  // what the lead's first warp decided
+    uint4 ring[kVWarps][kDeep][32];   // vectors on their way
     int gone[kMaxNodes];
     int path[kMaxNodes];              // the lead's, as the rest:
     int rejected[kMaxNodes];
     int token[kMaxNodes], parent[kMaxNodes];
     float uniform[kMaxNodes];
+};
+
+// A lane's vectors of a row, `hop` apart, on their way through its own places in shared memory: in registers they would be
+// waited for when they are moved along, or the loop unrolled past the instruction cache.
+struct Stream {
+    const uint4 *src, *place;
+    int64_t ask, hop, to;
+    int at;
+
+    DG_DEVINL Stream(VShared& sh, const uint4* row, int64_t v, int64_t hop_, int64_t to_)
+        : src(row), place(&sh.ring[threadIdx.x >> 5][0][threadIdx.x & 31]), ask(v), hop(hop_), to(to_), at(0) {
+        for (int k = 0; k < kDeep - 1; ++k) request(k);
+    }
+    DG_DEVINL void request(int slot) {
+        if (ask < to)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dg::smem_u32(place + slot * 32)), "l"(src + ask) : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ask += hop;
+    }
+    DG_DEVINL uint4 next() {   // the next vector (anything behind the last)
+        request(at ? at - 1 : kDeep - 1);   // the place that was read last
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
+        const uint4 r = place[at * 32];
+        at = at == kDeep - 1 ? 0 : at + 1;
+        return r;
+    }
 };
 
 template <typename T>
@@ -178,107 +216,111 @@ DG_DEVINL uint64_t f2_mul(uint64_t a, uint64_t b) {
 }
 DG_DEVINL uint64_t f2_sub(uint64_t a, uint64_t b) { return f2_fma(b, f2(-1.f, -1.f), a); }
 
-// 2^((x - top) c) of two logits, each as hi + lo.  The exponent in two floats: the difference (with what its rounding left
-// out where logits are fp32; of bf16 logits it is exact unless one is 2^16 times the other), its product with c.  Then
-// 2^(j / 32) 2^g with the terms up to g^4 (the next is below 2^-39).  Differences below d_min, -inf and NaN among
-// them, weigh 2^-120: nothing at any place after the point.
+// 2^((x - top) c) of two logits as w (1 + e), w a table's 2^(j / 32) times a power of two, |e| < 2^-6.  The exponent in two
+// floats: the difference (with what its rounding left out where logits are fp32; of bf16 logits it is exact unless one
+// is 2^16 times the other), its product with c, cut into j, the power and g, |g| <= 1 / 64; e from the terms up to g^4 (the
+// next is below 2^-39) and what the table's rounding left out.  Differences below d_min, -inf and NaN among them, weigh
+// 2^-120: nothing at any place after the point.
 template <typename T>
-DG_DEVINL void weights2(const VShared& sh, float x0, float x1, float top, uint64_t& hi, uint64_t& lo) {
+DG_DEVINL void weights2(const VShared& sh, float x0, float x1, float top, uint64_t& w, uint64_t& e) {
     const uint64_t x = f2(x0, x1), nt = f2(-top, -top);
-    uint64_t d = f2_add(x, nt), left = 0;
+    const uint64_t c = f2(sh.c_hi, sh.c_hi), nc = f2(-sh.c_hi, -sh.c_hi), cl = f2(sh.c_lo, sh.c_lo);
+    const uint64_t magic = f2(12582912.f, 12582912.f);       // 1.5 2^23: rounds to a whole number
+    uint64_t d = f2_add(x, nt);
+    float d0, d1;
+    f2_split(d, d0, d1);
+    uint64_t left = 0;
     if constexpr (sizeof(T) == 4) {
         const uint64_t z = f2_sub(d, x);
         left = f2_add(f2_sub(x, f2_sub(d, z)), f2_sub(nt, z));
-    }
-    float d0, d1;
-    f2_split(d, d0, d1);
-    const bool low0 = !(d0 > sh.d_min), low1 = !(d1 > sh.d_min);
-    d = f2(low0 ? sh.d_min : d0, low1 ? sh.d_min : d1);
-    const uint64_t c = f2(sh.c_hi, sh.c_hi), cl = f2(sh.c_lo, sh.c_lo);
-    const uint64_t p = f2_mul(d, c);
-    uint64_t q = f2_fma(d, c, f2_mul(p, f2(-1.f, -1.f)));
-    q = f2_fma(d, cl, q);
-    if constexpr (sizeof(T) == 4) {
         float l0, l1;
         f2_split(left, l0, l1);
-        q = f2_fma(f2(low0 ? 0.f : l0, low1 ? 0.f : l1), c, q);
+        left = f2(d0 > sh.d_min ? l0 : 0.f, d1 > sh.d_min ? l1 : 0.f);
     }
-    const uint64_t magic = f2(12582912.f, 12582912.f);       // 1.5 2^23: rounds to a whole number
+    d = f2(fmaxf(d0, sh.d_min), fmaxf(d1, sh.d_min));
+    const uint64_t p = f2_mul(d, c), over = f2_fma(d, nc, p);   // over: what p's rounding has too much
     const uint64_t t = f2_fma(p, f2(32.f, 32.f), magic);
     uint64_t g = f2_fma(f2_sub(t, magic), f2(-0.03125f, -0.03125f), p);
-    g = f2_add(g, q);
-    uint64_t e = f2_fma(g, f2(9.6181291e-3f, 9.6181291e-3f), f2(5.5504109e-2f, 5.5504109e-2f));
+    g = f2_fma(d, cl, f2_sub(g, over));
+    if constexpr (sizeof(T) == 4) g = f2_fma(left, c, g);
+    e = f2_fma(g, f2(9.6181291e-3f, 9.6181291e-3f), f2(5.5504109e-2f, 5.5504109e-2f));
     e = f2_fma(g, e, f2(0.24022651f, 0.24022651f));
     e = f2_fma(g, e, f2(0.69314718f, 0.69314718f));
     float t0, t1;
     f2_split(t, t0, t1);
     const int k0 = __float_as_int(t0), k1 = __float_as_int(t1);   // (whole number in the low bits, the rest of the magic above)
-    const int j0 = k0 & 31, j1 = k1 & 31;
-    e = f2_fma(g, e, f2(sh.rest[j0], sh.rest[j1]));
-    const uint64_t w = f2(__int_as_float(__float_as_int(sh.pow[j0]) + ((k0 << 18) & 0xff800000)),
-                          __int_as_float(__float_as_int(sh.pow[j1]) + ((k1 << 18) & 0xff800000)));
-    hi = f2_fma(w, e, w);
-    lo = f2_fma(w, e, f2_sub(w, hi));
+    e = f2_fma(g, e, f2(sh.rest[k0 & 31], sh.rest[k1 & 31]));
+    w = f2(__int_as_float(__float_as_int(sh.pow[k0 & 31]) + (k0 & ~31) * (1 << 18)),
+           __int_as_float(__float_as_int(sh.pow[k1 & 31]) + (k1 & ~31) * (1 << 18)));
 }
 
 DG_DEVINL float unit(float q) { return fminf(fmaxf(q, 0.f), 1.f); }   // (a NaN is 0)
 
-// The sum of a vector's weights in fixed point; with q_row of what q times the row's sum leaves of them.  Elements whose
-// bit of `out` is set are left out.
-template <typename T>
-DG_DEVINL uint64_t vector_sum(const VShared& sh, const VerifyArgs& a, const Command& c, const uint4& r, int64_t v,
-                              const float* q_row, uint32_t out) {
+// The sum of a vector's weights in fixed point; with Left of what q times the row's sum leaves of them.  Elements whose
+// bit of `out` is set are left out.  What a weight has in multiples of 2^-20 adds up exactly; the rest, below 2^-6 of the
+// weight, in fp32.
+template <typename T, bool Left>
+DG_DEVINL uint64_t vector_sum(const VShared& sh, const uint4& r, int64_t v, const float* q_row, uint32_t out) {
     constexpr int N = Vec<T>::kN;
+    const int64_t V = sh.V;
     float x[N];
-    unpack<T>(r, v, a.V, x);
+    unpack<T>(r, v, V, x);
     float q[N];
-    if (q_row) {
+    if constexpr (Left) {
 #pragma unroll
         for (int h = 0; h < N / 4; ++h) {   // (four that begin before V end within the row)
-            const float4 f = v * N + 4 * h < a.V ? __ldg(reinterpret_cast<const float4*>(q_row + v * N) + h) : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 f = v * N + 4 * h < V ? __ldg(reinterpret_cast<const float4*>(q_row + v * N) + h) : make_float4(1.f, 1.f, 1.f, 1.f);
             q[4 * h] = unit(f.x);
             q[4 * h + 1] = unit(f.y);
             q[4 * h + 2] = unit(f.z);
             q[4 * h + 3] = unit(f.w);
         }
     }
-    const uint64_t grid = f2(12.f, 12.f);       // 1.5 2^3: rounds to multiples of 2^-20
+    const uint64_t grid = f2(12.f, 12.f), minus_grid = f2(-12.f, -12.f);   // 1.5 2^3: rounds to multiples of 2^-20
     uint64_t coarse = 0, fine = 0;
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
-        uint64_t hi, lo;
-        weights2<T>(sh, x[e], x[e + 1], c.top, hi, lo);
-        if (q_row) {                            // hi + lo - q (w_hi + w_lo), or 0
-            const uint64_t qq = f2(q[e], q[e + 1]), wh = f2(c.w_hi, c.w_hi);
+    for (int i = 0; i < N; i += 2) {
+        uint64_t w, e;
+        weights2<T>(sh, x[i], x[i + 1], sh.cmd.top, w, e);
+        if constexpr (Left) {                   // w (1 + e) - q (w_hi + w_lo), or 0
+            const uint64_t hi = f2_fma(w, e, w), lo = f2_fma(w, e, f2_sub(w, hi));
+            const uint64_t qq = f2(q[i], q[i + 1]), wh = f2(sh.cmd.w_hi, sh.cmd.w_hi);
             const uint64_t p = f2_mul(qq, wh);
-            const uint64_t pl = f2_fma(qq, f2(c.w_lo, c.w_lo), f2_fma(qq, wh, f2_mul(p, f2(-1.f, -1.f))));
+            const uint64_t pl = f2_fma(qq, f2(sh.cmd.w_lo, sh.cmd.w_lo), f2_fma(qq, wh, f2_mul(p, f2(-1.f, -1.f))));
             const uint64_t d = f2_sub(hi, p), z = f2_sub(d, hi);
             const uint64_t err = f2_sub(f2_sub(hi, f2_sub(d, z)), f2_add(p, z));
             const uint64_t l = f2_add(err, f2_sub(lo, pl));
             const uint64_t h = f2_add(d, l);
-            lo = f2_add(f2_sub(d, h), l);
+            const uint64_t rest = f2_add(f2_sub(d, h), l);
             float h0, h1, l0, l1;
             f2_split(h, h0, h1);
-            f2_split(lo, l0, l1);
-            hi = f2(h0 > 0.f ? h0 : 0.f, h1 > 0.f ? h1 : 0.f);
-            lo = f2(h0 > 0.f ? l0 : 0.f, h1 > 0.f ? l1 : 0.f);
+            f2_split(rest, l0, l1);
+            w = f2(h0 > 0.f ? h0 : 0.f, h1 > 0.f ? h1 : 0.f);
+            e = f2(h0 > 0.f ? l0 : 0.f, h1 > 0.f ? l1 : 0.f);   // here the rest itself
         }
-        if (out >> e & 3u) {
-            float h0, h1, l0, l1;
-            f2_split(hi, h0, h1);
-            f2_split(lo, l0, l1);
-            hi = f2(out >> e & 1u ? 0.f : h0, out >> e & 2u ? 0.f : h1);
-            lo = f2(out >> e & 1u ? 0.f : l0, out >> e & 2u ? 0.f : l1);
+        if (out >> i & 3u) {
+            float h0, h1;
+            f2_split(w, h0, h1);
+            w = f2(out >> i & 1u ? 0.f : h0, out >> i & 2u ? 0.f : h1);
+            if constexpr (Left) {
+                f2_split(e, h0, h1);
+                e = f2(out >> i & 1u ? 0.f : h0, out >> i & 2u ? 0.f : h1);
+            }
         }
-        const uint64_t m = f2_sub(f2_add(hi, grid), grid);
+        const uint64_t m = f2_add(f2_add(w, grid), minus_grid);
         coarse = f2_add(coarse, m);
-        fine = f2_add(f2_add(fine, f2_sub(hi, m)), lo);
+        fine = f2_add(fine, f2_sub(w, m));
+        fine = Left ? f2_add(fine, e) : f2_fma(w, e, fine);
     }
     float c0, c1, g0, g1;
     f2_split(coarse, c0, c1);
     f2_split(fine, g0, g1);
+    // (a vector's fine part stays below 2^-3: within 2^47 - 32-bit parts of it, in two steps)
     const int64_t whole = __float2int_rn((c0 + c1) * 1048576.f);
-    return (uint64_t)((whole << (a.frac - 20)) + __float2int_rn((g0 + g1) * __int_as_float((a.frac + 127) << 23)));
+    const float f = g0 + g1, high = rintf(f * 1048576.f);
+    const int64_t first = whole + (int64_t)(int)high;
+    const float low = fmaf(high, -0x1p-20f, f);
+    return (uint64_t)((first << (sh.frac - 20)) + __float2int_rn(low * __int_as_float((sh.frac + 127) << 23)));
 }
 
 DG_DEVINL uint64_t warp_add(uint64_t v) {
@@ -303,10 +345,32 @@ DG_DEVINL Part part_of(int64_t V, int cta, int n_cta, int warp) {
     return Part{min(from, nv), min(from + each, nv)};
 }
 
+// Joins the statistics of the first n (a power of two) lanes, for all of them.
+template <bool Sum, int n>
+DG_DEVINL Partial join_stats(Partial q, float c) {
+    float top = q.top;
+#pragma unroll
+    for (int o = n / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if constexpr (Sum) {
+        q.sum *= ex2((q.top - (top == -INFINITY ? 0.f : top)) * c);   // (-inf: 0; a NaN or +inf: a NaN)
+#pragma unroll
+        for (int o = n / 2; o; o >>= 1) q.sum += __shfl_xor_sync(0xffffffffu, q.sum, o);
+    } else {
+        if (q.top != top) q.arg = 0x7fffffff;
+#pragma unroll
+        for (int o = n / 2; o; o >>= 1) {
+            q.arg = min(q.arg, __shfl_xor_sync(0xffffffffu, q.arg, o));
+            q.bad |= __shfl_xor_sync(0xffffffffu, q.bad, o);
+        }
+    }
+    q.top = top;
+    return q;
+}
+
 // A row's maximum, its smallest place (without Sum), and with Sum the sum of 2^((x - maximum) c), of this CTA's part.
 template <typename T, bool Sum>
 DG_DEVINL Partial row_stats(VShared& sh, const T* row, int64_t V, int cta, int n_cta) {
-    constexpr int N = Vec<T>::kN, kDeep = 4;
+    constexpr int N = Vec<T>::kN;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Part p = part_of<T>(V, cta, n_cta, warp);
     const uint4* src = reinterpret_cast<const uint4*>(row);
@@ -314,71 +378,47 @@ DG_DEVINL Partial row_stats(VShared& sh, const T* row, int64_t V, int cta, int n
     float top = -INFINITY, sum = 0.f;
     int arg = 0x7fffffff;
     bool bad = false;
-    for (int64_t v0 = p.from + lane; v0 < p.to; v0 += 32 * kDeep) {
-        uint4 r[kDeep];
+    int64_t v = p.from + lane;
+    Stream in(sh, src, v, 32, p.to);
+#pragma unroll 1
+    for (; v < p.to; v += 32) {
+        const uint4 now = in.next();
+        float x[N];
+        unpack<T>(now, v, V, x);
+        float most = x[0];
 #pragma unroll
-        for (int k = 0; k < kDeep; ++k)
-            if (v0 + k * 32 < p.to) r[k] = __ldg(src + v0 + k * 32);
+        for (int e = 1; e < N; ++e) most = fmaxf(most, x[e]);
+        if constexpr (Sum) {
+            if (most > top) {
+                sum *= ex2((top - most) * c);   // (0 of -inf: 0 stays 0)
+                top = most;
+            }
+            const float at = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int k = 0; k < kDeep; ++k) {
-            const int64_t v = v0 + k * 32;
-            if (v >= p.to) break;
-            float x[N];
-            unpack<T>(r[k], v, V, x);
-            float most = x[0];
+            for (int e = 0; e < N; ++e) sum += ex2((x[e] - at) * c);   // a NaN or +inf makes it a NaN
+        } else {
 #pragma unroll
-            for (int e = 1; e < N; ++e) most = fmaxf(most, x[e]);
-            if constexpr (Sum) {
-                if (most > top) {
-                    sum *= ex2((top - most) * c);   // (0 of -inf: 0 stays 0)
-                    top = most;
-                }
-                const float at = top == -INFINITY ? 0.f : top;
+            for (int e = 0; e < N; ++e) bad = bad || !(x[e] < INFINITY);
+            if (most > top) {
+                top = most;
 #pragma unroll
-                for (int e = 0; e < N; ++e) sum += ex2((x[e] - at) * c);   // a NaN or +inf makes it a NaN
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) bad = bad || !(x[e] < INFINITY);
-                if (most > top) {
-                    top = most;
-#pragma unroll
-                    for (int e = N - 1; e >= 0; --e)
-                        if (x[e] == most) arg = (int)(v * N + e);
-                }
+                for (int e = N - 1; e >= 0; --e)
+                    if (x[e] == most) arg = (int)(v * N + e);
             }
         }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const float t = __shfl_xor_sync(0xffffffffu, top, o);
-        const float m = fmaxf(top, t);
-        if constexpr (Sum) {
-            const float s = __shfl_xor_sync(0xffffffffu, sum, o);
-            const float at = m == -INFINITY ? 0.f : m;
-            sum = sum * ex2((top - at) * c) + s * ex2((t - at) * c);
-        } else {
-            const int g = __shfl_xor_sync(0xffffffffu, arg, o);
-            arg = t > top ? g : t == top ? min(arg, g) : arg;
-            bad = bad | __shfl_xor_sync(0xffffffffu, (int)bad, o);
-        }
-        top = m;
-    }
+    const Partial w = join_stats<Sum, 32>(Partial{top, sum, arg, bad}, c);
     if (lane == 0) {
-        sh.w_top[warp] = top;
-        sh.w_sum[warp] = sum;
-        sh.w_arg[warp] = arg;
-        sh.w_bad[warp] = bad;
+        sh.w_top[warp] = w.top;
+        sh.w_sum[warp] = w.sum;
+        sh.w_arg[warp] = w.arg;
+        sh.w_bad[warp] = w.bad;
     }
     __syncthreads();
-    Partial q{-INFINITY, 0.f, 0x7fffffff, 0, 0};
-    if (tid == 0) {
-        for (int w = 0; w < kVWarps; ++w) q.top = fmaxf(q.top, sh.w_top[w]);
-        const float at = q.top == -INFINITY ? 0.f : q.top;
-        for (int w = 0; w < kVWarps; ++w) {
-            if constexpr (Sum) q.sum += sh.w_sum[w] * ex2((sh.w_top[w] - at) * c);
-            if (sh.w_top[w] == q.top) q.arg = min(q.arg, sh.w_arg[w]);
-            q.bad |= sh.w_bad[w];
-        }
+    Partial q{-INFINITY, 0.f, 0x7fffffff, 0};
+    if (warp == 0) {
+        if (lane < kVWarps) q = Partial{sh.w_top[lane], sh.w_sum[lane], sh.w_arg[lane], sh.w_bad[lane]};
+        q = join_stats<Sum, kVWarps>(q, c);
     }
     return q;
 }
@@ -392,25 +432,32 @@ DG_DEVINL uint32_t left_out(const VShared& sh, int64_t v) {
     return out;
 }
 
-// A warp's sum of the vectors from .. to - 1.
-template <typename T>
-DG_DEVINL uint64_t range_sum(const VShared& sh, const VerifyArgs& a, const Command& c, const uint4* src, const float* q_row,
-                             int64_t from, int64_t to) {
+// A warp's sum of every `hop`-th 32 vectors of from .. to - 1; with `tiles`, each 32 vectors' sum there instead.  A function of
+// its own: in line, twice, its constants and the walk's state do not fit the registers together.
+template <typename T, bool Left>
+__device__ __noinline__ uint64_t range_sum(VShared& sh, const uint4* src, const float* q_row, int64_t from, int64_t hop,
+                                           int64_t to, uint64_t* tiles) {
+    const int lane = threadIdx.x & 31;
     uint64_t sum = 0;
-    int64_t v = from + (threadIdx.x & 31);
-    uint4 r = v < to ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
-    while (v < to) {
-        const int64_t nv = v + 32;
-        const uint4 next = nv < to ? __ldg(src + nv) : r;
-        sum += vector_sum<T>(sh, a, c, r, v, q_row, sh.n_gone ? left_out<T>(sh, v) : 0u);
-        r = next;
-        v = nv;
+    int64_t v = from + lane;
+    Stream in(sh, src, v, hop, to);
+    const bool gone = sh.n_gone > 0;
+#pragma unroll 1
+    for (; v - lane < to; v += hop) {
+        const uint4 now = in.next();
+        const uint64_t s = v < to ? vector_sum<T, Left>(sh, now, v, q_row, gone ? left_out<T>(sh, v) : 0u) : 0ull;
+        if (tiles) {
+            const uint64_t all = warp_add(s);
+            if (lane == 0) tiles[(v - lane - from) / 32] = all;
+        } else {
+            sum += s;
+        }
     }
-    return warp_add(sum);
+    return tiles ? 0 : warp_add(sum);
 }
 
-// Sums of the weights by warp (q_row: of what a draft's distribution leaves of them), and the CTA's.
-template <typename T>
+// Sums of the weights by warp (Left: of what a draft's distribution leaves of them), and the CTA's.
+template <typename T, bool Left>
 DG_DEVINL Partial row_sums(VShared& sh, const T* row, const VerifyArgs& a, const Command& c, const float* q_row, int cta,
                            int n_cta, int q0, int ql) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -427,33 +474,42 @@ DG_DEVINL Partial row_sums(VShared& sh, const T* row, const VerifyArgs& a, const
         __syncthreads();
     }
     const Part p = part_of<T>(a.V, cta, n_cta, warp);
-    const uint64_t sum = range_sum<T>(sh, a, c, reinterpret_cast<const uint4*>(row), q_row, p.from, p.to);
+    const uint64_t sum = range_sum<T, Left>(sh, reinterpret_cast<const uint4*>(row), q_row, p.from, 32, p.to, nullptr);
     if (lane == 0) sh.warp_sum[warp] = sum;
     __syncthreads();
     Partial q{};
     if (tid == 0)
-        for (int w = 0; w < kVWarps; ++w) q.fixed += sh.warp_sum[w];
+    {
+        uint64_t f = 0;
+        for (int w = 0; w < kVWarps; ++w) f += sh.warp_sum[w];
+        q.set_fixed(f);
+    }
     return q;
 }
 
 // The token whose cumulated weight passes the target, which lies in this CTA's part (warp_sum and gone are as row_sums left
 // them for these weights).  The CTA's warps sum up to 64 segments of what is left, until that is 32 vectors.
-template <typename T>
-DG_DEVINL void find_token(VShared& sh, const T* row, const VerifyArgs& a, const Command& c, const float* q_row, int cta, int n_cta) {
+template <typename T, bool Left>
+__device__ __noinline__ void find_token(VShared& sh, const T* row, const float* q_row, int cta, int n_cta, int32_t* out_tokens) {
     constexpr int N = Vec<T>::kN;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint4* src = reinterpret_cast<const uint4*>(row);
-    uint64_t target = c.target;
+    uint64_t target = sh.cmd.target;
     int owner = 0;
     while (owner < kVWarps - 1 && target >= sh.warp_sum[owner]) target -= sh.warp_sum[owner++];
-    Part p = part_of<T>(a.V, cta, n_cta, owner);
+    Part p = part_of<T>(sh.V, cta, n_cta, owner);
     while (p.to - p.from > 32) {
         const int64_t tiles = (p.to - p.from + 31) / 32, each = (tiles + kSegments - 1) / kSegments * 32;
         const int n = (int)((p.to - p.from + each - 1) / each);
-        for (int i = warp; i < n; i += kVWarps) {
-            const int64_t from = p.from + i * each;
-            const uint64_t s = range_sum<T>(sh, a, c, src, q_row, from, min(from + each, p.to));
-            if (lane == 0) sh.segment[i] = s;
+        if (each == 32) {
+            range_sum<T, Left>(sh, src, q_row, p.from + warp * 32, 32 * kVWarps, p.to, sh.segment + warp);
+        } else {
+#pragma unroll 1
+            for (int i = warp; i < n; i += kVWarps) {
+                const int64_t from = p.from + i * each;
+                const uint64_t s = range_sum<T, Left>(sh, src, q_row, from, 32, min(from + each, p.to), nullptr);
+                if (lane == 0) sh.segment[i] = s;
+            }
         }
         __syncthreads();
         int i = 0;
@@ -470,7 +526,7 @@ DG_DEVINL void find_token(VShared& sh, const T* row, const VerifyArgs& a, const 
     if (in) {
         r = __ldg(src + v);
         out = sh.n_gone ? left_out<T>(sh, v) : 0u;
-        mine = vector_sum<T>(sh, a, c, r, v, q_row, out);
+        mine = vector_sum<T, Left>(sh, r, v, q_row, out);
     }
     uint64_t incl = mine;
 #pragma unroll
@@ -479,15 +535,17 @@ DG_DEVINL void find_token(VShared& sh, const T* row, const VerifyArgs& a, const 
         if (lane >= o) incl += y;
     }
     const uint32_t past = __ballot_sync(0xffffffffu, in && incl > target);
-    if (past ? lane != __ffs(past) - 1 : lane != 0) return;
-    const uint64_t before = incl - mine;
-    int at = N - 1;
-    for (int e = 0; e < N - 1; ++e)   // the first e whose sum up to it passes
-        if (before + vector_sum<T>(sh, a, c, r, v, q_row, out | (0xffffffffu << (e + 1))) > target) {
-            at = e;
-            break;
-        }
-    a.out_tokens[c.out] = (int32_t)min(v * N + at, a.V - 1);
+    const int at = past ? __ffs(past) - 1 : 0;   // the vector's lane; then a lane sums its elements up to the lane's own
+    r.x = __shfl_sync(0xffffffffu, r.x, at);
+    r.y = __shfl_sync(0xffffffffu, r.y, at);
+    r.z = __shfl_sync(0xffffffffu, r.z, at);
+    r.w = __shfl_sync(0xffffffffu, r.w, at);
+    out = __shfl_sync(0xffffffffu, out, at);
+    const uint64_t before = __shfl_sync(0xffffffffu, incl - mine, at);
+    const bool passes = before + vector_sum<T, Left>(sh, r, p.from + at, q_row, out | (0xfffffffeu << (lane & (N - 1)))) > target;
+    const uint32_t which = __ballot_sync(0xffffffffu, passes) & ((1u << N) - 1);
+    if (lane == 0)
+        out_tokens[sh.cmd.out] = (int32_t)min((p.from + at) * N + (which ? __ffs(which) - 1 : N - 1), sh.V - 1);
 }
 
 // What the lead's first warp knows of a child before the row's statistics are there.
@@ -523,7 +581,7 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
     last = -1;
     // The sum's bound: its exponents' roundings (2^-23 of each, weighted by weights that fall faster than exponents
     // grow), the exponentials (2^-22), the joins, this comparison, and 2^-24 an addition of a thread.
-    const F sum = Exact ? (F)ldexp((double)st.fixed, -a.frac) : (F)st.sum;
+    const F sum = Exact ? (F)ldexp((double)st.fixed(), -a.frac) : (F)st.sum;
     const F slack = Exact ? (F)0 : sum * ((F)0x1p-15f + (F)a.V / (F)(n_cta * kVThreads) * (F)0x1p-23f);
     F left = sum;
     int n_rejected = 0;
@@ -533,12 +591,12 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
         F w = 0;
         if (T_ > 0.f && k.is && k.token >= 0 && k.token < a.V) {
             if constexpr (Exact) {
-                uint64_t hi, lo;
-                weights2<T>(sh, k.x, k.x, st.top, hi, lo);
+                uint64_t ww, ee;
+                weights2<T>(sh, k.x, k.x, st.top, ww, ee);
                 float h, l, unused;
-                f2_split(hi, h, unused);
-                f2_split(lo, l, unused);
-                w = h > 0x1p-119f ? (F)h + (F)l : (F)0;
+                f2_split(ww, h, unused);
+                f2_split(ee, l, unused);
+                w = h > 0x1p-119f ? (F)h + (F)h * (F)l : (F)0;
             } else {
                 w = ex2((k.x - st.top) * sh.c_hi);
             }
@@ -579,14 +637,14 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVThreads, 2) k_verify(const __grid_constant__ VerifyArgs a) {
     __shared__ VShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int n_cta = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
     const int s = (int)(blockIdx.x / n_cta), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         dg::mbar_init(&sh.told, 1);
-        dg::mbar_init(&sh.parts, (uint32_t)n_cta);
+        dg::mbar_init(&sh.parts, 1);
         dg::fence_mbar_init();
     }
     if (tid < 32) {
@@ -607,6 +665,8 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
         sh.c_lo = (float)(c - (double)sh.c_hi);
         sh.d_min = -120.f / sh.c_hi;
         sh.n_gone = 0;
+        sh.V = a.V;
+        sh.frac = a.frac;
     }
     // The lead alone looks at what decides how often the cluster meets.
     int accepted = 0;
@@ -648,16 +708,19 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
         const float* q_row = c.draft >= 0 ? a.probs + (int64_t)(q0 + c.draft) * a.ldq : nullptr;
         Child k{false, -1, 0.f, 0.f, 0.f};
         if (cta == 0 && warp == 0 && walks) k = child_of<T>(sh, a, row, q0, ql, c.node, c.node + 1 + lane, T_);
-        Partial mine{-INFINITY, 0.f, 0x7fffffff, 0, 0};
+        Partial mine{-INFINITY, 0.f, 0x7fffffff, 0};
+        if (tid == 0) dg::mbar_arrive_expect_tx(cta == 0 ? &sh.parts : &sh.told, cta == 0 ? 16u * n_cta : (uint32_t)sizeof(Command));
         if (c.op == kStats) {
             if (ql > 0) mine = T_ > 0.f ? row_stats<T, true>(sh, row, a.V, cta, n_cta) : row_stats<T, false>(sh, row, a.V, cta, n_cta);
         } else {
-            mine = row_sums<T>(sh, row, a, c, q_row, cta, n_cta, q0, ql);
+            mine = c.op == kLeft ? row_sums<T, true>(sh, row, a, c, q_row, cta, n_cta, q0, ql)
+                                 : row_sums<T, false>(sh, row, a, c, nullptr, cta, n_cta, q0, ql);
         }
         if (meeting == 0) cluster.barrier_wait(std::move(arrived));
         if (tid == 0) {   // this CTA's part to the lead
-            cluster.map_shared_rank(&sh, 0)->part[cta] = mine;
-            arrive_cluster(dg::mapa_shared(&sh.parts, 0));
+            send16(dg::mapa_shared(&sh.part[cta], 0),
+                   make_uint4(__float_as_uint(mine.top), __float_as_uint(mine.sum), (uint32_t)mine.arg, (uint32_t)mine.bad),
+                   dg::mapa_shared(&sh.parts, 0));
         }
         if (cta != 0) {
             if (!dg::mbar_wait_cluster(&sh.told, meeting & 1u)) {
@@ -667,10 +730,6 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
             c = sh.cmd;
             if (c.op == kExit) break;
             if (c.op == kFind) {
-                if (cta == c.cta) {
-                    row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + c.node) * a.ld;
-                    find_token<T>(sh, row, a, c, c.draft >= 0 ? a.probs + (int64_t)(q0 + c.draft) * a.ldq : nullptr, cta, n_cta);
-                }
                 break;
             }
             continue;
@@ -690,7 +749,7 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
                                __float2ull_rz((u * 0x1p32f - truncf(u * 0x1p32f)) * 0x1p32f);
             uint64_t target = __umul64hi(sum, U);
             int owner = 0;
-            while (owner < n_cta - 1 && target >= sh.part[owner].fixed) target -= sh.part[owner++].fixed;
+            while (owner < n_cta - 1 && target >= sh.part[owner].fixed()) target -= sh.part[owner++].fixed();
             next = c;
             next.op = kFind;
             next.cta = owner;
@@ -698,14 +757,14 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
             next.out = q0 + accepted;
         };
         if (walks && c.op == kStats) {
-            Partial t{-INFINITY, 0.f, 0x7fffffff, 0, 0};
-            for (int i = 0; i < n_cta; ++i) t.top = fmaxf(t.top, sh.part[i].top);
-            const float at = t.top == -INFINITY ? 0.f : t.top;
-            for (int i = 0; i < n_cta; ++i) {
-                if (T_ > 0.f) t.sum += sh.part[i].sum * ex2((sh.part[i].top - at) * sh.c_hi);
-                if (sh.part[i].top == t.top) t.arg = min(t.arg, sh.part[i].arg);
-                t.bad |= sh.part[i].bad;
-            }
+            Partial t{-INFINITY, 0.f, 0x7fffffff, 0};
+            if (lane < n_cta) t = sh.part[lane];
+            t = T_ > 0.f ? join_stats<true, kMaxCluster>(t, sh.c_hi) : join_stats<false, kMaxCluster>(t, 0.f);
+            t.top = __shfl_sync(0xffffffffu, t.top, 0);   // (all lanes': the first half has joined)
+            t.sum = __shfl_sync(0xffffffffu, t.sum, 0);
+            t.arg = __shfl_sync(0xffffffffu, t.arg, 0);
+            t.bad = __shfl_sync(0xffffffffu, t.bad, 0);
+            if (T_ > 0.f) t.bad = 0;
             stats = t;
             const bool nan = t.bad || !(t.top < INFINITY) || !(t.sum < INFINITY);
             if (nan || t.top == -INFINITY) {
@@ -714,8 +773,8 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
             }
         } else if (walks) {
             uint64_t f = 0;
-            for (int i = 0; i < n_cta; ++i) f += sh.part[i].fixed;
-            stats.fixed = f;
+            for (int i = 0; i < n_cta; ++i) f += sh.part[i].fixed();
+            stats.set_fixed(f);
         }
         if (!finish && (c.op == kStats || (c.op == kSum && c.minus < 0))) {   // (minus -1: a sum asked for by a decision)
             if (warp == 0) {
@@ -750,30 +809,31 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
             }
         } else if (!finish && c.op == kSum) {
             if (a.probs && rejected >= 0) {
-                const double w = ldexp((double)stats.fixed, -a.frac);
+                const double w = ldexp((double)stats.fixed(), -a.frac);
                 next.op = kLeft;
                 next.draft = rejected;
                 next.w_hi = (float)w;
                 next.w_lo = (float)(w - (double)next.w_hi);
-            } else if (c.minus > 0 && stats.fixed == 0) {
+            } else if (c.minus > 0 && stats.fixed() == 0) {
                 next.op = kSum;          // nothing is left: all of the row again
             } else {
-                draw_from(stats.fixed);
+                draw_from(stats.fixed());
             }
         } else if (!finish) {            // kLeft
-            if (stats.fixed == 0) {      // nothing is left: the row itself, whose sums are made again
+            if (stats.fixed() == 0) {      // nothing is left: the row itself, whose sums are made again
                 rejected = -1;
                 next.op = kSum;
             } else {
-                draw_from(stats.fixed);
+                draw_from(stats.fixed());
             }
         }
         if (finish) next.op = kExit;
         __syncthreads();   // the parts are read: the next ones may come
         if (tid > 0 && tid < n_cta) {
-            VShared* to = cluster.map_shared_rank(&sh, tid);
-            to->cmd = next;
-            arrive_cluster(dg::mapa_shared(&sh.told, (uint32_t)tid));
+            const uint4* words = reinterpret_cast<const uint4*>(&next);
+            const uint32_t to = dg::mapa_shared(&sh.cmd, (uint32_t)tid), bar = dg::mapa_shared(&sh.told, (uint32_t)tid);
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(Command) / 16); ++i) send16(to + 16 * i, words[i], bar);
         }
         if (walks && (next.op == kExit || next.op == kFind)) {   // the walk's outputs
             for (int i = tid; i < ql; i += kVThreads) {
@@ -787,14 +847,20 @@ __global__ void __launch_bounds__(kVThreads, 2) k_verify(const VerifyArgs a) {
         }
         if (next.op == kExit) break;
         if (next.op == kFind) {
-            if (next.cta == 0) {
-                row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + next.node) * a.ld;
-                find_token<T>(sh, row, a, next, next.draft >= 0 ? a.probs + (int64_t)(q0 + next.draft) * a.ldq : nullptr, 0, n_cta);
-            }
+            c = next;
+            if (tid == 0) sh.cmd = next;
+            __syncthreads();
             break;
         }
         c = next;
+        if (tid == 0) sh.cmd = next;
     }
+    if (c.op != kFind || c.cta != cta) return;
+    const T* row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + c.node) * a.ld;
+    if (c.draft >= 0)
+        find_token<T, true>(sh, row, a.probs + (int64_t)(q0 + c.draft) * a.ldq, cta, n_cta, a.out_tokens);
+    else
+        find_token<T, false>(sh, row, nullptr, cta, n_cta, a.out_tokens);
 }
 
 // ------------------------------------------------------------------ kept paths
