@@ -42,7 +42,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // added exactly from there on, whatever the order.
 // Acceptance compares fp32 sums, unless they come within their own bound of the border: then the row is summed
 // like the last one (kSum) and compared again.
-constexpr int kVThreads = 256, kVWarps = kVThreads / 32;
+constexpr int kVThreads = 128, kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxNodes = 1024;
 constexpr int kSegments = 64;      // that a part is searched in at a time
@@ -637,7 +637,7 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVThreads, 2) k_verify(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVThreads, 4) k_verify(const __grid_constant__ VerifyArgs a) {
     __shared__ VShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int n_cta = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
@@ -995,7 +995,7 @@ extern "C" dg_status dg_verify_drafts(const void* logits, dg_dtype dtype, int64_
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
     int cluster = 8;
-    while (cluster > 1 && (int64_t)n_seq * cluster > 2 * (int64_t)sms) cluster /= 2;
+    while (cluster > 1 && (int64_t)n_seq * cluster > 4 * (int64_t)sms) cluster /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)n_seq * cluster);
     cfg.blockDim = dim3(kVThreads);
