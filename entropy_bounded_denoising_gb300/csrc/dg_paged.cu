@@ -42,15 +42,6 @@ struct AppendArgs {
     unsigned* status;
 };
 
-// With norms of the heads and rows' own positions (dg_kv_append_norm).
-struct NormArgs : AppendArgs {
-    const float* norm[2];      // of queries and of keys; null: not normed
-    const int32_t* positions;  // null: the slots' numbers
-    float eps;
-};
-template <bool Norm>
-using ArgsOf = std::conditional_t<Norm, NormArgs, AppendArgs>;
-
 struct Task {
     int row, head;   // row of the unit; heads in order: key heads, value heads, query heads
     int at, dist;    // the first chunk's dimension, and how far behind it the second one lies
@@ -90,50 +81,6 @@ DG_DEVINL void rotate_neighbours(uint4& x, const float2* cs) {
         const float u = lo_f(a[e]), w = hi_f(a[e]);
         a[e] = pack_bf16x2(u * c.x - w * c.y, u * c.y + w * c.x);
     }
-}
-
-// The sixteen values of a task as floats, and back.
-DG_DEVINL void unpack16(const uint4& x, const uint4& y, float (&f)[16]) {
-    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        f[2 * e] = lo_f(w[e]);
-        f[2 * e + 1] = hi_f(w[e]);
-    }
-}
-DG_DEVINL void pack16(const float (&f)[16], uint4& x, uint4& y) {
-    x = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-    y = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
-}
-
-// The sum over a head's 2^head_shift lanes, which lie side by side.
-DG_DEVINL float head_sum(float v, int head_shift) {
-    for (int o = 1; o < (1 << head_shift); o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-// f / sqrt(mean f^2 + eps) over a head.  A sum of squares past fp32 (values from 2^60 on) is taken of values 2^-70 as large,
-// beside which eps is nothing.  (Whole warp; squares below fp32 are below eps, which is at least 2^-126.)
-DG_DEVINL void norm_head(float (&f)[16], int head_shift, int D, float eps) {
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
-    ss = head_sum(ss, head_shift);
-    const bool large = !(ss <= 0x1p120f);   // (a NaN is rid of nothing here)
-    if (__any_sync(0xffffffffu, large)) {
-        const float s = large ? 0x1p-70f : 1.f;
-        eps = large ? eps * 0x1p-140f : eps;
-        ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            f[e] *= s;
-            ss = fmaf(f[e], f[e], ss);
-        }
-        ss = head_sum(ss, head_shift);
-    }
-    const float r = rsqrtf(ss / (float)D + eps);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) f[e] *= r;
 }
 
 // w radians as a fraction of a turn in 64-bit fixed point: floor(w / (2 pi) 2^64) mod 2^64, within two units of the
@@ -187,18 +134,13 @@ DG_DEVINL int row_position(const AppendArgs& a, int t, int s) {
 // place at once; four where there are several rounds of blocks (more bytes on the way and fewer lookups
 // a byte).  One against four, the same rows again and again: 64 rows 3.4 and 5.1 us, 2048 rows 8.4 and 8.2, the 30k
 // rows 154 and 138.
-//
-// Norm (dg_kv_append_norm): a head's D / 16 lanes add up its squares; its values stay in fp32 from the norm through the
-// rotation.
-template <bool Interleaved, int PerThread, bool Norm>
-__global__ void __launch_bounds__(kAppendThreads, Norm || PerThread == 4 ? 4 : 8) k_kv_append(const ArgsOf<Norm> a) {
+template <bool Interleaved, int PerThread>
+__global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_append(const AppendArgs a) {
     constexpr int kPerThread = PerThread, kUnit = kAppendThreads * PerThread;   // tasks of a block
     constexpr int kRows = kUnit / 8 + 2;       // rows of a unit: at least 8 tasks each (one key head of 64)
     __shared__ int64_t place[kRows];           // cache offset of a row's slot, -1 = skipped
     __shared__ int32_t position[kRows];
     __shared__ float2 cs[kUnit * 4 + 2 * 128]; // cosine and sine of its angles
-    __shared__ int32_t turn_by[Norm ? kRows : 1];            // its position as the rotation takes it
-    __shared__ __align__(16) float weight[Norm ? 512 : 4];   // of queries, of keys
     dg::pdl_wait();
     dg::pdl_release();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -252,13 +194,6 @@ __global__ void __launch_bounds__(kAppendThreads, Norm || PerThread == 4 ? 4 : 8
     if (mine >= 0) {
         p = row_position(a, (int)(row0 + mine), owner);
         position[mine] = p;
-        if constexpr (Norm) turn_by[mine] = a.positions ? a.positions[row0 + mine] : p;
-    }
-    if constexpr (Norm) {
-        for (int i = tid; i < 2 * a.D; i += kAppendThreads) {
-            const float* w = a.norm[i >= a.D];
-            weight[i] = w ? w[i >= a.D ? i - a.D : i] : 0.f;
-        }
     }
     __syncthreads();
     if (mine >= 0) {
@@ -275,7 +210,7 @@ __global__ void __launch_bounds__(kAppendThreads, Norm || PerThread == 4 ? 4 : 8
     for (int i = tid; i < rows * half; i += kAppendThreads) {
         const int r = i / half;
         const double w = i == tid ? w0 : a.inv_freq[i - r * half];
-        const int64_t u = (int64_t)(turns_of(w) * (uint64_t)(Norm ? turn_by : position)[r]);
+        const int64_t u = (int64_t)(turns_of(w) * (uint64_t)position[r]);
         float sn, c;
         sincospif((float)u * 1.0842021724855044e-19f, &sn, &c);  // 2^-63: half turns in [-1, 1]
         cs[i] = make_float2(c, sn);
@@ -284,50 +219,8 @@ __global__ void __launch_bounds__(kAppendThreads, Norm || PerThread == 4 ? 4 : 8
 #pragma unroll
     for (int u = 0; u < kPerThread; ++u) {
         const Task k = task_of(a, skip + u * kAppendThreads + tid);
-        if constexpr (Norm) {   // (a head's lanes have one row and are of one head: they go the same ways)
-            const bool key = k.head < a.Hkv, in = k.row < rows && (key || k.head >= 2 * a.Hkv);
-            const bool normed = in && a.norm[key ? 1 : 0];
-            if (__any_sync(0xffffffffu, in)) {
-                float f[16];
-                unpack16(x[u], y[u], f);
-                if (!in) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = 0.f;
-                }
-                if (__any_sync(0xffffffffu, normed)) {
-                    float n[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) n[e] = f[e];
-                    norm_head(n, a.head_shift, a.D, a.eps);
-                    const float4* w = reinterpret_cast<const float4*>(weight + (key ? a.D : 0));
-                    if (normed) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float4 v = w[(k.at + (c < 2 ? 0 : k.dist)) / 4 + (c & 1)];
-                            f[4 * c] = n[4 * c] * v.x;
-                            f[4 * c + 1] = n[4 * c + 1] * v.y;
-                            f[4 * c + 2] = n[4 * c + 2] * v.z;
-                            f[4 * c + 3] = n[4 * c + 3] * v.w;
-                        }
-                    }
-                }
-                if (in && k.turn) {
-                    const float2* c = cs + k.row * half + (Interleaved ? k.at / 2 : k.at);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        // pair e: dimensions e of both chunks, or two neighbours of the first (4 pairs) or second chunk
-                        const int i = Interleaved ? 2 * e : e, j = Interleaved ? 2 * e + 1 : e + 8;
-                        const float2 z = Interleaved && e >= 4 ? c[half / 2 + e - 4] : c[e];
-                        const float p0 = f[i], p1 = f[j];
-                        f[i] = p0 * z.x - p1 * z.y;
-                        f[j] = p0 * z.y + p1 * z.x;
-                    }
-                }
-                if (normed || (in && k.turn)) pack16(f, x[u], y[u]);
-            }
-        }
         if (k.row >= rows || place[k.row] < 0) continue;
-        if (!Norm && k.turn) {
+        if (k.turn) {
             const float2* c = cs + k.row * half;
             if (Interleaved) {
                 rotate_neighbours(x[u], c + k.at / 2);
@@ -342,6 +235,213 @@ __global__ void __launch_bounds__(kAppendThreads, Norm || PerThread == 4 ? 4 : 8
         *reinterpret_cast<uint4*>(dst + k.at) = x[u];
         *reinterpret_cast<uint4*>(dst + k.at + k.dist) = y[u];
     }
+}
+
+// ------------------------------------------------------------------ append with norms
+// A warp owns up to T groups of 32 / (D / 16) heads of one row: a head's D / 16 lanes hold 32 bytes each, two chunks as in a
+// task of the append, and the same dimensions in every group, so that a lane reads its cosines and sines once a
+// warp and its weights where it lies in a line with its neighbours.  The data is asked for first; the row's sequence and slot
+// are looked up and its sines computed while it is on the way, by the warp itself: nothing waits for a block.
+// Values stay in fp32 from the norm through the rotation.
+struct NormArgs : AppendArgs {
+    const float* norm[2];      // of keys and of queries; null: not normed
+    const int32_t* positions;  // null: the slots' numbers
+    float eps;
+    int32_t groups, chunks;    // groups of heads in a row, and warps that they take
+};
+constexpr int kNormWarps = 8;
+
+// The sixteen values of a task as floats, and back.
+DG_DEVINL void unpack16(const uint4& x, const uint4& y, float (&f)[16]) {
+    const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[2 * e] = lo_f(w[e]);
+        f[2 * e + 1] = hi_f(w[e]);
+    }
+}
+DG_DEVINL void pack16(const float (&f)[16], uint4& x, uint4& y) {
+    x = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    y = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]), pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
+}
+
+// The sum over a head's lanes, which lie side by side.
+template <int Lanes>
+DG_DEVINL float head_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < Lanes; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// 1 / sqrt(mean f^2 + eps) over a head.  A sum of squares past fp32 (values from 2^60 on) is taken of values 2^-70 as large,
+// beside which eps is nothing; f is then scaled.  (Whole warp; squares below fp32 are below eps, at least 2^-126.)
+template <int D>
+DG_DEVINL float norm_of(float (&f)[16], float eps) {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+        s0 = fmaf(f[e], f[e], s0);
+        s1 = fmaf(f[e + 1], f[e + 1], s1);
+    }
+    float ss = head_sum<D / 16>(s0 + s1);
+    const bool large = !(ss <= 0x1p120f);   // (or a NaN, which stays one)
+    if (__any_sync(0xffffffffu, large)) {
+        if (large) {
+            eps *= 0x1p-140f;
+            ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                f[e] *= 0x1p-70f;
+                ss = fmaf(f[e], f[e], ss);
+            }
+        }
+        const float again = head_sum<D / 16>(ss);
+        ss = large ? again : ss;
+    }
+    return rsqrtf(fmaf(ss, 1.f / D, eps));
+}
+
+template <bool Interleaved, int D, int T>
+__global__ void __launch_bounds__(kNormWarps * 32, T == 1 ? 4 : 2) k_kv_append_norm(const __grid_constant__ NormArgs a) {
+    constexpr int G = D / 16, Heads = 32 / G;   // lanes of a head, heads of a group
+    __shared__ float4 weight[2][4][G];          // [keys, queries][quarter of a lane's values][lane of the head]
+    __shared__ float4 turns[kNormWarps][4][G];  // a row's cosines and sines: [pairs 2 e, 2 e + 1 of a lane][lane]
+    dg::pdl_wait();
+    dg::pdl_release();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // every sequence and frequency is checked by blocks of their own, as in the append
+    if (blockIdx.x >= a.row_blocks) {
+        const int s = (int)(blockIdx.x - a.row_blocks) * (kNormWarps * 32) + tid;
+        if ((s < a.n_seq && !dg::paged_seq(a.kv, a.cu_q, a.total_q, s, 0x7fffffff).ok) ||
+            (s < a.rot / 2 && !has_angle(a.inv_freq[s])))
+            dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+        return;
+    }
+    const int64_t task = (int64_t)blockIdx.x * kNormWarps + warp;
+    int64_t row;
+    int g0 = 0;       // the first group
+    if (a.chunks == 1) {
+        row = task;
+    } else {
+        row = a.narrow ? (int64_t)((uint32_t)task / (uint32_t)a.chunks) : task / a.chunks;
+        g0 = (int)(task - row * a.chunks) * T;
+    }
+    const bool real = row < a.total_q;
+    const int tt = lane % G, sub = lane / G, half = a.rot / 2, heads = 2 * a.Hkv + (a.q ? a.Hq : 0);
+    const bool turn = tt < a.rot / 16;
+    const int at = turn ? tt * 8 : a.rot + (tt - a.rot / 16) * 8, dist = turn ? a.rot / 2 : (D - a.rot) / 2;
+    // a value head lies in chunks half a head apart; its lanes read it so
+    uint4 x[T], y[T];
+#pragma unroll
+    for (int u = 0; u < T; ++u) {
+        const int h = (g0 + u) * Heads + sub;
+        x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (real && h < heads) {
+            const bool value = h >= a.Hkv && h < 2 * a.Hkv;
+            const uint16_t* src = h < a.Hkv       ? a.k + row * a.ldk + (int64_t)h * D
+                                  : value         ? a.v + row * a.ldv + (int64_t)(h - a.Hkv) * D
+                                                  : a.q + row * a.ldq + (int64_t)(h - 2 * a.Hkv) * D;
+            x[u] = *reinterpret_cast<const uint4*>(src + (value ? tt * 8 : at));
+            y[u] = *reinterpret_cast<const uint4*>(src + (value ? tt * 8 + D / 2 : at + dist));
+        }
+    }
+    // the weights in the order in which lanes take them
+    for (int i = tid; i < 8 * G; i += kNormWarps * 32) {
+        const int which = i / (4 * G), c = i / G & 3, l = i % G;
+        const bool tl = l < a.rot / 16;
+        const int al = (tl ? l * 8 : a.rot + (l - a.rot / 16) * 8) + (c & 1) * 4 + (c < 2 ? 0 : tl ? a.rot / 2 : (D - a.rot) / 2);
+        const float* w = a.norm[which];
+        if (w) weight[which][c][l] = make_float4(w[al], w[al + 1], w[al + 2], w[al + 3]);
+    }
+    // the row's place and angles
+    int64_t place = -1;
+    int by = 0;
+    if (real) {
+        const int s = dg::warp_owner(a.cu_q, a.n_seq, (int)row);
+        const int p = row_position(a, (int)row, s);
+        by = a.positions ? a.positions[row] : p;
+        if (p >= 0) {
+            const int32_t page = a.kv.page_table[(int64_t)s * a.kv.max_pages + (p >> a.kv.page_shift)];
+            if (page < 0 || page >= a.kv.n_pages) {
+                if (lane == 0) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
+            } else {
+                place = page * a.kv.page_stride + (p & ((1 << a.kv.page_shift) - 1)) * a.kv.slot_stride;
+            }
+        }
+        for (int j = lane; j < half; j += 32) {
+            const int64_t u = (int64_t)(turns_of(a.inv_freq[j]) * (uint64_t)(int64_t)by);
+            float sn, c;
+            sincospif((float)u * 1.0842021724855044e-19f, &sn, &c);  // 2^-63: half turns in [-1, 1]
+            // pair j is a lane's e-th: dimensions e of both its chunks, or neighbours, four pairs a chunk
+            const int second = Interleaved && j >= half / 2, jj = second ? j - half / 2 : j;
+            const int l = Interleaved ? jj / 4 : jj / 8, e = Interleaved ? jj % 4 + 4 * second : jj % 8;
+            reinterpret_cast<float2*>(&turns[warp][e / 2][l])[e & 1] = make_float2(c, sn);
+        }
+    }
+    __syncthreads();   // the weights; and a warp's own turns
+    if (place < 0) return;   // (the whole warp: it has one row)
+#pragma unroll
+    for (int u = 0; u < T; ++u) {
+        if ((g0 + u) * Heads >= heads) break;
+        const int h = (g0 + u) * Heads + sub;
+        const bool key = h < a.Hkv, value = !key && h < 2 * a.Hkv;
+        const bool normed = !value && a.norm[key ? 0 : 1], turned = !value && turn;
+        if (__any_sync(0xffffffffu, normed || turned)) {
+            float f[16];
+            unpack16(x[u], y[u], f);
+            if (__any_sync(0xffffffffu, normed)) {
+                float n[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) n[e] = f[e];
+                const float r = norm_of<D>(n, a.eps);
+                if (normed) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float4 w = weight[key ? 0 : 1][c][tt];
+                        f[4 * c] = n[4 * c] * r * w.x;
+                        f[4 * c + 1] = n[4 * c + 1] * r * w.y;
+                        f[4 * c + 2] = n[4 * c + 2] * r * w.z;
+                        f[4 * c + 3] = n[4 * c + 3] * r * w.w;
+                    }
+                }
+            }
+            if (turned) {
+#pragma unroll
+                for (int e2 = 0; e2 < 4; ++e2) {
+                    const float4 z = turns[warp][e2][tt];
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const int e = 2 * e2 + o, i = Interleaved ? 2 * e : e, j = Interleaved ? 2 * e + 1 : e + 8;
+                        const float c = o ? z.z : z.x, sn = o ? z.w : z.y, p0 = f[i], p1 = f[j];
+                        f[i] = p0 * c - p1 * sn;
+                        f[j] = p0 * sn + p1 * c;
+                    }
+                }
+            }
+            if (normed || turned) pack16(f, x[u], y[u]);
+        }
+        if (h >= heads) continue;
+        uint16_t* dst = key     ? a.kv.k + place + h * a.kv.head_stride
+                        : value ? a.kv.v + place + (h - a.Hkv) * a.kv.head_stride
+                                : a.q_out + (row * a.Hq + (h - 2 * a.Hkv)) * D;
+        *reinterpret_cast<uint4*>(dst + (value ? tt * 8 : at)) = x[u];
+        *reinterpret_cast<uint4*>(dst + (value ? tt * 8 + D / 2 : at + dist)) = y[u];
+    }
+}
+
+template <bool Interleaved, int D>
+cudaError_t launch_norm(NormArgs& a, bool small, cudaStream_t stream) {
+    constexpr int T = 8;
+    a.groups = ((a.q ? a.Hq : 0) + 2 * a.Hkv + 512 / D - 1) / (512 / D);
+    a.chunks = small ? a.groups : (a.groups + T - 1) / T;
+    const int64_t tasks = a.total_q * a.chunks;
+    a.narrow = tasks < (1LL << 31);
+    const int64_t row_blocks = (tasks + kNormWarps - 1) / kNormWarps;
+    const int64_t blocks = row_blocks + (std::max(a.n_seq, a.rot / 2) + kNormWarps * 32 - 1) / (kNormWarps * 32);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    a.row_blocks = (uint32_t)row_blocks;
+    return dghost::launch_pdl(small ? k_kv_append_norm<Interleaved, D, 1> : k_kv_append_norm<Interleaved, D, T>,
+                              dim3((unsigned)blocks), dim3(kNormWarps * 32), 0, stream, a);
 }
 
 }  // namespace
@@ -381,31 +481,29 @@ dg_status paged_kv(const dg_paged_kv* cache, int32_t D, dg::PagedKV* c) {
 
 namespace {
 
-// Checks and launch shared by dg_kv_append and dg_kv_append_norm.
-template <bool Norm>
-dg_status append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q, int64_t ldq,
-                 uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q, int32_t Hq, int32_t Hkv,
-                 int32_t D, const float* q_norm, const float* k_norm, float eps, const int32_t* positions,
-                 const double* inv_freq, int32_t rot_dim, int32_t interleaved, const dg_paged_kv* cache,
-                 dg_stream_t stream) {
+// Checks and arguments shared by dg_kv_append and dg_kv_append_norm; false: `rc` is the answer.
+bool append_args(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q, int64_t ldq,
+                 uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q, int32_t Hq, int32_t Hkv, int32_t D,
+                 const double* inv_freq, int32_t rot_dim, const dg_paged_kv* cache, AppendArgs& a, dg_status& rc) {
+    auto answer = [&](dg_status s) {
+        rc = s;
+        return false;
+    };
     if (n_seq < 0 || n_seq > 65535 || total_q < 0 || total_q >= (1LL << 31) || Hq < 1 || Hq > 65535 || Hkv < 1 ||
         Hkv > 65535)
-        return DG_ERR_INVALID_ARG;
-    if (D != 64 && D != 128 && D != 256) return DG_ERR_UNSUPPORTED;
-    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 || (rot_dim > 0 && !inv_freq)) return DG_ERR_INVALID_ARG;
-    if ((q_norm || k_norm) && !(eps >= 0x1p-126f && eps < INFINITY)) return DG_ERR_INVALID_ARG;
-    if (n_seq == 0 || total_q == 0) return DG_OK;
-    if (!k || !v || !cu_q || (q != nullptr) != (q_out != nullptr) || (q_norm && !q)) return DG_ERR_INVALID_ARG;
-    if (ldk < (int64_t)Hkv * D || ldv < (int64_t)Hkv * D || (q && ldq < (int64_t)Hq * D)) return DG_ERR_INVALID_ARG;
-    if (ldk >= (1LL << 31) || ldv >= (1LL << 31) || (q && ldq >= (1LL << 31))) return DG_ERR_INVALID_ARG;
-    if (q && q_out == q && ldq != (int64_t)Hq * D) return DG_ERR_INVALID_ARG;
+        return answer(DG_ERR_INVALID_ARG);
+    if (D != 64 && D != 128 && D != 256) return answer(DG_ERR_UNSUPPORTED);
+    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 || (rot_dim > 0 && !inv_freq)) return answer(DG_ERR_INVALID_ARG);
+    if (n_seq == 0 || total_q == 0) return answer(DG_OK);
+    if (!k || !v || !cu_q || (q != nullptr) != (q_out != nullptr)) return answer(DG_ERR_INVALID_ARG);
+    if (ldk < (int64_t)Hkv * D || ldv < (int64_t)Hkv * D || (q && ldq < (int64_t)Hq * D)) return answer(DG_ERR_INVALID_ARG);
+    if (ldk >= (1LL << 31) || ldv >= (1LL << 31) || (q && ldq >= (1LL << 31))) return answer(DG_ERR_INVALID_ARG);
+    if (q && q_out == q && ldq != (int64_t)Hq * D) return answer(DG_ERR_INVALID_ARG);
     if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))) || ldk % 8 || ldv % 8 ||
-        (q && ldq % 8) || !dghost::on_multiple(cu_q, 4) || !dghost::on_multiple(inv_freq, 8) ||
-        !dghost::on_multiple(q_norm, 4) || !dghost::on_multiple(k_norm, 4) || !dghost::on_multiple(positions, 4))
-        return DG_ERR_ALIGNMENT;
-    ArgsOf<Norm> a;
+        (q && ldq % 8) || !dghost::on_multiple(cu_q, 4) || !dghost::on_multiple(inv_freq, 8))
+        return answer(DG_ERR_ALIGNMENT);
     const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
-    if (ok != DG_OK) return ok;
+    if (ok != DG_OK) return answer(ok);
     a.k = k;
     a.v = v;
     a.q = q;
@@ -425,26 +523,7 @@ dg_status append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
     a.head_shift = D == 64 ? 2 : D == 128 ? 3 : 4;
     a.status = dghost::status_word();
     a.narrow = total_q * a.tasks < (1LL << 31);
-    if constexpr (Norm) {
-        a.norm[0] = q_norm;
-        a.norm[1] = k_norm;
-        a.positions = positions;
-        a.eps = eps;
-    }
-    const int sms = dghost::sm_count();
-    if (sms <= 0) return DG_ERR_CUDA;
-    const bool one = total_q * a.tasks <= (int64_t)sms * 2048;
-    const int64_t unit = one ? kAppendThreads : kAppendThreads * 4;
-    const int64_t row_blocks = (total_q * a.tasks + unit - 1) / unit;
-    const int64_t blocks = row_blocks + (n_seq + kAppendThreads - 1) / kAppendThreads;
-    if (blocks > 0x7fffffffLL) return DG_ERR_INVALID_ARG;
-    a.row_blocks = (uint32_t)row_blocks;
-    const cudaError_t e =
-        dghost::launch_pdl(one ? (interleaved ? k_kv_append<true, 1, Norm> : k_kv_append<false, 1, Norm>)
-                               : (interleaved ? k_kv_append<true, 4, Norm> : k_kv_append<false, 4, Norm>),
-                           dim3((unsigned)blocks), dim3(kAppendThreads), 0, (cudaStream_t)stream, a);
-    dghost::count_launch();
-    return dghost::cuda_status(e);
+    return true;
 }
 
 }  // namespace
@@ -453,8 +532,22 @@ extern "C" dg_status dg_kv_append(const uint16_t* k, int64_t ldk, const uint16_t
                                   int64_t ldq, uint16_t* q_out, const int32_t* cu_q, int32_t n_seq, int64_t total_q,
                                   int32_t Hq, int32_t Hkv, int32_t D, const double* inv_freq, int32_t rot_dim,
                                   int32_t interleaved, const dg_paged_kv* cache, dg_stream_t stream) {
-    return append<false>(k, ldk, v, ldv, q, ldq, q_out, cu_q, n_seq, total_q, Hq, Hkv, D, nullptr, nullptr, 0.f, nullptr,
-                         inv_freq, rot_dim, interleaved, cache, stream);
+    AppendArgs a;
+    dg_status rc;
+    if (!append_args(k, ldk, v, ldv, q, ldq, q_out, cu_q, n_seq, total_q, Hq, Hkv, D, inv_freq, rot_dim, cache, a, rc)) return rc;
+    const int sms = dghost::sm_count();
+    if (sms <= 0) return DG_ERR_CUDA;
+    const bool one = total_q * a.tasks <= (int64_t)sms * 2048;
+    const int64_t unit = one ? kAppendThreads : kAppendThreads * 4;
+    const int64_t row_blocks = (total_q * a.tasks + unit - 1) / unit;
+    const int64_t blocks = row_blocks + (n_seq + kAppendThreads - 1) / kAppendThreads;
+    if (blocks > 0x7fffffffLL) return DG_ERR_INVALID_ARG;
+    a.row_blocks = (uint32_t)row_blocks;
+    const cudaError_t e = dghost::launch_pdl(one ? (interleaved ? k_kv_append<true, 1> : k_kv_append<false, 1>)
+                                                 : (interleaved ? k_kv_append<true, 4> : k_kv_append<false, 4>),
+                                             dim3((unsigned)blocks), dim3(kAppendThreads), 0, (cudaStream_t)stream, a);
+    dghost::count_launch();
+    return dghost::cuda_status(e);
 }
 
 extern "C" dg_status dg_kv_append_norm(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, const uint16_t* q,
@@ -462,6 +555,29 @@ extern "C" dg_status dg_kv_append_norm(const uint16_t* k, int64_t ldk, const uin
                                        int32_t Hq, int32_t Hkv, int32_t D, const float* q_norm, const float* k_norm,
                                        float eps, const int32_t* positions, const double* inv_freq, int32_t rot_dim,
                                        int32_t interleaved, const dg_paged_kv* cache, dg_stream_t stream) {
-    return append<true>(k, ldk, v, ldv, q, ldq, q_out, cu_q, n_seq, total_q, Hq, Hkv, D, q_norm, k_norm, eps, positions,
-                        inv_freq, rot_dim, interleaved, cache, stream);
+    if ((q_norm || k_norm) && !(eps >= 0x1p-126f && eps < INFINITY)) return DG_ERR_INVALID_ARG;
+    NormArgs a;
+    dg_status rc;
+    if (!append_args(k, ldk, v, ldv, q, ldq, q_out, cu_q, n_seq, total_q, Hq, Hkv, D, inv_freq, rot_dim, cache, a, rc)) return rc;
+    if (q_norm && !q) return DG_ERR_INVALID_ARG;
+    if (!dghost::on_multiple(q_norm, 4) || !dghost::on_multiple(k_norm, 4) || !dghost::on_multiple(positions, 4))
+        return DG_ERR_ALIGNMENT;
+    a.norm[0] = k_norm;
+    a.norm[1] = q_norm;
+    a.positions = positions;
+    a.eps = eps;
+    const int sms = dghost::sm_count();
+    if (sms <= 0) return DG_ERR_CUDA;
+    const bool small = total_q * a.tasks <= (int64_t)sms * 2048;
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (D == 64)
+        e = interleaved ? launch_norm<true, 64>(a, small, st) : launch_norm<false, 64>(a, small, st);
+    else if (D == 128)
+        e = interleaved ? launch_norm<true, 128>(a, small, st) : launch_norm<false, 128>(a, small, st);
+    else
+        e = interleaved ? launch_norm<true, 256>(a, small, st) : launch_norm<false, 256>(a, small, st);
+    if (e == cudaErrorInvalidConfiguration) return DG_ERR_INVALID_ARG;
+    dghost::count_launch();
+    return dghost::cuda_status(e);
 }
