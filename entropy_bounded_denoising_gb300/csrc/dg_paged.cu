@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "dg_paged.cuh"
@@ -249,7 +250,7 @@ struct NormArgs : AppendArgs {
     float eps;
     int32_t groups, chunks;    // groups of heads in a row, and warps that they take
 };
-constexpr int kNormWarps = 8;
+constexpr int kNormWarps = 4;
 
 // The sixteen values of a task as floats, and back.
 DG_DEVINL void unpack16(const uint4& x, const uint4& y, float (&f)[16]) {
@@ -301,9 +302,14 @@ DG_DEVINL float norm_of(float (&f)[16], float eps) {
     return rsqrtf(fmaf(ss, 1.f / D, eps));
 }
 
+DG_DEVINL void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dg::smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <bool Interleaved, int D, int T>
-__global__ void __launch_bounds__(kNormWarps * 32, T == 1 ? 4 : 2) k_kv_append_norm(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kNormWarps * 32, T == 1 ? 8 : 6) k_kv_append_norm(const __grid_constant__ NormArgs a) {
     constexpr int G = D / 16, Heads = 32 / G;   // lanes of a head, heads of a group
+    extern __shared__ uint4 norm_data[];        // [warp][group][chunk][lane]: the data on its way (in registers: 16 warps an SM for 24)
     __shared__ float4 weight[2][4][G];          // [keys, queries][quarter of a lane's values][lane of the head]
     __shared__ float4 turns[kNormWarps][4][G];  // a row's cosines and sines: [pairs 2 e, 2 e + 1 of a lane][lane]
     dg::pdl_wait();
@@ -331,20 +337,20 @@ __global__ void __launch_bounds__(kNormWarps * 32, T == 1 ? 4 : 2) k_kv_append_n
     const bool turn = tt < a.rot / 16;
     const int at = turn ? tt * 8 : a.rot + (tt - a.rot / 16) * 8, dist = turn ? a.rot / 2 : (D - a.rot) / 2;
     // a value head lies in chunks half a head apart; its lanes read it so
-    uint4 x[T], y[T];
+    uint4* const data = norm_data + warp * (T * 64) + lane;
 #pragma unroll
     for (int u = 0; u < T; ++u) {
         const int h = (g0 + u) * Heads + sub;
-        x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
         if (real && h < heads) {
             const bool value = h >= a.Hkv && h < 2 * a.Hkv;
             const uint16_t* src = h < a.Hkv       ? a.k + row * a.ldk + (int64_t)h * D
                                   : value         ? a.v + row * a.ldv + (int64_t)(h - a.Hkv) * D
                                                   : a.q + row * a.ldq + (int64_t)(h - 2 * a.Hkv) * D;
-            x[u] = *reinterpret_cast<const uint4*>(src + (value ? tt * 8 : at));
-            y[u] = *reinterpret_cast<const uint4*>(src + (value ? tt * 8 + D / 2 : at + dist));
+            cp_async16(data + u * 64, src + (value ? tt * 8 : at));
+            cp_async16(data + u * 64 + 32, src + (value ? tt * 8 + D / 2 : at + dist));
         }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     // the weights in the order in which lanes take them
     for (int i = tid; i < 8 * G; i += kNormWarps * 32) {
         const int which = i / (4 * G), c = i / G & 3, l = i % G;
@@ -378,17 +384,23 @@ __global__ void __launch_bounds__(kNormWarps * 32, T == 1 ? 4 : 2) k_kv_append_n
             reinterpret_cast<float2*>(&turns[warp][e / 2][l])[e & 1] = make_float2(c, sn);
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();   // the weights; and a warp's own turns
     if (place < 0) return;   // (the whole warp: it has one row)
-#pragma unroll
+#pragma unroll 1
     for (int u = 0; u < T; ++u) {
         if ((g0 + u) * Heads >= heads) break;
         const int h = (g0 + u) * Heads + sub;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+        if (h < heads) {
+            x = data[u * 64];
+            y = data[u * 64 + 32];
+        }
         const bool key = h < a.Hkv, value = !key && h < 2 * a.Hkv;
         const bool normed = !value && a.norm[key ? 0 : 1], turned = !value && turn;
         if (__any_sync(0xffffffffu, normed || turned)) {
             float f[16];
-            unpack16(x[u], y[u], f);
+            unpack16(x, y, f);
             if (__any_sync(0xffffffffu, normed)) {
                 float n[16];
 #pragma unroll
@@ -418,14 +430,14 @@ __global__ void __launch_bounds__(kNormWarps * 32, T == 1 ? 4 : 2) k_kv_append_n
                     }
                 }
             }
-            if (normed || turned) pack16(f, x[u], y[u]);
+            if (normed || turned) pack16(f, x, y);
         }
         if (h >= heads) continue;
         uint16_t* dst = key     ? a.kv.k + place + h * a.kv.head_stride
                         : value ? a.kv.v + place + (h - a.Hkv) * a.kv.head_stride
                                 : a.q_out + (row * a.Hq + (h - 2 * a.Hkv)) * D;
-        *reinterpret_cast<uint4*>(dst + (value ? tt * 8 : at)) = x[u];
-        *reinterpret_cast<uint4*>(dst + (value ? tt * 8 + D / 2 : at + dist)) = y[u];
+        *reinterpret_cast<uint4*>(dst + (value ? tt * 8 : at)) = x;
+        *reinterpret_cast<uint4*>(dst + (value ? tt * 8 + D / 2 : at + dist)) = y;
     }
 }
 
@@ -440,8 +452,21 @@ cudaError_t launch_norm(NormArgs& a, bool small, cudaStream_t stream) {
     const int64_t blocks = row_blocks + (std::max(a.n_seq, a.rot / 2) + kNormWarps * 32 - 1) / (kNormWarps * 32);
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     a.row_blocks = (uint32_t)row_blocks;
-    return dghost::launch_pdl(small ? k_kv_append_norm<Interleaved, D, 1> : k_kv_append_norm<Interleaved, D, T>,
-                              dim3((unsigned)blocks), dim3(kNormWarps * 32), 0, stream, a);
+    if (small)
+        return dghost::launch_pdl(k_kv_append_norm<Interleaved, D, 1>, dim3((unsigned)blocks), dim3(kNormWarps * 32),
+                                  kNormWarps * 1024, stream, a);
+    constexpr int kBytes = kNormWarps * T * 1024;
+    // the attribute once a device
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+        e = cudaFuncSetAttribute(k_kv_append_norm<Interleaved, D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        if (e != cudaSuccess) return e;
+        if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    return dghost::launch_pdl(k_kv_append_norm<Interleaved, D, T>, dim3((unsigned)blocks), dim3(kNormWarps * 32), kBytes, stream, a);
 }
 
 }  // namespace

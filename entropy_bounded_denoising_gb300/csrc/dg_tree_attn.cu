@@ -127,7 +127,7 @@ struct __align__(8) TreeShared {
     int64_t sums[kThreads / 32], items[kThreads / 32];
     int64_t found_start;
     Piece piece[kRing];           // nt 0: no more
-    int32_t top_position[2][4];
+    int32_t top_position[2][8];   // by warp: the last and the first position of its rows
     int32_t found_seq, zeros;     // zeros: some sequence has queries and no keys
     uint32_t tmem_base;
     int abort_flag;
@@ -458,23 +458,22 @@ DG_DEVINL void leave_piece(TreeShared& sh, uint32_t k) {
 }
 
 // Bits below n.
-DG_DEVINL uint64_t below(int64_t n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+DG_DEVINL uint64_t below(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
-// The keys j0 .. j0 + 63 that a row sees: `pos` its position, `row` its query's row.
-DG_DEVINL uint64_t seen_keys(const TreeArgs& a, const Piece& z, int j0, int pos, int64_t row) {
-    const int ctx = z.kl - z.ql;
-    uint64_t m = below((int64_t)(a.mask ? ctx : pos + 1) - j0);
-    if (a.window >= 0) m &= ~below((int64_t)pos - a.window - j0) | below((int64_t)a.sinks - j0);
-    if (a.mask && j0 + kKeys > ctx) {
-        const uint32_t* w = a.mask + row * a.mask_words;
-        const int n0 = j0 - ctx;             // node of bit 0, from -63 on
-        auto word = [&](int i) -> uint64_t { return i >= 0 && i < a.mask_words ? w[i] : 0u; };
-        const int i = n0 >> 5, sh = n0 & 31;   // (floors)
-        uint64_t bits = (word(i) >> sh) | (word(i + 1) << (32 - sh));
-        if (sh) bits |= word(i + 2) << (64 - sh);
-        m |= bits & below((int64_t)z.kl - j0) & ~below(-(int64_t)n0);
-    }
-    return m;
+// The keys j0 .. j0 + 63 from lo to hi, and those below `sinks` up to hi.
+DG_DEVINL uint64_t keys_between(int j0, int lo, int hi, int sinks) {
+    return below(hi - j0 + 1) & (~below(lo - j0) | below(sinks - j0));
+}
+
+// The nodes among them that a query sees, `row` being its row.
+DG_DEVINL uint64_t seen_nodes(const TreeArgs& a, const Piece& z, int j0, int64_t row) {
+    const uint32_t* w = a.mask + row * a.mask_words;
+    const int n0 = j0 - (z.kl - z.ql);       // node of bit 0, from -63 on
+    auto word = [&](int i) -> uint64_t { return i >= 0 && i < a.mask_words ? w[i] : 0u; };
+    const int i = n0 >> 5, sh = n0 & 31;     // (floors)
+    uint64_t bits = (word(i) >> sh) | (word(i + 1) << (32 - sh));
+    if (sh) bits |= word(i + 2) << (64 - sh);
+    return bits & below(z.kl - j0) & ~below(-n0);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -730,20 +729,26 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             const bool valid = qi < z.nq && hi < z.nh;
             const bool idle = !__any_sync(0xffffffffu, valid);   // no row of this warp's: only its arrivals
             const int64_t qrow = (int64_t)z.qrow + (valid ? qi : 0);
-            int pos = ctx + z.qi0 + (valid ? qi : 0), top = ctx + z.qi0 + z.nq - 1;
+            int pos = ctx + z.qi0 + (valid ? qi : 0), low = ctx + z.qi0, top = low + z.nq - 1;
             if (a.mask && a.window >= 0) {   // the nodes' own positions, and the last of the item's
                 pos = max(a.positions[qrow], ctx);
-                const int w = __reduce_max_sync(0xffffffffu, pos);
+                const int w = __reduce_max_sync(0xffffffffu, valid ? pos : ctx), w0 = __reduce_min_sync(0xffffffffu, valid ? pos : 0x7fffffff);
                 int32_t* tops = sh.top_position[k & 1u];
-                if (lane == 0) tops[q] = w;
+                if (lane == 0) {
+                    tops[q] = w;
+                    tops[4 + q] = w0;
+                }
                 if (!meet()) {
                     ok = false;
                     break;
                 }
                 top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+                low = min(min(tops[4], tops[5]), min(tops[6], tops[7]));
             }
             const int all_hi = a.mask ? ctx - 1 : ctx + z.qi0;   // every row sees keys up to it,
-            const int64_t all_lo = a.window < 0 ? 0 : (int64_t)top - a.window;   // from here on
+            const int all_lo = a.window < 0 ? 0 : max(0, top - a.window);   // from here on;
+            const int any_lo = a.window < 0 ? 0 : max(0, low - a.window);   // some row from here on;
+            const int row_lo = a.window < 0 ? 0 : max(0, pos - a.window), row_hi = a.mask ? ctx - 1 : pos;   // and this one
             float m_ref = -INFINITY, l = 0.f;
             for (int i = 0; i < nt; ++i) {
                 const uint32_t gi = g + (uint32_t)i;
@@ -769,17 +774,23 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                 if (lane == 0) dg::mbar_arrive(&sh.sempty);
                 const int j0 = z.tile(i) * kKeys, j1 = j0 + kKeys - 1;
                 if (j1 > all_hi || (j0 < all_lo && j1 >= a.sinks)) {   // not all of it is seen by all
-                    const uint64_t m = valid ? seen_keys(a, z, j0, pos, qrow) : 0ull;
-                    const uint32_t w0 = __reduce_or_sync(0xffffffffu, (uint32_t)m);
-                    const uint32_t w1 = __reduce_or_sync(0xffffffffu, (uint32_t)(m >> 32));
-                    uint64_t* seen = sh.seen[masked & 1u];
-                    ++masked;
-                    if (lane == 0) seen[q] = (uint64_t)w1 << 32 | w0;
-                    if (!meet()) {
-                        ok = false;
-                        break;
+                    uint64_t m = valid ? keys_between(j0, row_lo, row_hi, a.sinks) : 0ull;
+                    // rows' ranges follow each other without gaps: some row sees each key of the first to the last
+                    uint64_t any_row = keys_between(j0, any_lo, a.mask ? ctx - 1 : top, a.sinks);
+                    if (a.mask && j1 >= ctx) {   // nodes: the warps join what their rows see
+                        const uint64_t nodes = valid ? seen_nodes(a, z, j0, qrow) : 0ull;
+                        m |= nodes;
+                        const uint32_t w0 = __reduce_or_sync(0xffffffffu, (uint32_t)nodes);
+                        const uint32_t w1 = __reduce_or_sync(0xffffffffu, (uint32_t)(nodes >> 32));
+                        uint64_t* seen = sh.seen[masked & 1u];
+                        ++masked;
+                        if (lane == 0) seen[q] = (uint64_t)w1 << 32 | w0;
+                        if (!meet()) {
+                            ok = false;
+                            break;
+                        }
+                        any_row |= seen[0] | seen[1] | seen[2] | seen[3];
                     }
-                    const uint64_t any_row = seen[0] | seen[1] | seen[2] | seen[3];
                     if (~any_row) {   // the values nobody sees
                         if (!wait_warp(&sh.vfull[gi & 1u], (gi >> 1) & 1u)) {
                             ok = false;
