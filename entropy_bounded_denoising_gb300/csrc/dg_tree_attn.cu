@@ -947,47 +947,80 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
 }
 
 // Joins an item's pieces: the last one of CTA c (slot 1) and the first ones (slot 0) of the CTAs that follow
-// it.  blockIdx.x = c, blockIdx.y = 16 of the dimensions; a thread owns a row's, most blocks find nothing to join.
+// it.  blockIdx.x = c, blockIdx.y = 16 of the dimensions; most blocks find nothing to join.  A thread owns a row's
+// 16 dimensions of every (kJoinThreads / rows)-th piece, kAtOnce pieces on their way at a time; the groups join in shared
+// memory in a fixed order.  A few items of up to dozens of pieces each take large blocks (us large / small: one request over
+// 16k keys 32 / 48, over 1k 21 / 19.5); more items, of which most blocks find none, small ones (8 requests over 2.3k keys
+// 33 / 27, 64 over 400 51 / 36.6).
 constexpr int kJoinDims = 16;
-template <int D>
-__global__ void __launch_bounds__(kTile) k_tree_join(const TreeArgs a) {
+template <int D, int kJoinThreads, int kAtOnce>
+__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
+    constexpr int Q = kJoinDims / 4;
+    __shared__ float4 s_o[kJoinThreads][Q];
+    __shared__ float2 s_ml[kJoinThreads];
     dg::pdl_wait();
     dg::pdl_release();
-    const int c = blockIdx.x, row = threadIdx.x;
+    const int c = blockIdx.x;
     const int4 d0 = a.desc[2 * c];
     if (d0.x == 0) return;
     const int n = d0.x + 1, nh = a.desc[2 * c + 1].x;
+    const int groups = kJoinThreads / a.rows, group = (int)threadIdx.x / a.rows, row = (int)threadIdx.x - group * a.rows;
     const int qi = row / a.hpt, hi = row - qi * a.hpt;
-    if (qi >= d0.w || hi >= nh) return;
+    const bool mine = group < groups && qi < d0.w && hi < nh;
     auto slot = [&](int i) -> int64_t { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) M = fmaxf(M, a.part_ml[slot(i) * a.rows + row].x);
-    float L = 0.f;
-    float4 o[kJoinDims / 4];
+    float M = -INFINITY, L = 0.f;
+    float4 o[Q];
 #pragma unroll
-    for (int e = 0; e < kJoinDims / 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float2 ml = a.part_ml[slot(i) * a.rows + row];
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        L += ml.y * f;
+    for (int e = 0; e < Q; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // adds a piece (maximum, sum, output) to the thread's
+    auto add = [&](float2 ml, const float4 (&v)[Q]) {
+        if (ml.x == -INFINITY) return;   // the row saw nothing of it, whatever its values
+        const float m = fmaxf(M, ml.x), f0 = M == -INFINITY ? 0.f : ex2(M - m), f1 = ex2(ml.x - m);
+        M = m;
+        L = L * f0 + ml.y * f1;
 #pragma unroll
-        for (int e = 0; e < kJoinDims / 4; ++e) {
-            const float4 v = a.part_o[(slot(i) * (D / 4) + blockIdx.y * (kJoinDims / 4) + e) * a.rows + row];
-            if (f != 0.f) {   // (a piece of which the row saw nothing adds nothing, whatever its values)
-                o[e].x += v.x * f;
-                o[e].y += v.y * f;
-                o[e].z += v.z * f;
-                o[e].w += v.w * f;
-            }
+        for (int e = 0; e < Q; ++e) {
+            o[e].x = o[e].x * f0 + v[e].x * f1;
+            o[e].y = o[e].y * f0 + v[e].y * f1;
+            o[e].z = o[e].z * f0 + v[e].z * f1;
+            o[e].w = o[e].w * f0 + v[e].w * f1;
         }
+    };
+    if (mine) {
+        for (int i0 = group; i0 < n; i0 += kAtOnce * groups) {
+            float2 ml[kAtOnce];
+            float4 v[kAtOnce][Q];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = i0 + k * groups;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (i >= n) continue;
+                ml[k] = a.part_ml[slot(i) * a.rows + row];
+#pragma unroll
+                for (int e = 0; e < Q; ++e) v[k][e] = a.part_o[(slot(i) * (D / 4) + blockIdx.y * Q + e) * a.rows + row];
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) add(ml[k], v[k]);
+        }
+    }
+    if (group > 0) {
+        s_ml[threadIdx.x] = make_float2(M, L);
+#pragma unroll
+        for (int e = 0; e < Q; ++e) s_o[threadIdx.x][e] = o[e];
+    }
+    __syncthreads();
+    if (group > 0 || !mine) return;
+    for (int k = 1; k < min(groups, n); ++k) {
+        float4 v[Q];
+#pragma unroll
+        for (int e = 0; e < Q; ++e) v[e] = s_o[k * a.rows + row][e];
+        add(s_ml[k * a.rows + row], v);
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     const int64_t out = ((int64_t)d0.y + qi) * a.Hq + d0.z + hi;
     uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + blockIdx.y * kJoinDims);
 #pragma unroll
-    for (int e = 0; e < kJoinDims / 4; e += 2)
+    for (int e = 0; e < Q; e += 2)
         dst[e / 2] = make_uint4(pack_bf16x2(o[e].x * inv, o[e].y * inv), pack_bf16x2(o[e].z * inv, o[e].w * inv),
                                 pack_bf16x2(o[e + 1].x * inv, o[e + 1].y * inv), pack_bf16x2(o[e + 1].z * inv, o[e + 1].w * inv));
     if (blockIdx.y == 0 && a.lse) a.lse[out] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
@@ -1003,8 +1036,17 @@ size_t piece_bytes(int32_t D, int rows) {
     return ctas * 32 + ctas * 2 * rows * ((size_t)D * 4 + 8);
 }
 
-// Whether a call takes the kernels for few rows (dg_tree_split.cu).
-bool few_rows(int32_t max_q_len, int32_t group) { return (int64_t)max_q_len * group <= 16; }
+// Whether a call takes the kernels for few rows (dg_tree_split.cu), whose items of 16 rows pass over the keys each; a tile
+// here takes all of a key head's up to 128.  One pass: there.  Up to four: there while the passes of all
+// sequences are few, since a call here takes 10 us more to start and to join.  Measured (us there / here), heads of
+// 128, 8 key heads: 8 requests over 2.3k keys, 16, 24, 32, 64 rows a key head 21 / 27, 25 / 27.5, 28 / 28, 40 / 29; one over
+// 1k, 32 and 64 rows 13 / 20; 64 over 400 keys, 16 and 24 rows 34 / 37, 40 / 38; 32 over 4k keys, 16, 24, 32 rows 70 / 72,
+// 85 / 68, 102 / 68.  Heads of 64: 64 over 400 keys, 24 and 32 rows 30 / 34, 36 / 35; 32 over 4k, 17, 24, 32 rows 45 / 56,
+// 55 / 55, 64 / 56.  Heads of 256, 4 key heads: 8 over 2.3k keys, 16, 24, 32 rows 25 / 28, 29 / 30, 33 / 30.
+bool few_rows(int32_t n_seq, int32_t max_q_len, int32_t Hkv, int32_t group, int32_t D) {
+    const int64_t passes = ((int64_t)max_q_len * group + 15) / 16;
+    return passes == 1 || (passes <= 4 && n_seq * (int64_t)Hkv * passes * (D / 64) <= 256);
+}
 
 template <int D>
 dg_status launch_tree(const dghost::TreeCall& c, void* workspace, cudaStream_t stream) {
@@ -1067,7 +1109,9 @@ dg_status launch_tree(const dghost::TreeCall& c, void* workspace, cudaStream_t s
     cudaError_t e = dghost::launch_pdl(k_tree<D>, dim3(grid), dim3(kThreads), tree_smem<D>(), stream, tq, tk, tv, a);
     dghost::count_launch();
     if (e != cudaSuccess) return DG_ERR_CUDA;
-    e = dghost::launch_pdl(k_tree_join<D>, dim3(grid, D / kJoinDims), dim3(kTile), 0, stream, a);
+    const int64_t items = (int64_t)a.n_seq * a.Hkv * a.head_tiles * (((int64_t)a.max_q_len + a.qpt - 1) / a.qpt);
+    e = items * 16 < grid ? dghost::launch_pdl(k_tree_join<D, 512, 4>, dim3(grid, D / kJoinDims), dim3(512), 0, stream, a)
+                         : dghost::launch_pdl(k_tree_join<D, 128, 2>, dim3(grid, D / kJoinDims), dim3(128), 0, stream, a);
     dghost::count_launch();
     return dghost::cuda_status(e);
 }
@@ -1110,7 +1154,7 @@ dg_status tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* 
     c.sinks = window < 0 ? 0 : sinks;
     c.scale = scale;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (few_rows(max_q_len, Hq / Hkv)) return dghost::tree_split(c, D, workspace, st);
+    if (few_rows(n_seq, max_q_len, Hkv, Hq / Hkv, D)) return dghost::tree_split(c, D, workspace, st);
     if (D == 64) return launch_tree<64>(c, workspace, st);
     return D == 128 ? launch_tree<128>(c, workspace, st) : launch_tree<256>(c, workspace, st);
 }
