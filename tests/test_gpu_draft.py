@@ -6,6 +6,7 @@ Attention: see draft_ref.attention.  Verification: tokens and paths equal wherev
 than 2^-28 to its border; the kernel's weights are within 2^-31.  Copies bit for bit."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -336,20 +337,96 @@ def test_sink_attention_is_causal_attention():
     ref.check_attention(b, o2, None)
 
 
-def test_attention_far_pages():
+@pytest.mark.parametrize("nodes", [9, 90])
+def test_attention_far_pages(nodes):
     """Offsets past 2^31 elements: pages spread over a pool of 2 * 4.3 GB."""
     n_pages, page, H, D = 33000, 64, 8, 128
     k = torch.empty((n_pages, page, H, D), dtype=ref.BF16, device=DEV)   # 2^31 elements: page 32768
     v = torch.empty_like(k)
-    b = ref.Batch([(9, 200, 1)], 16, H, D, page, seed=2).fill_keys()
+    b = ref.Batch([(nodes, 200, 1)], 16, H, D, page, seed=2).fill_keys()
     kk, vv = b.keys(0)
     pages = [n_pages - 1, 0, n_pages - 2, 4500]
     b.table = torch.tensor([pages], **I32)
     b.k_cache, b.v_cache, b.n_pages = k, v, n_pages
     at = b.slots(0, range(200))
     k[at], v[at] = kk, vv
-    anc = [set(range(i + 1)) for i in range(9)]
-    _run_attention(b, [dref.visible(9, 200, anc=anc)], mask=dref.words(anc, 1, DEV))
+    anc = [set(range(i + 1)) for i in range(nodes)]
+    _run_attention(b, [dref.visible(nodes, 200, anc=anc)], mask=dref.words(anc, 3, DEV))
+
+
+# few rows a key head take kernels of their own: the same edges there
+SMALL = [(4, 300), (3, 3), (1, 1), (0, 9), (0, 0), (2, 0), (4, 64), (1, 700), (3, 65)]
+
+
+@pytest.mark.parametrize("window,sinks", [(-1, 0), (40, 0), (100, 70), (0, 1)])
+@pytest.mark.parametrize("Hq,Hkv,D,page,head_major", [(16, 8, 128, 16, False), (4, 4, 64, 8, True), (4, 1, 256, 64, False),
+                                                      (8, 4, 64, 16, False), (2, 1, 128, 32, True), (3, 1, 256, 8, False)])
+def test_small_trees(Hq, Hkv, D, page, head_major, window, sinks):
+    b, oks, mask, pos = _tree_batch(SMALL, Hq, Hkv, D, page, 12, window, sinks, head_major=head_major, before=2, after=3)
+    _run_attention(b, oks, mask=mask, positions=pos if window >= 0 else None, window=window, sinks=sinks)
+
+
+def test_small_trees_in_pairs():
+    """One or two nodes over heads of 64: two key heads go as one."""
+    for window, sinks in ((-1, 0), (30, 5)):
+        b, oks, mask, pos = _tree_batch([(2, 200), (1, 1), (2, 2), (1, 90), (2, 1000)], 8, 8, 64, 16, 4, window, sinks)
+        _run_attention(b, oks, mask=mask, positions=pos, window=window, sinks=sinks)
+
+
+def test_small_trees_masks_and_values():
+    empty = lambda a, anc: [set() if i % 3 == 0 else s | {a, a + 1, 31} for i, s in enumerate(anc)]  # noqa: E731
+    seqs = [(4, 4), (3, 3), (1, 1), (4, 80), (2, 64)]
+    for D, Hkv in ((64, 2), (128, 2), (256, 1)):
+        b, oks, mask, pos = _tree_batch(seqs, 4 * Hkv, Hkv, D, 16, 3, anc_of=empty)
+        _run_attention(b, oks, mask=mask)
+        for scale in (0.0, -0.3, 1e-30):
+            _run_attention(b, oks, mask=mask, scale=scale)
+        # all rows empty
+        b, oks, mask, pos = _tree_batch(seqs, 4 * Hkv, Hkv, D, 16, 3, 0, 0, anc_of=lambda a, anc: [set() for _ in anc])
+        oks = [dref.visible(a, m, anc=[set()] * a, positions=[1000] * a, window=0) for a, m in seqs]
+        o, lse = _run_attention(b, oks, mask=mask, positions=torch.full_like(pos, 1000), window=0)
+        assert (o == 0).all() and (lse == -math.inf).all()
+        # what nobody sees
+        hidden = lambda a, anc: [{j for j in s if j != 1} | {0} for s in anc]  # noqa: E731
+        b, oks, mask, pos = _tree_batch([(4, 300), (4, 4), (3, 500)], 4 * Hkv, Hkv, D, 16, 8, 50, 3, anc_of=hidden)
+        keys = [b.keys(s) for s in range(3)]
+        b.keys = lambda s: keys[s]
+        for s, (a, m, _) in enumerate(b.seqs):
+            at = b.slots(s, torch.nonzero(~oks[s].any(0))[:, 0])
+            b.k_cache[at] = math.nan
+            b.v_cache[at] = torch.tensor([math.inf, -math.inf, math.nan, 3e38] * (D // 4), dtype=ref.BF16, device=DEV)
+            for page in range(-(-m // 16)):
+                if not oks[s][:, page * 16:page * 16 + 16].any():
+                    b.table[s, page] = -9
+        _run_attention(b, oks, mask=mask, positions=pos, window=50, sinks=3)
+
+
+def test_tree_positions_before_the_context():
+    """A node's position below its context's length counts as that length."""
+    for seqs in ([(4, 300), (2, 70)], [(60, 300), (20, 90)]):
+        b, _, mask, pos = _tree_batch(seqs, 8, 2, 128, 16, 5)
+        low = torch.randint(-1000, 200, pos.shape, **I32)
+        oks, at = [], 0
+        words = mask.cpu().numpy().view("uint8")
+        for a, m in seqs:
+            bits = np.unpackbits(words[at:at + a], axis=1, bitorder="little")
+            anc = [set(np.nonzero(r)[0].tolist()) for r in bits]
+            oks.append(dref.visible(a, m, anc=anc, positions=[max(p, m - a) for p in low[at:at + a].tolist()], window=33, sinks=2))
+            at += a
+        _run_attention(b, oks, mask=mask, positions=low, window=33, sinks=2)
+
+
+def test_sink_prompts_unseen_context():
+    b = ref.Batch([(100, 900, 1), (40, 600, 1)], 8, 4, 128, 16, seed=3).fill_keys()
+    oks = [dref.visible(a, m, window=70, sinks=5) for a, m, _ in b.seqs]
+    keys = [b.keys(s) for s in range(2)]
+    b.keys = lambda s: keys[s]
+    for s, (a, m, _) in enumerate(b.seqs):
+        at = b.slots(s, torch.nonzero(~oks[s].any(0))[:, 0])
+        b.k_cache[at] = math.nan
+        b.v_cache[at] = math.nan
+        b.table[s, 1:(m - a - 70) // 16] = 1 << 30
+    _run_attention(b, oks, window=70, sinks=5)
 
 
 # ------------------------------------------------------------------ verification
@@ -538,6 +615,36 @@ def test_verify_odd_drafts():
         d.probs[3 * s + 1, :V] = [0.0, 1.0, 7.0, -1.0, math.nan, math.inf, 2.0 ** -140][s % 7]
     d.u[1::3] = 0.99
     d.run().check()
+
+
+def test_verify_temperatures():
+    """Temperatures at the ends of their range: the largest token alone, and all tokens but the masked ones alike."""
+    V = 640
+    for dtype in (torch.bfloat16, torch.float32):
+        d = Drafts([4] * 30, V, 6, T=2.0 ** -64, dtype=dtype)
+        d.x[:, 5] = 100.0
+        d.run().check()
+        assert (d.out.view(30, 4)[:, 0] == 5).all()
+        d = Drafts([1] * 50, V, 6, T=2.0 ** 64, dtype=dtype)
+        d.x[:, :V] = torch.where(torch.arange(V) % 2 == 0, torch.full_like(d.x[:, :V], -math.inf), d.x[:, :V])
+        d.run()
+        assert dg.dg_get_device_status() == 0
+        want = ((d.un.double() * (V // 2)).floor() * 2 + 1).int()
+        assert torch.equal(d.out.cpu(), want)
+    d = Drafts([1] * 50, V, 6, T=1.0, dtype=torch.float32, std=1e38)   # differences past fp32
+    over = torch.isinf(d.x).any(1).tolist()                             # some rows hold an infinity
+    d.run().check(status=1, skip=[s for s in range(50) if over[s]])
+    d.x = d.x.clamp(-3e38, 3e38)
+    d.run().check()
+
+
+def test_verify_nothing():
+    d = Drafts([0, 0], 16, 1)
+    d.run().check()
+    assert d.n_accept.tolist() == [-1, -1]
+    z = torch.zeros(0, **I32)
+    dg.dg_verify_drafts(torch.zeros((0, 16), device=DEV), z, z.new_zeros(1), torch.zeros(0, device=DEV),
+                        torch.zeros(0, device=DEV), torch.zeros(0, device=DEV), z, z.clone(), z.clone())
 
 
 def test_verify_distribution():
