@@ -9,8 +9,8 @@
 // and are joined by a second kernel in the order of the line.  Where there are many items a run takes whole ones.
 //
 // A CTA (two an SM; one for heads of 256):
-//   warp 0      walks the run, publishes its pieces in a ring and copies their queries, keys and values (two tiles
-//               each), page by page, a box a lane;
+//   warp 0      walks the run, publishes its pieces in a ring and copies their queries, and their keys and
+//               values through one ring of five tiles (ten for heads of 64), page by page, a box a lane;
 //   warp 1      issues the products: S = Q K^T (128 x 64) into TMEM, O += P V with P from TMEM;
 //   warps 2..5  the softmax, a row a thread.
 // A tile that not all rows see whole gets each row's 64-bit mask: the window's and the context's ranges, and the row's
@@ -65,7 +65,8 @@ struct TreeArgs {
 template <int D>
 struct TreeCfg {
     static constexpr uint32_t kQBytes = (D / kSub) * kQSub, kKVBytes = (D / kSub) * kKSub;
-    static constexpr uint32_t kOffQ = 0, kOffK = kQBytes, kOffV = kOffK + 2 * kKVBytes, kOffBar = kOffV + 2 * kKVBytes;
+    static constexpr uint32_t kBufs = D == 64 ? 10 : 5;     // tiles of keys or values on their way or in use
+    static constexpr uint32_t kOffQ = 0, kOffKV = kQBytes, kOffBar = kOffKV + kBufs * kKVBytes;
     static constexpr uint32_t kColS = 0, kColO = 64, kColP = 64 + D;
     static constexpr uint32_t kTmemCols = D == 256 ? 512 : 256;
     static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
@@ -115,9 +116,18 @@ struct Piece {
 };
 constexpr uint32_t kStarts = 1, kEnds = 2;
 
+// Keys and values share one ring of buffers, in the order K0, K1, V0, K2, V1, ..., that of the products.
+DG_DEVINL uint32_t keys_at(uint32_t n) { return n == 0 ? 0u : 2u * n - 1u; }
+DG_DEVINL uint32_t values_at(uint32_t n) { return 2u * n + 2u; }
+template <uint32_t N>
+struct RingAt {   // a place in the ring and the parity of its use
+    uint32_t slot, parity;
+    DG_DEVINL explicit RingAt(uint32_t n) : slot(n % N), parity(n / N & 1u) {}
+};
+
 struct __align__(8) TreeShared {
     uint64_t qfull, qempty, oempty;
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2];   // separate rings: a K buffer is free once its S is done
+    uint64_t full[10], empty[10];
     uint64_t sfull, sempty;
     uint64_t pfull[2], pvdone[2];
     uint64_t mmadone;
@@ -132,9 +142,11 @@ struct __align__(8) TreeShared {
     uint32_t tmem_base;
     int abort_flag;
 };
+// (Two CTAs an SM of 115712 bytes each, two CTAs' own kilobytes beside them, are all of its shared memory.)
 template <int D>
 constexpr size_t tree_smem() {
-    return 1024 + TreeCfg<D>::kOffBar + sizeof(TreeShared) + 64;
+    static_assert((TreeCfg<D>::kOffBar + sizeof(TreeShared)) <= (TreeCfg<D>::kCtasPerSm == 2 ? 115712 : 232448), "shared memory");
+    return TreeCfg<D>::kOffBar + sizeof(TreeShared);
 }
 
 DG_DEVINL bool try_wait(uint64_t* bar, uint32_t parity) {
@@ -484,20 +496,20 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
     using C = TreeCfg<D>;
     constexpr uint32_t kKVBytes = C::kKVBytes;
     constexpr uint32_t kColS = C::kColS, kColO = C::kColO, kColP = C::kColP, kTmemCols = C::kTmemCols;
-    extern __shared__ __align__(1024) unsigned char tree_smem_raw[];
-    unsigned char* smem =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tree_smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr uint32_t kBufs = C::kBufs;
+    using At = RingAt<kBufs>;
+    extern __shared__ __align__(1024) unsigned char smem[];
     TreeShared& sh = *reinterpret_cast<TreeShared*>(smem + C::kOffBar);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         dg::mbar_init(&sh.qfull, 1);
         dg::mbar_init(&sh.qempty, 1);
         dg::mbar_init(&sh.oempty, 4);
+        for (uint32_t i = 0; i < kBufs; ++i) {
+            dg::mbar_init(&sh.full[i], 1);
+            dg::mbar_init(&sh.empty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
-            dg::mbar_init(&sh.kfull[i], 1);
-            dg::mbar_init(&sh.kempty[i], 1);
-            dg::mbar_init(&sh.vfull[i], 1);
-            dg::mbar_init(&sh.vempty[i], 1);
             dg::mbar_init(&sh.pfull[i], 4);
             dg::mbar_init(&sh.pvdone[i], 1);
         }
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
 
     if (warp == 0) {
         // ------------------------------------------------ the walk and the copies, a whole warp
-        // Tile n's keys, then tile n - 1's values, in the order in which the products free their places; behind a piece's
+        // Tile n's keys, then tile n - 1's values, in the ring's order; behind a piece's
         // first keys its queries, whose place the same product frees as that of the second tile's keys.  A lane copies a
         // box of a page's slots x 64 columns; the lanes hold the page numbers of the tiles to come, and ask for
         // the next ones (the next piece's first ones too) before they are needed.
@@ -564,16 +576,17 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
         int32_t en = more ? entries(zn, 0) : 0;
         uint32_t n_keys = 0, n_values = 0, n_queries = 0;   // copies asked for
         int v_page = 0, v_slot = 0, v_hk = 0;               // of the last tile's values
-        auto copy = [&](const CUtensorMap* tm, unsigned char* dst, uint64_t* full, int slot, int hk, int page) {
-            if (lane == 0) dg::mbar_arrive_expect_tx(full, kKVBytes);
+        auto copy = [&](const CUtensorMap* tm, const At& to, int slot, int hk, int page) {
+            if (!wait_warp(&sh.empty[to.slot], to.parity ^ 1u)) return false;
+            if (lane == 0) dg::mbar_arrive_expect_tx(&sh.full[to.slot], kKVBytes);
             __syncwarp();
             if (box < boxes)
-                dg::tma_load_4d(dst + col * kKSub + (box << box_shift) * kSub * 2, tm, col * kSub, slot, hk, page, full);
+                dg::tma_load_4d(smem + C::kOffKV + to.slot * kKVBytes + col * kKSub + (box << box_shift) * kSub * 2, tm,
+                                col * kSub, slot, hk, page, &sh.full[to.slot]);
+            return true;
         };
         auto values = [&]() {                               // of the tile before
-            const int st = (int)(n_values & 1u);
-            if (!wait_warp(&sh.vempty[st], ((n_values >> 1) & 1u) ^ 1u)) return false;
-            copy(&tmV, smem + C::kOffV + st * kKVBytes, &sh.vfull[st], v_slot, v_hk, v_page);
+            if (!copy(&tmV, At(values_at(n_values)), v_slot, v_hk, v_page)) return false;
             ++n_values;
             return true;
         };
@@ -599,14 +612,13 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                     e = e_next;
                     e_next = entries(z, i + ahead);
                 }
-                const int st = (int)(n_keys & 1u), j0 = z.tile(i) * kKeys;
+                const int j0 = z.tile(i) * kKeys;
                 const int page = __shfl_sync(0xffffffffu, e, ((i - held) * boxes + box) & 31);
                 const int at = (j0 + (box << box_shift)) & ((1 << a.kv.page_shift) - 1);
-                if (!wait_warp(&sh.kempty[st], ((n_keys >> 1) & 1u) ^ 1u)) {
+                if (!copy(&tmK, At(keys_at(n_keys)), at, z.hk, page)) {
                     ok = false;
                     break;
                 }
-                copy(&tmK, smem + C::kOffK + st * kKVBytes, &sh.kfull[st], at, z.hk, page);
                 ++n_keys;
                 if (n_keys > 1 && !values()) {
                     ok = false;
@@ -635,9 +647,10 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
         if (ok && n_keys > 0) ok = values();
         if (!ok && lane == 0) do_abort(sh, a.status);
         if (__any_sync(0xffffffffu, !ok || aborted(sh))) {   // never leave with a copy still landing in shared memory
-            for (uint32_t b = 1; b <= 2; ++b) {
-                if (n_keys >= b) (void)wait_warp(&sh.kfull[(n_keys - b) & 1u], ((n_keys - b) >> 1) & 1u);
-                if (n_values >= b) (void)wait_warp(&sh.vfull[(n_values - b) & 1u], ((n_values - b) >> 1) & 1u);
+            const uint32_t top = max(n_keys > 0 ? keys_at(n_keys - 1) + 1 : 0u, n_values > 0 ? values_at(n_values - 1) + 1 : 0u);
+            for (uint32_t n = top > kBufs ? top - kBufs : 0u; n < top; ++n) {   // the last use of each buffer
+                const bool is_keys = n == 0 || (n & 1u);
+                if (is_keys ? (n + 1) / 2 < n_keys : n / 2 - 1 < n_values) (void)wait_warp(&sh.full[At(n).slot], At(n).parity);
             }
             if (n_queries > 0) (void)wait_warp(&sh.qfull, (n_queries - 1u) & 1u);
         }
@@ -659,13 +672,13 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                 for (int i = 0; i <= nt; ++i) {
                     if (i < nt) {   // S of tile g + i, once the softmax has read the last S
                         const uint32_t gs = g + (uint32_t)i;
-                        const int st = (int)(gs & 1u);
-                        if (!wait(&sh.kfull[st], (gs >> 1) & 1u) || !wait(&sh.sempty, (gs & 1u) ^ 1u)) {
+                        const At at(keys_at(gs));
+                        if (!wait(&sh.full[at.slot], at.parity) || !wait(&sh.sempty, (gs & 1u) ^ 1u)) {
                             ok = false;
                             break;
                         }
                         dg::tc_fence_after();
-                        const uint32_t sK = dg::smem_u32(smem + C::kOffK + st * kKVBytes);
+                        const uint32_t sK = dg::smem_u32(smem + C::kOffKV + at.slot * kKVBytes);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t offq = (uint32_t)(kk >> 2) * kQSub + (uint32_t)(kk & 3) * 32u;
@@ -674,26 +687,27 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                                            dg::smem_desc(sK + offk, 16, 1024, 128), idS, kk > 0 ? 1u : 0u);
                         }
                         dg::tc_commit(&sh.sfull);
-                        dg::tc_commit(&sh.kempty[st]);
+                        dg::tc_commit(&sh.empty[at.slot]);
                         if (i == nt - 1) dg::tc_commit(&sh.qempty);   // the queries, after the piece's last S
                     }
                     if (i >= 1) {   // O += P V of tile g + i - 1 once the softmax has written P
                         const uint32_t gp = g + (uint32_t)i - 1u;
                         const int st = (int)(gp & 1u);
-                        if (!wait(&sh.pfull[st], (gp >> 1) & 1u) || !wait(&sh.vfull[st], (gp >> 1) & 1u) ||
+                        const At at(values_at(gp));
+                        if (!wait(&sh.pfull[st], (gp >> 1) & 1u) || !wait(&sh.full[at.slot], at.parity) ||
                             (i == 1 && !wait(&sh.oempty, (k & 1u) ^ 1u))) {   // the last piece's O read out
                             ok = false;
                             break;
                         }
                         dg::tc_fence_after();
-                        const uint32_t sV = dg::smem_u32(smem + C::kOffV + st * kKVBytes);
+                        const uint32_t sV = dg::smem_u32(smem + C::kOffKV + at.slot * kKVBytes);
 #pragma unroll
                         for (int kk = 0; kk < kKeys / 16; ++kk)
                             dg::tc_mma_f16_ts(tmem + kColO, tmem + kColP + (uint32_t)(st * 32 + kk * 8),
                                               dg::smem_desc(sV + (uint32_t)kk * 16u * 128u, kKSub, 1024, 128), idO,
                                               (i > 1 || kk > 0) ? 1u : 0u);
                         dg::tc_commit(&sh.pvdone[st]);
-                        dg::tc_commit(&sh.vempty[st]);
+                        dg::tc_commit(&sh.empty[at.slot]);
                     }
                 }
                 g += (uint32_t)nt;
@@ -792,11 +806,12 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                         any_row |= seen[0] | seen[1] | seen[2] | seen[3];
                     }
                     if (~any_row) {   // the values nobody sees
-                        if (!wait_warp(&sh.vfull[gi & 1u], (gi >> 1) & 1u)) {
+                        const At at(values_at(gi));
+                        if (!wait_warp(&sh.full[at.slot], at.parity)) {
                             ok = false;
                             break;
                         }
-                        unsigned char* vt = smem + C::kOffV + (gi & 1u) * kKVBytes;
+                        unsigned char* vt = smem + C::kOffKV + at.slot * kKVBytes;
                         for (int c = row; c < kKeys * (D / kSub) * 8; c += 128) {   // 16-byte chunks
                             if (!(any_row >> ((c >> 3) & (kKeys - 1)) & 1u))
                                 reinterpret_cast<uint4*>(vt)[c] = make_uint4(0u, 0u, 0u, 0u);
