@@ -165,11 +165,9 @@ DG_DEVINL bool wait(uint64_t* bar, uint32_t parity) {   // bounded, as every wai
     return false;
 }
 DG_DEVINL bool wait_warp(uint64_t* bar, uint32_t parity) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = wait(bar, parity) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    return ok != 0;
+    for (uint32_t i = 0; i < 4u * dg::kWaitPolls; ++i)
+        if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
+    return false;
 }
 DG_DEVINL bool aborted(const TreeShared& sh) { return *(volatile const int*)&sh.abort_flag != 0; }
 DG_DEVINL void do_abort(TreeShared& sh, unsigned* status) {
