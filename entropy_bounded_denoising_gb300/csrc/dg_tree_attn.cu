@@ -35,7 +35,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTile = 128;      // rows of an item
 constexpr int kKeys = 64;       // keys of a tile
 constexpr int kSub = 64;        // columns of a 128-byte swizzle atom
-constexpr uint32_t kQSub = kTile * kSub * 2, kKSub = kKeys * kSub * 2;
+constexpr uint32_t kQSub = kTile * kSub * 2;
+constexpr uint32_t kAtom = 8 * kSub * 2;   // of keys and values: 8 slots x 64 columns
 constexpr float kRescaleAbove = 8.f;   // log2 units a row's maximum may grow before it moves: P <= 2^8
 constexpr int kThreads = 192;
 constexpr int kRing = 4;        // pieces published ahead
@@ -55,6 +56,8 @@ struct TreeArgs {
     int32_t rows;               // of a piece in the workspace (multiple of 32)
     int32_t negate;             // the products' sign: scale_log2 is the scale's magnitude, so the largest score stays the largest
     float scale_log2;
+    int32_t box_shift;          // slots of a copy of keys or values: 8 .. 64
+    int32_t by_slot, mul2, mul3, mul8;   // its coordinates: (0, by_slot * slot, mul2 * head, mul3 * head + mul8 * (slot / 8), page)
     dg::PagedKV kv;
     float4* part_o;             // [grid][2][D / 4][rows]
     float2* part_ml;            // [grid][2][rows]: maximum, sum
@@ -64,7 +67,7 @@ struct TreeArgs {
 
 template <int D>
 struct TreeCfg {
-    static constexpr uint32_t kQBytes = (D / kSub) * kQSub, kKVBytes = (D / kSub) * kKSub;
+    static constexpr uint32_t kQBytes = (D / kSub) * kQSub, kKVBytes = kKeys * D * 2;
     static constexpr uint32_t kBufs = D == 64 ? 10 : 5;     // tiles of keys or values on their way or in use
     static constexpr uint32_t kOffQ = 0, kOffKV = kQBytes, kOffBar = kOffKV + kBufs * kKVBytes;
     static constexpr uint32_t kColS = 0, kColO = 64, kColP = 64 + D;
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
         // ------------------------------------------------ the walk and the copies, a whole warp
         // Tile n's keys, then tile n - 1's values, in the ring's order; behind a piece's
         // first keys its queries, whose place the same product frees as that of the second tile's keys.  A lane copies a
-        // box of a page's slots x 64 columns; the lanes hold the page numbers of the tiles to come, and ask for
+        // box of a page's slots; the lanes hold the page numbers of the tiles to come, and ask for
         // the next ones (the next piece's first ones too) before they are needed.
         if (lane == 0) {
             dg::prefetch_tmap(&tmQ);
@@ -550,10 +553,10 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             dg::prefetch_tmap(&tmV);
         }
         constexpr int kCols = D / kSub;
-        const int box_shift = min(a.kv.page_shift, 6), size = 1 << box_shift, boxes = kKeys >> box_shift;
+        const int box_shift = a.box_shift, size = 1 << box_shift, boxes = kKeys >> box_shift;
         const int ahead = 32 / boxes;                       // tiles whose pages the warp holds
         const int my_tile = lane / boxes, my_box = lane - my_tile * boxes;   // as a holder
-        const int box = lane / kCols, col = lane - box * kCols;              // as a copier
+        const int box = min(lane, boxes - 1);                                // as a copier
         const uint32_t q_bytes = (uint32_t)(a.hpt * a.qpt) * kSub * 2 * kCols;
         if (few) run = find_run_warp(a);
         if (lane == 0) sh.zeros = run.zeros;
@@ -578,9 +581,9 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             if (!wait_warp(&sh.empty[to.slot], to.parity ^ 1u)) return false;
             if (lane == 0) dg::mbar_arrive_expect_tx(&sh.full[to.slot], kKVBytes);
             __syncwarp();
-            if (box < boxes)
-                dg::tma_load_4d(smem + C::kOffKV + to.slot * kKVBytes + col * kKSub + (box << box_shift) * kSub * 2, tm,
-                                col * kSub, slot, hk, page, &sh.full[to.slot]);
+            if (lane < boxes)
+                dg::tma_load_5d(smem + C::kOffKV + to.slot * kKVBytes + (box << box_shift) * D * 2, tm, 0, a.by_slot * slot,
+                                a.mul2 * hk, a.mul3 * hk + a.mul8 * (slot >> 3), page, &sh.full[to.slot]);
             return true;
         };
         auto values = [&]() {                               // of the tile before
@@ -680,9 +683,9 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t offq = (uint32_t)(kk >> 2) * kQSub + (uint32_t)(kk & 3) * 32u;
-                            const uint32_t offk = (uint32_t)(kk >> 2) * kKSub + (uint32_t)(kk & 3) * 32u;
+                            const uint32_t offk = (uint32_t)(kk >> 2) * kAtom + (uint32_t)(kk & 3) * 32u;
                             dg::tc_mma_f16(tmem + kColS, dg::smem_desc(sQ + offq, 16, 1024, 128),
-                                           dg::smem_desc(sK + offk, 16, 1024, 128), idS, kk > 0 ? 1u : 0u);
+                                           dg::smem_desc(sK + offk, 16, (D / kSub) * kAtom, 128), idS, kk > 0 ? 1u : 0u);
                         }
                         dg::tc_commit(&sh.sfull);
                         dg::tc_commit(&sh.empty[at.slot]);
@@ -702,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
 #pragma unroll
                         for (int kk = 0; kk < kKeys / 16; ++kk)
                             dg::tc_mma_f16_ts(tmem + kColO, tmem + kColP + (uint32_t)(st * 32 + kk * 8),
-                                              dg::smem_desc(sV + (uint32_t)kk * 16u * 128u, kKSub, 1024, 128), idO,
+                                              dg::smem_desc(sV + (uint32_t)kk * 16u * D * 2u, kAtom, (D / kSub) * kAtom, 128), idO,
                                               (i > 1 || kk > 0) ? 1u : 0u);
                         dg::tc_commit(&sh.pvdone[st]);
                         dg::tc_commit(&sh.empty[at.slot]);
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                         }
                         unsigned char* vt = smem + C::kOffKV + at.slot * kKVBytes;
                         for (int c = row; c < kKeys * (D / kSub) * 8; c += 128) {   // 16-byte chunks
-                            if (!(any_row >> ((c >> 3) & (kKeys - 1)) & 1u))
+                            if (!(any_row >> ((c >> 6) / (D / kSub) * 8 + ((c >> 3) & 7)) & 1u))
                                 reinterpret_cast<uint4*>(vt)[c] = make_uint4(0u, 0u, 0u, 0u);
                         }
                         dg::fence_proxy_async_smem();   // before the product reads them (pfull below)
@@ -1098,14 +1101,35 @@ dg_status launch_tree(const dghost::TreeCall& c, void* workspace, cudaStream_t s
         const uint32_t box[3] = {(uint32_t)kSub, (uint32_t)a.hpt, (uint32_t)a.qpt};
         if (!dghost::encode_tmap(&tq, 0, 3, const_cast<uint16_t*>(c.q), dims, strides, box, 128)) return DG_ERR_CUDA;
     }
-    for (auto [tm, base] : {std::pair<CUtensorMap*, uint16_t*>{&tk, a.kv.k}, {&tv, a.kv.v}}) {
-        // a page: 64 columns of a head, up to 64 of its slots
-        const uint64_t dims[4] = {(uint64_t)D, 1ull << a.kv.page_shift, (uint64_t)a.Hkv, (uint64_t)a.kv.n_pages};
-        const uint64_t strides[3] = {(uint64_t)a.kv.slot_stride * 2, (uint64_t)a.kv.head_stride * 2,
-                                     (uint64_t)a.kv.page_stride * 2};
-        const uint32_t box[4] = {(uint32_t)kSub, 1u << std::min(a.kv.page_shift, 6), 1u, 1u};
-        if (!dghost::encode_tmap(tm, 0, 4, base, dims, strides, box, 128)) return DG_ERR_CUDA;
+    // Keys and values lie in shared memory as [8 slots][64 columns of D][slot], so that one copy brings a head's slots of
+    // a page, up to 64.  Its dimensions are 64 columns, 8 slots, D / 64, slots / 8, page: the head has to go with
+    // one of them.  Slot by slot its columns follow the last head's; head by head its slots do.  For a cache with gaps
+    // between the two a copy is of 8 slots (32 trees of 64 nodes: see the file's head).
+    const uint64_t cols = D / kSub, ps = 1ull << a.kv.page_shift;
+    uint64_t dims[5] = {(uint64_t)kSub, 8, cols, ps / 8, (uint64_t)a.kv.n_pages};
+    uint64_t strides[4] = {(uint64_t)a.kv.slot_stride * 2, (uint64_t)kSub * 2, (uint64_t)a.kv.slot_stride * 16,
+                           (uint64_t)a.kv.page_stride * 2};
+    a.box_shift = std::min(a.kv.page_shift, 6);
+    uint32_t box[5] = {(uint32_t)kSub, 8, (uint32_t)cols, 1u << (a.box_shift - 3), 1};
+    a.by_slot = a.mul2 = a.mul3 = 0;
+    a.mul8 = 1;
+    if (a.kv.slot_stride < (1LL << 36) && (a.kv.head_stride == D || a.Hkv == 1)) {
+        dims[2] *= (uint64_t)a.Hkv;
+        a.mul2 = (int32_t)cols;
+    } else if (a.kv.slot_stride < (1LL << 36) && a.kv.head_stride == a.kv.slot_stride << a.kv.page_shift) {
+        dims[3] *= (uint64_t)a.Hkv;
+        a.mul3 = (int32_t)(ps / 8);
+    } else {
+        dims[1] = ps;
+        dims[3] = (uint64_t)a.Hkv;
+        strides[2] = (uint64_t)a.kv.head_stride * 2;
+        a.box_shift = 3;
+        box[3] = 1;
+        a.by_slot = a.mul3 = 1;
+        a.mul8 = 0;
     }
+    for (auto [tm, base] : {std::pair<CUtensorMap*, uint16_t*>{&tk, a.kv.k}, {&tv, a.kv.v}})
+        if (!dghost::encode_tmap(tm, 0, 5, base, dims, strides, box, 128)) return DG_ERR_CUDA;
     // the attribute once a device
     static std::atomic<uint64_t> ready{0};
     int dev = 0;

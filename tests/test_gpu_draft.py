@@ -366,6 +366,23 @@ def test_small_trees(Hq, Hkv, D, page, head_major, window, sinks):
     _run_attention(b, oks, mask=mask, positions=pos if window >= 0 else None, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("D,page,head_major", [(64, 8, False), (128, 16, True), (128, 128, False), (256, 64, True), (256, 8, False)])
+@pytest.mark.parametrize("gap", ["columns", "slots", "heads"])
+def test_trees_over_strided_caches(D, page, head_major, gap):
+    """Caches with gaps behind their columns, slots or heads."""
+    for seqs in ([(70, 200), (5, 5), (40, 333), (1, 64)], [(2, 130), (1, 1)]):
+        b, oks, mask, pos = _tree_batch(seqs, 6, 3, D, page, 4, 50, 3, head_major=head_major)
+        for name in ("k_cache", "v_cache"):
+            old = getattr(b, name)
+            n, slots, heads, _ = old.shape
+            s, h, d = page + (gap == "slots"), heads + (gap == "heads"), D + (8 if gap == "columns" else 0)
+            wide = torch.full((n, h, s, d) if head_major else (n, s, h, d), math.nan, dtype=ref.BF16, device=DEV)
+            new = (wide.transpose(1, 2) if head_major else wide)[:, :page, :heads, :D]
+            new.copy_(old)
+            setattr(b, name, new)
+        _run_attention(b, oks, mask=mask, positions=pos, window=50, sinks=3)
+
+
 def test_small_trees_in_pairs():
     """One or two nodes over heads of 64: two key heads go as one."""
     for window, sinks in ((-1, 0), (30, 5)):
