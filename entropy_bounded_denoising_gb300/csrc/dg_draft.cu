@@ -42,6 +42,11 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // added exactly from there on, whatever the order.
 // Acceptance compares fp32 sums, unless they come within their own bound of the border: then the row is summed
 // like the last one (kSum) and compared again.
+//
+// Measured: one chain of 5 drafts over 32768 tokens, bf16, 15 to 18 us by what is accepted: a node takes about 4, the row's
+// maximum, its sum and the two trips to and from the lead.  64 trees of 32 over 262144 tokens 60 us, where the bytes of the
+// rows walked take 8: the sums of a row that decides, some 47 lane cycles a token, and sequences that walk further than
+// others.  With weights in plain instead of packed pairs of fp32 67 us, with CTAs of 256 threads, two an SM, 67 too.
 constexpr int kVThreads = 128, kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxNodes = 1024;
@@ -866,7 +871,8 @@ __global__ void __launch_bounds__(kVThreads, 4) k_verify(const __grid_constant__
 // ------------------------------------------------------------------ kept paths
 // A thread owns 16 bytes of a head in one layer's keys or values and takes the path's nodes in order.  Node path[i] goes to
 // slot i <= path[i] behind the context, and every later node lies at path[k] >= k > i: nothing is overwritten
-// before it is read.
+// before it is read.  250 paths in 8 layers, 33 MB to and fro, take 7.9 us, one path in 12 layers 3.1: a launch, and four reads
+// that wait for one another (offsets, path, pages, data).
 constexpr int kKeepThreads = 256;
 constexpr int kKeepChunk = 256;    // moves whose places are worked out at a time
 

@@ -244,6 +244,9 @@ __global__ void __launch_bounds__(kAppendThreads, PerThread == 1 ? 8 : 4) k_kv_a
 // warp and its weights where it lies in a line with its neighbours.  The data is asked for first; the row's sequence and slot
 // are looked up and its sines computed while it is on the way, by the warp itself: nothing waits for a block.
 // Values stay in fp32 from the norm through the rotation.
+// Bound by memory from a few thousand rows on: ragged prompts of 18k rows, 16 / 8 heads of 128, 594 MB to and fro, take 104.5
+// us, 84 % of a copy's rate, by instructions as much (62 % of all issue slots); in registers, without shared memory, they
+// took 114.  64 rows take 3.4 us, a launch and the reads that wait for one another; 32 trees of 64 rows 10.8.
 struct NormArgs : AppendArgs {
     const float* norm[2];      // of keys and of queries; null: not normed
     const int32_t* positions;  // null: the slots' numbers

@@ -498,11 +498,11 @@ DG_API dg_status dg_kv_append_norm(const uint16_t* k, int64_t ldk, const uint16_
  *             queries raises DG_DEV_BAD_PARAM and is skipped; the other refusals are the same.
  * A row that sees no key at all gets 0 and an lse of -inf.  A node that no query of its sequence sees, and context
  * that no query sees, may hold anything; a value that some queries see and others not must be finite.
- * Scores, maxima and sums are in fp32; the weights are rounded to bf16 for the product with v, which is divided by
- * the sum of the unrounded ones.
+ * Scores, maxima and sums are in fp32; the weights are rounded to bf16 for the product with v.  The product is divided
+ * by the sum of the unrounded weights, or, in calls of few rows a key head, of the rounded ones; lse is the unrounded ones'.
  *   workspace (device) >= dg_tree_attention_workspace_bytes(), 16-byte aligned, no initial contents; calls that
  *             overlap on the GPU need their own.  The size never falls as n_seq or max_q_len grow.
- * Limits and errors as dg_paged_attention; max_q_len <= 65536.  At most two kernels. */
+ * Limits and errors as dg_paged_attention; max_q_len <= 65536.  Two kernels. */
 DG_API size_t dg_tree_attention_workspace_bytes(int32_t n_seq, int32_t max_q_len, int32_t Hq, int32_t Hkv, int32_t D);
 DG_API dg_status dg_tree_attention(const uint16_t* q, const dg_paged_kv* cache, uint16_t* o, float* lse,
                                    const int32_t* cu_q, const uint32_t* tree_mask, int32_t mask_words,
@@ -529,8 +529,8 @@ DG_API dg_status dg_sink_attention(const uint16_t* q, const dg_paged_kv* cache, 
  *     leaves p_v without x_c (a token tried before has nothing left; all of p_v where nothing is left).
  * An accepted child is the next v.  Where none is, the walk ends, and the next token is the smallest t with
  * sum_{t' <= t} left(t') > next_uniforms[s] * sum left.  With temperature 0 a child is accepted iff its token is the
- * smallest argmax of the row, which is also the next token; the random numbers are not read.  Of draft
- * distributions so verified the produced tokens have the target's.
+ * smallest argmax of the row, which is also the next token; the random numbers are not read.  With drafts drawn
+ * from draft_probs and independent uniform numbers the produced tokens are distributed as the target's own.
  *   logits    (device) [total][ld] of dtype, 16-byte aligned, ld >= V, ld * sizeof(dtype) a multiple of 16; columns
  *             from V on do not count.  Only rows that the walk comes to are read.
  *   tokens    (device) [total] int32, the roots' unused; one outside [0, V) is never accepted.
