@@ -6,6 +6,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -43,7 +44,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Acceptance compares fp32 sums, unless they come within their own bound of the border: then the row is summed
 // like the last one (kSum) and compared again.
 //
-// Measured: one chain of 5 drafts over 32768 tokens, bf16, 15 to 18 us by what is accepted: a node takes about 4, the row's
+// Measured: one chain of 5 drafts over 32768 tokens, bf16, 13 to 16 us by what is accepted: a node takes 3 to 4, the row's
 // maximum, its sum and the two trips to and from the lead.  64 trees of 32 over 262144 tokens 60 us, where the bytes of the
 // rows walked take 8: the sums of a row that decides, some 47 lane cycles a token, and sequences that walk further than
 // others.  With weights in plain instead of packed pairs of fp32 67 us, with CTAs of 256 threads, two an SM, 67 too.
@@ -1000,8 +1001,22 @@ extern "C" dg_status dg_verify_drafts(const void* logits, dg_dtype dtype, int64_
     a.status = dghost::status_word();
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
-    int cluster = 8;
-    while (cluster > 1 && (int64_t)n_seq * cluster > 4 * (int64_t)sms) cluster /= 2;
+    // As many CTAs a sequence as run at once, four an SM; sixteen only for few sequences, since such clusters do not fill
+    // the GPU.  Measured (us with 16 / 8 / 4 / 2 CTAs), chains of 5 over 32k tokens: one 13.2 / 14.6 / 18.3 / 24.9, 24 21.3 /
+    // 23.3, 37 29.4 / 23.7, 300 167 / 96 / 74 / 66; trees of 32 over 262k: 16 29.4 / 40.6, 64 71 / 61 / 87 / 146, 128 121 / 102 /
+    // 110 / 164.
+    int cluster = (int64_t)n_seq * 32 <= 5 * (int64_t)sms ? kMaxCluster : 8;
+    while (cluster > 1 && cluster <= 8 && (int64_t)n_seq * cluster > 4 * (int64_t)sms) cluster /= 2;
+    // clusters past 8 are asked for once a device
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return DG_ERR_CUDA;
+    if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1u)) {
+        if (cudaFuncSetAttribute(k_verify<uint16_t>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaFuncSetAttribute(k_verify<float>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return DG_ERR_CUDA;
+        if (dev <= 63) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)n_seq * cluster);
     cfg.blockDim = dim3(kVThreads);

@@ -596,7 +596,9 @@ extern "C" dg_status dg_kv_append_norm(const uint16_t* k, int64_t ldk, const uin
     a.eps = eps;
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
-    const bool small = total_q * a.tasks <= (int64_t)sms * 2048;
+    // One group of heads a warp while they all run at once, then eight (us one / eight, rows of 16 / 8 heads of 128: 64 3.6 /
+    // 5.9, 256 4.1 / 6.0, 512 5.3 / 6.2, 1024 8.5 / 7.0).
+    const bool small = total_q * a.tasks <= (int64_t)sms * 1152;
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (D == 64)

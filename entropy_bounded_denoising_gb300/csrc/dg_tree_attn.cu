@@ -6,7 +6,7 @@
 // the first tokens that stay visible, then those from the window's (or the context's) first to its last key.  All
 // tiles of all items, in order, form one line that is cut into equal runs, one for each of the resident CTAs; a
 // run's first and last items may be pieces, which go to the workspace as (maximum, sum, unnormalised output)
-// and are joined by a second kernel in the order of the line.  Where there are many items a run takes whole ones.
+// and are joined by a second kernel in the order of the line.
 //
 // A CTA (two an SM; one for heads of 256):
 //   warp 0      walks the run, publishes its pieces in a ring and copies their queries, and their keys and
@@ -20,7 +20,7 @@
 // Measured: 32 trees of 64 nodes over up to 4k keys, 16 / 8 heads of 128: 82 us, where their bytes take 53 and the same
 // call with all keys in L2 takes 61: start and join take 12, the rest is the copies' (4.9 TB/s; a ring of four tiles
 // for five 84, copies asked into L2 three to eight tiles ahead 89 to 108).  9 trees of 199 nodes through windows of 2500,
-// 20 / 4 heads of 256: 102.5 us, 610 TFLOP/s; two prompts of 4000 through windows of 1500, 8 / 4 heads of 64: 52 us, 400
+// 20 / 4 heads of 256: 102.5 us, 610 TFLOP/s; two prompts of 4000 through windows of 1500, 8 / 4 heads of 64: 50.5 us, 410
 // TFLOP/s: both are bound by a tile's chain of steps in the softmax, about 1500 cycles a CTA.  A warp's wait by one lane
 // and a shuffle, for all lanes' own, made that 10 % longer (111 and 57 us).
 #include <cuda.h>
@@ -144,7 +144,7 @@ struct __align__(8) TreeShared {
     uint64_t wfull[kRing], wempty[kRing];
     uint64_t met;                 // the four softmax warps' own barrier (bounded, unlike bar.sync)
     uint64_t seen[2][4];          // of a masked tile, by warp: the keys some row sees
-    int64_t sums[kThreads / 32], items[kThreads / 32];
+    int64_t sums[kThreads / 32];
     int64_t found_start;
     Piece piece[kRing];           // nt 0: no more
     int32_t top_position[2][8];   // by warp: the last and the first position of its rows
@@ -238,7 +238,6 @@ DG_DEVINL SeqLine seq_line(const TreeArgs& a, const RawSeq& x) {
 struct Run {
     int64_t per_cta, start, end, seq_start;
     int seq;
-    bool whole;      // items are not cut: a run has those that begin in it
     bool zeros;      // some sequence has queries and no keys
 };
 
@@ -257,63 +256,24 @@ DG_DEVINL int64_t warp_scan(int64_t v) {   // inclusive
     return v;
 }
 
-// Runs shorter than this many tiles cost more in pieces than they gain.
+// Tiles of a run, at least (us for 2 / 4 / 8 tiles, trees of 64 nodes, 8 key heads of 128: one over 300 keys 20.8 / 22.0 / 28.1,
+// over 4096 26.7 / 23.2 / 24.5, two over 1000 21.7 / 23.9 / 26.9, eight over 300 18.4 / 20.1 / 27.6).
 constexpr int kMinRun = 2;
 
-DG_DEVINL void cut(Run& r, int64_t total, int64_t items) {
+DG_DEVINL void cut(Run& r, int64_t total) {
     r.per_cta = max((int64_t)kMinRun, total < (1LL << 31) ? (int64_t)(((uint32_t)total + gridDim.x - 1) / gridDim.x)
                                                           : (total + gridDim.x - 1) / gridDim.x);
     r.start = min(total, (int64_t)blockIdx.x * r.per_cta);
     r.end = min(total, r.start + r.per_cta);
-    r.whole = items >= 8 * (int64_t)gridDim.x;
     r.seq = 0;
     r.seq_start = 0;
 }
 
-// The run of a call of few sequences, found by one warp while the others wait for its pieces.
-constexpr int kFew = 4;
-DG_DEVINL Run find_run_warp(const TreeArgs& a) {
-    const int lane = threadIdx.x & 31;
-    int64_t c[kFew];
-    int64_t sum = 0;
-    int items = 0;    // (query tiles of 128 sequences: below 2^31 together, as their queries are)
-    bool zeros = false;
-    RawSeq raw[kFew];
-#pragma unroll
-    for (int k = 0; k < kFew; ++k) raw[k] = raw_seq(a, k * 32 + lane);
-#pragma unroll
-    for (int k = 0; k < kFew; ++k) {
-        c[k] = 0;
-        if (k * 32 >= a.n_seq) continue;
-        const SeqLine p = seq_line(a, raw[k]);
-        if (blockIdx.x == 0 && !p.seq.ok) dg::raise_status(a.status, DG_DEV_BAD_PARAM);
-        c[k] = p.cost(a);
-        zeros = zeros || (p.seq.ok && p.seq.kl == 0 && p.seq.ql > 0);
-        sum += c[k];
-        items += p.q_tiles;
-    }
-    Run r;
-    cut(r, warp_sum(sum), (int64_t)__reduce_add_sync(0xffffffffu, items) * a.head_tiles * a.Hkv);
-    r.zeros = __any_sync(0xffffffffu, zeros);
-    int64_t base = 0;
-#pragma unroll
-    for (int k = 0; k < kFew; ++k) {
-        if (k * 32 >= a.n_seq) break;
-        const int64_t incl = base + warp_scan(c[k]);
-        const uint32_t hit = __ballot_sync(0xffffffffu, incl - c[k] <= r.start && r.start < incl);
-        if (hit) {
-            r.seq = k * 32 + __ffs(hit) - 1;
-            r.seq_start = __shfl_sync(0xffffffffu, incl - c[k], __ffs(hit) - 1);
-        }
-        base = __shfl_sync(0xffffffffu, incl, 31);
-    }
-    return r;
-}
-
-// Of many: the whole CTA.  Two passes over the sequences' costs, the second up to the one that the run begins in.
+// The whole CTA: two passes over the sequences' costs, the second up to the one that the run begins in.  (By one warp
+// alone, while the others wait for its pieces, within 1 % for 1 to 100 sequences.)
 DG_DEVINL Run find_run(const TreeArgs& a, TreeShared& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t mine = 0, first = 0, items = 0;
+    int64_t mine = 0, first = 0;
     bool zeros = false;
 #pragma unroll 4
     for (int s = tid; s < a.n_seq; s += kThreads) {
@@ -323,25 +283,16 @@ DG_DEVINL Run find_run(const TreeArgs& a, TreeShared& sh) {
         zeros = zeros || (p.seq.ok && p.seq.kl == 0 && p.seq.ql > 0);
         if (s == tid) first = c;
         mine += c;
-        items += p.q_tiles;
     }
     mine = warp_sum(mine);
-    items = warp_sum(items);
-    if (lane == 0) {
-        sh.sums[warp] = mine;
-        sh.items[warp] = items;
-    }
+    if (lane == 0) sh.sums[warp] = mine;
     Run r;
     r.zeros = __syncthreads_or(zeros);
     int64_t total = 0;
-    items = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        total += sh.sums[w];
-        items += sh.items[w];
-    }
+    for (int w = 0; w < kThreads / 32; ++w) total += sh.sums[w];
     __syncthreads();
-    cut(r, total, items * a.head_tiles * a.Hkv);
+    cut(r, total);
     if (r.start >= r.end) return r;   // the same for the whole CTA
     int64_t base = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += kThreads) {
@@ -375,7 +326,6 @@ DG_DEVINL Run find_run(const TreeArgs& a, TreeShared& sh) {
 struct Walk {
     int64_t begin, at, end, per_cta;   // of the item on the line; where the run is in it
     int s, hk, qt, ht;
-    bool whole;
     SeqLine p;
     RawSeq next_raw;                   // of the sequence behind it
 
@@ -383,7 +333,6 @@ struct Walk {
         end = r.end;
         at = r.start;
         per_cta = r.per_cta;
-        whole = r.whole;
         s = r.seq;
         hk = qt = ht = 0;
         begin = r.seq_start;
@@ -409,10 +358,10 @@ struct Walk {
 
     DG_DEVINL bool next(const TreeArgs& a, Piece& z) {
         while (at < end) {
-            const int64_t to = whole ? begin + p.len : min(end, begin + p.len);
+            const int64_t to = min(end, begin + p.len);
             const int t0 = (int)(at - begin);
             const Range r = range_of(a, p.seq, qt);
-            const bool skip = whole ? t0 != 0 : t0 >= r.nt;
+            const bool skip = t0 >= r.nt;   // past the item's last tile: the line has room for the longest
             if (!skip) {
                 z.s = s;
                 z.hk = hk;
@@ -542,10 +491,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0);
     dg::pdl_wait();
     dg::pdl_release();
-    // With few sequences warp 0 finds the run by itself.
-    const bool few = a.n_seq <= 32 * kFew;
-    Run run;
-    if (!few) run = find_run(a, sh);
+    const Run run = find_run(a, sh);
     const uint32_t sQ = dg::smem_u32(smem + C::kOffQ);
 
     if (warp == 0) {
@@ -565,7 +511,6 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
         const int my_tile = lane / boxes, my_box = lane - my_tile * boxes;   // as a holder
         const int box = min(lane, boxes - 1);                                // as a copier
         const uint32_t q_bytes = (uint32_t)(a.hpt * a.qpt) * kSub * 2 * kCols;
-        if (few) run = find_run_warp(a);
         if (lane == 0) sh.zeros = run.zeros;
         Walk walk;
         walk.start(a, run);
