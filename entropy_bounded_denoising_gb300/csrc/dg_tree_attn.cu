@@ -20,9 +20,10 @@
 // Measured: 32 trees of 64 nodes over up to 4k keys, 16 / 8 heads of 128: 82 us, where their bytes take 53 and the same
 // call with all keys in L2 takes 61: start and join take 12, the rest is the copies' (4.9 TB/s; a ring of four tiles
 // for five 84, copies asked into L2 three to eight tiles ahead 89 to 108).  9 trees of 199 nodes through windows of 2500,
-// 20 / 4 heads of 256: 102.5 us, 610 TFLOP/s; two prompts of 4000 through windows of 1500, 8 / 4 heads of 64: 50.5 us, 410
-// TFLOP/s: both are bound by a tile's chain of steps in the softmax, about 1500 cycles a CTA.  A warp's wait by one lane
-// and a shuffle, for all lanes' own, made that 10 % longer (111 and 57 us).
+// 20 / 4 heads of 256: 96.8 us, 646 TFLOP/s; two prompts of 4000 through windows of 1500, 8 / 4 heads of 64: 50.4 us, 411
+// TFLOP/s: both are bound by a tile's chain of steps, in the softmax 1300 to 1500 cycles, and at heads of 256 the product
+// S, which reads the queries again for every 64 keys (700 cycles).  Waits by one lane and a shuffle, for all lanes' own,
+// made the chain 10 % longer.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
