@@ -21,9 +21,9 @@
 // call with all keys in L2 takes 61: start and join take 12, the rest is the copies' (4.9 TB/s; a ring of four tiles
 // for five 84, copies asked into L2 three to eight tiles ahead 89 to 108).  9 trees of 199 nodes through windows of 2500,
 // 20 / 4 heads of 256: 96.8 us, 646 TFLOP/s; two prompts of 4000 through windows of 1500, 8 / 4 heads of 64: 50.4 us, 411
-// TFLOP/s: both are bound by a tile's chain of steps, in the softmax 1300 to 1500 cycles, and at heads of 256 the product
-// S, which reads the queries again for every 64 keys (700 cycles).  Waits by one lane and a shuffle, for all lanes' own,
-// made the chain 10 % longer.
+// TFLOP/s: both are bound by a tile's chain of steps, in the softmax 1300 to 1400 cycles, at heads of 256 S 700.
+// Waits by one lane and a shuffle, for all lanes' own, made the chain 10 % longer.  At heads of 256 the queries in tensor
+// memory changed the 96.8 us to 95.8, and two softmax warps a quarter of the rows, each for half of a tile's keys, to 99.7.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
