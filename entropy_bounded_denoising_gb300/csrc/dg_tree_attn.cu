@@ -943,8 +943,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
     for (int e = 0; e < Q; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     // adds a piece (maximum, sum, output) to the thread's
     auto add = [&](float2 ml, const float4 (&v)[Q]) {
-        if (ml.x == -INFINITY) return;   // the row saw nothing of it, whatever its values
-        const float m = fmaxf(M, ml.x), f0 = M == -INFINITY ? 0.f : ex2(M - m), f1 = ex2(ml.x - m);
+        if (ml.x == -INFINITY && ml.y == 0.f) return;   // the row saw nothing of it, whatever its values
+        // (a maximum of -inf beside a sum that is a NaN: all it saw there were NaNs, which it keeps)
+        const float m = fmaxf(M, ml.x), f0 = M == -INFINITY ? 1.f : ex2(M - m), f1 = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
         M = m;
         L = L * f0 + ml.y * f1;
 #pragma unroll

@@ -1,0 +1,80 @@
+"""GPU tests of the calls for drafted tokens at their edges: NaN where somebody sees it."""
+import math
+
+import pytest
+import torch
+
+import draft_ref as dref
+import serving_ref as ref
+from test_gpu_draft import _run_attention, _tree_batch
+
+pytestmark = pytest.mark.gpu
+
+import entropy_bounded_denoising_gb300 as dg  # noqa: E402
+
+DEV = "cuda"
+I32 = dict(dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ NaN in sight
+def _attend_only(b, mask, pos, window, sinks):
+    """o and lse of a batch, without a comparison."""
+    o = torch.full((b.total, b.Hq, b.D), 5.0, dtype=ref.BF16, device=DEV)
+    lse = torch.full((b.total, b.Hq), 5.0, device=DEV)
+    max_q = max(s[0] for s in b.seqs)
+    dg.dg_clear_device_status()
+    if mask is not None:
+        dg.dg_tree_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, mask, max_q, lse=lse, window=window,
+                             sinks=sinks, positions=pos if window >= 0 else None)
+    else:
+        dg.dg_sink_attention(b.q, b.k_cache, b.v_cache, o, b.table, b.cu, b.kv_len, max_q, lse=lse, window=window, sinks=sinks)
+    assert dg.dg_get_device_status() == 0
+    return o, lse
+
+
+# (nodes, keys) of the sequences: few rows a key head and many; one request over a long context, whose items many CTAs
+# share; several whose items are cut between the first tokens and the window; items that one CTA has whole
+NAN_CASES = [("few", [(4, 900), (1, 70), (3, 3)]), ("long", [(64, 9000)]), ("cut", [(33, 300)] * 5),
+             ("whole", [(64, 64), (40, 41)] * 40)]
+
+
+@pytest.mark.parametrize("tree", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 8, 128), (8, 4, 64), (6, 2, 256)])
+@pytest.mark.parametrize("name,seqs", NAN_CASES, ids=[c[0] for c in NAN_CASES])
+def test_nan_that_a_row_sees(name, seqs, Hq, Hkv, D, tree):
+    """A NaN query, or a NaN key that a row sees, makes that row's o and lse NaN, wherever its item is cut; every other
+    row is right."""
+    window, sinks = (40, 1) if name == "cut" or not tree else (-1, 0)
+    b, oks, mask, pos = _tree_batch(seqs, Hq, Hkv, D, 16, 17, window, sinks)
+    if not tree:
+        mask, oks = None, [dref.visible(a, m, window=window, sinks=sinks) for a, m in seqs]
+    o0, l0 = _run_attention(b, oks, mask=mask, positions=pos if tree and window >= 0 else None, window=window, sinks=sinks)
+    cu, group, s = b.cu.tolist(), Hq // Hkv, len(seqs) // 2
+    a, m = seqs[s]
+
+    def attend(rows_heads):   # [total, Hq]: the rows that have to be NaN; the rest of the outputs
+        o, lse = _attend_only(b, mask, pos, window, sinks)
+        assert torch.isnan(o[rows_heads]).all() and torch.isnan(lse[rows_heads]).all()
+        o[rows_heads], lse[rows_heads] = o0[rows_heads], l0[rows_heads]
+        return o, lse
+
+    # a query: NaN as a whole, and in one dimension
+    for row, head, dims in ((cu[s], Hq - 1, slice(0, D)), (cu[s + 1] - 1, 0, slice(D - 1, D))):
+        bad = torch.zeros((b.total, Hq), dtype=torch.bool, device=DEV)
+        bad[row, head] = True
+        old = b.q[row, head].clone()
+        b.q[row, head, dims] = math.nan
+        o, lse = attend(bad)
+        b.q[row, head] = old
+        dref.check_attention(b, o, lse, oks)
+    # a key of one key head: the first of all (with a window the first token that stays), the context's last, a node
+    for j in sorted({0, max(0, m - a - 1), m - 1}):
+        at = b.slots(s, [j])
+        old = b.k_cache[at[0], at[1], Hkv - 1].clone()
+        b.k_cache[at[0], at[1], Hkv - 1] = math.nan
+        bad = torch.zeros((b.total, Hq), dtype=torch.bool, device=DEV)
+        bad[cu[s]:cu[s + 1], (Hkv - 1) * group:] = oks[s][:, j].to(DEV)[:, None]
+        assert bad.any()
+        o, lse = attend(bad)
+        b.k_cache[at[0], at[1], Hkv - 1] = old
+        dref.check_attention(b, o, lse, oks)
