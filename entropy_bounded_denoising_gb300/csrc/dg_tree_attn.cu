@@ -5,8 +5,12 @@
 // keys share a tile, so keys and values are read once for 128 / (Hq / Hkv) queries.  It visits tiles of 64 keys: those of
 // the first tokens that stay visible, then those from the window's (or the context's) first to its last key.  All
 // tiles of all items, in order, form one line that is cut into equal runs, one for each of the resident CTAs; a
-// run's first and last items may be pieces, which go to the workspace as (maximum, sum, unnormalised output)
+// run's first and last items may be pieces, which go to the workspace as (maximum, sums, unnormalised output)
 // and are joined by a second kernel in the order of the line.
+//
+// The weights are rounded to bf16 for the product with V, so the product is divided by the sum of the rounded ones: a row
+// is then an exact mean of the values it sees, with weights off by half a bf16 step.  Divided by the unrounded sum the
+// mean itself is off by as much again (values that are all alike came out a step away).  lse takes the unrounded sum.
 //
 // A CTA (two an SM; one for heads of 256):
 //   warp 0      walks the run, publishes its pieces in a ring and copies their queries, and their keys and
@@ -68,7 +72,7 @@ struct TreeArgs {
     int32_t by_slot, mul2, mul3, mul8;   // its coordinates: (0, by_slot * slot, mul2 * head, mul3 * head + mul8 * (slot / 8), page)
     dg::PagedKV kv;
     float4* part_o;             // [grid][2][D / 4][rows]
-    float2* part_ml;            // [grid][2][rows]: maximum, sum
+    float4* part_ml;            // [grid][2][rows]: maximum, sum of the weights, of the rounded weights
     int4* desc;                 // [grid][2]: CTAs that follow (0: nothing to join), first query's row, first head, queries; heads
     unsigned* status;
 };
@@ -77,8 +81,14 @@ template <int D>
 struct TreeCfg {
     static constexpr uint32_t kQBytes = (D / kSub) * kQSub, kKVBytes = kKeys * D * 2;
     static constexpr uint32_t kBufs = D == 64 ? 10 : 5;     // tiles of keys or values on their way or in use
-    static constexpr uint32_t kOffQ = 0, kOffKV = kQBytes, kOffBar = kOffKV + kBufs * kKVBytes;
-    static constexpr uint32_t kColS = 0, kColO = 64, kColP = 64 + D;
+    // The rounded weights' sum: for heads of 64 by the product, whose values have 16 more columns, all ones; for heads of 128
+    // tensor memory has no room for them, for heads of 256 an instruction, and the softmax adds (for heads of 64 4 us
+    // more of 50).
+    static constexpr bool kSumsByProduct = D == 64;
+    static constexpr int kValueCols = D + (kSumsByProduct ? 16 : 0);
+    static constexpr uint32_t kOffQ = 0, kOffKV = kQBytes, kOffOnes = kOffKV + kBufs * kKVBytes,
+                              kOffBar = kOffOnes + (kSumsByProduct ? 2 * kAtom : 0);
+    static constexpr uint32_t kColS = 0, kColO = 64, kColL = kColO + D, kColP = kColO + kValueCols;
     static constexpr uint32_t kTmemCols = D == 256 ? 512 : 256;
     static constexpr int kCtasPerSm = D == 256 ? 1 : 2;
     static constexpr int kMaxCtas = D == 256 ? 256 : 512;   // grid bound the workspace is sized for
@@ -110,6 +120,12 @@ DG_DEVINL uint64_t f2_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+// a and b plus the two halves of a pair, in fp32.
+DG_DEVINL void add_bf16x2(uint32_t pair, float& a, float& b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.rn.f32.bf16 %0, lo, %0;\n\tadd.rn.f32.bf16 %1, hi, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(pair));
 }
 
 // A run's part of one item.
@@ -482,6 +498,11 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
         sh.abort_flag = 0;
         dg::fence_mbar_init();
     }
+    if constexpr (C::kSumsByProduct) {
+        if (threadIdx.x < 2 * kAtom / 16)
+            reinterpret_cast<uint4*>(smem + C::kOffOnes)[threadIdx.x] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+        dg::fence_proxy_async_smem();
+    }
     if (warp == 1) {
         dg::tmem_alloc(&sh.tmem_base, kTmemCols);
         dg::tmem_relinquish();
@@ -613,7 +634,8 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
         if (dg::elect_leader()) {
             // S = Q K^T: both K-major, bit 13 negates Q; O += P V: the values' rows are N-major
             const uint32_t idS = dg::instr_desc(kTile, kKeys, false) | (a.negate ? 1u << 13 : 0u);
-            constexpr uint32_t idO = dg::instr_desc(kTile, D, true);
+            constexpr uint32_t idO = dg::instr_desc(kTile, C::kValueCols, true);
+            const uint32_t sOnes = dg::smem_u32(smem + C::kOffOnes);
             uint32_t g = 0;
             bool ok = true;
             for (uint32_t k = 0; ok && !aborted(sh); ++k) {
@@ -656,10 +678,12 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                         dg::tc_fence_after();
                         const uint32_t sV = dg::smem_u32(smem + C::kOffKV + at.slot * kKVBytes);
 #pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                        for (int kk = 0; kk < kKeys / 16; ++kk) {
+                            const uint32_t v = sV + (uint32_t)kk * 16u * D * 2u;   // 16 keys; the next 64 columns: kAtom on, or the ones
                             dg::tc_mma_f16_ts(tmem + kColO, tmem + kColP + (uint32_t)(st * 32 + kk * 8),
-                                              dg::smem_desc(sV + (uint32_t)kk * 16u * D * 2u, kAtom, (D / kSub) * kAtom, 128), idO,
+                                              dg::smem_desc(v, C::kSumsByProduct ? sOnes - v : kAtom, (D / kSub) * kAtom, 128), idO,
                                               (i > 1 || kk > 0) ? 1u : 0u);
+                        }
                         dg::tc_commit(&sh.pvdone[st]);
                         dg::tc_commit(&sh.empty[at.slot]);
                     }
@@ -717,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             const int all_lo = a.window < 0 ? 0 : max(0, top - a.window);   // from here on;
             const int any_lo = a.window < 0 ? 0 : max(0, low - a.window);   // some row from here on;
             const int row_lo = a.window < 0 ? 0 : max(0, pos - a.window), row_hi = a.mask ? ctx - 1 : pos;   // and this one
-            float m_ref = -INFINITY, l = 0.f;
+            float m_ref = -INFINITY, l = 0.f, lr = 0.f;   // lr: of the rounded weights
             for (int i = 0; i < nt; ++i) {
                 const uint32_t gi = g + (uint32_t)i;
                 if (!wait_warp(&sh.sfull, gi & 1u)) {
@@ -806,7 +830,12 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                         const float m_new = fmaxf(m_ref, tmax);
                         const float alpha = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);
                         l *= alpha;
+                        lr *= alpha;
                         if (i > 0) {
+                            if constexpr (C::kSumsByProduct) {
+                                const uint32_t ta = tmem + lane_base + C::kColL;
+                                dg::tmem_st1(ta, dg::tmem_ld1(ta) * alpha);
+                            }
 #pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 float o[32];
@@ -835,11 +864,17 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                             pk[c * 16 + e / 2] = pack_bf16x2(p0, p1);
                         }
                     }
+                    dg::tmem_st32u(tmem + lane_base + kColP + (gi & 1u) * 32u, pk);
+                    if constexpr (!C::kSumsByProduct) {   // the rounded weights' sum, while they are on their way
+                        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) add_bf16x2(pk[e], rs[2 * (e & 1)], rs[2 * (e & 1) + 1]);
+                        lr += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+                    }
                     float sa, sb;
                     f2_split(acc, sa, sb);
-                    dg::tmem_st32u(tmem + lane_base + kColP + (gi & 1u) * 32u, pk);
-                    dg::tmem_st_wait();
                     l += sa + sb;
+                    dg::tmem_st_wait();
                 }
                 dg::tc_fence_before();
                 __syncwarp();
@@ -854,7 +889,8 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
             dg::tc_fence_after();
             if (!idle) {
                 const bool whole = z.flags == (kStarts | kEnds);
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                if constexpr (C::kSumsByProduct) lr = dg::tmem_ld1(tmem + lane_base + C::kColL);
+                const float inv = lr > 0.f ? 1.f / lr : 0.f;
                 const int64_t out = qrow * a.Hq + z.h0 + (valid ? hi : 0);
                 const int64_t slot = (int64_t)blockIdx.x * 2 + (z.flags & kStarts ? 1 : 0);
 #pragma unroll 1
@@ -879,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, TreeCfg<D>::kCtasPerSm)
                     }
                 }
                 if (valid && whole && a.lse) a.lse[out] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
-                if (valid && !whole) a.part_ml[slot * a.rows + row] = make_float2(m_ref, l);
+                if (valid && !whole) a.part_ml[slot * a.rows + row] = make_float4(m_ref, l, lr, 0.f);
             }
             if (row == 0 && (z.flags & kStarts) && !(z.flags & kEnds)) {
                 a.desc[2 * blockIdx.x] = make_int4(z.last - (int)blockIdx.x, z.qrow, z.h0, z.nq);
@@ -926,7 +962,7 @@ template <int D, int kJoinThreads, int kAtOnce>
 __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
     constexpr int Q = kJoinDims / 4;
     __shared__ float4 s_o[kJoinThreads][Q];
-    __shared__ float2 s_ml[kJoinThreads];
+    __shared__ float4 s_ml[kJoinThreads];
     dg::pdl_wait();
     dg::pdl_release();
     const int c = blockIdx.x;
@@ -937,17 +973,18 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
     const int qi = row / a.hpt, hi = row - qi * a.hpt;
     const bool mine = group < groups && qi < d0.w && hi < nh;
     auto slot = [&](int i) -> int64_t { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
-    float M = -INFINITY, L = 0.f;
+    float M = -INFINITY, L = 0.f, Lr = 0.f;
     float4 o[Q];
 #pragma unroll
     for (int e = 0; e < Q; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    // adds a piece (maximum, sum, output) to the thread's
-    auto add = [&](float2 ml, const float4 (&v)[Q]) {
+    // adds a piece (maximum, sums, output) to the thread's
+    auto add = [&](const float4& ml, const float4 (&v)[Q]) {
         if (ml.x == -INFINITY && ml.y == 0.f) return;   // the row saw nothing of it, whatever its values
         // (a maximum of -inf beside a sum that is a NaN: all it saw there were NaNs, which it keeps)
         const float m = fmaxf(M, ml.x), f0 = M == -INFINITY ? 1.f : ex2(M - m), f1 = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
         M = m;
         L = L * f0 + ml.y * f1;
+        Lr = Lr * f0 + ml.z * f1;
 #pragma unroll
         for (int e = 0; e < Q; ++e) {
             o[e].x = o[e].x * f0 + v[e].x * f1;
@@ -958,12 +995,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
     };
     if (mine) {
         for (int i0 = group; i0 < n; i0 += kAtOnce * groups) {
-            float2 ml[kAtOnce];
+            float4 ml[kAtOnce];
             float4 v[kAtOnce][Q];
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 const int i = i0 + k * groups;
-                ml[k] = make_float2(-INFINITY, 0.f);
+                ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
                 if (i >= n) continue;
                 ml[k] = a.part_ml[slot(i) * a.rows + row];
 #pragma unroll
@@ -974,7 +1011,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
         }
     }
     if (group > 0) {
-        s_ml[threadIdx.x] = make_float2(M, L);
+        s_ml[threadIdx.x] = make_float4(M, L, Lr, 0.f);
 #pragma unroll
         for (int e = 0; e < Q; ++e) s_o[threadIdx.x][e] = o[e];
     }
@@ -986,7 +1023,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreeArgs a) {
         for (int e = 0; e < Q; ++e) v[e] = s_o[k * a.rows + row][e];
         add(s_ml[k * a.rows + row], v);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = Lr > 0.f ? 1.f / Lr : 0.f;
     const int64_t out = ((int64_t)d0.y + qi) * a.Hq + d0.z + hi;
     uint4* dst = reinterpret_cast<uint4*>(a.o + out * D + blockIdx.y * kJoinDims);
 #pragma unroll
@@ -1003,7 +1040,7 @@ int piece_rows(int32_t max_q_len, int32_t group) {
 }
 size_t piece_bytes(int32_t D, int rows) {
     const size_t ctas = D == 256 ? TreeCfg<256>::kMaxCtas : TreeCfg<128>::kMaxCtas;
-    return ctas * 32 + ctas * 2 * rows * ((size_t)D * 4 + 8);
+    return ctas * 32 + ctas * 2 * rows * ((size_t)D * 4 + 16);
 }
 
 // Whether a call takes the kernels for few rows (dg_tree_split.cu), whose items of 16 rows pass over the keys each; a tile
@@ -1097,7 +1134,7 @@ dg_status launch_tree(const dghost::TreeCall& c, void* workspace, cudaStream_t s
     const unsigned grid = (unsigned)std::min(sms * C::kCtasPerSm, C::kMaxCtas);
     a.desc = static_cast<int4*>(workspace);
     a.part_o = reinterpret_cast<float4*>(a.desc + 2 * C::kMaxCtas);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)C::kMaxCtas * 2 * (D / 4) * a.rows);
+    a.part_ml = reinterpret_cast<float4*>(a.part_o + (size_t)C::kMaxCtas * 2 * (D / 4) * a.rows);
     cudaError_t e = dghost::launch_pdl(k_tree<D>, dim3(grid), dim3(kThreads), tree_smem<D>(), stream, tq, tk, tv, a);
     dghost::count_launch();
     if (e != cudaSuccess) return DG_ERR_CUDA;

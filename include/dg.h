@@ -499,8 +499,8 @@ DG_API dg_status dg_kv_append_norm(const uint16_t* k, int64_t ldk, const uint16_
  * A row that sees no key at all gets 0 and an lse of -inf; one that is NaN, or sees a key that is, NaN in both.  A node that no
  * query of its sequence sees, and context that no query sees, may hold anything; a value that some queries see and others
  * not must be finite.
- * Scores, maxima and sums are in fp32; the weights are rounded to bf16 for the product with v.  The product is divided
- * by the sum of the unrounded weights, or, in calls of few rows a key head, of the rounded ones; lse is the unrounded ones'.
+ * Scores, maxima and sums are in fp32; the weights are rounded to bf16 for the product with v, which is divided by the sum
+ * of the rounded ones; lse is the unrounded ones'.
  *   workspace (device) >= dg_tree_attention_workspace_bytes(), 16-byte aligned, no initial contents; calls that
  *             overlap on the GPU need their own.  The size never falls as n_seq or max_q_len grow.
  * Limits and errors as dg_paged_attention; max_q_len <= 65536.  Two kernels. */
