@@ -369,12 +369,15 @@ PyObject* verify_drafts(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         if (!THPVariable_Check(a[0])) refuse(PyExc_TypeError, c.named("logits") + " must be a tensor");
         const at::ScalarType type = THPVariable_Unpack(a[0]).scalar_type();
         if (type != at::kBFloat16 && type != at::kFloat) refuse(PyExc_TypeError, "logits must be bfloat16 or float32");
-        // rows of any stride: the last dimension's elements follow each other
+        // rows of any stride: the last dimension's elements follow each other.  A single row's stride says how far apart the
+        // rows of its buffer lie, and counts where the library needs more columns than the row has and they lie there.
         auto rows = [&](PyObject* o, const char* name, at::ScalarType t, int64_t& ld) -> const at::Tensor& {
             const at::Tensor& x = c.tensor(o, name, t);
             if (x.dim() != 2 || (x.size(1) > 1 && x.stride(1) != 1))
                 refuse(PyExc_ValueError, c.named(name) + " must be [total, columns] with contiguous rows");
             ld = x.size(0) > 1 ? x.stride(0) : x.size(1);
+            const int64_t es = (int64_t)x.element_size(), held = (int64_t)x.storage().nbytes() / es - x.storage_offset();
+            if (x.size(0) == 1 && ld * es % 16 && x.stride(0) > ld && (ld * es + 15) / 16 * 16 <= held * es) ld = x.stride(0);
             return x;
         };
         int64_t ld, ldq = 0;

@@ -6,7 +6,7 @@ import torch
 
 import draft_ref as dref
 import serving_ref as ref
-from test_gpu_draft import _run_attention, _tree_batch
+from test_gpu_draft import Drafts, _run_attention, _tree_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,42 @@ def test_values_that_are_alike_stay_what_they_are(name, seqs, Hq, Hkv, D, tree):
     b.v_cache[:] = value
     o, _ = _attend_only(b, mask if tree else None, pos, window, sinks)
     assert torch.equal(o, value.expand_as(o)), float((o.double() / value.double() - 1).abs().max())
+
+
+# ------------------------------------------------------------------ verification
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [50257, 1001, 1000])
+def test_verify_columns_of_a_padded_buffer(V, dtype):
+    """The first V columns of padded logits and draft rows, for one row as for two, the buffer's last among them."""
+    pad = -(-V // 8) * 8
+    for sizes in ([1], [2], [1, 1]):
+        for at in (0, 3):
+            d = Drafts(sizes, V, V + at, T=0.8, dtype=dtype, probs=True)
+            want = Drafts(sizes, V, V + at, T=0.8, dtype=dtype, probs=True).run()
+            want.check()
+            # (columns of other requests before them, now and then)
+            buf = torch.full((3 + d.total, pad + at // 3 * 8), math.nan, dtype=dtype, device=DEV)[:, at // 3 * 8:]
+            probs = torch.full((3 + d.total, pad + at // 3 * 8), 0.5, device=DEV)[:, at // 3 * 8:]
+            rows = slice(at, at + d.total)
+            buf[rows, :V], probs[rows, :V] = d.x[:, :V].to(DEV), d.probs[:, :V].to(DEV)
+            count, path, out = torch.zeros(len(sizes), **I32), torch.zeros(d.total, **I32), torch.zeros(d.total, **I32)
+            dg.dg_verify_drafts(buf[rows, :V], d.tokens.to(DEV), d.cu, d.T.to(DEV), d.u.to(DEV), d.un.to(DEV), count, path, out,
+                                draft_probs=probs[rows, :V])
+            assert dg.dg_get_device_status() == 0
+            assert torch.equal(count, want.n_accept) and torch.equal(path, want.path) and torch.equal(out, want.out)
+
+
+def test_verify_one_row_without_a_buffer():
+    """A row of its own: its columns have to be whole pieces of 16 bytes, whatever stride it names."""
+    for V, ok in ((1000, True), (1001, False)):
+        row = torch.randn((1, V), device=DEV, dtype=torch.bfloat16)
+        for x in (row, row.as_strided((1, V), (V + 7 - (V + 7) % 8 + 8, 1))):   # (a stride with nothing behind it)
+            args = (x, torch.zeros(1, **I32), torch.tensor([0, 1], **I32), torch.ones(1, device=DEV), torch.zeros(1, device=DEV),
+                    torch.zeros(1, device=DEV), torch.zeros(1, **I32), torch.zeros(1, **I32), torch.zeros(1, **I32))
+            if ok:
+                dg.dg_verify_drafts(*args)
+                assert args[6].item() == 0
+            else:
+                with pytest.raises(dg.DGError):
+                    dg.dg_verify_drafts(*args)
+    dg.dg_clear_device_status()
