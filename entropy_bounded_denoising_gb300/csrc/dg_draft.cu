@@ -709,7 +709,9 @@ __global__ void __launch_bounds__(kVThreads, 4) k_verify(const __grid_constant__
     Command c{kStats, 0, 0, -1, 0, 0.f, 0.f, 0.f, 0, 0};
     Partial stats{};            // of the row at `node` (the lead's)
     int rejected = -1;          // the draft rejected there
-    for (uint32_t meeting = 0;; ++meeting) {
+    uint32_t meeting = 0;
+    bool met = true;            // false: a wait of this CTA ran out, for all its threads alike
+    for (;; ++meeting) {
         const T* row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + c.node) * a.ld;
         const float* q_row = c.draft >= 0 ? a.probs + (int64_t)(q0 + c.draft) * a.ldq : nullptr;
         Child k{false, -1, 0.f, 0.f, 0.f};
@@ -729,23 +731,18 @@ __global__ void __launch_bounds__(kVThreads, 4) k_verify(const __grid_constant__
                    dg::mapa_shared(&sh.parts, 0));
         }
         if (cta != 0) {
-            if (!dg::mbar_wait_cluster(&sh.told, meeting & 1u)) {
-                if (tid == 0) dg::raise_status(a.status, DG_DEV_TIMEOUT);
-                break;
-            }
+            met = __syncthreads_and(dg::mbar_wait_cluster(&sh.told, meeting & 1u));
+            if (!met) break;
             c = sh.cmd;
-            if (c.op == kExit) break;
-            if (c.op == kFind) {
-                break;
-            }
+            if (c.op == kExit || c.op == kFind) break;
             continue;
         }
 
         // The lead decides what comes next.
         Command next{kExit, c.node, 0, -1, 0, stats.top, 0.f, 0.f, 0, 0};
         bool finish = !walks, no_token = false;
-        if (!dg::mbar_wait_cluster(&sh.parts, meeting & 1u)) {   // (bounded; the others' waits run out as well)
-            if (tid == 0) dg::raise_status(a.status, DG_DEV_TIMEOUT);
+        met = __syncthreads_and(dg::mbar_wait_cluster(&sh.parts, meeting & 1u));
+        if (!met) {
             finish = true;
             walks = false;
         }
@@ -861,12 +858,24 @@ __global__ void __launch_bounds__(kVThreads, 4) k_verify(const __grid_constant__
         c = next;
         if (tid == 0) sh.cmd = next;
     }
-    if (c.op != kFind || c.cta != cta) return;
-    const T* row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + c.node) * a.ld;
-    if (c.draft >= 0)
-        find_token<T, true>(sh, row, a.probs + (int64_t)(q0 + c.draft) * a.ldq, cta, n_cta, a.out_tokens);
-    else
-        find_token<T, false>(sh, row, nullptr, cta, n_cta, a.out_tokens);
+    // This CTA sends nothing more.  None leaves before all have come so far, so that nobody sends into the memory of a CTA
+    // that is gone: also after a wait that ran out (all are bounded, so all come here), whose CTA then waits, as
+    // long again at most, for what may be on its way to it.
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // (no data to be seen behind it)
+    if (met && c.op == kFind && c.cta == cta) {
+        const T* row = reinterpret_cast<const T*>(a.logits) + (int64_t)(q0 + c.node) * a.ld;
+        if (c.draft >= 0)
+            find_token<T, true>(sh, row, a.probs + (int64_t)(q0 + c.draft) * a.ldq, cta, n_cta, a.out_tokens);
+        else
+            find_token<T, false>(sh, row, nullptr, cta, n_cta, a.out_tokens);
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (!met) {
+        if (tid == 0) dg::raise_status(a.status, DG_DEV_TIMEOUT);
+        (void)dg::mbar_wait_cluster(cta == 0 ? &sh.parts : &sh.told, meeting & 1u);
+    }
 }
 
 // ------------------------------------------------------------------ kept paths

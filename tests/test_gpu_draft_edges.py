@@ -134,3 +134,30 @@ def test_verify_one_row_without_a_buffer():
                 with pytest.raises(dg.DGError):
                     dg.dg_verify_drafts(*args)
     dg.dg_clear_device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [3, 40, 200, 500, 700])
+def test_verify_clusters_that_end_apart(n, dtype):
+    """Sequences of no nodes, refused ones, ones that end at the root and long walks side by side, in clusters of every size,
+    again and again on one stream: each as by itself, and no wait runs out."""
+    sizes = [(0, 1, 40, 3, 12)[i % 5] for i in range(n)]
+    V = 700
+    d = Drafts(sizes, V, n, T=0.5, dtype=dtype, near=1.0)
+    d.u *= 0.05
+    refused = [s for s in range(n) if s % 7 == 3 and sizes[s]]
+    for s in refused:
+        d.T[s] = -1.0
+    d.run()
+    d.check(status=dg.DG_DEV_BAD_PARAM if refused else 0, skip=refused)
+    n_acc = d.n_accept.tolist()
+    assert all(n_acc[s] == -1 for s in refused)
+    assert n < 40 or max(n_acc) > 5   # (of three sequences one alone has drafts)
+    x, tok, cu, T, u, un, _, _ = d.dev
+    want = d.n_accept.clone(), d.path.clone(), d.out.clone()
+    for _ in range(20):
+        got = [torch.full_like(t, -9) for t in want]
+        dg.dg_verify_drafts(x, tok, cu, T, u, un, *got, V=V)
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    assert dg.dg_get_device_status() & dg.DG_DEV_TIMEOUT == 0
+    dg.dg_clear_device_status()
