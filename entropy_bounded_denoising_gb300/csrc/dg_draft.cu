@@ -586,7 +586,8 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
     const int lane = threadIdx.x & 31;
     last = -1;
     // The sum's bound: its exponents' roundings (2^-23 of each, weighted by weights that fall faster than exponents
-    // grow), the exponentials (2^-22), the joins, this comparison, and 2^-24 an addition of a thread.
+    // grow), the exponentials (2^-22), the joins, this comparison, and 2^-24 an addition of a thread.  Every rejected sibling
+    // taken off it rounds once more, 2^-24 of it at most.
     const F sum = Exact ? (F)ldexp((double)st.fixed(), -a.frac) : (F)st.sum;
     const F slack = Exact ? (F)0 : sum * ((F)0x1p-15f + (F)a.V / (F)(n_cta * kVThreads) * (F)0x1p-23f);
     F left = sum;
@@ -628,7 +629,8 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
                 again = __any_sync(0xffffffffu, again);
                 if (!again) {
                     const F lhs = ut * (left > 0 ? left : (F)0);
-                    if (!Exact && fabsf((float)(lhs - wt)) <= (float)(ut * slack) && (ut > 0 || wt > 0)) return -2;
+                    const F bound = slack + sum * ((F)n_rejected * (F)0x1p-24f);
+                    if (!Exact && fabsf((float)(lhs - wt)) <= (float)(ut * bound) && (ut > 0 || wt > 0)) return -2;
                     if (lhs < wt) return base + from;
                     left -= wt;
                     if (lane == 0) sh.rejected[n_rejected] = t;

@@ -161,3 +161,21 @@ def test_verify_clusters_that_end_apart(n, dtype):
         assert all(torch.equal(g, w) for g, w in zip(got, want))
     assert dg.dg_get_device_status() & dg.DG_DEV_TIMEOUT == 0
     dg.dg_clear_device_status()
+
+
+def test_verify_many_rejected_siblings():
+    """A thousand siblings of 2^-24.03 of the mass each, rejected before the one in question: taken off an fp32 sum one by one
+    they vanish, 5.8e-5 of it together.  Uniform numbers between the border and where it would then lie, and beyond."""
+    us = [0.49999, 0.499995, 0.499999, 0.500001, 0.50001, 0.51, 0.4]
+    d = Drafts([1002] * len(us), 1100, 1, T=1.0, dtype=torch.float32, tree=True)
+    d.parents[:] = 0
+    d.x[:, :1100] = -math.inf
+    d.x[:, :2] = 0.0
+    d.x[:, 2:1002] = -23.03 * math.log(2)
+    d.u[:] = 0.9999
+    for s, u in enumerate(us):
+        d.tokens[1002 * s + 1:1002 * s + 1001] = torch.arange(2, 1002, dtype=torch.int32)
+        d.tokens[1002 * s + 1001] = 1
+        d.u[1002 * s + 1001] = u
+    d.run().check()
+    assert d.n_accept.tolist() == [int(u < 0.5) for u in us]
