@@ -608,6 +608,8 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
                 w = ex2((k.x - st.top) * sh.c_hi);
             }
         }
+        // Against 0 any probability wins, also one that is too small for its weight to be told from 0.
+        const uint32_t possible = __ballot_sync(0xffffffffu, k.is && k.x > -INFINITY);
         uint32_t todo = __ballot_sync(0xffffffffu, k.is);
         while (todo) {
             const int from = __ffs(todo) - 1;
@@ -620,7 +622,8 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
             }
             const F wt = __shfl_sync(0xffffffffu, w, from), ut = __shfl_sync(0xffffffffu, k.u, from);
             if (a.probs) {
-                const F m = ut * (F)__shfl_sync(0xffffffffu, k.q, from), lhs = m * sum;
+                const F q = (F)__shfl_sync(0xffffffffu, k.q, from), m = ut * q, lhs = m * sum;
+                if ((ut == 0 || q == 0) && (possible >> from & 1u)) return base + from;
                 if (!Exact && fabsf((float)(lhs - wt)) <= (float)(m * slack) && (lhs > 0 || wt > 0)) return -2;
                 if (lhs < wt) return base + from;
             } else {
@@ -628,6 +631,7 @@ DG_DEVINL int decide(VShared& sh, const VerifyArgs& a, const T* row, int q0, int
                 for (int i = lane; i < n_rejected; i += 32) again = again || sh.rejected[i] == t;
                 again = __any_sync(0xffffffffu, again);
                 if (!again) {
+                    if (ut == 0 && (possible >> from & 1u)) return base + from;
                     const F lhs = ut * (left > 0 ? left : (F)0);
                     const F bound = slack + sum * ((F)n_rejected * (F)0x1p-24f);
                     if (!Exact && fabsf((float)(lhs - wt)) <= (float)(ut * bound) && (ut > 0 || wt > 0)) return -2;

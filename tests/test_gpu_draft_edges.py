@@ -179,3 +179,38 @@ def test_verify_many_rejected_siblings():
         d.u[1002 * s + 1001] = u
     d.run().check()
     assert d.n_accept.tolist() == [int(u < 0.5) for u in us]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_verify_against_zero(dtype):
+    """u q or u m of 0 is below every probability that is not 0, also below those that fp32 does not hold."""
+    V, low = 50, [0.0, -84.5, -88.0, -90.0, -200.0, -600.0, -math.inf]
+
+    def rows(n, **kw):
+        d = Drafts(n, V, 3, T=1.0, dtype=dtype, **kw)
+        d.x[:, :V] = -math.inf
+        d.x[:, :len(low)] = torch.tensor(low, dtype=dtype)
+        d.x[:, 10] = 0.0
+        return d
+    # chains of one draft: u = 0; and a draft whose distribution gave it 0
+    d = rows([2] * len(low))
+    d.tokens[1::2] = torch.arange(len(low), dtype=torch.int32)
+    d.u[1::2] = 0.0
+    d.run().check()
+    assert d.n_accept.tolist() == [1] * (len(low) - 1) + [0]
+    d = rows([2] * len(low), probs=True)
+    d.tokens[1::2] = torch.arange(len(low), dtype=torch.int32)
+    d.probs[:] = 0.0
+    d.u[1::2] = 0.75
+    d.run().check()
+    assert d.n_accept.tolist() == [1] * (len(low) - 1) + [0]
+    # behind siblings that are impossible, rejected, or so near their border that the row is summed exactly
+    near = float(torch.nextafter(torch.tensor(0.5), torch.tensor(1.0)))
+    d = rows([4] * len(low), tree=True)
+    d.parents[:] = 0
+    for s in range(len(low)):
+        d.tokens[4 * s + 1:4 * s + 4] = torch.tensor([6, 10, s], dtype=torch.int32)
+        d.u[4 * s + 1:4 * s + 4] = torch.tensor([0.0, near, 0.0])
+    d.run().check()
+    assert d.n_accept.tolist() == [1] * (len(low) - 1) + [0]
+    assert d.path.view(-1, 4)[:-1, 1].tolist() == [3] * (len(low) - 1)
