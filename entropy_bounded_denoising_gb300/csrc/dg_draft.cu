@@ -1062,9 +1062,12 @@ extern "C" dg_status dg_kv_keep(const dg_paged_kv* cache, int32_t n_layers, int6
     KeepArgs a;
     const dg_status ok = dghost::paged_kv(cache, D, &a.kv);
     if (ok != DG_OK) return ok;
-    for (const int32_t* p : {cache->kv_len, n_accept}) {   // what other blocks of the sequence still read
+    // what other blocks, of this sequence and of others, still read
+    const std::pair<const int32_t*, int64_t> read[] = {{cache->kv_len, n_seq}, {n_accept, n_seq}, {cu_q, (int64_t)n_seq + 1},
+                                                       {path, total_q}, {cache->page_table, (int64_t)n_seq * cache->max_pages}};
+    for (const auto& [p, words] : read) {
         const uintptr_t from = reinterpret_cast<uintptr_t>(new_len), at = reinterpret_cast<uintptr_t>(p);
-        if (from < at + 4 * (uintptr_t)n_seq && at < from + 4 * (uintptr_t)n_seq) return DG_ERR_INVALID_ARG;
+        if (from < at + 4 * (uintptr_t)words && at < from + 4 * (uintptr_t)n_seq) return DG_ERR_INVALID_ARG;
     }
     if (n_layers > 1 && layer_stride % 8) return DG_ERR_ALIGNMENT;
     if (!dghost::on_multiple(cu_q, 4) || !dghost::on_multiple(path, 4) || !dghost::on_multiple(n_accept, 4) ||

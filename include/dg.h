@@ -567,7 +567,8 @@ DG_API dg_status dg_verify_drafts(const void* logits, dg_dtype dtype, int64_t ld
  *             multiple of 8 below 2^55, ignored for one layer), all with one page table.  The nodes' pages must not be
  *             shared with another sequence.
  *   path (device) [total_q] int32, n_accept (device) [n_seq] int32.
- *   new_len   (device, out) [n_seq] int32; must not overlap kv_len or n_accept, which other blocks still read.
+ *   new_len   (device, out) [n_seq] int32; must not overlap kv_len, n_accept, cu_q, path or the page table, which other
+ *             blocks still read.
  * A sequence whose offsets lie outside [0, total_q], with kv_len < q_len, kv_len > max_pages * page_size, n_accept
  * outside [-1, q_len), a path that does not ascend within [0, q_len), or a page it needs outside [0, n_pages) raises
  * DG_DEV_BAD_PARAM; nothing of it moves, and new_len = kv_len.
