@@ -1016,12 +1016,18 @@ extern "C" dg_status dg_verify_drafts(const void* logits, dg_dtype dtype, int64_
     a.status = dghost::status_word();
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
-    // As many CTAs a sequence as run at once, four an SM; sixteen only for few sequences, since such clusters do not fill
-    // the GPU.  Measured (us with 16 / 8 / 4 / 2 CTAs), chains of 5 over 32k tokens: one 13.2 / 14.6 / 18.3 / 24.9, 24 21.3 /
-    // 23.3, 37 29.4 / 23.7, 300 167 / 96 / 74 / 66; trees of 32 over 262k: 16 29.4 / 40.6, 64 71 / 61 / 87 / 146, 128 121 / 102 /
-    // 110 / 164.
-    int cluster = (int64_t)n_seq * 32 <= 5 * (int64_t)sms ? kMaxCluster : 8;
-    while (cluster > 1 && cluster <= 8 && (int64_t)n_seq * cluster > 4 * (int64_t)sms) cluster /= 2;
+    // CTAs of a sequence: as many as have a vector a thread of the row, and run at once: four an SM, three in clusters of sixteen,
+    // which do not fill the GPU.  Where a CTA's part of a row is long, several waves of larger clusters are as good.
+    // Measured (us with 16 / 8 / 4 / 2 / 1 CTAs), chains of 5 with draft rows: over 4k tokens 8 18.4 / 17.5 / 17.6 / 20.1, 300 - / 61 / 36 /
+    // 24 / 26; 32k: 1 13.9 / 15.0 / 18.0 / 23.1, 28 23.0 / 24.9, 37 30 / 24.6 / 30.1, 96 - / 40 / 37 / 48, 200 - / 66 / 57 / 62 / 84; 262k: 24 60 / 84,
+    // 48 94 / 102, 64 109 / 110 / 157, 200 - / 245 / 273 / 377, 600 - / 651 / 644 / 710 / 820.  Over 198 shapes (1 to 600 chains, trees of 32
+    // and single rows of 4k to 262k tokens) the rule loses 0.6 % to the best on average, at most 21 %.
+    const int64_t row_bytes = V * es;
+    int cluster = kMaxCluster;
+    while (cluster > 1 && cluster * (int64_t)kVThreads * 16 > row_bytes) cluster /= 2;
+    while (cluster > 1 &&
+           n_seq * (int64_t)cluster > (cluster > 8 ? 3 : 4) * (int64_t)sms * std::max<int64_t>(1, row_bytes / cluster / 16384))
+        cluster /= 2;
     // clusters past 8 are asked for once a device
     static std::atomic<uint64_t> ready{0};
     int dev = 0;

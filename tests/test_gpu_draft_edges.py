@@ -137,12 +137,12 @@ def test_verify_one_row_without_a_buffer():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("n", [3, 40, 200, 500, 700])
-def test_verify_clusters_that_end_apart(n, dtype):
+@pytest.mark.parametrize("n,V", [(3, 700), (40, 700), (200, 700), (500, 700), (700, 700),
+                                 (3, 20000), (40, 20000), (100, 20000), (200, 20000), (500, 20000)])
+def test_verify_clusters_that_end_apart(n, V, dtype):
     """Sequences of no nodes, refused ones, ones that end at the root and long walks side by side, in clusters of every size,
     again and again on one stream: each as by itself, and no wait runs out."""
     sizes = [(0, 1, 40, 3, 12)[i % 5] for i in range(n)]
-    V = 700
     d = Drafts(sizes, V, n, T=0.5, dtype=dtype, near=1.0)
     d.u *= 0.05
     refused = [s for s in range(n) if s % 7 == 3 and sizes[s]]
@@ -159,6 +159,11 @@ def test_verify_clusters_that_end_apart(n, dtype):
         got = [torch.full_like(t, -9) for t in want]
         dg.dg_verify_drafts(x, tok, cu, T, u, un, *got, V=V)
         assert all(torch.equal(g, w) for g, w in zip(got, want))
+    for s in range(n)[:: max(1, n // 6)]:   # alone, in the largest cluster its row takes
+        rows = slice(*d.cu[s:s + 2].tolist())
+        got = [torch.full_like(t, -9) for t in (want[0][s:s + 1], want[1][rows], want[2][rows])]
+        dg.dg_verify_drafts(x[rows], tok[rows], cu[s:s + 2] - cu[s], T[s:s + 1], u[rows], un[s:s + 1], *got, V=V)
+        assert torch.equal(got[0], want[0][s:s + 1]) and torch.equal(got[1], want[1][rows]) and torch.equal(got[2], want[2][rows])
     assert dg.dg_get_device_status() & dg.DG_DEV_TIMEOUT == 0
     dg.dg_clear_device_status()
 
