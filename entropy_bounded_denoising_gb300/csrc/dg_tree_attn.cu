@@ -1043,16 +1043,21 @@ size_t piece_bytes(int32_t D, int rows) {
     return ctas * 32 + ctas * 2 * rows * ((size_t)D * 4 + 16);
 }
 
-// Whether a call takes the kernels for few rows (dg_tree_split.cu), whose items of 16 rows pass over the keys each; a tile
-// here takes all of a key head's up to 128.  One pass: there.  Up to four: there while the passes of all
-// sequences are few, since a call here takes 10 us more to start and to join.  Measured (us there / here), heads of
-// 128, 8 key heads: 8 requests over 2.3k keys, 16, 24, 32, 64 rows a key head 21 / 27, 25 / 27.5, 28 / 28, 40 / 29; one over
-// 1k, 32 and 64 rows 13 / 20; 64 over 400 keys, 16 and 24 rows 34 / 37, 40 / 38; 32 over 4k keys, 16, 24, 32 rows 70 / 72,
-// 85 / 68, 102 / 68.  Heads of 64: 64 over 400 keys, 24 and 32 rows 30 / 34, 36 / 35; 32 over 4k, 17, 24, 32 rows 45 / 56,
-// 55 / 55, 64 / 56.  Heads of 256, 4 key heads: 8 over 2.3k keys, 16, 24, 32 rows 25 / 28, 29 / 30, 33 / 30.
+// Whether a call takes the kernels for few rows (dg_tree_split.cu), whose items of up to 16 rows pass over the keys each; a
+// tile here takes all of a key head's up to 128, and a call 10 us more to start and to join.  The lengths are not known to the
+// host.  Measured (us there / here), trees of one query head a key head, contexts of up to 400, 2300 and 8000 tokens:
+//   heads of 64: 32 sequences, 8 key heads, 17 rows 17.6 / 20.6, 35 / 34, 84 / 97, 20 rows 17.9 / 20.9, 43 / 34, 91 / 91; 4 sequences, 32 rows
+//     10.7 / 14.6, 16.2 / 16.1, 24.5 / 21.1;
+//   heads of 128: 32 sequences, 8 key heads, 16 rows 19.9 / 21.3, 49 / 47, 116 / 114, 20 rows 25.4 / 24.6, 62 / 48, 145 / 120; 4
+//     sequences, 20 rows 11.1 / 15.9, 18.4 / 19.2, 39 / 31; 2, 32 rows 11.1 / 21.0, 18.2 / 24.8, 33.2 / 33.5;
+//   heads of 256: 32 sequences, 4 key heads, 9 rows 22.2 / 24.0, 54 / 47, 131 / 124, 16 rows 23.9 / 21.2, 55 / 48, 124 / 115; 2
+//     sequences, 16 rows 12.5 / 22.2, 20.6 / 26.0, 27.7 / 30.3.
+// Over 2414 shapes (heads of 64, 128, 256, 1 to 8 key heads, 1 to 128 sequences, 9 to 64 rows) the rule loses 1.6 % to the
+// better path on average.  The most, 71 %, is 64 rows of short contexts (8 sequences, one key head of 256, 400 tokens 13.1 / 22.4),
+// which over 8000 tokens lose up to 40 % there.
 bool few_rows(int32_t n_seq, int32_t max_q_len, int32_t Hkv, int32_t group, int32_t D) {
-    const int64_t passes = ((int64_t)max_q_len * group + 15) / 16;
-    return passes == 1 || (passes <= 4 && n_seq * (int64_t)Hkv * passes * (D / 64) <= 256);
+    const int64_t rows = (int64_t)max_q_len * group;
+    return rows <= (D == 64 ? 18 : D == 128 ? 16 : 8) || (rows <= 64 && n_seq * (int64_t)Hkv * rows * D <= 98304);
 }
 
 template <int D>

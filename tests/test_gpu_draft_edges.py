@@ -219,3 +219,17 @@ def test_verify_against_zero(dtype):
     d.run().check()
     assert d.n_accept.tolist() == [1] * (len(low) - 1) + [0]
     assert d.path.view(-1, 4)[:-1, 1].tolist() == [3] * (len(low) - 1)
+
+
+# ------------------------------------------------------------------ the choice of path
+@pytest.mark.parametrize("seqs,Hq,Hkv,D", [([(17, 200), (1, 1), (9, 60)] * 30, 4, 4, 64), ([(18, 200)] * 50, 8, 8, 64),
+                                           ([(19, 200), (2, 30)] * 50, 8, 8, 64), ([(5, 90), (1, 2)] * 60, 12, 4, 128),
+                                           ([(3, 90), (4, 4)] * 60, 3, 1, 256), ([(2, 90)] * 70, 8, 2, 256),
+                                           ([(64, 500)], 8, 8, 128), ([(32, 400), (1, 9)], 16, 8, 64), ([(32, 77)] * 3, 4, 2, 256)])
+def test_paths_on_either_side_of_the_rule(seqs, Hq, Hkv, D):
+    """Calls near the number of rows, sequences and heads where the kernels for few rows hand over to those for many."""
+    for window, sinks in ((-1, 0), (30, 3)):
+        b, oks, mask, pos = _tree_batch(seqs, Hq, Hkv, D, 16, 29, window, sinks)
+        _run_attention(b, oks, mask=mask, positions=pos, window=window, sinks=sinks)
+        w, k = (window, sinks) if window >= 0 else (1000, 0)
+        _run_attention(b, [dref.visible(a, m, window=w, sinks=k) for a, m in seqs], window=w, sinks=k)
