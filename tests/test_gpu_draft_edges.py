@@ -221,6 +221,46 @@ def test_verify_against_zero(dtype):
     assert d.path.view(-1, 4)[:-1, 1].tolist() == [3] * (len(low) - 1)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_verify_draft_distribution_of_the_targets(dtype):
+    """A draft's distribution that is the target's, rounded to fp32: u just below 1 accepts (the rounding is at most 2^-24
+    of p, and within 2^-28 of that in one comparison of some 600).  Rejected all the same (a token outside the vocabulary),
+    its rounding alone is left, which weights within 2^-31 of p follow within 2^-30; with 1 everywhere nothing is left,
+    and the row itself counts."""
+    V, n = 400, 40
+
+    def make(**kw):
+        d = Drafts([3] * n, V, 5, T=1.0, probs=True, dtype=dtype, **kw)
+        for s in range(n):
+            for i in (1, 2):
+                d.probs[3 * s + i, :V] = torch.softmax(d.x[3 * s + i - 1, :V].double(), 0).float()
+        return d
+    d = make()
+    d.u[:] = 1 - 2.0 ** -24
+    d.run().check(allow=1)
+    assert (d.n_accept == 2).sum() >= n - 1
+    d = make()
+    d.tokens[1::3] = V
+    d.run()
+    assert dg.dg_get_device_status() == 0 and (d.n_accept == 0).all() and (d.out.view(n, 3)[:, 1:] == -1).all()
+    for s, t in enumerate(d.out[::3].tolist()):
+        p = torch.softmax(d.x[3 * s, :V].double(), 0)
+        assert float(p[t] - d.probs[3 * s + 1, t].double()) >= -2.0 ** -30 * float(p[t]), s
+    d = make()
+    d.tokens[1::3] = -1
+    d.probs[1::3] = 1.0
+    d.run().check()
+    assert (d.n_accept == 0).all()
+    d = make()                     # one token that has everything, in the row and in the draft's
+    d.x[:, :V] = -math.inf
+    d.x[:, 7] = 2.0
+    d.tokens[1::3] = 8
+    d.probs[1::3] = 0.0
+    d.probs[1::3, 7:9] = 1.0
+    d.run().check()
+    assert (d.out[::3] == 7).all()
+
+
 # ------------------------------------------------------------------ the choice of path
 @pytest.mark.parametrize("seqs,Hq,Hkv,D", [([(17, 200), (1, 1), (9, 60)] * 30, 4, 4, 64), ([(18, 200)] * 50, 8, 8, 64),
                                            ([(19, 200), (2, 30)] * 50, 8, 8, 64), ([(5, 90), (1, 2)] * 60, 12, 4, 128),
