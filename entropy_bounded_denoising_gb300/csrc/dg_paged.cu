@@ -278,7 +278,8 @@ DG_DEVINL float head_sum(float v) {
 }
 
 // 1 / sqrt(mean f^2 + eps) over a head.  A sum of squares past fp32 (values from 2^60 on) is taken of values 2^-70 as large,
-// beside which eps is nothing; f is then scaled.  (Whole warp; squares below fp32 are below eps, at least 2^-126.)
+// beside which eps is nothing unless it is as large (then for its own sake: the two might pass fp32 together); f is then
+// scaled.  (Whole warp; squares below fp32 are below eps, at least 2^-126.)
 template <int D>
 DG_DEVINL float norm_of(float (&f)[16], float eps) {
     float s0 = 0.f, s1 = 0.f;
@@ -288,7 +289,7 @@ DG_DEVINL float norm_of(float (&f)[16], float eps) {
         s1 = fmaf(f[e + 1], f[e + 1], s1);
     }
     float ss = head_sum<D / 16>(s0 + s1);
-    const bool large = !(ss <= 0x1p120f);   // (or a NaN, which stays one)
+    const bool large = !(ss <= 0x1p120f) || eps > 0x1p120f;   // (or a NaN, which stays one)
     if (__any_sync(0xffffffffu, large)) {
         if (large) {
             eps *= 0x1p-140f;

@@ -1,4 +1,4 @@
-"""GPU tests of the calls for drafted tokens at their edges: NaN where somebody sees it."""
+"""GPU tests of the calls for drafted tokens at their edges."""
 import math
 
 import pytest
@@ -6,7 +6,7 @@ import torch
 
 import draft_ref as dref
 import serving_ref as ref
-from test_gpu_draft import Drafts, _run_attention, _tree_batch
+from test_gpu_draft import Drafts, _append, _run_attention, _tree_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -259,6 +259,14 @@ def test_verify_draft_distribution_of_the_targets(dtype):
     d.probs[1::3, 7:9] = 1.0
     d.run().check()
     assert (d.out[::3] == 7).all()
+
+
+# ------------------------------------------------------------------ normed append
+@pytest.mark.parametrize("eps", [3.4028234663852886e38, 3.4e38, 2.0 ** 121, 2.0 ** 119])
+@pytest.mark.parametrize("scale", [1.0, 1e16, 1.1e18, 1e30])
+def test_append_norm_large_eps(scale, eps):
+    """eps near fp32's largest number, beside squares whose mean would take their sum past it."""
+    _append(ref.Batch([(7, 9, 1), (30, 64, 1)], 3, 1, 64, 16, seed=4, fill=0.0), 64, False, scale=scale, eps=eps)
 
 
 # ------------------------------------------------------------------ the choice of path
