@@ -44,10 +44,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Acceptance compares fp32 sums, unless they come within their own bound of the border: then the row is summed
 // like the last one (kSum) and compared again.
 //
-// Measured: one chain of 5 drafts over 32768 tokens, bf16, 13 to 16 us by what is accepted: a node takes 3 to 4, the row's
-// maximum, its sum and the two trips to and from the lead.  64 trees of 32 over 262144 tokens 60 us, where the bytes of the
-// rows walked take 8: the sums of a row that decides, some 47 lane cycles a token, and sequences that walk further than
-// others.  With weights in plain instead of packed pairs of fp32 67 us, with CTAs of 256 threads, two an SM, 67 too.
+// Measured: one chain of 5 drafts over 32768 tokens, bf16, 9 to 18 us by what is accepted: a node takes 3 to 4, the row's
+// maximum, its sum and the two trips to and from the lead.  64 trees of 32 over 262144 tokens 61 to 64 us, where the bytes of
+// the rows walked take 8: the sums of a row that decides, some 47 lane cycles a token, and sequences that walk further than
+// others.  With weights in plain instead of packed pairs of fp32 7 us more, with CTAs of 256 threads, two an SM, too.
 constexpr int kVThreads = 128, kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxNodes = 1024;
@@ -1016,15 +1016,17 @@ extern "C" dg_status dg_verify_drafts(const void* logits, dg_dtype dtype, int64_
     a.status = dghost::status_word();
     const int sms = dghost::sm_count();
     if (sms <= 0) return DG_ERR_CUDA;
-    // CTAs of a sequence: as many as have a vector a thread of the row, and run at once: four an SM, three in clusters of sixteen,
-    // which do not fill the GPU.  Where a CTA's part of a row is long, several waves of larger clusters are as good.
-    // Measured (us with 16 / 8 / 4 / 2 / 1 CTAs), chains of 5 with draft rows: over 4k tokens 8 18.4 / 17.5 / 17.6 / 20.1, 300 - / 61 / 36 /
-    // 24 / 26; 32k: 1 13.9 / 15.0 / 18.0 / 23.1, 28 23.0 / 24.9, 37 30 / 24.6 / 30.1, 96 - / 40 / 37 / 48, 200 - / 66 / 57 / 62 / 84; 262k: 24 60 / 84,
-    // 48 94 / 102, 64 109 / 110 / 157, 200 - / 245 / 273 / 377, 600 - / 651 / 644 / 710 / 820.  Over 198 shapes (1 to 600 chains, trees of 32
-    // and single rows of 4k to 262k tokens) the rule loses 0.6 % to the best on average, at most 21 %.
+    // CTAs of a sequence: as many as have a vector a thread of the row, two at least, and run at once: four an SM, three in
+    // clusters of sixteen, which do not fill the GPU.  Where a CTA's part of a row is long, several waves of larger clusters are as
+    // good.
+    // Measured (us with 16 / 8 / 4 / 2 / 1 CTAs), chains of 5 with draft rows: over 2k tokens 8 18.1 / 17.3 / 17.4 / 17.6 / 19.7, 600
+    // - / 113 / 63 / 40 / 28; 4k 300 - / 61 / 36 / 24 / 26; 32k 1 13.9 / 15.0 / 18.0 / 23.1, 28 23.0 / 24.9, 37 30 / 24.6 / 30.1, 96 - /
+    // 40 / 37 / 48, 200 - / 66 / 57 / 62 / 84; 262k 24 60 / 84, 48 94 / 102, 64 109 / 110 / 157, 200 - / 245 / 273 / 377, 600 - / 651 / 644 /
+    // 710 / 820.  Over 443 shapes (1 to 600 chains, trees of 32 and single rows of 1k to 262k tokens, bf16 and fp32) the rule
+    // loses 0.7 % to the best on average, at most 26 %.
     const int64_t row_bytes = V * es;
     int cluster = kMaxCluster;
-    while (cluster > 1 && cluster * (int64_t)kVThreads * 16 > row_bytes) cluster /= 2;
+    while (cluster > 2 && cluster * (int64_t)kVThreads * 16 > row_bytes) cluster /= 2;
     while (cluster > 1 &&
            n_seq * (int64_t)cluster > (cluster > 8 ? 3 : 4) * (int64_t)sms * std::max<int64_t>(1, row_bytes / cluster / 16384))
         cluster /= 2;
