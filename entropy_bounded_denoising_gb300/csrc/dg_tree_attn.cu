@@ -22,12 +22,14 @@
 // memory before the product (what they hold is nobody's, and 0 * NaN is not 0).
 //
 // Measured: 32 trees of 64 nodes over up to 4k keys, 16 / 8 heads of 128: 82 us, where their bytes take 53 and the same
-// call with all keys in L2 takes 61: start and join take 12, the rest is the copies' (4.9 TB/s; a ring of four tiles
-// for five 84, copies asked into L2 three to eight tiles ahead 89 to 108).  9 trees of 199 nodes through windows of 2500,
-// 20 / 4 heads of 256: 96.8 us, 646 TFLOP/s; two prompts of 4000 through windows of 1500, 8 / 4 heads of 64: 50.4 us, 411
-// TFLOP/s: both are bound by a tile's chain of steps, in the softmax 1300 to 1400 cycles, at heads of 256 S 700.
+// call with all keys in L2 takes 62: start and join take 12, the rest is the copies' (4.9 TB/s; a ring of four tiles
+// for five 2 us more, copies asked into L2 three to eight tiles ahead 7 to 26).  Two prompts of 4000 through windows of 1500, 8 / 4
+// heads of 64: 51 us, 406 TFLOP/s, bound by a tile's chain of steps, in the softmax 1300 to 1400 cycles.  9 trees of 199 nodes
+// through windows of 2500, 20 / 4 heads of 256: 97.6 us, 641 TFLOP/s; a tile takes some 2600 cycles, of which the softmax works
+// 1450 and waits 1000 for S.  The copies are not why (93.8 with all pages one sequence's); S, whose 16 products take 720 cycles,
+// follows on the tensor pipe the last P V, of nearly 600, and the hand-overs between warps come on top.
 // Waits by one lane and a shuffle, for all lanes' own, made the chain 10 % longer.  At heads of 256 the queries in tensor
-// memory changed the 96.8 us to 95.8, and two softmax warps a quarter of the rows, each for half of a tile's keys, to 99.7.
+// memory took 1 us off, and two softmax warps a quarter of the rows, each for half of a tile's keys, added 3.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
